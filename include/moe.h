@@ -1,5 +1,6 @@
 /*
- * moe.h - C ABI of the GB300 (sm_103a) Mixture-of-Experts layer forward pass.
+ * moe.h - C ABI of the GB300 (sm_103a) Mixture-of-Experts layer: the forward
+ * pass, and the gradients that train it.
  *
  * The layer, as "How Mixture of Experts Scales Model Parameters" states it:
  *   X (n x d) -> router: one d x E linear layer, softmax per row
@@ -337,6 +338,129 @@ moe_status moe_forward_pooled_staged(const moe_config *cfg, const void *x, const
                                      int32_t *miss_list, int32_t *counts, void *ws,
                                      size_t ws_bytes, void *stream, moe_stage_hook hook,
                                      void *user);
+
+/* ------------------------------------------------------------------------
+ * Training the layer: the layer norm in front of it, the expert FFNs with what
+ * their gradient needs, and the gradients of every stage.  (An addition of
+ * this library; the pages state the forward pass.)  One training step of a
+ * pre-norm layer y = x + MoE(norm(x)) runs
+ *   moe_layernorm, moe_route, moe_dispatch, moe_expert_ffn_train, moe_combine,
+ * then, from the gradient dy of the layer's output,
+ *   moe_combine_backward      dy        -> dy_perm, dgate
+ *   moe_expert_ffn_backward   dy_perm   -> dx_perm, dW1, dW3, dW2
+ *   moe_route_backward        dgate, dx_perm -> dx, dWg, dbias
+ *   moe_layernorm_backward    dx        -> the norm's dx, dgamma, dbeta.
+ * Layers are f32 throughout or bf16 throughout (act_dtype = weight_dtype);
+ * other configurations return MOE_ERR_UNSUPPORTED.  A dense gated block, or a
+ * shared expert, is the layer with n_experts = top_k = 1 and offsets {0, n}
+ * (d_ff_shared is not read by these entry points).
+ * Sums run in fp32 and in a fixed order: a call repeated on the same inputs
+ * writes the same bits.  Gradients are written, not added to what the buffers
+ * hold.  Outputs must not overlap inputs or each other.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of workspace for the moe_*_train and moe_*_backward entry points that
+ * take cfg.  At least moe_workspace_size(cfg), so that one workspace can serve
+ * every stage of a step (and every layer of a stack in turn): nothing in it
+ * lives from one call to the next but the status word.  Host-only. */
+moe_status moe_train_workspace_size(const moe_config *cfg, size_t *bytes);
+
+/* Rows of a layer norm.  Row r of x starts ldx elements after row r - 1 (the
+ * other leading dimensions likewise); 0 stands for d.  Rows may be of any
+ * width; those that are whole 16-byte vectors with leading dimensions that
+ * are too are read and written by vectors. */
+typedef struct {
+  int64_t rows;          /* >= 0 */
+  int64_t ldx, ldy;      /* x and y; dx and dy of the gradient: lddx, lddy */
+  int64_t lddx, lddy;
+  int32_t d;             /* >= 1 */
+  int32_t dtype;         /* MOE_F32 or MOE_BF16: x, y, dx, dy, gamma, beta */
+  float eps;             /* >= 0, added to the variance */
+  int32_t reserved;      /* 0 */
+} moe_norm_config;
+
+/* Layer norm:  mean = sum_i x_i / d,  rstd = 1 / sqrt(sum_i (x_i - mean)^2 / d + eps),
+ *   y_i = (x_i - mean) * rstd * gamma_i + beta_i.
+ * beta may be NULL (no shift).  mean, rstd fp32 [rows], as
+ * moe_layernorm_backward takes them, or both NULL.  The variance is summed
+ * around the mean (not as a difference of squares). */
+moe_status moe_layernorm(const moe_norm_config *cfg, const void *x, const void *gamma,
+                         const void *beta, void *y, float *mean, float *rstd, void *stream);
+
+/* Bytes of scratch for moe_layernorm_backward (256-byte aligned; no status
+ * word in it).  Host-only. */
+moe_status moe_layernorm_workspace_size(const moe_norm_config *cfg, size_t *bytes);
+
+/* The layer norm's gradient, with xh_i = (x_i - mean) * rstd and w_i = dy_i * gamma_i:
+ *   dx_i = rstd * (w_i - sum_j w_j / d - xh_i * sum_j w_j xh_j / d),
+ *   dgamma_i = sum_rows dy_i xh_i,   dbeta_i = sum_rows dy_i.
+ * dgamma, dbeta fp32 [d], each may be NULL.  With rows = 0 they are zero. */
+moe_status moe_layernorm_backward(const moe_norm_config *cfg, const void *x, const void *gamma,
+                                  const float *mean, const float *rstd, const void *dy, void *dx,
+                                  float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                                  void *stream);
+
+/* moe_expert_ffn that keeps what its gradient needs, for f32 and bf16 layers:
+ *   SWIGLU: g = x W1^T, u = x W3^T, h = silu(g) * u;   RELU: h = max(x W1^T, 0).
+ * g, u, h act_dtype [n*K][d_ff] (g and u NULL for RELU; all three needed
+ * otherwise); y_perm act_dtype [n*K][d].  h is formed from the fp32 products,
+ * then g, u and h are each rounded once to act_dtype. */
+moe_status moe_expert_ffn_train(const moe_config *cfg, const void *x_perm, const int32_t *offsets,
+                                const moe_weights *w, void *g, void *u, void *h, void *y_perm,
+                                void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of the expert weights (device pointers; weight_dtype, laid out as
+ * the weights).  A NULL entry is not computed (a frozen matrix). */
+typedef struct {
+  void *W1;   /* [E][d_ff][d] */
+  void *W3;   /* [E][d_ff][d], SWIGLU only */
+  void *W2;   /* [E][d][d_ff] */
+} moe_expert_grads;
+
+/* Gradient of the expert FFNs over the dispatched segments.  Per expert, with
+ * s = 1 / (1 + e^-g):
+ *   dh = dy W2;   du = dh * g s;   dg = dh * u s (1 + g (1 - s))   (RELU: dg = dh where h > 0)
+ *   dx = dg W1 + du W3;   dW1 = dg^T x;   dW3 = du^T x;   dW2 = dy^T h.
+ * g, u, h as moe_expert_ffn_train wrote them.  dx_perm act_dtype [n*K][d], or
+ * NULL.  The gradients of an expert without rows are zero.  bf16 layers round
+ * dg and du once to bf16 (they are tensor-core operands). */
+moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
+                                   const int32_t *offsets, const moe_weights *w, const void *g,
+                                   const void *u, const void *h, const void *dy_perm,
+                                   void *dx_perm, const moe_expert_grads *grads, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/* Gradient of moe_combine:
+ *   dy_perm[inv_perm[t*K+j]] = topk_gate[t][j] * dy[t],
+ *   dgate[t][j] = sum_i dy[t][i] * y_perm[inv_perm[t*K+j]][i].
+ * dy act_dtype [n][d]; y_perm, dy_perm act_dtype [n*K][d]; dgate fp32 [n][K].
+ * y_perm and dgate may both be NULL (a frozen router).  The gradient of
+ * y_shared is dy itself.  An inv_perm entry outside [0, n*K) sets
+ * MOE_ERR_BAD_INDEX; its dgate is 0. */
+moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const void *y_perm,
+                                const int32_t *inv_perm, const float *topk_gate, void *dy_perm,
+                                float *dgate, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of moe_route (gates, softmax, linear layer) and of the row copies
+ * of moe_dispatch.  The logits' gradient dl [n][E] is formed from dgate:
+ *   RENORM:    dl = g_j (dgate_j - sum_i g_i dgate_i) at the chosen experts, else 0;
+ *   TOP_PROB:  dl_e = [e chosen] p_e dgate_e - p_e sum_i p_i dgate_i over the chosen i;
+ *   + aux * (E / n) * p_e (f_e - sum_i f_i p_i)   when f is given: the load-balancing
+ *     loss of moe_route_stats, its alpha (times the loss's own gradient) in aux,
+ *     with f held constant;
+ * then
+ *   dx[t] = dl[t] Wg + sum_j dx_perm[inv_perm[t*K+j]],   dWg = dl^T x,   dbias = sum_t dl[t].
+ * probs fp32 [n][E] as moe_route wrote it (may be NULL for RENORM without f);
+ * f fp32 [E] or NULL.  dx_perm and inv_perm may both be NULL (the router's
+ * share alone).  dx act_dtype [n][d], dWg act_dtype [E][d], dbias fp32 [E]:
+ * each may be NULL.  bf16 layers round dl once to bf16 for the two products
+ * (dbias sums it in fp32).  A topk_idx outside [0, E) sets MOE_ERR_BAD_INDEX
+ * and its slot counts as a gate of zero. */
+moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_weights *w,
+                              const float *probs, const int32_t *topk_idx, const float *topk_gate,
+                              const float *dgate, const float *f, float aux,
+                              const int32_t *inv_perm, const void *dx_perm, void *dx, void *dWg,
+                              float *dbias, void *ws, size_t ws_bytes, void *stream);
 
 /* Synchronises `stream`, then returns the workspace's device status word
  * (MOE_OK if no device-side fault was recorded).  detail, if not NULL,

@@ -7,51 +7,14 @@
 // experts, added up by weight") the K weighted outputs of a token are added.
 //   y[t] = sum_{j<k} g[t][j] * y_perm[inv_perm[t*k + j]]  (+ y_shared[t])
 // fp32 accumulation in slot order, then one rounding to the output type.
+// gates == nullptr stands for gates of one: the gradient of the dispatch's row
+// copies (dx[t] = the sum of its k rows' gradients, + the router's share).
 #include "common.cuh"
 #include "launch.h"
+#include "vec16.cuh"
 
 namespace moe {
 namespace {
-
-template <typename T>
-struct Vec16 {
-  static constexpr int N = 16 / sizeof(T);
-};
-
-template <typename T>
-__device__ __forceinline__ void unpack16(const uint4 &u, float *f);
-template <>
-__device__ __forceinline__ void unpack16<float>(const uint4 &u, float *f) {
-  f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-  f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-}
-template <>
-__device__ __forceinline__ void unpack16<__nv_bfloat16>(const uint4 &u, float *f) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 pack16(const float *f);
-template <>
-__device__ __forceinline__ uint4 pack16<float>(const float *f) {
-  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                    __float_as_uint(f[3]));
-}
-template <>
-__device__ __forceinline__ uint4 pack16<__nv_bfloat16>(const float *f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // Thread = one 16-byte vector of an output row.  The slots are taken eight at
 // a time: their indices and gates, then their rows, are all loaded before the
@@ -83,7 +46,7 @@ combine_kernel(const uint4 *__restrict__ y_perm, const int32_t *__restrict__ inv
         q[u] = -1;
         if (j0 + u < k) {
           q[u] = inv_perm[(int64_t)t * k + j0 + u];
-          g[u] = gates[(int64_t)t * k + j0 + u];
+          g[u] = gates ? gates[(int64_t)t * k + j0 + u] : 1.f;
         }
       }
 #pragma unroll
@@ -136,7 +99,7 @@ combine_rows_kernel(const uint4 *__restrict__ y_perm, const int32_t *__restrict_
       q = -1;
     }
     s_q[j] = q;
-    s_g[j] = gates[(int64_t)t * k + j];
+    s_g[j] = gates ? gates[(int64_t)t * k + j] : 1.f;
   }
   __syncthreads();
   const int v0 = blockIdx.y * 256 * VB + threadIdx.x;

@@ -3,20 +3,11 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "api.h"
 #include "launch.h"
 #include "moe.h"
 
 namespace moe {
-namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-bool ok_ptr(const void *p) { return p != nullptr && aligned(p, 16); }
-cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
-int act_size(const moe_config &c) { return c.act_dtype == MOE_F32 ? 4 : 2; }
-int h_size(const moe_config &c) { return c.act_dtype == MOE_F32 ? 4 : 2; }
 
 moe_status check_config(const moe_config *c) {
   if (c == nullptr) return MOE_ERR_INVALID_ARG;
@@ -80,11 +71,6 @@ moe_status check_expert_weights(const moe_config &c, const moe_weights *w) {
   return MOE_OK;
 }
 
-struct Layout {
-  size_t status, route_count, sync, logits, topk_idx, topk_gate, counts, offsets, perm, inv_perm,
-      x_perm, h, y_perm, y_shared, h_shared, act16, total;
-};
-
 Layout layout_of(const moe_config &c) {
   Layout L{};
   const size_t n = c.n, E = c.n_experts, P = (size_t)c.n * c.top_k;
@@ -118,10 +104,7 @@ Layout layout_of(const moe_config &c) {
   return L;
 }
 
-template <typename T>
-T *at(void *ws, size_t off) {
-  return reinterpret_cast<T *>(static_cast<char *>(ws) + off);
-}
+namespace {
 
 moe_status check_ws(const moe_config &c, const void *ws, size_t ws_bytes) {
   if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
@@ -129,17 +112,9 @@ moe_status check_ws(const moe_config &c, const void *ws, size_t ws_bytes) {
   return MOE_OK;
 }
 
-moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
 // Bytes from the status word through the per-launch counters (one memset
 // clears them all before a forward pass).
 size_t cleared_bytes(const Layout &L) { return L.sync - L.status + decode_layer_sync_bytes(); }
-
-#define MOE_TRY(expr)                   \
-  do {                                  \
-    const moe_status _st = (expr);      \
-    if (_st != MOE_OK) return _st;      \
-  } while (0)
 
 // The two GEMM stages of the MXFP4 tensor-core path (f16 activations).
 void mx_stages(const moe_config &c, const int32_t *offsets, const moe_weights *w, void *ws,

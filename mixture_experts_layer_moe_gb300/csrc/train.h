@@ -1,0 +1,71 @@
+// Host-side launchers of the training kernels (internal; the public ABI is moe.h).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe.h"
+
+namespace moe {
+
+// ------------------------------------------------------------- layer norm
+cudaError_t launch_norm(const moe_norm_config &c, const void *x, const void *gamma,
+                        const void *beta, void *y, float *mean, float *rstd, cudaStream_t s);
+size_t norm_backward_scratch(const moe_norm_config &c);
+cudaError_t launch_norm_backward(const moe_norm_config &c, const void *x, const void *gamma,
+                                 const float *mean, const float *rstd, const void *dy, void *dx,
+                                 float *dgamma, float *dbeta, void *scratch, cudaStream_t s);
+
+// --------------------------------------------------------- combine, router
+cudaError_t launch_combine_backward(int dtype, const void *dy, const void *y_perm,
+                                    const int32_t *inv_perm, const float *gates, void *dy_perm,
+                                    float *dgate, int n, int k, int d, int *status,
+                                    cudaStream_t s);
+
+// dl [n][pitch] (dtype; columns E .. pitch - 1 zero) and, when dbias is set,
+// the column sums, through route_grad_scratch(c) bytes of scratch.
+// dl may be nullptr (dbias alone).
+size_t route_grad_scratch(const moe_config &c);
+cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int32_t *topk_idx,
+                              const float *gates, const float *dgate, const float *f, float aux,
+                              void *dl, int pitch, float *dbias, float *scratch, int *status,
+                              cudaStream_t s);
+
+// ------------------------------------------------------- grouped products
+enum {
+  kRowsPlain = 0,       // out = A B (+ A2 B2)
+  kRowsRelu = 1,        // out = max(A B, 0)
+  kRowsSwiglu = 2,      // out = silu(A B) * (A B2), out_g = A B, out_u = A B2
+  kRowsReluGrad = 3,    // out = A B where h > 0
+  kRowsSwigluGrad = 4,  // v = A B: out = v u s (1 + g (1 - s)), out_u = v g s
+};
+
+// Products that write rows of the segments: for q in segment e,
+//   out[q][c] = epi( sum_k A[q][k] B_e(k, c) ),   c < N.
+// b_rows: B is stored [E][K][N] (the weights of a gradient), else [E][N][K].
+struct RowsProduct {
+  int dtype, epi, b_rows;
+  const int32_t *offsets;   // nullptr: one segment [0, rows) of expert 0
+  int num_experts, rows, K, N;
+  int lda;                  // elements from one row of A to the next (0: K)
+  const void *A, *A2;       // A2: the second product's rows (kRowsPlain) or nullptr
+  const void *B, *B2;
+  const void *g, *u, *h;    // kept rows [rows][N] that a gradient's epilogue reads
+  void *out, *out_g, *out_u;   // [rows][N]
+};
+cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s);
+
+// Products over the rows of each segment (a weight's gradient):
+//   out_e[m][c] = sum_{q in segment e} A[q][m] B[q][c],   m < M, c < N;
+// zero for a segment without rows.
+struct GradProduct {
+  int dtype;
+  const int32_t *offsets;   // nullptr: one segment [0, rows) of expert 0
+  int num_experts, rows, M, N;
+  int lda;                  // elements from one row of A to the next (0: M)
+  const void *A, *B;
+  void *out;                // [E][M][N]
+};
+cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,347 @@
+// The C entry points that train the layer (include/moe.h): argument checks,
+// the training workspace and the launch sequences.
+#include <stdint.h>
+
+#include "api.h"
+#include "launch.h"
+#include "moe.h"
+#include "train.h"
+
+namespace moe {
+namespace {
+
+// The layer's workspace, then the scratch of the gradients.
+struct TrainLayout {
+  size_t status, dg, du, dl, dx_router, bias_parts, total;
+};
+
+// dl's rows are padded to whole 16-byte vectors of bf16.
+int dl_pitch(const moe_config &c) { return (c.n_experts + 7) / 8 * 8; }
+
+TrainLayout train_layout_of(const moe_config &c) {
+  moe_config c1 = c;
+  c1.d_ff_shared = 0;
+  const Layout base = layout_of(c1);
+  const size_t P = (size_t)c.n * c.top_k, z = act_size(c);
+  TrainLayout L{};
+  L.status = base.status;
+  L.dg = base.h;              // [P][d_ff]
+  L.dx_router = base.x_perm;  // [n][d]
+  size_t off = layout_of(c).total;
+  auto take = [&](size_t bytes) {
+    const size_t a = off;
+    off += align_up(bytes);
+    return a;
+  };
+  L.du = take(P * c.d_ff * z);
+  L.dl = take((size_t)c.n * dl_pitch(c) * z);
+  L.bias_parts = take(route_grad_scratch(c));
+  L.total = off;
+  return L;
+}
+
+moe_status check_train_config(const moe_config *c) {
+  MOE_TRY(check_config(c));
+  if (c->weight_dtype != c->act_dtype) return MOE_ERR_UNSUPPORTED;   // (MXFP4, NVFP4)
+  return MOE_OK;
+}
+
+moe_status check_train_ws(const moe_config &c, const void *ws, size_t ws_bytes) {
+  if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < train_layout_of(c).total) return MOE_ERR_WORKSPACE;
+  return MOE_OK;
+}
+
+// The routed experts' weights alone (shared-expert weights are not read here).
+moe_status check_routed_weights(const moe_config &c, const moe_weights *w) {
+  moe_config c1 = c;
+  c1.d_ff_shared = 0;
+  moe_weights w1 = w ? *w : moe_weights{};
+  w1.Ws1 = w1.Ws2 = w1.Ws3 = nullptr;
+  return check_expert_weights(c1, &w1);
+}
+
+bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
+
+cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
+  return launch_rows_simt(p, status, s);
+}
+
+cudaError_t launch_grad(const GradProduct &p, int *status, cudaStream_t s) {
+  return launch_grad_simt(p, status, s);
+}
+
+moe_status check_norm(const moe_norm_config *c) {
+  if (c == nullptr || c->rows < 0 || c->d < 1 || c->reserved != 0) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!(c->eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+  for (int64_t ld : {c->ldx, c->ldy, c->lddx, c->lddy})
+    if (ld != 0 && (ld < c->d || ld > INT64_MAX / 4 / (c->rows > 0 ? c->rows : 1)))
+      return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// Leading dimensions of 0 stand for d.
+moe_norm_config dense(const moe_norm_config &c) {
+  moe_norm_config r = c;
+  for (int64_t *ld : {&r.ldx, &r.ldy, &r.lddx, &r.lddy})
+    if (*ld == 0) *ld = r.d;
+  return r;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_train_workspace_size(const moe_config *cfg, size_t *bytes) {
+  MOE_TRY(check_train_config(cfg));
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = train_layout_of(*cfg).total;
+  return MOE_OK;
+}
+
+moe_status moe_layernorm(const moe_norm_config *cfg, const void *x, const void *gamma,
+                         const void *beta, void *y, float *mean, float *rstd, void *stream) {
+  MOE_TRY(check_norm(cfg));
+  if (!ok_ptr(gamma) || !ok_or_null(beta) || (mean == nullptr) != (rstd == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!ok_or_null(mean) || !ok_or_null(rstd)) return MOE_ERR_INVALID_ARG;
+  if (cfg->rows == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(y)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_norm(dense(*cfg), x, gamma, beta, y, mean, rstd, as_stream(stream)));
+}
+
+moe_status moe_layernorm_workspace_size(const moe_norm_config *cfg, size_t *bytes) {
+  MOE_TRY(check_norm(cfg));
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = align_up(norm_backward_scratch(dense(*cfg)));
+  return MOE_OK;
+}
+
+moe_status moe_layernorm_backward(const moe_norm_config *cfg, const void *x, const void *gamma,
+                                  const float *mean, const float *rstd, const void *dy, void *dx,
+                                  float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                                  void *stream) {
+  MOE_TRY(check_norm(cfg));
+  if (!ok_ptr(gamma) || !ok_or_null(dgamma) || !ok_or_null(dbeta)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = as_stream(stream);
+  const moe_norm_config c = dense(*cfg);
+  if (c.rows == 0) {
+    if (dgamma) MOE_TRY(cuda_status(cudaMemsetAsync(dgamma, 0, (size_t)c.d * 4, s)));
+    if (dbeta) MOE_TRY(cuda_status(cudaMemsetAsync(dbeta, 0, (size_t)c.d * 4, s)));
+    return MOE_OK;
+  }
+  if (!ok_ptr(x) || !ok_ptr(mean) || !ok_ptr(rstd) || !ok_ptr(dy) || !ok_ptr(dx))
+    return MOE_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < norm_backward_scratch(c)) return MOE_ERR_WORKSPACE;
+  return cuda_status(
+      launch_norm_backward(c, x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, s));
+}
+
+moe_status moe_expert_ffn_train(const moe_config *cfg, const void *x_perm, const int32_t *offsets,
+                                const moe_weights *w, void *g, void *u, void *h, void *y_perm,
+                                void *ws, size_t ws_bytes, void *stream) {
+  MOE_TRY(check_train_config(cfg));
+  const moe_config &c = *cfg;
+  MOE_TRY(check_routed_weights(c, w));
+  if (!ok_ptr(x_perm) || !ok_ptr(offsets) || !ok_ptr(h) || !ok_ptr(y_perm))
+    return MOE_ERR_INVALID_ARG;
+  const bool gated = c.act == MOE_ACT_SWIGLU;
+  if (gated ? !ok_ptr(g) || !ok_ptr(u) : g != nullptr || u != nullptr) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_train_ws(c, ws, ws_bytes));
+  int *status = at<int>(ws, train_layout_of(c).status);
+  cudaStream_t s = as_stream(stream);
+  RowsProduct up{};
+  up.dtype = c.act_dtype;
+  up.epi = gated ? kRowsSwiglu : kRowsRelu;
+  up.offsets = offsets;
+  up.num_experts = c.n_experts;
+  up.rows = c.n * c.top_k;
+  up.K = c.d;
+  up.N = c.d_ff;
+  up.A = x_perm;
+  up.B = w->W1;
+  up.B2 = w->W3;
+  up.out = h;
+  up.out_g = g;
+  up.out_u = u;
+  MOE_TRY(cuda_status(launch_rows(up, status, s)));
+  RowsProduct dn = up;
+  dn.epi = kRowsPlain;
+  dn.K = c.d_ff;
+  dn.N = c.d;
+  dn.A = h;
+  dn.B = w->W2;
+  dn.B2 = nullptr;
+  dn.out = y_perm;
+  dn.out_g = dn.out_u = nullptr;
+  return cuda_status(launch_rows(dn, status, s));
+}
+
+moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
+                                   const int32_t *offsets, const moe_weights *w, const void *g,
+                                   const void *u, const void *h, const void *dy_perm,
+                                   void *dx_perm, const moe_expert_grads *grads, void *ws,
+                                   size_t ws_bytes, void *stream) {
+  MOE_TRY(check_train_config(cfg));
+  const moe_config &c = *cfg;
+  MOE_TRY(check_routed_weights(c, w));
+  if (!ok_ptr(x_perm) || !ok_ptr(offsets) || !ok_ptr(h) || !ok_ptr(dy_perm) ||
+      !ok_or_null(dx_perm) || grads == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  const bool gated = c.act == MOE_ACT_SWIGLU;
+  if (gated ? !ok_ptr(g) || !ok_ptr(u) : g != nullptr || u != nullptr) return MOE_ERR_INVALID_ARG;
+  if (!ok_or_null(grads->W1) || !ok_or_null(grads->W3) || !ok_or_null(grads->W2))
+    return MOE_ERR_INVALID_ARG;
+  if (!gated && grads->W3) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_train_ws(c, ws, ws_bytes));
+  const TrainLayout L = train_layout_of(c);
+  int *status = at<int>(ws, L.status);
+  cudaStream_t s = as_stream(stream);
+  const int P = c.n * c.top_k;
+  void *dg = at<void>(ws, L.dg), *du = at<void>(ws, L.du);
+
+  GradProduct gw{};
+  gw.dtype = c.act_dtype;
+  gw.offsets = offsets;
+  gw.num_experts = c.n_experts;
+  gw.rows = P;
+  if (grads->W2) {
+    gw.M = c.d;
+    gw.N = c.d_ff;
+    gw.A = dy_perm;
+    gw.B = h;
+    gw.out = grads->W2;
+    MOE_TRY(cuda_status(launch_grad(gw, status, s)));
+  }
+  if (!dx_perm && !grads->W1 && !grads->W3) return MOE_OK;
+  RowsProduct r{};
+  r.dtype = c.act_dtype;
+  r.epi = gated ? kRowsSwigluGrad : kRowsReluGrad;
+  r.b_rows = 1;
+  r.offsets = offsets;
+  r.num_experts = c.n_experts;
+  r.rows = P;
+  r.K = c.d;
+  r.N = c.d_ff;
+  r.A = dy_perm;
+  r.B = w->W2;
+  r.g = g;
+  r.u = u;
+  r.h = h;
+  r.out = dg;
+  r.out_u = gated ? du : nullptr;
+  MOE_TRY(cuda_status(launch_rows(r, status, s)));
+  gw.M = c.d_ff;
+  gw.N = c.d;
+  gw.B = x_perm;
+  if (grads->W1) {
+    gw.A = dg;
+    gw.out = grads->W1;
+    MOE_TRY(cuda_status(launch_grad(gw, status, s)));
+  }
+  if (grads->W3) {
+    gw.A = du;
+    gw.out = grads->W3;
+    MOE_TRY(cuda_status(launch_grad(gw, status, s)));
+  }
+  if (dx_perm) {
+    RowsProduct x{};
+    x.dtype = c.act_dtype;
+    x.epi = kRowsPlain;
+    x.b_rows = 1;
+    x.offsets = offsets;
+    x.num_experts = c.n_experts;
+    x.rows = P;
+    x.K = c.d_ff;
+    x.N = c.d;
+    x.A = dg;
+    x.B = w->W1;
+    x.A2 = gated ? du : nullptr;
+    x.B2 = w->W3;
+    x.out = dx_perm;
+    MOE_TRY(cuda_status(launch_rows(x, status, s)));
+  }
+  return MOE_OK;
+}
+
+moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const void *y_perm,
+                                const int32_t *inv_perm, const float *topk_gate, void *dy_perm,
+                                float *dgate, void *ws, size_t ws_bytes, void *stream) {
+  MOE_TRY(check_train_config(cfg));
+  const moe_config &c = *cfg;
+  if (!ok_ptr(dy) || !ok_ptr(inv_perm) || !ok_ptr(topk_gate) || !ok_ptr(dy_perm))
+    return MOE_ERR_INVALID_ARG;
+  if ((y_perm == nullptr) != (dgate == nullptr) || !ok_or_null(y_perm) || !ok_or_null(dgate))
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_train_ws(c, ws, ws_bytes));
+  return cuda_status(launch_combine_backward(c.act_dtype, dy, y_perm, inv_perm, topk_gate, dy_perm,
+                                             dgate, c.n, c.top_k, c.d,
+                                             at<int>(ws, train_layout_of(c).status),
+                                             as_stream(stream)));
+}
+
+moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_weights *w,
+                              const float *probs, const int32_t *topk_idx, const float *topk_gate,
+                              const float *dgate, const float *f, float aux,
+                              const int32_t *inv_perm, const void *dx_perm, void *dx, void *dWg,
+                              float *dbias, void *ws, size_t ws_bytes, void *stream) {
+  MOE_TRY(check_train_config(cfg));
+  const moe_config &c = *cfg;
+  MOE_TRY(check_router_weights(c, w));
+  if (!ok_ptr(topk_idx) || !ok_ptr(topk_gate) || !ok_ptr(dgate)) return MOE_ERR_INVALID_ARG;
+  if (!ok_or_null(probs) || !ok_or_null(f) || !ok_or_null(inv_perm) || !ok_or_null(dx_perm) ||
+      !ok_or_null(dx) || !ok_or_null(dWg) || !ok_or_null(dbias))
+    return MOE_ERR_INVALID_ARG;
+  if ((c.gate == MOE_GATE_TOP_PROB || f) && probs == nullptr) return MOE_ERR_INVALID_ARG;
+  if ((inv_perm == nullptr) != (dx_perm == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (dx_perm && !dx) return MOE_ERR_INVALID_ARG;
+  if (dWg && !ok_ptr(x)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_train_ws(c, ws, ws_bytes));
+  const TrainLayout L = train_layout_of(c);
+  int *status = at<int>(ws, L.status);
+  cudaStream_t s = as_stream(stream);
+  const int pitch = dl_pitch(c);
+  void *dl = dx || dWg ? at<void>(ws, L.dl) : nullptr;
+  if (dl || dbias)
+    MOE_TRY(cuda_status(launch_route_grad(c, probs, topk_idx, topk_gate, dgate, f, aux, dl, pitch,
+                                          dbias, at<float>(ws, L.bias_parts), status, s)));
+  if (dWg) {
+    GradProduct gw{};
+    gw.dtype = c.act_dtype;
+    gw.num_experts = 1;
+    gw.rows = c.n;
+    gw.M = c.n_experts;
+    gw.N = c.d;
+    gw.lda = pitch;
+    gw.A = dl;
+    gw.B = x;
+    gw.out = dWg;
+    MOE_TRY(cuda_status(launch_grad(gw, status, s)));
+  }
+  if (dx) {
+    RowsProduct r{};
+    r.dtype = c.act_dtype;
+    r.epi = kRowsPlain;
+    r.b_rows = 1;
+    r.num_experts = 1;
+    r.rows = c.n;
+    r.K = c.n_experts;
+    r.N = c.d;
+    r.lda = pitch;
+    r.A = dl;
+    r.B = w->Wg;
+    r.out = dx_perm ? at<void>(ws, L.dx_router) : dx;
+    MOE_TRY(cuda_status(launch_rows(r, status, s)));
+    if (dx_perm)
+      MOE_TRY(cuda_status(launch_combine(c.act_dtype, dx_perm, inv_perm, nullptr, r.out, dx, c.n,
+                                         c.top_k, c.d, status, s)));
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -52,6 +52,16 @@ class moe_expert_pool(ctypes.Structure):
 POOL_SELECTED, POOL_RESIDENT, POOL_LOOKUPS, POOL_SERVED = 0, 1, 2, 3
 
 
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("lddx", ctypes.c_int64), ("lddy", ctypes.c_int64), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class moe_expert_grads(ctypes.Structure):
+    _fields_ = [("W1", ctypes.c_void_p), ("W3", ctypes.c_void_p), ("W2", ctypes.c_void_p)]
+
+
 class moe_workspace_layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("status", "logits", "topk_idx", "topk_gate", "counts", "offsets", "perm",
@@ -67,6 +77,8 @@ def _load() -> ctypes.CDLL:
     cfgp = ctypes.POINTER(moe_config)
     wp = ctypes.POINTER(moe_weights)
     pp = ctypes.POINTER(moe_expert_pool)
+    np_ = ctypes.POINTER(moe_norm_config)
+    gp = ctypes.POINTER(moe_expert_grads)
     sig = {
         "moe_workspace_size": [cfgp, ctypes.POINTER(SZ)],
         "moe_workspace_layout_of": [cfgp, ctypes.POINTER(moe_workspace_layout)],
@@ -82,6 +94,14 @@ def _load() -> ctypes.CDLL:
         "moe_classify_experts": [cfgp, P, P, ctypes.c_int32, P, P, P, P, SZ, P],
         "moe_forward_pooled": [cfgp, P, wp, pp, P, P, P, P, P, SZ, P],
         "moe_forward_pooled_staged": [cfgp, P, wp, pp, P, P, P, P, P, SZ, P, STAGE_HOOK, P],
+        "moe_train_workspace_size": [cfgp, ctypes.POINTER(SZ)],
+        "moe_layernorm": [np_, P, P, P, P, P, P, P],
+        "moe_layernorm_workspace_size": [np_, ctypes.POINTER(SZ)],
+        "moe_layernorm_backward": [np_, P, P, P, P, P, P, P, P, P, SZ, P],
+        "moe_expert_ffn_train": [cfgp, P, P, wp, P, P, P, P, P, SZ, P],
+        "moe_expert_ffn_backward": [cfgp, P, P, wp, P, P, P, P, P, gp, P, SZ, P],
+        "moe_combine_backward": [cfgp, P, P, P, P, P, P, P, SZ, P],
+        "moe_route_backward": [cfgp, P, wp, P, P, P, P, P, ctypes.c_float, P, P, P, P, P, P, SZ, P],
         "moe_status_check": [P, P, ctypes.POINTER(ctypes.c_int32)],
         "moe_status_clear": [P, P],
         "moe_selftest_wait_timeout": [P, ctypes.c_uint64, P],
@@ -263,6 +283,126 @@ def moe_forward_pooled_staged(cfg, x, w: moe_weights, pool: moe_expert_pool, y, 
                                           ctypes.byref(pool), _ptr(y), _ptr(state),
                                           _ptr(miss_list), _ptr(counts), _ptr(ws), ws.numel(),
                                           _stream(stream), cb, None), "moe_forward_pooled_staged")
+
+
+def make_expert_grads(grads: dict) -> moe_expert_grads:
+    """moe_expert_grads from a dict of device tensors (keys W1, W3, W2; missing or None: not
+    computed)."""
+    g = grads.get
+    return moe_expert_grads(_ptr(g("W1")), _ptr(g("W3")), _ptr(g("W2")))
+
+
+def moe_train_workspace_size(cfg) -> int:
+    c = make_config(cfg)
+    out = ctypes.c_size_t(0)
+    _check(_lib.moe_train_workspace_size(ctypes.byref(c), ctypes.byref(out)),
+           "moe_train_workspace_size")
+    return out.value
+
+
+def alloc_train_workspace(cfg, device="cuda") -> torch.Tensor:
+    """A zeroed workspace tensor of moe_train_workspace_size(cfg) bytes (256-byte aligned)."""
+    ws = torch.zeros(moe_train_workspace_size(cfg), dtype=torch.uint8, device=device)
+    assert ws.data_ptr() % 256 == 0
+    return ws
+
+
+_NORM_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _norm_rows(t: torch.Tensor, like: torch.Tensor):
+    """(pointer, elements from one row to the next) of a [rows, d] tensor whose rows are dense."""
+    if t.dim() != 2 or t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError("rows of a layer norm must be [rows, d] tensors of one shape and type")
+    rows, d = t.shape
+    if d > 1 and t.stride(1) != 1:
+        raise ValueError("rows of a layer norm must be dense")
+    return t.data_ptr(), t.stride(0) if rows > 1 else d
+
+
+def _norm_vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, what: str):
+    if t is not None and (t.dtype != dtype or t.numel() != n):
+        raise ValueError(f"{what} must hold {n} values of {dtype}")
+    return _ptr(t)
+
+
+def _norm_config(x: torch.Tensor, eps: float = 0.0) -> moe_norm_config:
+    if x.dtype not in _NORM_DTYPE:
+        raise ValueError("a layer norm takes float32 or bfloat16 rows")
+    _, ldx = _norm_rows(x, x)
+    return moe_norm_config(x.shape[0], ldx, 0, 0, 0, x.shape[1], _NORM_DTYPE[x.dtype], eps, 0)
+
+
+def moe_layernorm(x, gamma, beta, y, mean, rstd, eps=1e-5, stream=None):
+    """x, y [rows, d] (rows may lie apart); beta and the pair mean, rstd may be None."""
+    c = _norm_config(x, eps)
+    xp, _ = _norm_rows(x, x)
+    yp, c.ldy = _norm_rows(y, x)
+    n, d = x.shape
+    _check(_lib.moe_layernorm(ctypes.byref(c), xp, _norm_vector(gamma, d, x.dtype, "gamma"),
+                              _norm_vector(beta, d, x.dtype, "beta"), yp,
+                              _norm_vector(mean, n, torch.float32, "mean"),
+                              _norm_vector(rstd, n, torch.float32, "rstd"), _stream(stream)),
+           "moe_layernorm")
+
+
+def moe_layernorm_workspace_size(rows: int, d: int, dtype: str) -> int:
+    """dtype "f32" or "bf16".  Enough for rows of any leading dimension."""
+    out, need = ctypes.c_size_t(0), 0
+    for ld in (d, d + 1):
+        c = moe_norm_config(rows, ld, ld, ld, ld, d, _DTYPE[dtype], 0.0, 0)
+        _check(_lib.moe_layernorm_workspace_size(ctypes.byref(c), ctypes.byref(out)),
+               "moe_layernorm_workspace_size")
+        need = max(need, out.value)
+    return need
+
+
+def moe_layernorm_backward(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, stream=None):
+    """ws: scratch of moe_layernorm_workspace_size bytes (uint8); dgamma, dbeta fp32 or None."""
+    c = _norm_config(x)
+    xp, _ = _norm_rows(x, x)
+    dyp, c.lddy = _norm_rows(dy, x)
+    dxp, c.lddx = _norm_rows(dx, x)
+    n, d = x.shape
+    f32 = torch.float32
+    _check(_lib.moe_layernorm_backward(
+        ctypes.byref(c), xp, _norm_vector(gamma, d, x.dtype, "gamma"),
+        _norm_vector(mean, n, f32, "mean"), _norm_vector(rstd, n, f32, "rstd"), dyp, dxp,
+        _norm_vector(dgamma, d, f32, "dgamma"), _norm_vector(dbeta, d, f32, "dbeta"), _ptr(ws),
+        ws.numel(), _stream(stream)), "moe_layernorm_backward")
+
+
+def moe_expert_ffn_train(cfg, x_perm, offsets, w: moe_weights, g, u, h, y_perm, ws, stream=None):
+    c = make_config(cfg)
+    _check(_lib.moe_expert_ffn_train(ctypes.byref(c), _ptr(x_perm), _ptr(offsets), ctypes.byref(w),
+                                     _ptr(g), _ptr(u), _ptr(h), _ptr(y_perm), _ptr(ws), ws.numel(),
+                                     _stream(stream)), "moe_expert_ffn_train")
+
+
+def moe_expert_ffn_backward(cfg, x_perm, offsets, w: moe_weights, g, u, h, dy_perm, dx_perm,
+                            grads: moe_expert_grads, ws, stream=None):
+    c = make_config(cfg)
+    _check(_lib.moe_expert_ffn_backward(ctypes.byref(c), _ptr(x_perm), _ptr(offsets),
+                                        ctypes.byref(w), _ptr(g), _ptr(u), _ptr(h), _ptr(dy_perm),
+                                        _ptr(dx_perm), ctypes.byref(grads), _ptr(ws), ws.numel(),
+                                        _stream(stream)), "moe_expert_ffn_backward")
+
+
+def moe_combine_backward(cfg, dy, y_perm, inv_perm, topk_gate, dy_perm, dgate, ws, stream=None):
+    c = make_config(cfg)
+    _check(_lib.moe_combine_backward(ctypes.byref(c), _ptr(dy), _ptr(y_perm), _ptr(inv_perm),
+                                     _ptr(topk_gate), _ptr(dy_perm), _ptr(dgate), _ptr(ws),
+                                     ws.numel(), _stream(stream)), "moe_combine_backward")
+
+
+def moe_route_backward(cfg, x, w: moe_weights, probs, topk_idx, topk_gate, dgate, f, aux, inv_perm,
+                       dx_perm, dx, dWg, dbias, ws, stream=None):
+    c = make_config(cfg)
+    _check(_lib.moe_route_backward(ctypes.byref(c), _ptr(x), ctypes.byref(w), _ptr(probs),
+                                   _ptr(topk_idx), _ptr(topk_gate), _ptr(dgate), _ptr(f),
+                                   float(aux), _ptr(inv_perm), _ptr(dx_perm), _ptr(dx), _ptr(dWg),
+                                   _ptr(dbias), _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_route_backward")
 
 
 def moe_status_check(ws, stream=None) -> tuple[int, int]:
