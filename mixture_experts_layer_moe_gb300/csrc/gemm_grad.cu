@@ -1,0 +1,405 @@
+// Weight gradients of the grouped products on a pair of SMs
+// (tcgen05.mma.cta_group::2): for every expert e
+//   out_e[m][c] = sum_{q in segment e} A[q][m] * B[q][c],
+// zero for a segment without rows.  dW2 = dy^T h, dW1 = dg^T x and
+// dW3 = du^T x of an expert (up to three such problems) share one launch, so
+// that only the last wave of the whole list is partly filled.
+//
+// The reduction runs over the segment's rows, which both operands store
+// strided: the MMA takes both as M-/N-major operands, staged as boxes of 64
+// columns x 64 rows (128-byte swizzle), and no transposed copy is made.  The
+// tile is D[c][m]: 256 output columns c on M (one per TMEM lane, 128 per CTA,
+// so that the lanes of a warp store neighbouring elements of an output row),
+// up to 256 output rows m on N.
+//
+// A segment ends anywhere: the last k-block of a tile reads into the next
+// segment (or past the array, where the copy fills zeros).  Steps of 16 rows
+// beyond the end are not issued; the rows between the end and the next
+// multiple of 16 are zeroed in shared memory, in both operands (a stray NaN
+// times zero would be NaN).  A k-block that needs this lands on a barrier of
+// its own in each CTA; a fixer warp per CTA zeroes the rows, makes the writes
+// visible to the async proxy, and the first CTA's fixer, once it has heard
+// from the second's, completes the stage's barrier that the MMA waits on.
+//
+// Roles (persistent, one CTA per SM, clusters of two): warp 0 TMA producer in
+// both CTAs, warp 1 of the first CTA issues the MMAs into two accumulators of
+// 256 columns, warps 2-5 drain them, warp 6 is the fixer.
+#include "common.cuh"
+#include "launch.h"
+#include "pair_common.cuh"
+#include "tc_common.cuh"
+#include "train.h"
+
+namespace moe {
+namespace {
+
+using namespace pair;
+
+constexpr int GM = 128;                       // output columns per CTA (MMA M = 256 per pair)
+constexpr int GN = 256;                       // output rows per tile at most (MMA N)
+constexpr int GK = 64;                        // segment rows per k-block
+constexpr int GS = 6;                         // pipeline stages
+constexpr int G_BOX = 64 * GK * 2;            // one 64 x 64 box: 8 KB
+constexpr int G_STAGE = 4 * G_BOX;            // two boxes of A (N side), two of B (M side)
+constexpr int G_EPI = 4;
+constexpr int G_THREADS = 32 * (3 + G_EPI);
+constexpr uint32_t G_TMEM_COLS = 512;
+constexpr int G_MAX_E = 256;
+constexpr size_t G_DYN_SMEM = 1024 + (size_t)GS * G_STAGE;
+
+struct GShared {
+  uint64_t full[GS];        // first CTA: both CTAs' boxes landed (and were fixed)
+  uint64_t empty[GS];       // both CTAs: the MMAs that read the stage completed
+  uint64_t tail_full[GS];   // this CTA's boxes of a k-block that needs fixing landed
+  uint64_t peer_fixed[GS];  // first CTA: the second CTA's fixer is done
+  uint64_t tfull[2], tempty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort, failed_on_entry, bad;
+  int offs[G_MAX_E + 1];
+};
+
+struct GArgs {
+  const int32_t *offsets;
+  int num_experts, rows, problems;
+  int M[kMaxGradProblems], N[kMaxGradProblems];
+  int first[kMaxGradProblems + 1];   // an expert's tiles before problem i
+  __nv_bfloat16 *out[kMaxGradProblems];
+  int *status;
+};
+struct GMaps {
+  CUtensorMap a[kMaxGradProblems], b[kMaxGradProblems];
+};
+
+struct GTile {
+  int e, prob, m0, nm, c0, beg, len;
+};
+
+__device__ __forceinline__ GTile g_decode(const GShared &sh, const GArgs &args, int t) {
+  GTile tl;
+  const int per = args.first[args.problems];
+  tl.e = t / per;
+  int r = t - tl.e * per;
+  tl.prob = 0;
+  while (tl.prob + 1 < args.problems && r >= args.first[tl.prob + 1]) ++tl.prob;
+  r -= args.first[tl.prob];
+  const int nc = (args.N[tl.prob] + 2 * GM - 1) / (2 * GM);
+  const int mb = r / nc;
+  tl.m0 = mb * GN;
+  tl.nm = min(GN, args.M[tl.prob] - tl.m0);
+  tl.c0 = (r - mb * nc) * 2 * GM;
+  tl.beg = sh.offs[tl.e];
+  tl.len = sh.offs[tl.e + 1] - tl.beg;
+  return tl;
+}
+
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  return *reinterpret_cast<const uint16_t *>(&h);
+}
+
+__global__ void __launch_bounds__(G_THREADS, 1)
+gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GArgs args) {
+  extern __shared__ uint8_t dyn_smem[];
+  __shared__ GShared sh;
+  uint8_t *smem = dyn_smem + ((1024 - (tc::smem_u32(dyn_smem) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int E = args.offsets ? args.num_experts : 1;
+
+  if (threadIdx.x == 0) {
+    sh.failed_on_entry = status_failed(args.status) ? 1 : 0;
+    sh.abort = sh.failed_on_entry;
+    sh.bad = 0;
+  }
+  for (int i = threadIdx.x; i <= E; i += G_THREADS)
+    sh.offs[i] = args.offsets ? args.offsets[i] : (i == 0 ? 0 : args.rows);
+  if (warp == 1) tmem_alloc2(&sh.tmem_base, G_TMEM_COLS);
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < GS; ++s) {
+      tc::mbar_init(&sh.full[s], 1);
+      tc::mbar_init(&sh.empty[s], 1);
+      tc::mbar_init(&sh.tail_full[s], 1);
+      tc::mbar_init(&sh.peer_fixed[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      tc::mbar_init(&sh.tfull[a], 1);
+      tc::mbar_init(&sh.tempty[a], 2 * G_EPI);
+    }
+    tc::mbar_init(&sh.drain, 1);
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < E; i += G_THREADS) {
+    const int b = sh.offs[i], en = sh.offs[i + 1];
+    if (b < 0 || en < b || en > args.rows) sh.bad = 1;   // (same value from every writer)
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc::tc_fence_after();
+  const uint32_t tmem_base = sh.tmem_base;
+  const int num_tiles = sh.bad ? 0 : E * args.first[args.problems];
+  if (sh.bad && rank == 0 && threadIdx.x == 0) set_status(args.status, MOE_ERR_BAD_INDEX, -1);
+  volatile int *abort = &sh.abort;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t tail_phase = 0;            // bit s: phase of the next fixed use of stage s
+      uint32_t used = 0, used_phase = 0, used_tail = 0;   // the last use of each stage
+      for (int t = pair; t < num_tiles && !*abort; t += n_pairs) {
+        const GTile tl = g_decode(sh, args, t);
+        const int half = ((tl.nm + 15) & ~15) >> 1;       // output rows staged by each CTA
+        const int boxes = (half + 63) >> 6;
+        const uint32_t bytes = (uint32_t)(2 + boxes) * G_BOX;
+        const CUtensorMap *ma = &maps.a[tl.prob], *mb = &maps.b[tl.prob];
+        const int m = tl.m0 + (int)rank * half, c = tl.c0 + (int)rank * GM;
+        for (int k = 0; k < tl.len; k += GK) {
+          if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) break;
+          const bool fix = tl.len - k < GK && ((tl.len - k) & 15) != 0;
+          uint8_t *sb = smem + stage * G_STAGE, *sa = sb + 2 * G_BOX;
+          uint32_t bar;
+          if (fix) {
+            bar = map_to_rank(tc::smem_u32(&sh.tail_full[stage]), rank);
+            tc::mbar_arrive_expect_tx(&sh.tail_full[stage], bytes);
+          } else {
+            bar = map_to_rank(tc::smem_u32(&sh.full[stage]), 0);
+            if (rank == 0) tc::mbar_arrive_expect_tx(&sh.full[stage], 2 * bytes);
+          }
+          for (int b = 0; b < boxes; ++b)
+            tma2_load_2d(ma, bar, sb + b * G_BOX, m + b * 64, tl.beg + k);
+          tma2_load_2d(mb, bar, sa, c, tl.beg + k);
+          tma2_load_2d(mb, bar, sa + G_BOX, c + 64, tl.beg + k);
+          const uint32_t bit = 1u << stage;
+          used |= bit;
+          used_tail = fix ? used_tail | bit : used_tail & ~bit;
+          const uint32_t ph = fix ? (tail_phase >> stage) & 1u : phase;
+          used_phase = ph ? used_phase | bit : used_phase & ~bit;
+          if (fix) tail_phase ^= bit;
+          if (++stage == GS) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (*abort) {
+        // let the copies in flight land before the pair exits (the second
+        // CTA's whole k-blocks count on the first CTA's barriers)
+        for (int s = 0; s < GS; ++s) {
+          if (!((used >> s) & 1u)) continue;
+          const uint32_t ph = (used_phase >> s) & 1u;
+          if ((used_tail >> s) & 1u) tc::mbar_wait_drain(&sh.tail_full[s], ph, 100000000ull);
+          else if (rank == 0) tc::mbar_wait_drain(&sh.full[s], ph, 100000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---------------- MMA issuer (first CTA of the pair)
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;
+      bool ok = true;
+      for (int t = pair; t < num_tiles && ok && !*abort; t += n_pairs) {
+        const GTile tl = g_decode(sh, args, t);
+        if (tl.len == 0) continue;
+        const uint32_t idesc = tc::idesc_bf16_f32(2 * GM, (tl.nm + 15) & ~15) |
+                               tc::kIdescAMajorMN | tc::kIdescBMajorMN;
+        const int acc = local & 1;
+        if (!mbar_wait_cluster(&sh.tempty[acc], ((local >> 1) & 1) ^ 1u, abort)) break;
+        tc::tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * GN);
+        for (int k = 0; k < tl.len; k += GK) {
+          if (!tc::mbar_wait(&sh.full[stage], phase, abort)) { ok = false; break; }
+          tc::tc_fence_after();
+          const uint32_t sb = tc::smem_u32(smem + stage * G_STAGE), sa = sb + 2 * G_BOX;
+          const int steps = (min(GK, tl.len - k) + 15) >> 4;
+          for (int i = 0; i < steps; ++i)
+            mma2_bf16(d_tmem, tc::smem_desc_sw128_mn(sa + i * 2048, G_BOX),
+                      tc::smem_desc_sw128_mn(sb + i * 2048, G_BOX), idesc,
+                      (k != 0 || i != 0) ? 1u : 0u);
+          mma2_commit_both(&sh.empty[stage]);
+          if (++stage == GS) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        mma2_commit_both(&sh.tfull[acc]);
+        ++local;
+      }
+      if (*abort) {
+        mma2_commit_self(&sh.drain);
+        tc::mbar_wait_drain(&sh.drain, 0, 100000000ull);
+      }
+    }
+  } else if (warp == 6) {
+    // ---------------- fixer (both CTAs)
+    int stage = 0;
+    uint32_t tail_phase = 0;
+    for (int t = pair; t < num_tiles; t += n_pairs) {
+      const GTile tl = g_decode(sh, args, t);
+      const int kb = (tl.len + GK - 1) / GK;
+      if (kb == 0) continue;
+      const int at = (stage + kb - 1) % GS;
+      stage = (stage + kb) % GS;
+      const int valid = tl.len - (kb - 1) * GK;           // rows of the last k-block
+      if ((valid & 15) == 0) continue;
+      const uint32_t ph = (tail_phase >> at) & 1u;
+      tail_phase ^= 1u << at;
+      const bool ok = tc::mbar_wait(&sh.tail_full[at], ph, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      // rows valid .. next multiple of 16 of every box (a swizzled row is a
+      // permutation of its own 128 bytes)
+      const int rows = 16 - (valid & 15);
+      uint8_t *base = smem + at * G_STAGE;
+      for (int i = lane; i < 4 * rows * 8; i += 32) {
+        const int box = i / (rows * 8), r = (i >> 3) % rows;
+        *reinterpret_cast<uint4 *>(base + box * G_BOX + (valid + r) * 128 + (i & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (rank == 1) {
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(tc::smem_u32(&sh.peer_fixed[at]), 0));
+      } else {
+        const bool peer = mbar_wait_cluster(&sh.peer_fixed[at], ph, abort);
+        if (!__all_sync(0xffffffffu, peer)) break;
+        if (lane == 0) tc::mbar_arrive(&sh.full[at]);
+      }
+    }
+  } else {
+    // ---------------- epilogue (both CTAs): warp w drains TMEM lanes 32*(w%4) .. +31
+    const int quarter = warp & 3;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t tempty_first = map_to_rank(tc::smem_u32(&sh.tempty[0]), 0);
+    int local = 0;
+    for (int t = pair; t < num_tiles; t += n_pairs) {
+      const GTile tl = g_decode(sh, args, t);
+      const int N = args.N[tl.prob];
+      const int col = tl.c0 + (int)rank * GM + quarter * 32 + lane;
+      uint16_t *o = reinterpret_cast<uint16_t *>(args.out[tl.prob]) +
+                    ((size_t)tl.e * args.M[tl.prob] + tl.m0) * N + col;
+      const int acc = local & 1;
+      if (tl.len != 0) {
+        const bool ok = tc::mbar_wait(&sh.tfull[acc], (local >> 1) & 1, abort);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc::tc_fence_after();
+      } else if (*abort) {
+        break;
+      }
+      const uint32_t tb = lane_base + (uint32_t)(acc * GN);
+#pragma unroll 1
+      for (int r0 = 0; r0 < tl.nm; r0 += 32) {
+        uint32_t a[32];
+        if (tl.len != 0) {
+          tc::tmem_ld32(tb + (uint32_t)r0, a);
+          tc::tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) a[i] = 0;
+        }
+        if (col < N) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (r0 + i < tl.nm) o[(size_t)(r0 + i) * N] = bf16_bits(__uint_as_float(a[i]));
+        }
+      }
+      if (tl.len != 0) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty_first + (uint32_t)(acc * sizeof(uint64_t)));
+        ++local;
+      }
+    }
+  }
+
+  __syncwarp();
+  tc::tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves (or frees its tensor memory) while the other may still
+  // read its shared memory, signal its barriers or write its tensor memory
+  cluster_sync();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tmem_dealloc2(tmem_base, G_TMEM_COLS);
+  }
+  if (threadIdx.x == 0 && sh.abort && !sh.failed_on_entry)
+    set_status(args.status, MOE_ERR_TIMEOUT, blockIdx.x);
+}
+
+int pairs_resident() {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (num_sms() / 2));
+  cfg.blockDim = dim3(G_THREADS);
+  cfg.dynamicSmemBytes = G_DYN_SMEM;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, gemm_grad_kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = num_sms() / 2;
+  }
+  return n;
+}
+
+}  // namespace
+
+bool gemm_grad_supported(const GradProduct &p) {
+  return p.dtype == MOE_BF16 && p.rows > 0 && tensor_maps_available() &&
+         p.num_experts <= G_MAX_E && (p.lda ? p.lda : p.M) % 8 == 0 && p.N % 8 == 0 &&
+         num_sms() >= 2;
+}
+
+cudaError_t launch_gemm_grad(const GradProduct *p, int count, int *status, cudaStream_t s) {
+  static int pairs = 0;
+  if (pairs == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        gemm_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_DYN_SMEM);
+    if (e != cudaSuccess) return e;
+    pairs = pairs_resident();
+  }
+  GMaps maps{};
+  GArgs a{};
+  a.offsets = p[0].offsets;
+  a.num_experts = p[0].num_experts;
+  a.rows = p[0].rows;
+  a.problems = count;
+  a.status = status;
+  const uint32_t box[2] = {64, GK};
+  for (int i = 0; i < count; ++i) {
+    a.M[i] = p[i].M;
+    a.N[i] = p[i].N;
+    a.out[i] = static_cast<__nv_bfloat16 *>(p[i].out);
+    a.first[i + 1] = a.first[i] + ((p[i].M + GN - 1) / GN) * ((p[i].N + 2 * GM - 1) / (2 * GM));
+    const uint64_t da[2] = {(uint64_t)(p[i].lda ? p[i].lda : p[i].M), (uint64_t)p[i].rows};
+    const uint64_t db[2] = {(uint64_t)p[i].N, (uint64_t)p[i].rows};
+    if (!make_tensor_map(&maps.a[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p[i].A, 2, da, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tensor_map(&maps.b[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p[i].B, 2, db, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(G_THREADS);
+  cfg.dynamicSmemBytes = G_DYN_SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_grad_kernel, maps, a);
+}
+
+}  // namespace moe

@@ -100,6 +100,10 @@ struct PArgs {
   __nv_bfloat16 *out;      // [rows][N]
   int *status;
   int tok_major;           // 1: token block outer, weight block fastest
+  int pairs;               // operand pairs summed (2: out = A W + A2 W2, EPI 0 on row-stored weights)
+  // training: what the forward keeps (EPI 5) and what a gradient reads and adds (EPI 6, 7), [rows][N]
+  __nv_bfloat16 *out_g, *out_u;
+  const uint16_t *g, *u, *h;
 };
 
 struct PTile {
@@ -153,17 +157,44 @@ __device__ __forceinline__ float silu_mul(float a, float b) {
   return __fdividef(a, 1.f + __expf(-a)) * b;
 }
 
+__device__ __forceinline__ float bf16_value(uint16_t b) {
+  return __uint_as_float((uint32_t)b << 16);
+}
+
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
   const __nv_bfloat16 h = __float2bfloat16_rn(v);
   return *reinterpret_cast<const uint16_t *>(&h);
 }
 
-// EPI: 0 plain, 1 relu, 2 swiglu (W = W1 rows, W3 = W3 rows).
-template <int EPI>
+// Kept rows of a gradient's epilogue: this thread's column of 32 tokens (h for
+// the ReLU, g and u for SwiGLU; 0 outside the segment).
+template <int EPI, int NG, int NU>
+__device__ __forceinline__ void load_kept(const PArgs &args, int tok0, int end, int col, bool col_ok,
+                                          uint16_t (&kg)[NG], uint16_t (&ku)[NU]) {
+  const uint16_t *g = EPI == 6 ? args.h : args.g;
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const bool ok = col_ok && tok0 + i < end;
+    const size_t at = (size_t)(tok0 + i) * args.N + col;
+    kg[i] = ok ? __ldg(g + at) : (uint16_t)0;
+    if constexpr (EPI == 7) ku[i] = ok ? __ldg(args.u + at) : (uint16_t)0;
+  }
+}
+
+// EPI: 0 plain, 1 relu, 2 swiglu (W = W1 rows, W3 = W3 rows), 5 swiglu that
+// also stores both products, 6 relu gradient, 7 swiglu gradient.
+// WROWS: the weights are stored with the output column contiguous ([E][K][N],
+// the forward's weights as their gradients read them): the MMA takes them as
+// an M-major operand, staged as two boxes of 64 columns x 64 reduction rows
+// (128-byte swizzle, the boxes 8 KB apart), and no transposed copy is made.
+template <int EPI, bool WROWS>
 __global__ void __launch_bounds__(P_THREADS, 1)
 gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-               const __grid_constant__ CUtensorMap tmW3, PArgs args) {
-  constexpr int OUT_CTA = (EPI == 2) ? PM / 2 : PM;   // output columns per CTA per tile
+               const __grid_constant__ CUtensorMap tmX2, const __grid_constant__ CUtensorMap tmW3,
+               PArgs args) {
+  constexpr bool GATED = EPI == 2 || EPI == 5;        // two weight matrices side by side
+  static_assert(!WROWS || !GATED, "the gated forward reads weights stored by output column");
+  constexpr int OUT_CTA = GATED ? PM / 2 : PM;        // output columns per CTA per tile
   constexpr int OUT_TILE = 2 * OUT_CTA;
   constexpr uint32_t TX_BYTES = 2u * P_STAGE;          // both CTAs' copies of one stage
   extern __shared__ uint8_t dyn_smem[];
@@ -174,12 +205,14 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int E = args.offsets ? args.num_experts : 1;
   const int n_wb = (args.N + OUT_TILE - 1) / OUT_TILE;
-  const int KB = (args.K + PK - 1) / PK;
+  const int KB1 = (args.K + PK - 1) / PK;             // k-blocks of one operand pair
+  const int KB = WROWS ? KB1 * args.pairs : KB1;
 
   if (threadIdx.x == 0) {
     tc::prefetch_tmap(&tmX);
     tc::prefetch_tmap(&tmW);
-    if (EPI == 2) tc::prefetch_tmap(&tmW3);
+    if (GATED || WROWS) tc::prefetch_tmap(&tmW3);
+    if (WROWS) tc::prefetch_tmap(&tmX2);
     sh.failed_on_entry = status_failed(args.status) ? 1 : 0;
     sh.abort = sh.failed_on_entry;
   }
@@ -264,8 +297,19 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
           uint8_t *sa = sb + P_B_BYTES;
           const uint32_t bar = map_to_rank(tc::smem_u32(&sh.full[stage]), 0);
           if (rank == 0) tc::mbar_arrive_expect_tx(&sh.full[stage], TX_BYTES);
+          if constexpr (WROWS) {
+            const bool second = kb >= KB1;
+            const int k0 = (second ? kb - KB1 : kb) * PK;
+            const CUtensorMap *w = second ? &tmW3 : &tmW;
+            tma2_load_2d(second ? &tmX2 : &tmX, bar, sb, k0, brow);
+            tma2_load_3d(w, bar, sa, wrow, k0, tl.e);                       // columns 0..63
+            tma2_load_3d(w, bar, sa + P_A_BYTES / 2, wrow + 64, k0, tl.e);  // columns 64..127
+            last_phase[stage] = (int)phase;
+            if (++stage == PS) { stage = 0; phase ^= 1u; }
+            continue;
+          }
           tma2_load_2d(&tmX, bar, sb, kb * PK, brow);
-          if constexpr (EPI == 2) {
+          if constexpr (GATED) {
             tma2_load_3d(&tmW, bar, sa, kb * PK, wrow, tl.e);               // rows 0..63
             tma2_load_3d(&tmW3, bar, sa + P_A_BYTES / 2, kb * PK, wrow, tl.e);  // rows 64..127
           } else {
@@ -293,7 +337,8 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       for (int t = pair; t < num_tiles && ok && !*abort; t += n_pairs, ++local) {
         const PTile tl = p_decode(sh, E, t, n_wb, tok_major);
         const int ntok = tl.ntok;
-        const uint32_t idesc = tc::idesc_bf16_f32(2 * PM, (ntok + 15) & ~15);
+        const uint32_t idesc =
+            tc::idesc_bf16_f32(2 * PM, (ntok + 15) & ~15) | (WROWS ? tc::kIdescAMajorMN : 0u);
         const int acc = local & 1;
         if (!mbar_wait_cluster(&sh.tempty[acc], ((local >> 1) & 1) ^ 1u, abort)) { ok = false; break; }
         tc::tc_fence_after();
@@ -305,8 +350,10 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
           const uint32_t sa = sb + P_B_BYTES;
 #pragma unroll
           for (int k = 0; k < PK / 16; ++k)
-            mma2_bf16(d_tmem, tc::smem_desc_sw128(sa + k * 32), tc::smem_desc_sw128(sb + k * 32),
-                      idesc, (kb != 0 || k != 0) ? 1u : 0u);
+            mma2_bf16(d_tmem,
+                      WROWS ? tc::smem_desc_sw128_mn(sa + k * 2048, P_A_BYTES / 2)
+                            : tc::smem_desc_sw128(sa + k * 32),
+                      tc::smem_desc_sw128(sb + k * 32), idesc, (kb != 0 || k != 0) ? 1u : 0u);
           mma2_commit_both(&sh.empty[stage]);
           if (++stage == PS) { stage = 0; phase ^= 1u; }
         }
@@ -331,8 +378,16 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       const PTile tl = p_decode(sh, E, t, n_wb, tok_major);
       const int ntok = tl.ntok;
       const int acc = local & 1;
+      // this thread's output column
+      const int col = GATED ? tl.wb * OUT_TILE + (int)rank * OUT_CTA + pq * 32 + lane
+                                 : tl.wb * OUT_TILE + (int)rank * OUT_CTA + quarter * 32 + lane;
+      const bool col_ok = col < args.N;
+      uint16_t *o = reinterpret_cast<uint16_t *>(args.out) + col;
+      // a gradient's kept rows: the first chunk is in flight during the wait
+      uint16_t kg[EPI >= 6 ? 32 : 1], ku[EPI == 7 ? 32 : 1];
+      if constexpr (EPI >= 6) load_kept<EPI>(args, tl.tok0, tl.seg_end, col, col_ok, kg, ku);
       const bool ok = tc::mbar_wait(&sh.tfull[acc], (local >> 1) & 1, abort);
-      if constexpr (EPI == 2) {
+      if constexpr (GATED) {
         // the two warps of a pair meet on named barriers below: they agree on
         // going on first (a warp whose wait ran out has raised *abort)
         if (tc::bar_or(1 + pq, 64, !ok)) break;
@@ -341,18 +396,13 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       }
       tc::tc_fence_after();
       const uint32_t tb = lane_base + (uint32_t)(acc * PN);
-      // this thread's output column
-      const int col = (EPI == 2) ? tl.wb * OUT_TILE + (int)rank * OUT_CTA + pq * 32 + lane
-                                 : tl.wb * OUT_TILE + (int)rank * OUT_CTA + quarter * 32 + lane;
-      const bool col_ok = col < args.N;
-      uint16_t *o = reinterpret_cast<uint16_t *>(args.out) + col;
 #pragma unroll 1
       for (int c = 0; c * 32 < ntok; ++c) {
         uint32_t a[32];
         tc::tmem_ld32(tb + (uint32_t)(c * 32), a);
         tc::tmem_ld_wait();
         const int tok0 = tl.tok0 + c * 32;
-        if constexpr (EPI == 2) {
+        if constexpr (GATED) {
           // the W1 warp (gate values) finishes tokens 0..15 of the chunk, the
           // W3 warp (up values) tokens 16..31; each hands the other its half
           float *to_w3 = xbuf + (size_t)((pq * 2 + (c & 1)) * 2) * P_XBUF;   // gates 16..31
@@ -363,20 +413,57 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             mine[lane * P_XROW + i] = __uint_as_float(w3 ? a[i] : a[16 + i]);
           asm volatile("bar.sync %0, 64;" ::"r"(3 + pq) : "memory");
           const float *theirs = w3 ? to_w3 : to_w1;
-          uint16_t hv[16];
+          uint16_t hv[16], gv[EPI == 5 ? 16 : 1], uv[EPI == 5 ? 16 : 1];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float other = theirs[lane * P_XROW + i];
             const float g = w3 ? other : __uint_as_float(a[i]);
             const float u = w3 ? __uint_as_float(a[16 + i]) : other;
             hv[i] = bf16_bits(silu_mul(g, u));
+            if constexpr (EPI == 5) {
+              gv[i] = bf16_bits(g);
+              uv[i] = bf16_bits(u);
+            }
           }
           const int tsub = w3 ? 16 : 0;
           if (col_ok) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int tok = tok0 + tsub + i;
-              if (tok < tl.seg_end) o[(size_t)tok * args.N] = hv[i];
+              if (tok < tl.seg_end) {
+                o[(size_t)tok * args.N] = hv[i];
+                if constexpr (EPI == 5) {
+                  reinterpret_cast<uint16_t *>(args.out_g)[(size_t)tok * args.N + col] = gv[i];
+                  reinterpret_cast<uint16_t *>(args.out_u)[(size_t)tok * args.N + col] = uv[i];
+                }
+              }
+            }
+          }
+        } else if constexpr (EPI >= 6) {
+          uint16_t dg[32], du[EPI == 7 ? 32 : 1];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float v = __uint_as_float(a[i]);
+            if constexpr (EPI == 6) {
+              dg[i] = bf16_value(kg[i]) > 0.f ? bf16_bits(v) : (uint16_t)0;
+            } else {
+              const float g = bf16_value(kg[i]), u = bf16_value(ku[i]);
+              const float sg = __fdividef(1.f, 1.f + __expf(-g));
+              dg[i] = bf16_bits(v * u * sg * (1.f + g * (1.f - sg)));
+              du[i] = bf16_bits(v * g * sg);
+            }
+          }
+          // the next chunk's kept rows are in flight while this one is stored
+          load_kept<EPI>(args, tok0 + 32, tl.seg_end, col, col_ok, kg, ku);
+          if (col_ok) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int tok = tok0 + i;
+              if (tok < tl.seg_end) {
+                o[(size_t)tok * args.N] = dg[i];
+                if constexpr (EPI == 7)
+                  reinterpret_cast<uint16_t *>(args.out_u)[(size_t)tok * args.N + col] = du[i];
+              }
             }
           }
         } else {
@@ -431,35 +518,39 @@ int pairs_resident(const void *kernel, size_t smem) {
   return n;
 }
 
-template <int EPI>
+template <int EPI, bool WROWS>
 cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
+  constexpr bool GATED = EPI == 2 || EPI == 5;
   static int pairs = 0;
   if (pairs == 0) {
-    cudaError_t e = cudaFuncSetAttribute(gemm_t2_kernel<EPI>,
+    cudaError_t e = cudaFuncSetAttribute(gemm_t2_kernel<EPI, WROWS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)P_DYN_SMEM);
     if (e != cudaSuccess) return e;
-    pairs = pairs_resident(reinterpret_cast<const void *>(gemm_t2_kernel<EPI>), P_DYN_SMEM);
+    pairs = pairs_resident(reinterpret_cast<const void *>(gemm_t2_kernel<EPI, WROWS>), P_DYN_SMEM);
   }
   const int E = g.offsets ? g.num_experts : 1;
-  CUtensorMap mX, mW, mW3;
-  const uint64_t dX[2] = {(uint64_t)g.K, (uint64_t)g.rows};
+  CUtensorMap mX, mW, mX2, mW3;
+  auto bf16_map = [](CUtensorMap *m, const void *p, int rank, const uint64_t *dims,
+                     const uint32_t *box) {
+    return make_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, rank, dims, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  const uint64_t dX[2] = {(uint64_t)(g.lda ? g.lda : g.K), (uint64_t)g.rows};
   const uint32_t bX[2] = {PK, PN / 2};
-  if (!make_tensor_map(&mX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.A, 2, dX, bX,
-                       CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  const uint64_t dW[3] = {(uint64_t)g.K, (uint64_t)g.N, (uint64_t)E};
-  const uint32_t bW[3] = {PK, (uint32_t)(EPI == 2 ? PM / 2 : PM), 1};
-  if (!make_tensor_map(&mW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.B, 3, dW, bW,
-                       CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  if (EPI == 2) {
-    if (!make_tensor_map(&mW3, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.B3, 3, dW, bW,
-                         CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
-  } else {
-    mW3 = mW;
+  if (!bf16_map(&mX, g.A, 2, dX, bX)) return cudaErrorInvalidValue;
+  // weights by output column: boxes of 64 reduction elements x 128 (64) rows;
+  // by reduction row: boxes of 64 columns x 64 reduction rows
+  const uint64_t dW[3] = {(uint64_t)(WROWS ? g.N : g.K), (uint64_t)(WROWS ? g.K : g.N),
+                          (uint64_t)E};
+  const uint32_t bW[3] = {PK, (uint32_t)(WROWS ? PK : GATED ? PM / 2 : PM), 1};
+  if (!bf16_map(&mW, g.B, 3, dW, bW)) return cudaErrorInvalidValue;
+  mW3 = mW;
+  mX2 = mX;
+  if (GATED || g.A2) {
+    if (!bf16_map(&mW3, g.B3, 3, dW, bW)) return cudaErrorInvalidValue;
   }
+  if (g.A2 && !bf16_map(&mX2, g.A2, 2, dX, bX)) return cudaErrorInvalidValue;
   PArgs a{};
   a.offsets = g.offsets;
   a.num_experts = g.num_experts;
@@ -468,10 +559,16 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
   a.N = g.N;
   a.out = static_cast<__nv_bfloat16 *>(g.out);
   a.status = status;
+  a.pairs = g.A2 ? 2 : 1;
+  a.out_g = static_cast<__nv_bfloat16 *>(g.out_g);
+  a.out_u = static_cast<__nv_bfloat16 *>(g.out_u);
+  a.g = static_cast<const uint16_t *>(g.kept_g);
+  a.u = static_cast<const uint16_t *>(g.kept_u);
+  a.h = static_cast<const uint16_t *>(g.kept_h);
   // token blocks outer when an average segment holds more rows than the
   // weights it meets (the shared expert's one segment of all n tokens)
   const long seg_rows = (long)g.rows / (E > 0 ? E : 1);
-  a.tok_major = seg_rows > (long)g.N * (EPI == 2 ? 2 : 1) ? 1 : 0;
+  a.tok_major = seg_rows > (long)g.N * (GATED ? 2 : 1) ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(P_THREADS);
@@ -484,23 +581,32 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_t2_kernel<EPI>, mX, mW, mW3, a);
+  return cudaLaunchKernelEx(&cfg, gemm_t2_kernel<EPI, WROWS>, mX, mW, mX2, mW3, a);
 }
 
 }  // namespace
 
 bool gemm_t2_supported(const GemmStage &g) {
+  const bool epi_ok = g.w_rows ? g.epi == 0 || g.epi == kEpiReluGrad || g.epi == kEpiSwigluGrad
+                               : g.epi >= 0 && g.epi <= 2 || g.epi == kEpiSwigluKeep;
   return g.rows > 0 && tensor_maps_available() && g.a_dtype == MOE_BF16 &&
-         g.b_dtype == MOE_BF16 && g.out_dtype == MOE_BF16 &&
-         (g.epi == 0 || g.epi == 1 || g.epi == 2) && g.num_experts <= P_MAX_E &&
-         g.K % 8 == 0 && g.N % 8 == 0 && num_sms() >= 2;
+         g.b_dtype == MOE_BF16 && g.out_dtype == MOE_BF16 && epi_ok && g.num_experts <= P_MAX_E &&
+         (g.lda ? g.lda : g.K) % 8 == 0 && g.N % 8 == 0 && num_sms() >= 2;
 }
 
 cudaError_t launch_gemm_t2(const GemmStage &g, int *status, cudaStream_t s) {
+  if (g.w_rows) {
+    switch (g.epi) {
+      case kEpiReluGrad: return launch_t2<kEpiReluGrad, true>(g, status, s);
+      case kEpiSwigluGrad: return launch_t2<kEpiSwigluGrad, true>(g, status, s);
+      default: return launch_t2<0, true>(g, status, s);
+    }
+  }
   switch (g.epi) {
-    case 1: return launch_t2<1>(g, status, s);
-    case 2: return launch_t2<2>(g, status, s);
-    default: return launch_t2<0>(g, status, s);
+    case 1: return launch_t2<1, false>(g, status, s);
+    case 2: return launch_t2<2, false>(g, status, s);
+    case kEpiSwigluKeep: return launch_t2<kEpiSwigluKeep, false>(g, status, s);
+    default: return launch_t2<0, false>(g, status, s);
   }
 }
 

@@ -123,7 +123,14 @@ struct GemmStage {
   float *logits;
   int *tile_count;
   int top_k, gate_mode;
+  // training (bf16 on the SM-pair kernel only)
+  int w_rows;            // 1: B is stored [E][K][N] (a gradient's reading of the weights)
+  int lda;               // elements from one row of A to the next (0: K); columns K .. are zero
+  const void *A2;        // w_rows, epi 0: out = A B + A2 B3, or nullptr
+  void *out_g, *out_u;   // kEpiSwigluKeep: both products; kEpiSwigluGrad: out_u is du (out: dg)
+  const void *kept_g, *kept_u, *kept_h;   // what the gradients' epilogues read, [rows][N]
 };
+constexpr int kEpiSwigluKeep = 5, kEpiReluGrad = 6, kEpiSwigluGrad = 7;
 cudaError_t launch_gemm_simt(const GemmStage &g, int *status, cudaStream_t s);
 
 // The same stage on tcgen05 tensor cores (fp32 accumulate in TMEM, TMA-fed):

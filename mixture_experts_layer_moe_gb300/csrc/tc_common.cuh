@@ -183,6 +183,26 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
   return d;
 }
 
+// Instruction descriptor bits: operand A / B is M-major / N-major (the reduction
+// dimension strided) instead of K-major.
+constexpr uint32_t kIdescAMajorMN = 1u << 15;
+constexpr uint32_t kIdescBMajorMN = 1u << 16;
+
+// Shared-memory matrix descriptor for an M- or N-major tile written by TMA
+// with 128-byte swizzling: boxes of 64 elements along M/N by k rows of 128
+// bytes.  Groups of 8 k rows are 1024 bytes apart (stride byte offset), the
+// boxes along M/N box_bytes apart (leading byte offset).  Advancing 16 along K
+// adds 2048 bytes to the start address.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t box_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((box_bytes >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
 // 32 lanes x 32 consecutive fp32 columns: thread (lane l of warp w) receives
 // row 32*(w%4)+l, columns [col, col+32) of the accumulator.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {

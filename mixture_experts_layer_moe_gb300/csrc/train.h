@@ -67,5 +67,10 @@ struct GradProduct {
   void *out;                // [E][M][N]
 };
 cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s);
+// Up to kMaxGradProblems of them over the same segments in one launch, on
+// tensor cores (bf16; SM pairs).
+constexpr int kMaxGradProblems = 3;
+bool gemm_grad_supported(const GradProduct &p);
+cudaError_t launch_gemm_grad(const GradProduct *p, int count, int *status, cudaStream_t s);
 
 }  // namespace moe

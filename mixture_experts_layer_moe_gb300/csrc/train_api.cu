@@ -63,12 +63,44 @@ moe_status check_routed_weights(const moe_config &c, const moe_weights *w) {
 
 bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
 
+// bf16 rows run on the tensor cores (SM pairs), fp32 rows on the CUDA cores.
 cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
-  return launch_rows_simt(p, status, s);
+  if (p.dtype == MOE_F32) return launch_rows_simt(p, status, s);
+  constexpr int epi[] = {0, 1, kEpiSwigluKeep, kEpiReluGrad, kEpiSwigluGrad};   // by kRows*
+  GemmStage g{};
+  g.a_dtype = g.b_dtype = g.out_dtype = MOE_BF16;
+  g.epi = epi[p.epi];
+  g.w_rows = p.b_rows;
+  g.offsets = p.offsets;
+  g.num_experts = p.num_experts;
+  g.rows = p.rows;
+  g.K = p.K;
+  g.N = p.N;
+  g.lda = p.lda;
+  g.A = p.A;
+  g.A2 = p.A2;
+  g.B = p.B;
+  g.B3 = p.B2;
+  g.out = p.out;
+  g.out_g = p.out_g;
+  g.out_u = p.out_u;
+  g.kept_g = p.g;
+  g.kept_u = p.u;
+  g.kept_h = p.h;
+  return gemm_t2_supported(g) ? launch_gemm_t2(g, status, s) : launch_rows_simt(p, status, s);
 }
 
-cudaError_t launch_grad(const GradProduct &p, int *status, cudaStream_t s) {
-  return launch_grad_simt(p, status, s);
+// Problems over the same segments: one launch on the tensor cores, else one
+// launch each.
+cudaError_t launch_grads(const GradProduct *p, int count, int *status, cudaStream_t s) {
+  bool tc = true;
+  for (int i = 0; i < count; ++i) tc = tc && gemm_grad_supported(p[i]);
+  if (tc) return count ? launch_gemm_grad(p, count, status, s) : cudaSuccess;
+  for (int i = 0; i < count; ++i) {
+    const cudaError_t e = launch_grad_simt(p[i], status, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 moe_status check_norm(const moe_norm_config *c) {
@@ -205,20 +237,24 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   const int P = c.n * c.top_k;
   void *dg = at<void>(ws, L.dg), *du = at<void>(ws, L.du);
 
-  GradProduct gw{};
-  gw.dtype = c.act_dtype;
-  gw.offsets = offsets;
-  gw.num_experts = c.n_experts;
-  gw.rows = P;
-  if (grads->W2) {
-    gw.M = c.d;
-    gw.N = c.d_ff;
-    gw.A = dy_perm;
-    gw.B = h;
-    gw.out = grads->W2;
-    MOE_TRY(cuda_status(launch_grad(gw, status, s)));
-  }
-  if (!dx_perm && !grads->W1 && !grads->W3) return MOE_OK;
+  GradProduct gw[kMaxGradProblems] = {};
+  int n_gw = 0;
+  auto weight_grad = [&](const void *A, const void *B, int M, int N, void *out) {
+    GradProduct &q = gw[n_gw++];
+    q.dtype = c.act_dtype;
+    q.offsets = offsets;
+    q.num_experts = c.n_experts;
+    q.rows = P;
+    q.M = M;
+    q.N = N;
+    q.A = A;
+    q.B = B;
+    q.out = out;
+  };
+  if (grads->W2) weight_grad(dy_perm, h, c.d, c.d_ff, grads->W2);
+  if (grads->W1) weight_grad(dg, x_perm, c.d_ff, c.d, grads->W1);
+  if (grads->W3) weight_grad(du, x_perm, c.d_ff, c.d, grads->W3);
+  if (!dx_perm && !grads->W1 && !grads->W3) return cuda_status(launch_grads(gw, n_gw, status, s));
   RowsProduct r{};
   r.dtype = c.act_dtype;
   r.epi = gated ? kRowsSwigluGrad : kRowsReluGrad;
@@ -236,19 +272,7 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   r.out = dg;
   r.out_u = gated ? du : nullptr;
   MOE_TRY(cuda_status(launch_rows(r, status, s)));
-  gw.M = c.d_ff;
-  gw.N = c.d;
-  gw.B = x_perm;
-  if (grads->W1) {
-    gw.A = dg;
-    gw.out = grads->W1;
-    MOE_TRY(cuda_status(launch_grad(gw, status, s)));
-  }
-  if (grads->W3) {
-    gw.A = du;
-    gw.out = grads->W3;
-    MOE_TRY(cuda_status(launch_grad(gw, status, s)));
-  }
+  MOE_TRY(cuda_status(launch_grads(gw, n_gw, status, s)));
   if (dx_perm) {
     RowsProduct x{};
     x.dtype = c.act_dtype;
@@ -321,7 +345,7 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
     gw.A = dl;
     gw.B = x;
     gw.out = dWg;
-    MOE_TRY(cuda_status(launch_grad(gw, status, s)));
+    MOE_TRY(cuda_status(launch_grads(&gw, 1, status, s)));
   }
   if (dx) {
     RowsProduct r{};
