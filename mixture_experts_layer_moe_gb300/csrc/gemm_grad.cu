@@ -12,7 +12,7 @@
 // to 256 output columns c on N, so that a thread of the epilogue holds
 // neighbouring elements of one output row: it packs them to 16 bytes, and each
 // warp hands 32 rows x 64 columns at a time to a TMA store (clipped at the
-// matrix's edge) from one of two buffers.  With m and c the other way round,
+// matrix's edge).  With m and c the other way round,
 // a thread's elements lie a row apart, and 2-byte stores took 9.5 us a tile:
 // 2.70 ms for the gradients of 32 experts (d 7168, d_ff 2048) with 18 rows
 // each, against TODO_MEASURED.
@@ -44,7 +44,7 @@ using namespace pair;
 constexpr int GM = 128;                       // output rows per CTA (MMA M = 256 per pair)
 constexpr int GN = 256;                       // output columns per tile at most (MMA N)
 constexpr int GK = 64;                        // segment rows per k-block
-constexpr int GS = 5;                         // pipeline stages
+constexpr int GS = 6;                         // pipeline stages
 constexpr int G_BOX = 64 * GK * 2;            // one 64 x 64 box: 8 KB
 constexpr int G_STAGE = 4 * G_BOX;            // two boxes of B (N side), two of A (M side)
 constexpr int G_EPI = 8;                      // epilogue warps: two per TMEM lane quarter
@@ -52,7 +52,7 @@ constexpr int G_THREADS = 32 * (3 + G_EPI);
 constexpr uint32_t G_TMEM_COLS = 512;
 constexpr int G_MAX_E = 256;
 constexpr int G_OUT = 32 * 128;               // one store: 32 rows x 64 columns, 128-byte swizzle
-constexpr size_t G_DYN_SMEM = 1024 + (size_t)GS * G_STAGE + (size_t)G_EPI * 2 * G_OUT;
+constexpr size_t G_DYN_SMEM = 1024 + (size_t)GS * G_STAGE + (size_t)G_EPI * G_OUT;
 
 struct GShared {
   uint64_t full[GS];        // first CTA: both CTAs' boxes landed (and were fixed)
@@ -158,39 +158,43 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer (both CTAs)
+      // (the loop below feeds both SMs' tensor cores from one thread: what it
+      // does per k-block is kept short)
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t tail_phase = 0;            // bit s: phase of the next fixed use of stage s
+      uint32_t tail_phase = 0;                            // bit s: phase of stage s's next fixed use
       uint32_t used = 0, used_phase = 0, used_tail = 0;   // the last use of each stage
+      const uint32_t full0 = map_to_rank(tc::smem_u32(&sh.full[0]), 0);
+      const uint32_t tail0 = map_to_rank(tc::smem_u32(&sh.tail_full[0]), rank);
       for (int t = pair; t < num_tiles && !*abort; t += n_pairs) {
         const GTile tl = g_decode(sh, args, t);
         const int half = ((tl.nc + 15) & ~15) >> 1;       // output columns staged by each CTA
-        const int boxes = (half + 63) >> 6;
-        const uint32_t bytes = (uint32_t)(2 + boxes) * G_BOX;
+        const bool two = half > 64;                       // one or two boxes of them
+        const uint32_t bytes = (uint32_t)(two ? 4 : 3) * G_BOX;
         const CUtensorMap *ma = &maps.a[tl.prob], *mb = &maps.b[tl.prob];
         const int m = tl.m0 + (int)rank * GM, c = tl.c0 + (int)rank * half;
-        for (int k = 0; k < tl.len; k += GK) {
+        const int end = tl.beg + tl.len;
+        for (int q = tl.beg; q < end; q += GK) {
           if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) break;
-          const bool fix = tl.len - k < GK && ((tl.len - k) & 15) != 0;
-          uint8_t *sb = smem + stage * G_STAGE, *sa = sb + 2 * G_BOX;
-          uint32_t bar;
-          if (fix) {
-            bar = map_to_rank(tc::smem_u32(&sh.tail_full[stage]), rank);
-            tc::mbar_arrive_expect_tx(&sh.tail_full[stage], bytes);
-          } else {
-            bar = map_to_rank(tc::smem_u32(&sh.full[stage]), 0);
-            if (rank == 0) tc::mbar_arrive_expect_tx(&sh.full[stage], 2 * bytes);
-          }
-          for (int b = 0; b < boxes; ++b)
-            tma2_load_2d(mb, bar, sb + b * G_BOX, c + b * 64, tl.beg + k);
-          tma2_load_2d(ma, bar, sa, m, tl.beg + k);
-          tma2_load_2d(ma, bar, sa + G_BOX, m + 64, tl.beg + k);
           const uint32_t bit = 1u << stage;
+          uint32_t bar = full0 + (uint32_t)stage * 8;
           used |= bit;
-          used_tail = fix ? used_tail | bit : used_tail & ~bit;
-          const uint32_t ph = fix ? (tail_phase >> stage) & 1u : phase;
-          used_phase = ph ? used_phase | bit : used_phase & ~bit;
-          if (fix) tail_phase ^= bit;
+          used_phase = phase ? used_phase | bit : used_phase & ~bit;
+          used_tail &= ~bit;
+          if (end - q < GK && ((end - q) & 15) != 0) {
+            bar = tail0 + (uint32_t)stage * 8;
+            tc::mbar_arrive_expect_tx(&sh.tail_full[stage], bytes);
+            used_tail |= bit;
+            used_phase = tail_phase & bit ? used_phase | bit : used_phase & ~bit;
+            tail_phase ^= bit;
+          } else if (rank == 0) {
+            tc::mbar_arrive_expect_tx(&sh.full[stage], 2 * bytes);
+          }
+          uint8_t *sb = smem + stage * G_STAGE;
+          tma2_load_2d(mb, bar, sb, c, q);
+          tma2_load_2d(ma, bar, sb + 2 * G_BOX, m, q);
+          tma2_load_2d(ma, bar, sb + 3 * G_BOX, m + 64, q);
+          if (two) tma2_load_2d(mb, bar, sb + G_BOX, c + 64, q);
           if (++stage == GS) { stage = 0; phase ^= 1u; }
         }
       }
@@ -212,6 +216,8 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
       uint32_t phase = 0;
       int local = 0;
       bool ok = true;
+      const uint64_t desc = tc::smem_desc_sw128_mn(tc::smem_u32(smem), G_BOX);
+      const uint32_t desc_lo = (uint32_t)desc, desc_hi = (uint32_t)(desc >> 32);
       for (int t = pair; t < num_tiles && ok && !*abort; t += n_pairs) {
         const GTile tl = g_decode(sh, args, t);
         if (tl.len == 0) continue;
@@ -224,12 +230,19 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
         for (int k = 0; k < tl.len; k += GK) {
           if (!tc::mbar_wait(&sh.full[stage], phase, abort)) { ok = false; break; }
           tc::tc_fence_after();
-          const uint32_t sb = tc::smem_u32(smem + stage * G_STAGE), sa = sb + 2 * G_BOX;
-          const int steps = (min(GK, tl.len - k) + 15) >> 4;
-          for (int i = 0; i < steps; ++i)
-            mma2_bf16(d_tmem, tc::smem_desc_sw128_mn(sa + i * 2048, G_BOX),
-                      tc::smem_desc_sw128_mn(sb + i * 2048, G_BOX), idesc,
-                      (k != 0 || i != 0) ? 1u : 0u);
+          // (low descriptor words: 16-byte units, 2048 bytes per 16 rows)
+          const uint32_t b_lo = desc_lo + (uint32_t)(stage * (G_STAGE / 16));
+          const uint32_t a_lo = b_lo + 2 * G_BOX / 16;
+          const int left = tl.len - k;
+          mma2_bf16_lo(d_tmem, a_lo, desc_hi, b_lo, desc_hi, idesc, k != 0);
+          if (left > 48) {
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+              mma2_bf16_lo(d_tmem, a_lo + i * 128, desc_hi, b_lo + i * 128, desc_hi, idesc, 1u);
+          } else {
+            if (left > 16) mma2_bf16_lo(d_tmem, a_lo + 128, desc_hi, b_lo + 128, desc_hi, idesc, 1u);
+            if (left > 32) mma2_bf16_lo(d_tmem, a_lo + 256, desc_hi, b_lo + 256, desc_hi, idesc, 1u);
+          }
           mma2_commit_both(&sh.empty[stage]);
           if (++stage == GS) { stage = 0; phase ^= 1u; }
         }
@@ -282,8 +295,8 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
     const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const uint32_t tempty_first = map_to_rank(tc::smem_u32(&sh.tempty[0]), 0);
-    uint8_t *stage_out = smem + GS * G_STAGE + (warp - 2) * 2 * G_OUT;
-    int local = 0, turn = 0;
+    uint8_t *stage_out = smem + GS * G_STAGE + (warp - 2) * G_OUT;
+    int local = 0;
     for (int t = pair; t < num_tiles; t += n_pairs) {
       const GTile tl = g_decode(sh, args, t);
       const int row = tl.m0 + (int)rank * GM + quarter * 32;   // this warp's first row
@@ -309,21 +322,18 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
           for (int i = 0; i < 32; ++i) a[0][i] = a[1][i] = 0;
         }
         if (!rows_ok) continue;
-        // the store before the last one has read its buffer
-        uint8_t *buf = stage_out + turn * G_OUT;
-        turn ^= 1;
-        if (lane == 0) tc::bulk_wait_read<1>();
+        if (lane == 0) tc::bulk_wait_read<0>();   // the store before has read the buffer
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const uint32_t *v = &a[q >> 2][(q & 3) * 8];
-          *reinterpret_cast<uint4 *>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+          *reinterpret_cast<uint4 *>(stage_out + lane * 128 + ((q ^ (lane & 7)) << 4)) =
               make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
                          bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) tc::tma_store_3d(&maps.out[tl.prob], buf, tl.c0 + c, row, tl.e);
+        if (lane == 0) tc::tma_store_3d(&maps.out[tl.prob], stage_out, tl.c0 + c, row, tl.e);
       }
       if (tl.len != 0) {
         tc::tc_fence_before();

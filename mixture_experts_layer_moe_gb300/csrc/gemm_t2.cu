@@ -282,9 +282,8 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       // ---------------- TMA producer (both CTAs)
       int stage = 0;
       uint32_t phase = 0;
-      int last_phase[PS];
-#pragma unroll
-      for (int s = 0; s < PS; ++s) last_phase[s] = -1;
+      uint32_t used = 0, used_phase = 0;   // bit s: stage s was used, in which phase last
+      const uint32_t full0 = map_to_rank(tc::smem_u32(&sh.full[0]), 0);
       for (int t = pair; t < num_tiles && !*abort; t += n_pairs) {
         const PTile tl = p_decode(sh, E, t, n_wb, tok_major);
         const int ntok = tl.ntok;
@@ -295,7 +294,9 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
           if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) break;
           uint8_t *sb = smem + stage * P_STAGE;
           uint8_t *sa = sb + P_B_BYTES;
-          const uint32_t bar = map_to_rank(tc::smem_u32(&sh.full[stage]), 0);
+          const uint32_t bar = full0 + (uint32_t)stage * 8;
+          used |= 1u << stage;
+          used_phase = phase ? used_phase | 1u << stage : used_phase & ~(1u << stage);
           if (rank == 0) tc::mbar_arrive_expect_tx(&sh.full[stage], TX_BYTES);
           if constexpr (WROWS) {
             const bool second = kb >= KB1;
@@ -304,7 +305,6 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             tma2_load_2d(second ? &tmX2 : &tmX, bar, sb, k0, brow);
             tma2_load_3d(w, bar, sa, wrow, k0, tl.e);                       // columns 0..63
             tma2_load_3d(w, bar, sa + P_A_BYTES / 2, wrow + 64, k0, tl.e);  // columns 64..127
-            last_phase[stage] = (int)phase;
             if (++stage == PS) { stage = 0; phase ^= 1u; }
             continue;
           }
@@ -315,7 +315,6 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
           } else {
             tma2_load_3d(&tmW, bar, sa, kb * PK, wrow, tl.e);
           }
-          last_phase[stage] = (int)phase;
           if (++stage == PS) { stage = 0; phase ^= 1u; }
         }
       }
@@ -323,8 +322,8 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         // let the copies in flight land before the pair exits (the second
         // CTA's copies count on these barriers too)
         for (int s = 0; s < PS; ++s)
-          if (last_phase[s] >= 0)
-            tc::mbar_wait_drain(&sh.full[s], (uint32_t)last_phase[s], 100000000ull);
+          if ((used >> s) & 1u)
+            tc::mbar_wait_drain(&sh.full[s], (used_phase >> s) & 1u, 100000000ull);
       }
     }
   } else if (warp == 1) {
@@ -334,6 +333,15 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       uint32_t phase = 0;
       int local = 0;
       bool ok = true;
+      // descriptors of stage 0; an MMA's own differ in the low words, in units
+      // of 16 bytes (building them anew for every MMA left the tensor pipe
+      // waiting for this thread)
+      const uint32_t sb0 = tc::smem_u32(smem);
+      const uint64_t b_desc = tc::smem_desc_sw128(sb0);
+      const uint64_t a_desc = WROWS ? tc::smem_desc_sw128_mn(sb0 + P_B_BYTES, P_A_BYTES / 2)
+                                    : tc::smem_desc_sw128(sb0 + P_B_BYTES);
+      const uint32_t a_lo = (uint32_t)a_desc, a_hi = (uint32_t)(a_desc >> 32);
+      const uint32_t b_lo = (uint32_t)b_desc, b_hi = (uint32_t)(b_desc >> 32);
       for (int t = pair; t < num_tiles && ok && !*abort; t += n_pairs, ++local) {
         const PTile tl = p_decode(sh, E, t, n_wb, tok_major);
         const int ntok = tl.ntok;
@@ -346,14 +354,11 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         for (int kb = 0; kb < KB; ++kb) {
           if (!tc::mbar_wait(&sh.full[stage], phase, abort)) { ok = false; break; }
           tc::tc_fence_after();
-          const uint32_t sb = tc::smem_u32(smem + stage * P_STAGE);
-          const uint32_t sa = sb + P_B_BYTES;
+          const uint32_t at = (uint32_t)(stage * (P_STAGE / 16));
 #pragma unroll
           for (int k = 0; k < PK / 16; ++k)
-            mma2_bf16(d_tmem,
-                      WROWS ? tc::smem_desc_sw128_mn(sa + k * 2048, P_A_BYTES / 2)
-                            : tc::smem_desc_sw128(sa + k * 32),
-                      tc::smem_desc_sw128(sb + k * 32), idesc, (kb != 0 || k != 0) ? 1u : 0u);
+            mma2_bf16_lo(d_tmem, a_lo + at + k * (WROWS ? 128 : 2), a_hi, b_lo + at + k * 2, b_hi,
+                         idesc, (kb != 0 || k != 0) ? 1u : 0u);
           mma2_commit_both(&sh.empty[stage]);
           if (++stage == PS) { stage = 0; phase ^= 1u; }
         }

@@ -105,6 +105,22 @@ __device__ __forceinline__ void mma2_bf16(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// The same with the descriptors given as their low words (start address and
+// leading byte offset, the only part that changes from one MMA to the next)
+// and their constant high words.
+__device__ __forceinline__ void mma2_bf16_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                             uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrives on the barrier at this shared-memory offset in both CTAs of the
 // pair once every MMA issued before has completed.
 __device__ __forceinline__ void mma2_commit_both(uint64_t *bar) {
