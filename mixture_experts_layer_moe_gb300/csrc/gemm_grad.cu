@@ -273,12 +273,12 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
       if (!__all_sync(0xffffffffu, ok)) break;
       // rows valid .. next multiple of 16 of every box (a swizzled row is a
       // permutation of its own 128 bytes)
-      const int rows = 16 - (valid & 15);
-      uint8_t *base = smem + at * G_STAGE;
-      for (int i = lane; i < 4 * rows * 8; i += 32) {
-        const int box = i / (rows * 8), r = (i >> 3) % rows;
-        *reinterpret_cast<uint4 *>(base + box * G_BOX + (valid + r) * 128 + (i & 7) * 16) =
-            make_uint4(0, 0, 0, 0);
+      // (8 lanes per row, 4 rows at a time)
+      uint8_t *base = smem + at * G_STAGE + (lane & 7) * 16;
+      for (int r = valid + (lane >> 3); r < ((valid + 15) & ~15); r += 4) {
+#pragma unroll
+        for (int box = 0; box < 4; ++box)
+          *reinterpret_cast<uint4 *>(base + box * G_BOX + r * 128) = make_uint4(0, 0, 0, 0);
       }
       fence_async_smem();
       __syncwarp();

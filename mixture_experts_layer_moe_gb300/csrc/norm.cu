@@ -4,14 +4,17 @@
 //   dgamma_i = sum_rows dy_i xh_i,   dbeta_i = sum_rows dy_i
 // Both are streams through HBM: the forward reads and writes each row once,
 // the gradient reads x and dy once and writes dx.  A row lives in the
-// registers of a group of threads (a warp for short rows, else the CTA), so
-// the variance is summed around the mean without a second read.  Groups walk
-// the rows with a grid stride, with the next row's loads in flight while the
-// current one is reduced.  In the gradient a thread owns the same columns of
-// every row it meets, so the column sums grow in its registers; each CTA
-// writes one partial row and a second launch adds the partials in order (no
-// atomics: the result does not depend on timing).
-// All statistics and sums are fp32.
+// registers of a group of threads (a warp for short rows, else up to a CTA),
+// so the variance is summed around the mean without a second read.  Groups
+// walk the rows with a grid stride.  Rows of 16-byte vectors arrive through a
+// ring in shared memory that each thread fills for itself, several rows ahead
+// (cp.async; no other thread reads its part, so no barrier guards the ring):
+// with one row ahead in registers the gradient's one CTA per SM waited for
+// memory (285 us at 16384 x 7168 bf16 against TODO_BWD).
+// In the gradient a thread owns the same columns of every row it meets, so the
+// column sums grow in its registers; each CTA writes one partial row and a
+// second launch adds the partials in order (no atomics: the result does not
+// depend on timing).  All statistics and sums are fp32.
 #include "common.cuh"
 #include "launch.h"
 #include "train.h"
@@ -20,109 +23,192 @@
 namespace moe {
 namespace {
 
-constexpr int N_MAX_THREADS = 512;
 constexpr int N_MAX_PARTS = 304;   // partial rows of the column sums (two CTAs per SM)
+constexpr int N_FWD_THREADS = 512, N_BWD_THREADS = 1024;
+constexpr int N_FWD_STAGES = 3;
+// rows in a thread's ring: 1024 threads hold 192 KB of them
+constexpr int bwd_stages(int vpt) { return vpt == 1 ? 6 : 3; }
 
-// VEC elements as they lie in memory: 16 bytes, or one element.
+// ------------------------------------------------------------ pairs of fp32
+// Two fp32 values per instruction (each half rounded as on its own): the
+// norms are bound by instruction issue before they are by HBM.
+__device__ __forceinline__ unsigned long long bits2(float2 a) {
+  return reinterpret_cast<unsigned long long &>(a);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// How a thread's share of a row is cut: chunks of 16 bytes, or (rows that are
+// not whole vectors) two elements tpr apart.  H pairs per chunk.
 template <typename T, int VEC>
-struct Raw {
-  uint4 v;
-  __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ void get(float *f) const { unpack16<T>(v, f); }
-  static __device__ __forceinline__ void put(T *p, const float *f) {
-    *reinterpret_cast<uint4 *>(p) = pack16<T>(f);
+struct Chunk {
+  static constexpr int H = VEC / 2, SPAN = VEC;
+  static __device__ __forceinline__ void unpack(uint4 raw, float2 *p) {
+    unpack16<T>(raw, reinterpret_cast<float *>(p));
   }
+  static __device__ __forceinline__ void load(const T *row, int col, int, int, float2 *p) {
+    unpack(*reinterpret_cast<const uint4 *>(row + col), p);
+  }
+  static __device__ __forceinline__ void store(T *row, int col, int, int, const float2 *p) {
+    *reinterpret_cast<uint4 *>(row + col) = pack16<T>(reinterpret_cast<const float *>(p));
+  }
+  static __device__ __forceinline__ void mask(int, int, int, float2 *) {}
 };
 template <typename T>
-struct Raw<T, 1> {
-  T v;
-  __device__ __forceinline__ void load(const T *p) { v = *p; }
-  __device__ __forceinline__ void get(float *f) const { f[0] = Elem<T>::to_f(v); }
-  static __device__ __forceinline__ void put(T *p, const float *f) { *p = Elem<T>::from_f(f[0]); }
+struct Chunk<T, 1> {
+  static constexpr int H = 1, SPAN = 2;
+  static __device__ __forceinline__ void load(const T *row, int col, int tpr, int d, float2 *p) {
+    p->x = Elem<T>::load(row + col);
+    p->y = col + tpr < d ? Elem<T>::load(row + col + tpr) : 0.f;
+  }
+  static __device__ __forceinline__ void store(T *row, int col, int tpr, int d, const float2 *p) {
+    row[col] = Elem<T>::from_f(p->x);
+    if (col + tpr < d) row[col + tpr] = Elem<T>::from_f(p->y);
+  }
+  // clears the second element where there is none
+  static __device__ __forceinline__ void mask(int col, int tpr, int d, float2 *p) {
+    if (col + tpr >= d) p->y = 0.f;
+  }
 };
 
-// Sum over the group: the warp, or the CTA through one of two alternating
-// buffers (a buffer is written again only after the barrier of the sum in
-// between, which every reader of it has reached).
+__device__ __forceinline__ void copy16_async(uint4 *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Sum over the group of `warps` warps this warp belongs to (its warps are
+// neighbours; every thread of the CTA takes part): a butterfly, then one over
+// the warps' sums, which pass through one of two alternating buffers (a buffer
+// is written again only after the barrier of the sum in between, which every
+// reader of it has reached).
 template <bool WARP>
-__device__ __forceinline__ float2 group_sum(float a, float b, float2 (*buf)[32], int &turn) {
+__device__ __forceinline__ float group_sum(float a, float (*buf)[32], int &turn, int warps) {
+  a = warp_sum_xor(a);
+  if (WARP) return a;
+  float *s = buf[turn];
+  turn ^= 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) s[warp] = a;
+  __syncthreads();
+  return warp_sum_xor(lane < warps ? s[warp / warps * warps + lane] : 0.f);
+}
+template <bool WARP>
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2 (*buf)[32], int &turn,
+                                             int first, int warps) {
   a = warp_sum_xor(a);
   b = warp_sum_xor(b);
   if (WARP) return make_float2(a, b);
   float2 *s = buf[turn];
   turn ^= 1;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(a, b);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) s[warp] = make_float2(a, b);
   __syncthreads();
-  float2 r = s[0];
-  const int nw = blockDim.x >> 5;
-  for (int w = 1; w < nw; ++w) {
-    r.x += s[w].x;
-    r.y += s[w].y;
-  }
-  return r;
+  const float2 r = lane < warps ? s[first + lane] : make_float2(0.f, 0.f);
+  return make_float2(warp_sum_xor(r.x), warp_sum_xor(r.y));
 }
 
+// Rows of a CTA: `groups` groups of tpr threads take neighbouring rows.
 template <typename T, int VEC, int VPT, bool WARP>
-__global__ void __launch_bounds__(N_MAX_THREADS)
+__global__ void __launch_bounds__(N_FWD_THREADS)
 norm_kernel(moe_norm_config c, const T *__restrict__ x, const T *__restrict__ gamma,
             const T *__restrict__ beta, T *__restrict__ y, float *__restrict__ mean_out,
-            float *__restrict__ rstd_out) {
-  __shared__ float2 buf[2][32];
-  const int tpr = WARP ? 32 : blockDim.x, tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int groups = WARP ? blockDim.x >> 5 : 1, group = WARP ? threadIdx.x >> 5 : 0;
-  const int d = c.d;
-  const float df = (float)d;
-  int turn = 0;
-  Raw<T, VEC> raw[VPT], ga[VPT], be[VPT];
+            float *__restrict__ rstd_out, int tpr, int groups) {
+  extern __shared__ __align__(16) uint4 ring[];   // [stage][chunk][thread]
+  __shared__ float buf[2][32];
+  using C = Chunk<T, VEC>;
+  constexpr bool RING = VEC > 1;
+  constexpr int NC = VPT * VEC / C::SPAN, H = C::H;
+  const int group = WARP ? threadIdx.x >> 5 : threadIdx.x / tpr;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x - group * tpr;
+  const int d = c.d, nthr = blockDim.x, warps = tpr >> 5;
+  const float inv_d = 1.f / (float)d;
+  int turn = 0, stage = 0;
   const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t r = (int64_t)blockIdx.x * groups + group;
+  const int64_t first = (int64_t)blockIdx.x * groups;
+  auto col_of = [&](int i) { return VEC > 1 ? (tid + i * tpr) * VEC : tid + 2 * i * tpr; };
+  auto fill = [&](int64_t r, int st) {
+    if (r < c.rows) {
+      const T *row = x + r * c.ldx;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int col = (tid + i * tpr) * VEC;
-    if (col < d) {
-      if (r < c.rows) raw[i].load(x + r * c.ldx + col);
-      ga[i].load(gamma + col);
-      if (beta) be[i].load(beta + col);
+      for (int i = 0; i < NC; ++i)
+        if (col_of(i) < d) copy16_async(&ring[(st * NC + i) * nthr + threadIdx.x], row + col_of(i));
     }
+    copy_commit();
+  };
+  if (RING) {
+    for (int st = 0; st < N_FWD_STAGES - 1; ++st) fill(first + group + st * step, st);
   }
-  for (; r < c.rows; r += step) {
-    float v[VPT][VEC];
-    float sum = 0.f;
+  for (int64_t r0 = first; r0 < c.rows; r0 += step) {
+    const int64_t r = r0 + group;
+    const bool live = r < c.rows;
+    float2 v[NC][H], sum = both(0.f), sq = both(0.f);
+    if (RING) {
+      // (the stage being filled was read in the iteration before, by this thread)
+      fill(r + (N_FWD_STAGES - 1) * step, stage == 0 ? N_FWD_STAGES - 1 : stage - 1);
+      copy_wait<N_FWD_STAGES - 1>();
+    }
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int col = (tid + i * tpr) * VEC;
-      if (col < d) {
-        raw[i].get(v[i]);
-        if (r + step < c.rows) raw[i].load(x + (r + step) * c.ldx + col);
+    for (int i = 0; i < NC; ++i) {
+      if (live && col_of(i) < d) {
+        if constexpr (RING) C::unpack(ring[(stage * NC + i) * nthr + threadIdx.x], v[i]);
+        else C::load(x + r * c.ldx, col_of(i), tpr, d, v[i]);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum += v[i][j];
+        for (int h = 0; h < H; ++h) sum = add2(sum, v[i][h]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < H; ++h) v[i][h] = both(0.f);
       }
     }
-    const float mean = group_sum<WARP>(sum, 0.f, buf, turn).x / df;
-    float sq = 0.f;
+    if (RING) stage = stage + 1 == N_FWD_STAGES ? 0 : stage + 1;
+    const float mean = group_sum<WARP>(sum.x + sum.y, buf, turn, warps) * inv_d;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if ((tid + i * tpr) * VEC < d) {
+    for (int i = 0; i < NC; ++i) {
+      if (col_of(i) < d) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          v[i][j] -= mean;
-          sq = fmaf(v[i][j], v[i][j], sq);
-        }
+        for (int h = 0; h < H; ++h) v[i][h] = add2(v[i][h], both(-mean));
+        C::mask(col_of(i), tpr, d, v[i]);
+#pragma unroll
+        for (int h = 0; h < H; ++h) sq = fma2(v[i][h], v[i][h], sq);
       }
     }
-    const float rstd = 1.f / sqrtf(group_sum<WARP>(sq, 0.f, buf, turn).x / df + c.eps);
+    const float var = group_sum<WARP>(sq.x + sq.y, buf, turn, warps) * inv_d;
+    const float rstd = rsqrtf(var + c.eps);
+    if (!live) continue;
+    T *out = y + r * c.ldy;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int col = (tid + i * tpr) * VEC;
-      if (col < d) {
-        float g[VEC], b[VEC];
-        ga[i].get(g);
+    for (int i = 0; i < NC; ++i) {
+      if (col_of(i) < d) {
+        // (gamma and beta come from L1: held in registers they would cost
+        // resident CTAs)
+        float2 g[H], b[H];
+        C::load(gamma, col_of(i), tpr, d, g);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) b[j] = 0.f;
-        if (beta) be[i].get(b);
+        for (int h = 0; h < H; ++h) b[h] = both(0.f);
+        if (beta) C::load(beta, col_of(i), tpr, d, b);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[i][j] = fmaf(v[i][j] * rstd, g[j], b[j]);
-        Raw<T, VEC>::put(y + r * c.ldy + col, v[i]);
+        for (int h = 0; h < H; ++h) v[i][h] = fma2(mul2(v[i][h], both(rstd)), g[h], b[h]);
+        C::store(out, col_of(i), tpr, d, v[i]);
       }
     }
     if (mean_out && tid == 0) {
@@ -135,101 +221,136 @@ norm_kernel(moe_norm_config c, const T *__restrict__ x, const T *__restrict__ ga
 // pg, pb: [gridDim.x][d] partial column sums (or the results themselves when
 // there is one CTA); either may be nullptr.
 template <typename T, int VEC, int VPT, bool WARP>
-__global__ void __launch_bounds__(N_MAX_THREADS)
+__global__ void __launch_bounds__(N_BWD_THREADS)
 norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__restrict__ gamma,
                      const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
                      const T *__restrict__ dy, T *__restrict__ dx, float *__restrict__ pg,
-                     float *__restrict__ pb) {
+                     float *__restrict__ pb, int tpr, int groups) {
+  extern __shared__ __align__(16) uint4 ring[];   // [stage][chunk][x, dy][thread]
   __shared__ float2 buf[2][32];
-  __shared__ float cols[WARP ? 8 * 32 * VPT * VEC : 1];
-  const int tpr = WARP ? 32 : blockDim.x, tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int groups = WARP ? blockDim.x >> 5 : 1, group = WARP ? threadIdx.x >> 5 : 0;
-  const int d = c.d;
-  const float df = (float)d;
-  int turn = 0;
-  Raw<T, VEC> rx[VPT], ry[VPT], ga[VPT];
-  float ag[VPT][VEC], ab[VPT][VEC];
+  using C = Chunk<T, VEC>;
+  constexpr bool RING = VEC > 1;
+  constexpr int STAGES = bwd_stages(VPT);
+  constexpr int NC = VPT * VEC / C::SPAN, H = C::H;
+  const int group = WARP ? threadIdx.x >> 5 : threadIdx.x / tpr;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x - group * tpr;
+  const int d = c.d, nthr = blockDim.x, warps = tpr >> 5, first_warp = group * warps;
+  const float inv_d = 1.f / (float)d;
+  int turn = 0, stage = 0;
+  float2 ga[NC][H], ag[NC][H], ab[NC][H];
+  auto col_of = [&](int i) { return VEC > 1 ? (tid + i * tpr) * VEC : tid + 2 * i * tpr; };
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (col_of(i) < d) C::load(gamma, col_of(i), tpr, d, ga[i]);
+#pragma unroll
+    for (int h = 0; h < H; ++h) ag[i][h] = ab[i][h] = both(0.f);
+  }
   const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t r = (int64_t)blockIdx.x * groups + group;
+  const int64_t first = (int64_t)blockIdx.x * groups;
+  auto fill = [&](int64_t r, int st) {
+    if (r < c.rows) {
+      const T *rx = x + r * c.ldx, *ry = dy + r * c.lddy;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int col = (tid + i * tpr) * VEC;
-    if (col < d) {
-      if (r < c.rows) {
-        rx[i].load(x + r * c.ldx + col);
-        ry[i].load(dy + r * c.lddy + col);
-      }
-      ga[i].load(gamma + col);
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) ag[i][j] = ab[i][j] = 0.f;
-  }
-  for (; r < c.rows; r += step) {
-    const float mean = mean_in[r], rstd = rstd_in[r];
-    float xh[VPT][VEC], w[VPT][VEC];
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int col = (tid + i * tpr) * VEC;
-      if (col < d) {
-        float g[VEC];
-        rx[i].get(xh[i]);
-        ry[i].get(w[i]);
-        ga[i].get(g);
-        if (r + step < c.rows) {
-          rx[i].load(x + (r + step) * c.ldx + col);
-          ry[i].load(dy + (r + step) * c.lddy + col);
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          xh[i][j] = (xh[i][j] - mean) * rstd;
-          ag[i][j] = fmaf(w[i][j], xh[i][j], ag[i][j]);
-          ab[i][j] += w[i][j];
-          w[i][j] *= g[j];
-          s1 += w[i][j];
-          s2 = fmaf(w[i][j], xh[i][j], s2);
+      for (int i = 0; i < NC; ++i) {
+        if (col_of(i) < d) {
+          uint4 *at = &ring[(st * NC + i) * 2 * nthr + threadIdx.x];
+          copy16_async(at, rx + col_of(i));
+          copy16_async(at + nthr, ry + col_of(i));
         }
       }
     }
-    const float2 s = group_sum<WARP>(s1, s2, buf, turn);
-    const float m1 = s.x / df, m2 = s.y / df;
+    copy_commit();
+  };
+  if (RING) {
+    for (int st = 0; st < STAGES - 1; ++st) fill(first + group + st * step, st);
+  }
+  float mean = 0.f, rstd = 0.f;
+  if (first + group < c.rows) {
+    mean = mean_in[first + group];
+    rstd = rstd_in[first + group];
+  }
+  for (int64_t r0 = first; r0 < c.rows; r0 += step) {
+    const int64_t r = r0 + group;
+    const bool live = r < c.rows;
+    float2 xh[NC][H], w[NC][H], s1 = both(0.f), s2 = both(0.f);
+    if (RING) {
+      fill(r + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+      copy_wait<STAGES - 1>();
+    }
+    float next_mean = 0.f, next_rstd = 0.f;
+    if (r + step < c.rows) {
+      next_mean = mean_in[r + step];
+      next_rstd = rstd_in[r + step];
+    }
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int col = (tid + i * tpr) * VEC;
-      if (col < d) {
+    for (int i = 0; i < NC; ++i) {
+      if (live && col_of(i) < d) {
+        if constexpr (RING) {
+          const uint4 *at = &ring[(stage * NC + i) * 2 * nthr + threadIdx.x];
+          C::unpack(at[0], xh[i]);
+          C::unpack(at[nthr], w[i]);
+        } else {
+          C::load(x + r * c.ldx, col_of(i), tpr, d, xh[i]);
+          C::load(dy + r * c.lddy, col_of(i), tpr, d, w[i]);
+        }
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) w[i][j] = rstd * (w[i][j] - m1 - xh[i][j] * m2);
-        Raw<T, VEC>::put(dx + r * c.lddx + col, w[i]);
+        for (int h = 0; h < H; ++h) {
+          // (an element that is not there has dy = 0)
+          xh[i][h] = mul2(add2(xh[i][h], both(-mean)), both(rstd));
+          ag[i][h] = fma2(w[i][h], xh[i][h], ag[i][h]);
+          ab[i][h] = add2(ab[i][h], w[i][h]);
+          w[i][h] = mul2(w[i][h], ga[i][h]);
+          s1 = add2(s1, w[i][h]);
+          s2 = fma2(w[i][h], xh[i][h], s2);
+        }
       }
     }
+    if (RING) stage = stage + 1 == STAGES ? 0 : stage + 1;
+    const float2 s = group_sum2<WARP>(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
+    const float2 m1 = both(-s.x * inv_d), m2 = both(-s.y * inv_d);
+    if (live) {
+      T *out = dx + r * c.lddx;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        if (col_of(i) < d) {
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            w[i][h] = mul2(fma2(xh[i][h], m2, add2(w[i][h], m1)), both(rstd));
+          C::store(out, col_of(i), tpr, d, w[i]);
+        }
+      }
+    }
+    mean = next_mean;
+    rstd = next_rstd;
   }
+  // the groups of the CTA meet in shared memory (the ring's, now read)
+  float *cols = reinterpret_cast<float *>(ring);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     float *part = which ? pb : pg;
     if (part == nullptr) continue;
     part += (int64_t)blockIdx.x * d;
-    if (WARP) {
-      __syncthreads();
+    const int width = tpr * VPT * VEC;
+    float *to = groups == 1 ? part : cols + group * width;
+    if (groups > 1) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < NC; ++i) {
+      if (col_of(i) < d) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          cols[group * 32 * VPT * VEC + (tid + i * 32) * VEC + j] = which ? ab[i][j] : ag[i][j];
-      __syncthreads();
-      for (int col = threadIdx.x; col < d; col += blockDim.x) {
-        float a = 0.f;
-        for (int g = 0; g < groups; ++g) a += cols[g * 32 * VPT * VEC + col];
-        part[col] = a;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int col = (tid + i * tpr) * VEC;
-        if (col < d) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) part[col + j] = which ? ab[i][j] : ag[i][j];
+        for (int h = 0; h < H; ++h) {
+          const float2 a = which ? ab[i][h] : ag[i][h];
+          to[col_of(i) + (VEC > 1 ? 2 * h : 0)] = a.x;
+          const int second = col_of(i) + (VEC > 1 ? 2 * h + 1 : tpr);
+          if (VEC > 1 || second < d) to[second] = a.y;
         }
       }
+    }
+    if (groups == 1) continue;
+    __syncthreads();
+    for (int col = threadIdx.x; col < d; col += nthr) {
+      float a = 0.f;
+      for (int g = 0; g < groups; ++g) a += cols[g * width + col];
+      part[col] = a;
     }
   }
 }
@@ -267,19 +388,19 @@ __global__ void __launch_bounds__(512)
 norm_wide_kernel(moe_norm_config c, const T *__restrict__ x, const T *__restrict__ gamma,
                  const T *__restrict__ beta, T *__restrict__ y, float *__restrict__ mean_out,
                  float *__restrict__ rstd_out) {
-  __shared__ float2 buf[2][32];
+  __shared__ float buf[2][32];
   int turn = 0;
   for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
     const T *xr = x + r * c.ldx;
     float sum = 0.f, sq = 0.f;
     for (int i = threadIdx.x; i < c.d; i += blockDim.x) sum += Elem<T>::load(xr + i);
-    const float mean = group_sum<false>(sum, 0.f, buf, turn).x / (float)c.d;
+    const float mean = group_sum<false>(sum, buf, turn, blockDim.x >> 5) / (float)c.d;
     for (int i = threadIdx.x; i < c.d; i += blockDim.x) {
       const float v = Elem<T>::load(xr + i) - mean;
       sq = fmaf(v, v, sq);
     }
     const float rstd =
-        1.f / sqrtf(group_sum<false>(sq, 0.f, buf, turn).x / (float)c.d + c.eps);
+        1.f / sqrtf(group_sum<false>(sq, buf, turn, blockDim.x >> 5) / (float)c.d + c.eps);
     for (int i = threadIdx.x; i < c.d; i += blockDim.x)
       y[r * c.ldy + i] = Elem<T>::from_f(
           fmaf((Elem<T>::load(xr + i) - mean) * rstd, Elem<T>::load(gamma + i),
@@ -307,7 +428,7 @@ norm_backward_wide_kernel(moe_norm_config c, const T *__restrict__ x, const T *_
       s1 += w;
       s2 = fmaf(w, (Elem<T>::load(xr + i) - mean) * rstd, s2);
     }
-    const float2 s = group_sum<false>(s1, s2, buf, turn);
+    const float2 s = group_sum2<false>(s1, s2, buf, turn, 0, blockDim.x >> 5);
     const float m1 = s.x / (float)c.d, m2 = s.y / (float)c.d;
     for (int i = threadIdx.x; i < c.d; i += blockDim.x) {
       const float w = Elem<T>::load(yr + i) * Elem<T>::load(gamma + i);
@@ -348,64 +469,83 @@ norm_columns_kernel(moe_norm_config c, const T *__restrict__ x, const float *__r
 }
 
 // ------------------------------------------------------------------- launch
+// Elements per thread: the forward keeps one row's values, the gradient four
+// per element (two of the row, two column sums) in at most 64 registers of
+// 1024 threads.
+template <typename T> constexpr int fwd_vpt(int vec) { return vec == 1 ? 16 : 4; }
+template <typename T> constexpr int bwd_vpt(int vec) { return 8 / vec; }
+
 // Threads per row for rows of d elements held as vpt pieces of vec per thread
-// (0: too wide).
-int threads_of(int d, int vec, int vpt) {
+// (0: wider than `most` threads hold).
+int threads_of(int d, int vec, int vpt, int most) {
   const int64_t per_warp = (int64_t)32 * vec * vpt;
   const int64_t warps = (d + per_warp - 1) / per_warp;
-  return warps * 32 <= N_MAX_THREADS ? (int)warps * 32 : 0;
+  return warps * 32 <= most ? (int)warps * 32 : 0;
 }
-
-constexpr int kScalarPieces = 16;
-template <typename T> constexpr int fwd_pieces() { return 4; }
-// the gradient's column sums take two registers per element: at most 16
-// elements per thread
-template <typename T> constexpr int bwd_pieces() { return sizeof(T) == 2 ? 2 : 4; }
 
 bool by_vectors(const moe_norm_config &c, int vec, bool backward) {
   return c.d % vec == 0 && c.ldx % vec == 0 &&
          (backward ? c.lddy % vec == 0 && c.lddx % vec == 0 : c.ldy % vec == 0);
 }
 
-// CTAs that walk the rows: `ctas_per_sm` per SM at most.
-unsigned grid_of(int64_t rows, int groups, int most) {
+// CTAs that walk the rows, `most` at most.
+int grid_of(int64_t rows, int groups, int64_t most) {
   const int64_t want = (rows + groups - 1) / groups;
-  return (unsigned)(want < most ? want : most);
+  return (int)(want < most ? want : most);
 }
 
-// Partial rows of the column sums.
+// How the gradient covers the rows.  Short rows share a CTA, up to 512 threads
+// of them (two CTAs of that size fit an SM).
 struct BwdPlan {
-  int vec, threads;   // threads per row, 0: the wide kernels
+  int vec, tpr;   // threads per row, 0: the wide kernels
   int groups, parts;
 };
 BwdPlan plan_backward(const moe_norm_config &c) {
   BwdPlan p;
   const int v16 = c.dtype == MOE_F32 ? 4 : 8;
   p.vec = by_vectors(c, v16, true) ? v16 : 1;
-  const int pieces = p.vec == 1 ? kScalarPieces : c.dtype == MOE_F32 ? bwd_pieces<float>()
-                                                                     : bwd_pieces<__nv_bfloat16>();
-  p.threads = threads_of(c.d, p.vec, pieces);
-  p.groups = p.threads == 32 ? 8 : 1;
-  if (p.threads) {
-    p.parts = (int)grid_of(c.rows, p.groups, N_MAX_PARTS);
-  } else {
-    p.parts = (int)grid_of(c.rows, 64, N_MAX_PARTS);
-  }
+  p.tpr = threads_of(c.d, p.vec, 8 / p.vec, N_BWD_THREADS);
+  p.groups = p.tpr == 0 ? 64 : p.tpr <= 512 ? 512 / p.tpr : 1;
+  // few rows: as many CTAs as there are, rather than full ones
+  while (p.tpr && p.groups > 1 && (c.rows + p.groups - 1) / p.groups < N_MAX_PARTS) p.groups /= 2;
+  p.parts = grid_of(c.rows, p.groups, N_MAX_PARTS);
   return p;
 }
 
-template <typename T, int VEC, int VPT>
+template <typename T, int VEC, int VPT, bool WARP>
 cudaError_t fwd(const moe_norm_config &c, const T *x, const T *gamma, const T *beta, T *y,
-                float *mean, float *rstd, int threads, cudaStream_t s) {
-  if (threads == 32) {
-    norm_kernel<T, VEC, VPT, true><<<grid_of(c.rows, 8, num_sms() * 4), 256, 0, s>>>(
-        c, x, gamma, beta, y, mean, rstd);
-  } else {
-    const int per_sm = threads > 1024 / 2 ? 1 : 1024 / threads;
-    norm_kernel<T, VEC, VPT, false><<<grid_of(c.rows, 1, num_sms() * per_sm), threads, 0, s>>>(
-        c, x, gamma, beta, y, mean, rstd);
+                float *mean, float *rstd, int tpr, cudaStream_t s) {
+  auto kernel = norm_kernel<T, VEC, VPT, WARP>;
+  const int groups = tpr <= 256 ? 256 / tpr : 1, threads = tpr * groups;
+  const size_t smem = VEC > 1 ? (size_t)N_FWD_STAGES * VPT * threads * 16 : 0;
+  static int resident[N_FWD_THREADS / 32 + 1] = {};   // CTAs per SM by warps per CTA
+  int &ctas = resident[threads / 32];
+  if (ctas == 0) {
+    cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        VEC > 1 ? N_FWD_STAGES * VPT * N_FWD_THREADS * 16 : 0);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+    if (ctas < 1) ctas = 1;
   }
+  kernel<<<grid_of(c.rows, groups, (int64_t)num_sms() * ctas), threads, smem, s>>>(
+      c, x, gamma, beta, y, mean, rstd, tpr, groups);
   return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t fwd_vec(const moe_norm_config &c, const T *x, const T *gamma, const T *beta, T *y,
+                    float *mean, float *rstd, cudaStream_t s) {
+  constexpr int VPT = fwd_vpt<T>(VEC);
+  const int tpr = threads_of(c.d, VEC, VPT, N_FWD_THREADS);
+  if (tpr == 0) {
+    norm_wide_kernel<T><<<grid_of(c.rows, 1, (int64_t)num_sms() * 4), 512, 0, s>>>(
+        c, x, gamma, beta, y, mean, rstd);
+    return cudaGetLastError();
+  }
+  return tpr == 32 ? fwd<T, VEC, VPT, true>(c, x, gamma, beta, y, mean, rstd, tpr, s)
+                   : fwd<T, VEC, VPT, false>(c, x, gamma, beta, y, mean, rstd, tpr, s);
 }
 
 template <typename T>
@@ -414,26 +554,38 @@ cudaError_t fwd_typed(const moe_norm_config &c, const void *xv, const void *gv, 
   const T *x = (const T *)xv, *gamma = (const T *)gv, *beta = (const T *)bv;
   T *y = (T *)yv;
   constexpr int V = Vec16<T>::N;
-  const bool vec = by_vectors(c, V, false);
-  const int threads = threads_of(c.d, vec ? V : 1, vec ? fwd_pieces<T>() : kScalarPieces);
-  if (threads == 0) {
-    norm_wide_kernel<T><<<grid_of(c.rows, 1, num_sms() * 4), 512, 0, s>>>(c, x, gamma, beta, y,
-                                                                          mean, rstd);
-    return cudaGetLastError();
-  }
-  if (vec) return fwd<T, V, fwd_pieces<T>()>(c, x, gamma, beta, y, mean, rstd, threads, s);
-  return fwd<T, 1, kScalarPieces>(c, x, gamma, beta, y, mean, rstd, threads, s);
+  return by_vectors(c, V, false) ? fwd_vec<T, V>(c, x, gamma, beta, y, mean, rstd, s)
+                                 : fwd_vec<T, 1>(c, x, gamma, beta, y, mean, rstd, s);
 }
 
-template <typename T, int VEC, int VPT>
-void bwd(const moe_norm_config &c, const BwdPlan &p, const T *x, const T *gamma, const float *mean,
-         const float *rstd, const T *dy, T *dx, float *pg, float *pb, cudaStream_t s) {
-  if (p.threads == 32)
-    norm_backward_kernel<T, VEC, VPT, true><<<p.parts, 256, 0, s>>>(c, x, gamma, mean, rstd, dy, dx,
-                                                                    pg, pb);
-  else
-    norm_backward_kernel<T, VEC, VPT, false><<<p.parts, p.threads, 0, s>>>(c, x, gamma, mean, rstd,
-                                                                           dy, dx, pg, pb);
+template <typename T, int VEC, bool WARP>
+cudaError_t bwd(const moe_norm_config &c, const BwdPlan &p, const T *x, const T *gamma,
+                const float *mean, const float *rstd, const T *dy, T *dx, float *pg, float *pb,
+                cudaStream_t s) {
+  constexpr int VPT = bwd_vpt<T>(VEC);
+  auto kernel = norm_backward_kernel<T, VEC, VPT, WARP>;
+  const int threads = p.tpr * p.groups;
+  const size_t ring = VEC > 1 ? (size_t)bwd_stages(VPT) * VPT * 2 * threads * 16 : 0;
+  const size_t cols = p.groups > 1 ? (size_t)threads * VPT * VEC * 4 : 0;
+  static bool set = false;
+  if (!set) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             6 * 2 * N_BWD_THREADS * 16);
+    if (e != cudaSuccess) return e;
+    set = true;
+  }
+  kernel<<<p.parts, threads, ring > cols ? ring : cols, s>>>(c, x, gamma, mean, rstd, dy, dx, pg,
+                                                             pb, p.tpr, p.groups);
+  return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t bwd_vec(const moe_norm_config &c, const BwdPlan &p, const T *x, const T *gamma,
+                    const float *mean, const float *rstd, const T *dy, T *dx, float *pg, float *pb,
+                    cudaStream_t s) {
+  return p.tpr == 32 ? bwd<T, VEC, true>(c, p, x, gamma, mean, rstd, dy, dx, pg, pb, s)
+                     : bwd<T, VEC, false>(c, p, x, gamma, mean, rstd, dy, dx, pg, pb, s);
 }
 
 template <typename T>
@@ -447,18 +599,19 @@ cudaError_t bwd_typed(const moe_norm_config &c, const void *xv, const void *gv, 
   const bool direct = p.parts == 1;
   if (dgamma) pg = direct ? dgamma : (float *)scratch;
   if (dbeta) pb = direct ? dbeta : (float *)scratch + (int64_t)p.parts * c.d;
-  if (p.threads == 0) {
-    norm_backward_wide_kernel<T><<<grid_of(c.rows, 1, num_sms() * 4), 512, 0, s>>>(
+  cudaError_t e;
+  if (p.tpr == 0) {
+    norm_backward_wide_kernel<T><<<grid_of(c.rows, 1, (int64_t)num_sms() * 4), 512, 0, s>>>(
         c, x, gamma, mean, rstd, dy, dx);
     if (pg || pb)
       norm_columns_kernel<T><<<dim3((c.d + 31) / 32, p.parts), 256, 0, s>>>(c, x, mean, rstd, dy,
                                                                             pg, pb);
+    e = cudaGetLastError();
   } else if (p.vec > 1) {
-    bwd<T, Vec16<T>::N, bwd_pieces<T>()>(c, p, x, gamma, mean, rstd, dy, dx, pg, pb, s);
+    e = bwd_vec<T, Vec16<T>::N>(c, p, x, gamma, mean, rstd, dy, dx, pg, pb, s);
   } else {
-    bwd<T, 1, kScalarPieces>(c, p, x, gamma, mean, rstd, dy, dx, pg, pb, s);
+    e = bwd_vec<T, 1>(c, p, x, gamma, mean, rstd, dy, dx, pg, pb, s);
   }
-  cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && !direct && (pg || pb))
     e = launch_pdl(column_sum_kernel, dim3((c.d + 31) / 32, 2), dim3(256), 0, s,
                    (const float *)pg, (const float *)pb, p.parts, (int)c.d, dgamma, dbeta);
