@@ -23,11 +23,11 @@
 namespace moe {
 namespace {
 
-constexpr int N_MAX_PARTS = 304;   // partial rows of the column sums (two CTAs per SM)
-constexpr int N_FWD_THREADS = 512, N_BWD_THREADS = 1024;
+constexpr int N_MAX_PARTS = 152;   // partial rows of the column sums: one CTA per SM
+constexpr int N_FWD_THREADS = 512, N_BWD_THREADS = 512;
 constexpr int N_FWD_STAGES = 3;
-// rows in a thread's ring: 1024 threads hold 192 KB of them
-constexpr int bwd_stages(int vpt) { return vpt == 1 ? 6 : 3; }
+// rows in a thread's ring: 512 threads hold 192 KB of them
+constexpr int bwd_stages(int vpt) { return vpt == 2 ? 6 : 3; }
 
 // ------------------------------------------------------------ pairs of fp32
 // Two fp32 values per instruction (each half rounded as on its own): the
@@ -113,19 +113,30 @@ __device__ __forceinline__ float group_sum(float a, float (*buf)[32], int &turn,
   __syncthreads();
   return warp_sum_xor(lane < warps ? s[warp / warps * warps + lane] : 0.f);
 }
+// Two sums at once: after one exchange the lower half warp carries a and the
+// upper one b, so that two butterflies cost the shuffles of one.
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 template <bool WARP>
 __device__ __forceinline__ float2 group_sum2(float a, float b, float2 (*buf)[32], int &turn,
                                              int first, int warps) {
-  a = warp_sum_xor(a);
-  b = warp_sum_xor(b);
-  if (WARP) return make_float2(a, b);
-  float2 *s = buf[turn];
-  turn ^= 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) s[warp] = make_float2(a, b);
-  __syncthreads();
-  const float2 r = lane < warps ? s[first + lane] : make_float2(0.f, 0.f);
-  return make_float2(warp_sum_xor(r.x), warp_sum_xor(r.y));
+  const bool upper = lane >= 16;
+  float v = half_sum((upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16));
+  if (!WARP) {
+    float *s = reinterpret_cast<float *>(buf[turn]);   // [which][warp]
+    turn ^= 1;
+    if ((lane & 15) == 0) s[(lane & 16) * 2 + warp] = v;
+    __syncthreads();
+    const float *mine = s + (lane & 16) * 2 + first;
+    const int i = lane & 15;
+    v = half_sum((i < warps ? mine[i] : 0.f) + (i + 16 < warps ? mine[i + 16] : 0.f));
+  }
+  const float other = __shfl_xor_sync(0xffffffffu, v, 16);
+  return upper ? make_float2(other, v) : make_float2(v, other);
 }
 
 // Rows of a CTA: `groups` groups of tpr threads take neighbouring rows.
@@ -237,6 +248,7 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
   const int d = c.d, nthr = blockDim.x, warps = tpr >> 5, first_warp = group * warps;
   const float inv_d = 1.f / (float)d;
   int turn = 0, stage = 0;
+  pdl_launch_dependents();   // (the column sums wait for this grid to end)
   float2 ga[NC][H], ag[NC][H], ab[NC][H];
   auto col_of = [&](int i) { return VEC > 1 ? (tid + i * tpr) * VEC : tid + 2 * i * tpr; };
 #pragma unroll
@@ -247,9 +259,13 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
   }
   const int64_t step = (int64_t)gridDim.x * groups;
   const int64_t first = (int64_t)blockIdx.x * groups;
-  auto fill = [&](int64_t r, int st) {
-    if (r < c.rows) {
-      const T *rx = x + r * c.ldx, *ry = dy + r * c.lddy;
+  // rows still to come, and where the next copies and the next result go
+  int64_t ahead = first + group;
+  const T *rx = x + ahead * c.ldx, *ry = dy + ahead * c.lddy;
+  T *out = dx + ahead * c.lddx;
+  const int64_t sx = step * c.ldx, sy = step * c.lddy, so = step * c.lddx;
+  auto fill = [&](int st) {
+    if (ahead < c.rows) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         if (col_of(i) < d) {
@@ -260,9 +276,12 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
       }
     }
     copy_commit();
+    ahead += step;
+    rx += sx;
+    ry += sy;
   };
   if (RING) {
-    for (int st = 0; st < STAGES - 1; ++st) fill(first + group + st * step, st);
+    for (int st = 0; st < STAGES - 1; ++st) fill(st);
   }
   float mean = 0.f, rstd = 0.f;
   if (first + group < c.rows) {
@@ -274,7 +293,7 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
     const bool live = r < c.rows;
     float2 xh[NC][H], w[NC][H], s1 = both(0.f), s2 = both(0.f);
     if (RING) {
-      fill(r + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+      fill(stage == 0 ? STAGES - 1 : stage - 1);
       copy_wait<STAGES - 1>();
     }
     float next_mean = 0.f, next_rstd = 0.f;
@@ -309,7 +328,6 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
     const float2 s = group_sum2<WARP>(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
     const float2 m1 = both(-s.x * inv_d), m2 = both(-s.y * inv_d);
     if (live) {
-      T *out = dx + r * c.lddx;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         if (col_of(i) < d) {
@@ -320,6 +338,7 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
         }
       }
     }
+    out += so;
     mean = next_mean;
     rstd = next_rstd;
   }
@@ -355,12 +374,12 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
   }
 }
 
-// out[which][col] = sum over count partial rows, in a fixed order: warp w of
-// eight adds rows w, w + 8, ..., then the eight sums are added.
-__global__ void __launch_bounds__(256)
+// out[which][col] = sum over count partial rows, in a fixed order: warp w of 32
+// adds rows w, w + 32, ..., then a butterfly adds the warps' sums.
+__global__ void __launch_bounds__(1024)
 column_sum_kernel(const float *__restrict__ pg, const float *__restrict__ pb, int count, int d,
                   float *__restrict__ dgamma, float *__restrict__ dbeta) {
-  __shared__ float s[8][33];
+  __shared__ float s[32][33];
   const float *part = blockIdx.y ? pb : pg;
   float *out = blockIdx.y ? dbeta : dgamma;
   pdl_wait();
@@ -370,15 +389,12 @@ column_sum_kernel(const float *__restrict__ pg, const float *__restrict__ pb, in
   float a = 0.f;
   if (col < d) {
 #pragma unroll 8
-    for (int r = warp; r < count; r += 8) a += part[(int64_t)r * d + col];
+    for (int r = warp; r < count; r += 32) a += part[(int64_t)r * d + col];
   }
   s[warp][lane] = a;
   __syncthreads();
-  if (warp == 0 && col < d) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) a += s[w][lane];
-    out[col] = a;
-  }
+  a = warp_sum_xor(s[lane][warp]);
+  if (lane == 0 && blockIdx.x * 32 + warp < d) out[blockIdx.x * 32 + warp] = a;
 }
 
 // Rows wider than a CTA holds in registers: one CTA per row, reading it again
@@ -469,11 +485,12 @@ norm_columns_kernel(moe_norm_config c, const T *__restrict__ x, const float *__r
 }
 
 // ------------------------------------------------------------------- launch
-// Elements per thread: the forward keeps one row's values, the gradient four
-// per element (two of the row, two column sums) in at most 64 registers of
-// 1024 threads.
-template <typename T> constexpr int fwd_vpt(int vec) { return vec == 1 ? 16 : 4; }
-template <typename T> constexpr int bwd_vpt(int vec) { return 8 / vec; }
+// Pieces per thread.  The gradient keeps five values per element (two of the
+// row, gamma, two column sums): 16 elements in 128 registers of 512 threads.
+// (8 elements in 64 registers of 1024 threads pay the sums over the row twice
+// as often: 177 us against 148 at 16384 x 7168 bf16.)
+constexpr int fwd_vpt(int vec) { return vec == 1 ? 16 : 4; }
+constexpr int bwd_vpt(int vec) { return 16 / vec; }
 
 // Threads per row for rows of d elements held as vpt pieces of vec per thread
 // (0: wider than `most` threads hold).
@@ -494,8 +511,8 @@ int grid_of(int64_t rows, int groups, int64_t most) {
   return (int)(want < most ? want : most);
 }
 
-// How the gradient covers the rows.  Short rows share a CTA, up to 512 threads
-// of them (two CTAs of that size fit an SM).
+// How the gradient covers the rows.  Short rows share a CTA of up to 512
+// threads, fewer where there are SMs to spare.
 struct BwdPlan {
   int vec, tpr;   // threads per row, 0: the wide kernels
   int groups, parts;
@@ -504,10 +521,9 @@ BwdPlan plan_backward(const moe_norm_config &c) {
   BwdPlan p;
   const int v16 = c.dtype == MOE_F32 ? 4 : 8;
   p.vec = by_vectors(c, v16, true) ? v16 : 1;
-  p.tpr = threads_of(c.d, p.vec, 8 / p.vec, N_BWD_THREADS);
-  p.groups = p.tpr == 0 ? 64 : p.tpr <= 512 ? 512 / p.tpr : 1;
-  // few rows: as many CTAs as there are, rather than full ones
-  while (p.tpr && p.groups > 1 && (c.rows + p.groups - 1) / p.groups < N_MAX_PARTS) p.groups /= 2;
+  p.tpr = threads_of(c.d, p.vec, bwd_vpt(p.vec), N_BWD_THREADS);
+  p.groups = p.tpr == 0 ? 64 : N_BWD_THREADS / p.tpr;
+  while (p.tpr && p.groups > 1 && c.rows <= (int64_t)(p.groups / 2) * N_MAX_PARTS) p.groups /= 2;
   p.parts = grid_of(c.rows, p.groups, N_MAX_PARTS);
   return p;
 }
@@ -537,7 +553,7 @@ cudaError_t fwd(const moe_norm_config &c, const T *x, const T *gamma, const T *b
 template <typename T, int VEC>
 cudaError_t fwd_vec(const moe_norm_config &c, const T *x, const T *gamma, const T *beta, T *y,
                     float *mean, float *rstd, cudaStream_t s) {
-  constexpr int VPT = fwd_vpt<T>(VEC);
+  constexpr int VPT = fwd_vpt(VEC);
   const int tpr = threads_of(c.d, VEC, VPT, N_FWD_THREADS);
   if (tpr == 0) {
     norm_wide_kernel<T><<<grid_of(c.rows, 1, (int64_t)num_sms() * 4), 512, 0, s>>>(
@@ -562,7 +578,7 @@ template <typename T, int VEC, bool WARP>
 cudaError_t bwd(const moe_norm_config &c, const BwdPlan &p, const T *x, const T *gamma,
                 const float *mean, const float *rstd, const T *dy, T *dx, float *pg, float *pb,
                 cudaStream_t s) {
-  constexpr int VPT = bwd_vpt<T>(VEC);
+  constexpr int VPT = bwd_vpt(VEC);
   auto kernel = norm_backward_kernel<T, VEC, VPT, WARP>;
   const int threads = p.tpr * p.groups;
   const size_t ring = VEC > 1 ? (size_t)bwd_stages(VPT) * VPT * 2 * threads * 16 : 0;
@@ -571,7 +587,7 @@ cudaError_t bwd(const moe_norm_config &c, const BwdPlan &p, const T *x, const T 
   if (!set) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             6 * 2 * N_BWD_THREADS * 16);
+                             6 * 4 * N_BWD_THREADS * 16);
     if (e != cudaSuccess) return e;
     set = true;
   }
@@ -613,7 +629,7 @@ cudaError_t bwd_typed(const moe_norm_config &c, const void *xv, const void *gv, 
     e = bwd_vec<T, 1>(c, p, x, gamma, mean, rstd, dy, dx, pg, pb, s);
   }
   if (e == cudaSuccess && !direct && (pg || pb))
-    e = launch_pdl(column_sum_kernel, dim3((c.d + 31) / 32, 2), dim3(256), 0, s,
+    e = launch_pdl(column_sum_kernel, dim3((c.d + 31) / 32, 2), dim3(1024), 0, s,
                    (const float *)pg, (const float *)pb, p.parts, (int)c.d, dgamma, dbeta);
   return e;
 }
