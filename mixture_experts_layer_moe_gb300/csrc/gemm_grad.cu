@@ -26,6 +26,15 @@
 // visible to the async proxy, and the first CTA's fixer, once it has heard
 // from the second's, completes the stage's barrier that the MMA waits on.
 //
+// Few tiles (a router's gradient: experts x d) leave SM pairs idle.  Then each
+// segment is cut into `splits` runs of rows: the tiles of a run store fp32
+// partial sums, and a second launch adds them in order and rounds once.
+//
+// A_K: the same tile for out[t][c] = sum_k A[t][k] B[k][c] over one segment,
+// A's reduction index contiguous (the rows' share of a router's gradient: short
+// reductions, where the store of the result is the work, and this epilogue's
+// packed stores are what that needs).
+//
 // Roles (persistent, one CTA per SM, clusters of two): warp 0 TMA producer in
 // both CTAs, warp 1 of the first CTA issues the MMAs into two accumulators of
 // 256 columns, warps 2-9 drain them (two warps per lane quarter, taking turns
@@ -72,6 +81,7 @@ struct GArgs {
   int M[kMaxGradProblems], N[kMaxGradProblems];
   int first[kMaxGradProblems + 1];   // an expert's tiles before problem i
   int width;                         // output columns per tile
+  int splits;                        // runs of rows per segment
   int *status;
 };
 struct GMaps {
@@ -80,13 +90,16 @@ struct GMaps {
 
 struct GTile {
   int e, prob, m0, c0, nc, beg, len;   // nc columns from c0
+  int z;                               // the output matrix
 };
 
+template <bool SPLIT>
 __device__ __forceinline__ GTile g_decode(const GShared &sh, const GArgs &args, int t) {
   GTile tl;
   const int per = args.first[args.problems];
-  tl.e = t / per;
-  int r = t - tl.e * per;
+  const int z = t / per;               // the expert, or expert * splits + run
+  tl.e = SPLIT ? z / args.splits : z;
+  int r = t - z * per;
   tl.prob = 0;
   while (tl.prob + 1 < args.problems && r >= args.first[tl.prob + 1]) ++tl.prob;
   r -= args.first[tl.prob];
@@ -97,6 +110,14 @@ __device__ __forceinline__ GTile g_decode(const GShared &sh, const GArgs &args, 
   tl.nc = min(args.width, args.N[tl.prob] - tl.c0);
   tl.beg = sh.offs[tl.e];
   tl.len = sh.offs[tl.e + 1] - tl.beg;
+  tl.z = z;
+  if (SPLIT) {
+    // runs of whole k-blocks
+    const int run = ((tl.len + args.splits - 1) / args.splits + GK - 1) / GK * GK;
+    const int from = min(tl.len, (z - tl.e * args.splits) * run);
+    tl.beg += from;
+    tl.len = min(run, tl.len - from);
+  }
   return tl;
 }
 
@@ -109,6 +130,7 @@ __device__ __forceinline__ uint32_t bf16x2_bits(uint32_t lo, uint32_t hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+template <bool A_K, bool SPLIT>
 __global__ void __launch_bounds__(G_THREADS, 1)
 gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GArgs args) {
   extern __shared__ uint8_t dyn_smem[];
@@ -151,7 +173,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
   cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem_base = sh.tmem_base;
-  const int num_tiles = sh.bad ? 0 : E * args.first[args.problems];
+  const int num_tiles = sh.bad ? 0 : E * args.splits * args.first[args.problems];
   if (sh.bad && rank == 0 && threadIdx.x == 0) set_status(args.status, MOE_ERR_BAD_INDEX, -1);
   volatile int *abort = &sh.abort;
 
@@ -167,7 +189,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
       const uint32_t full0 = map_to_rank(tc::smem_u32(&sh.full[0]), 0);
       const uint32_t tail0 = map_to_rank(tc::smem_u32(&sh.tail_full[0]), rank);
       for (int t = pair; t < num_tiles && !*abort; t += n_pairs) {
-        const GTile tl = g_decode(sh, args, t);
+        const GTile tl = g_decode<SPLIT>(sh, args, t);
         const int half = ((tl.nc + 15) & ~15) >> 1;       // output columns staged by each CTA
         const bool two = half > 64;                       // one or two boxes of them
         const uint32_t bytes = (uint32_t)(two ? 4 : 3) * G_BOX;
@@ -181,7 +203,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
           used |= bit;
           used_phase = phase ? used_phase | bit : used_phase & ~bit;
           used_tail &= ~bit;
-          if (end - q < GK && ((end - q) & 15) != 0) {
+          if (!A_K && end - q < GK && ((end - q) & 15) != 0) {
             bar = tail0 + (uint32_t)stage * 8;
             tc::mbar_arrive_expect_tx(&sh.tail_full[stage], bytes);
             used_tail |= bit;
@@ -192,8 +214,12 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
           }
           uint8_t *sb = smem + stage * G_STAGE;
           tma2_load_2d(mb, bar, sb, c, q);
-          tma2_load_2d(ma, bar, sb + 2 * G_BOX, m, q);
-          tma2_load_2d(ma, bar, sb + 3 * G_BOX, m + 64, q);
+          if constexpr (A_K) {
+            tma2_load_2d(ma, bar, sb + 2 * G_BOX, q, m);
+          } else {
+            tma2_load_2d(ma, bar, sb + 2 * G_BOX, m, q);
+            tma2_load_2d(ma, bar, sb + 3 * G_BOX, m + 64, q);
+          }
           if (two) tma2_load_2d(mb, bar, sb + G_BOX, c + 64, q);
           if (++stage == GS) { stage = 0; phase ^= 1u; }
         }
@@ -216,13 +242,16 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
       uint32_t phase = 0;
       int local = 0;
       bool ok = true;
-      const uint64_t desc = tc::smem_desc_sw128_mn(tc::smem_u32(smem), G_BOX);
-      const uint32_t desc_lo = (uint32_t)desc, desc_hi = (uint32_t)(desc >> 32);
+      const uint32_t sa0 = tc::smem_u32(smem) + 2 * G_BOX;
+      const uint64_t b_desc = tc::smem_desc_sw128_mn(tc::smem_u32(smem), G_BOX);
+      const uint64_t a_desc = A_K ? tc::smem_desc_sw128(sa0) : tc::smem_desc_sw128_mn(sa0, G_BOX);
+      const uint32_t b_lo = (uint32_t)b_desc, b_hi = (uint32_t)(b_desc >> 32);
+      const uint32_t a_lo = (uint32_t)a_desc, a_hi = (uint32_t)(a_desc >> 32);
       for (int t = pair; t < num_tiles && ok && !*abort; t += n_pairs) {
-        const GTile tl = g_decode(sh, args, t);
+        const GTile tl = g_decode<SPLIT>(sh, args, t);
         if (tl.len == 0) continue;
         const uint32_t idesc = tc::idesc_bf16_f32(2 * GM, (tl.nc + 15) & ~15) |
-                               tc::kIdescAMajorMN | tc::kIdescBMajorMN;
+                               (A_K ? 0u : tc::kIdescAMajorMN) | tc::kIdescBMajorMN;
         const int acc = local & 1;
         if (!mbar_wait_cluster(&sh.tempty[acc], ((local >> 1) & 1) ^ 1u, abort)) break;
         tc::tc_fence_after();
@@ -230,18 +259,20 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
         for (int k = 0; k < tl.len; k += GK) {
           if (!tc::mbar_wait(&sh.full[stage], phase, abort)) { ok = false; break; }
           tc::tc_fence_after();
-          // (low descriptor words: 16-byte units, 2048 bytes per 16 rows)
-          const uint32_t b_lo = desc_lo + (uint32_t)(stage * (G_STAGE / 16));
-          const uint32_t a_lo = b_lo + 2 * G_BOX / 16;
+          // (low descriptor words: 16-byte units; 16 rows are 2048 bytes, 16
+          // elements of a contiguous reduction 32)
+          constexpr uint32_t A_STEP = A_K ? 2 : 128;
+          const uint32_t bl = b_lo + (uint32_t)(stage * (G_STAGE / 16));
+          const uint32_t al = a_lo + (uint32_t)(stage * (G_STAGE / 16));
           const int left = tl.len - k;
-          mma2_bf16_lo(d_tmem, a_lo, desc_hi, b_lo, desc_hi, idesc, k != 0);
+          mma2_bf16_lo(d_tmem, al, a_hi, bl, b_hi, idesc, k != 0);
           if (left > 48) {
 #pragma unroll
             for (int i = 1; i < 4; ++i)
-              mma2_bf16_lo(d_tmem, a_lo + i * 128, desc_hi, b_lo + i * 128, desc_hi, idesc, 1u);
+              mma2_bf16_lo(d_tmem, al + i * A_STEP, a_hi, bl + i * 128, b_hi, idesc, 1u);
           } else {
-            if (left > 16) mma2_bf16_lo(d_tmem, a_lo + 128, desc_hi, b_lo + 128, desc_hi, idesc, 1u);
-            if (left > 32) mma2_bf16_lo(d_tmem, a_lo + 256, desc_hi, b_lo + 256, desc_hi, idesc, 1u);
+            if (left > 16) mma2_bf16_lo(d_tmem, al + A_STEP, a_hi, bl + 128, b_hi, idesc, 1u);
+            if (left > 32) mma2_bf16_lo(d_tmem, al + 2 * A_STEP, a_hi, bl + 256, b_hi, idesc, 1u);
           }
           mma2_commit_both(&sh.empty[stage]);
           if (++stage == GS) { stage = 0; phase ^= 1u; }
@@ -256,17 +287,18 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
       }
     }
   } else if (warp == 2 + G_EPI) {
-    // ---------------- fixer (both CTAs)
+    // ---------------- fixer (both CTAs; with A_K the copies fill zeros past
+    // both operands' ends)
     int stage = 0;
     uint32_t tail_phase = 0;
     for (int t = pair; t < num_tiles; t += n_pairs) {
-      const GTile tl = g_decode(sh, args, t);
+      const GTile tl = g_decode<SPLIT>(sh, args, t);
       const int kb = (tl.len + GK - 1) / GK;
       if (kb == 0) continue;
       const int at = (stage + kb - 1) % GS;
       stage = (stage + kb) % GS;
       const int valid = tl.len - (kb - 1) * GK;           // rows of the last k-block
-      if ((valid & 15) == 0) continue;
+      if (A_K || (valid & 15) == 0) continue;
       const uint32_t ph = (tail_phase >> at) & 1u;
       tail_phase ^= 1u << at;
       const bool ok = tc::mbar_wait(&sh.tail_full[at], ph, abort);
@@ -298,7 +330,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
     uint8_t *stage_out = smem + GS * G_STAGE + (warp - 2) * G_OUT;
     int local = 0;
     for (int t = pair; t < num_tiles; t += n_pairs) {
-      const GTile tl = g_decode(sh, args, t);
+      const GTile tl = g_decode<SPLIT>(sh, args, t);
       const int row = tl.m0 + (int)rank * GM + quarter * 32;   // this warp's first row
       const bool rows_ok = row < args.M[tl.prob];
       const int acc = local & 1;
@@ -322,18 +354,30 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
           for (int i = 0; i < 32; ++i) a[0][i] = a[1][i] = 0;
         }
         if (!rows_ok) continue;
-        if (lane == 0) tc::bulk_wait_read<0>();   // the store before has read the buffer
-        __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t *v = &a[q >> 2][(q & 3) * 8];
-          *reinterpret_cast<uint4 *>(stage_out + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-              make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
-                         bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+        for (int half = 0; half < (SPLIT ? 2 : 1); ++half) {
+          // a 128-byte piece of each row: 64 elements, or 32 partial sums
+          const int col = tl.c0 + c + half * 32;
+          if (SPLIT && col >= args.N[tl.prob]) break;
+          if (lane == 0) tc::bulk_wait_read<0>();   // the store before has read the buffer
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint4 w;
+            if constexpr (SPLIT) {
+              const uint32_t *v = &a[half][q * 4];
+              w = make_uint4(v[0], v[1], v[2], v[3]);
+            } else {
+              const uint32_t *v = &a[q >> 2][(q & 3) * 8];
+              w = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
+                             bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+            }
+            *reinterpret_cast<uint4 *>(stage_out + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::tma_store_3d(&maps.out[tl.prob], stage_out, col, row, tl.z);
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::tma_store_3d(&maps.out[tl.prob], stage_out, tl.c0 + c, row, tl.e);
       }
       if (tl.len != 0) {
         tc::tc_fence_before();
@@ -359,76 +403,43 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
     set_status(args.status, MOE_ERR_TIMEOUT, blockIdx.x);
 }
 
-int pairs_resident() {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (num_sms() / 2));
-  cfg.blockDim = dim3(G_THREADS);
-  cfg.dynamicSmemBytes = G_DYN_SMEM;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, gemm_grad_kernel, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    n = num_sms() / 2;
+// out[i] = sum over the runs of partial[run][i], in order: the runs' matrices
+// of one expert follow one another.
+struct SumArgs {
+  const float *part[kMaxGradProblems];
+  __nv_bfloat16 *out[kMaxGradProblems];
+  int64_t per_expert[kMaxGradProblems];   // M * N (a multiple of 8)
+  int experts, splits;
+  int *status;
+};
+__global__ void __launch_bounds__(256) grad_sum_kernel(SumArgs a) {
+  pdl_wait();
+  if (status_failed(a.status)) return;
+  const int p = blockIdx.y;
+  const int64_t per = a.per_expert[p], total = per * a.experts;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < total;
+       i += (int64_t)gridDim.x * 256 * 8) {
+    const int64_t e = i / per;
+    const float4 *src = reinterpret_cast<const float4 *>(a.part[p] + e * a.splits * per + (i - e * per));
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+      const float4 u = src[s * (per / 4)], v = src[s * (per / 4) + 1];
+      x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
+      y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+    }
+    auto pack = [](float l, float h) { return bf16x2_bits(__float_as_uint(l), __float_as_uint(h)); };
+    *reinterpret_cast<uint4 *>(a.out[p] + i) =
+        make_uint4(pack(x.x, x.y), pack(x.z, x.w), pack(y.x, y.y), pack(y.z, y.w));
   }
-  return n;
 }
 
-}  // namespace
+constexpr int kPairs = 76;   // SM pairs that the plans count on
 
-bool gemm_grad_supported(const GradProduct &p) {
-  return p.dtype == MOE_BF16 && p.rows > 0 && tensor_maps_available() &&
-         p.num_experts <= G_MAX_E && (p.lda ? p.lda : p.M) % 8 == 0 && p.N % 8 == 0 &&
-         num_sms() >= 2;
-}
-
-cudaError_t launch_gemm_grad(const GradProduct *p, int count, int *status, cudaStream_t s) {
-  static int pairs = 0;
-  if (pairs == 0) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        gemm_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_DYN_SMEM);
-    if (e != cudaSuccess) return e;
-    pairs = pairs_resident();
-  }
-  GMaps maps{};
-  GArgs a{};
-  a.offsets = p[0].offsets;
-  a.num_experts = p[0].num_experts;
-  a.rows = p[0].rows;
-  a.problems = count;
-  a.status = status;
-  const uint32_t box[2] = {64, GK}, box_out[3] = {64, 32, 1};
-  const int E = p[0].offsets ? p[0].num_experts : 1;
-  // narrower tiles where 256 columns leave SM pairs without a tile
-  for (a.width = GN; a.width > 64; a.width /= 2) {
-    int64_t tiles = 0;
-    for (int i = 0; i < count; ++i)
-      tiles += (int64_t)E * ((p[i].M + 2 * GM - 1) / (2 * GM)) * ((p[i].N + a.width - 1) / a.width);
-    if (tiles >= pairs) break;
-  }
-  for (int i = 0; i < count; ++i) {
-    a.M[i] = p[i].M;
-    a.N[i] = p[i].N;
-    a.first[i + 1] = a.first[i] + ((p[i].M + 2 * GM - 1) / (2 * GM)) *
-                                      ((p[i].N + a.width - 1) / a.width);
-    const uint64_t da[2] = {(uint64_t)(p[i].lda ? p[i].lda : p[i].M), (uint64_t)p[i].rows};
-    const uint64_t db[2] = {(uint64_t)p[i].N, (uint64_t)p[i].rows};
-    const uint64_t dout[3] = {(uint64_t)p[i].N, (uint64_t)p[i].M, (uint64_t)E};
-    if (!make_tensor_map(&maps.a[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p[i].A, 2, da, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tensor_map(&maps.b[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p[i].B, 2, db, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tensor_map(&maps.out[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p[i].out, 3, dout,
-                         box_out, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
-  }
+template <bool A_K, bool SPLIT>
+cudaError_t launch(const GMaps &maps, const GArgs &a, cudaStream_t s) {
+  auto kernel = gemm_grad_kernel<A_K, SPLIT>;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(G_THREADS);
   cfg.dynamicSmemBytes = G_DYN_SMEM;
   cfg.stream = s;
@@ -439,7 +450,149 @@ cudaError_t launch_gemm_grad(const GradProduct *p, int count, int *status, cudaS
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_grad_kernel, maps, a);
+  static int pairs = 0;
+  if (pairs == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_DYN_SMEM);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs < 1) {
+      cudaGetLastError();
+      pairs = num_sms() / 2;
+    }
+  }
+  cfg.gridDim = dim3(2 * pairs);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, a);
+}
+
+int64_t tiles_of(const GradProduct *p, int count, int width) {
+  int64_t tiles = 0;
+  for (int i = 0; i < count; ++i)
+    tiles += (int64_t)(p[i].offsets ? p[i].num_experts : 1) *
+             ((p[i].M + 2 * GM - 1) / (2 * GM)) * ((p[i].N + width - 1) / width);
+  return tiles;
+}
+
+// Narrower tiles where 256 columns leave SM pairs without a tile.
+int width_of(const GradProduct *p, int count, int splits) {
+  int width = GN;
+  while (width > 64 && tiles_of(p, count, width) * splits < kPairs) width /= 2;
+  return width;
+}
+
+bool encode(CUtensorMap *m, const void *p, int rank, const uint64_t *dims, const uint32_t *box) {
+  return make_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, rank, dims, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+bool gemm_grad_supported(const GradProduct &p) {
+  return p.dtype == MOE_BF16 && p.rows > 0 && tensor_maps_available() &&
+         p.num_experts <= G_MAX_E && (p.lda ? p.lda : p.M) % 8 == 0 && p.N % 8 == 0 &&
+         num_sms() >= 2;
+}
+
+// Two tiles per pair at most, and 512 rows of an average segment per run at
+// least: a run's tile then costs more than the 512 KB of partial sums that it
+// adds to write and read.  (Router gradient of 16384 tokens, 256 experts, d
+// 7168: 28 tiles; TODO_SPLIT.)
+int grad_splits(const GradProduct *p, int count) {
+  if (count == 0 || p[0].dtype != MOE_BF16) return 1;
+  const int64_t tiles = tiles_of(p, count, GN);
+  const int E = p[0].offsets ? p[0].num_experts : 1;
+  if (tiles >= kPairs) return 1;
+  const int64_t most = 2 * kPairs / tiles, by_rows = p[0].rows / E / 512;
+  const int64_t n = most < by_rows ? most : by_rows;
+  return n < 2 ? 1 : (int)n;
+}
+
+size_t grad_scratch(const GradProduct *p, int count) {
+  const int splits = grad_splits(p, count);
+  size_t bytes = 0;
+  for (int i = 0; splits > 1 && i < count; ++i)
+    bytes += (size_t)splits * (p[i].offsets ? p[i].num_experts : 1) * p[i].M * p[i].N * 4;
+  return bytes;
+}
+
+cudaError_t launch_gemm_grad(const GradProduct *p, int count, int splits, float *scratch,
+                             int *status, cudaStream_t s) {
+  GMaps maps{};
+  GArgs a{};
+  a.offsets = p[0].offsets;
+  a.num_experts = p[0].num_experts;
+  a.rows = p[0].rows;
+  a.problems = count;
+  a.status = status;
+  a.splits = splits;
+  a.width = width_of(p, count, splits);
+  const int E = p[0].offsets ? p[0].num_experts : 1;
+  const uint32_t box[2] = {64, GK}, box_out[3] = {splits > 1 ? 32u : 64u, 32, 1};
+  SumArgs sum{};
+  sum.experts = E;
+  sum.splits = splits;
+  sum.status = status;
+  int64_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    a.M[i] = p[i].M;
+    a.N[i] = p[i].N;
+    a.first[i + 1] = a.first[i] + ((p[i].M + 2 * GM - 1) / (2 * GM)) *
+                                      ((p[i].N + a.width - 1) / a.width);
+    const uint64_t da[2] = {(uint64_t)(p[i].lda ? p[i].lda : p[i].M), (uint64_t)p[i].rows};
+    const uint64_t db[2] = {(uint64_t)p[i].N, (uint64_t)p[i].rows};
+    const uint64_t dout[3] = {(uint64_t)p[i].N, (uint64_t)p[i].M, (uint64_t)E * splits};
+    if (!encode(&maps.a[i], p[i].A, 2, da, box) || !encode(&maps.b[i], p[i].B, 2, db, box))
+      return cudaErrorInvalidValue;
+    if (splits == 1) {
+      if (!encode(&maps.out[i], p[i].out, 3, dout, box_out)) return cudaErrorInvalidValue;
+      continue;
+    }
+    sum.part[i] = scratch;
+    sum.out[i] = static_cast<__nv_bfloat16 *>(p[i].out);
+    sum.per_expert[i] = (int64_t)p[i].M * p[i].N;
+    if (!make_tensor_map(&maps.out[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, scratch, 3, dout, box_out,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+    scratch += (int64_t)splits * E * sum.per_expert[i];
+    if (sum.per_expert[i] * E > most) most = sum.per_expert[i] * E;
+  }
+  if (splits == 1) return launch<false, false>(maps, a, s);
+  const cudaError_t e = launch<false, true>(maps, a, s);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (most / 8 + 255) / 256;
+  return launch_pdl(grad_sum_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216), count),
+                    dim3(256), 0, s, sum);
+}
+
+bool gemm_router_rows_supported(const RowsProduct &p) {
+  return p.dtype == MOE_BF16 && p.epi == kRowsPlain && p.b_rows && p.offsets == nullptr &&
+         p.A2 == nullptr && p.rows > 0 && tensor_maps_available() && p.N % 8 == 0 &&
+         (p.lda ? p.lda : p.K) % 8 == 0 && num_sms() >= 2;
+}
+
+cudaError_t launch_gemm_router_rows(const RowsProduct &p, int *status, cudaStream_t s) {
+  GradProduct shape{};
+  shape.M = p.rows;
+  shape.N = p.N;
+  GMaps maps{};
+  GArgs a{};
+  a.num_experts = 1;
+  a.rows = p.K;      // the reduction
+  a.problems = 1;
+  a.status = status;
+  a.splits = 1;
+  a.width = width_of(&shape, 1, 1);
+  a.M[0] = p.rows;
+  a.N[0] = p.N;
+  a.first[1] = (int)tiles_of(&shape, 1, a.width);
+  const uint64_t da[2] = {(uint64_t)(p.lda ? p.lda : p.K), (uint64_t)p.rows};
+  const uint64_t db[2] = {(uint64_t)p.N, (uint64_t)p.K};
+  const uint64_t dout[3] = {(uint64_t)p.N, (uint64_t)p.rows, 1};
+  const uint32_t box_a[2] = {GK, GM}, box_b[2] = {64, GK}, box_out[3] = {64, 32, 1};
+  if (!encode(&maps.a[0], p.A, 2, da, box_a) || !encode(&maps.b[0], p.B, 2, db, box_b) ||
+      !encode(&maps.out[0], p.out, 3, dout, box_out))
+    return cudaErrorInvalidValue;
+  return launch<true, false>(maps, a, s);
 }
 
 }  // namespace moe

@@ -71,6 +71,15 @@ cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s);
 // tensor cores (bf16; SM pairs).
 constexpr int kMaxGradProblems = 3;
 bool gemm_grad_supported(const GradProduct &p);
-cudaError_t launch_gemm_grad(const GradProduct *p, int count, int *status, cudaStream_t s);
+// Runs that the segments' rows are cut into where the problems are too few to
+// fill the SMs (1: not cut), and the scratch that the partial sums take.  Both
+// go by the shapes alone.
+int grad_splits(const GradProduct *p, int count);
+size_t grad_scratch(const GradProduct *p, int count);
+cudaError_t launch_gemm_grad(const GradProduct *p, int count, int splits, float *scratch,
+                             int *status, cudaStream_t s);
+// A RowsProduct of one segment with a short reduction, on the same kernel.
+bool gemm_router_rows_supported(const RowsProduct &p);
+cudaError_t launch_gemm_router_rows(const RowsProduct &p, int *status, cudaStream_t s);
 
 }  // namespace moe

@@ -12,11 +12,36 @@ namespace {
 
 // The layer's workspace, then the scratch of the gradients.
 struct TrainLayout {
-  size_t status, dg, du, dl, dx_router, bias_parts, total;
+  size_t status, dg, du, dl, dx_router, bias_parts, grad_parts, total;
 };
 
 // dl's rows are padded to whole 16-byte vectors of bf16.
 int dl_pitch(const moe_config &c) { return (c.n_experts + 7) / 8 * 8; }
+
+// The weight gradients of the experts and of the router (operands unset).
+void expert_grads_of(const moe_config &c, const int32_t *offsets, GradProduct (&p)[3]) {
+  const int M[3] = {c.d, c.d_ff, c.d_ff}, N[3] = {c.d_ff, c.d, c.d};   // W2, W1, W3
+  for (int i = 0; i < 3; ++i) {
+    p[i] = GradProduct{};
+    p[i].dtype = c.act_dtype;
+    p[i].offsets = offsets;
+    p[i].num_experts = c.n_experts;
+    p[i].rows = c.n * c.top_k;
+    p[i].M = M[i];
+    p[i].N = N[i];
+  }
+}
+GradProduct router_grad_of(const moe_config &c) {
+  GradProduct p{};
+  p.dtype = c.act_dtype;
+  p.num_experts = 1;
+  p.rows = c.n;
+  p.M = c.n_experts;
+  p.N = c.d;
+  p.lda = dl_pitch(c);
+  return p;
+}
+int expert_problems(const moe_config &c) { return c.act == MOE_ACT_SWIGLU ? 3 : 2; }
 
 TrainLayout train_layout_of(const moe_config &c) {
   moe_config c1 = c;
@@ -36,6 +61,11 @@ TrainLayout train_layout_of(const moe_config &c) {
   L.du = take(P * c.d_ff * z);
   L.dl = take((size_t)c.n * dl_pitch(c) * z);
   L.bias_parts = take(route_grad_scratch(c));
+  GradProduct experts[3];
+  expert_grads_of(c, reinterpret_cast<const int32_t *>(16), experts);   // (shapes alone)
+  const GradProduct router = router_grad_of(c);
+  const size_t ge = grad_scratch(experts, expert_problems(c)), gr = grad_scratch(&router, 1);
+  L.grad_parts = take(ge > gr ? ge : gr);
   L.total = off;
   return L;
 }
@@ -66,6 +96,7 @@ bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
 // bf16 rows run on the tensor cores (SM pairs), fp32 rows on the CUDA cores.
 cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   if (p.dtype == MOE_F32) return launch_rows_simt(p, status, s);
+  if (gemm_router_rows_supported(p)) return launch_gemm_router_rows(p, status, s);
   constexpr int epi[] = {0, 1, kEpiSwigluKeep, kEpiReluGrad, kEpiSwigluGrad};   // by kRows*
   GemmStage g{};
   g.a_dtype = g.b_dtype = g.out_dtype = MOE_BF16;
@@ -91,11 +122,14 @@ cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
 }
 
 // Problems over the same segments: one launch on the tensor cores, else one
-// launch each.
-cudaError_t launch_grads(const GradProduct *p, int count, int *status, cudaStream_t s) {
+// launch each.  splits, parts: as grad_splits and grad_scratch of all the
+// layer's problems say, whichever of them are wanted (so that a gradient has
+// the same bits alone and with the others).
+cudaError_t launch_grads(const GradProduct *p, int count, int splits, float *parts, int *status,
+                         cudaStream_t s) {
   bool tc = true;
   for (int i = 0; i < count; ++i) tc = tc && gemm_grad_supported(p[i]);
-  if (tc) return count ? launch_gemm_grad(p, count, status, s) : cudaSuccess;
+  if (tc) return count ? launch_gemm_grad(p, count, splits, parts, status, s) : cudaSuccess;
   for (int i = 0; i < count; ++i) {
     const cudaError_t e = launch_grad_simt(p[i], status, s);
     if (e != cudaSuccess) return e;
@@ -237,24 +271,23 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   const int P = c.n * c.top_k;
   void *dg = at<void>(ws, L.dg), *du = at<void>(ws, L.du);
 
-  GradProduct gw[kMaxGradProblems] = {};
+  GradProduct all[3], gw[kMaxGradProblems];
+  expert_grads_of(c, offsets, all);
+  const int splits = grad_splits(all, expert_problems(c));
+  float *parts = at<float>(ws, L.grad_parts);
+  const void *left[3] = {dy_perm, dg, du}, *right[3] = {h, x_perm, x_perm};
+  void *out[3] = {grads->W2, grads->W1, grads->W3};
   int n_gw = 0;
-  auto weight_grad = [&](const void *A, const void *B, int M, int N, void *out) {
-    GradProduct &q = gw[n_gw++];
-    q.dtype = c.act_dtype;
-    q.offsets = offsets;
-    q.num_experts = c.n_experts;
-    q.rows = P;
-    q.M = M;
-    q.N = N;
-    q.A = A;
-    q.B = B;
-    q.out = out;
-  };
-  if (grads->W2) weight_grad(dy_perm, h, c.d, c.d_ff, grads->W2);
-  if (grads->W1) weight_grad(dg, x_perm, c.d_ff, c.d, grads->W1);
-  if (grads->W3) weight_grad(du, x_perm, c.d_ff, c.d, grads->W3);
-  if (!dx_perm && !grads->W1 && !grads->W3) return cuda_status(launch_grads(gw, n_gw, status, s));
+  for (int i = 0; i < 3; ++i) {
+    if (!out[i]) continue;
+    gw[n_gw] = all[i];
+    gw[n_gw].A = left[i];
+    gw[n_gw].B = right[i];
+    gw[n_gw].out = out[i];
+    ++n_gw;
+  }
+  if (!dx_perm && !grads->W1 && !grads->W3)
+    return cuda_status(launch_grads(gw, n_gw, splits, parts, status, s));
   RowsProduct r{};
   r.dtype = c.act_dtype;
   r.epi = gated ? kRowsSwigluGrad : kRowsReluGrad;
@@ -272,7 +305,7 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   r.out = dg;
   r.out_u = gated ? du : nullptr;
   MOE_TRY(cuda_status(launch_rows(r, status, s)));
-  MOE_TRY(cuda_status(launch_grads(gw, n_gw, status, s)));
+  MOE_TRY(cuda_status(launch_grads(gw, n_gw, splits, parts, status, s)));
   if (dx_perm) {
     RowsProduct x{};
     x.dtype = c.act_dtype;
@@ -335,17 +368,12 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
     MOE_TRY(cuda_status(launch_route_grad(c, probs, topk_idx, topk_gate, dgate, f, aux, dl, pitch,
                                           dbias, at<float>(ws, L.bias_parts), status, s)));
   if (dWg) {
-    GradProduct gw{};
-    gw.dtype = c.act_dtype;
-    gw.num_experts = 1;
-    gw.rows = c.n;
-    gw.M = c.n_experts;
-    gw.N = c.d;
-    gw.lda = pitch;
+    GradProduct gw = router_grad_of(c);
     gw.A = dl;
     gw.B = x;
     gw.out = dWg;
-    MOE_TRY(cuda_status(launch_grads(&gw, 1, status, s)));
+    MOE_TRY(cuda_status(launch_grads(&gw, 1, grad_splits(&gw, 1), at<float>(ws, L.grad_parts),
+                                     status, s)));
   }
   if (dx) {
     RowsProduct r{};

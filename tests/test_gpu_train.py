@@ -204,6 +204,10 @@ FFN_CASES = [
     (40, 64, 96, 256, 4, "bf16", "swiglu", "even"),
     (9, 1544, 64, 3, 2, "bf16", "swiglu", "even"),
     (700, 512, 1024, 1, 1, "bf16", "swiglu", "even"),
+    # few tiles and many rows: the weight gradients' reduction is cut into runs
+    (2100, 72, 136, 2, 1, "bf16", "swiglu", [2099, 1]),
+    (2500, 264, 64, 2, 1, "bf16", "relu", [1233, 1267]),
+    (1600, 72, 72, 1, 1, "bf16", "swiglu", "even"),
     (1, 4, 4, 1, 1, "f32", "swiglu", "even"),
     (256, 128, 512, 4, 1, "f32", "relu", "even"),
     (83, 36, 100, 7, 2, "f32", "swiglu", "even"),
@@ -453,7 +457,8 @@ ROUTE_CASES = [(n, d, E, k, dt, gate, aux)
                    (1, 8, 1, 1, "top_prob", 0.01), (256, 128, 4, 1, "top_prob", 0.01),
                    (200, 72, 8, 2, "renorm", 0.0), (33, 520, 37, 5, "renorm", 0.3),
                    (700, 264, 256, 8, "renorm", 0.0), (65, 136, 200, 6, "top_prob", 0.2),
-                   (3, 64, 40, 40, "renorm", 0.0), (2500, 24, 3, 2, "top_prob", 0.0))]
+                   (3, 64, 40, 40, "renorm", 0.0), (2500, 24, 3, 2, "top_prob", 0.0),
+                   (1537, 520, 130, 4, "renorm", 0.1))]
 
 
 @pytest.mark.parametrize("n,d,E,k,dtype,gate,aux", ROUTE_CASES)
