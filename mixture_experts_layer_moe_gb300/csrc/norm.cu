@@ -378,12 +378,12 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
 // adds rows w, w + 32, ..., then a butterfly adds the warps' sums.
 __global__ void __launch_bounds__(1024)
 column_sum_kernel(const float *__restrict__ pg, const float *__restrict__ pb, int count, int d,
-                  float *__restrict__ dgamma, float *__restrict__ dbeta) {
+                  float *__restrict__ dgamma, float *__restrict__ dbeta, const int *status) {
   __shared__ float s[32][33];
   const float *part = blockIdx.y ? pb : pg;
   float *out = blockIdx.y ? dbeta : dgamma;
   pdl_wait();
-  if (out == nullptr) return;
+  if (out == nullptr || status_failed(status)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col = blockIdx.x * 32 + lane;
   float a = 0.f;
@@ -629,12 +629,17 @@ cudaError_t bwd_typed(const moe_norm_config &c, const void *xv, const void *gv, 
     e = bwd_vec<T, 1>(c, p, x, gamma, mean, rstd, dy, dx, pg, pb, s);
   }
   if (e == cudaSuccess && !direct && (pg || pb))
-    e = launch_pdl(column_sum_kernel, dim3((c.d + 31) / 32, 2), dim3(1024), 0, s,
-                   (const float *)pg, (const float *)pb, p.parts, (int)c.d, dgamma, dbeta);
+    e = launch_column_sum(pg, pb, p.parts, c.d, dgamma, dbeta, nullptr, s);
   return e;
 }
 
 }  // namespace
+
+cudaError_t launch_column_sum(const float *pa, const float *pb, int count, int d, float *a,
+                              float *b, const int *status, cudaStream_t s) {
+  return launch_pdl(column_sum_kernel, dim3((d + 31) / 32, b ? 2 : 1), dim3(1024), 0, s, pa, pb,
+                    count, d, a, b, status);
+}
 
 cudaError_t launch_norm(const moe_norm_config &c, const void *x, const void *gamma,
                         const void *beta, void *y, float *mean, float *rstd, cudaStream_t s) {

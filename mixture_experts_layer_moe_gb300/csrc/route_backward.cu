@@ -26,6 +26,7 @@ route_grad_kernel(const float *__restrict__ probs, const int32_t *__restrict__ t
                   const float *__restrict__ f, float aux_scale, int renorm, int n, int E, int k,
                   T *__restrict__ dl, int pitch, float *__restrict__ bias_parts, int *status) {
   __shared__ float s_sum[RB_WARPS][RB_SLOTS * 32];
+  pdl_launch_dependents();   // (the column sums wait for this grid to end)
   if (status_failed(status)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float fe[RB_SLOTS], col[RB_SLOTS];
@@ -44,22 +45,40 @@ route_grad_kernel(const float *__restrict__ probs, const int32_t *__restrict__ t
       v[i] = 0.f;
       fp = fmaf(fe[i], p[i], fp);
     }
-    // sum over the chosen experts of gate * dgate (lanes take slots)
+    // the token's choices, 32 slots at a time, one per lane; first the sum over
+    // the chosen experts of gate * dgate, then each choice's term to the lane
+    // that holds its expert
     float sum = 0.f;
-    for (int j = lane; j < k; j += 32) {
-      const int e = topk_idx[(int64_t)t * k + j];
-      if (e < 0 || e >= E) set_status(status, MOE_ERR_BAD_INDEX, t * k + j);
-      else sum = fmaf(gates[(int64_t)t * k + j], dgate[(int64_t)t * k + j], sum);
+    int e_l = -1;
+    float g_l = 0.f, dg_l = 0.f;
+    auto choices = [&](int j0) {
+      const int j = j0 + lane;
+      e_l = -1;
+      if (j < k) {
+        e_l = topk_idx[(int64_t)t * k + j];
+        g_l = gates[(int64_t)t * k + j];
+        dg_l = dgate[(int64_t)t * k + j];
+        if (e_l < 0 || e_l >= E) {
+          set_status(status, MOE_ERR_BAD_INDEX, t * k + j);
+          e_l = -1;
+        }
+      }
+    };
+    for (int j0 = 0; j0 < k; j0 += 32) {
+      choices(j0);
+      if (e_l >= 0) sum = fmaf(g_l, dg_l, sum);
     }
     sum = warp_sum_xor(sum);
-    for (int j = 0; j < k; ++j) {
-      const int e = topk_idx[(int64_t)t * k + j];
-      if (e < 0 || e >= E) continue;
-      const float g = gates[(int64_t)t * k + j], dg = dgate[(int64_t)t * k + j];
-      const float add = renorm ? g * (dg - sum) : g * dg;
+    for (int j0 = 0; j0 < k; j0 += 32) {
+      if (k > 32) choices(j0);
+      const float term = renorm ? g_l * (dg_l - sum) : g_l * dg_l;
+      for (int j = 0; j < min(32, k - j0); ++j) {
+        const int e = __shfl_sync(0xffffffffu, e_l, j);
+        const float add = __shfl_sync(0xffffffffu, term, j);
 #pragma unroll
-      for (int i = 0; i < RB_SLOTS; ++i)
-        if (e == lane + 32 * i) v[i] += add;
+        for (int i = 0; i < RB_SLOTS; ++i)
+          if (e == lane + 32 * i) v[i] += add;
+      }
     }
     if (f) fp = warp_sum_xor(fp);
 #pragma unroll
@@ -82,18 +101,6 @@ route_grad_kernel(const float *__restrict__ probs, const int32_t *__restrict__ t
     for (int w = 0; w < RB_WARPS; ++w) a += s_sum[w][e];
     bias_parts[(int64_t)blockIdx.x * E + e] = a;
   }
-}
-
-__global__ void __launch_bounds__(256)
-bias_sum_kernel(const float *__restrict__ parts, int count, int E, float *__restrict__ dbias,
-                const int *status) {
-  if (status_failed(status)) return;
-  const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (e >= E) return;
-  float a = 0.f;
-  for (int c = lane; c < count; c += 32) a += parts[(int64_t)c * E + e];
-  a = warp_sum_xor(a);
-  if (lane == 0) dbias[e] = a;
 }
 
 int grid_of(int n) {
@@ -123,7 +130,7 @@ cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int
         probs, topk_idx, gates, dgate, f, scale, renorm, c.n, E, c.top_k, (__nv_bfloat16 *)dl,
         pitch, parts, status);
   if (dbias && grid > 1)
-    bias_sum_kernel<<<(E + 7) / 8, 256, 0, s>>>(scratch, grid, E, dbias, status);
+    return launch_column_sum(scratch, nullptr, grid, E, dbias, nullptr, status, s);
   return cudaGetLastError();
 }
 

@@ -16,6 +16,11 @@ cudaError_t launch_norm_backward(const moe_norm_config &c, const void *x, const 
                                  const float *mean, const float *rstd, const void *dy, void *dx,
                                  float *dgamma, float *dbeta, void *scratch, cudaStream_t s);
 
+// a[i] = sum over `count` rows of pa[row][i], i < d, in a fixed order; b from pb
+// likewise (each output nullptr: not wanted; b is the second of two).
+cudaError_t launch_column_sum(const float *pa, const float *pb, int count, int d, float *a,
+                              float *b, const int *status, cudaStream_t s);
+
 // --------------------------------------------------------- combine, router
 cudaError_t launch_combine_backward(int dtype, const void *dy, const void *y_perm,
                                     const int32_t *inv_perm, const float *gates, void *dy_perm,
@@ -53,6 +58,7 @@ struct RowsProduct {
   const void *g, *u, *h;    // kept rows [rows][N] that a gradient's epilogue reads
   void *out, *out_g, *out_u;   // [rows][N]
 };
+// (fp32)
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s);
 
 // Products over the rows of each segment (a weight's gradient):
@@ -66,6 +72,7 @@ struct GradProduct {
   const void *A, *B;
   void *out;                // [E][M][N]
 };
+// (fp32)
 cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s);
 // Up to kMaxGradProblems of them over the same segments in one launch, on
 // tensor cores (bf16; SM pairs).

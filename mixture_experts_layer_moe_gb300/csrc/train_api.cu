@@ -118,7 +118,7 @@ cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   g.kept_g = p.g;
   g.kept_u = p.u;
   g.kept_h = p.h;
-  return gemm_t2_supported(g) ? launch_gemm_t2(g, status, s) : launch_rows_simt(p, status, s);
+  return gemm_t2_supported(g) ? launch_gemm_t2(g, status, s) : cudaErrorNotSupported;
 }
 
 // Problems over the same segments: one launch on the tensor cores, else one

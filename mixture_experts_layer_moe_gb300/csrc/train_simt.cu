@@ -3,11 +3,15 @@
 // The path of fp32 layers (tensor cores multiply fp32 operands in fewer
 // bits), written for their sizes: a layer of a few hundred rows, whose
 // launches cost as much as its products.
-// A CTA computes a 64 x 64 tile of one segment's rows (RowsProduct) or of one
-// expert's gradient (GradProduct), 4 x 4 outputs per thread, over steps of 16
-// along the reduction.  The three storage orders of the operands differ in
-// how a tile is staged only: in shared memory both operands lie reduction
-// index first, so that a thread reads its 4 + 4 values as two float4.
+// A CTA computes a tile of one segment's rows (RowsProduct) or of one expert's
+// gradient (GradProduct) with 256 threads: 64 x 64, or 32 x 32 where the larger
+// tiles would not give every SM one.  The next step's operands are loaded into
+// registers while the current one is multiplied, and shared memory is double
+// buffered, so a step waits for memory once, not twice (256 rows, d 128, d_ff
+// 512, 4 experts, forward: 49 us without either, TODO_SIMT).
+// The three storage orders of the operands differ in how a tile is staged
+// only: in shared memory both operands lie reduction index first, so that a
+// thread reads its values of a step as two vectors.
 #include <math.h>
 
 #include "common.cuh"
@@ -17,38 +21,68 @@
 namespace moe {
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 16, T_THREADS = 256, T_LD = TM + 4;
+constexpr int T_THREADS = 256;
 
-// Stages a TK x 64 tile: element (kk, i) is src[i * ld + kk] (K_FAST) or
-// src[kk * ld + i]; zero outside i < ni, kk < nk.
-template <typename T, bool K_FAST>
-__device__ __forceinline__ void stage(float (*dst)[T_LD], const T *src, int64_t ld, int ni, int nk) {
+// TILE x TILE outputs per CTA, R x R per thread, TK reduction indexes a step.
+template <int TILE>
+struct Geo {
+  static constexpr int R = TILE / 16, TK = 1024 / TILE, LD = TILE + 4;
+  static constexpr int LOADS = TILE * TK / T_THREADS;
+  using Buf = float[TK][LD];
+};
+
+// This thread's part of a TK x TILE operand tile: element (kk, i) is
+// src[i * ld + kk] (K_FAST) or src[kk * ld + i]; zero outside i < ni, kk < nk.
+template <typename T, bool K_FAST, int TILE>
+struct Part {
+  using G = Geo<TILE>;
+  float v[G::LOADS];
+  static __device__ __forceinline__ int kk(int l) { return K_FAST ? l % G::TK : l / TILE; }
+  static __device__ __forceinline__ int ii(int l) { return K_FAST ? l / G::TK : l % TILE; }
+  __device__ __forceinline__ void load(const T *src, int64_t ld, int ni, int nk) {
 #pragma unroll
-  for (int c = 0; c < TM * TK / T_THREADS; ++c) {
-    const int l = threadIdx.x + c * T_THREADS;
-    const int kk = K_FAST ? l % TK : l / TM;
-    const int i = K_FAST ? l / TK : l % TM;
-    float v = 0.f;
-    if (i < ni && kk < nk) v = Elem<T>::load(src + (K_FAST ? i * ld + kk : kk * ld + i));
-    dst[kk][i] = v;
+    for (int c = 0; c < G::LOADS; ++c) {
+      const int l = threadIdx.x + c * T_THREADS, k = kk(l), i = ii(l);
+      v[c] = i < ni && k < nk ? Elem<T>::load(src + (K_FAST ? i * ld + k : k * ld + i)) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(typename G::Buf &dst) const {
+#pragma unroll
+    for (int c = 0; c < G::LOADS; ++c) {
+      const int l = threadIdx.x + c * T_THREADS;
+      dst[kk(l)][ii(l)] = v[c];
+    }
+  }
+};
+
+template <int R>
+__device__ __forceinline__ void read_vec(const float *p, float (&v)[R]) {
+  if constexpr (R == 4) {
+    const float4 t = *reinterpret_cast<const float4 *>(p);
+    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+  } else {
+    const float2 t = *reinterpret_cast<const float2 *>(p);
+    v[0] = t.x; v[1] = t.y;
   }
 }
 
-__device__ __forceinline__ void tile_fma(float (&acc)[4][4], const float (*as)[T_LD],
-                                         const float (*bs)[T_LD], int tx, int ty) {
+template <int TILE, int R = Geo<TILE>::R>
+__device__ __forceinline__ void tile_fma(float (&acc)[R][R], const typename Geo<TILE>::Buf &as,
+                                         const typename Geo<TILE>::Buf &bs, int tx, int ty) {
+#pragma unroll 16
+  for (int kk = 0; kk < Geo<TILE>::TK; ++kk) {
+    float a[R], b[R];
+    read_vec(&as[kk][ty * R], a);
+    read_vec(&bs[kk][tx * R], b);
 #pragma unroll
-  for (int kk = 0; kk < TK; ++kk) {
-    const float4 a4 = *reinterpret_cast<const float4 *>(&as[kk][ty * 4]);
-    const float4 b4 = *reinterpret_cast<const float4 *>(&bs[kk][tx * 4]);
-    const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      for (int j = 0; j < R; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
   }
 }
 
 // Expert and row range of this CTA's tile; false when there is none.
+template <int TM>
 __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int rows, int tile, int &e,
                                           int &row0, int &end, int *status) {
   if (offsets == nullptr) {
@@ -76,40 +110,52 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int row
   return false;
 }
 
-template <typename T, int EPI, bool B_ROWS>
+template <typename T, int EPI, bool B_ROWS, int TILE>
 __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int *status) {
+  using G = Geo<TILE>;
+  constexpr int R = G::R;
   constexpr bool DUAL = EPI == kRowsSwiglu;
-  __shared__ __align__(16) float as[TK][T_LD], bs[TK][T_LD], b2s[DUAL ? TK : 1][T_LD];
+  __shared__ __align__(16) typename G::Buf as[2], bs[2], b2s[DUAL ? 2 : 1];
   if (status_failed(status)) return;
   int e, row0, end;
-  if (!find_tile(p.offsets, p.num_experts, p.rows, blockIdx.x, e, row0, end, status)) return;
-  const int n0 = blockIdx.y * TN, N = p.N, K = p.K;
+  if (!find_tile<TILE>(p.offsets, p.num_experts, p.rows, blockIdx.x, e, row0, end, status)) return;
+  const int n0 = blockIdx.y * TILE, N = p.N, K = p.K;
   const int64_t lda = p.lda ? p.lda : K;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {}, acc2[4][4] = {};
-  for (int half = 0; half < (EPI == kRowsPlain && p.A2 ? 2 : 1); ++half) {
-    const T *A = static_cast<const T *>(half ? p.A2 : p.A) + row0 * lda;
-    const int64_t base = (int64_t)e * N * K + (B_ROWS ? (int64_t)n0 : (int64_t)n0 * K);
-    const T *B = static_cast<const T *>(half ? p.B2 : p.B) + base;
-    for (int k0 = 0; k0 < K; k0 += TK) {
-      stage<T, true>(as, A + k0, lda, end - row0, K - k0);
-      if constexpr (B_ROWS) stage<T, false>(bs, B + (int64_t)k0 * N, N, N - n0, K - k0);
-      else stage<T, true>(bs, B + k0, K, N - n0, K - k0);
-      if constexpr (DUAL)
-        stage<T, true>(b2s, static_cast<const T *>(p.B2) + base + k0, K, N - n0, K - k0);
-      __syncthreads();
-      tile_fma(acc, as, bs, tx, ty);
-      if constexpr (DUAL) tile_fma(acc2, as, b2s, tx, ty);
-      __syncthreads();
-    }
+  const int64_t base = (int64_t)e * N * K + (B_ROWS ? (int64_t)n0 : (int64_t)n0 * K);
+  float acc[R][R] = {}, acc2[R][R] = {};
+  // the steps of the one or two operand pairs, one after the other
+  const int steps1 = (K + G::TK - 1) / G::TK;
+  const int steps = steps1 * (EPI == kRowsPlain && p.A2 ? 2 : 1);
+  Part<T, true, TILE> pa, pb2;
+  Part<T, !B_ROWS, TILE> pb;
+  auto load = [&](int step) {
+    const bool second = step >= steps1;
+    const int k0 = (second ? step - steps1 : step) * G::TK;
+    const T *A = static_cast<const T *>(second ? p.A2 : p.A) + row0 * lda;
+    const T *B = static_cast<const T *>(second ? p.B2 : p.B) + base;
+    pa.load(A + k0, lda, end - row0, K - k0);
+    pb.load(B_ROWS ? B + (int64_t)k0 * N : B + k0, B_ROWS ? N : K, N - n0, K - k0);
+    if constexpr (DUAL) pb2.load(static_cast<const T *>(p.B2) + base + k0, K, N - n0, K - k0);
+  };
+  load(0);
+  for (int step = 0; step < steps; ++step) {
+    const int buf = step & 1;
+    pa.store(as[buf]);
+    pb.store(bs[buf]);
+    if constexpr (DUAL) pb2.store(b2s[buf]);
+    __syncthreads();
+    if (step + 1 < steps) load(step + 1);
+    tile_fma<TILE>(acc, as[buf], bs[buf], tx, ty);
+    if constexpr (DUAL) tile_fma<TILE>(acc2, as[buf], b2s[buf], tx, ty);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = row0 + ty * 4 + i;
+  for (int i = 0; i < R; ++i) {
+    const int r = row0 + ty * R + i;
     if (r >= end) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + tx * 4 + j;
+    for (int j = 0; j < R; ++j) {
+      const int c = n0 + tx * R + j;
       if (c >= N) continue;
       const int64_t at = (int64_t)r * N + c;
       float v = acc[i][j];
@@ -133,11 +179,13 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   }
 }
 
-template <typename T>
+template <typename T, int TILE>
 __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int *status) {
-  __shared__ __align__(16) float as[TK][T_LD], bs[TK][T_LD];
+  using G = Geo<TILE>;
+  constexpr int R = G::R;
+  __shared__ __align__(16) typename G::Buf as[2], bs[2];
   if (status_failed(status)) return;
-  const int e = blockIdx.z, m0 = blockIdx.y * TM, n0 = blockIdx.x * TN, M = p.M, N = p.N;
+  const int e = blockIdx.z, m0 = blockIdx.y * TILE, n0 = blockIdx.x * TILE, M = p.M, N = p.N;
   const int beg = p.offsets ? p.offsets[e] : 0, end = p.offsets ? p.offsets[e + 1] : p.rows;
   if (beg < 0 || end < beg || end > p.rows) {
     if (threadIdx.x == 0) set_status(status, MOE_ERR_BAD_INDEX, e);
@@ -145,58 +193,74 @@ __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int
   }
   const int64_t lda = p.lda ? p.lda : M;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
+  float acc[R][R] = {};
   const T *A = static_cast<const T *>(p.A) + m0, *B = static_cast<const T *>(p.B) + n0;
-  for (int q = beg; q < end; q += TK) {
-    stage<T, false>(as, A + q * lda, lda, M - m0, end - q);
-    stage<T, false>(bs, B + (int64_t)q * N, N, N - n0, end - q);
+  Part<T, false, TILE> pa, pb;
+  auto load = [&](int q) {
+    pa.load(A + q * lda, lda, M - m0, end - q);
+    pb.load(B + (int64_t)q * N, N, N - n0, end - q);
+  };
+  if (beg < end) load(beg);
+  for (int q = beg, buf = 0; q < end; q += G::TK, buf ^= 1) {
+    pa.store(as[buf]);
+    pb.store(bs[buf]);
     __syncthreads();
-    tile_fma(acc, as, bs, tx, ty);
-    __syncthreads();
+    if (q + G::TK < end) load(q + G::TK);
+    tile_fma<TILE>(acc, as[buf], bs[buf], tx, ty);
   }
   T *out = static_cast<T *>(p.out) + (int64_t)e * M * N;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + ty * 4 + i;
+  for (int i = 0; i < R; ++i) {
+    const int m = m0 + ty * R + i;
     if (m >= M) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + tx * 4 + j;
+    for (int j = 0; j < R; ++j) {
+      const int c = n0 + tx * R + j;
       if (c < N) out[(int64_t)m * N + c] = Elem<T>::from_f(acc[i][j]);
     }
   }
 }
 
-template <typename T>
+template <typename T, int TILE>
 cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
-  const int mt = (p.rows + TM - 1) / TM + (p.offsets ? p.num_experts : 0);
-  const dim3 grid(mt, (p.N + TN - 1) / TN);
+  const int mt = (p.rows + TILE - 1) / TILE + (p.offsets ? p.num_experts : 0);
+  const dim3 grid(mt, (p.N + TILE - 1) / TILE);
   if (p.epi == kRowsPlain && p.b_rows)
-    rows_simt_kernel<T, kRowsPlain, true><<<grid, T_THREADS, 0, s>>>(p, status);
+    rows_simt_kernel<T, kRowsPlain, true, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
   else if (p.epi == kRowsPlain)
-    rows_simt_kernel<T, kRowsPlain, false><<<grid, T_THREADS, 0, s>>>(p, status);
+    rows_simt_kernel<T, kRowsPlain, false, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
   else if (p.epi == kRowsRelu)
-    rows_simt_kernel<T, kRowsRelu, false><<<grid, T_THREADS, 0, s>>>(p, status);
+    rows_simt_kernel<T, kRowsRelu, false, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
   else if (p.epi == kRowsSwiglu)
-    rows_simt_kernel<T, kRowsSwiglu, false><<<grid, T_THREADS, 0, s>>>(p, status);
+    rows_simt_kernel<T, kRowsSwiglu, false, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
   else if (p.epi == kRowsReluGrad)
-    rows_simt_kernel<T, kRowsReluGrad, true><<<grid, T_THREADS, 0, s>>>(p, status);
+    rows_simt_kernel<T, kRowsReluGrad, true, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
   else
-    rows_simt_kernel<T, kRowsSwigluGrad, true><<<grid, T_THREADS, 0, s>>>(p, status);
+    rows_simt_kernel<T, kRowsSwigluGrad, true, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
   return cudaGetLastError();
 }
 
+// Whether this many 64 x 64 tiles give each SM one.
+bool large_tiles(int64_t tiles) { return tiles >= num_sms(); }
+
 }  // namespace
 
+// fp32 layers only: bf16 layers run on the tensor cores.
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s) {
-  return p.dtype == MOE_F32 ? launch_rows<float>(p, status, s)
-                            : launch_rows<__nv_bfloat16>(p, status, s);
+  if (p.dtype != MOE_F32) return cudaErrorInvalidValue;
+  return large_tiles((int64_t)((p.rows + 63) / 64) * ((p.N + 63) / 64))
+             ? launch_rows<float, 64>(p, status, s)
+             : launch_rows<float, 32>(p, status, s);
 }
 
 cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s) {
-  const dim3 grid((p.N + TN - 1) / TN, (p.M + TM - 1) / TM, p.offsets ? p.num_experts : 1);
-  if (p.dtype == MOE_F32) grad_simt_kernel<float><<<grid, T_THREADS, 0, s>>>(p, status);
-  else grad_simt_kernel<__nv_bfloat16><<<grid, T_THREADS, 0, s>>>(p, status);
+  if (p.dtype != MOE_F32) return cudaErrorInvalidValue;
+  const int E = p.offsets ? p.num_experts : 1;
+  const bool large = large_tiles((int64_t)((p.N + 63) / 64) * ((p.M + 63) / 64) * E);
+  const int tile = large ? 64 : 32;
+  const dim3 grid((p.N + tile - 1) / tile, (p.M + tile - 1) / tile, E);
+  if (large) grad_simt_kernel<float, 64><<<grid, T_THREADS, 0, s>>>(p, status);
+  else grad_simt_kernel<float, 32><<<grid, T_THREADS, 0, s>>>(p, status);
   return cudaGetLastError();
 }
 
