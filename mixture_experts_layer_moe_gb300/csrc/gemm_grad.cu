@@ -142,12 +142,12 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
   const int E = args.offsets ? args.num_experts : 1;
 
   if (threadIdx.x == 0) {
-    sh.failed_on_entry = status_failed(args.status) ? 1 : 0;
-    sh.abort = sh.failed_on_entry;
-    sh.bad = 0;
+    for (int i = 0; i < args.problems; ++i) {
+      tc::prefetch_tmap(&maps.a[i]);
+      tc::prefetch_tmap(&maps.b[i]);
+      tc::prefetch_tmap(&maps.out[i]);
+    }
   }
-  for (int i = threadIdx.x; i <= E; i += G_THREADS)
-    sh.offs[i] = args.offsets ? args.offsets[i] : (i == 0 ? 0 : args.rows);
   if (warp == 1) tmem_alloc2(&sh.tmem_base, G_TMEM_COLS);
   if (threadIdx.x == 32) {
     for (int s = 0; s < GS; ++s) {
@@ -163,6 +163,16 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
     tc::mbar_init(&sh.drain, 1);
     tc::fence_mbar_init();
   }
+  // (all above ran beside the end of the kernel before; from here on its
+  // results are read)
+  pdl_wait();
+  if (threadIdx.x == 0) {
+    sh.failed_on_entry = status_failed(args.status) ? 1 : 0;
+    sh.abort = sh.failed_on_entry;
+    sh.bad = 0;
+  }
+  for (int i = threadIdx.x; i <= E; i += G_THREADS)
+    sh.offs[i] = args.offsets ? args.offsets[i] : (i == 0 ? 0 : args.rows);
   __syncthreads();
   for (int i = threadIdx.x; i < E; i += G_THREADS) {
     const int b = sh.offs[i], en = sh.offs[i + 1];
@@ -392,6 +402,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
+  pdl_launch_dependents();
   // neither CTA leaves (or frees its tensor memory) while the other may still
   // read its shared memory, signal its barriers or write its tensor memory
   cluster_sync();
@@ -443,13 +454,15 @@ cudaError_t launch(const GMaps &maps, const GArgs &a, cudaStream_t s) {
   cfg.blockDim = dim3(G_THREADS);
   cfg.dynamicSmemBytes = G_DYN_SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 1;   // (the occupancy query takes the cluster alone)
   static int pairs = 0;
   if (pairs == 0) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -462,6 +475,7 @@ cudaError_t launch(const GMaps &maps, const GArgs &a, cudaStream_t s) {
     }
   }
   cfg.gridDim = dim3(2 * pairs);
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
 

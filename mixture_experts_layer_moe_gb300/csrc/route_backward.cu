@@ -26,7 +26,8 @@ route_grad_kernel(const float *__restrict__ probs, const int32_t *__restrict__ t
                   const float *__restrict__ f, float aux_scale, int renorm, int n, int E, int k,
                   T *__restrict__ dl, int pitch, float *__restrict__ bias_parts, int *status) {
   __shared__ float s_sum[RB_WARPS][RB_SLOTS * 32];
-  pdl_launch_dependents();   // (the column sums wait for this grid to end)
+  pdl_launch_dependents();
+  pdl_wait();
   if (status_failed(status)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float fe[RB_SLOTS], col[RB_SLOTS];
@@ -121,17 +122,18 @@ cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int
   const float scale = aux * (float)E / (float)c.n;
   // one CTA's sums are the result
   float *parts = dbias == nullptr ? nullptr : grid == 1 ? dbias : scratch;
+  const dim3 blocks(grid), threads(32 * RB_WARPS);
+  cudaError_t e;
   if (c.act_dtype == MOE_F32)
-    route_grad_kernel<float><<<grid, 32 * RB_WARPS, 0, s>>>(
-        probs, topk_idx, gates, dgate, f, scale, renorm, c.n, E, c.top_k, (float *)dl, pitch, parts,
-        status);
+    e = launch_pdl(route_grad_kernel<float>, blocks, threads, 0, s, probs, topk_idx, gates, dgate, f,
+                   scale, renorm, c.n, E, c.top_k, (float *)dl, pitch, parts, status);
   else
-    route_grad_kernel<__nv_bfloat16><<<grid, 32 * RB_WARPS, 0, s>>>(
-        probs, topk_idx, gates, dgate, f, scale, renorm, c.n, E, c.top_k, (__nv_bfloat16 *)dl,
-        pitch, parts, status);
-  if (dbias && grid > 1)
-    return launch_column_sum(scratch, nullptr, grid, E, dbias, nullptr, status, s);
-  return cudaGetLastError();
+    e = launch_pdl(route_grad_kernel<__nv_bfloat16>, blocks, threads, 0, s, probs, topk_idx, gates,
+                   dgate, f, scale, renorm, c.n, E, c.top_k, (__nv_bfloat16 *)dl, pitch, parts,
+                   status);
+  if (e == cudaSuccess && dbias && grid > 1)
+    e = launch_column_sum(scratch, nullptr, grid, E, dbias, nullptr, status, s);
+  return e;
 }
 
 }  // namespace moe

@@ -8,7 +8,7 @@
 // tiles would not give every SM one.  The next step's operands are loaded into
 // registers while the current one is multiplied, and shared memory is double
 // buffered, so a step waits for memory once, not twice (256 rows, d 128, d_ff
-// 512, 4 experts, forward: 49 us without either, TODO_SIMT).
+// 512, 4 experts, forward: 49 us without any of it, 15.6 with).
 // The three storage orders of the operands differ in how a tile is staged
 // only: in shared memory both operands lie reduction index first, so that a
 // thread reads its values of a step as two vectors.
@@ -23,10 +23,14 @@ namespace {
 
 constexpr int T_THREADS = 256;
 
-// TILE x TILE outputs per CTA, R x R per thread, TK reduction indexes a step.
+// TILE x TILE outputs per CTA, 4 x 4 per thread, TK reduction indexes a step.
+// A 32 x 32 tile has threads for four groups, which take a quarter of a step's
+// indexes each and are added up at the end (2 x 2 outputs per thread instead
+// read shared memory four times as often).
 template <int TILE>
 struct Geo {
-  static constexpr int R = TILE / 16, TK = 1024 / TILE, LD = TILE + 4;
+  static constexpr int TX = TILE / 4, GROUPS = T_THREADS / (TX * TX);
+  static constexpr int TK = TILE == 64 ? 16 : 64, LD = TILE + 4;
   static constexpr int LOADS = TILE * TK / T_THREADS;
   using Buf = float[TK][LD];
 };
@@ -55,31 +59,65 @@ struct Part {
   }
 };
 
-template <int R>
-__device__ __forceinline__ void read_vec(const float *p, float (&v)[R]) {
-  if constexpr (R == 4) {
-    const float4 t = *reinterpret_cast<const float4 *>(p);
-    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-  } else {
-    const float2 t = *reinterpret_cast<const float2 *>(p);
-    v[0] = t.x; v[1] = t.y;
+template <int TILE>
+__device__ __forceinline__ void tile_fma(float (&acc)[4][4], const typename Geo<TILE>::Buf &as,
+                                         const typename Geo<TILE>::Buf &bs, int tx, int ty, int g) {
+#pragma unroll
+  for (int kk = 0; kk < Geo<TILE>::TK; kk += Geo<TILE>::GROUPS) {
+    const float4 a4 = *reinterpret_cast<const float4 *>(&as[kk + g][ty * 4]);
+    const float4 b4 = *reinterpret_cast<const float4 *>(&bs[kk + g][tx * 4]);
+    const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
   }
 }
 
-template <int TILE, int R = Geo<TILE>::R>
-__device__ __forceinline__ void tile_fma(float (&acc)[R][R], const typename Geo<TILE>::Buf &as,
-                                         const typename Geo<TILE>::Buf &bs, int tx, int ty) {
-#pragma unroll 16
-  for (int kk = 0; kk < Geo<TILE>::TK; ++kk) {
-    float a[R], b[R];
-    read_vec(&as[kk][ty * R], a);
-    read_vec(&bs[kk][tx * R], b);
+// Adds the groups' sums in order, through `scratch` (GROUPS x TILE x TILE
+// floats of shared memory that nothing else uses any more), so that each
+// thread ends with four neighbouring outputs of one row: acc[0].
+template <int TILE>
+__device__ __forceinline__ void join_groups(float (&acc)[4][4], float *scratch, int tx, int ty,
+                                            int g) {
+  if constexpr (Geo<TILE>::GROUPS > 1) {
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4 *>(scratch + (g * TILE + ty * 4 + i) * TILE + tx * 4) =
+          make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    __syncthreads();
+    float4 sum = *reinterpret_cast<const float4 *>(scratch + threadIdx.x * 4);
 #pragma unroll
-      for (int j = 0; j < R; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    for (int h = 1; h < Geo<TILE>::GROUPS; ++h) {
+      const float4 v = *reinterpret_cast<const float4 *>(scratch + h * TILE * TILE + threadIdx.x * 4);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    acc[0][0] = sum.x;
+    acc[0][1] = sum.y;
+    acc[0][2] = sum.z;
+    acc[0][3] = sum.w;
   }
 }
+
+// This thread's place: its 4 x 4 outputs while summing, and the rows x 4
+// outputs it ends with.
+template <int TILE>
+struct Place {
+  static constexpr int ROWS = Geo<TILE>::GROUPS > 1 ? 1 : 4;
+  int tx, ty, g, row, col;
+  __device__ __forceinline__ Place() {
+    constexpr int TX = Geo<TILE>::TX;
+    g = threadIdx.x / (TX * TX);
+    tx = threadIdx.x % TX;
+    ty = threadIdx.x / TX % TX;
+    row = ROWS == 1 ? threadIdx.x / TX : ty * 4;
+    col = tx * 4;
+  }
+};
 
 // Expert and row range of this CTA's tile; false when there is none.
 template <int TM>
@@ -113,17 +151,22 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int row
 template <typename T, int EPI, bool B_ROWS, int TILE>
 __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int *status) {
   using G = Geo<TILE>;
-  constexpr int R = G::R;
   constexpr bool DUAL = EPI == kRowsSwiglu;
-  __shared__ __align__(16) typename G::Buf as[2], bs[2], b2s[DUAL ? 2 : 1];
+  // (three operands of deep steps: one buffer and a second barrier)
+  constexpr int BUFS = DUAL && TILE == 32 ? 1 : 2;
+  __shared__ __align__(16) typename G::Buf pool[(DUAL ? 3 : 2) * BUFS];
+  typename G::Buf *as = pool, *bs = pool + BUFS, *b2s = pool + (DUAL ? 2 * BUFS : 0);
+  static_assert(sizeof(pool) >= sizeof(float) * G::GROUPS * TILE * TILE || G::GROUPS == 1,
+                "join_groups' scratch");
+  pdl_wait();
   if (status_failed(status)) return;
   int e, row0, end;
   if (!find_tile<TILE>(p.offsets, p.num_experts, p.rows, blockIdx.x, e, row0, end, status)) return;
   const int n0 = blockIdx.y * TILE, N = p.N, K = p.K;
   const int64_t lda = p.lda ? p.lda : K;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const Place<TILE> me;
   const int64_t base = (int64_t)e * N * K + (B_ROWS ? (int64_t)n0 : (int64_t)n0 * K);
-  float acc[R][R] = {}, acc2[R][R] = {};
+  float acc[4][4] = {}, acc2[4][4] = {};
   // the steps of the one or two operand pairs, one after the other
   const int steps1 = (K + G::TK - 1) / G::TK;
   const int steps = steps1 * (EPI == kRowsPlain && p.A2 ? 2 : 1);
@@ -140,22 +183,28 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   };
   load(0);
   for (int step = 0; step < steps; ++step) {
-    const int buf = step & 1;
+    const int buf = BUFS == 2 ? step & 1 : 0;
+    if (BUFS == 1 && step > 0) __syncthreads();
     pa.store(as[buf]);
     pb.store(bs[buf]);
     if constexpr (DUAL) pb2.store(b2s[buf]);
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
-    tile_fma<TILE>(acc, as[buf], bs[buf], tx, ty);
-    if constexpr (DUAL) tile_fma<TILE>(acc2, as[buf], b2s[buf], tx, ty);
+    tile_fma<TILE>(acc, as[buf], bs[buf], me.tx, me.ty, me.g);
+    if constexpr (DUAL) tile_fma<TILE>(acc2, as[buf], b2s[buf], me.tx, me.ty, me.g);
   }
+  // (the next kernel's CTAs, placed from the start, would share these SMs: 25 us
+  // for the two products of the tiny layer's forward, 20 launched apart, 15.6 so)
+  pdl_launch_dependents();
+  join_groups<TILE>(acc, &pool[0][0][0], me.tx, me.ty, me.g);
+  if constexpr (DUAL) join_groups<TILE>(acc2, &pool[0][0][0], me.tx, me.ty, me.g);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int r = row0 + ty * R + i;
+  for (int i = 0; i < Place<TILE>::ROWS; ++i) {
+    const int r = row0 + me.row + i;
     if (r >= end) continue;
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int c = n0 + tx * R + j;
+    for (int j = 0; j < 4; ++j) {
+      const int c = n0 + me.col + j;
       if (c >= N) continue;
       const int64_t at = (int64_t)r * N + c;
       float v = acc[i][j];
@@ -182,8 +231,10 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
 template <typename T, int TILE>
 __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int *status) {
   using G = Geo<TILE>;
-  constexpr int R = G::R;
   __shared__ __align__(16) typename G::Buf as[2], bs[2];
+  static_assert(sizeof(as) >= sizeof(float) * G::GROUPS * TILE * TILE || G::GROUPS == 1,
+                "join_groups' scratch");
+  pdl_wait();
   if (status_failed(status)) return;
   const int e = blockIdx.z, m0 = blockIdx.y * TILE, n0 = blockIdx.x * TILE, M = p.M, N = p.N;
   const int beg = p.offsets ? p.offsets[e] : 0, end = p.offsets ? p.offsets[e + 1] : p.rows;
@@ -192,8 +243,8 @@ __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int
     return;
   }
   const int64_t lda = p.lda ? p.lda : M;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[R][R] = {};
+  const Place<TILE> me;
+  float acc[4][4] = {};
   const T *A = static_cast<const T *>(p.A) + m0, *B = static_cast<const T *>(p.B) + n0;
   Part<T, false, TILE> pa, pb;
   auto load = [&](int q) {
@@ -206,16 +257,18 @@ __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int
     pb.store(bs[buf]);
     __syncthreads();
     if (q + G::TK < end) load(q + G::TK);
-    tile_fma<TILE>(acc, as[buf], bs[buf], tx, ty);
+    tile_fma<TILE>(acc, as[buf], bs[buf], me.tx, me.ty, me.g);
   }
   T *out = static_cast<T *>(p.out) + (int64_t)e * M * N;
+  pdl_launch_dependents();
+  join_groups<TILE>(acc, &as[0][0][0], me.tx, me.ty, me.g);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int m = m0 + ty * R + i;
+  for (int i = 0; i < Place<TILE>::ROWS; ++i) {
+    const int m = m0 + me.row + i;
     if (m >= M) continue;
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int c = n0 + tx * R + j;
+    for (int j = 0; j < 4; ++j) {
+      const int c = n0 + me.col + j;
       if (c < N) out[(int64_t)m * N + c] = Elem<T>::from_f(acc[i][j]);
     }
   }
@@ -225,19 +278,22 @@ template <typename T, int TILE>
 cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   const int mt = (p.rows + TILE - 1) / TILE + (p.offsets ? p.num_experts : 0);
   const dim3 grid(mt, (p.N + TILE - 1) / TILE);
+  cudaError_t e;
   if (p.epi == kRowsPlain && p.b_rows)
-    rows_simt_kernel<T, kRowsPlain, true, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
+    e = launch_pdl(rows_simt_kernel<T, kRowsPlain, true, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
   else if (p.epi == kRowsPlain)
-    rows_simt_kernel<T, kRowsPlain, false, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
+    e = launch_pdl(rows_simt_kernel<T, kRowsPlain, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
   else if (p.epi == kRowsRelu)
-    rows_simt_kernel<T, kRowsRelu, false, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
+    e = launch_pdl(rows_simt_kernel<T, kRowsRelu, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
   else if (p.epi == kRowsSwiglu)
-    rows_simt_kernel<T, kRowsSwiglu, false, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
+    e = launch_pdl(rows_simt_kernel<T, kRowsSwiglu, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
   else if (p.epi == kRowsReluGrad)
-    rows_simt_kernel<T, kRowsReluGrad, true, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
+    e = launch_pdl(rows_simt_kernel<T, kRowsReluGrad, true, TILE>, grid, dim3(T_THREADS), 0, s, p,
+                   status);
   else
-    rows_simt_kernel<T, kRowsSwigluGrad, true, TILE><<<grid, T_THREADS, 0, s>>>(p, status);
-  return cudaGetLastError();
+    e = launch_pdl(rows_simt_kernel<T, kRowsSwigluGrad, true, TILE>, grid, dim3(T_THREADS), 0, s, p,
+                   status);
+  return e;
 }
 
 // Whether this many 64 x 64 tiles give each SM one.
@@ -259,9 +315,8 @@ cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s) 
   const bool large = large_tiles((int64_t)((p.N + 63) / 64) * ((p.M + 63) / 64) * E);
   const int tile = large ? 64 : 32;
   const dim3 grid((p.N + tile - 1) / tile, (p.M + tile - 1) / tile, E);
-  if (large) grad_simt_kernel<float, 64><<<grid, T_THREADS, 0, s>>>(p, status);
-  else grad_simt_kernel<float, 32><<<grid, T_THREADS, 0, s>>>(p, status);
-  return cudaGetLastError();
+  return launch_pdl(large ? grad_simt_kernel<float, 64> : grad_simt_kernel<float, 32>, grid,
+                    dim3(T_THREADS), 0, s, p, status);
 }
 
 }  // namespace moe

@@ -310,40 +310,42 @@ def alloc_train_workspace(cfg, device="cuda") -> torch.Tensor:
 _NORM_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _norm_rows(t: torch.Tensor, like: torch.Tensor):
+def _norm_rows(t: torch.Tensor, shape, dtype) -> tuple[int, int]:
     """(pointer, elements from one row to the next) of a [rows, d] tensor whose rows are dense."""
-    if t.dim() != 2 or t.shape != like.shape or t.dtype != like.dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError("rows of a layer norm must be [rows, d] tensors of one shape and type")
-    rows, d = t.shape
-    if d > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError("rows of a layer norm must be dense")
-    return t.data_ptr(), t.stride(0) if rows > 1 else d
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
-def _norm_vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, what: str):
-    if t is not None and (t.dtype != dtype or t.numel() != n):
-        raise ValueError(f"{what} must hold {n} values of {dtype}")
+def _norm_vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n:
+        raise ValueError(f"a layer norm's vector must hold {n} values of {dtype}")
     return _ptr(t)
 
 
-def _norm_config(x: torch.Tensor, eps: float = 0.0) -> moe_norm_config:
-    if x.dtype not in _NORM_DTYPE:
-        raise ValueError("a layer norm takes float32 or bfloat16 rows")
-    _, ldx = _norm_rows(x, x)
-    return moe_norm_config(x.shape[0], ldx, 0, 0, 0, x.shape[1], _NORM_DTYPE[x.dtype], eps, 0)
+def _norm_shape(x: torch.Tensor):
+    dtype = _NORM_DTYPE.get(x.dtype)
+    if dtype is None or x.dim() != 2:
+        raise ValueError("a layer norm takes [rows, d] tensors of float32 or bfloat16")
+    return x.shape, x.dtype, dtype
 
 
 def moe_layernorm(x, gamma, beta, y, mean, rstd, eps=1e-5, stream=None):
     """x, y [rows, d] (rows may lie apart); beta and the pair mean, rstd may be None."""
-    c = _norm_config(x, eps)
-    xp, _ = _norm_rows(x, x)
-    yp, c.ldy = _norm_rows(y, x)
-    n, d = x.shape
-    _check(_lib.moe_layernorm(ctypes.byref(c), xp, _norm_vector(gamma, d, x.dtype, "gamma"),
-                              _norm_vector(beta, d, x.dtype, "beta"), yp,
-                              _norm_vector(mean, n, torch.float32, "mean"),
-                              _norm_vector(rstd, n, torch.float32, "rstd"), _stream(stream)),
-           "moe_layernorm")
+    shape, xt, code = _norm_shape(x)
+    n, d = shape
+    xp, ldx = _norm_rows(x, shape, xt)
+    yp, ldy = _norm_rows(y, shape, xt)
+    c = moe_norm_config(n, ldx, ldy, 0, 0, d, code, eps, 0)
+    f32 = torch.float32
+    _check(_lib.moe_layernorm(ctypes.byref(c), xp, _norm_vector(gamma, d, xt),
+                              _norm_vector(beta, d, xt), yp, _norm_vector(mean, n, f32),
+                              _norm_vector(rstd, n, f32), _stream(stream)), "moe_layernorm")
 
 
 def moe_layernorm_workspace_size(rows: int, d: int, dtype: str) -> int:
@@ -359,17 +361,18 @@ def moe_layernorm_workspace_size(rows: int, d: int, dtype: str) -> int:
 
 def moe_layernorm_backward(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, stream=None):
     """ws: scratch of moe_layernorm_workspace_size bytes (uint8); dgamma, dbeta fp32 or None."""
-    c = _norm_config(x)
-    xp, _ = _norm_rows(x, x)
-    dyp, c.lddy = _norm_rows(dy, x)
-    dxp, c.lddx = _norm_rows(dx, x)
-    n, d = x.shape
+    shape, xt, code = _norm_shape(x)
+    n, d = shape
+    xp, ldx = _norm_rows(x, shape, xt)
+    dyp, lddy = _norm_rows(dy, shape, xt)
+    dxp, lddx = _norm_rows(dx, shape, xt)
+    c = moe_norm_config(n, ldx, 0, lddx, lddy, d, code, 0.0, 0)
     f32 = torch.float32
     _check(_lib.moe_layernorm_backward(
-        ctypes.byref(c), xp, _norm_vector(gamma, d, x.dtype, "gamma"),
-        _norm_vector(mean, n, f32, "mean"), _norm_vector(rstd, n, f32, "rstd"), dyp, dxp,
-        _norm_vector(dgamma, d, f32, "dgamma"), _norm_vector(dbeta, d, f32, "dbeta"), _ptr(ws),
-        ws.numel(), _stream(stream)), "moe_layernorm_backward")
+        ctypes.byref(c), xp, _norm_vector(gamma, d, xt), _norm_vector(mean, n, f32),
+        _norm_vector(rstd, n, f32), dyp, dxp, _norm_vector(dgamma, d, f32),
+        _norm_vector(dbeta, d, f32), _ptr(ws), ws.numel(), _stream(stream)),
+        "moe_layernorm_backward")
 
 
 def moe_expert_ffn_train(cfg, x_perm, offsets, w: moe_weights, g, u, h, y_perm, ws, stream=None):
