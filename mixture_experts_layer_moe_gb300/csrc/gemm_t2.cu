@@ -29,7 +29,7 @@
 //              first CTA one thread issues the MMAs (M 256, N <= 256, K 16) into
 //              two accumulators of 256 columns and commits to the barriers of
 //              both CTAs at once (multicast arrive).
-//   warps 2-5  epilogue in both CTAs: each drains its own TMEM lanes, applies
+//   warps 2..  epilogue in both CTAs: each drains its own TMEM lanes, applies
 //              the activation, rounds to bf16 and stores the rows masked to the
 //              segment, then arrives (remotely, for the second CTA) on the
 //              first CTA's accumulator-empty barrier.
@@ -67,15 +67,23 @@ constexpr int PS = 6;                           // pipeline stages
 constexpr int P_B_BYTES = (PN / 2) * PK * 2;    // this CTA's half of the token tile: 16 KB
 constexpr int P_A_BYTES = PM * PK * 2;          // this CTA's weight rows: 16 KB
 constexpr int P_STAGE = P_B_BYTES + P_A_BYTES;  // 32 KB (tokens first, then weights)
-constexpr int P_EPI = 4;                        // epilogue warps
-constexpr int P_THREADS = 32 * (2 + P_EPI);
+// epilogue warps: one to three per TMEM lane quarter, which take turns of 32
+// tokens (16 for a gradient).  A training epilogue moves two to four values per
+// product; where the reduction is short it is what bounds the kernel (64
+// experts of 512 rows, d = d_ff = 1024: up projection 155 -> 133 us with 8
+// warps, dg and du 183 -> 132 with 8 and 120 with 12).
+template <int EPI>
+constexpr int epi_warps() { return EPI >= 6 ? 12 : EPI == 5 ? 8 : 4; }
+template <int EPI>
+constexpr int pair_threads() { return 32 * (2 + epi_warps<EPI>()); }
 constexpr uint32_t P_TMEM_COLS = 512;           // two accumulators of PN columns
 constexpr int P_MAX_E = 256;
-// SwiGLU exchange: per warp pair, two chunk buffers (alternating), each with
-// 16 values per lane going each way; rows of 17 floats avoid bank conflicts
+// SwiGLU exchange: two chunk buffers per column half (two warp pairs with one
+// buffer each, or one pair with two, alternating), each with 16 values per
+// lane going each way; rows of 17 floats avoid bank conflicts
 constexpr int P_XROW = 17;
 constexpr int P_XBUF = 32 * P_XROW;              // floats of one direction of one chunk
-constexpr size_t P_XBYTES = (size_t)2 * 2 * 2 * P_XBUF * 4;   // pairs x chunks x directions
+constexpr size_t P_XBYTES = (size_t)2 * 2 * 2 * P_XBUF * 4;   // halves x buffers x directions
 constexpr size_t P_DYN_SMEM = 1024 + (size_t)PS * P_STAGE + P_XBYTES;
 static_assert(P_STAGE % 1024 == 0, "stage alignment");
 
@@ -166,18 +174,19 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
   return *reinterpret_cast<const uint16_t *>(&h);
 }
 
-// Kept rows of a gradient's epilogue: this thread's column of 32 tokens (h for
+// Kept rows of a gradient's epilogue: this thread's column of 16 tokens (h for
 // the ReLU, g and u for SwiGLU; 0 outside the segment).
-template <int EPI, int NG, int NU>
+constexpr int KEPT = 16;
+template <int EPI>
 __device__ __forceinline__ void load_kept(const PArgs &args, int tok0, int end, int col, bool col_ok,
-                                          uint16_t (&kg)[NG], uint16_t (&ku)[NU]) {
-  const uint16_t *g = EPI == 6 ? args.h : args.g;
+                                          uint16_t (&kg)[KEPT], uint16_t (&ku)[KEPT]) {
+  const size_t at = (size_t)tok0 * args.N + col;
+  const uint16_t *g = (EPI == 6 ? args.h : args.g) + at, *u = args.u + at;
 #pragma unroll
-  for (int i = 0; i < NG; ++i) {
+  for (int i = 0; i < KEPT; ++i) {
     const bool ok = col_ok && tok0 + i < end;
-    const size_t at = (size_t)(tok0 + i) * args.N + col;
-    kg[i] = ok ? __ldg(g + at) : (uint16_t)0;
-    if constexpr (EPI == 7) ku[i] = ok ? __ldg(args.u + at) : (uint16_t)0;
+    kg[i] = ok ? __ldg(g + (size_t)i * args.N) : (uint16_t)0;
+    if constexpr (EPI == 7) ku[i] = ok ? __ldg(u + (size_t)i * args.N) : (uint16_t)0;
   }
 }
 
@@ -188,11 +197,12 @@ __device__ __forceinline__ void load_kept(const PArgs &args, int tok0, int end, 
 // an M-major operand, staged as two boxes of 64 columns x 64 reduction rows
 // (128-byte swizzle, the boxes 8 KB apart), and no transposed copy is made.
 template <int EPI, bool WROWS>
-__global__ void __launch_bounds__(P_THREADS, 1)
+__global__ void __launch_bounds__(pair_threads<EPI>(), 1)
 gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                const __grid_constant__ CUtensorMap tmX2, const __grid_constant__ CUtensorMap tmW3,
                PArgs args) {
   constexpr bool GATED = EPI == 2 || EPI == 5;        // two weight matrices side by side
+  constexpr int P_EPI = epi_warps<EPI>(), P_THREADS = pair_threads<EPI>(), TURNS = P_EPI / 4;
   static_assert(!WROWS || !GATED, "the gated forward reads weights stored by output column");
   constexpr int OUT_CTA = GATED ? PM / 2 : PM;        // output columns per CTA per tile
   constexpr int OUT_TILE = 2 * OUT_CTA;
@@ -377,7 +387,7 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     }
   } else {
     // ---------------- epilogue (both CTAs): warp w drains TMEM lanes 32*(w%4) .. +31
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
     const int pq = quarter & 1;                  // SwiGLU: W1 quarter pq pairs with W3 quarter pq + 2
     const bool w3 = quarter >= 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
@@ -394,20 +404,57 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       const bool col_ok = col < args.N;
       uint16_t *o = reinterpret_cast<uint16_t *>(args.out) + col;
       // a gradient's kept rows: the first chunk is in flight during the wait
-      uint16_t kg[EPI >= 6 ? 32 : 1], ku[EPI == 7 ? 32 : 1];
-      if constexpr (EPI >= 6) load_kept<EPI>(args, tl.tok0, tl.seg_end, col, col_ok, kg, ku);
+      uint16_t kg[KEPT], ku[KEPT];
+      if constexpr (EPI >= 6)
+        load_kept<EPI>(args, tl.tok0 + part * KEPT, tl.seg_end, col, col_ok, kg, ku);
       const bool ok = tc::mbar_wait(&sh.tfull[acc], (local >> 1) & 1, abort);
       if constexpr (GATED) {
         // the two warps of a pair meet on named barriers below: they agree on
         // going on first (a warp whose wait ran out has raised *abort)
-        if (tc::bar_or(1 + pq, 64, !ok)) break;
+        if (tc::bar_or(1 + pq + 2 * part, 64, !ok)) break;
       } else {
         if (!__all_sync(0xffffffffu, ok)) break;
       }
       tc::tc_fence_after();
       const uint32_t tb = lane_base + (uint32_t)(acc * PN);
+      if constexpr (EPI >= 6) {
+        // 16 tokens at a time: the next ones' kept rows are in flight while
+        // these are formed and stored
 #pragma unroll 1
-      for (int c = 0; c * 32 < ntok; ++c) {
+        for (int c = part; c * KEPT < ntok; c += TURNS) {
+          uint32_t a[KEPT];
+          tc::tmem_ld16(tb + (uint32_t)(c * KEPT), a);
+          tc::tmem_ld_wait();
+          const int tok0 = tl.tok0 + c * KEPT;
+          uint16_t dg[KEPT], du[KEPT];
+#pragma unroll
+          for (int i = 0; i < KEPT; ++i) {
+            const float v = __uint_as_float(a[i]);
+            if constexpr (EPI == 6) {
+              dg[i] = bf16_value(kg[i]) > 0.f ? bf16_bits(v) : (uint16_t)0;
+            } else {
+              const float g = bf16_value(kg[i]), u = bf16_value(ku[i]);
+              const float sg = __fdividef(1.f, 1.f + __expf(-g));
+              dg[i] = bf16_bits(v * u * sg * (1.f + g * (1.f - sg)));
+              du[i] = bf16_bits(v * g * sg);
+            }
+          }
+          load_kept<EPI>(args, tok0 + KEPT * TURNS, tl.seg_end, col, col_ok, kg, ku);
+          if (col_ok) {
+            uint16_t *og = o + (size_t)tok0 * args.N;
+            uint16_t *ou = reinterpret_cast<uint16_t *>(args.out_u) + (size_t)tok0 * args.N + col;
+#pragma unroll
+            for (int i = 0; i < KEPT; ++i) {
+              if (tok0 + i < tl.seg_end) {
+                og[(size_t)i * args.N] = dg[i];
+                if constexpr (EPI == 7) ou[(size_t)i * args.N] = du[i];
+              }
+            }
+          }
+        }
+      } else {
+#pragma unroll 1
+      for (int c = part; c * 32 < ntok; c += TURNS) {
         uint32_t a[32];
         tc::tmem_ld32(tb + (uint32_t)(c * 32), a);
         tc::tmem_ld_wait();
@@ -415,13 +462,14 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         if constexpr (GATED) {
           // the W1 warp (gate values) finishes tokens 0..15 of the chunk, the
           // W3 warp (up values) tokens 16..31; each hands the other its half
+          // (buffer c & 1: alternating for one pair, one for each of two)
           float *to_w3 = xbuf + (size_t)((pq * 2 + (c & 1)) * 2) * P_XBUF;   // gates 16..31
           float *to_w1 = to_w3 + P_XBUF;                                    // ups 0..15
           float *mine = w3 ? to_w1 : to_w3;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             mine[lane * P_XROW + i] = __uint_as_float(w3 ? a[i] : a[16 + i]);
-          asm volatile("bar.sync %0, 64;" ::"r"(3 + pq) : "memory");
+          asm volatile("bar.sync %0, 64;" ::"r"(5 + pq + 2 * part) : "memory");
           const float *theirs = w3 ? to_w3 : to_w1;
           uint16_t hv[16], gv[EPI == 5 ? 16 : 1], uv[EPI == 5 ? 16 : 1];
 #pragma unroll
@@ -436,6 +484,8 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             }
           }
           const int tsub = w3 ? 16 : 0;
+          // a pair with one buffer: both have read it before either writes again
+          if (TURNS == 2) asm volatile("bar.sync %0, 64;" ::"r"(9 + pq + 2 * part) : "memory");
           if (col_ok) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -446,33 +496,6 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                   reinterpret_cast<uint16_t *>(args.out_g)[(size_t)tok * args.N + col] = gv[i];
                   reinterpret_cast<uint16_t *>(args.out_u)[(size_t)tok * args.N + col] = uv[i];
                 }
-              }
-            }
-          }
-        } else if constexpr (EPI >= 6) {
-          uint16_t dg[32], du[EPI == 7 ? 32 : 1];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float v = __uint_as_float(a[i]);
-            if constexpr (EPI == 6) {
-              dg[i] = bf16_value(kg[i]) > 0.f ? bf16_bits(v) : (uint16_t)0;
-            } else {
-              const float g = bf16_value(kg[i]), u = bf16_value(ku[i]);
-              const float sg = __fdividef(1.f, 1.f + __expf(-g));
-              dg[i] = bf16_bits(v * u * sg * (1.f + g * (1.f - sg)));
-              du[i] = bf16_bits(v * g * sg);
-            }
-          }
-          // the next chunk's kept rows are in flight while this one is stored
-          load_kept<EPI>(args, tok0 + 32, tl.seg_end, col, col_ok, kg, ku);
-          if (col_ok) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int tok = tok0 + i;
-              if (tok < tl.seg_end) {
-                o[(size_t)tok * args.N] = dg[i];
-                if constexpr (EPI == 7)
-                  reinterpret_cast<uint16_t *>(args.out_u)[(size_t)tok * args.N + col] = du[i];
               }
             }
           }
@@ -487,6 +510,7 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             }
           }
         }
+      }
       }
       tc::tc_fence_before();
       __syncwarp();
@@ -509,10 +533,10 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     set_status(args.status, MOE_ERR_TIMEOUT, blockIdx.x);
 }
 
-int pairs_resident(const void *kernel, size_t smem) {
+int pairs_resident(const void *kernel, int threads, size_t smem) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (num_sms() / 2));
-  cfg.blockDim = dim3(P_THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -538,7 +562,8 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)P_DYN_SMEM);
     if (e != cudaSuccess) return e;
-    pairs = pairs_resident(reinterpret_cast<const void *>(gemm_t2_kernel<EPI, WROWS>), P_DYN_SMEM);
+    pairs = pairs_resident(reinterpret_cast<const void *>(gemm_t2_kernel<EPI, WROWS>),
+                           pair_threads<EPI>(), P_DYN_SMEM);
   }
   const int E = g.offsets ? g.num_experts : 1;
   CUtensorMap mX, mW, mX2, mW3;
@@ -582,7 +607,7 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
   a.tok_major = seg_rows > (long)g.N * (GATED ? 2 : 1) ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(P_THREADS);
+  cfg.blockDim = dim3(pair_threads<EPI>());
   cfg.dynamicSmemBytes = P_DYN_SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

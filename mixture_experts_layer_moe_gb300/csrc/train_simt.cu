@@ -31,30 +31,41 @@ template <int TILE>
 struct Geo {
   static constexpr int TX = TILE / 4, GROUPS = T_THREADS / (TX * TX);
   static constexpr int TK = TILE == 64 ? 16 : 64, LD = TILE + 4;
-  static constexpr int LOADS = TILE * TK / T_THREADS;
+  static constexpr int LOADS = TILE * TK / 4 / T_THREADS;   // vectors of 4 per thread
   using Buf = float[TK][LD];
 };
 
-// This thread's part of a TK x TILE operand tile: element (kk, i) is
-// src[i * ld + kk] (K_FAST) or src[kk * ld + i]; zero outside i < ni, kk < nk.
-template <typename T, bool K_FAST, int TILE>
+// This thread's part of a TK x TILE operand tile, as vectors of 4: element
+// (kk, i) is src[i * ld + kk] (K_FAST) or src[kk * ld + i]; zero outside i < ni,
+// kk < nk.  The contiguous bound and ld are multiples of 4, and src is 16-byte
+// aligned.
+template <bool K_FAST, int TILE>
 struct Part {
   using G = Geo<TILE>;
-  float v[G::LOADS];
-  static __device__ __forceinline__ int kk(int l) { return K_FAST ? l % G::TK : l / TILE; }
-  static __device__ __forceinline__ int ii(int l) { return K_FAST ? l / G::TK : l % TILE; }
-  __device__ __forceinline__ void load(const T *src, int64_t ld, int ni, int nk) {
+  float4 v[G::LOADS];
+  static __device__ __forceinline__ int kk(int l) { return K_FAST ? l % (G::TK / 4) * 4 : l / (TILE / 4); }
+  static __device__ __forceinline__ int ii(int l) { return K_FAST ? l / (G::TK / 4) : l % (TILE / 4) * 4; }
+  __device__ __forceinline__ void load(const float *src, int64_t ld, int ni, int nk) {
 #pragma unroll
     for (int c = 0; c < G::LOADS; ++c) {
       const int l = threadIdx.x + c * T_THREADS, k = kk(l), i = ii(l);
-      v[c] = i < ni && k < nk ? Elem<T>::load(src + (K_FAST ? i * ld + k : k * ld + i)) : 0.f;
+      v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < ni && k < nk)
+        v[c] = *reinterpret_cast<const float4 *>(src + (K_FAST ? i * ld + k : k * ld + i));
     }
   }
   __device__ __forceinline__ void store(typename G::Buf &dst) const {
 #pragma unroll
     for (int c = 0; c < G::LOADS; ++c) {
-      const int l = threadIdx.x + c * T_THREADS;
-      dst[kk(l)][ii(l)] = v[c];
+      const int l = threadIdx.x + c * T_THREADS, k = kk(l), i = ii(l);
+      if (K_FAST) {
+        dst[k][i] = v[c].x;
+        dst[k + 1][i] = v[c].y;
+        dst[k + 2][i] = v[c].z;
+        dst[k + 3][i] = v[c].w;
+      } else {
+        *reinterpret_cast<float4 *>(&dst[k][i]) = v[c];
+      }
     }
   }
 };
@@ -119,6 +130,14 @@ struct Place {
   }
 };
 
+__device__ __forceinline__ void get4(const void *p, int64_t at, float (&v)[4]) {
+  const float4 t = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+  v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+}
+__device__ __forceinline__ void put4(void *p, int64_t at, const float (&v)[4]) {
+  *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
 // Expert and row range of this CTA's tile; false when there is none.
 template <int TM>
 __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int rows, int tile, int &e,
@@ -148,7 +167,7 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int row
   return false;
 }
 
-template <typename T, int EPI, bool B_ROWS, int TILE>
+template <int EPI, bool B_ROWS, int TILE>
 __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int *status) {
   using G = Geo<TILE>;
   constexpr bool DUAL = EPI == kRowsSwiglu;
@@ -170,16 +189,18 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   // the steps of the one or two operand pairs, one after the other
   const int steps1 = (K + G::TK - 1) / G::TK;
   const int steps = steps1 * (EPI == kRowsPlain && p.A2 ? 2 : 1);
-  Part<T, true, TILE> pa, pb2;
-  Part<T, !B_ROWS, TILE> pb;
+  Part<true, TILE> pa, pb2;
+  Part<!B_ROWS, TILE> pb;
+  // (a row's padding, lda > K, holds zeros and may be read)
+  const int ka = p.lda ? p.lda : K;
   auto load = [&](int step) {
     const bool second = step >= steps1;
     const int k0 = (second ? step - steps1 : step) * G::TK;
-    const T *A = static_cast<const T *>(second ? p.A2 : p.A) + row0 * lda;
-    const T *B = static_cast<const T *>(second ? p.B2 : p.B) + base;
-    pa.load(A + k0, lda, end - row0, K - k0);
+    const float *A = static_cast<const float *>(second ? p.A2 : p.A) + row0 * lda;
+    const float *B = static_cast<const float *>(second ? p.B2 : p.B) + base;
+    pa.load(A + k0, lda, end - row0, ka - k0);
     pb.load(B_ROWS ? B + (int64_t)k0 * N : B + k0, B_ROWS ? N : K, N - n0, K - k0);
-    if constexpr (DUAL) pb2.load(static_cast<const T *>(p.B2) + base + k0, K, N - n0, K - k0);
+    if constexpr (DUAL) pb2.load(static_cast<const float *>(p.B2) + base + k0, K, N - n0, K - k0);
   };
   load(0);
   for (int step = 0; step < steps; ++step) {
@@ -198,37 +219,44 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   pdl_launch_dependents();
   join_groups<TILE>(acc, &pool[0][0][0], me.tx, me.ty, me.g);
   if constexpr (DUAL) join_groups<TILE>(acc2, &pool[0][0][0], me.tx, me.ty, me.g);
+  const int c = n0 + me.col;   // (N is a multiple of 4)
+  if (c >= N) return;
 #pragma unroll
   for (int i = 0; i < Place<TILE>::ROWS; ++i) {
     const int r = row0 + me.row + i;
     if (r >= end) continue;
+    const int64_t at = (int64_t)r * N + c;
+    float(&v)[4] = acc[i];
+    if constexpr (EPI == kRowsRelu) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + me.col + j;
-      if (c >= N) continue;
-      const int64_t at = (int64_t)r * N + c;
-      float v = acc[i][j];
-      if constexpr (EPI == kRowsRelu) v = v < 0.f ? 0.f : v;
-      if constexpr (EPI == kRowsSwiglu) {
-        static_cast<T *>(p.out_g)[at] = Elem<T>::from_f(v);
-        static_cast<T *>(p.out_u)[at] = Elem<T>::from_f(acc2[i][j]);
-        v = v / (1.f + expf(-v)) * acc2[i][j];
+      for (int j = 0; j < 4; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
+    } else if constexpr (EPI == kRowsSwiglu) {
+      put4(p.out_g, at, v);
+      put4(p.out_u, at, acc2[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = v[j] / (1.f + expf(-v[j])) * acc2[i][j];
+    } else if constexpr (EPI == kRowsReluGrad) {
+      float h[4];
+      get4(p.h, at, h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = h[j] > 0.f ? v[j] : 0.f;
+    } else if constexpr (EPI == kRowsSwigluGrad) {
+      float g[4], u[4], du[4];
+      get4(p.g, at, g);
+      get4(p.u, at, u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float s = 1.f / (1.f + expf(-g[j]));
+        du[j] = v[j] * g[j] * s;
+        v[j] = v[j] * u[j] * s * (1.f + g[j] * (1.f - s));
       }
-      if constexpr (EPI == kRowsReluGrad)
-        v = Elem<T>::load(static_cast<const T *>(p.h) + at) > 0.f ? v : 0.f;
-      if constexpr (EPI == kRowsSwigluGrad) {
-        const float g = Elem<T>::load(static_cast<const T *>(p.g) + at);
-        const float u = Elem<T>::load(static_cast<const T *>(p.u) + at);
-        const float s = 1.f / (1.f + expf(-g));
-        static_cast<T *>(p.out_u)[at] = Elem<T>::from_f(v * g * s);
-        v = v * u * s * (1.f + g * (1.f - s));
-      }
-      static_cast<T *>(p.out)[at] = Elem<T>::from_f(v);
+      put4(p.out_u, at, du);
     }
+    put4(p.out, at, v);
   }
 }
 
-template <typename T, int TILE>
+template <int TILE>
 __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int *status) {
   using G = Geo<TILE>;
   __shared__ __align__(16) typename G::Buf as[2], bs[2];
@@ -245,10 +273,10 @@ __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int
   const int64_t lda = p.lda ? p.lda : M;
   const Place<TILE> me;
   float acc[4][4] = {};
-  const T *A = static_cast<const T *>(p.A) + m0, *B = static_cast<const T *>(p.B) + n0;
-  Part<T, false, TILE> pa, pb;
+  const float *A = static_cast<const float *>(p.A) + m0, *B = static_cast<const float *>(p.B) + n0;
+  Part<false, TILE> pa, pb;
   auto load = [&](int q) {
-    pa.load(A + q * lda, lda, M - m0, end - q);
+    pa.load(A + q * lda, lda, (int)lda - m0, end - q);
     pb.load(B + (int64_t)q * N, N, N - n0, end - q);
   };
   if (beg < end) load(beg);
@@ -259,39 +287,35 @@ __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int
     if (q + G::TK < end) load(q + G::TK);
     tile_fma<TILE>(acc, as[buf], bs[buf], me.tx, me.ty, me.g);
   }
-  T *out = static_cast<T *>(p.out) + (int64_t)e * M * N;
   pdl_launch_dependents();
   join_groups<TILE>(acc, &as[0][0][0], me.tx, me.ty, me.g);
+  const int c = n0 + me.col;   // (N is a multiple of 4)
+  if (c >= N) return;
 #pragma unroll
   for (int i = 0; i < Place<TILE>::ROWS; ++i) {
     const int m = m0 + me.row + i;
-    if (m >= M) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + me.col + j;
-      if (c < N) out[(int64_t)m * N + c] = Elem<T>::from_f(acc[i][j]);
-    }
+    if (m < M) put4(p.out, ((int64_t)e * M + m) * N + c, acc[i]);
   }
 }
 
-template <typename T, int TILE>
+template <int TILE>
 cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   const int mt = (p.rows + TILE - 1) / TILE + (p.offsets ? p.num_experts : 0);
   const dim3 grid(mt, (p.N + TILE - 1) / TILE);
   cudaError_t e;
   if (p.epi == kRowsPlain && p.b_rows)
-    e = launch_pdl(rows_simt_kernel<T, kRowsPlain, true, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
+    e = launch_pdl(rows_simt_kernel<kRowsPlain, true, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
   else if (p.epi == kRowsPlain)
-    e = launch_pdl(rows_simt_kernel<T, kRowsPlain, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
+    e = launch_pdl(rows_simt_kernel<kRowsPlain, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
   else if (p.epi == kRowsRelu)
-    e = launch_pdl(rows_simt_kernel<T, kRowsRelu, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
+    e = launch_pdl(rows_simt_kernel<kRowsRelu, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
   else if (p.epi == kRowsSwiglu)
-    e = launch_pdl(rows_simt_kernel<T, kRowsSwiglu, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
+    e = launch_pdl(rows_simt_kernel<kRowsSwiglu, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
   else if (p.epi == kRowsReluGrad)
-    e = launch_pdl(rows_simt_kernel<T, kRowsReluGrad, true, TILE>, grid, dim3(T_THREADS), 0, s, p,
+    e = launch_pdl(rows_simt_kernel<kRowsReluGrad, true, TILE>, grid, dim3(T_THREADS), 0, s, p,
                    status);
   else
-    e = launch_pdl(rows_simt_kernel<T, kRowsSwigluGrad, true, TILE>, grid, dim3(T_THREADS), 0, s, p,
+    e = launch_pdl(rows_simt_kernel<kRowsSwigluGrad, true, TILE>, grid, dim3(T_THREADS), 0, s, p,
                    status);
   return e;
 }
@@ -305,8 +329,8 @@ bool large_tiles(int64_t tiles) { return tiles >= num_sms(); }
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s) {
   if (p.dtype != MOE_F32) return cudaErrorInvalidValue;
   return large_tiles((int64_t)((p.rows + 63) / 64) * ((p.N + 63) / 64))
-             ? launch_rows<float, 64>(p, status, s)
-             : launch_rows<float, 32>(p, status, s);
+             ? launch_rows<64>(p, status, s)
+             : launch_rows<32>(p, status, s);
 }
 
 cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s) {
@@ -315,7 +339,7 @@ cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s) 
   const bool large = large_tiles((int64_t)((p.N + 63) / 64) * ((p.M + 63) / 64) * E);
   const int tile = large ? 64 : 32;
   const dim3 grid((p.N + tile - 1) / tile, (p.M + tile - 1) / tile, E);
-  return launch_pdl(large ? grad_simt_kernel<float, 64> : grad_simt_kernel<float, 32>, grid,
+  return launch_pdl(large ? grad_simt_kernel<64> : grad_simt_kernel<32>, grid,
                     dim3(T_THREADS), 0, s, p, status);
 }
 
