@@ -1,0 +1,28 @@
+// Two fp32 values per instruction, each half rounded as on its own.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace moe {
+
+__device__ __forceinline__ unsigned long long bits2(float2 a) {
+  return reinterpret_cast<unsigned long long &>(a);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+}  // namespace moe

@@ -11,11 +11,14 @@
 // (cp.async; no other thread reads its part, so no barrier guards the ring):
 // with one row ahead in registers the gradient's one CTA per SM waited for
 // memory (285 us at 16384 x 7168 bf16 against TODO_BWD).
+// The sums use two fp32 values per instruction: the norms are bound by
+// instruction issue before they are by HBM.
 // In the gradient a thread owns the same columns of every row it meets, so the
 // column sums grow in its registers; each CTA writes one partial row and a
 // second launch adds the partials in order (no atomics: the result does not
 // depend on timing).  All statistics and sums are fp32.
 #include "common.cuh"
+#include "fp32x2.cuh"
 #include "launch.h"
 #include "train.h"
 #include "vec16.cuh"
@@ -28,29 +31,6 @@ constexpr int N_FWD_THREADS = 512, N_BWD_THREADS = 512;
 constexpr int N_FWD_STAGES = 3;
 // rows in a thread's ring: 512 threads hold 192 KB of them
 constexpr int bwd_stages(int vpt) { return vpt == 2 ? 6 : 3; }
-
-// ------------------------------------------------------------ pairs of fp32
-// Two fp32 values per instruction (each half rounded as on its own): the
-// norms are bound by instruction issue before they are by HBM.
-__device__ __forceinline__ unsigned long long bits2(float2 a) {
-  return reinterpret_cast<unsigned long long &>(a);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return reinterpret_cast<float2 &>(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return reinterpret_cast<float2 &>(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-  return reinterpret_cast<float2 &>(r);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // How a thread's share of a row is cut: chunks of 16 bytes, or (rows that are
 // not whole vectors) two elements tpr apart.  H pairs per chunk.

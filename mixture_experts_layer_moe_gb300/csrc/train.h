@@ -72,11 +72,10 @@ struct GradProduct {
   const void *A, *B;
   void *out;                // [E][M][N]
 };
-// (fp32)
-cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s);
-// Up to kMaxGradProblems of them over the same segments in one launch, on
-// tensor cores (bf16; SM pairs).
 constexpr int kMaxGradProblems = 3;
+// Up to kMaxGradProblems of them over the same segments in one launch (fp32).
+cudaError_t launch_grad_simt(const GradProduct *p, int count, int *status, cudaStream_t s);
+// The same on tensor cores (bf16; SM pairs).
 bool gemm_grad_supported(const GradProduct &p);
 // Runs that the segments' rows are cut into where the problems are too few to
 // fill the SMs (1: not cut), and the scratch that the partial sums take.  Both

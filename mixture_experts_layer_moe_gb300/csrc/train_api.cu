@@ -121,20 +121,17 @@ cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   return gemm_t2_supported(g) ? launch_gemm_t2(g, status, s) : cudaErrorNotSupported;
 }
 
-// Problems over the same segments: one launch on the tensor cores, else one
-// launch each.  splits, parts: as grad_splits and grad_scratch of all the
-// layer's problems say, whichever of them are wanted (so that a gradient has
-// the same bits alone and with the others).
+// Weight gradients over the same segments, in one launch.  splits, parts: as
+// grad_splits and grad_scratch of all the layer's problems say, whichever of
+// them are wanted (so that a gradient has the same bits alone and with the
+// others).
 cudaError_t launch_grads(const GradProduct *p, int count, int splits, float *parts, int *status,
                          cudaStream_t s) {
-  bool tc = true;
-  for (int i = 0; i < count; ++i) tc = tc && gemm_grad_supported(p[i]);
-  if (tc) return count ? launch_gemm_grad(p, count, splits, parts, status, s) : cudaSuccess;
-  for (int i = 0; i < count; ++i) {
-    const cudaError_t e = launch_grad_simt(p[i], status, s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  if (count == 0) return cudaSuccess;
+  if (p[0].dtype == MOE_F32) return launch_grad_simt(p, count, status, s);
+  for (int i = 0; i < count; ++i)
+    if (!gemm_grad_supported(p[i])) return cudaErrorNotSupported;
+  return launch_gemm_grad(p, count, splits, parts, status, s);
 }
 
 moe_status check_norm(const moe_norm_config *c) {

@@ -15,6 +15,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "fp32x2.cuh"
 #include "launch.h"
 #include "train.h"
 
@@ -71,17 +72,18 @@ struct Part {
 };
 
 template <int TILE>
-__device__ __forceinline__ void tile_fma(float (&acc)[4][4], const typename Geo<TILE>::Buf &as,
+__device__ __forceinline__ void tile_fma(float2 (&acc)[4][2], const typename Geo<TILE>::Buf &as,
                                          const typename Geo<TILE>::Buf &bs, int tx, int ty, int g) {
 #pragma unroll
   for (int kk = 0; kk < Geo<TILE>::TK; kk += Geo<TILE>::GROUPS) {
     const float4 a4 = *reinterpret_cast<const float4 *>(&as[kk + g][ty * 4]);
     const float4 b4 = *reinterpret_cast<const float4 *>(&bs[kk + g][tx * 4]);
-    const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+    const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+    const float2 b[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      for (int j = 0; j < 2; ++j) acc[i][j] = fma2(both(a[i]), b[j], acc[i][j]);
   }
 }
 
@@ -89,14 +91,14 @@ __device__ __forceinline__ void tile_fma(float (&acc)[4][4], const typename Geo<
 // floats of shared memory that nothing else uses any more), so that each
 // thread ends with four neighbouring outputs of one row: acc[0].
 template <int TILE>
-__device__ __forceinline__ void join_groups(float (&acc)[4][4], float *scratch, int tx, int ty,
+__device__ __forceinline__ void join_groups(float2 (&acc)[4][2], float *scratch, int tx, int ty,
                                             int g) {
   if constexpr (Geo<TILE>::GROUPS > 1) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float4 *>(scratch + (g * TILE + ty * 4 + i) * TILE + tx * 4) =
-          make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+          make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
     __syncthreads();
     float4 sum = *reinterpret_cast<const float4 *>(scratch + threadIdx.x * 4);
 #pragma unroll
@@ -107,10 +109,8 @@ __device__ __forceinline__ void join_groups(float (&acc)[4][4], float *scratch, 
       sum.z += v.z;
       sum.w += v.w;
     }
-    acc[0][0] = sum.x;
-    acc[0][1] = sum.y;
-    acc[0][2] = sum.z;
-    acc[0][3] = sum.w;
+    acc[0][0] = make_float2(sum.x, sum.y);
+    acc[0][1] = make_float2(sum.z, sum.w);
   }
 }
 
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   const int64_t lda = p.lda ? p.lda : K;
   const Place<TILE> me;
   const int64_t base = (int64_t)e * N * K + (B_ROWS ? (int64_t)n0 : (int64_t)n0 * K);
-  float acc[4][4] = {}, acc2[4][4] = {};
+  float2 acc[4][2] = {}, acc2[4][2] = {};
   // the steps of the one or two operand pairs, one after the other
   const int steps1 = (K + G::TK - 1) / G::TK;
   const int steps = steps1 * (EPI == kRowsPlain && p.A2 ? 2 : 1);
@@ -226,15 +226,16 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
     const int r = row0 + me.row + i;
     if (r >= end) continue;
     const int64_t at = (int64_t)r * N + c;
-    float(&v)[4] = acc[i];
+    float v[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
     if constexpr (EPI == kRowsRelu) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
     } else if constexpr (EPI == kRowsSwiglu) {
+      const float u[4] = {acc2[i][0].x, acc2[i][0].y, acc2[i][1].x, acc2[i][1].y};
       put4(p.out_g, at, v);
-      put4(p.out_u, at, acc2[i]);
+      put4(p.out_u, at, u);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = v[j] / (1.f + expf(-v[j])) * acc2[i][j];
+      for (int j = 0; j < 4; ++j) v[j] = v[j] / (1.f + expf(-v[j])) * u[j];
     } else if constexpr (EPI == kRowsReluGrad) {
       float h[4];
       get4(p.h, at, h);
@@ -256,15 +257,27 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   }
 }
 
+// Problems over the same segments share a launch: CTA blockIdx.x takes a tile
+// of an expert's gradients, blockIdx.y the expert.
+struct GradSet {
+  GradProduct p[kMaxGradProblems];
+  int first[kMaxGradProblems + 1];   // an expert's tiles before problem i
+};
 template <int TILE>
-__global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int *status) {
+__global__ void __launch_bounds__(T_THREADS)
+grad_simt_kernel(const __grid_constant__ GradSet set, int *status) {
   using G = Geo<TILE>;
   __shared__ __align__(16) typename G::Buf as[2], bs[2];
   static_assert(sizeof(as) >= sizeof(float) * G::GROUPS * TILE * TILE || G::GROUPS == 1,
                 "join_groups' scratch");
   pdl_wait();
   if (status_failed(status)) return;
-  const int e = blockIdx.z, m0 = blockIdx.y * TILE, n0 = blockIdx.x * TILE, M = p.M, N = p.N;
+  int which = 0;
+  while ((int)blockIdx.x >= set.first[which + 1]) ++which;
+  const GradProduct &p = set.p[which];
+  const int M = p.M, N = p.N, e = blockIdx.y;
+  const int tile = blockIdx.x - set.first[which], across = (N + TILE - 1) / TILE;
+  const int m0 = tile / across * TILE, n0 = tile % across * TILE;
   const int beg = p.offsets ? p.offsets[e] : 0, end = p.offsets ? p.offsets[e + 1] : p.rows;
   if (beg < 0 || end < beg || end > p.rows) {
     if (threadIdx.x == 0) set_status(status, MOE_ERR_BAD_INDEX, e);
@@ -272,7 +285,7 @@ __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int
   }
   const int64_t lda = p.lda ? p.lda : M;
   const Place<TILE> me;
-  float acc[4][4] = {};
+  float2 acc[4][2] = {};
   const float *A = static_cast<const float *>(p.A) + m0, *B = static_cast<const float *>(p.B) + n0;
   Part<false, TILE> pa, pb;
   auto load = [&](int q) {
@@ -294,7 +307,8 @@ __global__ void __launch_bounds__(T_THREADS) grad_simt_kernel(GradProduct p, int
 #pragma unroll
   for (int i = 0; i < Place<TILE>::ROWS; ++i) {
     const int m = m0 + me.row + i;
-    if (m < M) put4(p.out, ((int64_t)e * M + m) * N + c, acc[i]);
+    const float v[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
+    if (m < M) put4(p.out, ((int64_t)e * M + m) * N + c, v);
   }
 }
 
@@ -333,14 +347,21 @@ cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s) 
              : launch_rows<32>(p, status, s);
 }
 
-cudaError_t launch_grad_simt(const GradProduct &p, int *status, cudaStream_t s) {
-  if (p.dtype != MOE_F32) return cudaErrorInvalidValue;
-  const int E = p.offsets ? p.num_experts : 1;
-  const bool large = large_tiles((int64_t)((p.N + 63) / 64) * ((p.M + 63) / 64) * E);
-  const int tile = large ? 64 : 32;
-  const dim3 grid((p.N + tile - 1) / tile, (p.M + tile - 1) / tile, E);
-  return launch_pdl(large ? grad_simt_kernel<64> : grad_simt_kernel<32>, grid,
-                    dim3(T_THREADS), 0, s, p, status);
+cudaError_t launch_grad_simt(const GradProduct *p, int count, int *status, cudaStream_t s) {
+  const int E = p[0].offsets ? p[0].num_experts : 1;
+  GradSet set{};
+  auto lay = [&](int tile) {
+    for (int i = 0; i < kMaxGradProblems; ++i) {
+      const int tiles = i < count ? ((p[i].N + tile - 1) / tile) * ((p[i].M + tile - 1) / tile) : 0;
+      if (i < count) set.p[i] = p[i];
+      set.first[i + 1] = set.first[i] + tiles;
+    }
+    return set.first[count];
+  };
+  const bool large = large_tiles((int64_t)lay(64) * E);
+  const dim3 grid(lay(large ? 64 : 32), E);
+  return launch_pdl(large ? grad_simt_kernel<64> : grad_simt_kernel<32>, grid, dim3(T_THREADS), 0,
+                    s, set, status);
 }
 
 }  // namespace moe
