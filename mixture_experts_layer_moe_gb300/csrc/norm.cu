@@ -29,6 +29,7 @@ namespace {
 constexpr int N_MAX_PARTS = 152;   // partial rows of the column sums: one CTA per SM
 constexpr int N_FWD_THREADS = 512, N_BWD_THREADS = 512;
 constexpr int N_FWD_STAGES = 3;
+constexpr int N_SMEM = 208 * 1024;   // dynamic shared memory of a CTA at most
 // rows in a thread's ring: 512 threads hold 192 KB of them
 constexpr int bwd_stages(int vpt) { return vpt == 2 ? 6 : 3; }
 
@@ -77,6 +78,34 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Rows that are not whole vectors arrive as the aligned 16-byte pieces that
+// cover them, in a slot of their group's own: copies a row of d elements into
+// slot, whose first element then lies (address of src) % 16 bytes into it.
+// `end`: past the last element of the tensor; a piece that reaches over it is
+// copied element by element.  The group's threads read one another's pieces.
+__host__ __device__ constexpr int slot_bytes(int d, int elem) { return (d * elem + 15) / 16 * 16 + 16; }
+template <typename T>
+__device__ __forceinline__ int head_of(const T *src) {
+  return (int)(reinterpret_cast<uintptr_t>(src) & 15);
+}
+template <typename T>
+__device__ __forceinline__ void copy_row(uint8_t *slot, const T *src, int d, const T *end, int tid,
+                                         int tpr) {
+  const int head = head_of(src);
+  const uint8_t *base = reinterpret_cast<const uint8_t *>(src) - head;
+  const int pieces = (head + d * (int)sizeof(T) + 15) >> 4;
+  for (int v = tid; v < pieces; v += tpr) {
+    const uint8_t *p = base + v * 16;
+    if (p + 16 <= reinterpret_cast<const uint8_t *>(end)) {
+      copy16_async(reinterpret_cast<uint4 *>(slot + v * 16), p);
+    } else {
+      const T *from = reinterpret_cast<const T *>(p);
+      T *to = reinterpret_cast<T *>(slot + v * 16);
+      for (int i = 0; from + i < end; ++i) to[i] = from[i];
+    }
+  }
+}
+
 // Sum over the group of `warps` warps this warp belongs to (its warps are
 // neighbours; every thread of the CTA takes part): a butterfly, then one over
 // the warps' sums, which pass through one of two alternating buffers (a buffer
@@ -119,13 +148,20 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, float2 (*buf)[32]
   return upper ? make_float2(other, v) : make_float2(v, other);
 }
 
+template <bool WARP>
+__device__ __forceinline__ void group_barrier() {
+  if (WARP) __syncwarp();
+  else __syncthreads();
+}
+
 // Rows of a CTA: `groups` groups of tpr threads take neighbouring rows.
 template <typename T, int VEC, int VPT, bool WARP>
-__global__ void __launch_bounds__(N_FWD_THREADS)
+__global__ void __launch_bounds__(N_FWD_THREADS, VEC == 1 ? 2 : 1)
 norm_kernel(moe_norm_config c, const T *__restrict__ x, const T *__restrict__ gamma,
             const T *__restrict__ beta, T *__restrict__ y, float *__restrict__ mean_out,
             float *__restrict__ rstd_out, int tpr, int groups) {
-  extern __shared__ __align__(16) uint4 ring[];   // [stage][chunk][thread]
+  // [stage][chunk][thread], or [stage][group] slots of whole rows
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float buf[2][32];
   using C = Chunk<T, VEC>;
   constexpr bool RING = VEC > 1;
@@ -138,32 +174,46 @@ norm_kernel(moe_norm_config c, const T *__restrict__ x, const T *__restrict__ ga
   const int64_t step = (int64_t)gridDim.x * groups;
   const int64_t first = (int64_t)blockIdx.x * groups;
   auto col_of = [&](int i) { return VEC > 1 ? (tid + i * tpr) * VEC : tid + 2 * i * tpr; };
+  const int slot = slot_bytes(d, sizeof(T));
+  const T *x_end = x + (c.rows - 1) * c.ldx + d;
+  auto slot_of = [&](int st) {
+    return reinterpret_cast<uint8_t *>(ring) + (st * groups + group) * slot;
+  };
   auto fill = [&](int64_t r, int st) {
     if (r < c.rows) {
       const T *row = x + r * c.ldx;
+      if constexpr (RING) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (col_of(i) < d) copy16_async(&ring[(st * NC + i) * nthr + threadIdx.x], row + col_of(i));
+        for (int i = 0; i < NC; ++i)
+          if (col_of(i) < d)
+            copy16_async(&ring[(st * NC + i) * nthr + threadIdx.x], row + col_of(i));
+      } else {
+        copy_row(slot_of(st), row, d, x_end, tid, tpr);
+      }
     }
     copy_commit();
   };
-  if (RING) {
-    for (int st = 0; st < N_FWD_STAGES - 1; ++st) fill(first + group + st * step, st);
-  }
+  for (int st = 0; st < N_FWD_STAGES - 1; ++st) fill(first + group + st * step, st);
   for (int64_t r0 = first; r0 < c.rows; r0 += step) {
     const int64_t r = r0 + group;
     const bool live = r < c.rows;
     float2 v[NC][H], sum = both(0.f), sq = both(0.f);
-    if (RING) {
-      // (the stage being filled was read in the iteration before, by this thread)
-      fill(r + (N_FWD_STAGES - 1) * step, stage == 0 ? N_FWD_STAGES - 1 : stage - 1);
-      copy_wait<N_FWD_STAGES - 1>();
+    // the stage being filled was read in the iteration before: by this thread,
+    // or by the group's, which have all reached the barrier since
+    if (!RING) {
+      copy_wait<N_FWD_STAGES - 2>();
+      group_barrier<WARP>();
     }
+    fill(r + (N_FWD_STAGES - 1) * step, stage == 0 ? N_FWD_STAGES - 1 : stage - 1);
+    if (RING) copy_wait<N_FWD_STAGES - 1>();
+    const T *row = nullptr;
+    if (!RING && live)
+      row = reinterpret_cast<const T *>(slot_of(stage) + head_of(x + r * c.ldx));
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       if (live && col_of(i) < d) {
         if constexpr (RING) C::unpack(ring[(stage * NC + i) * nthr + threadIdx.x], v[i]);
-        else C::load(x + r * c.ldx, col_of(i), tpr, d, v[i]);
+        else C::load(row, col_of(i), tpr, d, v[i]);
 #pragma unroll
         for (int h = 0; h < H; ++h) sum = add2(sum, v[i][h]);
       } else {
@@ -171,7 +221,7 @@ norm_kernel(moe_norm_config c, const T *__restrict__ x, const T *__restrict__ ga
         for (int h = 0; h < H; ++h) v[i][h] = both(0.f);
       }
     }
-    if (RING) stage = stage + 1 == N_FWD_STAGES ? 0 : stage + 1;
+    stage = stage + 1 == N_FWD_STAGES ? 0 : stage + 1;
     const float mean = group_sum<WARP>(sum.x + sum.y, buf, turn, warps) * inv_d;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -217,7 +267,8 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
                      const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
                      const T *__restrict__ dy, T *__restrict__ dx, float *__restrict__ pg,
                      float *__restrict__ pb, int tpr, int groups) {
-  extern __shared__ __align__(16) uint4 ring[];   // [stage][chunk][x, dy][thread]
+  // [stage][chunk][x, dy][thread], or [stage][group][x, dy] slots of whole rows
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float2 buf[2][32];
   using C = Chunk<T, VEC>;
   constexpr bool RING = VEC > 1;
@@ -244,15 +295,25 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
   const T *rx = x + ahead * c.ldx, *ry = dy + ahead * c.lddy;
   T *out = dx + ahead * c.lddx;
   const int64_t sx = step * c.ldx, sy = step * c.lddy, so = step * c.lddx;
+  const int slot = slot_bytes(d, sizeof(T));
+  const T *x_end = x + (c.rows - 1) * c.ldx + d, *y_end = dy + (c.rows - 1) * c.lddy + d;
+  auto slot_of = [&](int st) {
+    return reinterpret_cast<uint8_t *>(ring) + (st * groups + group) * 2 * slot;
+  };
   auto fill = [&](int st) {
     if (ahead < c.rows) {
+      if constexpr (RING) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        if (col_of(i) < d) {
-          uint4 *at = &ring[(st * NC + i) * 2 * nthr + threadIdx.x];
-          copy16_async(at, rx + col_of(i));
-          copy16_async(at + nthr, ry + col_of(i));
+        for (int i = 0; i < NC; ++i) {
+          if (col_of(i) < d) {
+            uint4 *at = &ring[(st * NC + i) * 2 * nthr + threadIdx.x];
+            copy16_async(at, rx + col_of(i));
+            copy16_async(at + nthr, ry + col_of(i));
+          }
         }
+      } else {
+        copy_row(slot_of(st), rx, d, x_end, tid, tpr);
+        copy_row(slot_of(st) + slot, ry, d, y_end, tid, tpr);
       }
     }
     copy_commit();
@@ -260,9 +321,7 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
     rx += sx;
     ry += sy;
   };
-  if (RING) {
-    for (int st = 0; st < STAGES - 1; ++st) fill(st);
-  }
+  for (int st = 0; st < STAGES - 1; ++st) fill(st);
   float mean = 0.f, rstd = 0.f;
   if (first + group < c.rows) {
     mean = mean_in[first + group];
@@ -272,9 +331,16 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
     const int64_t r = r0 + group;
     const bool live = r < c.rows;
     float2 xh[NC][H], w[NC][H], s1 = both(0.f), s2 = both(0.f);
-    if (RING) {
-      fill(stage == 0 ? STAGES - 1 : stage - 1);
-      copy_wait<STAGES - 1>();
+    if (!RING) {
+      copy_wait<STAGES - 2>();
+      group_barrier<WARP>();
+    }
+    fill(stage == 0 ? STAGES - 1 : stage - 1);
+    if (RING) copy_wait<STAGES - 1>();
+    const T *row_x = nullptr, *row_y = nullptr;
+    if (!RING && live) {
+      row_x = reinterpret_cast<const T *>(slot_of(stage) + head_of(x + r * c.ldx));
+      row_y = reinterpret_cast<const T *>(slot_of(stage) + slot + head_of(dy + r * c.lddy));
     }
     float next_mean = 0.f, next_rstd = 0.f;
     if (r + step < c.rows) {
@@ -289,8 +355,8 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
           C::unpack(at[0], xh[i]);
           C::unpack(at[nthr], w[i]);
         } else {
-          C::load(x + r * c.ldx, col_of(i), tpr, d, xh[i]);
-          C::load(dy + r * c.lddy, col_of(i), tpr, d, w[i]);
+          C::load(row_x, col_of(i), tpr, d, xh[i]);
+          C::load(row_y, col_of(i), tpr, d, w[i]);
         }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -304,7 +370,7 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
         }
       }
     }
-    if (RING) stage = stage + 1 == STAGES ? 0 : stage + 1;
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
     const float2 s = group_sum2<WARP>(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
     const float2 m1 = both(-s.x * inv_d), m2 = both(-s.y * inv_d);
     if (live) {
@@ -322,7 +388,9 @@ norm_backward_kernel(moe_norm_config c, const T *__restrict__ x, const T *__rest
     mean = next_mean;
     rstd = next_rstd;
   }
-  // the groups of the CTA meet in shared memory (the ring's, now read)
+  // the groups of the CTA meet in shared memory (the ring's, now read; no copy
+  // is in flight: the ones issued past the last row were empty)
+  copy_wait<0>();
   float *cols = reinterpret_cast<float *>(ring);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -513,13 +581,13 @@ cudaError_t fwd(const moe_norm_config &c, const T *x, const T *gamma, const T *b
                 float *mean, float *rstd, int tpr, cudaStream_t s) {
   auto kernel = norm_kernel<T, VEC, VPT, WARP>;
   const int groups = tpr <= 256 ? 256 / tpr : 1, threads = tpr * groups;
-  const size_t smem = VEC > 1 ? (size_t)N_FWD_STAGES * VPT * threads * 16 : 0;
+  const size_t smem = VEC > 1 ? (size_t)N_FWD_STAGES * VPT * threads * 16
+                              : (size_t)N_FWD_STAGES * groups * slot_bytes(c.d, sizeof(T));
   static int resident[N_FWD_THREADS / 32 + 1] = {};   // CTAs per SM by warps per CTA
   int &ctas = resident[threads / 32];
   if (ctas == 0) {
-    cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        VEC > 1 ? N_FWD_STAGES * VPT * N_FWD_THREADS * 16 : 0);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         N_SMEM);
     if (e == cudaSuccess)
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, smem);
     if (e != cudaSuccess) return e;
@@ -561,13 +629,14 @@ cudaError_t bwd(const moe_norm_config &c, const BwdPlan &p, const T *x, const T 
   constexpr int VPT = bwd_vpt(VEC);
   auto kernel = norm_backward_kernel<T, VEC, VPT, WARP>;
   const int threads = p.tpr * p.groups;
-  const size_t ring = VEC > 1 ? (size_t)bwd_stages(VPT) * VPT * 2 * threads * 16 : 0;
+  const size_t ring = VEC > 1
+                          ? (size_t)bwd_stages(VPT) * VPT * 2 * threads * 16
+                          : (size_t)bwd_stages(VPT) * p.groups * 2 * slot_bytes(c.d, sizeof(T));
   const size_t cols = p.groups > 1 ? (size_t)threads * VPT * VEC * 4 : 0;
   static bool set = false;
   if (!set) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             6 * 4 * N_BWD_THREADS * 16);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, N_SMEM);
     if (e != cudaSuccess) return e;
     set = true;
   }
