@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "train.h"
+#include "vec16.cuh"
 
 namespace moe {
 namespace {
@@ -104,6 +105,114 @@ route_grad_kernel(const float *__restrict__ probs, const int32_t *__restrict__ t
   }
 }
 
+// The rows' gradient where dl has entries at the token's k choices alone (RENORM
+// without the loss):
+//   dx[t] = sum_j (dx_perm[q_j] + c_j Wg[e_j]),   c_j = g_j (dgate_j - sum g dgate),
+// in one pass: the k router rows of a token come from L2 (Wg is a few MB), so
+// the launch moves what the sum of the expert rows moves, and neither dl Wg nor
+// a rounding of it is kept.  CTA (t, c) takes vectors [c * 256 VB, ...) of
+// token t's row; four slots' rows are in flight per thread, and the sum runs in
+// slot order.  (blockDim.x: 256, or fewer for a row of fewer vectors.)
+constexpr int RR_SLOTS = 4;
+__device__ __forceinline__ uint4 load_now(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+template <typename T, int VB>
+__global__ void __launch_bounds__(256)
+route_rows_kernel(const uint4 *__restrict__ dx_perm, const int32_t *__restrict__ inv_perm,
+                  const int32_t *__restrict__ topk_idx, const float *__restrict__ gates,
+                  const float *__restrict__ dgate, const uint4 *__restrict__ Wg,
+                  uint4 *__restrict__ dx, int n, int E, int k, int vpr, int *status) {
+  constexpr int V = Vec16<T>::N;
+  __shared__ int s_q[kRouteRowsMaxK], s_e[kRouteRowsMaxK];
+  __shared__ float s_c[kRouteRowsMaxK];
+  pdl_launch_dependents();
+  pdl_wait();
+  if (status_failed(status)) return;
+  const int t = blockIdx.x, P = n * k;
+  if (threadIdx.x < 32) {
+    // (k <= 32: one slot per lane)
+    const int j = threadIdx.x;
+    int q = -1, e = -1;
+    float g = 0.f, dg = 0.f;
+    if (j < k) {
+      const int64_t pair = (int64_t)t * k + j;
+      e = topk_idx[pair];
+      if (e < 0 || e >= E) {
+        if (blockIdx.y == 0) set_status(status, MOE_ERR_BAD_INDEX, (int)pair);
+        e = -1;
+      } else {
+        g = gates[pair];
+        dg = dgate[pair];
+      }
+      if (dx_perm) {
+        q = inv_perm[pair];
+        if (q < 0 || q >= P) {
+          if (blockIdx.y == 0) set_status(status, MOE_ERR_BAD_INDEX, (int)pair);
+          q = -1;
+        }
+      }
+    }
+    const float sum = warp_sum_xor(g * dg);
+    if (j < kRouteRowsMaxK) {
+      s_q[j] = q;
+      s_e[j] = e;
+      s_c[j] = g * (dg - sum);
+    }
+  }
+  __syncthreads();
+  const int v0 = blockIdx.y * blockDim.x * VB + threadIdx.x;
+  float acc[VB][V];
+#pragma unroll
+  for (int b = 0; b < VB; ++b)
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[b][c] = 0.f;
+  // (a slot or a vector that is not there reads a valid one and drops it, so
+  // that all loads of a round are issued before the first is used)
+  int at[VB];
+#pragma unroll
+  for (int b = 0; b < VB; ++b) at[b] = min(v0 + b * (int)blockDim.x, vpr - 1);
+  const uint4 *rows = dx_perm ? dx_perm : Wg;
+  for (int j0 = 0; j0 < k; j0 += RR_SLOTS) {
+    uint4 r[RR_SLOTS][VB], w[RR_SLOTS][VB];
+    int q[RR_SLOTS], e[RR_SLOTS];
+#pragma unroll
+    for (int u = 0; u < RR_SLOTS; ++u) {
+      const int j = min(j0 + u, k - 1);
+      q[u] = s_q[j];
+      e[u] = s_e[j];
+#pragma unroll
+      for (int b = 0; b < VB; ++b) {
+        r[u][b] = load_now(rows + (int64_t)max(q[u], 0) * vpr + at[b]);
+        w[u][b] = load_now(Wg + (int64_t)max(e[u], 0) * vpr + at[b]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < RR_SLOTS; ++u) {
+      if (j0 + u >= k) break;
+      const float c = s_c[j0 + u];
+#pragma unroll
+      for (int b = 0; b < VB; ++b) {
+        float f[V], g[V];
+        unpack16<T>(r[u][b], f);
+        unpack16<T>(w[u][b], g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (q[u] >= 0) acc[b][i] += f[i];
+          if (e[u] >= 0) acc[b][i] = fmaf(c, g[i], acc[b][i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < VB; ++b)
+    if (v0 + b * (int)blockDim.x < vpr) dx[(int64_t)t * vpr + at[b]] = pack16<T>(acc[b]);
+}
+
 int grid_of(int n) {
   const int want = (n + RB_WARPS - 1) / RB_WARPS;
   return want < RB_MAX_CTAS ? want : RB_MAX_CTAS;
@@ -134,6 +243,33 @@ cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int
   if (e == cudaSuccess && dbias && grid > 1)
     e = launch_column_sum(scratch, nullptr, grid, E, dbias, nullptr, status, s);
   return e;
+}
+
+// Against the product dl Wg and the sum of the rows in launches of their own,
+// the whole gradient of a bf16 router took (us, one launch / two):
+//   n 16384, d 7168, 256 experts: k = 2 299 / 344, k = 4 380 / 389, k = 8 572 / 514
+//   n 2048, d 7168, k = 8 99 / 98;  n 1024, d 1024, k = 8 22 / 28;  n 1, k = 8 16 / 22
+// so long rows of many choices take the product: there the reads of Wg's rows
+// from L2 outweigh writing and reading dl Wg.  (fp32: 2048 tokens, d 1024, 256
+// experts, k = 8 59 / 93.)
+bool route_rows_supported(const moe_config &c, const float *f) {
+  if (c.gate != MOE_GATE_RENORM || f != nullptr || c.top_k > kRouteRowsMaxK) return false;
+  return c.act_dtype == MOE_F32 || c.top_k <= 4 || (int64_t)c.n * c.d <= 1 << 23;
+}
+
+cudaError_t launch_route_rows(const moe_config &c, const void *Wg, const int32_t *topk_idx,
+                              const float *gates, const float *dgate, const int32_t *inv_perm,
+                              const void *dx_perm, void *dx, int *status, cudaStream_t s) {
+  const int vpr = c.d / (c.act_dtype == MOE_F32 ? 4 : 8);
+  // two vectors per thread where that still leaves two CTAs per SM
+  const bool two = vpr > 256 && (int64_t)c.n * ((vpr + 511) / 512) >= 2 * 152;
+  const int threads = vpr < 256 ? (vpr + 31) / 32 * 32 : 256, per_cta = threads * (two ? 2 : 1);
+  const dim3 grid(c.n, (vpr + per_cta - 1) / per_cta);
+  auto with = c.act_dtype == MOE_F32
+                  ? (two ? route_rows_kernel<float, 2> : route_rows_kernel<float, 1>)
+                  : (two ? route_rows_kernel<__nv_bfloat16, 2> : route_rows_kernel<__nv_bfloat16, 1>);
+  return launch_pdl(with, grid, dim3(threads), 0, s, (const uint4 *)dx_perm, inv_perm, topk_idx, gates,
+                    dgate, (const uint4 *)Wg, (uint4 *)dx, c.n, c.n_experts, c.top_k, vpr, status);
 }
 
 }  // namespace moe

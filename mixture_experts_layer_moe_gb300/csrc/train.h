@@ -36,6 +36,14 @@ cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int
                               void *dl, int pitch, float *dbias, float *scratch, int *status,
                               cudaStream_t s);
 
+// dx from the expert rows' gradients and the router's in one pass, where dl has
+// entries at the chosen experts alone and these are few.
+constexpr int kRouteRowsMaxK = 16;
+bool route_rows_supported(const moe_config &c, const float *f);
+cudaError_t launch_route_rows(const moe_config &c, const void *Wg, const int32_t *topk_idx,
+                              const float *gates, const float *dgate, const int32_t *inv_perm,
+                              const void *dx_perm, void *dx, int *status, cudaStream_t s);
+
 // ------------------------------------------------------- grouped products
 enum {
   kRowsPlain = 0,       // out = A B (+ A2 B2)

@@ -360,7 +360,8 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
   int *status = at<int>(ws, L.status);
   cudaStream_t s = as_stream(stream);
   const int pitch = dl_pitch(c);
-  void *dl = dx || dWg ? at<void>(ws, L.dl) : nullptr;
+  const bool rows = dx && route_rows_supported(c, f);   // dx without dl
+  void *dl = (dx && !rows) || dWg ? at<void>(ws, L.dl) : nullptr;
   if (dl || dbias)
     MOE_TRY(cuda_status(launch_route_grad(c, probs, topk_idx, topk_gate, dgate, f, aux, dl, pitch,
                                           dbias, at<float>(ws, L.bias_parts), status, s)));
@@ -372,7 +373,10 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
     MOE_TRY(cuda_status(launch_grads(&gw, 1, grad_splits(&gw, 1), at<float>(ws, L.grad_parts),
                                      status, s)));
   }
-  if (dx) {
+  if (rows) {
+    MOE_TRY(cuda_status(launch_route_rows(c, w->Wg, topk_idx, topk_gate, dgate, inv_perm, dx_perm,
+                                          dx, status, s)));
+  } else if (dx) {
     RowsProduct r{};
     r.dtype = c.act_dtype;
     r.epi = kRowsPlain;

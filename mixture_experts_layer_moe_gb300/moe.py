@@ -165,8 +165,14 @@ def make_pool(slot_of: torch.Tensor, pool: dict) -> moe_expert_pool:
                            _ptr(g("W2q")), _ptr(g("S1")), _ptr(g("S3")), _ptr(g("S2")))
 
 
+# the current stream's handle without a Stream object (a microsecond of each call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
