@@ -1,4 +1,4 @@
-"""GB300 (sm_103a) Mixture-of-Experts layer forward pass.
+"""GB300 (sm_103a) Mixture-of-Experts layer: the forward pass and its training.
 
 The compute runs in the CUDA kernels of ``libmoe_gb300.so`` behind the C ABI
 declared in ``include/moe.h``; ``mixture_experts_layer_moe_gb300.moe`` is the
