@@ -60,6 +60,7 @@
 // tile list comes from the segment offsets on the device; empty segments give
 // no tiles.
 #include "common.cuh"
+#include "gate_math.cuh"
 #include "launch.h"
 #include "pair_common.cuh"
 #include "tc_common.cuh"
@@ -82,7 +83,7 @@ constexpr int P_STAGE = P_B_BYTES + P_A_BYTES;  // 32 KB (tokens first, then wei
 // experts of 512 rows, d = d_ff = 1024: up projection 155 -> 133 us with 8
 // warps, dg and du 183 -> 132 with 8 and 120 with 12).
 template <int EPI>
-constexpr int epi_warps() { return EPI >= 6 ? 12 : EPI == 5 ? 8 : 4; }
+constexpr int epi_warps() { return EPI == 6 || EPI == 7 ? 12 : EPI == 5 ? 8 : 4; }
 template <int EPI>
 constexpr int pair_threads() { return 32 * (2 + epi_warps<EPI>()); }
 constexpr uint32_t P_TMEM_COLS = 512;           // two accumulators of PN columns
@@ -121,10 +122,16 @@ struct PArgs {
   // training: what the forward keeps (EPI 5) and what a gradient reads and adds (EPI 6, 7), [rows][N]
   __nv_bfloat16 *out_g, *out_u;
   const uint16_t *g, *u, *h;
+  // EPI 8: fp32 partial sums parts[mat][split][rows][N] of `splits` ranges of
+  // the reduction, for one or two weight matrices
+  float *parts;
+  int splits, mats;
 };
 
 struct PTile {
   int e, tok0, ntok, seg_end, wb;
+  int mat, split;   // EPI 8
+  int kb0, kb1;     // k-blocks
 };
 
 // Tokens per block of a segment of c tokens: the segment splits into
@@ -170,19 +177,6 @@ __device__ __forceinline__ PTile p_decode(const PShared &sh, int E, int t, int n
   return tl;
 }
 
-__device__ __forceinline__ float silu_mul(float a, float b) {
-  return __fdividef(a, 1.f + __expf(-a)) * b;
-}
-
-__device__ __forceinline__ float bf16_value(uint16_t b) {
-  return __uint_as_float((uint32_t)b << 16);
-}
-
-__device__ __forceinline__ uint16_t bf16_bits(float v) {
-  const __nv_bfloat16 h = __float2bfloat16_rn(v);
-  return *reinterpret_cast<const uint16_t *>(&h);
-}
-
 // Kept rows of a gradient's epilogue: this thread's column of 16 tokens (h for
 // the ReLU, g and u for SwiGLU; 0 outside the segment).
 constexpr int KEPT = 16;
@@ -200,7 +194,8 @@ __device__ __forceinline__ void load_kept(const PArgs &args, int tok0, int end, 
 }
 
 // EPI: 0 plain, 1 relu, 2 swiglu (W = W1 rows, W3 = W3 rows), 5 swiglu that
-// also stores both products, 6 relu gradient, 7 swiglu gradient.
+// also stores both products, 6 relu gradient, 7 swiglu gradient, 8 fp32 partial
+// sums of a range of the reduction.
 // WROWS: the weights are stored with the output column contiguous ([E][K][N],
 // the forward's weights as their gradients read them): the MMA takes them as
 // an M-major operand, staged as two boxes of 64 columns x 64 reduction rows
@@ -223,14 +218,32 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int E = args.offsets ? args.num_experts : 1;
-  const int n_wb = (args.N + OUT_TILE - 1) / OUT_TILE;
+  // weight blocks of a matrix, and all that a token block meets (with EPI 8 a
+  // block is its matrix's, then split by ranges of the reduction)
+  const int n_wb1 = (args.N + OUT_TILE - 1) / OUT_TILE;
+  const int n_wb = EPI == 8 ? n_wb1 * args.mats * args.splits : n_wb1;
   const int KB1 = (args.K + PK - 1) / PK;             // k-blocks of one operand pair
   const int KB = WROWS ? KB1 * args.pairs : KB1;
+  const int KBS = EPI == 8 ? (KB + args.splits - 1) / args.splits : KB;   // of one range
+  auto decode = [&](int t) {
+    PTile tl = p_decode(sh, E, t, n_wb, args.tok_major != 0);
+    tl.mat = 0;
+    tl.split = 0;
+    if constexpr (EPI == 8) {
+      tl.split = tl.wb % args.splits;
+      tl.wb /= args.splits;
+      tl.mat = tl.wb / n_wb1;
+      tl.wb -= tl.mat * n_wb1;
+    }
+    tl.kb0 = tl.split * KBS;
+    tl.kb1 = min(KB, tl.kb0 + KBS);
+    return tl;
+  };
 
   if (threadIdx.x == 0) {
     tc::prefetch_tmap(&tmX);
     tc::prefetch_tmap(&tmW);
-    if (GATED || WROWS) tc::prefetch_tmap(&tmW3);
+    if (GATED || WROWS || EPI == 8) tc::prefetch_tmap(&tmW3);
     if (WROWS) tc::prefetch_tmap(&tmX2);
   }
   if (warp == 1) tmem_alloc2(&sh.tmem_base, P_TMEM_COLS);
@@ -299,7 +312,6 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   const uint32_t tmem_base = sh.tmem_base;
   const int num_tiles = sh.num_tiles;
   volatile int *abort = &sh.abort;
-  const bool tok_major = args.tok_major != 0;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -309,12 +321,12 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       uint32_t used = 0, used_phase = 0;   // bit s: stage s was used, in which phase last
       const uint32_t full0 = map_to_rank(tc::smem_u32(&sh.full[0]), 0);
       for (int t = pair; t < num_tiles && !*abort; t += n_pairs) {
-        const PTile tl = p_decode(sh, E, t, n_wb, tok_major);
+        const PTile tl = decode(t);
         const int ntok = tl.ntok;
         const int half = ((ntok + 15) & ~15) >> 1;   // tokens staged by each CTA
         const int brow = tl.tok0 + (int)rank * half;
         const int wrow = tl.wb * OUT_TILE + (int)rank * OUT_CTA;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
           if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) break;
           uint8_t *sb = smem + stage * P_STAGE;
           uint8_t *sa = sb + P_B_BYTES;
@@ -337,7 +349,7 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             tma2_load_3d(&tmW, bar, sa, kb * PK, wrow, tl.e);               // rows 0..63
             tma2_load_3d(&tmW3, bar, sa + P_A_BYTES / 2, kb * PK, wrow, tl.e);  // rows 64..127
           } else {
-            tma2_load_3d(&tmW, bar, sa, kb * PK, wrow, tl.e);
+            tma2_load_3d(EPI == 8 && tl.mat ? &tmW3 : &tmW, bar, sa, kb * PK, wrow, tl.e);
           }
           if (++stage == PS) { stage = 0; phase ^= 1u; }
         }
@@ -367,7 +379,7 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       const uint32_t a_lo = (uint32_t)a_desc, a_hi = (uint32_t)(a_desc >> 32);
       const uint32_t b_lo = (uint32_t)b_desc, b_hi = (uint32_t)(b_desc >> 32);
       for (int t = pair; t < num_tiles && ok && !*abort; t += n_pairs, ++local) {
-        const PTile tl = p_decode(sh, E, t, n_wb, tok_major);
+        const PTile tl = decode(t);
         const int ntok = tl.ntok;
         const uint32_t idesc =
             tc::idesc_bf16_f32(2 * PM, (ntok + 15) & ~15) | (WROWS ? tc::kIdescAMajorMN : 0u);
@@ -375,14 +387,14 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         if (!mbar_wait_cluster(&sh.tempty[acc], ((local >> 1) & 1) ^ 1u, abort)) { ok = false; break; }
         tc::tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PN);
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
           if (!tc::mbar_wait(&sh.full[stage], phase, abort)) { ok = false; break; }
           tc::tc_fence_after();
           const uint32_t at = (uint32_t)(stage * (P_STAGE / 16));
 #pragma unroll
           for (int k = 0; k < PK / 16; ++k)
             mma2_bf16_lo(d_tmem, a_lo + at + k * (WROWS ? 128 : 2), a_hi, b_lo + at + k * 2, b_hi,
-                         idesc, (kb != 0 || k != 0) ? 1u : 0u);
+                         idesc, (kb != tl.kb0 || k != 0) ? 1u : 0u);
           mma2_commit_both(&sh.empty[stage]);
           if (++stage == PS) { stage = 0; phase ^= 1u; }
         }
@@ -404,7 +416,7 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     float *xbuf = reinterpret_cast<float *>(smem + (size_t)PS * P_STAGE);
     int local = 0;
     for (int t = pair; t < num_tiles; t += n_pairs, ++local) {
-      const PTile tl = p_decode(sh, E, t, n_wb, tok_major);
+      const PTile tl = decode(t);
       const int ntok = tl.ntok;
       const int acc = local & 1;
       // this thread's output column
@@ -412,9 +424,11 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
           tl.wb * OUT_TILE + (int)rank * OUT_CTA + (GATED ? pq : quarter) * 32 + lane;
       const bool col_ok = col < args.N;
       uint16_t *o = reinterpret_cast<uint16_t *>(args.out) + col;
+      float *plane =
+          args.parts + (size_t)(tl.mat * args.splits + tl.split) * args.rows * args.N + col;   // EPI 8
       // a gradient's kept rows: the first chunk is in flight during the wait
       uint16_t kg[KEPT], ku[KEPT];
-      if constexpr (EPI >= 6)
+      if constexpr (EPI == 6 || EPI == 7)
         load_kept<EPI>(args, tl.tok0 + part * KEPT, tl.seg_end, col, col_ok, kg, ku);
       const bool ok = tc::mbar_wait(&sh.tfull[acc], (local >> 1) & 1, abort);
       if constexpr (GATED) {
@@ -426,7 +440,7 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       }
       tc::tc_fence_after();
       const uint32_t tb = lane_base + (uint32_t)(acc * PN);
-      if constexpr (EPI >= 6) {
+      if constexpr (EPI == 6 || EPI == 7) {
         // 16 tokens at a time: the next ones' kept rows are in flight while
         // these are formed and stored
 #pragma unroll 1
@@ -442,10 +456,10 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             if constexpr (EPI == 6) {
               dg[i] = bf16_value(kg[i]) > 0.f ? bf16_bits(v) : (uint16_t)0;
             } else {
-              const float g = bf16_value(kg[i]), u = bf16_value(ku[i]);
-              const float sg = __fdividef(1.f, 1.f + __expf(-g));
-              dg[i] = bf16_bits(v * u * sg * (1.f + g * (1.f - sg)));
-              du[i] = bf16_bits(v * g * sg);
+              float a_g, a_u;
+              swiglu_grad(v, bf16_value(kg[i]), bf16_value(ku[i]), a_g, a_u);
+              dg[i] = bf16_bits(a_g);
+              du[i] = bf16_bits(a_u);
             }
           }
           load_kept<EPI>(args, tok0 + KEPT * TURNS, tl.seg_end, col, col_ok, kg, ku);
@@ -515,7 +529,9 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 float v = __uint_as_float(a[i]);
                 if constexpr (EPI == 1) v = fmaxf(v, 0.f);
                 const int tok = tok0 + i;
-                if (tok < tl.seg_end) o[(size_t)tok * args.N] = bf16_bits(v);
+                if (tok >= tl.seg_end) continue;
+                if constexpr (EPI == 8) plane[(size_t)tok * args.N] = v;
+                else o[(size_t)tok * args.N] = bf16_bits(v);
               }
             }
           }
@@ -592,7 +608,7 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
   if (!bf16_map(&mW, g.B, 3, dW, bW)) return cudaErrorInvalidValue;
   mW3 = mW;
   mX2 = mX;
-  if (GATED || g.A2) {
+  if (g.B3) {
     if (!bf16_map(&mW3, g.B3, 3, dW, bW)) return cudaErrorInvalidValue;
   }
   if (g.A2 && !bf16_map(&mX2, g.A2, 2, dX, bX)) return cudaErrorInvalidValue;
@@ -610,6 +626,9 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
   a.g = static_cast<const uint16_t *>(g.kept_g);
   a.u = static_cast<const uint16_t *>(g.kept_u);
   a.h = static_cast<const uint16_t *>(g.kept_h);
+  a.parts = g.parts;
+  a.splits = g.splits;
+  a.mats = g.mats;
   // token blocks outer when an average segment holds more rows than the
   // weights it meets (the shared expert's one segment of all n tokens)
   const long seg_rows = (long)g.rows / (E > 0 ? E : 1);
@@ -638,8 +657,10 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
 }  // namespace
 
 bool gemm_t2_supported(const GemmStage &g) {
-  const bool epi_ok = g.w_rows ? g.epi == 0 || g.epi == kEpiReluGrad || g.epi == kEpiSwigluGrad
-                               : g.epi >= 0 && g.epi <= 2 || g.epi == kEpiSwigluKeep;
+  const bool epi_ok =
+      g.epi == kEpiPartial ||
+      (g.w_rows ? g.epi == 0 || g.epi == kEpiReluGrad || g.epi == kEpiSwigluGrad
+                : (g.epi >= 0 && g.epi <= 2) || g.epi == kEpiSwigluKeep);
   return g.rows > 0 && tensor_maps_available() && g.a_dtype == MOE_BF16 &&
          g.b_dtype == MOE_BF16 && g.out_dtype == MOE_BF16 && epi_ok && g.num_experts <= P_MAX_E &&
          (g.lda ? g.lda : g.K) % 8 == 0 && g.N % 8 == 0 && num_sms() >= 2;
@@ -650,6 +671,7 @@ cudaError_t launch_gemm_t2(const GemmStage &g, int *status, cudaStream_t s) {
     switch (g.epi) {
       case kEpiReluGrad: return launch_t2<kEpiReluGrad, true>(g, status, s);
       case kEpiSwigluGrad: return launch_t2<kEpiSwigluGrad, true>(g, status, s);
+      case kEpiPartial: return launch_t2<kEpiPartial, true>(g, status, s);
       default: return launch_t2<0, true>(g, status, s);
     }
   }
@@ -657,6 +679,7 @@ cudaError_t launch_gemm_t2(const GemmStage &g, int *status, cudaStream_t s) {
     case 1: return launch_t2<1, false>(g, status, s);
     case 2: return launch_t2<2, false>(g, status, s);
     case kEpiSwigluKeep: return launch_t2<kEpiSwigluKeep, false>(g, status, s);
+    case kEpiPartial: return launch_t2<kEpiPartial, false>(g, status, s);
     default: return launch_t2<0, false>(g, status, s);
   }
 }

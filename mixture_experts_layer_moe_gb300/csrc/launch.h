@@ -129,8 +129,12 @@ struct GemmStage {
   const void *A2;        // w_rows, epi 0: out = A B + A2 B3, or nullptr
   void *out_g, *out_u;   // kEpiSwigluKeep: both products; kEpiSwigluGrad: out_u is du (out: dg)
   const void *kept_g, *kept_u, *kept_h;   // what the gradients' epilogues read, [rows][N]
+  // kEpiPartial: parts[mat][split][rows][N] = the products with B (and B3, mats
+  // = 2) over each of `splits` ranges of the reduction, fp32
+  float *parts;
+  int splits, mats;
 };
-constexpr int kEpiSwigluKeep = 5, kEpiReluGrad = 6, kEpiSwigluGrad = 7;
+constexpr int kEpiSwigluKeep = 5, kEpiReluGrad = 6, kEpiSwigluGrad = 7, kEpiPartial = 8;
 cudaError_t launch_gemm_simt(const GemmStage &g, int *status, cudaStream_t s);
 
 // The same stage on tcgen05 tensor cores (fp32 accumulate in TMEM, TMA-fed):

@@ -69,6 +69,14 @@ struct RowsProduct {
 // (fp32)
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s);
 
+// The same with the reduction cut into ranges where its tiles are few (bf16):
+// how many (1: not cut; by the shape alone), the scratch that takes, and the
+// launches; `whole` is the product as the pair kernel takes it.
+int rows_splits(const RowsProduct &p);
+size_t rows_scratch(const RowsProduct &p);
+cudaError_t launch_rows_split(const RowsProduct &p, const struct GemmStage &whole, int splits,
+                              float *parts, int *status, cudaStream_t s);
+
 // Products over the rows of each segment (a weight's gradient):
 //   out_e[m][c] = sum_{q in segment e} A[q][m] B[q][c],   m < M, c < N;
 // zero for a segment without rows.

@@ -12,7 +12,7 @@ namespace {
 
 // The layer's workspace, then the scratch of the gradients.
 struct TrainLayout {
-  size_t status, dg, du, dl, dx_router, bias_parts, grad_parts, total;
+  size_t status, dg, du, dl, dx_router, bias_parts, parts, total;
 };
 
 // dl's rows are padded to whole 16-byte vectors of bf16.
@@ -41,6 +41,27 @@ GradProduct router_grad_of(const moe_config &c) {
   p.lda = dl_pitch(c);
   return p;
 }
+// The row products of the experts (operands unset): the two projections, dg and
+// du, and dx.
+enum RowsKind { kUp, kDown, kGateGrad, kInputGrad };
+RowsProduct rows_of(const moe_config &c, RowsKind kind) {
+  const bool gated = c.act == MOE_ACT_SWIGLU;
+  RowsProduct p{};
+  p.dtype = c.act_dtype;
+  p.epi = kind == kUp ? (gated ? kRowsSwiglu : kRowsRelu)
+          : kind == kGateGrad ? (gated ? kRowsSwigluGrad : kRowsReluGrad)
+                              : kRowsPlain;
+  p.b_rows = kind == kGateGrad || kind == kInputGrad;
+  p.num_experts = c.n_experts;
+  p.rows = c.n * c.top_k;
+  const bool wide = kind == kUp || kind == kGateGrad;   // d -> d_ff
+  p.K = wide ? c.d : c.d_ff;
+  p.N = wide ? c.d_ff : c.d;
+  // (shapes alone; the callers set the operands)
+  p.offsets = reinterpret_cast<const int32_t *>(16);
+  if (kind == kInputGrad && gated) p.A2 = reinterpret_cast<const void *>(16);
+  return p;
+}
 int expert_problems(const moe_config &c) { return c.act == MOE_ACT_SWIGLU ? 3 : 2; }
 
 TrainLayout train_layout_of(const moe_config &c) {
@@ -65,7 +86,12 @@ TrainLayout train_layout_of(const moe_config &c) {
   expert_grads_of(c, reinterpret_cast<const int32_t *>(16), experts);   // (shapes alone)
   const GradProduct router = router_grad_of(c);
   const size_t ge = grad_scratch(experts, expert_problems(c)), gr = grad_scratch(&router, 1);
-  L.grad_parts = take(ge > gr ? ge : gr);
+  size_t parts = ge > gr ? ge : gr;   // (used by one launch after the other)
+  for (RowsKind kind : {kUp, kDown, kGateGrad, kInputGrad}) {
+    const size_t r = rows_scratch(rows_of(c, kind));
+    if (r > parts) parts = r;
+  }
+  L.parts = take(parts);
   L.total = off;
   return L;
 }
@@ -94,7 +120,8 @@ moe_status check_routed_weights(const moe_config &c, const moe_weights *w) {
 bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
 
 // bf16 rows run on the tensor cores (SM pairs), fp32 rows on the CUDA cores.
-cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
+// parts: rows_scratch(p) bytes.
+cudaError_t launch_rows(const RowsProduct &p, float *parts, int *status, cudaStream_t s) {
   if (p.dtype == MOE_F32) return launch_rows_simt(p, status, s);
   if (gemm_router_rows_supported(p)) return launch_gemm_router_rows(p, status, s);
   constexpr int epi[] = {0, 1, kEpiSwigluKeep, kEpiReluGrad, kEpiSwigluGrad};   // by kRows*
@@ -118,7 +145,10 @@ cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   g.kept_g = p.g;
   g.kept_u = p.u;
   g.kept_h = p.h;
-  return gemm_t2_supported(g) ? launch_gemm_t2(g, status, s) : cudaErrorNotSupported;
+  if (!gemm_t2_supported(g)) return cudaErrorNotSupported;
+  const int splits = rows_splits(p);
+  return splits > 1 ? launch_rows_split(p, g, splits, parts, status, s)
+                    : launch_gemm_t2(g, status, s);
 }
 
 // Weight gradients over the same segments, in one launch.  splits, parts: as
@@ -218,31 +248,22 @@ moe_status moe_expert_ffn_train(const moe_config *cfg, const void *x_perm, const
   MOE_TRY(check_train_ws(c, ws, ws_bytes));
   int *status = at<int>(ws, train_layout_of(c).status);
   cudaStream_t s = as_stream(stream);
-  RowsProduct up{};
-  up.dtype = c.act_dtype;
-  up.epi = gated ? kRowsSwiglu : kRowsRelu;
+  float *parts = at<float>(ws, train_layout_of(c).parts);
+  RowsProduct up = rows_of(c, kUp);
   up.offsets = offsets;
-  up.num_experts = c.n_experts;
-  up.rows = c.n * c.top_k;
-  up.K = c.d;
-  up.N = c.d_ff;
   up.A = x_perm;
   up.B = w->W1;
   up.B2 = w->W3;
   up.out = h;
   up.out_g = g;
   up.out_u = u;
-  MOE_TRY(cuda_status(launch_rows(up, status, s)));
-  RowsProduct dn = up;
-  dn.epi = kRowsPlain;
-  dn.K = c.d_ff;
-  dn.N = c.d;
+  MOE_TRY(cuda_status(launch_rows(up, parts, status, s)));
+  RowsProduct dn = rows_of(c, kDown);
+  dn.offsets = offsets;
   dn.A = h;
   dn.B = w->W2;
-  dn.B2 = nullptr;
   dn.out = y_perm;
-  dn.out_g = dn.out_u = nullptr;
-  return cuda_status(launch_rows(dn, status, s));
+  return cuda_status(launch_rows(dn, parts, status, s));
 }
 
 moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
@@ -271,7 +292,7 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   GradProduct all[3], gw[kMaxGradProblems];
   expert_grads_of(c, offsets, all);
   const int splits = grad_splits(all, expert_problems(c));
-  float *parts = at<float>(ws, L.grad_parts);
+  float *parts = at<float>(ws, L.parts);
   const void *left[3] = {dy_perm, dg, du}, *right[3] = {h, x_perm, x_perm};
   void *out[3] = {grads->W2, grads->W1, grads->W3};
   int n_gw = 0;
@@ -285,15 +306,8 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   }
   if (!dx_perm && !grads->W1 && !grads->W3)
     return cuda_status(launch_grads(gw, n_gw, splits, parts, status, s));
-  RowsProduct r{};
-  r.dtype = c.act_dtype;
-  r.epi = gated ? kRowsSwigluGrad : kRowsReluGrad;
-  r.b_rows = 1;
+  RowsProduct r = rows_of(c, kGateGrad);
   r.offsets = offsets;
-  r.num_experts = c.n_experts;
-  r.rows = P;
-  r.K = c.d;
-  r.N = c.d_ff;
   r.A = dy_perm;
   r.B = w->W2;
   r.g = g;
@@ -301,24 +315,17 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   r.h = h;
   r.out = dg;
   r.out_u = gated ? du : nullptr;
-  MOE_TRY(cuda_status(launch_rows(r, status, s)));
+  MOE_TRY(cuda_status(launch_rows(r, parts, status, s)));
   MOE_TRY(cuda_status(launch_grads(gw, n_gw, splits, parts, status, s)));
   if (dx_perm) {
-    RowsProduct x{};
-    x.dtype = c.act_dtype;
-    x.epi = kRowsPlain;
-    x.b_rows = 1;
+    RowsProduct x = rows_of(c, kInputGrad);
     x.offsets = offsets;
-    x.num_experts = c.n_experts;
-    x.rows = P;
-    x.K = c.d_ff;
-    x.N = c.d;
     x.A = dg;
     x.B = w->W1;
     x.A2 = gated ? du : nullptr;
     x.B2 = w->W3;
     x.out = dx_perm;
-    MOE_TRY(cuda_status(launch_rows(x, status, s)));
+    MOE_TRY(cuda_status(launch_rows(x, parts, status, s)));
   }
   return MOE_OK;
 }
@@ -370,7 +377,7 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
     gw.A = dl;
     gw.B = x;
     gw.out = dWg;
-    MOE_TRY(cuda_status(launch_grads(&gw, 1, grad_splits(&gw, 1), at<float>(ws, L.grad_parts),
+    MOE_TRY(cuda_status(launch_grads(&gw, 1, grad_splits(&gw, 1), at<float>(ws, L.parts),
                                      status, s)));
   }
   if (rows) {
@@ -389,7 +396,7 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
     r.A = dl;
     r.B = w->Wg;
     r.out = dx_perm ? at<void>(ws, L.dx_router) : dx;
-    MOE_TRY(cuda_status(launch_rows(r, status, s)));
+    MOE_TRY(cuda_status(launch_rows(r, nullptr, status, s)));
     if (dx_perm)
       MOE_TRY(cuda_status(launch_combine(c.act_dtype, dx_perm, inv_perm, nullptr, r.out, dx, c.n,
                                          c.top_k, c.d, status, s)));

@@ -208,6 +208,11 @@ FFN_CASES = [
     (2100, 72, 136, 2, 1, "bf16", "swiglu", [2099, 1]),
     (2500, 264, 64, 2, 1, "bf16", "relu", [1233, 1267]),
     (1600, 72, 72, 1, 1, "bf16", "swiglu", "even"),
+    # few tiles and long reductions: the row products are cut into ranges
+    (33, 72, 2104, 2, 1, "bf16", "swiglu", [20, 13]),
+    (33, 2104, 72, 2, 1, "bf16", "swiglu", [0, 33]),
+    (300, 136, 1096, 1, 1, "bf16", "relu", "even"),
+    (7, 1096, 136, 1, 1, "bf16", "relu", "even"),
     (1, 4, 4, 1, 1, "f32", "swiglu", "even"),
     (256, 128, 512, 4, 1, "f32", "relu", "even"),
     (83, 36, 100, 7, 2, "f32", "swiglu", "even"),
@@ -395,6 +400,27 @@ def test_ffn_rows_outside_the_segments_stay(lib, dtype):
     for t in gr.values():
         assert torch.isfinite(t).all()
     assert sum(counts) == 33
+
+
+@pytest.mark.parametrize("d,F", [(1096, 72), (72, 1096)])
+def test_ffn_rows_outside_the_segments_stay_with_cut_reductions(lib, d, F):
+    s = _ffn_inputs((40, d, F, 2, 1, "bf16", "swiglu", [20, 20]))
+    s["offsets"] = torch.tensor([3, 20, 33], dtype=torch.int32, device="cuda")
+    for key in ("x", "dy"):
+        s[key][:3] = float("nan")
+        s[key][33:] = float("nan")
+    ws = lib.alloc_train_workspace(s["cfg"])
+    ws[256:] = 255                                       # (NaN wherever scratch is not written)
+    g, u, h, y = (_empty(s, w, 5.0) for w in (F, F, F, d))
+    lib.moe_expert_ffn_train(s["cfg"], s["x"], s["offsets"], lib.make_weights(s), g, u, h, y, ws)
+    dx, gr = _empty(s, d, 5.0), _grads(s)
+    lib.moe_expert_ffn_backward(s["cfg"], s["x"], s["offsets"], lib.make_weights(s), g, u, h, s["dy"],
+                                dx, lib.make_expert_grads(gr), ws)
+    _ok(lib, ws)
+    for t in (g, u, h, y, dx):
+        assert (t[:3] == 5.0).all() and (t[33:] == 5.0).all() and torch.isfinite(t[3:33]).all()
+    for t in gr.values():
+        assert torch.isfinite(t).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
