@@ -65,8 +65,12 @@ struct RowsProduct {
   const void *B, *B2;
   const void *g, *u, *h;    // kept rows [rows][N] that a gradient's epilogue reads
   void *out, *out_g, *out_u;   // [rows][N]
+  // kRowsPlain on the CUDA cores: out[q] += sum_j add[add_inv[q * add_k + j]]
+  const void *add;             // [rows * add_k][N] or nullptr
+  const int32_t *add_inv;
+  int add_k;
 };
-// (fp32)
+// fp32, and small bf16 products.
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s);
 
 // The same with the reduction cut into ranges where its tiles are few (bf16):
@@ -89,7 +93,8 @@ struct GradProduct {
   void *out;                // [E][M][N]
 };
 constexpr int kMaxGradProblems = 3;
-// Up to kMaxGradProblems of them over the same segments in one launch (fp32).
+// Up to kMaxGradProblems of them over the same segments in one launch (fp32, and
+// small bf16 products).
 cudaError_t launch_grad_simt(const GradProduct *p, int count, int *status, cudaStream_t s);
 // The same on tensor cores (bf16; SM pairs).
 bool gemm_grad_supported(const GradProduct &p);

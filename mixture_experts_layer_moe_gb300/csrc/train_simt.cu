@@ -2,12 +2,15 @@
 //
 // The path of fp32 layers (tensor cores multiply fp32 operands in fewer
 // bits), written for their sizes: a layer of a few hundred rows, whose
-// launches cost as much as its products.
+// launches cost as much as its products; and of bf16 layers so small that
+// setting up the tensor-core kernels is most of their time (32 x 32 tiles).
 // A CTA computes a tile of one segment's rows (RowsProduct) or of one expert's
 // gradient (GradProduct) with 256 threads: 64 x 64, or 32 x 32 where the larger
 // tiles would not give every SM one.  The next step's operands are loaded into
-// registers while the current one is multiplied, and shared memory is double
-// buffered, so a step waits for memory once, not twice (256 rows, d 128, d_ff
+// registers while the current one is multiplied (two steps ahead took the
+// registers of resident CTAs: 770 us for 743 at 4096 rows of 16 experts, d 512,
+// d_ff 1024), and shared memory is double buffered, so a step waits for memory
+// once, not twice (256 rows, d 128, d_ff
 // 512, 4 experts, forward: 49 us without any of it, 15.6 with).
 // The three storage orders of the operands differ in how a tile is staged
 // only: in shared memory both operands lie reduction index first, so that a
@@ -36,23 +39,39 @@ struct Geo {
   using Buf = float[TK][LD];
 };
 
+__device__ __forceinline__ float4 load4(const float *p) {
+  return *reinterpret_cast<const float4 *>(p);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+  const uint2 w = *reinterpret_cast<const uint2 *>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
+                                             *reinterpret_cast<const uint32_t *>(&b));
+}
+
 // This thread's part of a TK x TILE operand tile, as vectors of 4: element
 // (kk, i) is src[i * ld + kk] (K_FAST) or src[kk * ld + i]; zero outside i < ni,
-// kk < nk.  The contiguous bound and ld are multiples of 4, and src is 16-byte
-// aligned.
-template <bool K_FAST, int TILE>
+// kk < nk.  The contiguous bound and ld are multiples of 4, and src lies on a
+// vector's boundary.
+template <typename T, bool K_FAST, int TILE>
 struct Part {
   using G = Geo<TILE>;
   float4 v[G::LOADS];
   static __device__ __forceinline__ int kk(int l) { return K_FAST ? l % (G::TK / 4) * 4 : l / (TILE / 4); }
   static __device__ __forceinline__ int ii(int l) { return K_FAST ? l / (G::TK / 4) : l % (TILE / 4) * 4; }
-  __device__ __forceinline__ void load(const float *src, int64_t ld, int ni, int nk) {
+  __device__ __forceinline__ void load(const T *src, int64_t ld, int ni, int nk) {
 #pragma unroll
     for (int c = 0; c < G::LOADS; ++c) {
       const int l = threadIdx.x + c * T_THREADS, k = kk(l), i = ii(l);
       v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < ni && k < nk)
-        v[c] = *reinterpret_cast<const float4 *>(src + (K_FAST ? i * ld + k : k * ld + i));
+      if (i < ni && k < nk) v[c] = load4(src + (K_FAST ? i * ld + k : k * ld + i));
     }
   }
   __device__ __forceinline__ void store(typename G::Buf &dst) const {
@@ -130,15 +149,18 @@ struct Place {
   }
 };
 
+template <typename T>
 __device__ __forceinline__ void get4(const void *p, int64_t at, float (&v)[4]) {
-  const float4 t = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+  const float4 t = load4(static_cast<const T *>(p) + at);
   v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
 }
+template <typename T>
 __device__ __forceinline__ void put4(void *p, int64_t at, const float (&v)[4]) {
-  *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  store4(static_cast<T *>(p) + at, v);
 }
 
-// Expert and row range of this CTA's tile; false when there is none.
+// Expert and row range of this CTA's tile; false when there is none.  Every warp
+// looks for itself, 32 experts at a time.
 template <int TM>
 __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int rows, int tile, int &e,
                                           int &row0, int &end, int *status) {
@@ -148,26 +170,59 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int row
     end = rows;
     return row0 < end;
   }
-  int acc = 0;
-  for (int x = 0; x < E; ++x) {
-    const int a = offsets[x], b = offsets[x + 1];
-    if (a < 0 || b < a || b > rows) {
-      if (threadIdx.x == 0) set_status(status, MOE_ERR_BAD_INDEX, x);
+  const unsigned all = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  int before = 0;   // tiles of the experts before x0
+  for (int x0 = 0; x0 < E; x0 += 32) {
+    const int x = x0 + lane;
+    int a = 0, b = 0;
+    if (x < E) {
+      a = offsets[x];
+      b = offsets[x + 1];
+    }
+    const bool bad = a < 0 || b < a || b > rows;
+    if (__any_sync(all, bad)) {
+      if (bad) set_status(status, MOE_ERR_BAD_INDEX, x);
       return false;
     }
-    const int nt = (b - a + TM - 1) / TM;
-    if (tile < acc + nt) {
-      e = x;
-      row0 = a + (tile - acc) * TM;
-      end = b;
+    const int own = (b - a + TM - 1) / TM;
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(all, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const unsigned hit = __ballot_sync(all, tile < before + upto);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      e = x0 + l;
+      row0 = __shfl_sync(all, a, l) + (tile - before - __shfl_sync(all, upto - own, l)) * TM;
+      end = __shfl_sync(all, b, l);
       return true;
     }
-    acc += nt;
+    before += __shfl_sync(all, upto, 31);
   }
   return false;
 }
 
-template <int EPI, bool B_ROWS, int TILE>
+// Steps of a product, with the next step's loads in flight: load(step) fills the
+// registers, store(buffer) writes them to shared memory, multiply(buffer) takes
+// the step.
+template <int BUFS, typename Load, typename Store, typename Multiply>
+__device__ __forceinline__ void run_steps(int steps, Load &&load, Store &&store,
+                                          Multiply &&multiply) {
+  if (steps > 0) load(0);
+  for (int step = 0; step < steps; ++step) {
+    const int buf = BUFS == 2 ? step & 1 : 0;
+    if (BUFS == 1 && step > 0) __syncthreads();
+    store(buf);
+    __syncthreads();
+    if (step + 1 < steps) load(step + 1);
+    multiply(buf);
+  }
+}
+
+template <typename T, int EPI, bool B_ROWS, int TILE>
 __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int *status) {
   using G = Geo<TILE>;
   constexpr bool DUAL = EPI == kRowsSwiglu;
@@ -189,31 +244,31 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   // the steps of the one or two operand pairs, one after the other
   const int steps1 = (K + G::TK - 1) / G::TK;
   const int steps = steps1 * (EPI == kRowsPlain && p.A2 ? 2 : 1);
-  Part<true, TILE> pa, pb2;
-  Part<!B_ROWS, TILE> pb;
+  Part<T, true, TILE> pa, pb2;
+  Part<T, !B_ROWS, TILE> pb;
   // (a row's padding, lda > K, holds zeros and may be read)
   const int ka = p.lda ? p.lda : K;
-  auto load = [&](int step) {
-    const bool second = step >= steps1;
-    const int k0 = (second ? step - steps1 : step) * G::TK;
-    const float *A = static_cast<const float *>(second ? p.A2 : p.A) + row0 * lda;
-    const float *B = static_cast<const float *>(second ? p.B2 : p.B) + base;
-    pa.load(A + k0, lda, end - row0, ka - k0);
-    pb.load(B_ROWS ? B + (int64_t)k0 * N : B + k0, B_ROWS ? N : K, N - n0, K - k0);
-    if constexpr (DUAL) pb2.load(static_cast<const float *>(p.B2) + base + k0, K, N - n0, K - k0);
-  };
-  load(0);
-  for (int step = 0; step < steps; ++step) {
-    const int buf = BUFS == 2 ? step & 1 : 0;
-    if (BUFS == 1 && step > 0) __syncthreads();
-    pa.store(as[buf]);
-    pb.store(bs[buf]);
-    if constexpr (DUAL) pb2.store(b2s[buf]);
-    __syncthreads();
-    if (step + 1 < steps) load(step + 1);
-    tile_fma<TILE>(acc, as[buf], bs[buf], me.tx, me.ty, me.g);
-    if constexpr (DUAL) tile_fma<TILE>(acc2, as[buf], b2s[buf], me.tx, me.ty, me.g);
-  }
+  run_steps<BUFS>(
+      steps,
+      [&](int step) {
+        const bool second = step >= steps1;
+        const int k0 = (second ? step - steps1 : step) * G::TK;
+        const T *A = static_cast<const T *>(second ? p.A2 : p.A) + row0 * lda;
+        const T *B = static_cast<const T *>(second ? p.B2 : p.B) + base;
+        pa.load(A + k0, lda, end - row0, ka - k0);
+        pb.load(B_ROWS ? B + (int64_t)k0 * N : B + k0, B_ROWS ? N : K, N - n0, K - k0);
+        if constexpr (DUAL)
+          pb2.load(static_cast<const T *>(p.B2) + base + k0, K, N - n0, K - k0);
+      },
+      [&](int buf) {
+        pa.store(as[buf]);
+        pb.store(bs[buf]);
+        if constexpr (DUAL) pb2.store(b2s[buf]);
+      },
+      [&](int buf) {
+        tile_fma<TILE>(acc, as[buf], bs[buf], me.tx, me.ty, me.g);
+        if constexpr (DUAL) tile_fma<TILE>(acc2, as[buf], b2s[buf], me.tx, me.ty, me.g);
+      });
   // (the next kernel's CTAs, placed from the start, would share these SMs: 25 us
   // for the two products of the tiny layer's forward, 20 launched apart, 15.6 so)
   pdl_launch_dependents();
@@ -232,28 +287,42 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
       for (int j = 0; j < 4; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
     } else if constexpr (EPI == kRowsSwiglu) {
       const float u[4] = {acc2[i][0].x, acc2[i][0].y, acc2[i][1].x, acc2[i][1].y};
-      put4(p.out_g, at, v);
-      put4(p.out_u, at, u);
+      put4<T>(p.out_g, at, v);
+      put4<T>(p.out_u, at, u);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = v[j] / (1.f + expf(-v[j])) * u[j];
     } else if constexpr (EPI == kRowsReluGrad) {
       float h[4];
-      get4(p.h, at, h);
+      get4<T>(p.h, at, h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = h[j] > 0.f ? v[j] : 0.f;
     } else if constexpr (EPI == kRowsSwigluGrad) {
       float g[4], u[4], du[4];
-      get4(p.g, at, g);
-      get4(p.u, at, u);
+      get4<T>(p.g, at, g);
+      get4<T>(p.u, at, u);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float s = 1.f / (1.f + expf(-g[j]));
         du[j] = v[j] * g[j] * s;
         v[j] = v[j] * u[j] * s * (1.f + g[j] * (1.f - s));
       }
-      put4(p.out_u, at, du);
+      put4<T>(p.out_u, at, du);
     }
-    put4(p.out, at, v);
+    if (EPI == kRowsPlain && p.add) {
+      // the sum of this row's add_k other rows
+      for (int j = 0; j < p.add_k; ++j) {
+        const int q = p.add_inv[(int64_t)r * p.add_k + j];
+        if (q < 0 || q >= p.rows * p.add_k) {
+          if (c == 0) set_status(status, MOE_ERR_BAD_INDEX, r * p.add_k + j);
+          continue;
+        }
+        float o[4];
+        get4<T>(p.add, (int64_t)q * N + c, o);
+#pragma unroll
+        for (int i4 = 0; i4 < 4; ++i4) v[i4] += o[i4];
+      }
+    }
+    put4<T>(p.out, at, v);
   }
 }
 
@@ -263,7 +332,7 @@ struct GradSet {
   GradProduct p[kMaxGradProblems];
   int first[kMaxGradProblems + 1];   // an expert's tiles before problem i
 };
-template <int TILE>
+template <typename T, int TILE>
 __global__ void __launch_bounds__(T_THREADS)
 grad_simt_kernel(const __grid_constant__ GradSet set, int *status) {
   using G = Geo<TILE>;
@@ -286,20 +355,20 @@ grad_simt_kernel(const __grid_constant__ GradSet set, int *status) {
   const int64_t lda = p.lda ? p.lda : M;
   const Place<TILE> me;
   float2 acc[4][2] = {};
-  const float *A = static_cast<const float *>(p.A) + m0, *B = static_cast<const float *>(p.B) + n0;
-  Part<false, TILE> pa, pb;
-  auto load = [&](int q) {
-    pa.load(A + q * lda, lda, (int)lda - m0, end - q);
-    pb.load(B + (int64_t)q * N, N, N - n0, end - q);
-  };
-  if (beg < end) load(beg);
-  for (int q = beg, buf = 0; q < end; q += G::TK, buf ^= 1) {
-    pa.store(as[buf]);
-    pb.store(bs[buf]);
-    __syncthreads();
-    if (q + G::TK < end) load(q + G::TK);
-    tile_fma<TILE>(acc, as[buf], bs[buf], me.tx, me.ty, me.g);
-  }
+  const T *A = static_cast<const T *>(p.A) + m0, *B = static_cast<const T *>(p.B) + n0;
+  Part<T, false, TILE> pa, pb;
+  run_steps<2>(
+      (end - beg + G::TK - 1) / G::TK,
+      [&](int step) {
+        const int q = beg + step * G::TK;
+        pa.load(A + q * lda, lda, (int)lda - m0, end - q);
+        pb.load(B + (int64_t)q * N, N, N - n0, end - q);
+      },
+      [&](int buf) {
+        pa.store(as[buf]);
+        pb.store(bs[buf]);
+      },
+      [&](int buf) { tile_fma<TILE>(acc, as[buf], bs[buf], me.tx, me.ty, me.g); });
   pdl_launch_dependents();
   join_groups<TILE>(acc, &as[0][0][0], me.tx, me.ty, me.g);
   const int c = n0 + me.col;   // (N is a multiple of 4)
@@ -308,30 +377,21 @@ grad_simt_kernel(const __grid_constant__ GradSet set, int *status) {
   for (int i = 0; i < Place<TILE>::ROWS; ++i) {
     const int m = m0 + me.row + i;
     const float v[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
-    if (m < M) put4(p.out, ((int64_t)e * M + m) * N + c, v);
+    if (m < M) put4<T>(p.out, ((int64_t)e * M + m) * N + c, v);
   }
 }
 
-template <int TILE>
+template <typename T, int TILE>
 cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   const int mt = (p.rows + TILE - 1) / TILE + (p.offsets ? p.num_experts : 0);
   const dim3 grid(mt, (p.N + TILE - 1) / TILE);
-  cudaError_t e;
-  if (p.epi == kRowsPlain && p.b_rows)
-    e = launch_pdl(rows_simt_kernel<kRowsPlain, true, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
-  else if (p.epi == kRowsPlain)
-    e = launch_pdl(rows_simt_kernel<kRowsPlain, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
-  else if (p.epi == kRowsRelu)
-    e = launch_pdl(rows_simt_kernel<kRowsRelu, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
-  else if (p.epi == kRowsSwiglu)
-    e = launch_pdl(rows_simt_kernel<kRowsSwiglu, false, TILE>, grid, dim3(T_THREADS), 0, s, p, status);
-  else if (p.epi == kRowsReluGrad)
-    e = launch_pdl(rows_simt_kernel<kRowsReluGrad, true, TILE>, grid, dim3(T_THREADS), 0, s, p,
-                   status);
-  else
-    e = launch_pdl(rows_simt_kernel<kRowsSwigluGrad, true, TILE>, grid, dim3(T_THREADS), 0, s, p,
-                   status);
-  return e;
+  auto with = p.epi == kRowsPlain && p.b_rows ? rows_simt_kernel<T, kRowsPlain, true, TILE>
+              : p.epi == kRowsPlain           ? rows_simt_kernel<T, kRowsPlain, false, TILE>
+              : p.epi == kRowsRelu            ? rows_simt_kernel<T, kRowsRelu, false, TILE>
+              : p.epi == kRowsSwiglu          ? rows_simt_kernel<T, kRowsSwiglu, false, TILE>
+              : p.epi == kRowsReluGrad        ? rows_simt_kernel<T, kRowsReluGrad, true, TILE>
+                                              : rows_simt_kernel<T, kRowsSwigluGrad, true, TILE>;
+  return launch_pdl(with, grid, dim3(T_THREADS), 0, s, p, status);
 }
 
 // Whether this many 64 x 64 tiles give each SM one.
@@ -339,12 +399,11 @@ bool large_tiles(int64_t tiles) { return tiles >= num_sms(); }
 
 }  // namespace
 
-// fp32 layers only: bf16 layers run on the tensor cores.
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s) {
-  if (p.dtype != MOE_F32) return cudaErrorInvalidValue;
+  if (p.dtype == MOE_BF16) return launch_rows<__nv_bfloat16, 32>(p, status, s);
   return large_tiles((int64_t)((p.rows + 63) / 64) * ((p.N + 63) / 64))
-             ? launch_rows<64>(p, status, s)
-             : launch_rows<32>(p, status, s);
+             ? launch_rows<float, 64>(p, status, s)
+             : launch_rows<float, 32>(p, status, s);
 }
 
 cudaError_t launch_grad_simt(const GradProduct *p, int count, int *status, cudaStream_t s) {
@@ -358,10 +417,12 @@ cudaError_t launch_grad_simt(const GradProduct *p, int count, int *status, cudaS
     }
     return set.first[count];
   };
-  const bool large = large_tiles((int64_t)lay(64) * E);
+  const bool bf16 = p[0].dtype == MOE_BF16, large = !bf16 && large_tiles((int64_t)lay(64) * E);
   const dim3 grid(lay(large ? 64 : 32), E);
-  return launch_pdl(large ? grad_simt_kernel<64> : grad_simt_kernel<32>, grid, dim3(T_THREADS), 0,
-                    s, set, status);
+  auto with = bf16    ? grad_simt_kernel<__nv_bfloat16, 32>
+              : large ? grad_simt_kernel<float, 64>
+                      : grad_simt_kernel<float, 32>;
+  return launch_pdl(with, grid, dim3(T_THREADS), 0, s, set, status);
 }
 
 }  // namespace moe
