@@ -453,8 +453,9 @@ moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const voi
  * probs fp32 [n][E] as moe_route wrote it (may be NULL for RENORM without f);
  * f fp32 [E] or NULL.  dx_perm and inv_perm may both be NULL (the router's
  * share alone).  dx act_dtype [n][d], dWg act_dtype [E][d], dbias fp32 [E]:
- * each may be NULL.  bf16 layers round dl once to bf16 for the two products
- * (dbias sums it in fp32).  A topk_idx outside [0, E) sets MOE_ERR_BAD_INDEX
+ * each may be NULL.  bf16 layers round dl to bf16 as an operand of its
+ * products, and dl Wg before the rows are added, where these run on the tensor
+ * cores (dbias sums dl in fp32).  A topk_idx outside [0, E) sets MOE_ERR_BAD_INDEX
  * and its slot counts as a gate of zero. */
 moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_weights *w,
                               const float *probs, const int32_t *topk_idx, const float *topk_gate,

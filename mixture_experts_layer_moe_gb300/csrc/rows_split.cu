@@ -101,7 +101,8 @@ int rows_splits(const RowsProduct &p) {
   const double whole = 2.5 + (double)kb * 0.4;   // (one round)
   int best = 1;
   double least = 0.8 * whole;
-  for (int n = 2; n <= 2 * RS_PAIRS && n <= kb; ++n) {
+  // (no more than two rounds)
+  for (int n = 2; n * tiles <= 2 * RS_PAIRS && n <= kb; ++n) {
     const int64_t each = (kb + n - 1) / n;
     if ((kb + each - 1) / each != n) continue;   // (a range would be empty)
     const double us = (double)((tiles * n + RS_PAIRS - 1) / RS_PAIRS) * (2.5 + each * 0.4) + 4 +

@@ -102,10 +102,11 @@ moe_status check_train_config(const moe_config *c) {
   return MOE_OK;
 }
 
-moe_status check_train_ws(const moe_config &c, const void *ws, size_t ws_bytes) {
+// Checks the workspace and lays it out.
+moe_status check_train_ws(const moe_config &c, const void *ws, size_t ws_bytes, TrainLayout &L) {
   if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < train_layout_of(c).total) return MOE_ERR_WORKSPACE;
-  return MOE_OK;
+  L = train_layout_of(c);
+  return ws_bytes < L.total ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
 // The routed experts' weights alone (shared-expert weights are not read here).
@@ -262,10 +263,11 @@ moe_status moe_expert_ffn_train(const moe_config *cfg, const void *x_perm, const
     return MOE_ERR_INVALID_ARG;
   const bool gated = c.act == MOE_ACT_SWIGLU;
   if (gated ? !ok_ptr(g) || !ok_ptr(u) : g != nullptr || u != nullptr) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_train_ws(c, ws, ws_bytes));
-  int *status = at<int>(ws, train_layout_of(c).status);
+  TrainLayout L;
+  MOE_TRY(check_train_ws(c, ws, ws_bytes, L));
+  int *status = at<int>(ws, L.status);
   cudaStream_t s = as_stream(stream);
-  float *parts = at<float>(ws, train_layout_of(c).parts);
+  float *parts = at<float>(ws, L.parts);
   RowsProduct up = rows_of(c, kUp);
   up.offsets = offsets;
   up.A = x_perm;
@@ -299,8 +301,8 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   if (!ok_or_null(grads->W1) || !ok_or_null(grads->W3) || !ok_or_null(grads->W2))
     return MOE_ERR_INVALID_ARG;
   if (!gated && grads->W3) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_train_ws(c, ws, ws_bytes));
-  const TrainLayout L = train_layout_of(c);
+  TrainLayout L;
+  MOE_TRY(check_train_ws(c, ws, ws_bytes, L));
   int *status = at<int>(ws, L.status);
   cudaStream_t s = as_stream(stream);
   const int P = c.n * c.top_k;
@@ -356,10 +358,11 @@ moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const voi
     return MOE_ERR_INVALID_ARG;
   if ((y_perm == nullptr) != (dgate == nullptr) || !ok_or_null(y_perm) || !ok_or_null(dgate))
     return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_train_ws(c, ws, ws_bytes));
+  TrainLayout L;
+  MOE_TRY(check_train_ws(c, ws, ws_bytes, L));
   return cuda_status(launch_combine_backward(c.act_dtype, dy, y_perm, inv_perm, topk_gate, dy_perm,
                                              dgate, c.n, c.top_k, c.d,
-                                             at<int>(ws, train_layout_of(c).status),
+                                             at<int>(ws, L.status),
                                              as_stream(stream)));
 }
 
@@ -379,8 +382,8 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
   if ((inv_perm == nullptr) != (dx_perm == nullptr)) return MOE_ERR_INVALID_ARG;
   if (dx_perm && !dx) return MOE_ERR_INVALID_ARG;
   if (dWg && !ok_ptr(x)) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_train_ws(c, ws, ws_bytes));
-  const TrainLayout L = train_layout_of(c);
+  TrainLayout L;
+  MOE_TRY(check_train_ws(c, ws, ws_bytes, L));
   int *status = at<int>(ws, L.status);
   cudaStream_t s = as_stream(stream);
   const int pitch = dl_pitch(c);
