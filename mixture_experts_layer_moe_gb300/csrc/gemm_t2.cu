@@ -72,6 +72,7 @@ using namespace pair;
 
 constexpr int PM = 128;                         // weight rows per CTA (MMA M = 256 per pair)
 constexpr int PN = 256;                         // tokens per tile at most (MMA N)
+constexpr int PN_SHORT = 32;                    // token rows of a short box
 constexpr int PK = 64;                          // k-block
 constexpr int PS = 6;                           // pipeline stages
 constexpr int P_B_BYTES = (PN / 2) * PK * 2;    // this CTA's half of the token tile: 16 KB
@@ -126,6 +127,12 @@ struct PArgs {
   // the reduction, for one or two weight matrices
   float *parts;
   int splits, mats;
+};
+
+// Tensor maps of the token rows (whole boxes, and the short ones for blocks of
+// at most 2 * PN_SHORT tokens), of the second pair's rows, and of the weights.
+struct PMaps {
+  CUtensorMap X, Xs, X2, X2s, W, W3;
 };
 
 struct PTile {
@@ -202,15 +209,12 @@ __device__ __forceinline__ void load_kept(const PArgs &args, int tok0, int end, 
 // (128-byte swizzle, the boxes 8 KB apart), and no transposed copy is made.
 template <int EPI, bool WROWS>
 __global__ void __launch_bounds__(pair_threads<EPI>(), 1)
-gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-               const __grid_constant__ CUtensorMap tmX2, const __grid_constant__ CUtensorMap tmW3,
-               PArgs args) {
+gemm_t2_kernel(const __grid_constant__ PMaps maps, const PArgs args) {
   constexpr bool GATED = EPI == 2 || EPI == 5;        // two weight matrices side by side
   constexpr int P_EPI = epi_warps<EPI>(), P_THREADS = pair_threads<EPI>(), TURNS = P_EPI / 4;
   static_assert(!WROWS || !GATED, "the gated forward reads weights stored by output column");
   constexpr int OUT_CTA = GATED ? PM / 2 : PM;        // output columns per CTA per tile
   constexpr int OUT_TILE = 2 * OUT_CTA;
-  constexpr uint32_t TX_BYTES = 2u * P_STAGE;          // both CTAs' copies of one stage
   extern __shared__ uint8_t dyn_smem[];
   __shared__ PShared sh;
   uint8_t *smem = dyn_smem + ((1024 - (tc::smem_u32(dyn_smem) & 1023)) & 1023);
@@ -241,10 +245,14 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   };
 
   if (threadIdx.x == 0) {
-    tc::prefetch_tmap(&tmX);
-    tc::prefetch_tmap(&tmW);
-    if (GATED || WROWS || EPI == 8) tc::prefetch_tmap(&tmW3);
-    if (WROWS) tc::prefetch_tmap(&tmX2);
+    tc::prefetch_tmap(&maps.X);
+    tc::prefetch_tmap(&maps.Xs);
+    tc::prefetch_tmap(&maps.W);
+    if (GATED || WROWS || EPI == 8) tc::prefetch_tmap(&maps.W3);
+    if (WROWS) {
+      tc::prefetch_tmap(&maps.X2);
+      tc::prefetch_tmap(&maps.X2s);
+    }
   }
   if (warp == 1) tmem_alloc2(&sh.tmem_base, P_TMEM_COLS);
   if (threadIdx.x == 32) {
@@ -324,6 +332,12 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         const PTile tl = decode(t);
         const int ntok = tl.ntok;
         const int half = ((ntok + 15) & ~15) >> 1;   // tokens staged by each CTA
+        // few tokens take a short box: whole ones would be half of what this
+        // SM copies, beside the weights that a block of few tokens waits for
+        // (one token, d 4096, d_ff 14336, one expert, forward: 99 -> 78 us)
+        const bool few = half <= PN_SHORT;
+        const uint32_t bytes = 2u * (P_A_BYTES + (few ? PN_SHORT : PN / 2) * PK * 2);
+        const CUtensorMap *x1 = few ? &maps.Xs : &maps.X, *x2 = few ? &maps.X2s : &maps.X2;
         const int brow = tl.tok0 + (int)rank * half;
         const int wrow = tl.wb * OUT_TILE + (int)rank * OUT_CTA;
         for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
@@ -333,23 +347,21 @@ gemm_t2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
           const uint32_t bar = full0 + (uint32_t)stage * 8;
           used |= 1u << stage;
           used_phase = phase ? used_phase | 1u << stage : used_phase & ~(1u << stage);
-          if (rank == 0) tc::mbar_arrive_expect_tx(&sh.full[stage], TX_BYTES);
+          if (rank == 0) tc::mbar_arrive_expect_tx(&sh.full[stage], bytes);   // of both CTAs
           if constexpr (WROWS) {
             const bool second = kb >= KB1;
             const int k0 = (second ? kb - KB1 : kb) * PK;
-            const CUtensorMap *w = second ? &tmW3 : &tmW;
-            tma2_load_2d(second ? &tmX2 : &tmX, bar, sb, k0, brow);
+            const CUtensorMap *w = second ? &maps.W3 : &maps.W;
+            tma2_load_2d(second ? x2 : x1, bar, sb, k0, brow);
             tma2_load_3d(w, bar, sa, wrow, k0, tl.e);                       // columns 0..63
             tma2_load_3d(w, bar, sa + P_A_BYTES / 2, wrow + 64, k0, tl.e);  // columns 64..127
-            if (++stage == PS) { stage = 0; phase ^= 1u; }
-            continue;
-          }
-          tma2_load_2d(&tmX, bar, sb, kb * PK, brow);
-          if constexpr (GATED) {
-            tma2_load_3d(&tmW, bar, sa, kb * PK, wrow, tl.e);               // rows 0..63
-            tma2_load_3d(&tmW3, bar, sa + P_A_BYTES / 2, kb * PK, wrow, tl.e);  // rows 64..127
+          } else if constexpr (GATED) {
+            tma2_load_2d(x1, bar, sb, kb * PK, brow);
+            tma2_load_3d(&maps.W, bar, sa, kb * PK, wrow, tl.e);                    // rows 0..63
+            tma2_load_3d(&maps.W3, bar, sa + P_A_BYTES / 2, kb * PK, wrow, tl.e);   // rows 64..127
           } else {
-            tma2_load_3d(EPI == 8 && tl.mat ? &tmW3 : &tmW, bar, sa, kb * PK, wrow, tl.e);
+            tma2_load_2d(x1, bar, sb, kb * PK, brow);
+            tma2_load_3d(EPI == 8 && tl.mat ? &maps.W3 : &maps.W, bar, sa, kb * PK, wrow, tl.e);
           }
           if (++stage == PS) { stage = 0; phase ^= 1u; }
         }
@@ -591,27 +603,28 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
                            pair_threads<EPI>(), P_DYN_SMEM);
   }
   const int E = g.offsets ? g.num_experts : 1;
-  CUtensorMap mX, mW, mX2, mW3;
+  PMaps m;
   auto bf16_map = [](CUtensorMap *m, const void *p, int rank, const uint64_t *dims,
                      const uint32_t *box) {
     return make_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, rank, dims, box,
                            CU_TENSOR_MAP_SWIZZLE_128B);
   };
   const uint64_t dX[2] = {(uint64_t)(g.lda ? g.lda : g.K), (uint64_t)g.rows};
-  const uint32_t bX[2] = {PK, PN / 2};
-  if (!bf16_map(&mX, g.A, 2, dX, bX)) return cudaErrorInvalidValue;
+  const uint32_t bX[2] = {PK, PN / 2}, bXs[2] = {PK, PN_SHORT};
   // weights by output column: boxes of 64 reduction elements x 128 (64) rows;
   // by reduction row: boxes of 64 columns x 64 reduction rows
   const uint64_t dW[3] = {(uint64_t)(WROWS ? g.N : g.K), (uint64_t)(WROWS ? g.K : g.N),
                           (uint64_t)E};
   const uint32_t bW[3] = {PK, (uint32_t)(WROWS ? PK : GATED ? PM / 2 : PM), 1};
-  if (!bf16_map(&mW, g.B, 3, dW, bW)) return cudaErrorInvalidValue;
-  mW3 = mW;
-  mX2 = mX;
-  if (g.B3) {
-    if (!bf16_map(&mW3, g.B3, 3, dW, bW)) return cudaErrorInvalidValue;
-  }
-  if (g.A2 && !bf16_map(&mX2, g.A2, 2, dX, bX)) return cudaErrorInvalidValue;
+  if (!bf16_map(&m.X, g.A, 2, dX, bX) || !bf16_map(&m.Xs, g.A, 2, dX, bXs) ||
+      !bf16_map(&m.W, g.B, 3, dW, bW))
+    return cudaErrorInvalidValue;
+  m.W3 = m.W;
+  m.X2 = m.X;
+  m.X2s = m.Xs;
+  if (g.B3 && !bf16_map(&m.W3, g.B3, 3, dW, bW)) return cudaErrorInvalidValue;
+  if (g.A2 && (!bf16_map(&m.X2, g.A2, 2, dX, bX) || !bf16_map(&m.X2s, g.A2, 2, dX, bXs)))
+    return cudaErrorInvalidValue;
   PArgs a{};
   a.offsets = g.offsets;
   a.num_experts = g.num_experts;
@@ -651,7 +664,7 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
   // experts, d 1024, d_ff 2048); the gradients' measured slower so (150.4
   // against 154.2 us for the latter's backward)
   cfg.numAttrs = WROWS ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, gemm_t2_kernel<EPI, WROWS>, mX, mW, mX2, mW3, a);
+  return cudaLaunchKernelEx(&cfg, gemm_t2_kernel<EPI, WROWS>, m, a);
 }
 
 }  // namespace
