@@ -8,6 +8,7 @@ module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -316,6 +317,12 @@ def alloc_train_workspace(cfg, device="cuda") -> torch.Tensor:
 _NORM_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_config(rows, ldx, ldy, lddx, lddy, d, dtype, eps):
+    """A moe_norm_config by reference (the library only reads it)."""
+    return ctypes.byref(moe_norm_config(rows, ldx, ldy, lddx, lddy, d, dtype, eps, 0))
+
+
 def _norm_rows(t: torch.Tensor, shape, dtype) -> tuple[int, int]:
     """(pointer, elements from one row to the next) of a [rows, d] tensor whose rows are dense."""
     if t.shape != shape or t.dtype is not dtype:
@@ -347,11 +354,11 @@ def moe_layernorm(x, gamma, beta, y, mean, rstd, eps=1e-5, stream=None):
     n, d = shape
     xp, ldx = _norm_rows(x, shape, xt)
     yp, ldy = _norm_rows(y, shape, xt)
-    c = moe_norm_config(n, ldx, ldy, 0, 0, d, code, eps, 0)
     f32 = torch.float32
-    _check(_lib.moe_layernorm(ctypes.byref(c), xp, _norm_vector(gamma, d, xt),
-                              _norm_vector(beta, d, xt), yp, _norm_vector(mean, n, f32),
-                              _norm_vector(rstd, n, f32), _stream(stream)), "moe_layernorm")
+    _check(_lib.moe_layernorm(
+        _norm_config(n, ldx, ldy, 0, 0, d, code, eps), xp, _norm_vector(gamma, d, xt),
+        _norm_vector(beta, d, xt), yp, _norm_vector(mean, n, f32), _norm_vector(rstd, n, f32),
+        _stream(stream)), "moe_layernorm")
 
 
 def moe_layernorm_workspace_size(rows: int, d: int, dtype: str) -> int:
@@ -372,10 +379,9 @@ def moe_layernorm_backward(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, stre
     xp, ldx = _norm_rows(x, shape, xt)
     dyp, lddy = _norm_rows(dy, shape, xt)
     dxp, lddx = _norm_rows(dx, shape, xt)
-    c = moe_norm_config(n, ldx, 0, lddx, lddy, d, code, 0.0, 0)
     f32 = torch.float32
     _check(_lib.moe_layernorm_backward(
-        ctypes.byref(c), xp, _norm_vector(gamma, d, xt), _norm_vector(mean, n, f32),
+        _norm_config(n, ldx, 0, lddx, lddy, d, code, 0.0), xp, _norm_vector(gamma, d, xt), _norm_vector(mean, n, f32),
         _norm_vector(rstd, n, f32), dyp, dxp, _norm_vector(dgamma, d, f32),
         _norm_vector(dbeta, d, f32), _ptr(ws), ws.numel(), _stream(stream)),
         "moe_layernorm_backward")
