@@ -514,7 +514,8 @@ bool gemm_grad_supported(const GradProduct &p) {
 // 7168: 28 tiles, 155 us at 64 columns each; 64 us in 140 runs of 256
 // columns and their sum.)
 int grad_splits(const GradProduct *p, int count) {
-  if (count == 0 || p[0].dtype != MOE_BF16) return 1;
+  if (count == 0) return 1;
+  if (grads_small(p, count)) return grad_splits_simt(p, count);
   const int64_t tiles = tiles_of(p, count, GN);
   const int E = p[0].offsets ? p[0].num_experts : 1;
   if (tiles >= kPairs) return 1;

@@ -70,7 +70,8 @@ struct RowsProduct {
   const int32_t *add_inv;
   int add_k;
 };
-// fp32, and small bf16 products.
+// fp32, and small bf16 products: at most so many multiplications each.
+constexpr int64_t kSmallProducts = 1 << 24;
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s);
 
 // The same with the reduction cut into ranges where its tiles are few (bf16):
@@ -93,9 +94,14 @@ struct GradProduct {
   void *out;                // [E][M][N]
 };
 constexpr int kMaxGradProblems = 3;
-// Up to kMaxGradProblems of them over the same segments in one launch (fp32, and
-// small bf16 products).
-cudaError_t launch_grad_simt(const GradProduct *p, int count, int *status, cudaStream_t s);
+// Up to kMaxGradProblems of them over the same segments in one launch on the CUDA
+// cores (where grads_small: fp32, and small bf16 products), with a second that
+// adds the runs where the rows are cut into several; splits, parts: as
+// grad_splits and grad_scratch (below) say.
+bool grads_small(const GradProduct *p, int count);
+int grad_splits_simt(const GradProduct *p, int count);
+cudaError_t launch_grad_simt(const GradProduct *p, int count, int splits, float *parts, int *status,
+                             cudaStream_t s);
 // The same on tensor cores (bf16; SM pairs).
 bool gemm_grad_supported(const GradProduct &p);
 // Runs that the segments' rows are cut into where the problems are too few to

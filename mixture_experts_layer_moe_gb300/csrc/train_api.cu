@@ -128,13 +128,13 @@ bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
 // rows, d = d_ff = 256 17, 25 / 20, 41;  400 rows, d 256, d_ff 384, 8 experts 31,
 // 49 / 18, 35;  16 rows, d = d_ff = 512, 4 experts 28, 48 / 17, 33.
 bool small_product(int64_t macs, int reduction) {
-  return macs <= (int64_t)1 << 24 && reduction <= 256;
+  return macs <= kSmallProducts && reduction <= 256;
 }
 
 // bf16 rows run on the tensor cores (SM pairs), fp32 rows on the CUDA cores.
 // parts: rows_scratch(p) bytes.
 cudaError_t launch_rows(const RowsProduct &p, float *parts, int *status, cudaStream_t s) {
-  if (p.dtype == MOE_F32 || (p.offsets && small_product((int64_t)p.rows * p.N * p.K, p.K)))
+  if (p.dtype == MOE_F32 || small_product((int64_t)p.rows * p.N * p.K, p.K))
     return launch_rows_simt(p, status, s);
   if (gemm_router_rows_supported(p)) return launch_gemm_router_rows(p, status, s);
   constexpr int epi[] = {0, 1, kEpiSwigluKeep, kEpiReluGrad, kEpiSwigluGrad};   // by kRows*
@@ -171,12 +171,7 @@ cudaError_t launch_rows(const RowsProduct &p, float *parts, int *status, cudaStr
 cudaError_t launch_grads(const GradProduct *p, int count, int splits, float *parts, int *status,
                          cudaStream_t s) {
   if (count == 0) return cudaSuccess;
-  bool small = true;
-  for (int i = 0; i < count; ++i)
-    small = small && p[i].offsets &&
-            small_product((int64_t)p[i].rows * p[i].M * p[i].N, p[i].rows / p[i].num_experts) &&
-            (int64_t)p[i].num_experts * p[i].M * p[i].N <= 1 << 19;   // (else storing it is the work)
-  if (p[0].dtype == MOE_F32 || small) return launch_grad_simt(p, count, status, s);
+  if (grads_small(p, count)) return launch_grad_simt(p, count, splits, parts, status, s);
   for (int i = 0; i < count; ++i)
     if (!gemm_grad_supported(p[i])) return cudaErrorNotSupported;
   return launch_gemm_grad(p, count, splits, parts, status, s);
@@ -415,8 +410,9 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
     r.lda = pitch;
     r.A = dl;
     r.B = w->Wg;
-    // (fp32: the sum of the expert rows in the product's epilogue)
-    const bool fused = c.act_dtype == MOE_F32;
+    // (on the CUDA cores: the sum of the expert rows in the product's epilogue)
+    const bool fused = c.act_dtype == MOE_F32 ||
+                       small_product((int64_t)c.n * c.n_experts * c.d, c.n_experts);
     if (fused && dx_perm) {
       r.add = dx_perm;
       r.add_inv = inv_perm;

@@ -327,7 +327,9 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
 }
 
 // Problems over the same segments share a launch: CTA blockIdx.x takes a tile
-// of an expert's gradients, blockIdx.y the expert.
+// of an expert's gradients, blockIdx.y the expert, blockIdx.z a run of the
+// segment's rows where these are cut (the outputs are then partial sums, the
+// runs' matrices of an expert one after the other).
 struct GradSet {
   GradProduct p[kMaxGradProblems];
   int first[kMaxGradProblems + 1];   // an expert's tiles before problem i
@@ -347,10 +349,15 @@ grad_simt_kernel(const __grid_constant__ GradSet set, int *status) {
   const int M = p.M, N = p.N, e = blockIdx.y;
   const int tile = blockIdx.x - set.first[which], across = (N + TILE - 1) / TILE;
   const int m0 = tile / across * TILE, n0 = tile % across * TILE;
-  const int beg = p.offsets ? p.offsets[e] : 0, end = p.offsets ? p.offsets[e + 1] : p.rows;
+  int beg = p.offsets ? p.offsets[e] : 0, end = p.offsets ? p.offsets[e + 1] : p.rows;
   if (beg < 0 || end < beg || end > p.rows) {
     if (threadIdx.x == 0) set_status(status, MOE_ERR_BAD_INDEX, e);
     return;
+  }
+  if (gridDim.z > 1) {
+    const int run = (end - beg + (int)gridDim.z - 1) / (int)gridDim.z;
+    beg = min(end, beg + (int)blockIdx.z * run);
+    end = min(end, beg + run);
   }
   const int64_t lda = p.lda ? p.lda : M;
   const Place<TILE> me;
@@ -377,7 +384,41 @@ grad_simt_kernel(const __grid_constant__ GradSet set, int *status) {
   for (int i = 0; i < Place<TILE>::ROWS; ++i) {
     const int m = m0 + me.row + i;
     const float v[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
-    if (m < M) put4<T>(p.out, ((int64_t)e * M + m) * N + c, v);
+    if (m >= M) continue;
+    const int64_t at = (((int64_t)e * gridDim.z + blockIdx.z) * M + m) * N + c;
+    if (gridDim.z > 1) put4<float>(p.out, at, v);   // partial sums
+    else put4<T>(p.out, at, v);
+  }
+}
+
+// out[i] = sum over the runs of part[run][i], in order.
+struct GradSum {
+  const float *part[kMaxGradProblems];
+  void *out[kMaxGradProblems];
+  int64_t per_expert[kMaxGradProblems];   // M * N (a multiple of 4)
+  int experts, splits;
+  int *status;
+};
+template <typename T>
+__global__ void __launch_bounds__(256) simt_sum_kernel(GradSum a) {
+  pdl_wait();
+  if (status_failed(a.status)) return;
+  const int p = blockIdx.y;
+  const int64_t per = a.per_expert[p], total = per * a.experts;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < total;
+       i += (int64_t)gridDim.x * 1024) {
+    const int64_t e = i / per;
+    const float *src = a.part[p] + e * a.splits * per + (i - e * per);
+    float x[4] = {};
+#pragma unroll 8
+    for (int s = 0; s < a.splits; ++s) {
+      const float4 u = load4(src + s * per);
+      x[0] += u.x;
+      x[1] += u.y;
+      x[2] += u.z;
+      x[3] += u.w;
+    }
+    put4<T>(a.out[p], i, x);
   }
 }
 
@@ -406,7 +447,41 @@ cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s) 
              : launch_rows<float, 32>(p, status, s);
 }
 
-cudaError_t launch_grad_simt(const GradProduct *p, int count, int *status, cudaStream_t s) {
+// bf16 gradients take the pair kernel where it is the faster.  CUDA cores / pair
+// kernel, a backward pass in us.  Of a router: 53 rows, d 80, 3 experts 7 / 10;
+// 2048 rows, d 256, 32 experts 14 / 16; 16384 rows, d 128, 8 experts 40 / 40.  Of
+// expert FFNs: 1024 rows of 8 experts, d = d_ff = 128 23 / 35; at d = d_ff = 64, 2000
+// rows of 2 18 / 17, 4000 of one 23 / 20.
+bool grads_small(const GradProduct *p, int count) {
+  if (count == 0 || p[0].dtype == MOE_F32) return true;
+  const int E = p[0].offsets ? p[0].num_experts : 1;
+  if (p[0].offsets && p[0].rows / E > 256) return false;
+  for (int i = 0; i < count; ++i)
+    if ((int64_t)p[i].rows * p[i].M * p[i].N > kSmallProducts ||
+        (int64_t)E * p[i].M * p[i].N > 1 << 19)   // (else storing it is the work)
+      return false;
+  return true;
+}
+
+// Tiles that leave most SMs without work have their rows cut into runs of 256
+// at least, with partial sums and a launch that adds them in order.  Whole / cut,
+// a backward pass in us, fp32: a router of 2048 rows, d 16, 180 experts 34 / 19;
+// of 16384 rows, d 128, 8 experts 185 / 38; FFNs with d = d_ff = 64, 4000 rows of
+// one expert 50 / 23.  Runs of 128 lost the added launch: 256 rows, d 128, 4
+// experts 12.5 / 15.6.
+int grad_splits_simt(const GradProduct *p, int count) {
+  if (count == 0) return 1;
+  const int E = p[0].offsets ? p[0].num_experts : 1;
+  int64_t tiles = 0;
+  for (int i = 0; i < count; ++i)
+    tiles += (int64_t)E * ((p[i].N + 31) / 32) * ((p[i].M + 31) / 32);
+  const int64_t most = 152 / tiles, by_rows = p[0].rows / E / 256;
+  const int64_t n = most < by_rows ? most : by_rows;
+  return n < 2 ? 1 : (int)n;
+}
+
+cudaError_t launch_grad_simt(const GradProduct *p, int count, int splits, float *parts, int *status,
+                             cudaStream_t s) {
   const int E = p[0].offsets ? p[0].num_experts : 1;
   GradSet set{};
   auto lay = [&](int tile) {
@@ -418,11 +493,31 @@ cudaError_t launch_grad_simt(const GradProduct *p, int count, int *status, cudaS
     return set.first[count];
   };
   const bool bf16 = p[0].dtype == MOE_BF16, large = !bf16 && large_tiles((int64_t)lay(64) * E);
-  const dim3 grid(lay(large ? 64 : 32), E);
+  const dim3 grid(lay(large ? 64 : 32), E, splits);
+  GradSum sum{};
+  int64_t most = 0;
+  if (splits > 1) {
+    for (int i = 0; i < count; ++i) {
+      const int64_t per = (int64_t)p[i].M * p[i].N;
+      sum.part[i] = parts;
+      sum.out[i] = p[i].out;
+      sum.per_expert[i] = per;
+      set.p[i].out = parts;
+      parts += per * E * splits;
+      if (per * E > most) most = per * E;
+    }
+    sum.experts = E;
+    sum.splits = splits;
+    sum.status = status;
+  }
   auto with = bf16    ? grad_simt_kernel<__nv_bfloat16, 32>
               : large ? grad_simt_kernel<float, 64>
                       : grad_simt_kernel<float, 32>;
-  return launch_pdl(with, grid, dim3(T_THREADS), 0, s, set, status);
+  const cudaError_t e = launch_pdl(with, grid, dim3(T_THREADS), 0, s, set, status);
+  if (e != cudaSuccess || splits == 1) return e;
+  const int64_t blocks = (most / 4 + 255) / 256;
+  return launch_pdl(bf16 ? simt_sum_kernel<__nv_bfloat16> : simt_sum_kernel<float>,
+                    dim3((unsigned)(blocks < 608 ? blocks : 608), count), dim3(256), 0, s, sum);
 }
 
 }  // namespace moe

@@ -217,6 +217,9 @@ FFN_CASES = [
     (256, 128, 512, 4, 1, "f32", "relu", "even"),
     (83, 36, 100, 7, 2, "f32", "swiglu", "even"),
     (sum(TAILS), 68, 132, len(TAILS), 1, "f32", "swiglu", TAILS),
+    (1400, 36, 68, 2, 1, "f32", "swiglu", [1399, 1]),
+    (700, 68, 36, 1, 1, "f32", "relu", "even"),
+    (1027, 36, 24, 1, 1, "f32", "swiglu", "even"),
 ]
 
 
