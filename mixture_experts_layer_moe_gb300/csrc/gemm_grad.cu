@@ -83,6 +83,7 @@ struct GArgs {
   int first[kMaxGradProblems + 1];   // an expert's tiles before problem i
   int width;                         // output columns per tile
   int splits;                        // runs of rows per segment
+  int beside;                        // 1: the next kernel runs beside this one
   int *status;
 };
 struct GMaps {
@@ -167,6 +168,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
   // (all above ran beside the end of the kernel before; from here on its
   // results are read)
   pdl_wait();
+  if (args.beside) pdl_launch_dependents();
   if (threadIdx.x == 0) {
     sh.failed_on_entry = status_failed(args.status) ? 1 : 0;
     sh.abort = sh.failed_on_entry;
@@ -475,7 +477,7 @@ cudaError_t launch(const GMaps &maps, const GArgs &a, cudaStream_t s) {
       pairs = num_sms() / 2;
     }
   }
-  cfg.gridDim = dim3(2 * pairs);
+  cfg.gridDim = dim3(2 * (a.beside ? a.beside : pairs));
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
@@ -533,7 +535,7 @@ size_t grad_scratch(const GradProduct *p, int count) {
 }
 
 cudaError_t launch_gemm_grad(const GradProduct *p, int count, int splits, float *scratch,
-                             int *status, cudaStream_t s) {
+                             int beside, int *status, cudaStream_t s) {
   GMaps maps{};
   GArgs a{};
   a.offsets = p[0].offsets;
@@ -542,6 +544,7 @@ cudaError_t launch_gemm_grad(const GradProduct *p, int count, int splits, float 
   a.problems = count;
   a.status = status;
   a.splits = splits;
+  a.beside = beside;
   a.width = width_of(p, count, splits);
   const int E = p[0].offsets ? p[0].num_experts : 1;
   const uint32_t box[2] = {64, GK}, box_out[3] = {splits > 1 ? 32u : 64u, 32, 1};

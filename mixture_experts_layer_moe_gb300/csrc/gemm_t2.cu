@@ -127,6 +127,9 @@ struct PArgs {
   // the reduction, for one or two weight matrices
   float *parts;
   int splits, mats;
+  // 1: runs beside the kernel before, whose results it does not read (that
+  // kernel lets it start once all before are complete), and ends after it
+  int beside;
 };
 
 // Tensor maps of the token rows (whole boxes, and the short ones for blocks of
@@ -269,7 +272,7 @@ gemm_t2_kernel(const __grid_constant__ PMaps maps, const PArgs args) {
   }
   // (all above ran beside the end of the kernel before; from here on its
   // results are read)
-  pdl_wait();
+  if (!WROWS || !args.beside) pdl_wait();
   if (threadIdx.x == 0) {
     sh.failed_on_entry = status_failed(args.status) ? 1 : 0;
     sh.abort = sh.failed_on_entry;
@@ -568,6 +571,7 @@ gemm_t2_kernel(const __grid_constant__ PMaps maps, const PArgs args) {
   }
   if (threadIdx.x == 0 && sh.abort && !sh.failed_on_entry)
     set_status(args.status, MOE_ERR_TIMEOUT, blockIdx.x);
+  if (WROWS && args.beside) pdl_wait();
 }
 
 int pairs_resident(const void *kernel, int threads, size_t smem) {
@@ -642,12 +646,13 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
   a.parts = g.parts;
   a.splits = g.splits;
   a.mats = g.mats;
+  a.beside = g.beside;
   // token blocks outer when an average segment holds more rows than the
   // weights it meets (the shared expert's one segment of all n tokens)
   const long seg_rows = (long)g.rows / (E > 0 ? E : 1);
   a.tok_major = seg_rows > (long)g.N * (GATED ? 2 : 1) ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pairs);
+  cfg.gridDim = dim3(2 * (g.beside ? g.beside : pairs));
   cfg.blockDim = dim3(pair_threads<EPI>());
   cfg.dynamicSmemBytes = P_DYN_SMEM;
   cfg.stream = s;
@@ -663,7 +668,7 @@ cudaError_t launch_t2(const GemmStage &g, int *status, cudaStream_t s) {
   // against 22.6 us for 200 tokens, 62.0 against 67.5 for 1024 x 2 of 16
   // experts, d 1024, d_ff 2048); the gradients' measured slower so (150.4
   // against 154.2 us for the latter's backward)
-  cfg.numAttrs = WROWS ? 1 : 2;
+  cfg.numAttrs = WROWS && !g.beside ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, gemm_t2_kernel<EPI, WROWS>, m, a);
 }
 

@@ -133,6 +133,7 @@ struct GemmStage {
   // = 2) over each of `splits` ranges of the reduction, fp32
   float *parts;
   int splits, mats;
+  int beside;            // w_rows: runs beside the kernel before (see launch_gemm_grad)
 };
 constexpr int kEpiSwigluKeep = 5, kEpiReluGrad = 6, kEpiSwigluGrad = 7, kEpiPartial = 8;
 cudaError_t launch_gemm_simt(const GemmStage &g, int *status, cudaStream_t s);

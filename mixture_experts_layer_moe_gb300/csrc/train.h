@@ -69,6 +69,7 @@ struct RowsProduct {
   const void *add;             // [rows * add_k][N] or nullptr
   const int32_t *add_inv;
   int add_k;
+  int beside;                  // see launch_gemm_grad
 };
 // fp32, and small bf16 products: at most so many multiplications each.
 constexpr int64_t kSmallProducts = 1 << 24;
@@ -109,8 +110,11 @@ bool gemm_grad_supported(const GradProduct &p);
 // go by the shapes alone.
 int grad_splits(const GradProduct *p, int count);
 size_t grad_scratch(const GradProduct *p, int count);
+// beside: 0, or the SM pairs that it takes so that the next launch, a b_rows
+// RowsProduct with `beside` pairs of its own that does not read its results,
+// runs at the same time.
 cudaError_t launch_gemm_grad(const GradProduct *p, int count, int splits, float *scratch,
-                             int *status, cudaStream_t s);
+                             int beside, int *status, cudaStream_t s);
 // A RowsProduct of one segment with a short reduction, on the same kernel.
 bool gemm_router_rows_supported(const RowsProduct &p);
 cudaError_t launch_gemm_router_rows(const RowsProduct &p, int *status, cudaStream_t s);

@@ -131,11 +131,14 @@ bool small_product(int64_t macs, int reduction) {
   return macs <= kSmallProducts && reduction <= 256;
 }
 
+bool on_cuda_cores(const RowsProduct &p) {
+  return p.dtype == MOE_F32 || small_product((int64_t)p.rows * p.N * p.K, p.K);
+}
+
 // bf16 rows run on the tensor cores (SM pairs), fp32 rows on the CUDA cores.
 // parts: rows_scratch(p) bytes.
 cudaError_t launch_rows(const RowsProduct &p, float *parts, int *status, cudaStream_t s) {
-  if (p.dtype == MOE_F32 || small_product((int64_t)p.rows * p.N * p.K, p.K))
-    return launch_rows_simt(p, status, s);
+  if (on_cuda_cores(p)) return launch_rows_simt(p, status, s);
   if (gemm_router_rows_supported(p)) return launch_gemm_router_rows(p, status, s);
   constexpr int epi[] = {0, 1, kEpiSwigluKeep, kEpiReluGrad, kEpiSwigluGrad};   // by kRows*
   GemmStage g{};
@@ -158,6 +161,7 @@ cudaError_t launch_rows(const RowsProduct &p, float *parts, int *status, cudaStr
   g.kept_g = p.g;
   g.kept_u = p.u;
   g.kept_h = p.h;
+  g.beside = p.beside;
   if (!gemm_t2_supported(g)) return cudaErrorNotSupported;
   const int splits = rows_splits(p);
   return splits > 1 ? launch_rows_split(p, g, splits, parts, status, s)
@@ -168,13 +172,31 @@ cudaError_t launch_rows(const RowsProduct &p, float *parts, int *status, cudaStr
 // grad_splits and grad_scratch of all the layer's problems say, whichever of
 // them are wanted (so that a gradient has the same bits alone and with the
 // others).
-cudaError_t launch_grads(const GradProduct *p, int count, int splits, float *parts, int *status,
-                         cudaStream_t s) {
+cudaError_t launch_grads(const GradProduct *p, int count, int splits, float *parts, int beside,
+                         int *status, cudaStream_t s) {
   if (count == 0) return cudaSuccess;
   if (grads_small(p, count)) return launch_grad_simt(p, count, splits, parts, status, s);
   for (int i = 0; i < count; ++i)
     if (!gemm_grad_supported(p[i])) return cudaErrorNotSupported;
-  return launch_gemm_grad(p, count, splits, parts, status, s);
+  return launch_gemm_grad(p, count, splits, parts, beside, status, s);
+}
+
+// Whether the backward of the expert FFNs runs its launches in two pairs, dW2
+// with dg and du, then dW1 and dW3 with dx, each launch on a share of the SMs.  With few
+// rows per expert the one of a pair writes matrices and the other reads them:
+// together HBM moves both ways, and the two share one ramp and one tail.
+// A pass in us, one after the other / in pairs (46 SM pairs write, 30 read):
+//   18 rows of 32 experts (d 7168, d_ff 2048) 1109 / 1043, 32 of 32 (2880, 2880)
+//   712 / 647, 64 of 128 (2048, 768) 563 / 505, 128 of 16 (1024, 2048) 142 / 131,
+//   128 of 8 (4096, 14336) 1200 / 1190;  with 256 rows 1443 / 1462 and 724 / 770
+//   of the first and third, with 1024 4141 / 4410 of the first.
+// (The first with 38 pairs each 1246, with 43 and 33 1111.)
+bool side_by_side(const moe_config &c, int splits, const RowsProduct &r, const RowsProduct &x) {
+  GradProduct p[3];
+  expert_grads_of(c, r.offsets, p);
+  return c.act_dtype == MOE_BF16 && splits == 1 && !grads_small(p, expert_problems(c)) &&
+         !on_cuda_cores(r) && !on_cuda_cores(x) && rows_splits(r) == 1 && rows_splits(x) == 1 &&
+         r.rows <= 128 * (int64_t)c.n_experts;
 }
 
 moe_status check_norm(const moe_norm_config *c) {
@@ -319,7 +341,7 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
     ++n_gw;
   }
   if (!dx_perm && !grads->W1 && !grads->W3)
-    return cuda_status(launch_grads(gw, n_gw, splits, parts, status, s));
+    return cuda_status(launch_grads(gw, n_gw, splits, parts, 0, status, s));
   RowsProduct r = rows_of(c, kGateGrad);
   r.offsets = offsets;
   r.A = dy_perm;
@@ -329,19 +351,27 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   r.h = h;
   r.out = dg;
   r.out_u = gated ? du : nullptr;
-  MOE_TRY(cuda_status(launch_rows(r, parts, status, s)));
-  MOE_TRY(cuda_status(launch_grads(gw, n_gw, splits, parts, status, s)));
-  if (dx_perm) {
-    RowsProduct x = rows_of(c, kInputGrad);
-    x.offsets = offsets;
-    x.A = dg;
-    x.B = w->W1;
-    x.A2 = gated ? du : nullptr;
-    x.B2 = w->W3;
-    x.out = dx_perm;
-    MOE_TRY(cuda_status(launch_rows(x, parts, status, s)));
+  RowsProduct x = rows_of(c, kInputGrad);
+  x.offsets = offsets;
+  x.A = dg;
+  x.B = w->W1;
+  x.A2 = gated ? du : nullptr;
+  x.B2 = w->W3;
+  x.out = dx_perm;
+  // SM pairs that write gradients while the others read weights (0: each launch
+  // has them all)
+  const int all_pairs = num_sms() / 2;
+  const int writing = side_by_side(c, splits, r, x) ? (3 * all_pairs + 4) / 5 : 0;
+  const int first = writing && grads->W2 ? 1 : 0, rest = n_gw - first;
+  if (first) {
+    r.beside = all_pairs - writing;
+    MOE_TRY(cuda_status(launch_grads(gw, 1, splits, parts, writing, status, s)));
   }
-  return MOE_OK;
+  MOE_TRY(cuda_status(launch_rows(r, parts, status, s)));
+  const bool both = writing && dx_perm && rest;
+  if (both) x.beside = all_pairs - writing;
+  MOE_TRY(cuda_status(launch_grads(gw + first, rest, splits, parts, both ? writing : 0, status, s)));
+  return dx_perm ? cuda_status(launch_rows(x, parts, status, s)) : MOE_OK;
 }
 
 moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const void *y_perm,
@@ -393,7 +423,7 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
     gw.B = x;
     gw.out = dWg;
     MOE_TRY(cuda_status(launch_grads(&gw, 1, grad_splits(&gw, 1), at<float>(ws, L.parts),
-                                     status, s)));
+                                     0, status, s)));
   }
   if (rows) {
     MOE_TRY(cuda_status(launch_route_rows(c, w->Wg, topk_idx, topk_gate, dgate, inv_perm, dx_perm,

@@ -189,6 +189,7 @@ def _counts(P, E, how, seed):
 
 EDGES = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 0, 255, 256, 257, 300]
 TAILS = [2, 31, 0, 33, 66, 95, 7, 198]
+MANY = [0, 1, 300, 17, 20] * 8
 
 # n, d, F, E, k, dtype, act, counts
 FFN_CASES = [
@@ -213,6 +214,9 @@ FFN_CASES = [
     (33, 2104, 72, 2, 1, "bf16", "swiglu", [0, 33]),
     (300, 136, 1096, 1, 1, "bf16", "relu", "even"),
     (7, 1096, 136, 1, 1, "bf16", "relu", "even"),
+    # few rows per expert and many tiles: weight gradients beside the row products
+    (sum(MANY), 264, 520, len(MANY), 1, "bf16", "swiglu", MANY),
+    (450, 520, 264, 40, 2, "bf16", "relu", "even"),
     (1, 4, 4, 1, 1, "f32", "swiglu", "even"),
     (256, 128, 512, 4, 1, "f32", "relu", "even"),
     (83, 36, 100, 7, 2, "f32", "swiglu", "even"),
@@ -627,6 +631,73 @@ def test_gradients_against_differences(lib):
         assert torch.equal(i1, idx0) and torch.equal(i2, idx0)   # (the loss is smooth in between)
         want = (gr[key].double() * v.double()).sum().item()
         assert abs((up - down) / (2 * e) - want) <= 2e-2 * abs(want), key
+
+
+@pytest.mark.parametrize("wanted", ["W1 W3 W2 dx", "W3 dx", "W2 dx", "W2 W1"])
+def test_ffn_backward_side_by_side_again_and_again(lib, wanted):
+    """Launches that run at the same time, back to back without a wait, followed at once by
+    work that overwrites their inputs: the bits of a run with a wait after each call."""
+    s = _ffn_inputs((sum(MANY), 264, 520, len(MANY), 1, "bf16", "swiglu", MANY), 5)
+    ws = lib.alloc_train_workspace(s["cfg"])
+    g, u, h, _y = _train(lib, s, ws)
+    gr = {key: t if key in wanted else None for key, t in _grads(s).items()}
+    dx = _empty(s, 264) if "dx" in wanted else None
+    x2, dy2 = s["x"].flip(0).contiguous(), s["dy"].flip(0).contiguous()
+    x, dy = s["x"].clone(), s["dy"].clone()
+    w = lib.make_weights(s)
+
+    def back():
+        lib.moe_expert_ffn_backward(s["cfg"], x, s["offsets"], w, g, u, h, dy, dx,
+                                    lib.make_expert_grads(gr), ws)
+        return [t.clone() for t in (dx, *gr.values()) if t is not None]
+
+    want = []
+    for a, b in ((s["x"], s["dy"]), (x2, dy2)):
+        x.copy_(a), dy.copy_(b)
+        torch.cuda.synchronize()
+        want.append(back())
+        _ok(lib, ws)
+    got = []
+    for i in range(10):
+        x.copy_((s["x"], x2)[i % 2]), dy.copy_((s["dy"], dy2)[i % 2])
+        got.append(back())
+    _ok(lib, ws)
+    for i, ts in enumerate(got):
+        for a, b in zip(ts, want[i % 2]):
+            assert torch.equal(a, b), i
+
+
+def test_ffn_backward_side_by_side_in_a_graph(lib):
+    s = _ffn_inputs((sum(MANY), 264, 520, len(MANY), 1, "bf16", "swiglu", MANY), 6)
+    ws = lib.alloc_train_workspace(s["cfg"])
+    g, u, h, _y = _train(lib, s, ws)
+    dx, gr, w = _empty(s, 264), _grads(s), lib.make_weights(s)
+    outs = (dx, *gr.values())
+
+    def back(stream=None):
+        lib.moe_expert_ffn_backward(s["cfg"], s["x"], s["offsets"], w, g, u, h, s["dy"], dx,
+                                    lib.make_expert_grads(gr), ws, stream=stream)
+
+    back()
+    _ok(lib, ws)
+    want = [t.clone() for t in outs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            back(side)
+            kept = [t.clone() for t in outs]        # (reads the results inside the graph)
+            for t in outs:
+                t.fill_(0)
+    for _ in range(3):
+        for t in kept:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(kept, want):
+            assert torch.equal(a, b)
+    _ok(lib, ws)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
