@@ -12,6 +12,11 @@
 // d_ff 1024), and shared memory is double buffered, so a step waits for memory
 // once, not twice (256 rows, d 128, d_ff
 // 512, 4 experts, forward: 49 us without any of it, 15.6 with).
+// Large layers are bound by reading the operands from shared memory (4096 rows of
+// 16 experts, d 512, d_ff 1024: its wavefronts at 82-92 % of their peak, the FMA pipe
+// at 45-54 %; 36 TFLOP/s).  8 x 8 outputs per thread read half as often (FMA 51-64
+// %) but need the tile's sums joined from groups of threads: 1 to 18 % less
+// time there, up to 18 % more for the short reductions of a router.
 // The three storage orders of the operands differ in how a tile is staged
 // only: in shared memory both operands lie reduction index first, so that a
 // thread reads its values of a step as two vectors.
@@ -400,7 +405,7 @@ struct GradSum {
   int *status;
 };
 template <typename T>
-__global__ void __launch_bounds__(256) simt_sum_kernel(GradSum a) {
+__global__ void __launch_bounds__(256) simt_sum_kernel(const __grid_constant__ GradSum a) {
   pdl_wait();
   if (status_failed(a.status)) return;
   const int p = blockIdx.y;
