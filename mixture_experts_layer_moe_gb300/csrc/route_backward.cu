@@ -224,8 +224,8 @@ size_t route_grad_scratch(const moe_config &c) { return (size_t)grid_of(c.n) * c
 
 cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int32_t *topk_idx,
                               const float *gates, const float *dgate, const float *f, float aux,
-                              void *dl, int pitch, float *dbias, float *scratch, int *status,
-                              cudaStream_t s) {
+                              void *dl, bool dl_f32, int pitch, float *dbias, float *scratch,
+                              int *status, cudaStream_t s) {
   const int grid = grid_of(c.n), E = c.n_experts;
   const int renorm = c.gate == MOE_GATE_RENORM;
   const float scale = aux * (float)E / (float)c.n;
@@ -233,7 +233,7 @@ cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int
   float *parts = dbias == nullptr ? nullptr : grid == 1 ? dbias : scratch;
   const dim3 blocks(grid), threads(32 * RB_WARPS);
   cudaError_t e;
-  if (c.act_dtype == MOE_F32)
+  if (dl_f32)
     e = launch_pdl(route_grad_kernel<float>, blocks, threads, 0, s, probs, topk_idx, gates, dgate, f,
                    scale, renorm, c.n, E, c.top_k, (float *)dl, pitch, parts, status);
   else

@@ -27,13 +27,13 @@ cudaError_t launch_combine_backward(int dtype, const void *dy, const void *y_per
                                     float *dgate, int n, int k, int d, int *status,
                                     cudaStream_t s);
 
-// dl [n][pitch] (dtype; columns E .. pitch - 1 zero) and, when dbias is set,
+// dl [n][pitch] (dl_f32: fp32, else bf16; columns E .. pitch - 1 zero) and, when dbias is set,
 // the column sums, through route_grad_scratch(c) bytes of scratch.
 // dl may be nullptr (dbias alone).
 size_t route_grad_scratch(const moe_config &c);
 cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int32_t *topk_idx,
                               const float *gates, const float *dgate, const float *f, float aux,
-                              void *dl, int pitch, float *dbias, float *scratch, int *status,
+                              void *dl, bool dl_f32, int pitch, float *dbias, float *scratch, int *status,
                               cudaStream_t s);
 
 // dx from the expert rows' gradients and the router's in one pass, where dl has
@@ -70,6 +70,9 @@ struct RowsProduct {
   const int32_t *add_inv;
   int add_k;
   int beside;                  // see launch_gemm_grad
+  // On the CUDA cores, for a bf16 layer: A and A2, or out and out_u of a
+  // gradient, are fp32
+  int a_f32, out_f32;
 };
 // fp32, and small bf16 products: at most so many multiplications each.
 constexpr int64_t kSmallProducts = 1 << 24;
@@ -93,6 +96,7 @@ struct GradProduct {
   int lda;                  // elements from one row of A to the next (0: M)
   const void *A, *B;
   void *out;                // [E][M][N]
+  int a_f32;                // on the CUDA cores, for a bf16 layer: A is fp32
 };
 constexpr int kMaxGradProblems = 3;
 // Up to kMaxGradProblems of them over the same segments in one launch on the CUDA

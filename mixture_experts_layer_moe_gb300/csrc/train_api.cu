@@ -18,6 +18,21 @@ struct TrainLayout {
 // dl's rows are padded to whole 16-byte vectors of bf16.
 int dl_pitch(const moe_config &c) { return (c.n_experts + 7) / 8 * 8; }
 
+// Whether a bf16 product is small enough for the CUDA cores: setting up the
+// pair kernels (clusters, tensor memory, tensor maps) takes about 6 us a launch,
+// so a short reduction and few products are faster without.  Forward and
+// gradient in us, CUDA cores / tensor cores: 53 rows, d 80, d_ff 24, 3 experts
+// 9, 10 / 13, 25;  1024 rows, d = d_ff = 128, 8 experts 15, 23 / 19, 35;  256
+// rows, d = d_ff = 256 17, 25 / 20, 41;  400 rows, d 256, d_ff 384, 8 experts 31,
+// 49 / 18, 35;  16 rows, d = d_ff = 512, 4 experts 28, 48 / 17, 33.
+bool small_product(int64_t macs, int reduction) {
+  return macs <= kSmallProducts && reduction <= 256;
+}
+
+bool on_cuda_cores(const RowsProduct &p) {
+  return p.dtype == MOE_F32 || small_product((int64_t)p.rows * p.N * p.K, p.K);
+}
+
 // The weight gradients of the experts and of the router (operands unset).
 void expert_grads_of(const moe_config &c, const int32_t *offsets, GradProduct (&p)[3]) {
   const int M[3] = {c.d, c.d_ff, c.d_ff}, N[3] = {c.d_ff, c.d, c.d};   // W2, W1, W3
@@ -63,6 +78,34 @@ RowsProduct rows_of(const moe_config &c, RowsKind kind) {
   return p;
 }
 int expert_problems(const moe_config &c) { return c.act == MOE_ACT_SWIGLU ? 3 : 2; }
+// The router's share of the rows' gradient, dl Wg (operands unset).
+RowsProduct router_rows_of(const moe_config &c) {
+  RowsProduct r{};
+  r.dtype = c.act_dtype;
+  r.epi = kRowsPlain;
+  r.b_rows = 1;
+  r.num_experts = 1;
+  r.rows = c.n;
+  r.K = c.n_experts;
+  r.N = c.d;
+  r.lda = dl_pitch(c);
+  return r;
+}
+
+// dg and du, or dl, are rounded to bf16 where tensor cores multiply them.  A
+// small layer, whose products all run on the CUDA cores, keeps them in fp32: with
+// few rows that rounding is not averaged out (one token, d 2776, d_ff 104: dW1
+// off by 3.1e-3 of its norm, 1.7e-3 without).
+bool wide_expert_grads(const moe_config &c) {
+  GradProduct p[3];
+  expert_grads_of(c, reinterpret_cast<const int32_t *>(16), p);
+  return grads_small(p, expert_problems(c)) && on_cuda_cores(rows_of(c, kGateGrad)) &&
+         on_cuda_cores(rows_of(c, kInputGrad));
+}
+bool wide_router_grads(const moe_config &c) {
+  const GradProduct p = router_grad_of(c);
+  return grads_small(&p, 1) && on_cuda_cores(router_rows_of(c));
+}
 
 TrainLayout train_layout_of(const moe_config &c) {
   moe_config c1 = c;
@@ -71,7 +114,6 @@ TrainLayout train_layout_of(const moe_config &c) {
   const size_t P = (size_t)c.n * c.top_k, z = act_size(c);
   TrainLayout L{};
   L.status = base.status;
-  L.dg = base.h;              // [P][d_ff]
   L.dx_router = base.x_perm;  // [n][d]
   size_t off = layout_of(c).total;
   auto take = [&](size_t bytes) {
@@ -79,8 +121,10 @@ TrainLayout train_layout_of(const moe_config &c) {
     off += align_up(bytes);
     return a;
   };
-  L.du = take(P * c.d_ff * z);
-  L.dl = take((size_t)c.n * dl_pitch(c) * z);
+  const bool wide = wide_expert_grads(c);   // (fp32 dg and du)
+  L.dg = wide && z < 4 ? take(P * c.d_ff * 4) : base.h;   // [P][d_ff]
+  L.du = take(P * c.d_ff * (wide ? 4 : z));
+  L.dl = take((size_t)c.n * dl_pitch(c) * (wide_router_grads(c) ? 4 : z));
   L.bias_parts = take(route_grad_scratch(c));
   GradProduct experts[3];
   expert_grads_of(c, reinterpret_cast<const int32_t *>(16), experts);   // (shapes alone)
@@ -119,21 +163,6 @@ moe_status check_routed_weights(const moe_config &c, const moe_weights *w) {
 }
 
 bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
-
-// Whether a bf16 product is small enough for the CUDA cores: setting up the
-// pair kernels (clusters, tensor memory, tensor maps) takes about 6 us a launch,
-// so a short reduction and few products are faster without.  Forward and
-// gradient in us, CUDA cores / tensor cores: 53 rows, d 80, d_ff 24, 3 experts
-// 9, 10 / 13, 25;  1024 rows, d = d_ff = 128, 8 experts 15, 23 / 19, 35;  256
-// rows, d = d_ff = 256 17, 25 / 20, 41;  400 rows, d 256, d_ff 384, 8 experts 31,
-// 49 / 18, 35;  16 rows, d = d_ff = 512, 4 experts 28, 48 / 17, 33.
-bool small_product(int64_t macs, int reduction) {
-  return macs <= kSmallProducts && reduction <= 256;
-}
-
-bool on_cuda_cores(const RowsProduct &p) {
-  return p.dtype == MOE_F32 || small_product((int64_t)p.rows * p.N * p.K, p.K);
-}
 
 // bf16 rows run on the tensor cores (SM pairs), fp32 rows on the CUDA cores.
 // parts: rows_scratch(p) bytes.
@@ -330,6 +359,7 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   const int splits = grad_splits(all, expert_problems(c));
   float *parts = at<float>(ws, L.parts);
   const void *left[3] = {dy_perm, dg, du}, *right[3] = {h, x_perm, x_perm};
+  const int wide = c.act_dtype == MOE_BF16 && wide_expert_grads(c);
   void *out[3] = {grads->W2, grads->W1, grads->W3};
   int n_gw = 0;
   for (int i = 0; i < 3; ++i) {
@@ -338,6 +368,7 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
     gw[n_gw].A = left[i];
     gw[n_gw].B = right[i];
     gw[n_gw].out = out[i];
+    gw[n_gw].a_f32 = i > 0 && wide;
     ++n_gw;
   }
   if (!dx_perm && !grads->W1 && !grads->W3)
@@ -351,6 +382,7 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   r.h = h;
   r.out = dg;
   r.out_u = gated ? du : nullptr;
+  r.out_f32 = wide;
   RowsProduct x = rows_of(c, kInputGrad);
   x.offsets = offsets;
   x.A = dg;
@@ -358,6 +390,7 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
   x.A2 = gated ? du : nullptr;
   x.B2 = w->W3;
   x.out = dx_perm;
+  x.a_f32 = wide;
   // SM pairs that write gradients while the others read weights (0: each launch
   // has them all)
   const int all_pairs = num_sms() / 2;
@@ -412,16 +445,18 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
   int *status = at<int>(ws, L.status);
   cudaStream_t s = as_stream(stream);
   const int pitch = dl_pitch(c);
+  const bool wide = wide_router_grads(c);
   const bool rows = dx && route_rows_supported(c, f);   // dx without dl
   void *dl = (dx && !rows) || dWg ? at<void>(ws, L.dl) : nullptr;
   if (dl || dbias)
-    MOE_TRY(cuda_status(launch_route_grad(c, probs, topk_idx, topk_gate, dgate, f, aux, dl, pitch,
-                                          dbias, at<float>(ws, L.bias_parts), status, s)));
+    MOE_TRY(cuda_status(launch_route_grad(c, probs, topk_idx, topk_gate, dgate, f, aux, dl, wide,
+                                          pitch, dbias, at<float>(ws, L.bias_parts), status, s)));
   if (dWg) {
     GradProduct gw = router_grad_of(c);
     gw.A = dl;
     gw.B = x;
     gw.out = dWg;
+    gw.a_f32 = c.act_dtype == MOE_BF16 && wide;
     MOE_TRY(cuda_status(launch_grads(&gw, 1, grad_splits(&gw, 1), at<float>(ws, L.parts),
                                      0, status, s)));
   }
@@ -429,20 +464,12 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
     MOE_TRY(cuda_status(launch_route_rows(c, w->Wg, topk_idx, topk_gate, dgate, inv_perm, dx_perm,
                                           dx, status, s)));
   } else if (dx) {
-    RowsProduct r{};
-    r.dtype = c.act_dtype;
-    r.epi = kRowsPlain;
-    r.b_rows = 1;
-    r.num_experts = 1;
-    r.rows = c.n;
-    r.K = c.n_experts;
-    r.N = c.d;
-    r.lda = pitch;
+    RowsProduct r = router_rows_of(c);
     r.A = dl;
     r.B = w->Wg;
+    r.a_f32 = c.act_dtype == MOE_BF16 && wide;
     // (on the CUDA cores: the sum of the expert rows in the product's epilogue)
-    const bool fused = c.act_dtype == MOE_F32 ||
-                       small_product((int64_t)c.n * c.n_experts * c.d, c.n_experts);
+    const bool fused = on_cuda_cores(r);
     if (fused && dx_perm) {
       r.add = dx_perm;
       r.add_inv = inv_perm;

@@ -227,7 +227,8 @@ __device__ __forceinline__ void run_steps(int steps, Load &&load, Store &&store,
   }
 }
 
-template <typename T, int EPI, bool B_ROWS, int TILE>
+// T: the layer's type, TA: A's, TO: that of a gradient's outputs.
+template <typename T, int EPI, bool B_ROWS, int TILE, typename TA = T, typename TO = T>
 __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int *status) {
   using G = Geo<TILE>;
   constexpr bool DUAL = EPI == kRowsSwiglu;
@@ -249,7 +250,8 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   // the steps of the one or two operand pairs, one after the other
   const int steps1 = (K + G::TK - 1) / G::TK;
   const int steps = steps1 * (EPI == kRowsPlain && p.A2 ? 2 : 1);
-  Part<T, true, TILE> pa, pb2;
+  Part<TA, true, TILE> pa;
+  Part<T, true, TILE> pb2;
   Part<T, !B_ROWS, TILE> pb;
   // (a row's padding, lda > K, holds zeros and may be read)
   const int ka = p.lda ? p.lda : K;
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
       [&](int step) {
         const bool second = step >= steps1;
         const int k0 = (second ? step - steps1 : step) * G::TK;
-        const T *A = static_cast<const T *>(second ? p.A2 : p.A) + row0 * lda;
+        const TA *A = static_cast<const TA *>(second ? p.A2 : p.A) + row0 * lda;
         const T *B = static_cast<const T *>(second ? p.B2 : p.B) + base;
         pa.load(A + k0, lda, end - row0, ka - k0);
         pb.load(B_ROWS ? B + (int64_t)k0 * N : B + k0, B_ROWS ? N : K, N - n0, K - k0);
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
         du[j] = v[j] * g[j] * s;
         v[j] = v[j] * u[j] * s * (1.f + g[j] * (1.f - s));
       }
-      put4<T>(p.out_u, at, du);
+      put4<TO>(p.out_u, at, du);
     }
     if (EPI == kRowsPlain && p.add) {
       // the sum of this row's add_k other rows
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
         for (int i4 = 0; i4 < 4; ++i4) v[i4] += o[i4];
       }
     }
-    put4<T>(p.out, at, v);
+    put4<TO>(p.out, at, v);
   }
 }
 
@@ -367,20 +369,29 @@ grad_simt_kernel(const __grid_constant__ GradSet set, int *status) {
   const int64_t lda = p.lda ? p.lda : M;
   const Place<TILE> me;
   float2 acc[4][2] = {};
-  const T *A = static_cast<const T *>(p.A) + m0, *B = static_cast<const T *>(p.B) + n0;
-  Part<T, false, TILE> pa, pb;
-  run_steps<2>(
-      (end - beg + G::TK - 1) / G::TK,
-      [&](int step) {
-        const int q = beg + step * G::TK;
-        pa.load(A + q * lda, lda, (int)lda - m0, end - q);
-        pb.load(B + (int64_t)q * N, N, N - n0, end - q);
-      },
-      [&](int buf) {
-        pa.store(as[buf]);
-        pb.store(bs[buf]);
-      },
-      [&](int buf) { tile_fma<TILE>(acc, as[buf], bs[buf], me.tx, me.ty, me.g); });
+  const T *B = static_cast<const T *>(p.B) + n0;
+  auto sum = [&](const auto *A, auto &pa) {
+    Part<T, false, TILE> pb;
+    run_steps<2>(
+        (end - beg + G::TK - 1) / G::TK,
+        [&](int step) {
+          const int q = beg + step * G::TK;
+          pa.load(A + m0 + q * lda, lda, (int)lda - m0, end - q);
+          pb.load(B + (int64_t)q * N, N, N - n0, end - q);
+        },
+        [&](int buf) {
+          pa.store(as[buf]);
+          pb.store(bs[buf]);
+        },
+        [&](int buf) { tile_fma<TILE>(acc, as[buf], bs[buf], me.tx, me.ty, me.g); });
+  };
+  if (sizeof(T) == 4 || p.a_f32) {
+    Part<float, false, TILE> pa;
+    sum(static_cast<const float *>(p.A), pa);
+  } else {
+    Part<T, false, TILE> pa;
+    sum(static_cast<const T *>(p.A), pa);
+  }
   pdl_launch_dependents();
   join_groups<TILE>(acc, &as[0][0][0], me.tx, me.ty, me.g);
   const int c = n0 + me.col;   // (N is a multiple of 4)
@@ -431,6 +442,13 @@ template <typename T, int TILE>
 cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   const int mt = (p.rows + TILE - 1) / TILE + (p.offsets ? p.num_experts : 0);
   const dim3 grid(mt, (p.N + TILE - 1) / TILE);
+  if constexpr (sizeof(T) == 2) {
+    // (fp32 dg, du and dl)
+    auto wide = p.a_f32 ? rows_simt_kernel<T, kRowsPlain, true, TILE, float>
+                : p.epi == kRowsReluGrad ? rows_simt_kernel<T, kRowsReluGrad, true, TILE, T, float>
+                                         : rows_simt_kernel<T, kRowsSwigluGrad, true, TILE, T, float>;
+    if (p.a_f32 || p.out_f32) return launch_pdl(wide, grid, dim3(T_THREADS), 0, s, p, status);
+  }
   auto with = p.epi == kRowsPlain && p.b_rows ? rows_simt_kernel<T, kRowsPlain, true, TILE>
               : p.epi == kRowsPlain           ? rows_simt_kernel<T, kRowsPlain, false, TILE>
               : p.epi == kRowsRelu            ? rows_simt_kernel<T, kRowsRelu, false, TILE>

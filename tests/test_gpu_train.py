@@ -553,6 +553,77 @@ def test_route_backward(lib, n, d, E, k, dtype, gate, aux):
     assert torch.equal(dx, dx3) and torch.equal(dWg, dW3) and torch.equal(db, db3)
 
 
+@pytest.mark.parametrize("n,d,E,k,gate", [(1, 16, 3, 3, "renorm"), (21, 168, 2, 1, "top_prob"),
+                                          (600, 24, 40, 2, "top_prob"), (5, 264, 37, 4, "renorm")])
+def test_route_backward_of_small_bf16_layers_rounds_once(lib, n, d, E, k, gate):
+    """dl stays in fp32 between the launches of a small layer: the only rounding to bf16 is
+    the output's."""
+    cfg = _cfg(n, d, 8, E, k, "bf16", gate=gate)
+    g = _gen(n + E)
+    x, Wg = _randn(g, n, d, dtype="bf16"), _randn(g, E, d, dtype="bf16", std=0.1)
+    probs = torch.softmax(_randn(g, n, E, std=1.5), 1)
+    p, idx = torch.sort(probs, dim=1, descending=True, stable=True)
+    p, idx = p[:, :k].contiguous(), idx[:, :k].to(torch.int32).contiguous()
+    gates = (p / p.sum(1, keepdim=True) if gate == "renorm" else p).contiguous()
+    dgate = _randn(g, n, k)
+    f = torch.full((E,), 1 / E, device="cuda")
+    ws = lib.alloc_train_workspace(cfg)
+    dx, dWg = torch.full_like(x, float("nan")), torch.full_like(Wg, float("nan"))
+    lib.moe_route_backward(cfg, x, lib.make_weights(dict(Wg=Wg)), probs, idx, gates, dgate, f, 0.1,
+                           None, None, dx, dWg, None, ws)
+    _ok(lib, ws)
+    dl = T.logits_backward(gate, probs, idx, gates, dgate, f, 0.1)
+    # (dl's own fp32 error as in test_route_backward)
+    mag = torch.zeros(n, E, dtype=torch.float64)
+    ag, adg, p64 = gates.cpu().double(), dgate.cpu().double().abs(), probs.cpu().double()
+    total = (ag * adg).sum(1, keepdim=True)
+    mag.scatter_(1, idx.cpu().long(), ag * (adg + (total if gate == "renorm" else 0)))
+    if gate != "renorm":
+        mag += p64 * total
+    mag += 0.1 * E / n * p64 * 2 / E
+    el = (k + E + 10) * V * mag
+    aW, ax = Wg.cpu().double().abs(), x.cpu().double().abs()
+    want = dl @ Wg.cpu().double()
+    ex = (el + 2 * E * V * (dl.abs() + el)) @ aW
+    _within(dx, want, ex + _u("bf16") * (want.abs() + ex), "dx")
+    want = dl.T @ x.cpu().double()
+    ew = (el + 2 * n * V * (dl.abs() + el)).T @ ax
+    _within(dWg, want, ew + _u("bf16") * (want.abs() + ew), "dWg")
+
+
+@pytest.mark.parametrize("n,d,F,E,act", [(1, 200, 104, 1, "swiglu"), (14, 200, 24, 3, "swiglu"),
+                                         (7, 24, 248, 4, "relu"), (100, 72, 136, 5, "swiglu")])
+def test_ffn_backward_of_small_bf16_layers_rounds_once(lib, n, d, F, E, act):
+    """dg and du stay in fp32 between the launches of a small layer."""
+    s = _ffn_inputs((n, d, F, E, 1, "bf16", act, "even"), 17)
+    ws = lib.alloc_train_workspace(s["cfg"])
+    g, u, h, _y = _train(lib, s, ws)
+    dx, gr = _empty(s, d), _grads(s)
+    lib.moe_expert_ffn_backward(s["cfg"], s["x"], s["offsets"], lib.make_weights(s), g, u, h,
+                                s["dy"], dx, lib.make_expert_grads(gr), ws)
+    _ok(lib, ws)
+    off = s["offsets"].cpu()
+    wdx, wW1, wW3, _wW2, wdg, wdu = T.ffn_backward(s["x"], off, s["W1"], s["W3"], s["W2"], g, u, h,
+                                                   s["dy"])
+    a = {key: None if t is None else t.cpu().double().abs() for key, t in
+         dict(x=s["x"], dy=s["dy"], W1=s["W1"], W3=s["W3"], W2=s["W2"], g=g, u=u).items()}
+    adh = _seg(lambda e, t: t @ a["W2"][e], off, a["dy"])
+    edg, edu = 2 * d * V * adh, None
+    if act == "swiglu":     # (the factors as in test_ffn_backward)
+        edu = 2 * d * V * adh * a["g"] + 3 * _act("bf16") * adh * a["g"]
+        edg = 1.1 * edg * a["u"] + 3 * _act("bf16") * adh * a["u"]
+    ex = _seg(lambda e, p, q: (p + 4 * F * V * q) @ a["W1"][e], off, edg, wdg.abs() + edg)
+    if act == "swiglu":
+        ex = ex + _seg(lambda e, p, q: (p + 4 * F * V * q) @ a["W3"][e], off, edu, wdu.abs() + edu)
+    _within(dx, wdx, ex + _u("bf16") * (wdx.abs() + ex), "dx")
+    o = off.tolist()
+    for got, want, dv, edv in ((gr["W1"], wW1, wdg, edg), (gr["W3"], wW3, wdu, edu)):
+        if got is not None:
+            b = torch.stack([(edv[p:q] + 2 * (q - p) * V * (dv[p:q].abs() + edv[p:q])).T
+                             @ a["x"][p:q] for p, q in zip(o, o[1:])])
+            _within(got, want, b + _u("bf16") * (want.abs() + b), "dW")
+
+
 def test_route_backward_masked_experts_and_bad_index(lib):
     """An expert that a -inf bias masks (probability 0) has no gradient; a choice outside
     the experts is reported and counts as a gate of zero."""
