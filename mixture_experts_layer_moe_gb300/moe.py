@@ -324,13 +324,20 @@ def _norm_config(rows, ldx, ldy, lddx, lddy, d, dtype, eps):
 
 
 def _norm_rows(t: torch.Tensor, shape, dtype) -> tuple[int, int]:
-    """(pointer, elements from one row to the next) of a [rows, d] tensor whose rows are dense."""
+    """(pointer, elements from one row to the next) of a [rows, d] tensor whose rows are dense.
+
+    Rows that share elements are refused: a row expanded to [rows, d] has a stride of 0, which the
+    library would take for d and so read (or write) past the one row that there is."""
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError("rows of a layer norm must be [rows, d] tensors of one shape and type")
     ld, one = t.stride()
     if one != 1 and shape[1] > 1:
         raise ValueError("rows of a layer norm must be dense")
-    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+    if shape[0] <= 1:
+        return t.data_ptr(), shape[1]
+    if ld < shape[1]:
+        raise ValueError("rows of a layer norm must not overlap (an expanded tensor: .contiguous())")
+    return t.data_ptr(), ld
 
 
 def _norm_vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype) -> Optional[int]:
