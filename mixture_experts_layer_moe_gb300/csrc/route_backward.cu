@@ -132,7 +132,10 @@ route_rows_kernel(const uint4 *__restrict__ dx_perm, const int32_t *__restrict__
   __shared__ float s_c[kRouteRowsMaxK];
   pdl_launch_dependents();
   pdl_wait();
-  if (status_failed(status)) return;
+  // (other CTAs of this launch may set the status meanwhile, so the threads of a
+  // CTA need not agree on it: all of them reach the barrier, and none reads
+  // indexes that warp 0 did not write)
+  const bool failed = status_failed(status);
   const int t = blockIdx.x, P = n * k;
   if (threadIdx.x < 32) {
     // (k <= 32: one slot per lane)
@@ -165,6 +168,7 @@ route_rows_kernel(const uint4 *__restrict__ dx_perm, const int32_t *__restrict__
     }
   }
   __syncthreads();
+  if (failed) return;
   const int v0 = blockIdx.y * blockDim.x * VB + threadIdx.x;
   float acc[VB][V];
 #pragma unroll
