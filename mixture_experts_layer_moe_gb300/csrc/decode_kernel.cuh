@@ -256,7 +256,10 @@ decode_mxfp4_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_consta
     }
   }
   pdl_wait();
-  if (status_failed(a.status)) return;
+  // (the CTAs of this launch may set the status themselves, so the threads of
+  // one need not agree on it: warp 0's first lane decides for all, by leaving
+  // no active experts)
+  const bool failed = status_failed(a.status);
 
   // the experts with a non-empty segment, in order (E <= 256, one round of loads)
   if (warp == 0) {
@@ -291,7 +294,7 @@ decode_mxfp4_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_consta
     }
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
-      s_nactive = bad ? 0 : seen;
+      s_nactive = bad || failed ? 0 : seen;
       if (bad) set_status(a.status, MOE_ERR_BAD_INDEX, -1);
       s_abort = 0;
       s_raw_done = 0;
