@@ -85,7 +85,8 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP4 = 2, MOE_NVFP4 = 3 } moe_dty
  * ("Top-K", 0.45/0.76 and 0.31/0.76). */
 typedef enum { MOE_GATE_TOP_PROB = 0, MOE_GATE_RENORM = 1 } moe_gate;
 
-/* Expert activation.  RELU: h = max(x W1^T, 0).  SWIGLU: h = silu(x W1^T) *
+/* Expert activation.  RELU: h = max(x W1^T, 0), NaN for a NaN product (f32 and
+ * bf16 weights).  SWIGLU: h = silu(x W1^T) *
  * (x W3^T), silu(a) = a / (1 + e^-a).  The pages name only "a nonlinear
  * activation"; SwiGLU's branch roles follow the Mixtral convention. */
 typedef enum { MOE_ACT_RELU = 0, MOE_ACT_SWIGLU = 1 } moe_act;

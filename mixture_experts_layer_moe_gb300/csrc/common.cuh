@@ -95,6 +95,9 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// max(v, 0), a NaN kept (fmaxf would return 0 for it and hide it).
+__device__ __forceinline__ float relu(float v) { return v <= 0.f ? 0.f : v; }
+
 // ------------------------------------------------------------- element types
 template <typename T> struct Elem;
 template <> struct Elem<float> {

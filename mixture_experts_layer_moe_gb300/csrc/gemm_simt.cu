@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(SB_THREADS) gemm_simt_kernel(GemmStage g, int 
       const int gn = n0 + tx * 4 + j;
       if (gn >= N) continue;
       float v = acc[i][j];
-      if constexpr (EPI == 1) v = fmaxf(v, 0.f);
+      if constexpr (EPI == 1) v = relu(v);
       if constexpr (EPI == 2) v = v / (1.f + expf(-v)) * acc3[i][j];
       out[(size_t)gr * N + gn] = Elem<TO>::from_f(v);
     }

@@ -542,7 +542,7 @@ gemm_t2_kernel(const __grid_constant__ PMaps maps, const PArgs args) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 float v = __uint_as_float(a[i]);
-                if constexpr (EPI == 1) v = fmaxf(v, 0.f);
+                if constexpr (EPI == 1) v = relu(v);
                 const int tok = tok0 + i;
                 if (tok >= tl.seg_end) continue;
                 if constexpr (EPI == 8) plane[(size_t)tok * args.N] = v;

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256) rows_finish_kernel(FinishArgs a) {
     sum_parts(a.parts + i * 8, plane, a.splits, v);
     if constexpr (EPI == kRowsRelu) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fmaxf(v[j], 0.f);
+      for (int j = 0; j < 8; ++j) v[j] = relu(v[j]);
     } else if constexpr (EPI == kRowsSwiglu) {
       float u[8];
       sum_parts(a.parts + a.splits * plane + i * 8, plane, a.splits, u);

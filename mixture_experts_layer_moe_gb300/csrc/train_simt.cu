@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
     float v[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
     if constexpr (EPI == kRowsRelu) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
+      for (int j = 0; j < 4; ++j) v[j] = relu(v[j]);
     } else if constexpr (EPI == kRowsSwiglu) {
       const float u[4] = {acc2[i][0].x, acc2[i][0].y, acc2[i][1].x, acc2[i][1].y};
       put4<T>(p.out_g, at, v);
