@@ -424,8 +424,8 @@ typedef struct {
  *   dx = dg W1 + du W3;   dW1 = dg^T x;   dW3 = du^T x;   dW2 = dy^T h.
  * g, u, h as moe_expert_ffn_train wrote them.  dx_perm act_dtype [n*K][d], or
  * NULL.  The gradients of an expert without rows are zero.  bf16 layers round
- * dg and du once to bf16 where they are tensor-core operands (layers too small for
- * the tensor cores keep them in fp32). */
+ * dg and du once to bf16 where they are tensor-core operands (layers so small that
+ * dx, dW1 and dW3 run on the CUDA cores keep them in fp32). */
 moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
                                    const int32_t *offsets, const moe_weights *w, const void *g,
                                    const void *u, const void *h, const void *dy_perm,

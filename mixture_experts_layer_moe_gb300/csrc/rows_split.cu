@@ -3,7 +3,8 @@
 // tokens, or its dx): the reduction is cut into ranges, whose products run side
 // by side on the pair kernel (kEpiPartial) and leave fp32 partial sums; a second
 // launch adds them in order and applies the epilogue that the whole product
-// would have had.
+// would have had.  A gradient whose dg and du are to stay in fp32 takes this path
+// uncut too (one range): the pair kernel's own epilogues store bf16.
 #include "api.h"
 #include "common.cuh"
 #include "gate_math.cuh"
@@ -21,7 +22,7 @@ struct FinishArgs {
   const int32_t *offsets;    // nullptr: all rows
   int num_experts, rows, N, splits;
   const uint4 *g, *u, *h;    // kept rows
-  uint4 *out, *out_g, *out_u;
+  void *out, *out_g, *out_u;
   int *status;
 };
 
@@ -38,7 +39,17 @@ __device__ __forceinline__ void sum_parts(const float *p, size_t plane, int spli
   }
 }
 
-template <int EPI>
+// Vector i of 8 outputs.
+template <typename T>
+__device__ __forceinline__ void store8(void *out, size_t i, const float (&v)[8]) {
+  constexpr int N = Vec16<T>::N;
+#pragma unroll
+  for (int q = 0; q < 8 / N; ++q)
+    static_cast<uint4 *>(out)[i * (8 / N) + q] = pack16<T>(v + q * N);
+}
+
+// TO: the type of a gradient's outputs.
+template <int EPI, typename TO = __nv_bfloat16>
 __global__ void __launch_bounds__(256) rows_finish_kernel(FinishArgs a) {
   pdl_wait();
   if (status_failed(a.status)) return;
@@ -57,8 +68,8 @@ __global__ void __launch_bounds__(256) rows_finish_kernel(FinishArgs a) {
     } else if constexpr (EPI == kRowsSwiglu) {
       float u[8];
       sum_parts(a.parts + a.splits * plane + i * 8, plane, a.splits, u);
-      a.out_g[i] = pack16<__nv_bfloat16>(v);
-      a.out_u[i] = pack16<__nv_bfloat16>(u);
+      store8<__nv_bfloat16>(a.out_g, i, v);
+      store8<__nv_bfloat16>(a.out_u, i, u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = silu_mul(v[j], u[j]);
     } else if constexpr (EPI == kRowsReluGrad) {
@@ -72,9 +83,9 @@ __global__ void __launch_bounds__(256) rows_finish_kernel(FinishArgs a) {
       unpack16<__nv_bfloat16>(a.u[i], u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) swiglu_grad(v[j], g[j], u[j], v[j], du[j]);
-      a.out_u[i] = pack16<__nv_bfloat16>(du);
+      store8<TO>(a.out_u, i, du);
     }
-    a.out[i] = pack16<__nv_bfloat16>(v);
+    store8<TO>(a.out, i, v);
   }
 }
 
@@ -117,7 +128,7 @@ int rows_splits(const RowsProduct &p) {
 
 size_t rows_scratch(const RowsProduct &p) {
   const int splits = rows_splits(p);
-  return splits > 1 ? (size_t)matrices_of(p) * splits * p.rows * p.N * 4 : 0;
+  return splits > 1 || p.out_f32 ? (size_t)matrices_of(p) * splits * p.rows * p.N * 4 : 0;
 }
 
 cudaError_t launch_rows_split(const RowsProduct &p, const GemmStage &whole, int splits,
@@ -139,12 +150,17 @@ cudaError_t launch_rows_split(const RowsProduct &p, const GemmStage &whole, int 
   a.g = (const uint4 *)p.g;
   a.u = (const uint4 *)p.u;
   a.h = (const uint4 *)p.h;
-  a.out = (uint4 *)p.out;
-  a.out_g = (uint4 *)p.out_g;
-  a.out_u = (uint4 *)p.out_u;
+  a.out = p.out;
+  a.out_g = p.out_g;
+  a.out_u = p.out_u;
   a.status = status;
   const int64_t blocks = ((int64_t)p.rows * p.N / 8 + 255) / 256;
   const dim3 grid((unsigned)(blocks < 1216 ? blocks : 1216));
+  if (p.out_f32) {
+    auto wide = p.epi == kRowsReluGrad ? rows_finish_kernel<kRowsReluGrad, float>
+                                       : rows_finish_kernel<kRowsSwigluGrad, float>;
+    return launch_pdl(wide, grid, dim3(256), 0, s, a);
+  }
   auto with = p.epi == kRowsPlain      ? rows_finish_kernel<kRowsPlain>
               : p.epi == kRowsRelu     ? rows_finish_kernel<kRowsRelu>
               : p.epi == kRowsSwiglu   ? rows_finish_kernel<kRowsSwiglu>

@@ -70,17 +70,18 @@ struct RowsProduct {
   const int32_t *add_inv;
   int add_k;
   int beside;                  // see launch_gemm_grad
-  // On the CUDA cores, for a bf16 layer: A and A2, or out and out_u of a
-  // gradient, are fp32
+  // For a bf16 layer: A and A2 are fp32 (on the CUDA cores), or out and out_u of a
+  // gradient are
   int a_f32, out_f32;
 };
 // fp32, and small bf16 products: at most so many multiplications each.
 constexpr int64_t kSmallProducts = 1 << 24;
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s);
 
-// The same with the reduction cut into ranges where its tiles are few (bf16):
-// how many (1: not cut; by the shape alone), the scratch that takes, and the
-// launches; `whole` is the product as the pair kernel takes it.
+// The same with the reduction cut into ranges where its tiles are few (bf16), or
+// whole with fp32 outputs: how many ranges (1: not cut; by the shape alone), the
+// scratch that takes, and the launches; `whole` is the product as the pair
+// kernel takes it.
 int rows_splits(const RowsProduct &p);
 size_t rows_scratch(const RowsProduct &p);
 cudaError_t launch_rows_split(const RowsProduct &p, const struct GemmStage &whole, int splits,

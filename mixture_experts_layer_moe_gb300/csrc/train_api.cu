@@ -93,14 +93,17 @@ RowsProduct router_rows_of(const moe_config &c) {
 }
 
 // dg and du, or dl, are rounded to bf16 where tensor cores multiply them.  A
-// small layer, whose products all run on the CUDA cores, keeps them in fp32: with
-// few rows that rounding is not averaged out (one token, d 2776, d_ff 104: dW1
-// off by 3.1e-3 of its norm, 1.7e-3 without).
+// small layer, where every product that takes them runs on the CUDA cores, keeps
+// them in fp32: with few rows that rounding is not averaged out (one token, d
+// 2776, d_ff 104: dW1 off by 3.1e-3 of its norm, 1.7e-3 without).  The product
+// that forms dg and du may run on the tensor cores all the same (a long
+// reduction over d), as partial sums (rows_split.cu): their second launch costs
+// 1 to 2 us where the reduction was not cut anyway (53 rows of 2 experts, d 520,
+// d_ff 248 24.8 us for the backward, 22.9 with the rounding).
 bool wide_expert_grads(const moe_config &c) {
   GradProduct p[3];
   expert_grads_of(c, reinterpret_cast<const int32_t *>(16), p);
-  return grads_small(p, expert_problems(c)) && on_cuda_cores(rows_of(c, kGateGrad)) &&
-         on_cuda_cores(rows_of(c, kInputGrad));
+  return grads_small(p, expert_problems(c)) && on_cuda_cores(rows_of(c, kInputGrad));
 }
 bool wide_router_grads(const moe_config &c) {
   const GradProduct p = router_grad_of(c);
@@ -132,8 +135,10 @@ TrainLayout train_layout_of(const moe_config &c) {
   const size_t ge = grad_scratch(experts, expert_problems(c)), gr = grad_scratch(&router, 1);
   size_t parts = ge > gr ? ge : gr;   // (used by one launch after the other)
   for (RowsKind kind : {kUp, kDown, kGateGrad, kInputGrad}) {
-    const size_t r = rows_scratch(rows_of(c, kind));
-    if (r > parts) parts = r;
+    RowsProduct r = rows_of(c, kind);
+    r.out_f32 = wide && z < 4 && kind == kGateGrad;
+    const size_t bytes = on_cuda_cores(r) ? 0 : rows_scratch(r);
+    if (bytes > parts) parts = bytes;
   }
   L.parts = take(parts);
   L.total = off;
@@ -192,9 +197,10 @@ cudaError_t launch_rows(const RowsProduct &p, float *parts, int *status, cudaStr
   g.kept_h = p.h;
   g.beside = p.beside;
   if (!gemm_t2_supported(g)) return cudaErrorNotSupported;
+  // (fp32 outputs: the pair kernel's epilogues store bf16)
   const int splits = rows_splits(p);
-  return splits > 1 ? launch_rows_split(p, g, splits, parts, status, s)
-                    : launch_gemm_t2(g, status, s);
+  return splits > 1 || p.out_f32 ? launch_rows_split(p, g, splits, parts, status, s)
+                                 : launch_gemm_t2(g, status, s);
 }
 
 // Weight gradients over the same segments, in one launch.  splits, parts: as
