@@ -457,8 +457,8 @@ moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const voi
  * f fp32 [E] or NULL.  dx_perm and inv_perm may both be NULL (the router's
  * share alone).  dx act_dtype [n][d], dWg act_dtype [E][d], dbias fp32 [E]:
  * each may be NULL.  bf16 layers round dl to bf16 as an operand of its
- * products, and dl Wg before the rows are added, where these run on the tensor
- * cores (dbias sums dl in fp32).  A topk_idx outside [0, E) sets MOE_ERR_BAD_INDEX
+ * products where these run on the tensor cores (dbias sums dl in fp32); dx is one
+ * fp32 sum, rounded once.  A topk_idx outside [0, E) sets MOE_ERR_BAD_INDEX
  * and its slot counts as a gate of zero; an inv_perm entry outside [0, n*K) sets
  * it and its row is left out.  Other parts of the outputs may then stay
  * unwritten. */

@@ -7,8 +7,6 @@
 // experts, added up by weight") the K weighted outputs of a token are added.
 //   y[t] = sum_{j<k} g[t][j] * y_perm[inv_perm[t*k + j]]  (+ y_shared[t])
 // fp32 accumulation in slot order, then one rounding to the output type.
-// gates == nullptr stands for gates of one: the gradient of the dispatch's row
-// copies (dx[t] = the sum of its k rows' gradients, + the router's share).
 #include "common.cuh"
 #include "launch.h"
 #include "vec16.cuh"
@@ -46,7 +44,7 @@ combine_kernel(const uint4 *__restrict__ y_perm, const int32_t *__restrict__ inv
         q[u] = -1;
         if (j0 + u < k) {
           q[u] = inv_perm[(int64_t)t * k + j0 + u];
-          g[u] = gates ? gates[(int64_t)t * k + j0 + u] : 1.f;
+          g[u] = gates[(int64_t)t * k + j0 + u];
         }
       }
 #pragma unroll
@@ -99,7 +97,7 @@ combine_rows_kernel(const uint4 *__restrict__ y_perm, const int32_t *__restrict_
       q = -1;
     }
     s_q[j] = q;
-    s_g[j] = gates ? gates[(int64_t)t * k + j] : 1.f;
+    s_g[j] = gates[(int64_t)t * k + j];
   }
   __syncthreads();
   const int v0 = blockIdx.y * 256 * VB + threadIdx.x;

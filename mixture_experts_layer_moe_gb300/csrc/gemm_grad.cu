@@ -32,9 +32,18 @@
 // partial sums, and a second launch adds them in order and rounds once.
 //
 // A_K: the same tile for out[t][c] = sum_k A[t][k] B[k][c] over one segment,
-// A's reduction index contiguous (the rows' share of a router's gradient: short
-// reductions, where the store of the result is the work, and this epilogue's
-// packed stores are what that needs).
+// A's reduction index contiguous (the router's share of its dx: short reductions,
+// where the store of the result is the work, and this epilogue's packed stores
+// are what that needs).
+//
+// ADD, with A_K: plus sum_{j < add_k} add[add_inv[t * add_k + j]][c], the
+// gradients of the token's expert rows, in the same fp32 sum, rounded once.  The
+// gathered rows are the work then, so two pipeline stages feed the MMAs and the
+// rest of shared memory is a ring of gathered pieces per epilogue warp, 112 KB
+// in flight per SM (GatherRing).  16384 tokens, d 7168, 8 rows each, 256 experts:
+// 404 us, 5.2 TB/s; one launch that stores dl Wg and one that sums took 434 and
+// rounded dl Wg to bf16 in between.  (Gathering into registers instead, 8 or 16
+// epilogue warps: 520 to 770 us.)
 //
 // Roles (persistent, one CTA per SM, clusters of two): warp 0 TMA producer in
 // both CTAs, warp 1 of the first CTA issues the MMAs into two accumulators of
@@ -45,6 +54,7 @@
 #include "pair_common.cuh"
 #include "tc_common.cuh"
 #include "train.h"
+#include "vec16.cuh"
 
 namespace moe {
 namespace {
@@ -55,6 +65,7 @@ constexpr int GM = 128;                       // output rows per CTA (MMA M = 25
 constexpr int GN = 256;                       // output columns per tile at most (MMA N)
 constexpr int GK = 64;                        // segment rows per k-block
 constexpr int GS = 6;                         // pipeline stages
+constexpr int g_stages(bool add) { return add ? 2 : GS; }
 constexpr int G_BOX = 64 * GK * 2;            // one 64 x 64 box: 8 KB
 constexpr int G_STAGE = 4 * G_BOX;            // two boxes of B (N side), two of A (M side)
 constexpr int G_EPI = 8;                      // epilogue warps: two per TMEM lane quarter
@@ -62,7 +73,12 @@ constexpr int G_THREADS = 32 * (3 + G_EPI);
 constexpr uint32_t G_TMEM_COLS = 512;
 constexpr int G_MAX_E = 256;
 constexpr int G_OUT = 32 * 128;               // one store: 32 rows x 64 columns, 128-byte swizzle
-constexpr size_t G_DYN_SMEM = 1024 + (size_t)GS * G_STAGE + (size_t)G_EPI * G_OUT;
+// ADD: a ring of G_RING such pieces per epilogue warp, each 32 gathered rows x 64
+// columns
+constexpr int G_RING = 4;
+constexpr size_t g_dyn_smem(bool add) {
+  return 1024 + (size_t)g_stages(add) * G_STAGE + (size_t)G_EPI * G_OUT * (add ? 1 + G_RING : 1);
+}
 
 struct GShared {
   uint64_t full[GS];        // first CTA: both CTAs' boxes landed (and were fixed)
@@ -85,6 +101,11 @@ struct GArgs {
   int splits;                        // runs of rows per segment
   int beside;                        // 1: the next kernel runs beside this one
   int *status;
+  // ADD: the rows added to the output ([M * add_k][N]).  An index outside them is
+  // skipped.
+  const uint4 *add;
+  const int32_t *add_inv;
+  int add_k;
 };
 struct GMaps {
   CUtensorMap a[kMaxGradProblems], b[kMaxGradProblems], out[kMaxGradProblems];
@@ -132,9 +153,98 @@ __device__ __forceinline__ uint32_t bf16x2_bits(uint32_t lo, uint32_t hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <bool A_K, bool SPLIT>
+// ADD: the rows that one epilogue warp adds, in the order in which it adds them
+// (tile, 64 columns, slot), copied asynchronously into its ring G_RING steps
+// ahead, across the tiles' borders.  A step is 32 rows x 64 columns, laid out as a
+// store's piece: row r's 16-byte vector v at 128 r + 16 (v ^ r % 8).  Eight lanes
+// copy a row's 128 bytes; a row or column that is not there is filled with
+// zeros.
+struct GatherRing {
+  const GShared &sh;
+  const GArgs &args;
+  uint8_t *ring;
+  int pair, n_pairs, num_tiles, rank, quarter, part, lane;
+  int t, row, col0, nc, c, j;   // the next step to copy: tile, its first row and columns, slot
+  int index;                    // this lane's row's, of that step
+  int fill, take;
+
+  // the first step of tile t, or of the next tile with one
+  __device__ __forceinline__ void seek() {
+    for (; t < num_tiles; t += n_pairs) {
+      const GTile tl = g_decode<false>(sh, args, t);
+      row = tl.m0 + rank * GM + quarter * 32;
+      col0 = tl.c0;
+      nc = tl.nc;
+      c = part * 64;
+      if (row < args.M[0] && c < nc) return;
+    }
+  }
+  __device__ __forceinline__ void load_index() {
+    index = -1;
+    if (t < num_tiles && row + lane < args.M[0])
+      index = __ldg(args.add_inv + (int64_t)(row + lane) * args.add_k + j);
+    if (index >= args.M[0] * args.add_k) index = -1;
+  }
+  __device__ __forceinline__ void start() {
+    t = pair;
+    j = fill = take = 0;
+    seek();
+    load_index();
+    for (int i = 0; i < G_RING; ++i) copy();
+  }
+  // copies a step (or nothing, past the last) as an asynchronous group
+  __device__ __forceinline__ void copy() {
+    if (t < num_tiles) {
+      const int v = lane & 7, col = col0 + c + v * 8, N = args.N[0];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = (lane >> 3) + 4 * i;
+        const int from = __shfl_sync(0xffffffffu, index, r);
+        const bool there = from >= 0 && col < N;
+        const uint4 *src = args.add + (there ? ((int64_t)from * N + col) / 8 : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         tc::smem_u32(ring + fill * G_OUT + r * 128 + ((v ^ (r & 7)) << 4))),
+                     "l"(src), "r"(there ? 16 : 0)
+                     : "memory");
+      }
+      if (++j == args.add_k) {
+        j = 0;
+        c += 128;
+        if (c >= nc) {
+          t += n_pairs;
+          seek();
+        }
+      }
+      load_index();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    fill = (fill + 1) % G_RING;
+  }
+  // adds the next step, this lane's row of it
+  __device__ __forceinline__ void add(uint32_t (&a)[2][32]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(G_RING - 1) : "memory");
+    __syncwarp();
+    const uint8_t *piece = ring + take * G_OUT + lane * 128;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float f[8];
+      unpack16<__nv_bfloat16>(*reinterpret_cast<const uint4 *>(piece + ((q ^ (lane & 7)) << 4)), f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t &x = a[q >> 2][(q & 3) * 8 + e];
+        x = __float_as_uint(__uint_as_float(x) + f[e]);
+      }
+    }
+    __syncwarp();   // (read by all before it is filled again)
+    take = (take + 1) % G_RING;
+    copy();
+  }
+};
+
+template <bool A_K, bool SPLIT, bool ADD>
 __global__ void __launch_bounds__(G_THREADS, 1)
 gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GArgs args) {
+  constexpr int STAGES = g_stages(ADD);
   extern __shared__ uint8_t dyn_smem[];
   __shared__ GShared sh;
   uint8_t *smem = dyn_smem + ((1024 - (tc::smem_u32(dyn_smem) & 1023)) & 1023);
@@ -152,7 +262,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
   }
   if (warp == 1) tmem_alloc2(&sh.tmem_base, G_TMEM_COLS);
   if (threadIdx.x == 32) {
-    for (int s = 0; s < GS; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       tc::mbar_init(&sh.full[s], 1);
       tc::mbar_init(&sh.empty[s], 1);
       tc::mbar_init(&sh.tail_full[s], 1);
@@ -234,13 +344,13 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
             tma2_load_2d(ma, bar, sb + 3 * G_BOX, m + 64, q);
           }
           if (two) tma2_load_2d(mb, bar, sb + G_BOX, c + 64, q);
-          if (++stage == GS) { stage = 0; phase ^= 1u; }
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
       if (*abort) {
         // let the copies in flight land before the pair exits (the second
         // CTA's whole k-blocks count on the first CTA's barriers)
-        for (int s = 0; s < GS; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
           if (!((used >> s) & 1u)) continue;
           const uint32_t ph = (used_phase >> s) & 1u;
           if ((used_tail >> s) & 1u) tc::mbar_wait_drain(&sh.tail_full[s], ph, 100000000ull);
@@ -288,7 +398,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
             if (left > 32) mma2_bf16_lo(d_tmem, al + 2 * A_STEP, a_hi, bl + 256, b_hi, idesc, 1u);
           }
           mma2_commit_both(&sh.empty[stage]);
-          if (++stage == GS) { stage = 0; phase ^= 1u; }
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
         mma2_commit_both(&sh.tfull[acc]);
@@ -308,8 +418,8 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
       const GTile tl = g_decode<SPLIT>(sh, args, t);
       const int kb = (tl.len + GK - 1) / GK;
       if (kb == 0) continue;
-      const int at = (stage + kb - 1) % GS;
-      stage = (stage + kb) % GS;
+      const int at = (stage + kb - 1) % STAGES;
+      stage = (stage + kb) % STAGES;
       const int valid = tl.len - (kb - 1) * GK;           // rows of the last k-block
       if (A_K || (valid & 15) == 0) continue;
       const uint32_t ph = (tail_phase >> at) & 1u;
@@ -340,8 +450,11 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
     const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const uint32_t tempty_first = map_to_rank(tc::smem_u32(&sh.tempty[0]), 0);
-    uint8_t *stage_out = smem + GS * G_STAGE + (warp - 2) * G_OUT;
+    uint8_t *stage_out = smem + STAGES * G_STAGE + (warp - 2) * G_OUT;
     int local = 0;
+    GatherRing gather{sh, args, smem + STAGES * G_STAGE + (G_EPI + (warp - 2) * G_RING) * G_OUT,
+                      pair, n_pairs, num_tiles, (int)rank, quarter, part, lane};
+    if (ADD) gather.start();
     for (int t = pair; t < num_tiles; t += n_pairs) {
       const GTile tl = g_decode<SPLIT>(sh, args, t);
       const int row = tl.m0 + (int)rank * GM + quarter * 32;   // this warp's first row
@@ -367,6 +480,8 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
           for (int i = 0; i < 32; ++i) a[0][i] = a[1][i] = 0;
         }
         if (!rows_ok) continue;
+        if (ADD)
+          for (int j = 0; j < args.add_k; ++j) gather.add(a);
 #pragma unroll
         for (int half = 0; half < (SPLIT ? 2 : 1); ++half) {
           // a 128-byte piece of each row: 64 elements, or 32 partial sums
@@ -400,6 +515,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
       }
     }
     if (lane == 0) tc::bulk_wait_all();
+    if (ADD) asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 
   __syncwarp();
@@ -450,12 +566,12 @@ __global__ void __launch_bounds__(256) grad_sum_kernel(SumArgs a) {
 
 constexpr int kPairs = 76;   // SM pairs that the plans count on
 
-template <bool A_K, bool SPLIT>
+template <bool A_K, bool SPLIT, bool ADD = false>
 cudaError_t launch(const GMaps &maps, const GArgs &a, cudaStream_t s) {
-  auto kernel = gemm_grad_kernel<A_K, SPLIT>;
+  auto kernel = gemm_grad_kernel<A_K, SPLIT, ADD>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(G_THREADS);
-  cfg.dynamicSmemBytes = G_DYN_SMEM;
+  cfg.dynamicSmemBytes = g_dyn_smem(ADD);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -469,7 +585,7 @@ cudaError_t launch(const GMaps &maps, const GArgs &a, cudaStream_t s) {
   static int pairs = 0;
   if (pairs == 0) {
     const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_DYN_SMEM);
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)g_dyn_smem(ADD));
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(2 * (num_sms() / 2));
     if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs < 1) {
@@ -612,7 +728,10 @@ cudaError_t launch_gemm_router_rows(const RowsProduct &p, int *status, cudaStrea
   if (!encode(&maps.a[0], p.A, 2, da, box_a) || !encode(&maps.b[0], p.B, 2, db, box_b) ||
       !encode(&maps.out[0], p.out, 3, dout, box_out))
     return cudaErrorInvalidValue;
-  return launch<true, false>(maps, a, s);
+  a.add = static_cast<const uint4 *>(p.add);
+  a.add_inv = p.add_inv;
+  a.add_k = p.add_k;
+  return p.add ? launch<true, false, true>(maps, a, s) : launch<true, false>(maps, a, s);
 }
 
 }  // namespace moe

@@ -82,7 +82,7 @@ cudaError_t launch_scatter_rows(const void *x, const int32_t *inv_perm, int P, i
 cudaError_t launch_gather(const void *x, const int32_t *perm, int P, int k, int n,
                           int64_t row_bytes, void *x_perm, int *status, cudaStream_t s);
 
-// y[t] = sum_j g[t][j] * y_perm[inv[t*k+j]] (+ y_shared[t]); gates nullptr: g = 1.
+// y[t] = sum_j g[t][j] * y_perm[inv[t*k+j]] (+ y_shared[t]).
 cudaError_t launch_combine(int act_dtype, const void *y_perm, const int32_t *inv_perm,
                            const float *gates, const void *y_shared, void *y, int n, int k,
                            int d, int *status, cudaStream_t s);

@@ -24,8 +24,9 @@ template <typename T>
 __global__ void __launch_bounds__(32 * RB_WARPS)
 route_grad_kernel(const float *__restrict__ probs, const int32_t *__restrict__ topk_idx,
                   const float *__restrict__ gates, const float *__restrict__ dgate,
-                  const float *__restrict__ f, float aux_scale, int renorm, int n, int E, int k,
-                  T *__restrict__ dl, int pitch, float *__restrict__ bias_parts, int *status) {
+                  const float *__restrict__ f, const int32_t *__restrict__ inv_perm,
+                  float aux_scale, int renorm, int n, int E, int k, T *__restrict__ dl, int pitch,
+                  float *__restrict__ bias_parts, int *status) {
   __shared__ float s_sum[RB_WARPS][RB_SLOTS * 32];
   pdl_launch_dependents();
   pdl_wait();
@@ -63,6 +64,10 @@ route_grad_kernel(const float *__restrict__ probs, const int32_t *__restrict__ t
         if (e_l < 0 || e_l >= E) {
           set_status(status, MOE_ERR_BAD_INDEX, t * k + j);
           e_l = -1;
+        }
+        if (inv_perm) {
+          const int q = inv_perm[(int64_t)t * k + j];
+          if (q < 0 || q >= n * k) set_status(status, MOE_ERR_BAD_INDEX, t * k + j);
         }
       }
     };
@@ -109,7 +114,7 @@ route_grad_kernel(const float *__restrict__ probs, const int32_t *__restrict__ t
 // without the loss):
 //   dx[t] = sum_j (dx_perm[q_j] + c_j Wg[e_j]),   c_j = g_j (dgate_j - sum g dgate),
 // in one pass: the k router rows of a token come from L2 (Wg is a few MB), so
-// the launch moves what the sum of the expert rows moves, and neither dl Wg nor
+// the launch moves what the sum of the expert rows moves, and neither dl nor
 // a rounding of it is kept.  CTA (t, c) takes vectors [c * 256 VB, ...) of
 // token t's row; four slots' rows are in flight per thread, and the sum runs in
 // slot order.  (blockDim.x: 256, or fewer for a row of fewer vectors.)
@@ -228,8 +233,8 @@ size_t route_grad_scratch(const moe_config &c) { return (size_t)grid_of(c.n) * c
 
 cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int32_t *topk_idx,
                               const float *gates, const float *dgate, const float *f, float aux,
-                              void *dl, bool dl_f32, int pitch, float *dbias, float *scratch,
-                              int *status, cudaStream_t s) {
+                              const int32_t *inv_perm, void *dl, bool dl_f32, int pitch,
+                              float *dbias, float *scratch, int *status, cudaStream_t s) {
   const int grid = grid_of(c.n), E = c.n_experts;
   const int renorm = c.gate == MOE_GATE_RENORM;
   const float scale = aux * (float)E / (float)c.n;
@@ -239,23 +244,25 @@ cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int
   cudaError_t e;
   if (dl_f32)
     e = launch_pdl(route_grad_kernel<float>, blocks, threads, 0, s, probs, topk_idx, gates, dgate, f,
-                   scale, renorm, c.n, E, c.top_k, (float *)dl, pitch, parts, status);
+                   inv_perm, scale, renorm, c.n, E, c.top_k, (float *)dl, pitch, parts, status);
   else
     e = launch_pdl(route_grad_kernel<__nv_bfloat16>, blocks, threads, 0, s, probs, topk_idx, gates,
-                   dgate, f, scale, renorm, c.n, E, c.top_k, (__nv_bfloat16 *)dl, pitch, parts,
-                   status);
+                   dgate, f, inv_perm, scale, renorm, c.n, E, c.top_k, (__nv_bfloat16 *)dl, pitch,
+                   parts, status);
   if (e == cudaSuccess && dbias && grid > 1)
     e = launch_column_sum(scratch, nullptr, grid, E, dbias, nullptr, status, s);
   return e;
 }
 
-// Against the product dl Wg and the sum of the rows in launches of their own,
-// the whole gradient of a bf16 router took (us, one launch / two):
-//   n 16384, d 7168, 256 experts: k = 2 299 / 344, k = 4 380 / 389, k = 8 572 / 514
-//   n 2048, d 7168, k = 8 99 / 98;  n 1024, d 1024, k = 8 22 / 28;  n 1, k = 8 16 / 22
-// so long rows of many choices take the product: there the reads of Wg's rows
-// from L2 outweigh writing and reading dl Wg.  (fp32: 2048 tokens, d 1024, 256
-// experts, k = 8 59 / 93.)
+// Against dl in a launch of its own and the product dl Wg with the rows added in
+// its epilogue, the whole gradient of a bf16 router took (us, this / the product):
+//   n 16384, d 7168, 256 experts: k = 2 299 / 254, k = 4 380 / 328, k = 8 572 / 488
+//   n 4096, d 4096, 64 experts, k = 2 57 / 59;  n 2048, d 7168, k = 8 100 / 88
+//   n 1024, d 1024, k = 8 23 / 27;  n 1, k = 8 14 / 21
+// Long rows of many choices take the product: the reads of Wg's rows from L2 are
+// what this sum waits for.  Few choices stay here although the product is the
+// faster on large batches: it rounds dl to bf16 as its operand, this sum
+// does not.  (fp32: 2048 tokens, d 1024, 256 experts, k = 8 59 / 93.)
 bool route_rows_supported(const moe_config &c, const float *f) {
   if (c.gate != MOE_GATE_RENORM || f != nullptr || c.top_k > kRouteRowsMaxK) return false;
   return c.act_dtype == MOE_F32 || c.top_k <= 4 || (int64_t)c.n * c.d <= 1 << 23;

@@ -29,12 +29,14 @@ cudaError_t launch_combine_backward(int dtype, const void *dy, const void *y_per
 
 // dl [n][pitch] (dl_f32: fp32, else bf16; columns E .. pitch - 1 zero) and, when dbias is set,
 // the column sums, through route_grad_scratch(c) bytes of scratch.
-// dl may be nullptr (dbias alone).
+// dl may be nullptr (dbias alone).  inv_perm [n*K], or nullptr: checked here for
+// the product that follows, which skips an index outside [0, n*K) and cannot set
+// the status itself (CTAs of a pair must not differ on it).
 size_t route_grad_scratch(const moe_config &c);
 cudaError_t launch_route_grad(const moe_config &c, const float *probs, const int32_t *topk_idx,
                               const float *gates, const float *dgate, const float *f, float aux,
-                              void *dl, bool dl_f32, int pitch, float *dbias, float *scratch, int *status,
-                              cudaStream_t s);
+                              const int32_t *inv_perm, void *dl, bool dl_f32, int pitch,
+                              float *dbias, float *scratch, int *status, cudaStream_t s);
 
 // dx from the expert rows' gradients and the router's in one pass, where dl has
 // entries at the chosen experts alone and these are few.
@@ -65,7 +67,7 @@ struct RowsProduct {
   const void *B, *B2;
   const void *g, *u, *h;    // kept rows [rows][N] that a gradient's epilogue reads
   void *out, *out_g, *out_u;   // [rows][N]
-  // kRowsPlain on the CUDA cores: out[q] += sum_j add[add_inv[q * add_k + j]]
+  // kRowsPlain, one segment: out[q] += sum_j add[add_inv[q * add_k + j]], in fp32
   const void *add;             // [rows * add_k][N] or nullptr
   const int32_t *add_inv;
   int add_k;

@@ -12,7 +12,7 @@ namespace {
 
 // The layer's workspace, then the scratch of the gradients.
 struct TrainLayout {
-  size_t status, dg, du, dl, dx_router, bias_parts, parts, total;
+  size_t status, dg, du, dl, bias_parts, parts, total;
 };
 
 // dl's rows are padded to whole 16-byte vectors of bf16.
@@ -117,7 +117,6 @@ TrainLayout train_layout_of(const moe_config &c) {
   const size_t P = (size_t)c.n * c.top_k, z = act_size(c);
   TrainLayout L{};
   L.status = base.status;
-  L.dx_router = base.x_perm;  // [n][d]
   size_t off = layout_of(c).total;
   auto take = [&](size_t bytes) {
     const size_t a = off;
@@ -174,6 +173,7 @@ bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
 cudaError_t launch_rows(const RowsProduct &p, float *parts, int *status, cudaStream_t s) {
   if (on_cuda_cores(p)) return launch_rows_simt(p, status, s);
   if (gemm_router_rows_supported(p)) return launch_gemm_router_rows(p, status, s);
+  if (p.add) return cudaErrorNotSupported;
   constexpr int epi[] = {0, 1, kEpiSwigluKeep, kEpiReluGrad, kEpiSwigluGrad};   // by kRows*
   GemmStage g{};
   g.a_dtype = g.b_dtype = g.out_dtype = MOE_BF16;
@@ -455,8 +455,9 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
   const bool rows = dx && route_rows_supported(c, f);   // dx without dl
   void *dl = (dx && !rows) || dWg ? at<void>(ws, L.dl) : nullptr;
   if (dl || dbias)
-    MOE_TRY(cuda_status(launch_route_grad(c, probs, topk_idx, topk_gate, dgate, f, aux, dl, wide,
-                                          pitch, dbias, at<float>(ws, L.bias_parts), status, s)));
+    MOE_TRY(cuda_status(launch_route_grad(c, probs, topk_idx, topk_gate, dgate, f, aux,
+                                          dx && !rows ? inv_perm : nullptr, dl, wide, pitch, dbias,
+                                          at<float>(ws, L.bias_parts), status, s)));
   if (dWg) {
     GradProduct gw = router_grad_of(c);
     gw.A = dl;
@@ -474,18 +475,12 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
     r.A = dl;
     r.B = w->Wg;
     r.a_f32 = c.act_dtype == MOE_BF16 && wide;
-    // (on the CUDA cores: the sum of the expert rows in the product's epilogue)
-    const bool fused = on_cuda_cores(r);
-    if (fused && dx_perm) {
-      r.add = dx_perm;
-      r.add_inv = inv_perm;
-      r.add_k = c.top_k;
-    }
-    r.out = dx_perm && !fused ? at<void>(ws, L.dx_router) : dx;
+    // (the sum of the expert rows in the product's epilogue, in fp32)
+    r.add = dx_perm;
+    r.add_inv = inv_perm;
+    r.add_k = c.top_k;
+    r.out = dx;
     MOE_TRY(cuda_status(launch_rows(r, nullptr, status, s)));
-    if (dx_perm && !fused)
-      MOE_TRY(cuda_status(launch_combine(c.act_dtype, dx_perm, inv_perm, nullptr, r.out, dx, c.n,
-                                         c.top_k, c.d, status, s)));
   }
   return MOE_OK;
 }

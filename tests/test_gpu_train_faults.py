@@ -71,3 +71,30 @@ def test_route_backward_with_many_bad_indexes(lib, n, d, k, dtype):
         right = (got - wdx).abs() <= bound + base.TINY
         assert (right | (got == 77.0)).all()
         assert right.any()
+
+
+@pytest.mark.parametrize("n,d,E,k", [(700, 2056, 16, 2), (3000, 1032, 40, 8), (200, 128, 8, 3)])
+def test_route_backward_of_a_dense_gradient_reports_bad_rows(lib, n, d, E, k):
+    """The product that adds the gathered rows skips indexes outside them; the status says so, and
+    the next call after the status was cleared is right."""
+    cfg = base._cfg(n, d, 8, E, k, "bf16", gate="top_prob")
+    s = _routing(n, d, E, k, "bf16", 3, "top_prob")
+    ws, w = lib.alloc_train_workspace(cfg), lib.make_weights(s)
+
+    def run(inv):
+        dx = torch.full_like(s["x"], 77.0)
+        lib.moe_route_backward(cfg, s["x"], w, s["probs"], s["idx"], s["gates"], s["dgate"], None, 0.0,
+                               inv, s["dxp"], dx, None, None, ws)
+        return dx
+
+    want = run(s["inv"])
+    base._ok(lib, ws)
+    assert not (want == 77.0).any()
+    for at, bad in ((0, -1), (n * k - 1, n * k), (n * k // 2, 2 ** 31 - 1), (7, -2 ** 31)):
+        inv = s["inv"].clone()
+        inv[at] = bad
+        run(inv)
+        assert lib.moe_status_check(ws) == (5, at)
+        lib.moe_status_clear(ws)
+    assert torch.equal(run(s["inv"]), want)
+    base._ok(lib, ws)

@@ -1,6 +1,7 @@
 """GPU: how often the training operators of bf16 layers round, where that differs from the
 roundings of their outputs."""
 import pytest
+import torch
 
 import test_gpu_train as base
 from oracle import train_oracle as T
@@ -35,3 +36,39 @@ def test_weight_gradients_of_one_token_have_one_roundings_error(lib):
     for got, want in ((gr["W1"], wW1), (gr["W3"], wW3)):
         off = ((got.cpu().double() - want).norm() / want.norm()).item()
         assert off <= 1.9e-3, off
+
+
+# gate rule, n, d, E, k: on the tensor cores (n E d > 2^24), whole and ragged tiles
+ROUTE_CASES = [("top_prob", 700, 2056, 16, 2), ("renorm", 1200, 7168, 32, 8),
+               ("top_prob", 33, 5000, 128, 5), ("renorm", 4099, 2880, 64, 8)]
+
+
+@pytest.mark.parametrize("gate,n,d,E,k", ROUTE_CASES)
+@pytest.mark.parametrize("rows", [True, False])
+def test_dx_of_the_router_is_one_sum_rounded_once(lib, gate, n, d, E, k, rows):
+    """dl Wg meets the expert rows in fp32.  The probabilities and the gates' gradients are such
+    that dl is a multiple of 2^-8 below 2^-1, so of 8 bits or fewer: exact in bf16 too."""
+    cfg = base._cfg(n, d, 8, E, k, "bf16", gate=gate)
+    g = base._gen(n + d)
+    x, Wg = base._randn(g, n, d, dtype="bf16"), base._randn(g, E, d, dtype="bf16")
+    dxp = base._randn(g, n * k, d, dtype="bf16", std=0.1)
+    inv = torch.randperm(n * k, generator=g, device="cuda").to(torch.int32)
+    idx = torch.rand(n, E, generator=g, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous()
+    p = 1.0 / (8 if gate == "renorm" else 16)
+    probs = torch.full((n, E), p, device="cuda")
+    gates = torch.full((n, k), p, device="cuda")
+    dgate = torch.randint(-1, 2, (n, k), generator=g, device="cuda").float()
+    dl = T.logits_backward(gate, probs, idx, gates, dgate)
+    assert torch.equal(dl, dl.to(torch.bfloat16).double())
+    ws = lib.alloc_train_workspace(cfg)
+    dx = torch.full_like(x, float("nan"))
+    lib.moe_route_backward(cfg, x, lib.make_weights(dict(Wg=Wg)), probs, idx, gates, dgate, None, 0.0,
+                           inv if rows else None, dxp if rows else None, dx, None, None, ws)
+    base._ok(lib, ws)
+    want = (dl.cuda() @ Wg.double()).cpu()
+    e = 2 * E * base.V * (dl.abs().cuda() @ Wg.double().abs()).cpu()
+    if rows:
+        own = dxp[inv.long()].view(n, k, d).double()
+        want += own.sum(1).cpu()
+        e += (k + 2) * base.V * (own.abs().sum(1).cpu() + (dl.abs().cuda() @ Wg.double().abs()).cpu())
+    base._within(dx, want, e + base._u("bf16") * (want.abs() + e), "dx")
