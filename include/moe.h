@@ -438,8 +438,8 @@ moe_status moe_expert_ffn_backward(const moe_config *cfg, const void *x_perm,
  * dy act_dtype [n][d]; y_perm, dy_perm act_dtype [n*K][d]; dgate fp32 [n][K].
  * y_perm and dgate may both be NULL (a frozen router).  The gradient of
  * y_shared is dy itself.  An inv_perm entry outside [0, n*K) sets
- * MOE_ERR_BAD_INDEX and is skipped (its dgate is 0); other parts of the outputs
- * may then stay unwritten. */
+ * MOE_ERR_BAD_INDEX and is skipped (its dgate is 0); the outputs are then
+ * not valid as a whole: other parts may stay unwritten. */
 moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const void *y_perm,
                                 const int32_t *inv_perm, const float *topk_gate, void *dy_perm,
                                 float *dgate, void *ws, size_t ws_bytes, void *stream);
@@ -460,8 +460,8 @@ moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const voi
  * products where these run on the tensor cores (dbias sums dl in fp32); dx is one
  * fp32 sum, rounded once.  A topk_idx outside [0, E) sets MOE_ERR_BAD_INDEX
  * and its slot counts as a gate of zero; an inv_perm entry outside [0, n*K) sets
- * it and its row is left out.  Other parts of the outputs may then stay
- * unwritten. */
+ * it and its row is left out.  The outputs are then not valid as a whole: parts
+ * may stay unwritten. */
 moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_weights *w,
                               const float *probs, const int32_t *topk_idx, const float *topk_gate,
                               const float *dgate, const float *f, float aux,

@@ -41,7 +41,7 @@
 // gathered rows are the work then, so two pipeline stages feed the MMAs and the
 // rest of shared memory is a ring of gathered pieces per epilogue warp, 112 KB
 // in flight per SM (GatherRing).  16384 tokens, d 7168, 8 rows each, 256 experts:
-// 404 us, 5.2 TB/s; one launch that stores dl Wg and one that sums took 434 and
+// 404 us, 5.3 TB/s; one launch that stores dl Wg and one that sums took 434 and
 // rounded dl Wg to bf16 in between.  (Gathering into registers instead, 8 or 16
 // epilogue warps: 520 to 770 us.)
 //

@@ -10,7 +10,7 @@
 // ring in shared memory that each thread fills for itself, several rows ahead
 // (cp.async; no other thread reads its part, so no barrier guards the ring):
 // with one row ahead in registers the gradient's one CTA per SM waited for
-// memory (285 us at 16384 x 7168 bf16 against 128 now).
+// memory (the kernel at 16384 x 7168 bf16 285 us, 130 now; 135 the whole call).
 // The sums use two fp32 values per instruction: the norms are bound by
 // instruction issue before they are by HBM.
 // In the gradient a thread owns the same columns of every row it meets, so the
@@ -536,7 +536,7 @@ norm_columns_kernel(moe_norm_config c, const T *__restrict__ x, const float *__r
 // Pieces per thread.  The gradient keeps five values per element (two of the
 // row, gamma, two column sums): 16 elements in 128 registers of 512 threads.
 // (8 elements in 64 registers of 1024 threads pay the sums over the row twice
-// as often: 177 us against 148 at 16384 x 7168 bf16.)
+// as often: before the ring 177 us against 148 at 16384 x 7168 bf16.)
 // The forward with four pieces of 16 bytes in 64 registers: 88 us at 16384 x
 // 7168 bf16; with two pieces 98, with one 124, with 96 registers 108.
 constexpr int fwd_vpt(int vec) { return vec == 1 ? 16 : 4; }
@@ -585,7 +585,9 @@ cudaError_t fwd(const moe_norm_config &c, const T *x, const T *gamma, const T *b
   const int groups = tpr <= 256 ? 256 / tpr : 1, threads = tpr * groups;
   const size_t smem = VEC > 1 ? (size_t)N_FWD_STAGES * VPT * threads * 16
                               : (size_t)N_FWD_STAGES * groups * slot_bytes(c.d, sizeof(T));
-  static int resident[N_FWD_THREADS / 32 + 1] = {};   // CTAs per SM by warps per CTA
+  // CTAs per SM by warps per CTA.  (The ring's size varies with d too where rows are
+  // not whole vectors, but 64 registers a thread are the tighter bound for each.)
+  static int resident[N_FWD_THREADS / 32 + 1] = {};
   int &ctas = resident[threads / 32];
   if (ctas == 0) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
