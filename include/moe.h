@@ -468,6 +468,148 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
                               const int32_t *inv_perm, const void *dx_perm, void *dx, void *dWg,
                               float *dbias, void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Round the layer in a training step: the joint of a block with the residual
+ * stream, dropout, and the loss that the gradient starts from.  (An addition of
+ * this library.)  With blocks l = 0, 1, ... a step runs
+ *   y_0 = norm(x_0);  b_l = block(y_l);  (x_{l+1}, y_{l+1}) = join(x_l, b_l);
+ *   moe_cross_entropy of the last y,
+ * and back: moe_cross_entropy_backward, moe_block_join_backward, the block's
+ * gradient, ...  Types: f32 throughout or bf16 throughout (statistics, sums,
+ * losses and the gradients of vectors fp32).  As above: sums run in fp32 and in
+ * a fixed order, gradients are written, not added, and outputs must not overlap
+ * inputs or each other (except where said).
+ * ------------------------------------------------------------------------ */
+
+/* Dropout of rows x [rows][d]: y = x / (1 - q) where an element is kept, 0
+ * (whatever x holds, a NaN too) where it is dropped, q = T / 65536 with
+ * T = floor(65536 p + 1/2).  What is kept depends on the generator's state and
+ * the element's place alone, so that the gradient is the same call on dy and no
+ * mask is stored: element (r, c) takes 16 bits of the Philox4x32-10 generator
+ * (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as 1, 2, 3",
+ * SC 2011) with key {seed low, seed high} and counter {c / 8, r, offset low,
+ * offset high}: bits 16 (c % 2) .. + 15 of word c % 8 / 2; it is dropped where
+ * they are below T.
+ *   rng: DEVICE pointer to {uint64 seed, uint64 offset}, 8-byte aligned, read when
+ *   the kernel runs (a captured graph follows its contents); may be NULL when
+ *   T = 0.  y may be x itself (with ldy = ldx). */
+typedef struct {
+  int64_t rows;        /* 0 .. 2^32 */
+  int64_t ldx, ldy;    /* as moe_norm_config's: elements between rows, 0 for d */
+  int32_t d;           /* >= 1 */
+  int32_t dtype;       /* MOE_F32 or MOE_BF16 */
+  float p;             /* 0 <= p, and T < 65536 */
+  int32_t reserved;    /* 0 */
+} moe_dropout_config;
+moe_status moe_dropout(const moe_dropout_config *cfg, const void *x, const uint64_t *rng, void *y,
+                       void *stream);
+
+/* Norms of the block joint.  RMS: v_i / sqrt(sum_j v_j^2 / d + eps) * gamma_i;
+ * LAYER: as moe_layernorm. */
+typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
+
+typedef struct {
+  int64_t rows;              /* 0 .. 2^32 */
+  int64_t ldx, ldb, ldr, ldy;          /* as moe_norm_config's, of x, b, r, y */
+  int64_t lddx, lddb, lddr, lddy;      /* of their gradients */
+  int32_t d;                 /* >= 1 */
+  int32_t dtype;             /* MOE_F32 or MOE_BF16: rows, gate, gammas, betas */
+  int32_t post, pre;         /* moe_norm_kind */
+  float eps;                 /* >= 0, of both norms */
+  float scale;               /* of the residual: finite */
+  float dropout;             /* p of moe_dropout, on the block's output; 0: none */
+  int32_t reserved;          /* 0 */
+} moe_join_config;
+
+/* Vectors [d] (device pointers).  gate may be NULL (all ones).  A gamma is needed
+ * with its norm, and a beta may be given with a LAYER norm (NULL: no shift);
+ * other entries must be NULL. */
+typedef struct {
+  const void *gate;                    /* of the block's output */
+  const void *post_gamma, *post_beta;  /* of the norm after the block */
+  const void *pre_gamma, *pre_beta;    /* of the norm before the next one */
+} moe_join_params;
+
+/* Gradients of the vectors, fp32 [d]; a NULL entry is not computed.  An entry
+ * whose vector is not there (and gate's without a gate) must be NULL, but a
+ * LAYER norm's beta gradient may be asked for without a beta. */
+typedef struct {
+  float *gate, *post_gamma, *post_beta, *pre_gamma, *pre_beta;
+} moe_join_grads;
+
+/* The joint of a block with the residual stream, in one pass over the rows:
+ *   z = post(b),   r = scale * x + gate . D(z),   y = pre(r)
+ * with D the dropout of moe_dropout (element (r, c) of the call's rows).  x: the
+ * residual stream, b: the block's output, r: the new stream, y: what the next
+ * block reads (NULL when pre is NONE, needed otherwise).  Both norms and the sum
+ * are formed in fp32 from the fp32 values (y from r before it is rounded).
+ * stats: fp32 [4][rows], or NULL: mean and 1 / deviation of the post norm, then
+ * of the pre norm (0 and 1 for NONE; mean 0 for RMS), as
+ * moe_block_join_backward takes them.  r may be x itself (with ldr = ldx). */
+moe_status moe_block_join(const moe_join_config *cfg, const void *x, const void *b,
+                          const moe_join_params *w, const uint64_t *rng, void *r, void *y,
+                          float *stats, void *stream);
+
+/* Bytes of scratch for moe_block_join_backward (256-byte aligned; no status word
+ * in it).  Host-only. */
+moe_status moe_block_join_workspace_size(const moe_join_config *cfg, size_t *bytes);
+
+/* The joint's gradient, from dr (of r; NULL: zero) and dy (of y; NULL: zero):
+ *   R = dr + [gradient of pre at r, of dy],   dx = scale * R,
+ *   u = D(R),  dz = gate . u,  db = [gradient of post at b, of dz],
+ *   dgate = sum_rows u z,  dpost_gamma = sum_rows dz bh,  dpost_beta = sum_rows dz,
+ *   dpre_gamma = sum_rows dy rh,  dpre_beta = sum_rows dy,
+ * bh and rh the rows that the norms centred and scaled.  b is read with a post
+ * norm or for dgate, r with a pre norm and a dy; else they may be NULL.  dx and
+ * db may each be NULL (not computed).  With rows = 0 the vectors' gradients are
+ * zero. */
+moe_status moe_block_join_backward(const moe_join_config *cfg, const void *b, const void *r,
+                                   const float *stats, const moe_join_params *w,
+                                   const uint64_t *rng, const void *dr, const void *dy, void *dx,
+                                   void *db, const moe_join_grads *grads, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/* Softmax cross entropy of a linear layer over a vocabulary. */
+typedef struct {
+  int32_t n;           /* tokens, 0 .. 1048576 (else MOE_ERR_UNSUPPORTED) */
+  int32_t d;           /* a multiple of 4 (f32) or 8 (bf16), else MOE_ERR_UNSUPPORTED */
+  int32_t vocab;       /* >= 1, of any size (at most INT32_MAX / 2) */
+  int32_t dtype;       /* MOE_F32 or MOE_BF16: x, W and their gradients */
+  float z_loss;        /* finite, >= 0 */
+  int32_t reserved;    /* 0 */
+} moe_loss_config;
+
+/* Bytes of workspace for the two entry points below, a status word at its start
+ * (moe_status_check); nothing else in it lives from one call to the next, and it
+ * may be any workspace that is large enough.  Holds the logits of a piece of the
+ * vocabulary (about 256 MB), 8 bytes per token and 256 entries of the
+ * vocabulary, and a few copies of x.  Host-only. */
+moe_status moe_cross_entropy_workspace_size(const moe_loss_config *cfg, size_t *bytes);
+
+/* Per token t with target v = targets[t]:
+ *   l = x[t] W^T,   lse = log sum_j e^{l_j},   loss = lse - l_v + z_loss * lse^2.
+ * x [n][d], W [vocab][d]; targets int32 [n]; loss, lse fp32 [n].  A negative
+ * target leaves its token out: loss and lse are 0, and whatever its row of x
+ * holds is not read.  A target >= vocab sets MOE_ERR_BAD_INDEX (detail: the
+ * token); the outputs are then not valid.  The logits are never stored as a
+ * whole. */
+moe_status moe_cross_entropy(const moe_loss_config *cfg, const void *x, const void *W,
+                             const int32_t *targets, float *loss, float *lse, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/* Its gradient, from dloss fp32 [n] (of each token's loss) and lse as
+ * moe_cross_entropy wrote it.  The logits are formed again:
+ *   dl_j = dloss * (e^{l_j - lse} (1 + 2 z_loss lse) - [j = v]),
+ *   dx = dl W,   dW = dl^T x.
+ * dx [n][d], dW [vocab][d], each may be NULL.  Rows of dx of left out tokens are
+ * zero, and these tokens add nothing to dW.  bf16: dl is rounded once to bf16
+ * where it is a tensor-core operand (small problems, on the CUDA cores, keep it
+ * in fp32). */
+moe_status moe_cross_entropy_backward(const moe_loss_config *cfg, const void *x, const void *W,
+                                      const int32_t *targets, const float *lse,
+                                      const float *dloss, void *dx, void *dW, void *ws,
+                                      size_t ws_bytes, void *stream);
+
 /* Synchronises `stream`, then returns the workspace's device status word
  * (MOE_OK if no device-side fault was recorded).  detail, if not NULL,
  * receives the detail word (e.g. the offending pair index). */

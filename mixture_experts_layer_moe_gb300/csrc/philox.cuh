@@ -1,0 +1,56 @@
+// The Philox4x32-10 counter-based generator (Salmon, Moraes, Dror, Shaw: "Parallel
+// random numbers: as easy as 1, 2, 3", SC 2011), and what dropout takes of it:
+// eight 16-bit numbers per call, for eight neighbouring elements of a row.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+struct RngState {
+  uint64_t seed, offset;
+};
+
+__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint2 k) {
+#pragma unroll
+  for (int round = 0; round < 10; ++round) {
+    const uint64_t a = (uint64_t)0xD2511F53u * c.x, b = (uint64_t)0xCD9E8D57u * c.z;
+    c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k.x, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ k.y,
+                   (uint32_t)a);
+    k.x += 0x9E3779B9u;
+    k.y += 0xBB67AE85u;
+  }
+  return c;
+}
+
+__device__ __forceinline__ uint4 dropout_bits(const RngState &st, uint32_t block, uint32_t row) {
+  return philox4x32_10(
+      make_uint4(block, row, (uint32_t)st.offset, (uint32_t)(st.offset >> 32)),
+      make_uint2((uint32_t)st.seed, (uint32_t)(st.seed >> 32)));
+}
+
+// Bit i: element 8 block + i of the row is kept.
+__device__ __forceinline__ uint32_t dropout_keep(const RngState &st, uint32_t block, uint32_t row,
+                                                 uint32_t threshold) {
+  const uint4 v = dropout_bits(st, block, row);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t keep = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    keep |= ((w[i] & 0xffffu) >= threshold ? 1u : 0u) << (2 * i);
+    keep |= ((w[i] >> 16) >= threshold ? 1u : 0u) << (2 * i + 1);
+  }
+  return keep;
+}
+
+// The threshold T of a probability (-1: not one that dropout takes), and the
+// factor of what is kept.
+inline int dropout_threshold(float p) {
+  if (!(p >= 0.f) || !(p < 1.f)) return -1;
+  const int t = (int)((double)p * 65536.0 + 0.5);
+  return t < 65536 ? t : -1;
+}
+inline float dropout_factor(int threshold) { return (float)(65536.0 / (65536.0 - threshold)); }
+
+}  // namespace moe

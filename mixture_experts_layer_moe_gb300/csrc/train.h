@@ -73,8 +73,12 @@ struct RowsProduct {
   int add_k;
   int beside;                  // see launch_gemm_grad
   // For a bf16 layer: A and A2 are fp32 (on the CUDA cores), or out and out_u of a
-  // gradient are
+  // gradient (on the CUDA cores also out of a plain product) are
   int a_f32, out_f32;
+  // kRowsPlain on the CUDA cores: elements from one row of out to the next, a
+  // multiple of 4 (0: N).  With it N may be any number; columns up to the next
+  // multiple of 4 are written as zeros.
+  int ldo;
 };
 // fp32, and small bf16 products: at most so many multiplications each.
 constexpr int64_t kSmallProducts = 1 << 24;
@@ -102,12 +106,12 @@ struct GradProduct {
   int a_f32;                // on the CUDA cores, for a bf16 layer: A is fp32
 };
 constexpr int kMaxGradProblems = 3;
+int grad_splits_simt(const GradProduct *p, int count);
 // Up to kMaxGradProblems of them over the same segments in one launch on the CUDA
 // cores (where grads_small: fp32, and small bf16 products), with a second that
 // adds the runs where the rows are cut into several; splits, parts: as
 // grad_splits and grad_scratch (below) say.
 bool grads_small(const GradProduct *p, int count);
-int grad_splits_simt(const GradProduct *p, int count);
 cudaError_t launch_grad_simt(const GradProduct *p, int count, int splits, float *parts, int *status,
                              cudaStream_t s);
 // The same on tensor cores (bf16; SM pairs).

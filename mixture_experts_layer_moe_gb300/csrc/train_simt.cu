@@ -281,13 +281,13 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   pdl_launch_dependents();
   join_groups<TILE>(acc, &pool[0][0][0], me.tx, me.ty, me.g);
   if constexpr (DUAL) join_groups<TILE>(acc2, &pool[0][0][0], me.tx, me.ty, me.g);
-  const int c = n0 + me.col;   // (N is a multiple of 4)
+  const int c = n0 + me.col;   // (N, or out's pitch, is a multiple of 4)
   if (c >= N) return;
 #pragma unroll
   for (int i = 0; i < Place<TILE>::ROWS; ++i) {
     const int r = row0 + me.row + i;
     if (r >= end) continue;
-    const int64_t at = (int64_t)r * N + c;
+    const int64_t at = (int64_t)r * (EPI == kRowsPlain && p.ldo ? p.ldo : N) + c;
     float v[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
     if constexpr (EPI == kRowsRelu) {
 #pragma unroll
@@ -445,6 +445,7 @@ cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   if constexpr (sizeof(T) == 2) {
     // (fp32 dg, du and dl)
     auto wide = p.a_f32 ? rows_simt_kernel<T, kRowsPlain, true, TILE, float>
+                : p.epi == kRowsPlain   ? rows_simt_kernel<T, kRowsPlain, false, TILE, T, float>
                 : p.epi == kRowsReluGrad ? rows_simt_kernel<T, kRowsReluGrad, true, TILE, T, float>
                                          : rows_simt_kernel<T, kRowsSwigluGrad, true, TILE, T, float>;
     if (p.a_f32 || p.out_f32) return launch_pdl(wide, grid, dim3(T_THREADS), 0, s, p, status);

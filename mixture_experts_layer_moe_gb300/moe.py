@@ -63,6 +63,35 @@ class moe_expert_grads(ctypes.Structure):
     _fields_ = [("W1", ctypes.c_void_p), ("W3", ctypes.c_void_p), ("W2", ctypes.c_void_p)]
 
 
+class moe_dropout_config(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("p", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class moe_join_config(ctypes.Structure):
+    _fields_ = ([("rows", ctypes.c_int64)]
+                + [(n, ctypes.c_int64) for n in
+                   ("ldx", "ldb", "ldr", "ldy", "lddx", "lddb", "lddr", "lddy")]
+                + [(n, ctypes.c_int32) for n in ("d", "dtype", "post", "pre")]
+                + [(n, ctypes.c_float) for n in ("eps", "scale", "dropout")]
+                + [("reserved", ctypes.c_int32)])
+
+
+class moe_join_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("gate", "post_gamma", "post_beta", "pre_gamma", "pre_beta")]
+
+
+class moe_join_grads(ctypes.Structure):
+    _fields_ = list(moe_join_params._fields_)
+
+
+class moe_loss_config(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("d", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("z_loss", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 class moe_workspace_layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("status", "logits", "topk_idx", "topk_gate", "counts", "offsets", "perm",
@@ -80,6 +109,8 @@ def _load() -> ctypes.CDLL:
     pp = ctypes.POINTER(moe_expert_pool)
     np_ = ctypes.POINTER(moe_norm_config)
     gp = ctypes.POINTER(moe_expert_grads)
+    dp, lp = ctypes.POINTER(moe_dropout_config), ctypes.POINTER(moe_loss_config)
+    jp, jw, jg = (ctypes.POINTER(t) for t in (moe_join_config, moe_join_params, moe_join_grads))
     sig = {
         "moe_workspace_size": [cfgp, ctypes.POINTER(SZ)],
         "moe_workspace_layout_of": [cfgp, ctypes.POINTER(moe_workspace_layout)],
@@ -103,6 +134,13 @@ def _load() -> ctypes.CDLL:
         "moe_expert_ffn_backward": [cfgp, P, P, wp, P, P, P, P, P, gp, P, SZ, P],
         "moe_combine_backward": [cfgp, P, P, P, P, P, P, P, SZ, P],
         "moe_route_backward": [cfgp, P, wp, P, P, P, P, P, ctypes.c_float, P, P, P, P, P, P, SZ, P],
+        "moe_dropout": [dp, P, P, P, P],
+        "moe_block_join": [jp, P, P, jw, P, P, P, P, P],
+        "moe_block_join_workspace_size": [jp, ctypes.POINTER(SZ)],
+        "moe_block_join_backward": [jp, P, P, P, jw, P, P, P, P, P, jg, P, SZ, P],
+        "moe_cross_entropy_workspace_size": [lp, ctypes.POINTER(SZ)],
+        "moe_cross_entropy": [lp, P, P, P, P, P, P, SZ, P],
+        "moe_cross_entropy_backward": [lp, P, P, P, P, P, P, P, P, SZ, P],
         "moe_status_check": [P, P, ctypes.POINTER(ctypes.c_int32)],
         "moe_status_clear": [P, P],
         "moe_selftest_wait_timeout": [P, ctypes.c_uint64, P],
@@ -425,6 +463,221 @@ def moe_route_backward(cfg, x, w: moe_weights, probs, topk_idx, topk_gate, dgate
                                    float(aux), _ptr(inv_perm), _ptr(dx_perm), _ptr(dx), _ptr(dWg),
                                    _ptr(dbias), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_route_backward")
+
+
+# ------------------------------------------------- round the layer in a training step
+_JOIN_NORM = {"none": 0, "rms": 1, "layer": 2}
+_JOIN_VECTORS = ("gate", "post_gamma", "post_beta", "pre_gamma", "pre_beta")
+
+
+class _Vectors:
+    """A struct of vectors, with the tensors it points to and what they have in common."""
+
+    def __init__(self, struct, tensors: dict, dtype=None):
+        unknown = set(tensors) - set(_JOIN_VECTORS)
+        if unknown:
+            raise ValueError(f"no vectors of a block joint: {sorted(unknown)}")
+        self.tensors = {k: t for k, t in tensors.items() if t is not None}
+        kinds = {(t.numel(), t.dtype, t.device) for t in self.tensors.values()}
+        if len(kinds) > 1:
+            raise ValueError("the vectors of a block joint are of one length, type and device")
+        self.d, self.dtype, self.device = kinds.pop() if kinds else (None, dtype, None)
+        if dtype is not None and self.dtype is not dtype:
+            raise ValueError(f"these vectors of a block joint hold {dtype}")
+        self.ref = ctypes.byref(struct(**{k: _ptr(t) for k, t in self.tensors.items()}))
+
+    def check(self, rows: torch.Tensor, dtype):
+        if self.tensors and (self.d != rows.shape[1] or self.dtype is not dtype
+                             or self.device != rows.device):
+            raise ValueError(f"the vectors of a block joint must hold {rows.shape[1]} values of "
+                             f"{dtype} on {rows.device}")
+
+
+def make_join_params(vectors: dict) -> _Vectors:
+    """The vectors of a block joint from a dict of device tensors (keys gate, post_gamma,
+    post_beta, pre_gamma, pre_beta; missing or None: not there)."""
+    return _Vectors(moe_join_params, vectors)
+
+
+def make_join_grads(vectors: dict) -> _Vectors:
+    """Where a block joint's gradient writes those of its vectors (fp32; missing or None: not
+    computed)."""
+    return _Vectors(moe_join_grads, vectors, torch.float32)
+
+
+def _step_rows(t: Optional[torch.Tensor], like: torch.Tensor) -> tuple[Optional[int], int]:
+    """(pointer, elements between rows) of rows shaped as `like`; None: (None, 0)."""
+    if t is None:
+        return None, 0
+    if t.shape != like.shape or t.dtype is not like.dtype or t.device != like.device:
+        raise ValueError(f"rows must be {list(like.shape)} of {like.dtype} on {like.device}")
+    ld, one = t.stride()
+    d = t.shape[1]
+    if one != 1 and d > 1:
+        raise ValueError("rows must be dense")
+    if t.shape[0] <= 1:
+        return t.data_ptr(), d
+    if ld < d:
+        raise ValueError("rows must not overlap (an expanded tensor: .contiguous())")
+    return t.data_ptr(), ld
+
+
+def _step_dtype(x: torch.Tensor) -> int:
+    code = _NORM_DTYPE.get(x.dtype)
+    if code is None or x.dim() != 2:
+        raise ValueError("rows must be a [rows, d] tensor of float32 or bfloat16")
+    return code
+
+
+def _fp32(t: Optional[torch.Tensor], shape, like: torch.Tensor) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.shape != shape or t.device != like.device:
+        raise ValueError(f"expected a float32 tensor of {list(shape)} on {like.device}")
+    return _ptr(t)
+
+
+def _rng(rng: Optional[torch.Tensor], like: torch.Tensor) -> Optional[int]:
+    """The generator's state: a device tensor of two 64-bit integers, seed and offset."""
+    if rng is None:
+        return None
+    if rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2 or rng.device != like.device:
+        raise ValueError(f"the generator's state is a tensor of two 64-bit integers on {like.device}")
+    return _ptr(rng)
+
+
+def _bytes(ws: torch.Tensor, like: torch.Tensor) -> tuple[int, int]:
+    if ws.dtype is not torch.uint8 or ws.device != like.device:
+        raise ValueError(f"a workspace is a uint8 tensor on {like.device}")
+    return _ptr(ws), ws.numel()
+
+
+@functools.lru_cache(maxsize=256)
+def _dropout_config(rows, ldx, ldy, d, dtype, p):
+    return ctypes.byref(moe_dropout_config(rows, ldx, ldy, d, dtype, p, 0))
+
+
+def moe_dropout(x, y, p: float, rng=None, stream=None):
+    """y = dropout of x [rows, d] (rows may lie apart; y may be x).  rng: device tensor of two
+    64-bit integers (seed, offset), read when the kernel runs; the same state gives the same
+    elements, so the gradient is this call on dy."""
+    code = _step_dtype(x)
+    n, d = x.shape
+    xp, ldx = _step_rows(x, x)
+    yp, ldy = _step_rows(y, x)
+    _check(_lib.moe_dropout(_dropout_config(n, ldx, ldy, d, code, p), xp, _rng(rng, x), yp,
+                            _stream(stream)), "moe_dropout")
+
+
+@functools.lru_cache(maxsize=256)
+def _join_config(rows, ldx, ldb, ldr, ldy, lddx, lddb, lddr, lddy, d, dtype, post, pre, eps, scale,
+                 p):
+    return ctypes.byref(moe_join_config(rows, ldx, ldb, ldr, ldy, lddx, lddb, lddr, lddy, d, dtype,
+                                        _JOIN_NORM[post], _JOIN_NORM[pre], eps, scale, p, 0))
+
+
+def moe_block_join(x, b, params: _Vectors, r, y, stats, *, post="rms", pre="rms", scale=1.0, p=0.0,
+                   rng=None, eps=1e-5, stream=None):
+    """r = scale x + gate . dropout(post(b)), y = pre(r); rows [rows, d] may lie apart.  params:
+    make_join_params; y None when pre is "none"; stats fp32 [4, rows] or None."""
+    code = _step_dtype(x)
+    n, d = x.shape
+    xp, ldx = _step_rows(x, x)
+    bp, ldb = _step_rows(b, x)
+    rp, ldr = _step_rows(r, x)
+    yp, ldy = _step_rows(y, x)
+    params.check(x, x.dtype)
+    _check(_lib.moe_block_join(
+        _join_config(n, ldx, ldb, ldr, ldy, 0, 0, 0, 0, d, code, post, pre, eps, scale, p), xp, bp,
+        params.ref, _rng(rng, x), rp, yp, _fp32(stats, (4, n), x), _stream(stream)),
+        "moe_block_join")
+
+
+def moe_block_join_workspace_size(rows: int, d: int, dtype: str) -> int:
+    """dtype "f32" or "bf16".  Enough for any norms and leading dimensions."""
+    out = ctypes.c_size_t(0)
+    c = moe_join_config(rows=rows, d=d, dtype=_DTYPE[dtype])
+    _check(_lib.moe_block_join_workspace_size(ctypes.byref(c), ctypes.byref(out)),
+           "moe_block_join_workspace_size")
+    return out.value
+
+
+def moe_block_join_backward(b, r, stats, params: _Vectors, dr, dy, dx, db, grads: _Vectors, ws, *,
+                            post="rms", pre="rms", scale=1.0, p=0.0, rng=None, stream=None):
+    """The gradient of moe_block_join (with its post, pre, scale, p and rng) from dr and dy (either
+    may be None); dx and db may be None, grads: make_join_grads, ws: scratch (uint8) of
+    moe_block_join_workspace_size bytes."""
+    like = next((t for t in (dr, dy, b) if t is not None), None)
+    if like is None:
+        raise ValueError("a block joint's gradient needs dr, dy or b")
+    code = _step_dtype(like)
+    n, d = like.shape
+    bp, ldb = _step_rows(b, like)
+    rp, ldr = _step_rows(r, like)
+    drp, lddr = _step_rows(dr, like)
+    dyp, lddy = _step_rows(dy, like)
+    dxp, lddx = _step_rows(dx, like)
+    dbp, lddb = _step_rows(db, like)
+    params.check(like, like.dtype)
+    grads.check(like, torch.float32)
+    _check(_lib.moe_block_join_backward(
+        _join_config(n, 0, ldb, ldr, 0, lddx, lddb, lddr, lddy, d, code, post, pre, 0.0, scale, p),
+        bp, rp, _fp32(stats, (4, n), like), params.ref, _rng(rng, like), drp, dyp, dxp, dbp,
+        grads.ref, *_bytes(ws, like), _stream(stream)), "moe_block_join_backward")
+
+
+@functools.lru_cache(maxsize=256)
+def _loss_config(n, d, vocab, dtype, z_loss):
+    return ctypes.byref(moe_loss_config(n, d, vocab, dtype, z_loss, 0))
+
+
+def _loss_operands(x, W, targets, z_loss):
+    code = _step_dtype(x)
+    n, d = x.shape
+    if W.dim() != 2 or W.shape[1] != d or W.dtype is not x.dtype or W.device != x.device:
+        raise ValueError(f"W must be [vocab, {d}] of {x.dtype} on {x.device}")
+    if targets.shape != (n,) or targets.dtype is not torch.int32 or targets.device != x.device:
+        raise ValueError(f"targets must be [{n}] of int32 on {x.device}")
+    return (_loss_config(n, d, W.shape[0], code, z_loss), _ptr(x), _ptr(W), _ptr(targets)), n
+
+
+def moe_cross_entropy_workspace_size(n: int, d: int, vocab: int, dtype: str) -> int:
+    """dtype "f32" or "bf16"."""
+    out = ctypes.c_size_t(0)
+    c = moe_loss_config(n, d, vocab, _DTYPE[dtype], 0.0, 0)
+    _check(_lib.moe_cross_entropy_workspace_size(ctypes.byref(c), ctypes.byref(out)),
+           "moe_cross_entropy_workspace_size")
+    return out.value
+
+
+def alloc_cross_entropy_workspace(n: int, d: int, vocab: int, dtype: str,
+                                  device="cuda") -> torch.Tensor:
+    """A workspace tensor of moe_cross_entropy_workspace_size bytes, its status word zeroed."""
+    ws = torch.empty(moe_cross_entropy_workspace_size(n, d, vocab, dtype), dtype=torch.uint8,
+                     device=device)
+    assert ws.data_ptr() % 256 == 0
+    ws[:256].zero_()
+    return ws
+
+
+def moe_cross_entropy(x, W, targets, loss, lse, ws, z_loss=0.0, stream=None):
+    """loss, lse fp32 [n] of x [n, d] W [vocab, d]^T against targets int32 [n] (negative: left
+    out); ws: moe_cross_entropy_workspace_size bytes (alloc_cross_entropy_workspace)."""
+    args, n = _loss_operands(x, W, targets, z_loss)
+    _check(_lib.moe_cross_entropy(*args, _fp32(loss, (n,), x), _fp32(lse, (n,), x),
+                                  *_bytes(ws, x), _stream(stream)), "moe_cross_entropy")
+
+
+def moe_cross_entropy_backward(x, W, targets, lse, dloss, dx, dW, ws, z_loss=0.0, stream=None):
+    """dx, dW (either may be None) from dloss fp32 [n] and lse as moe_cross_entropy wrote it."""
+    args, n = _loss_operands(x, W, targets, z_loss)
+    for t, like in ((dx, x), (dW, W)):
+        if t is not None and (t.shape != like.shape or t.dtype is not like.dtype
+                              or t.device != like.device):
+            raise ValueError("dx and dW are shaped and typed as x and W")
+    _check(_lib.moe_cross_entropy_backward(*args, _fp32(lse, (n,), x), _fp32(dloss, (n,), x),
+                                           _ptr(dx), _ptr(dW), *_bytes(ws, x), _stream(stream)),
+           "moe_cross_entropy_backward")
 
 
 def moe_status_check(ws, stream=None) -> tuple[int, int]:

@@ -1,0 +1,643 @@
+"""GPU: dropout, the block joint and the cross entropy against the float64 oracle
+(oracle/step_oracle.py).
+
+Tolerances are element by element and come from the arithmetic.  With u the half
+step of the output type (bf16 2^-8, fp32 2^-24) and v = 2^-24: a value rounded
+once is off by u |value|; an fp32 operation by v; a sum of m fp32 terms by at most
+m v sum |term| in any order (2 m v for products on the tensor cores, whose adders
+may truncate); an operand's error goes through a product with the absolute values
+of the other one; e^a with the hardware's exponential by 2^-20 + 2^-22 |a|
+relative (its argument is rounded in fp32).  Each bound below is that, written out.
+"""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import step_oracle as S
+
+pytestmark = pytest.mark.gpu
+
+V = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+TINY = 1e-37
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from mixture_experts_layer_moe_gb300 import build
+    build.build()
+    from mixture_experts_layer_moe_gb300 import moe
+    assert torch.cuda.is_available()
+    return moe
+
+
+def _u(dtype):
+    return torch.finfo(DT[dtype]).eps / 2
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, *shape, dtype="f32", std=1.0, mean=0.0):
+    return (torch.randn(shape, generator=g, device="cuda") * std + mean).to(DT[dtype])
+
+
+def _within(got, want, bound, what):
+    got = got.detach().cpu().double()
+    assert torch.isfinite(got).all(), what
+    over = (got - want).abs() - bound - TINY
+    assert over.max().item() <= 0, (what, over.max().item(),
+                                    ((got - want).abs() / (bound + TINY)).max().item())
+
+
+def _rows(t, pad, fill=float("nan")):
+    """t's rows inside a buffer whose rows are pad elements longer, the rest filled."""
+    if pad == 0:
+        return t.contiguous()
+    buf = torch.full((t.shape[0], t.shape[1] + pad), fill, dtype=t.dtype, device="cuda")
+    buf[:, :t.shape[1]] = t
+    return buf[:, :t.shape[1]]
+
+
+def _out(rows, d, pad, dtype):
+    return _rows(torch.full((rows, d), float("nan"), dtype=DT[dtype], device="cuda"), pad, 7.0)
+
+
+def _gaps_stay(t, pad):
+    rows, d = t.shape
+    return pad == 0 or bool((t.as_strided((rows, pad), (d + pad, 1), d) == 7.0).all())
+
+
+def _rng(seed, offset):
+    return torch.tensor([seed, offset], dtype=torch.int64, device="cuda")
+
+
+# -------------------------------------------------------------------- dropout
+# rows, d, pad, dtype: single elements, widths round the vectors, rows apart, wide rows
+ROWS = [(r, d, pad, dt)
+        for dt in ("bf16", "f32")
+        for r, d, pad in ((1, 1, 0), (3, 2, 0), (1, 2880, 0), (9, 8, 0), (33, 127, 0), (17, 128, 3),
+                          (700, 256, 8), (5, 511, 1), (40, 520, 0), (257, 1001, 3), (6, 1024, 0),
+                          (900, 2880, 0), (3, 4104, 8), (77, 7168, 0), (4, 8192, 0), (3, 8200, 0),
+                          (2, 16392, 0), (3, 9001, 2))]
+
+
+@pytest.mark.parametrize("rows,d,pad,dtype", ROWS)
+def test_dropout(lib, rows, d, pad, dtype):
+    g = _gen(rows * 3 + d)
+    x, y = _rows(_randn(g, rows, d, dtype=dtype), pad), _out(rows, d, pad, dtype)
+    rng = _rng(2 ** 62 + 12345 * rows, -7 - d)
+    lib.moe_dropout(x, y, 0.3, rng)
+    want = S.dropout(x, rng, 0.3)
+    # the factor is rounded to fp32, then the product, then the result
+    _within(y, want, (2 * V + _u(dtype)) * want.abs(), "y")
+    assert torch.equal(y.cpu() == 0, want == 0) and _gaps_stay(y, pad)
+    # in place, and no dropout
+    z = _rows(x.contiguous(), pad, 7.0)
+    lib.moe_dropout(z, z, 0.3, rng)
+    assert torch.equal(z, y) and _gaps_stay(z, pad)
+    lib.moe_dropout(x, y, 0.0)
+    assert torch.equal(y, x)
+
+
+def test_dropout_hides_what_it_drops(lib):
+    """A NaN or infinity in a dropped place becomes 0; a kept one stays."""
+    keep = S.keep(5, 6, 9, 300, 0.5)
+    for bad in (float("nan"), float("inf")):
+        x = torch.full((9, 300), bad, device="cuda")
+        y = torch.empty_like(x)
+        lib.moe_dropout(x, y, 0.5, _rng(5, 6))
+        assert (y.cpu()[~keep] == 0).all() and not torch.isfinite(y.cpu()[keep]).any()
+
+
+def test_dropout_in_a_graph_follows_the_state(lib):
+    x, y = torch.ones(64, 512, device="cuda"), torch.empty(64, 512, device="cuda")
+    rng = _rng(1, 0)
+    lib.moe_dropout(x, y, 0.5, rng)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.moe_dropout(x, y, 0.5, rng)
+        rng[1] += 1
+    rng[1] = 0
+    for offset in range(3):
+        graph.replay()
+        assert torch.equal(y.cpu() != 0, S.keep(1, offset, 64, 512, 0.5))
+
+
+# ----------------------------------------------------------------- block joint
+def _adds(d):
+    """Terms that one fp32 sum over a row adds up in sequence, at most."""
+    return 64 + d / 256
+
+
+def _join_case(rows, d, pad, dtype, post, pre, gate, p, scale, beta=True, seed=0):
+    g = _gen(seed + rows * 7 + d)
+    params = {}
+    if gate:
+        params["gate"] = _randn(g, d, dtype=dtype, std=0.5, mean=0.5)
+    for side, kind in (("post", post), ("pre", pre)):
+        if kind != "none":
+            params[side + "_gamma"] = _randn(g, d, dtype=dtype, std=0.2, mean=1.0)
+        if kind == "layer" and beta:
+            params[side + "_beta"] = _randn(g, d, dtype=dtype)
+    x = _rows(_randn(g, rows, d, dtype=dtype, std=2.0, mean=0.3), pad)
+    b = _rows(_randn(g, rows, d, dtype=dtype, std=0.7, mean=0.1), pad)
+    dr, dy = (_rows(_randn(g, rows, d, dtype=dtype), pad) for _ in range(2))
+    kw = dict(post=post, pre=pre, scale=scale, p=p, rng=_rng(seed + 99, rows + d) if p else None)
+    return params, x, b, dr, (dy if pre != "none" else None), kw
+
+
+def _vec(params, key, d, other):
+    t = params.get(key)
+    return torch.full((d,), float(other), dtype=torch.float64) if t is None else t.cpu().double()
+
+
+def _norm_bound(v, ev, mean, rstd, out, gamma, beta, kind, d):
+    """Error bounds of a norm's output, mean and rstd whose rows v are off by ev."""
+    if kind == "none":
+        return ev, torch.zeros_like(rstd), torch.zeros_like(rstd)
+    n, c = _adds(d), (v - mean[:, None]).abs()
+    dm = n * V * v.abs().mean(1) + ev.mean(1) if kind == "layer" else torch.zeros_like(rstd)
+    er = ((n + 8) * V + (dm * rstd) ** 2 + (c * ev).mean(1) * rstd ** 2 + (ev ** 2).mean(1) * rstd ** 2)
+    eo = (gamma.abs() * rstd[:, None] * (ev + dm[:, None] + c * (4 * V + er[:, None]))
+          + 2 * V * (out.abs() + beta.abs()))
+    return eo, dm + V * mean.abs(), rstd * er
+
+
+def _check_join(lib, case, pad, dtype):
+    params, x, b, _, _, kw = case
+    rows, d = x.shape
+    r, stats = _out(rows, d, pad, dtype), torch.full((4, rows), float("nan"), device="cuda")
+    y = _out(rows, d, pad, dtype) if kw["pre"] != "none" else None
+    lib.moe_block_join(x, b, lib.make_join_params(params), r, y, stats, **kw)
+    wr, wy, ws, wz = S.join(x, b, params, **kw)
+    vec = lambda key, other: _vec(params, key, d, other)
+    zero = torch.zeros(rows, d, dtype=torch.float64)
+    b64 = b.cpu().double()
+    ez, em1, er1 = _norm_bound(b64, zero, ws[0], ws[1], wz, vec("post_gamma", 1),
+                               vec("post_beta", 0), kw["post"], d)
+    f = S.factors(kw["rng"], rows, d, kw["p"])
+    gz = f * wz * vec("gate", 1)
+    er = (vec("gate", 1).abs() * f * (ez + 2 * V * wz.abs()) + 2 * V * gz.abs()
+          + V * (kw["scale"] * x.cpu().double()).abs() + V * wr.abs())
+    _within(r, wr, er + _u(dtype) * (wr.abs() + er), "r")
+    bounds = [em1, er1 + TINY]
+    if y is not None:
+        ey, em2, er2 = _norm_bound(wr, er, ws[2], ws[3], wy, vec("pre_gamma", 1), vec("pre_beta", 0),
+                                   kw["pre"], d)
+        _within(y, wy, ey + _u(dtype) * (wy.abs() + ey), "y")
+    else:
+        em2 = er2 = torch.zeros(rows, dtype=torch.float64)
+    _within(stats, ws, torch.stack((bounds[0], bounds[1], em2, er2)) + V * ws.abs(), "stats")
+    assert _gaps_stay(r, pad) and (y is None or _gaps_stay(y, pad))
+    # without statistics, and in place: the same bits
+    r2 = _rows(x.contiguous(), pad, 7.0)
+    y2 = _out(rows, d, pad, dtype) if y is not None else None
+    lib.moe_block_join(r2, b, lib.make_join_params(params), r2, y2, None, **kw)
+    assert torch.equal(r2, r) and (y is None or torch.equal(y2, y)) and _gaps_stay(r2, pad)
+    return r, stats
+
+
+def _back_bound(w, ew, h, eh, rstd, kind, d):
+    """The norm's gradient from w and the normed rows h: its value's error bound."""
+    if kind == "none":
+        return ew
+    n = _adds(d)
+    mean = lambda t: t.mean(1, keepdim=True)
+    m1, m2 = mean(w) if kind == "layer" else 0 * mean(w), mean(w * h)
+    e1 = mean(ew) + (n + 2) * V * mean(w.abs()) if kind == "layer" else 0 * mean(w)
+    e2 = mean(ew * h.abs() + w.abs() * eh) + (n + 8) * V * mean((w * h).abs())
+    return rstd[:, None] * (ew + e1 + h.abs() * e2 + m2.abs() * eh
+                            + 4 * V * (w.abs() + m1.abs() + (h * m2).abs()))
+
+
+def _check_join_backward(lib, case, r, stats, pad, dtype):
+    params, _, b, dr, dy, kw = case
+    rows, d = b.shape
+    kept = [k for k in ("gate", "post_gamma", "post_beta", "pre_gamma", "pre_beta")
+            if (k in params or (k.endswith("beta") and kw[k.split("_")[0]] == "layer"))]
+    grads = {k: torch.full((d,), 9.0, device="cuda") for k in kept}
+    dx, db = _out(rows, d, pad, dtype), _out(rows, d, pad, dtype)
+    ws = torch.empty(lib.moe_block_join_workspace_size(rows, d, dtype), dtype=torch.uint8,
+                     device="cuda")
+    w = lib.make_join_params(params)
+    back = lambda dr, dy, dx, db, grads: lib.moe_block_join_backward(
+        b, r, stats, w, dr, dy, dx, db, lib.make_join_grads(grads), ws, **kw)
+    back(dr, dy, dx, db, grads)
+    wdx, wdb, wg = S.join_backward(b, r, stats, params, dr, dy, **kw)
+    vec = lambda key, other: _vec(params, key, d, other)
+    st = stats.cpu().double()
+    R = dr.cpu().double()
+    eR = torch.zeros_like(R)
+    eg = {}
+    if dy is not None:
+        dy64 = dy.cpu().double()
+        rh = (r.cpu().double() - st[2][:, None]) * st[3][:, None]
+        wy = dy64 * vec("pre_gamma", 1)
+        G = S._back(wy, rh, st[3], kw["pre"])
+        eR = _back_bound(wy, V * wy.abs(), rh, 3 * V * rh.abs(), st[3], kw["pre"], d)
+        eR = eR + 2 * V * (R.abs() + G.abs())
+        R = R + G
+        eg["pre_gamma"] = (rows + 16) * V * (dy64 * rh).abs().sum(0) + 3 * V * (dy64 * rh).abs().sum(0)
+        eg["pre_beta"] = (rows + 16) * V * dy64.abs().sum(0)
+    _within(dx, wdx, abs(kw["scale"]) * eR + V * wdx.abs() + _u(dtype) * (wdx.abs() + eR), "dx")
+    f = S.factors(kw["rng"], rows, d, kw["p"])
+    b64 = b.cpu().double()
+    bh = b64 if kw["post"] == "none" else (b64 - st[0][:, None]) * st[1][:, None]
+    ebh = 0 * bh if kw["post"] == "none" else 3 * V * bh.abs()
+    u, eu = f * R, f * (eR + 2 * V * R.abs())
+    a = (vec("gate", 1) * vec("post_gamma", 1)).abs()
+    wz = u * vec("gate", 1) * vec("post_gamma", 1)
+    ew = a * eu + 3 * V * wz.abs()
+    eb = _back_bound(wz, ew, bh, ebh, st[1], kw["post"], d)
+    _within(db, wdb, eb + _u(dtype) * (wdb.abs() + eb), "db")
+    A, B = (u * bh).sum(0), u.sum(0)
+    eA = (eu * bh.abs() + u.abs() * ebh).sum(0) + (rows + 16) * V * (u * bh).abs().sum(0)
+    eB = eu.sum(0) + (rows + 16) * V * u.abs().sum(0)
+    gamma, beta, gate = vec("post_gamma", 1).abs(), vec("post_beta", 0).abs(), vec("gate", 1).abs()
+    eg["gate"] = gamma * eA + beta * eB + 3 * V * (gamma * A.abs() + beta * B.abs())
+    eg["post_gamma"] = gate * (eA + 2 * V * A.abs())
+    eg["post_beta"] = gate * (eB + 2 * V * B.abs())
+    for k in kept:
+        _within(grads[k], wg[k], eg[k], k)
+    assert _gaps_stay(dx, pad) and _gaps_stay(db, pad)
+    # each output alone: the same bits
+    for k in kept:
+        one = {k: torch.full((d,), 5.0, device="cuda")}
+        back(dr, dy, None, None, one)
+        assert torch.equal(one[k], grads[k]), k
+    dx2, db2 = _out(rows, d, pad, dtype), _out(rows, d, pad, dtype)
+    back(dr, dy, dx2, None, {})
+    back(dr, dy, None, db2, {})
+    assert torch.equal(dx2, dx) and torch.equal(db2, db)
+
+
+KINDS = list(itertools.product(("none", "rms", "layer"), repeat=2))
+
+
+@pytest.mark.parametrize("i,rows,d,pad,dtype", [(i, *c) for i, c in enumerate(ROWS)])
+def test_join(lib, i, rows, d, pad, dtype):
+    post, pre = KINDS[i % 9]
+    if d < 3:      # (a norm's gradient over one or two elements is all cancellation)
+        post = pre = "none"
+    case = _join_case(rows, d, pad, dtype, post, pre, gate=i % 2 == 0, p=(0.0, 0.25, 0.5)[i % 3],
+                      scale=(1.0, 0.75)[i % 2])
+    r, stats = _check_join(lib, case, pad, dtype)
+    _check_join_backward(lib, case, r, stats, pad, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,pad", [(96, 0), (96, 3), (1160, 0), (8448, 0)])
+@pytest.mark.parametrize("post,pre", KINDS)
+def test_join_kinds(lib, post, pre, d, pad, dtype):
+    for gate, p, beta in ((True, 0.1, True), (False, 0.0, False)):
+        case = _join_case(41, d, pad, dtype, post, pre, gate, p, 0.5, beta, seed=3)
+        r, stats = _check_join(lib, case, pad, dtype)
+        _check_join_backward(lib, case, r, stats, pad, dtype)
+
+
+@pytest.mark.parametrize("d", [64, 100, 9000])
+def test_join_backward_of_one_gradient(lib, d):
+    """dr alone, dy alone, neither: the missing one counts as zero."""
+    params, x, b, dr, dy, kw = _join_case(11, d, 0, "f32", "layer", "rms", True, 0.2, 1.0)
+    r, stats = torch.empty_like(x), torch.empty(4, 11, device="cuda")
+    w = lib.make_join_params(params)
+    lib.moe_block_join(x, b, w, r, torch.empty_like(x), stats, **kw)
+    ws = torch.empty(lib.moe_block_join_workspace_size(11, d, "f32"), dtype=torch.uint8,
+                     device="cuda")
+
+    def back(dr, dy):
+        out = [torch.full_like(x, float("nan")) for _ in range(2)]
+        grads = {k: torch.full((d,), float("nan"), device="cuda") for k in params}
+        lib.moe_block_join_backward(b, r, stats, w, dr, dy, *out, lib.make_join_grads(grads), ws, **kw)
+        return out + list(grads.values())
+
+    zero = torch.zeros_like(x)
+    for given, full in (((dr, None), (dr, zero)), ((None, dy), (zero, dy)), ((None, None), (zero, zero))):
+        for got, want in zip(back(*given), back(*full)):
+            assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("d", [64, 67, 9000])
+def test_join_keeps_a_nan_in_its_row(lib, d):
+    params, x, b, dr, dy, kw = _join_case(6, d, 0, "bf16", "rms", "rms", False, 0.0, 1.0)
+    x[2, 5] = float("nan")
+    dr[4, 7] = float("inf")
+    r, y, stats = torch.empty_like(x), torch.empty_like(x), torch.empty(4, 6, device="cuda")
+    w = lib.make_join_params(params)
+    lib.moe_block_join(x, b, w, r, y, stats, **kw)
+    others = [0, 1, 3, 4, 5]
+    assert torch.isnan(y[2]).all() and torch.isfinite(y[others]).all()
+    assert torch.isfinite(r[2, torch.arange(d) != 5]).all()
+    dx, db = torch.empty_like(x), torch.empty_like(x)
+    ws = torch.empty(lib.moe_block_join_workspace_size(6, d, "bf16"), dtype=torch.uint8, device="cuda")
+    lib.moe_block_join_backward(b, r, stats, w, dr, dy, dx, db, lib.make_join_grads({}), ws, **kw)
+    clean = [0, 1, 3, 5]
+    assert torch.isfinite(dx[clean]).all() and torch.isfinite(db[clean]).all()
+
+
+def test_join_without_rows(lib):
+    e, v = torch.empty(0, 16, device="cuda"), torch.ones(16, device="cuda")
+    params = lib.make_join_params(dict(gate=v, post_gamma=v, pre_gamma=v))
+    st, ws = torch.empty(4, 0, device="cuda"), torch.empty(0, dtype=torch.uint8, device="cuda")
+    lib.moe_block_join(e, e, params, e, e, st)
+    grads = {k: torch.full((16,), 3.0, device="cuda") for k in ("gate", "post_gamma", "pre_gamma")}
+    lib.moe_block_join_backward(e, e, st, params, e, e, e, e, lib.make_join_grads(grads), ws)
+    assert all(t.abs().max() == 0 for t in grads.values())
+    lib.moe_dropout(e, e, 0.5, _rng(1, 1))
+
+
+# --------------------------------------------------------------- cross entropy
+# n, d, vocab, dtype, share left out: single tokens and entries, sizes round the tiles, odd
+# vocabularies, long reductions, several pieces of the vocabulary
+LOSS_CASES = [
+    (1, 8, 1, "bf16", 0.0), (1, 8, 2, "bf16", 0.0), (3, 16, 5, "bf16", 0.0), (2, 64, 257, "bf16", 0.0),
+    (33, 72, 300, "bf16", 0.3), (5, 264, 4099, "bf16", 0.0), (128, 256, 1000, "bf16", 0.1),
+    (129, 512, 513, "bf16", 0.5), (255, 1024, 2051, "bf16", 0.0), (256, 64, 256, "bf16", 0.0),
+    (257, 128, 8200, "bf16", 0.2), (600, 320, 3001, "bf16", 0.1), (1, 2880, 20011, "bf16", 0.0),
+    (40, 4096, 769, "bf16", 0.5), (1100, 512, 511, "bf16", 0.05), (2500, 64, 777, "bf16", 0.1),
+    (1, 4, 1, "f32", 0.0), (1, 4, 3, "f32", 0.0), (3, 12, 5, "f32", 0.0), (2, 64, 257, "f32", 0.5),
+    (33, 36, 300, "f32", 0.3), (256, 128, 4099, "f32", 0.1), (70, 260, 515, "f32", 0.0),
+    (1000, 64, 1027, "f32", 0.2), (2500, 16, 130, "f32", 0.1), (17000, 8, 40, "f32", 0.5),
+]
+
+
+def _loss_case(n, d, vocab, dtype, out, seed=0):
+    g = _gen(seed + n + d + vocab)
+    W = _randn(g, vocab, d, dtype=dtype, std=1.5 * d ** -0.5)
+    t = torch.randint(vocab, (n,), generator=g, device="cuda")
+    boost = 4 * torch.rand(n, 1, generator=g, device="cuda")
+    x = (_randn(g, n, d) + boost * W[t].float()).to(DT[dtype])
+    left = torch.rand(n, generator=g, device="cuda") < out
+    t = torch.where(left, -1 - t, t).to(torch.int32)
+    x[left] = float("nan")          # (what a left out row holds is not read)
+    return x, W, t, left
+
+
+def _ok(lib, ws):
+    st, detail = lib.moe_status_check(ws)
+    assert st == 0, (lib.status_string(st), detail)
+
+
+def _logit_error(x, W, dtype):
+    """Bound of the logits' errors (rows that count)."""
+    k = 2 if dtype == "bf16" else 1
+    return k * x.shape[1] * V * (x.cpu().double().abs() @ W.cpu().double().abs().T)
+
+
+@pytest.mark.parametrize("z_loss", [0.0, 1e-3])
+@pytest.mark.parametrize("n,d,vocab,dtype,out", LOSS_CASES)
+def test_cross_entropy(lib, n, d, vocab, dtype, out, z_loss):
+    x, W, t, left = _loss_case(n, d, vocab, dtype, out)
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, dtype)
+    ws[256:] = 0xFF                 # (a NaN wherever the call reads what it did not write)
+    loss, lse = (torch.full((n,), float("nan"), device="cuda") for _ in range(2))
+    lib.moe_cross_entropy(x, W, t, loss, lse, ws, z_loss)
+    _ok(lib, ws)
+    clean = torch.where(left[:, None], 0, x)
+    wloss, wlse, logits = S.cross_entropy(clean, W, t, z_loss)
+    el = _logit_error(clean, W, dtype)
+    p = torch.softmax(logits, 1)
+    top = logits.amax(1, keepdim=True)
+    e = ((p * (el + 2 ** -20 + 2 ** -22 * (top - logits))).sum(1) + (64 + vocab / 8192) * V
+         + 2 * V * (wlse.abs() + top[:, 0].abs()))
+    at = t.cpu().long().clamp(min=0)[:, None]
+    counted = (t >= 0).cpu()
+    _within(lse, wlse, torch.where(counted, e, 0.0), "lse")
+    eloss = (e + el.gather(1, at)[:, 0] + 2 * V * (wlse.abs() + logits.gather(1, at)[:, 0].abs())
+             + z_loss * (2 * wlse.abs() * e + e * e + 4 * V * wlse ** 2))
+    _within(loss, wloss, torch.where(counted, eloss, 0.0), "loss")
+    again = torch.empty_like(loss), torch.empty_like(lse)
+    lib.moe_cross_entropy(x, W, t, *again, ws, z_loss)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("z_loss", [0.0, 1e-3])
+@pytest.mark.parametrize("n,d,vocab,dtype,out", LOSS_CASES)
+def test_cross_entropy_backward(lib, n, d, vocab, dtype, out, z_loss):
+    x, W, t, left = _loss_case(n, d, vocab, dtype, out, 5)
+    clean = torch.where(left[:, None], 0, x)
+    lse = S.cross_entropy(clean, W, t, z_loss)[1].float().cuda()
+    dloss = _randn(_gen(n), n, std=1.0)
+    dloss[left] = float("nan")
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, dtype)
+    ws[256:] = 0xFF
+    dx, dW = torch.full_like(x, float("nan")), torch.full_like(W, float("nan"))
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, dx, dW, ws, z_loss)
+    _ok(lib, ws)
+    wdx, wdW, wdl = S.cross_entropy_backward(clean, W, t, lse, torch.where(left, 0, dloss), z_loss)
+    aW, ax = W.cpu().double().abs(), clean.cpu().double().abs()
+    counted = (t >= 0).cpu()[:, None]
+    ls = lse.cpu().double()[:, None]
+    logits = clean.cpu().double() @ W.cpu().double().T
+    f = (1 + 2 * z_loss * ls).abs()
+    p = torch.exp(logits - ls) * f
+    hot = torch.zeros_like(p).scatter_(1, t.cpu().long().clamp(min=0)[:, None], 1.0)
+    el = _logit_error(clean, W, dtype)
+    edl = (torch.where(left, 0, dloss).abs().cpu().double()[:, None]
+           * (p * (el + el * el + 2 ** -20 + 2 ** -22 * (logits - ls).abs() + 4 * V) + 3 * V * (p + hot)))
+    edl = torch.where(counted, edl, 0.0)
+    edl = edl + _u(dtype) * (wdl.abs() + edl)
+    k = 2 if dtype == "bf16" else 1
+    adl = wdl.abs() + edl
+    ex = (edl + k * (vocab + 16) * V * adl) @ aW
+    _within(dx, wdx, ex + _u(dtype) * (wdx.abs() + ex), "dx")
+    assert (dx[left] == 0).all()
+    eW = (edl + k * (n + 16) * V * adl).T @ ax
+    _within(dW, wdW, eW + _u(dtype) * (wdW.abs() + eW), "dW")
+    # either alone: the same bits
+    one = torch.empty_like(dx), torch.empty_like(dW)
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, one[0], None, ws, z_loss)
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, None, one[1], ws, z_loss)
+    assert torch.equal(one[0], dx) and torch.equal(one[1], dW)
+
+
+@pytest.mark.parametrize("n,d,vocab,dtype", [(40, 64, 500, "bf16"), (300, 512, 3000, "bf16"),
+                                             (40, 64, 500, "f32")])
+def test_cross_entropy_of_no_counted_token(lib, n, d, vocab, dtype):
+    x, W, t, _ = _loss_case(n, d, vocab, dtype, 1.1)
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, dtype)
+    ws[256:] = 0xFF
+    loss, lse = (torch.full((n,), float("nan"), device="cuda") for _ in range(2))
+    lib.moe_cross_entropy(x, W, t, loss, lse, ws)
+    assert (loss == 0).all() and (lse == 0).all()
+    dx, dW = torch.full_like(x, float("nan")), torch.full_like(W, float("nan"))
+    lib.moe_cross_entropy_backward(x, W, t, lse, loss, dx, dW, ws)
+    _ok(lib, ws)
+    assert (dx == 0).all() and (dW == 0).all()
+
+
+@pytest.mark.parametrize("n,d,vocab,dtype", [(40, 64, 500, "bf16"), (300, 512, 3000, "bf16"),
+                                             (40, 64, 500, "f32")])
+def test_cross_entropy_reports_a_target_outside(lib, n, d, vocab, dtype):
+    x, W, t, _ = _loss_case(n, d, vocab, dtype, 0.0)
+    t[7] = vocab
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, dtype)
+    loss, lse = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    lib.moe_cross_entropy(x, W, t, loss, lse, ws)
+    assert lib.moe_status_check(ws) == (5, 7)
+    # the status stays until it is cleared; then the workspace serves again
+    lib.moe_cross_entropy_backward(x, W, t, lse, loss, torch.empty_like(x), None, ws)
+    assert lib.moe_status_check(ws)[0] == 5
+    lib.moe_status_clear(ws)
+    t[7] = vocab - 1
+    lib.moe_cross_entropy(x, W, t, loss, lse, ws)
+    _ok(lib, ws)
+    wloss = S.cross_entropy(x, W, t)[0]
+    assert (loss.cpu().double() - wloss).abs().max() < 1e-3
+
+
+def test_cross_entropy_of_far_logits(lib):
+    """Logits of thousands: the maximum is subtracted first, lse and loss stay exact to fp32."""
+    x = torch.zeros(3, 64, device="cuda")
+    x[:, 0] = torch.tensor([1.0, -1.0, 100.0])
+    W = torch.zeros(300, 64, device="cuda")
+    W[:, 0] = torch.arange(300, device="cuda") * 10.0
+    t = torch.tensor([299, 0, 5], dtype=torch.int32, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        xt, Wt = x.to(dtype), W.to(dtype)
+        ws = lib.alloc_cross_entropy_workspace(3, 64, 300, "f32")
+        loss, lse = torch.zeros(3, device="cuda"), torch.zeros(3, device="cuda")
+        lib.moe_cross_entropy(xt, Wt, t, loss, lse, ws)
+        wloss, wlse, _ = S.cross_entropy(xt, Wt, t)
+        _within(lse, wlse, 4 * V * wlse.abs() + 2 ** -19, "lse")
+        _within(loss, wloss, 8 * V * wlse.abs() + 2 ** -19, "loss")
+
+
+def test_cross_entropy_without_tokens(lib):
+    e = torch.empty(0, 64, device="cuda")
+    W, dW = torch.ones(10, 64, device="cuda"), torch.full((10, 64), 3.0, device="cuda")
+    t, v = torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, device="cuda")
+    ws = lib.alloc_cross_entropy_workspace(0, 64, 10, "f32")
+    lib.moe_cross_entropy(e, W, t, v, v, ws)
+    lib.moe_cross_entropy_backward(e, W, t, v, v, e, dW, ws)
+    assert (dW == 0).all()
+
+
+# --------------------------------------------------------- together, as used
+def _step(lib, s, ws):
+    """The last block's joint, the loss, and back to the block's output."""
+    n, d = s["x"].shape
+    kw = dict(post="rms", pre="rms", p=0.1, rng=s["rng"])
+    lib.moe_block_join(s["x"], s["b"], s["w"], s["r"], s["y"], s["stats"], **kw)
+    lib.moe_cross_entropy(s["y"], s["W"], s["t"], s["loss"], s["lse"], ws)
+    lib.moe_cross_entropy_backward(s["y"], s["W"], s["t"], s["lse"], s["dloss"], s["dy"], s["dW"], ws)
+    lib.moe_block_join_backward(s["b"], s["r"], s["stats"], s["w"], None, s["dy"], s["dx"], s["db"],
+                                lib.make_join_grads(s["grads"]), s["scratch"], **kw)
+
+
+@pytest.mark.parametrize("n,d,vocab", [(37, 64, 300), (300, 512, 4001)])
+def test_a_step_captured_and_replayed(lib, n, d, vocab):
+    """A run of the operators in a graph, replayed on other inputs and on another stream, gives the
+    bits of the eager calls, and follows the generator's state."""
+    g = _gen(8)
+    vectors = {k: _randn(g, d, dtype="bf16", std=0.2, mean=1.0) for k in
+               ("gate", "post_gamma", "pre_gamma")}
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    s = dict(x=bf(n, d), b=bf(n, d), r=bf(n, d), y=bf(n, d), dy=bf(n, d), dx=bf(n, d), db=bf(n, d),
+             W=_randn(g, vocab, d, dtype="bf16", std=d ** -0.5), dW=bf(vocab, d),
+             t=torch.zeros(n, dtype=torch.int32, device="cuda"), rng=_rng(3, 0),
+             stats=torch.zeros(4, n, device="cuda"), loss=torch.zeros(n, device="cuda"),
+             lse=torch.zeros(n, device="cuda"), dloss=torch.full((n,), 1.0 / n, device="cuda"),
+             w=lib.make_join_params(vectors),
+             grads={k: torch.zeros(d, device="cuda") for k in vectors},
+             scratch=torch.zeros(lib.moe_block_join_workspace_size(n, d, "bf16"), dtype=torch.uint8,
+                                 device="cuda"))
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, "bf16")
+    _step(lib, s, ws)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        _step(lib, s, ws)
+    names = ("r", "y", "stats", "loss", "lse", "dy", "dW", "dx", "db")
+    for turn in range(3):
+        s["x"].copy_(_randn(g, n, d, dtype="bf16"))
+        s["b"].copy_(_randn(g, n, d, dtype="bf16"))
+        s["t"].copy_(torch.randint(-vocab // 4, vocab, (n,), generator=g, device="cuda"))
+        s["rng"][1] = turn
+        _step(lib, s, ws)
+        want = [s[k].clone() for k in names] + [v.clone() for v in s["grads"].values()]
+        for k in names:
+            s[k].fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        for name, a, b in zip((*names, *s["grads"]), want, [s[k] for k in names] + list(s["grads"].values())):
+            assert torch.equal(a, b), name
+    _ok(lib, ws)
+
+
+def test_the_layer_between_joints(lib):
+    """norm, the MoE layer, its joint, the loss and the whole way back: the gradient of the residual
+    stream against differences of the loss (fp32)."""
+    import moe_synth
+    n, d, F, E, k, vocab = 24, 32, 48, 4, 2, 60
+    cfg = moe_synth.MoEConfig("t", n, d, F, E, k, "f32", "f32", "renorm", "swiglu")
+    g = _gen(17)
+    f = lambda *s, std=1.0: _randn(g, *s, std=std)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    x, one = f(n, d), torch.ones(d, device="cuda")
+    t = dict(Wg=f(E, d, std=0.3), W1=f(E, F, d, std=0.2), W3=f(E, F, d, std=0.2),
+             W2=f(E, d, F, std=0.2))
+    w, W = lib.make_weights(t), f(vocab, d, std=0.3)
+    targets = torch.randint(vocab, (n,), generator=g, device="cuda").to(torch.int32)
+    targets[3] = -1
+    ws, rng = lib.alloc_train_workspace(cfg), _rng(4, 4)
+    lws = lib.alloc_cross_entropy_workspace(n, d, vocab, "f32")
+    join = lib.make_join_params(dict(gate=0.5 * one, post_gamma=one, pre_gamma=one))
+    kw = dict(post="rms", pre="rms", p=0.2, rng=rng)
+    dloss = (targets >= 0).float() / (n - 1)
+
+    def forward(x):
+        s = dict(y=torch.empty(n, d, device="cuda"), mean=torch.empty(n, device="cuda"),
+                 rstd=torch.empty(n, device="cuda"), idx=i32(n, k), gate=torch.empty(n, k, device="cuda"),
+                 probs=torch.empty(n, E, device="cuda"), counts=i32(E), off=i32(E + 1),
+                 perm=i32(n * k), inv=i32(n * k), xp=torch.empty(n * k, d, device="cuda"),
+                 g=torch.empty(n * k, F, device="cuda"), u=torch.empty(n * k, F, device="cuda"),
+                 h=torch.empty(n * k, F, device="cuda"), yp=torch.empty(n * k, d, device="cuda"),
+                 b=torch.empty(n, d, device="cuda"), r=torch.empty(n, d, device="cuda"),
+                 out=torch.empty(n, d, device="cuda"), stats=torch.empty(4, n, device="cuda"),
+                 loss=torch.empty(n, device="cuda"), lse=torch.empty(n, device="cuda"))
+        lib.moe_layernorm(x, one, None, s["y"], s["mean"], s["rstd"])
+        lib.moe_route(cfg, s["y"], w, s["idx"], s["gate"], s["probs"], ws)
+        lib.moe_dispatch(cfg, s["idx"], s["y"], s["counts"], s["off"], s["perm"], s["inv"], s["xp"], ws)
+        lib.moe_expert_ffn_train(cfg, s["xp"], s["off"], w, s["g"], s["u"], s["h"], s["yp"], ws)
+        lib.moe_combine(cfg, s["yp"], s["inv"], s["gate"], None, s["b"], ws)
+        lib.moe_block_join(x, s["b"], join, s["r"], s["out"], s["stats"], **kw)
+        lib.moe_cross_entropy(s["out"], W, targets, s["loss"], s["lse"], lws)
+        return s
+
+    s = forward(x)
+    e = lambda *shape: torch.empty(*shape, device="cuda")
+    dout, dx, db, dyp, dgate, dxp, dy, dn = (e(n, d), e(n, d), e(n, d), e(n * k, d), e(n, k),
+                                            e(n * k, d), e(n, d), e(n, d))
+    scratch = torch.zeros(max(lib.moe_block_join_workspace_size(n, d, "f32"),
+                              lib.moe_layernorm_workspace_size(n, d, "f32")), dtype=torch.uint8,
+                          device="cuda")
+    lib.moe_cross_entropy_backward(s["out"], W, targets, s["lse"], dloss, dout, None, lws)
+    lib.moe_block_join_backward(s["b"], s["r"], s["stats"], join, None, dout, dx, db,
+                                lib.make_join_grads({}), scratch, **kw)
+    lib.moe_combine_backward(cfg, db, s["yp"], s["inv"], s["gate"], dyp, dgate, ws)
+    lib.moe_expert_ffn_backward(cfg, s["xp"], s["off"], w, s["g"], s["u"], s["h"], dyp, dxp,
+                                lib.make_expert_grads({}), ws)
+    lib.moe_route_backward(cfg, s["y"], w, s["probs"], s["idx"], s["gate"], dgate, None, 0.0,
+                           s["inv"], dxp, dy, None, None, ws)
+    lib.moe_layernorm_backward(x, one, s["mean"], s["rstd"], dy, dn, None, None, scratch)
+    _ok(lib, ws)
+    _ok(lib, lws)
+    grad = (dx + dn).double()
+    h = 2e-3
+    for seed in range(3):
+        step = _randn(_gen(seed), n, d)
+        ends = []
+        for sign in (1, -1):
+            moved = forward(x + sign * h * step)
+            assert torch.equal(moved["idx"], s["idx"])     # (the choice of experts stays)
+            ends.append((moved["loss"].double() * dloss.double()).sum().item())
+        slope, want = (ends[0] - ends[1]) / (2 * h), (grad * step.double()).sum().item()
+        # fp32 losses of about 4, off by some 2^-22, over 2 h; the third derivative times h^2 / 6
+        assert abs(slope - want) <= 4 * 2 ** -20 / (2 * h) + 50 * h * h, (slope, want)
