@@ -573,7 +573,7 @@ moe_status moe_block_join_backward(const moe_join_config *cfg, const void *b, co
 typedef struct {
   int32_t n;           /* tokens, 0 .. 1048576 (else MOE_ERR_UNSUPPORTED) */
   int32_t d;           /* a multiple of 4 (f32) or 8 (bf16), else MOE_ERR_UNSUPPORTED */
-  int32_t vocab;       /* >= 1, of any size (at most INT32_MAX / 2) */
+  int32_t vocab;       /* 1 .. 16777216, of any size in between */
   int32_t dtype;       /* MOE_F32 or MOE_BF16: x, W and their gradients */
   float z_loss;        /* finite, >= 0 */
   int32_t reserved;    /* 0 */

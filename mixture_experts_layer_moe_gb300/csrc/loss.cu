@@ -9,11 +9,18 @@
 // workspace in fp32 with the token contiguous, lT [piece][pitch]: then dx = dl W
 // is a sum over lT's rows (GradProduct: cut into runs where the tiles are few)
 // and dW = dl^T x a product of its rows (RowsProduct).
+//
+// On the tensor cores (other bf16 problems, loss_pair.cu) the forward reduces the
+// logits as it forms them.  The gradient forms a piece's logits again and
+// stores their gradient in bf16, dl [n][pitch], which two products then read: dW
+// (launch_gemm_grad, rounded once from the whole sum over the tokens) and dx,
+// which adds up over the pieces in fp32 and is rounded once at the end.
 #include <math.h>
 
 #include "api.h"
 #include "common.cuh"
 #include "launch.h"
+#include "loss.h"
 #include "step.h"
 #include "train.h"
 #include "vec16.cuh"
@@ -24,17 +31,26 @@ namespace {
 constexpr int L_CHUNK = 256;                           // vocabulary entries of a partial sum
 constexpr int64_t L_PIECE_BYTES = (int64_t)256 << 20;  // of a piece's logits, about
 constexpr int64_t L_PIECE_MAX = 1 << 22;               // entries of a piece
+constexpr int L_MAX_SPLITS = 76;
 
 struct LossLayout {
   size_t status, range, list, target, lse, dloss, at, x, sums, logits, dx, parts, total;
-  int pitch;    // tokens, rounded up to whole vectors of fp32
+  bool pair;    // on the tensor cores
+  int pitch;    // CUDA cores: tokens, rounded up to whole vectors of fp32
   int piece;    // vocabulary entries of a piece at most (a multiple of L_CHUNK where there are several)
-  int pieces, chunks;
+  int pieces;
+  int width, chunks;   // entries per tile of the forward; partial sums per token
+  int planes;          // dx: its partial sums
 };
 
 int elem_size(const moe_loss_config &c) { return c.dtype == MOE_F32 ? 4 : 2; }
 
-// dx of a piece (operands unset).
+// A bf16 problem that is faster without setting up the pair kernels.
+bool small_loss(const moe_loss_config &c) {
+  return (int64_t)c.n * c.vocab * c.d <= kSmallProducts && c.d <= 256;
+}
+
+// dx of a piece on the CUDA cores, dW of one on the tensor cores (operands unset).
 GradProduct dx_product(const moe_loss_config &c, const LossLayout &L, int entries) {
   GradProduct p{};
   p.dtype = c.dtype;
@@ -46,16 +62,31 @@ GradProduct dx_product(const moe_loss_config &c, const LossLayout &L, int entrie
   p.a_f32 = c.dtype == MOE_BF16;
   return p;
 }
+int dl_pitch(int entries) { return (entries + 7) / 8 * 8; }
+GradProduct dw_product(const moe_loss_config &c, int entries) {
+  GradProduct p{};
+  p.dtype = c.dtype;
+  p.offsets = reinterpret_cast<const int32_t *>(16);   // (set by the caller)
+  p.num_experts = 1;
+  p.rows = c.n;
+  p.M = entries;
+  p.N = c.d;
+  p.lda = dl_pitch(entries);
+  return p;
+}
 
 LossLayout loss_layout(const moe_loss_config &c) {
   LossLayout L{};
   const size_t n = c.n, z = elem_size(c);
+  L.pair = c.dtype == MOE_BF16 && !small_loss(c);
   L.pitch = (c.n + 3) / 4 * 4;
-  int64_t fit = L_PIECE_BYTES / ((int64_t)L.pitch * 4 + 1) / L_CHUNK * L_CHUNK;
+  int64_t fit = L_PIECE_BYTES / ((int64_t)L.pitch * (L.pair ? 2 : 4) + 1) / L_CHUNK * L_CHUNK;
   if (fit > L_PIECE_MAX) fit = L_PIECE_MAX;
   L.piece = (int)(fit < L_CHUNK ? L_CHUNK : fit < c.vocab ? fit : c.vocab);
   L.pieces = (int)(((int64_t)c.vocab + L.piece - 1) / L.piece);
-  L.chunks = (int)(((int64_t)c.vocab + L_CHUNK - 1) / L_CHUNK);
+  L.width = L.pair ? loss_width(c.n, c.vocab) : 0;
+  L.chunks = L.pair ? loss_chunks(c.vocab, L.width) : (c.vocab + L_CHUNK - 1) / L_CHUNK;
+  L.planes = L.pair ? loss_dx_splits(c.n, c.d, L.piece, L_MAX_SPLITS) : L.pieces;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t a = off;
@@ -70,13 +101,30 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.dloss = take((size_t)L.pitch * 4);
   L.at = take(n * 4);
   L.x = take(n * c.d * z);
+  const size_t both = off;
+  // what the forward alone and the gradient alone use shares its place
   L.sums = take(n * L.chunks * sizeof(float2));
-  L.logits = take((size_t)L.piece * L.pitch * 4);
-  L.dx = take((size_t)L.pieces * n * c.d * z);
-  const GradProduct dx = dx_product(c, L, L.piece);
-  const int splits = c.n > 0 ? grad_splits_simt(&dx, 1) : 1;
-  L.parts = take(splits > 1 ? (size_t)splits * n * c.d * 4 : 0);
-  L.total = off;
+  if (!L.pair) L.logits = take((size_t)L.piece * L.pitch * 4);
+  const size_t forward = off;
+  if (L.pair) {
+    off = both;
+    L.logits = take(n * dl_pitch(L.piece) * 2);
+  }
+  L.dx = take((size_t)L.planes * n * c.d * (L.pair ? 4 : z));
+  size_t parts = 0;
+  if (L.pair) {
+    for (int entries : {L.piece, c.vocab - (L.pieces - 1) * L.piece}) {
+      const GradProduct p = dw_product(c, entries);
+      const size_t bytes = grad_scratch(&p, 1);
+      if (bytes > parts) parts = bytes;
+    }
+  } else if (c.n > 0) {
+    const GradProduct p = dx_product(c, L, L.piece);
+    const int splits = grad_splits_simt(&p, 1);
+    if (splits > 1) parts = (size_t)splits * n * c.d * 4;
+  }
+  L.parts = take(parts);
+  L.total = off > forward ? off : forward;
   return L;
 }
 
@@ -293,26 +341,32 @@ loss_grad_kernel(float4 *__restrict__ lt, int pitch4, int entries, int v0, float
   }
 }
 
-// dx of the counted tokens: the pieces' sums, added in order.
-template <typename T>
+// dx of the counted tokens: the partial sums [planes][n][d] of type TI, added in
+// order.
+template <typename T, typename TI>
 __global__ void __launch_bounds__(256)
-loss_dx_kernel(const T *__restrict__ parts, int pieces, int n, int vecs,
+loss_dx_kernel(const TI *__restrict__ parts, int planes, int n, int vecs,
                const int32_t *__restrict__ range, const int32_t *__restrict__ list,
                T *__restrict__ dx, const int *status) {
-  constexpr int N = Vec16<T>::N;
+  constexpr int N = Vec16<T>::N, NI = Vec16<TI>::N;
   pdl_wait();
   if (status_failed(status)) return;
-  const int64_t total = (int64_t)range[1] * vecs, plane = (int64_t)n * vecs;
+  const int64_t total = (int64_t)range[1] * vecs, plane = (int64_t)n * vecs * (N / NI);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
     const int64_t j = i / vecs;
-    const uint4 *from = reinterpret_cast<const uint4 *>(parts) + i;
-    float v[N], w[N];
-    unpack16<T>(from[0], v);
-    for (int p = 1; p < pieces; ++p) {
-      unpack16<T>(from[p * plane], w);
+    const uint4 *from = reinterpret_cast<const uint4 *>(parts) + i * (N / NI);
+    float v[N], w[NI];
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[k] += w[k];
+    for (int h = 0; h < N / NI; ++h) unpack16<TI>(from[h], v + h * NI);
+#pragma unroll 4
+    for (int p = 1; p < planes; ++p) {
+#pragma unroll
+      for (int h = 0; h < N / NI; ++h) {
+        unpack16<TI>(from[p * plane + h], w);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) v[h * NI + k] += w[k];
+      }
     }
     reinterpret_cast<uint4 *>(dx)[(int64_t)list[j] * vecs + (i - j * vecs)] = pack16<T>(v);
   }
@@ -341,9 +395,39 @@ cudaError_t piece_logits(const moe_loss_config &c, const LossLayout &L, const vo
   return launch_rows_simt(p, at<int>(ws, L.status), s);
 }
 
-}  // namespace
+template <typename T, typename TI>
+cudaError_t finish_dx(const moe_loss_config &c, const LossLayout &L, void *dx, void *ws,
+                      cudaStream_t s) {
+  const int vecs = c.d / Vec16<T>::N;
+  return launch_pdl(loss_dx_kernel<T, TI>, dim3(blocks_of((int64_t)c.n * vecs)), dim3(256), 0, s,
+                    at<TI>(ws, L.dx), L.planes, c.n, vecs, at<int32_t>(ws, L.range),
+                    at<int32_t>(ws, L.list), (T *)dx, at<int>(ws, L.status));
+}
 
-size_t loss_workspace(const moe_loss_config &c) { return loss_layout(c).total; }
+// The operands that a piece's products on the tensor cores share.
+LossProduct pair_product(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
+                         int entries, void *ws) {
+  LossProduct p{};
+  p.n = c.n;
+  p.d = c.d;
+  p.entries = entries;
+  p.v0 = v0;
+  p.range = at<int32_t>(ws, L.range);
+  p.target = at<int32_t>(ws, L.target);
+  p.x = at<void>(ws, L.x);
+  p.W = (const char *)W + (size_t)v0 * c.d * 2;
+  p.width = L.width;
+  p.chunks = L.chunks;
+  p.sums = at<float2>(ws, L.sums);
+  p.at = at<float>(ws, L.at);
+  p.lse = at<float>(ws, L.lse);
+  p.dloss = at<float>(ws, L.dloss);
+  p.z_loss = c.z_loss;
+  p.dl = at<void>(ws, L.logits);
+  p.pitch = dl_pitch(entries);
+  p.planes = at<float>(ws, L.dx);
+  return p;
+}
 
 #define LOSS_TRY(expr)                       \
   do {                                       \
@@ -351,19 +435,88 @@ size_t loss_workspace(const moe_loss_config &c) { return loss_layout(c).total; }
     if (_e != cudaSuccess) return _e;        \
   } while (0)
 
+cudaError_t piece_gradient_simt(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
+                                int entries, int i, bool dx, void *dW, void *ws, cudaStream_t s) {
+  const size_t row = (size_t)c.d * elem_size(c);
+  int *status = at<int>(ws, L.status);
+  LOSS_TRY(piece_logits(c, L, W, v0, entries, ws, s));
+  LOSS_TRY(launch_pdl(loss_grad_kernel, dim3(blocks_of((int64_t)entries * L.pitch / 4)), dim3(256),
+                      0, s, at<float4>(ws, L.logits), L.pitch / 4, entries, v0, c.z_loss,
+                      at<int32_t>(ws, L.range), at<int4>(ws, L.target), at<float4>(ws, L.lse),
+                      at<float4>(ws, L.dloss), status));
+  if (dW) {
+    RowsProduct p{};
+    p.dtype = c.dtype;
+    p.epi = kRowsPlain;
+    p.b_rows = 1;
+    p.num_experts = 1;
+    p.rows = entries;
+    p.K = c.n;
+    p.N = c.d;
+    p.lda = L.pitch;
+    p.A = at<void>(ws, L.logits);
+    p.B = at<void>(ws, L.x);
+    p.out = (char *)dW + v0 * row;
+    p.a_f32 = c.dtype == MOE_BF16;
+    LOSS_TRY(launch_rows_simt(p, status, s));
+  }
+  if (!dx) return cudaSuccess;
+  GradProduct p = dx_product(c, L, entries);
+  p.A = at<void>(ws, L.logits);
+  p.B = (const char *)W + v0 * row;
+  p.out = at<char>(ws, L.dx) + (size_t)i * c.n * row;
+  return launch_grad_simt(&p, 1, grad_splits_simt(&p, 1), at<float>(ws, L.parts), status, s);
+}
+
+cudaError_t piece_gradient_pair(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
+                                int entries, int i, bool dx, void *dW, void *ws, cudaStream_t s) {
+  int *status = at<int>(ws, L.status);
+  LossProduct p = pair_product(c, L, W, v0, entries, ws);
+  LOSS_TRY(launch_loss_logit_grad(p, status, s));
+  if (dW) {
+    GradProduct g = dw_product(c, entries);
+    g.offsets = p.range;
+    g.A = p.dl;
+    g.B = p.x;
+    g.out = (char *)dW + (size_t)v0 * c.d * 2;
+    const int splits = grad_splits(&g, 1);
+    float *parts = at<float>(ws, L.parts);
+    if (grads_small(&g, 1)) {
+      LOSS_TRY(launch_grad_simt(&g, 1, splits, parts, status, s));
+    } else {
+      if (!gemm_grad_supported(g)) return cudaErrorNotSupported;
+      LOSS_TRY(launch_gemm_grad(&g, 1, splits, parts, 0, status, s));
+    }
+  }
+  if (!dx) return cudaSuccess;
+  // (the last piece may be cut into fewer ranges, and adds to the first planes)
+  p.splits = entries == L.piece ? L.planes : loss_dx_splits(c.n, c.d, entries, L.planes);
+  p.add = i > 0;
+  return launch_loss_dx(p, status, s);
+}
+
+}  // namespace
+
+size_t loss_workspace(const moe_loss_config &c) { return loss_layout(c).total; }
+
 cudaError_t launch_loss(const moe_loss_config &c, const void *x, const void *W,
                         const int32_t *targets, float *loss, float *lse, void *ws, cudaStream_t s) {
   const LossLayout L = loss_layout(c);
+  if (L.pair && !loss_pair_supported(c)) return cudaErrorNotSupported;
   int *status = at<int>(ws, L.status);
   LOSS_TRY(launch_pack(c, L, x, targets, nullptr, nullptr, loss, lse, nullptr, ws, s));
-  for (int v0 = 0; v0 < c.vocab; v0 += L.piece) {
-    const int entries = c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece;
-    LOSS_TRY(piece_logits(c, L, W, v0, entries, ws, s));
-    LOSS_TRY(launch_pdl(loss_chunk_kernel,
-                        dim3((c.n + 31) / 32, (entries + L_CHUNK - 1) / L_CHUNK), dim3(256), 0, s,
-                        at<float>(ws, L.logits), L.pitch, entries, v0, L.chunks,
-                        at<int32_t>(ws, L.range), at<int32_t>(ws, L.target), at<float>(ws, L.at),
-                        at<float2>(ws, L.sums), status));
+  if (L.pair) {
+    LOSS_TRY(launch_loss_sums(pair_product(c, L, W, 0, c.vocab, ws), status, s));
+  } else {
+    for (int v0 = 0; v0 < c.vocab; v0 += L.piece) {
+      const int entries = c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece;
+      LOSS_TRY(piece_logits(c, L, W, v0, entries, ws, s));
+      LOSS_TRY(launch_pdl(loss_chunk_kernel,
+                          dim3((c.n + 31) / 32, (entries + L_CHUNK - 1) / L_CHUNK), dim3(256), 0, s,
+                          at<float>(ws, L.logits), L.pitch, entries, v0, L.chunks,
+                          at<int32_t>(ws, L.range), at<int32_t>(ws, L.target), at<float>(ws, L.at),
+                          at<float2>(ws, L.sums), status));
+    }
   }
   return launch_pdl(loss_finish_kernel, dim3((c.n + 7) / 8), dim3(256), 0, s,
                     at<float2>(ws, L.sums), L.chunks, c.z_loss, at<int32_t>(ws, L.range),
@@ -374,51 +527,17 @@ cudaError_t launch_loss_backward(const moe_loss_config &c, const void *x, const 
                                  const int32_t *targets, const float *lse, const float *dloss,
                                  void *dx, void *dW, void *ws, cudaStream_t s) {
   const LossLayout L = loss_layout(c);
-  int *status = at<int>(ws, L.status);
-  const size_t row = (size_t)c.d * elem_size(c);
+  if (L.pair && !loss_pair_supported(c)) return cudaErrorNotSupported;
   LOSS_TRY(launch_pack(c, L, x, targets, lse, dloss, nullptr, nullptr, dx, ws, s));
+  auto piece = L.pair ? piece_gradient_pair : piece_gradient_simt;
   for (int v0 = 0, i = 0; v0 < c.vocab; v0 += L.piece, ++i) {
     const int entries = c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece;
-    const void *Wp = (const char *)W + v0 * row;
-    LOSS_TRY(piece_logits(c, L, W, v0, entries, ws, s));
-    LOSS_TRY(launch_pdl(loss_grad_kernel, dim3(blocks_of((int64_t)entries * L.pitch / 4)), dim3(256),
-                        0, s, at<float4>(ws, L.logits), L.pitch / 4, entries, v0, c.z_loss,
-                        at<int32_t>(ws, L.range), at<int4>(ws, L.target), at<float4>(ws, L.lse),
-                        at<float4>(ws, L.dloss), status));
-    if (dW) {
-      RowsProduct p{};
-      p.dtype = c.dtype;
-      p.epi = kRowsPlain;
-      p.b_rows = 1;
-      p.num_experts = 1;
-      p.rows = entries;
-      p.K = c.n;
-      p.N = c.d;
-      p.lda = L.pitch;
-      p.A = at<void>(ws, L.logits);
-      p.B = at<void>(ws, L.x);
-      p.out = (char *)dW + v0 * row;
-      p.a_f32 = c.dtype == MOE_BF16;
-      LOSS_TRY(launch_rows_simt(p, status, s));
-    }
-    if (dx) {
-      GradProduct p = dx_product(c, L, entries);
-      p.A = at<void>(ws, L.logits);
-      p.B = Wp;
-      p.out = at<char>(ws, L.dx) + (size_t)i * c.n * row;
-      LOSS_TRY(launch_grad_simt(&p, 1, grad_splits_simt(&p, 1), at<float>(ws, L.parts), status, s));
-    }
+    LOSS_TRY(piece(c, L, W, v0, entries, i, dx != nullptr, dW, ws, s));
   }
   if (!dx) return cudaSuccess;
-  const int vecs = (int)(row / 16);
-  const dim3 grid(blocks_of((int64_t)c.n * vecs));
-  if (c.dtype == MOE_F32)
-    return launch_pdl(loss_dx_kernel<float>, grid, dim3(256), 0, s, at<float>(ws, L.dx), L.pieces,
-                      c.n, vecs, at<int32_t>(ws, L.range), at<int32_t>(ws, L.list), (float *)dx,
-                      status);
-  return launch_pdl(loss_dx_kernel<__nv_bfloat16>, grid, dim3(256), 0, s,
-                    at<__nv_bfloat16>(ws, L.dx), L.pieces, c.n, vecs, at<int32_t>(ws, L.range),
-                    at<int32_t>(ws, L.list), (__nv_bfloat16 *)dx, status);
+  if (c.dtype == MOE_F32) return finish_dx<float, float>(c, L, dx, ws, s);
+  return L.pair ? finish_dx<__nv_bfloat16, float>(c, L, dx, ws, s)
+                : finish_dx<__nv_bfloat16, __nv_bfloat16>(c, L, dx, ws, s);
 }
 
 }  // namespace moe

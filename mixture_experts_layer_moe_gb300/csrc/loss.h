@@ -1,0 +1,44 @@
+// The tensor-core products of the cross entropy (loss_pair.cu), for loss.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe.h"
+
+namespace moe {
+
+// Tokens are packed rows [n][d] of which range[1] count (read on the device);
+// `entries` of the vocabulary from v0 on, W their rows [entries][d].
+struct LossProduct {
+  int n, d, entries, v0;
+  const int32_t *range, *target;
+  const void *x, *W;
+  // sums: (maximum, sum of e^(l - maximum)) per token and half of a tile,
+  // [n][chunks], and the target's logit
+  float2 *sums;
+  int width, chunks;      // entries per tile
+  float *at;
+  // the logits' gradient, bf16 [n][pitch], columns from `entries` on zero
+  const float *lse, *dloss;
+  float z_loss;
+  void *dl;
+  int pitch;
+  // dx in fp32: `splits` ranges of the entries, planes [split][n][d]; added to
+  // what they hold, or stored
+  float *planes;
+  int splits, add;
+};
+
+bool loss_pair_supported(const moe_loss_config &c);   // (makes CUDA calls)
+// Entries per tile of the forward, and how many partial sums that makes.
+int loss_width(int n, int vocab);
+inline int loss_chunks(int vocab, int width) { return 2 * ((vocab + width - 1) / width); }
+// Ranges of the entries for dx, `most` at most.
+int loss_dx_splits(int n, int d, int entries, int most);
+
+cudaError_t launch_loss_sums(const LossProduct &p, int *status, cudaStream_t s);
+cudaError_t launch_loss_logit_grad(const LossProduct &p, int *status, cudaStream_t s);
+cudaError_t launch_loss_dx(const LossProduct &p, int *status, cudaStream_t s);
+
+}  // namespace moe
