@@ -1,4 +1,10 @@
-// Dropout of rows: y = x / (1 - q) where element (r, c) is kept, else 0 (philox.cuh).
+// Dropout of rows: y = x / (1 - q) where element (r, c) is kept, else 0.  A stream
+// through HBM: the mask is made from the element's place (philox.cuh), eight
+// elements per call of the generator, and never stored.
+//
+// A thread takes blocks of eight elements, a grid's stride apart (their row and
+// place move on by a constant: no division per block), and loads U of them
+// before it makes the masks of the first.
 #include "common.cuh"
 #include "launch.h"
 #include "philox.cuh"
@@ -8,41 +14,148 @@
 namespace moe {
 namespace {
 
-// One thread per block of eight elements of a row.
+constexpr int D_THREADS = 256;
+
+// A block of eight elements as 16-byte vectors.
 template <typename T>
-__global__ void __launch_bounds__(256)
-dropout_kernel(moe_dropout_config c, const T *x, const RngState *rng, T *y, int threshold,
-               float factor) {
-  const RngState st = threshold ? *rng : RngState{0, 0};
-  const int blocks = (c.d + 7) / 8;
-  const int64_t total = c.rows * blocks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / blocks;
-    const int k = (int)(i - r * blocks);
-    const uint32_t keep = dropout_keep(st, k, (uint32_t)r, threshold);
-    const T *from = x + r * c.ldx + k * 8;
-    T *to = y + r * c.ldy + k * 8;
-    const int n = min(8, c.d - k * 8);
-    for (int j = 0; j < n; ++j)
-      to[j] = Elem<T>::from_f(keep >> j & 1 ? Elem<T>::load(from + j) * factor : 0.f);
+struct Block8 {
+  static constexpr int N = 8 * sizeof(T) / 16;
+  uint4 v[N];
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
   }
+  __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) reinterpret_cast<uint4 *>(p)[i] = v[i];
+  }
+  __device__ __forceinline__ void drop(uint32_t keep, float factor) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      constexpr int E = Vec16<T>::N;
+      float f[E];
+      unpack16<T>(v[i], f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = keep >> (i * E + e) & 1 ? f[e] * factor : 0.f;
+      v[i] = pack16<T>(f);
+    }
+  }
+};
+
+struct DropArgs {
+  moe_dropout_config c;
+  const RngState *rng;
+  int threshold, blocks;    // blocks of a row
+  float factor;
+  int64_t step_rows;        // a grid's stride: rows, and blocks of the last one
+  int step_blocks;
+};
+
+// Rows on vector boundaries (x and y may be the same).
+template <typename T, int U>
+__global__ void __launch_bounds__(D_THREADS) dropout_kernel(const __grid_constant__ DropArgs a,
+                                                            const T *x, T *y) {
+  const moe_dropout_config &c = a.c;
+  const RngState st = a.threshold ? *a.rng : RngState{0, 0};
+  const int64_t start = (int64_t)blockIdx.x * D_THREADS + threadIdx.x;
+  int64_t r = start / a.blocks;
+  int k = (int)(start - r * a.blocks);
+  while (r < c.rows) {
+    Block8<T> v[U];
+    int64_t row[U];
+    int at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      row[u] = r;
+      at[u] = k;
+      if (r < c.rows && k * 8 + 8 <= c.d) v[u].load(x + r * c.ldx + k * 8);
+      r += a.step_rows;
+      k += a.step_blocks;
+      if (k >= a.blocks) {
+        k -= a.blocks;
+        ++r;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (row[u] >= c.rows) break;
+      const uint32_t keep = dropout_keep(st, at[u], (uint32_t)row[u], a.threshold);
+      T *to = y + row[u] * c.ldy + at[u] * 8;
+      if (at[u] * 8 + 8 <= c.d) {
+        v[u].drop(keep, a.factor);
+        v[u].store(to);
+      } else {
+        const T *from = x + row[u] * c.ldx + at[u] * 8;
+        for (int i = 0; i < c.d - at[u] * 8; ++i)
+          to[i] = Elem<T>::from_f(keep >> i & 1 ? Elem<T>::load(from + i) * a.factor : 0.f);
+      }
+    }
+  }
+}
+
+// Rows anywhere: a warp takes 256 columns of a row, a lane makes the mask of a
+// block, and the elements go by lanes.
+template <typename T>
+__global__ void __launch_bounds__(D_THREADS) dropout_odd_kernel(const __grid_constant__ DropArgs a,
+                                                                const T *x, T *y) {
+  const moe_dropout_config &c = a.c;
+  const RngState st = a.threshold ? *a.rng : RngState{0, 0};
+  const int lane = threadIdx.x & 31;
+  const int64_t start = (int64_t)blockIdx.x * (D_THREADS / 32) + (threadIdx.x >> 5);
+  int64_t r = start / a.blocks;   // (here blocks of 256 columns, one per warp)
+  int k = (int)(start - r * a.blocks);
+  while (r < c.rows) {
+    const T *from = x + r * c.ldx;
+    T *to = y + r * c.ldy;
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = k * 256 + i * 32 + lane;
+      if (col < c.d) v[i] = from[col];
+    }
+    const uint32_t keep = dropout_keep(st, k * 32 + lane, (uint32_t)r, a.threshold);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = k * 256 + i * 32 + lane;
+      const uint32_t mask = __shfl_sync(0xffffffffu, keep, i * 4 + (lane >> 3));
+      if (col < c.d)
+        to[col] = Elem<T>::from_f(mask >> (lane & 7) & 1 ? Elem<T>::to_f(v[i]) * a.factor : 0.f);
+    }
+    r += a.step_rows;
+    k += a.step_blocks;
+    if (k >= a.blocks) {
+      k -= a.blocks;
+      ++r;
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch(const moe_dropout_config &c, int threshold, const T *x, const RngState *rng,
+                   T *y, cudaStream_t s) {
+  constexpr int U = 16 / (int)sizeof(T) / 2;   // (bf16 4, fp32 2: 64 bytes a thread)
+  constexpr int E = Vec16<T>::N;
+  DropArgs a{c, rng, threshold, 0, dropout_factor(threshold), 0, 0};
+  const bool vectors = c.rows == 1 || (c.ldx % E == 0 && c.ldy % E == 0);
+  a.blocks = vectors ? (c.d + 7) / 8 : (c.d + 255) / 256;
+  const int per = vectors ? D_THREADS : D_THREADS / 32;
+  const int64_t want = (c.rows * a.blocks + per - 1) / per, most = (int64_t)num_sms() * 8;
+  const int64_t grid = want < most ? want : most;
+  a.step_rows = grid * per / a.blocks;
+  a.step_blocks = (int)(grid * per - a.step_rows * a.blocks);
+  if (vectors) dropout_kernel<T, U><<<(unsigned)grid, D_THREADS, 0, s>>>(a, x, y);
+  else dropout_odd_kernel<T><<<(unsigned)grid, D_THREADS, 0, s>>>(a, x, y);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_dropout(const moe_dropout_config &c, int threshold, const void *x,
                            const uint64_t *rng, void *y, cudaStream_t s) {
-  const int64_t blocks = (c.rows * ((c.d + 7) / 8) + 255) / 256, most = (int64_t)num_sms() * 8;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most));
   const RngState *st = reinterpret_cast<const RngState *>(rng);
-  const float f = dropout_factor(threshold);
-  if (c.dtype == MOE_F32)
-    dropout_kernel<float><<<grid, 256, 0, s>>>(c, (const float *)x, st, (float *)y, threshold, f);
-  else
-    dropout_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
-        c, (const __nv_bfloat16 *)x, st, (__nv_bfloat16 *)y, threshold, f);
-  return cudaGetLastError();
+  return c.dtype == MOE_F32
+             ? launch<float>(c, threshold, (const float *)x, st, (float *)y, s)
+             : launch<__nv_bfloat16>(c, threshold, (const __nv_bfloat16 *)x, st, (__nv_bfloat16 *)y, s);
 }
 
 }  // namespace moe
