@@ -6,6 +6,7 @@
 // place move on by a constant: no division per block), and loads U of them
 // before it makes the masks of the first.
 #include "common.cuh"
+#include "fp32x2.cuh"
 #include "launch.h"
 #include "philox.cuh"
 #include "step.h"
@@ -29,14 +30,19 @@ struct Block8 {
 #pragma unroll
     for (int i = 0; i < N; ++i) reinterpret_cast<uint4 *>(p)[i] = v[i];
   }
-  __device__ __forceinline__ void drop(uint32_t keep, float factor) {
+  __device__ __forceinline__ void drop(const uint4 &bits, uint32_t cut, float factor) {
+    const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       constexpr int E = Vec16<T>::N;
       float f[E];
       unpack16<T>(v[i], f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = keep >> (i * E + e) & 1 ? f[e] * factor : 0.f;
+      for (int e = 0; e < E; e += 2) {
+        const float2 g = mul2(make_float2(f[e], f[e + 1]), both(factor));
+        f[e] = kept_even(w[(i * E + e) / 2], cut) ? g.x : 0.f;
+        f[e + 1] = kept_odd(w[(i * E + e) / 2], cut) ? g.y : 0.f;
+      }
       v[i] = pack16<T>(f);
     }
   }
@@ -56,7 +62,7 @@ template <typename T, int U>
 __global__ void __launch_bounds__(D_THREADS) dropout_kernel(const __grid_constant__ DropArgs a,
                                                             const T *x, T *y) {
   const moe_dropout_config &c = a.c;
-  const RngState st = a.threshold ? *a.rng : RngState{0, 0};
+  const RngState st = load_state(a.threshold ? a.rng : nullptr);
   const int64_t start = (int64_t)blockIdx.x * D_THREADS + threadIdx.x;
   int64_t r = start / a.blocks;
   int k = (int)(start - r * a.blocks);
@@ -79,12 +85,12 @@ __global__ void __launch_bounds__(D_THREADS) dropout_kernel(const __grid_constan
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (row[u] >= c.rows) break;
-      const uint32_t keep = dropout_keep(st, at[u], (uint32_t)row[u], a.threshold);
       T *to = y + row[u] * c.ldy + at[u] * 8;
       if (at[u] * 8 + 8 <= c.d) {
-        v[u].drop(keep, a.factor);
+        v[u].drop(dropout_bits(st, at[u], (uint32_t)row[u]), (uint32_t)a.threshold << 16, a.factor);
         v[u].store(to);
       } else {
+        const uint32_t keep = dropout_keep(st, at[u], (uint32_t)row[u], a.threshold);
         const T *from = x + row[u] * c.ldx + at[u] * 8;
         for (int i = 0; i < c.d - at[u] * 8; ++i)
           to[i] = Elem<T>::from_f(keep >> i & 1 ? Elem<T>::load(from + i) * a.factor : 0.f);
@@ -99,7 +105,7 @@ template <typename T>
 __global__ void __launch_bounds__(D_THREADS) dropout_odd_kernel(const __grid_constant__ DropArgs a,
                                                                 const T *x, T *y) {
   const moe_dropout_config &c = a.c;
-  const RngState st = a.threshold ? *a.rng : RngState{0, 0};
+  const RngState st = load_state(a.threshold ? a.rng : nullptr);
   const int lane = threadIdx.x & 31;
   const int64_t start = (int64_t)blockIdx.x * (D_THREADS / 32) + (threadIdx.x >> 5);
   int64_t r = start / a.blocks;   // (here blocks of 256 columns, one per warp)

@@ -12,6 +12,21 @@ struct RngState {
   uint64_t seed, offset;
 };
 
+// The state, known to be the same in all lanes (every lane calls): what depends on
+// it alone, the rounds' keys, then takes the uniform datapath and its registers.
+// (16384 x 7168 bf16 dropout 88 us without, 82 so.)
+__device__ __forceinline__ uint64_t same_in_warp(uint64_t v) {
+  const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)v);
+  const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(v >> 32));
+  return (uint64_t)hi << 32 | lo;
+}
+// (nullptr: nothing is dropped)
+__device__ __forceinline__ RngState load_state(const RngState *p) {
+  RngState s{0, 0};
+  if (p != nullptr) s = *p;
+  return RngState{same_in_warp(s.seed), same_in_warp(s.offset)};
+}
+
 __device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint2 k) {
 #pragma unroll
   for (int round = 0; round < 10; ++round) {
@@ -30,17 +45,21 @@ __device__ __forceinline__ uint4 dropout_bits(const RngState &st, uint32_t block
       make_uint2((uint32_t)st.seed, (uint32_t)(st.seed >> 32)));
 }
 
+// Whether the elements of a word, an even one and the next, are kept, from the
+// threshold in the upper half of `cut` (a lower half is compared where it is
+// shifted to: no bits are extracted).
+__device__ __forceinline__ bool kept_even(uint32_t word, uint32_t cut) { return word << 16 >= cut; }
+__device__ __forceinline__ bool kept_odd(uint32_t word, uint32_t cut) { return word >= cut; }
+
 // Bit i: element 8 block + i of the row is kept.
 __device__ __forceinline__ uint32_t dropout_keep(const RngState &st, uint32_t block, uint32_t row,
                                                  uint32_t threshold) {
   const uint4 v = dropout_bits(st, block, row);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w}, cut = threshold << 16;
   uint32_t keep = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    keep |= ((w[i] & 0xffffu) >= threshold ? 1u : 0u) << (2 * i);
-    keep |= ((w[i] >> 16) >= threshold ? 1u : 0u) << (2 * i + 1);
-  }
+  for (int i = 0; i < 4; ++i)
+    keep |= (kept_even(w[i], cut) ? 1u << (2 * i) : 0u) | (kept_odd(w[i], cut) ? 2u << (2 * i) : 0u);
   return keep;
 }
 
