@@ -41,31 +41,35 @@ join_vec_kernel(const __grid_constant__ Fwd<T> a, int tpr, int groups, int stage
   extern __shared__ __align__(16) uint4 dyn[];   // [stage][row][block][b, x][vector][thread]
   __shared__ float2 buf[2][32];
   using V = Vec8<T>;
+  constexpr int PIECE = NB == 1 ? 2 * V8_PIECE : V8_PIECE, STAGE = R * NB * 2 * V::Q * PIECE;
   const moe_join_config &c = a.c;
-  const int d = c.d, warps = tpr >> 5, nthr = blockDim.x;
-  const int group = WARP ? threadIdx.x >> 5 : threadIdx.x / tpr;
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x - group * tpr;
+  const int d = c.d, warps = tpr >> 5, warp = threadIdx.x >> 5;
+  const int group = WARP ? warp : warp / warps, tid = threadIdx.x - group * tpr;
   const int first_warp = group * warps;
   const float inv_d = 1.f / (float)d;
   const RngState st = load_state(DROP ? a.rng : nullptr);
   const uint32_t cut = (uint32_t)a.threshold << 16;
   const bool layer1 = CENTRED && c.post == MOE_NORM_LAYER, layer2 = CENTRED && c.pre == MOE_NORM_LAYER;
-  int turn = 0, stage = 0;
+  const bool norm1 = c.post != MOE_NORM_NONE, norm2 = c.pre != MOE_NORM_NONE;
+  int turn = 0;
+  // blocks of this thread: the first from column 8 tid on, `apart` bytes between them
+  const int apart = tpr * 8 * (int)sizeof(T);
   bool on[NB];
-  int col[NB];
   // what the block's output and the joined row are multiplied by, and shifted
   Block8 p1[NB], p2[NB], q1[CENTRED ? NB : 1], q2[CENTRED ? NB : 1];
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    col[n] = (tid + n * tpr) * 8;
-    on[n] = col[n] < d;
+    const int col = (tid + n * tpr) * 8;
+    on[n] = col < d;
+    p1[n] = p2[n] = fill8(0.f);
+    if (CENTRED) q1[n] = q2[n] = fill8(0.f);
     if (!on[n]) continue;
-    p1[n] = V::param(a.gate, col[n], 1.f);
-    const Block8 g = V::param(a.post_gamma, col[n], 1.f);
-    p2[n] = V::param(a.pre_gamma, col[n], 1.f);
+    p1[n] = V::param(a.gate, col, 1.f);
+    const Block8 g = V::param(a.post_gamma, col, 1.f);
+    p2[n] = V::param(a.pre_gamma, col, 1.f);
     if (CENTRED) {
-      q1[n] = V::param(a.post_beta, col[n], 0.f);
-      q2[n] = V::param(a.pre_beta, col[n], 0.f);
+      q1[n] = V::param(a.post_beta, col, 0.f);
+      q2[n] = V::param(a.pre_beta, col, 0.f);
     }
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
@@ -75,31 +79,30 @@ join_vec_kernel(const __grid_constant__ Fwd<T> a, int tpr, int groups, int stage
     }
   }
   const int64_t step = (int64_t)gridDim.x * groups * R;
-  const int64_t first = ((int64_t)blockIdx.x * groups + group) * R;
-  auto piece = [&](int at, int k, int n, int t) {
-    return dyn + ((((at * R + k) * NB + n) * 2 + t) * V::Q) * nthr + threadIdx.x;
+  int64_t row = ((int64_t)blockIdx.x * groups + group) * R, ahead = row;
+  uint8_t *const mine = reinterpret_cast<uint8_t *>(dyn) + threadIdx.x * 16;
+  uint8_t *const ring_end = mine + stages * STAGE;
+  auto bytes = [](int64_t elements) { return elements * (int64_t)sizeof(T); };
+  auto start = [&](const T *p, int64_t ld) {
+    return reinterpret_cast<const char *>(p + row * ld + tid * 8);
   };
-  int64_t ahead = first;
-  const T *b_ahead = a.b + first * c.ldb, *x_ahead = a.x + first * c.ldx;
-  const int64_t sb = step * c.ldb, sx = step * c.ldx;
-  auto fill = [&](int at) {
+  const char *b_ahead = start(a.b, c.ldb), *x_ahead = start(a.x, c.ldx);
+  char *r_out = const_cast<char *>(start(a.r, c.ldr)), *y_out = const_cast<char *>(start(a.y, c.ldy));
+  auto fill = [&](uint8_t *to) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       if (ahead + k >= c.rows) break;
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         if (!on[n]) continue;
-#pragma unroll
-        for (int q = 0; q < V::Q; ++q) {
-          copy16_async(piece(at, k, n, 0) + q * nthr, b_ahead + k * c.ldb + col[n] + q * 8 / V::Q);
-          copy16_async(piece(at, k, n, 1) + q * nthr, x_ahead + k * c.ldx + col[n] + q * 8 / V::Q);
-        }
+        V::template copy<PIECE>(to, (k * NB + n) * 2, b_ahead + k * bytes(c.ldb) + n * apart);
+        V::template copy<PIECE>(to, (k * NB + n) * 2 + 1, x_ahead + k * bytes(c.ldx) + n * apart);
       }
     }
     copy_commit();
     ahead += step;
-    b_ahead += sb;
-    x_ahead += sx;
+    b_ahead += bytes(step * c.ldb);
+    x_ahead += bytes(step * c.ldx);
   };
   // the rows' sums over their group
   auto sums = [&](float2 (&s)[R]) {
@@ -112,13 +115,11 @@ join_vec_kernel(const __grid_constant__ Fwd<T> a, int tpr, int groups, int stage
       s[R - 1].x = t.y;
     }
   };
-  for (int i = 0; i < stages - 1; ++i) fill(i);
-  const int64_t first_of_cta = (int64_t)blockIdx.x * groups * R;
-  T *r_out = a.r + first * c.ldr, *y_out = a.y + first * c.ldy;
-  for (int64_t r0 = first_of_cta; r0 < c.rows; r0 += step) {
-    const int64_t row = r0 + group * R;
+  for (int i = 0; i < stages - 1; ++i) fill(mine + i * STAGE);
+  uint8_t *now = mine, *next = mine + (stages - 1) * STAGE;
+  for (int64_t r0 = (int64_t)blockIdx.x * groups * R; r0 < c.rows; r0 += step) {
     // (the stage being filled was read by this thread in the iteration before)
-    fill(stage == 0 ? stages - 1 : stage - 1);
+    fill(next);
     copies_wait(stages - 1);
     Block8 v[R][NB];
     float mean1[R], rstd1[R], mean2[R], rstd2[R];
@@ -131,7 +132,7 @@ join_vec_kernel(const __grid_constant__ Fwd<T> a, int tpr, int groups, int stage
       rstd1[k] = rstd2[k] = 1.f;
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        v[k][n] = there(k, n) ? V::load(piece(stage, k, n, 0), nthr) : fill8(0.f);
+        v[k][n] = there(k, n) ? V::template ring<PIECE>(now, (k * NB + n) * 2) : fill8(0.f);
         if (layer1) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) s[k] = add2(s[k], v[k][n].v[h]);
@@ -152,7 +153,7 @@ join_vec_kernel(const __grid_constant__ Fwd<T> a, int tpr, int groups, int stage
         }
       }
     }
-    if (c.post != MOE_NORM_NONE) {
+    if (norm1) {
 #pragma unroll
       for (int k = 0; k < R; ++k)
 #pragma unroll
@@ -174,16 +175,16 @@ join_vec_kernel(const __grid_constant__ Fwd<T> a, int tpr, int groups, int stage
           continue;
         }
         Block8 &z = v[k][n];
-        const Block8 x = V::load(piece(stage, k, n, 1), nthr);
+        const Block8 x = V::template ring<PIECE>(now, (k * NB + n) * 2 + 1);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           z.v[h] = mul2(z.v[h], both(rstd1[k]));
           z.v[h] = CENTRED ? fma2(z.v[h], p1[n].v[h], q1[n].v[h]) : mul2(z.v[h], p1[n].v[h]);
         }
-        if (DROP) drop8(z, dropout_bits(st, col[n] >> 3, (uint32_t)(row + k)), cut);
+        if (DROP) drop8(z, dropout_bits(st, tid + n * tpr, (uint32_t)(row + k)), cut);
 #pragma unroll
         for (int h = 0; h < 4; ++h) z.v[h] = fma2(both(c.scale), x.v[h], z.v[h]);
-        V::store(r_out + k * c.ldr + col[n], z);
+        V::store(r_out + k * bytes(c.ldr) + n * apart, z);
         if (layer2) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) s[k] = add2(s[k], z.v[h]);
@@ -193,8 +194,9 @@ join_vec_kernel(const __grid_constant__ Fwd<T> a, int tpr, int groups, int stage
         }
       }
     }
-    stage = stage + 1 == stages ? 0 : stage + 1;
-    if (c.pre != MOE_NORM_NONE) {
+    next = now;
+    now = now + STAGE == ring_end ? mine : now + STAGE;
+    if (norm2) {
       sums(s);
       if (layer2) {
 #pragma unroll
@@ -225,7 +227,7 @@ join_vec_kernel(const __grid_constant__ Fwd<T> a, int tpr, int groups, int stage
             z.v[h] = mul2(z.v[h], both(rstd2[k]));
             z.v[h] = CENTRED ? fma2(z.v[h], p2[n].v[h], q2[n].v[h]) : mul2(z.v[h], p2[n].v[h]);
           }
-          V::store(y_out + k * c.ldy + col[n], z);
+          V::store(y_out + k * bytes(c.ldy) + n * apart, z);
         }
       }
     }
@@ -239,8 +241,9 @@ join_vec_kernel(const __grid_constant__ Fwd<T> a, int tpr, int groups, int stage
         a.stats[3 * c.rows + row + k] = rstd2[k];
       }
     }
-    r_out += step * c.ldr;
-    y_out += step * c.ldy;
+    row += step;
+    r_out += bytes(step * c.ldr);
+    y_out += bytes(step * c.ldy);
   }
 }
 
@@ -504,8 +507,10 @@ cudaError_t run_odd(const Fwd<T> &a, int tpr, cudaStream_t s) {
 template <typename T, int NB, int R, bool WARP, bool DROP, bool CENTRED>
 cudaError_t run_vec(const Fwd<T> &a, int tpr, cudaStream_t s) {
   auto kernel = join_vec_kernel<T, NB, R, WARP, DROP, CENTRED>;
-  const int groups = tpr <= 128 ? 128 / tpr : 1, threads = tpr * groups;
-  const size_t stage = (size_t)threads * R * NB * 2 * Vec8<T>::Q * 16;
+  int groups = tpr < 512 ? 512 / tpr : 1;
+  while (groups > 1 && a.c.rows <= (int64_t)(groups / 2) * R * num_sms()) groups /= 2;
+  const int threads = tpr * groups;
+  const size_t stage = (size_t)R * NB * 2 * Vec8<T>::Q * (NB == 1 ? 2 * V8_PIECE : V8_PIECE);
   int stages = 3;
   while (stages > 1 && stages * stage > J_SMEM) --stages;
   const size_t smem = stages * stage;

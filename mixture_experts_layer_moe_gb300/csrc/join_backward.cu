@@ -6,7 +6,6 @@ namespace {
 
 using namespace join;
 
-constexpr int BNB = 2, BR = 1;
 constexpr int J_PARTS = 152;   // partial rows of the column sums, at most
 constexpr int J_SUMS = 4;      // sum u bh, sum u, sum dy rh, sum dy
 
@@ -27,16 +26,17 @@ struct Bwd {
 };
 
 
-// The statistics of a row as the forward left them.
-template <typename T>
+// The statistics of a row as the forward left them: the post norm's mean and 1 /
+// deviation, then the pre norm's (MEANS: the means are read).
+template <typename T, bool MEANS = true>
 __device__ __forceinline__ float4 stats_of(const Bwd<T> &a, int64_t row) {
   float4 v = make_float4(0.f, 1.f, 0.f, 1.f);
   if (a.c.post != MOE_NORM_NONE) {
-    v.x = a.stats[row];
+    if (MEANS) v.x = a.stats[row];
     v.y = a.stats[a.c.rows + row];
   }
-  if (a.c.pre != MOE_NORM_NONE && a.dy) {
-    v.z = a.stats[2 * a.c.rows + row];
+  if (a.dy) {
+    if (MEANS) v.z = a.stats[2 * a.c.rows + row];
     v.w = a.stats[3 * a.c.rows + row];
   }
   return v;
@@ -62,219 +62,205 @@ __device__ __forceinline__ void store_columns(const Bwd<T> &a, float *cols, int 
   }
 }
 
-// Rows of whole vectors, as the forward's kernel takes them.  CENTRED: a layer norm
-// is among the norms; the sums of u and dy may be wanted then.
-template <typename T, int NB, int R, bool WARP, bool DROP, bool CENTRED>
+// Rows of whole vectors, as the forward's kernel takes them.  With rc = r - mean2, bc = b
+// - mean1 (the rows themselves without a layer norm, which CENTRED says there is):
+//   g = dr + rstd2 dy gamma2 + c2 rc + e2,   c2 = -rstd2^2 mean(w rh),  e2 = -rstd2 mean(w),
+//   h = D(g) rstd1 gate gamma1,   db = h + c1 bc + e1  likewise,
+// so that neither rh nor bh is formed for itself.
+template <typename T, int NB, bool WARP, bool DROP, bool CENTRED>
 __global__ void __launch_bounds__(512, 1)
-join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, int stages,
-                         int tensors) {
-  extern __shared__ __align__(16) uint4 dyn[];   // [stage][row][block][tensor][vector][thread]
+join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, int stages) {
+  extern __shared__ __align__(16) uint4 dyn[];   // [stage][block][dr, dy, r, b][vector][thread]
   __shared__ float2 buf[2][32];
   using V = Vec8<T>;
+  constexpr int PIECE = V8_PIECE, STAGE = NB * 4 * V::Q * PIECE;
+  enum { DR, DY, RR, BB };
   const moe_join_config &c = a.c;
-  const int d = c.d, warps = tpr >> 5, nthr = blockDim.x;
-  const int group = WARP ? threadIdx.x >> 5 : threadIdx.x / tpr;
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x - group * tpr;
+  const int d = c.d, warps = tpr >> 5, warp = threadIdx.x >> 5;
+  const int group = WARP ? warp : warp / warps, tid = threadIdx.x - group * tpr;
   const int first_warp = group * warps;
   const bool has_dr = a.dr != nullptr, has_dy = a.dy != nullptr, has_b = a.has_b;
-  const int at_b = has_dr, at_dy = at_b + has_b, at_r = at_dy + 1;   // (dr first)
+  const bool norm1 = c.post != MOE_NORM_NONE;
+  const bool layer1 = CENTRED && c.post == MOE_NORM_LAYER, layer2 = CENTRED && c.pre == MOE_NORM_LAYER;
   const float inv_d = 1.f / (float)d;
   const RngState st = load_state(DROP ? a.rng : nullptr);
   const uint32_t cut = (uint32_t)a.threshold << 16;
-  int turn = 0, stage = 0;
+  int turn = 0;
   pdl_launch_dependents();   // (the column sums wait for this grid to end)
+  const int apart = tpr * 8 * (int)sizeof(T);
   bool on[NB];
-  int col[NB];
   // what D's kept elements and dy are multiplied by; the column sums of u bh, dy rh, u
   // and dy, those of u without dropout's factor
   Block8 p1[NB], p2[NB], sum_a[NB], sum_c[NB], sum_b[CENTRED ? NB : 1], sum_e[CENTRED ? NB : 1];
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
-    col[n] = (tid + n * tpr) * 8;
-    on[n] = col[n] < d;
-    sum_a[n] = sum_c[n] = fill8(0.f);
+    const int col = (tid + n * tpr) * 8;
+    on[n] = col < d;
+    p1[n] = p2[n] = sum_a[n] = sum_c[n] = fill8(0.f);
     if (CENTRED) sum_b[n] = sum_e[n] = fill8(0.f);
     if (!on[n]) continue;
-    p1[n] = V::param(a.gate, col[n], 1.f);
-    p2[n] = V::param(a.pre_gamma, col[n], 1.f);
-    const Block8 g = V::param(a.post_gamma, col[n], 1.f);
+    p1[n] = V::param(a.gate, col, 1.f);
+    p2[n] = V::param(a.pre_gamma, col, 1.f);
+    const Block8 g = V::param(a.post_gamma, col, 1.f);
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       p1[n].v[h] = mul2(p1[n].v[h], g.v[h]);
       if (DROP) p1[n].v[h] = mul2(p1[n].v[h], both(a.factor));
     }
   }
-  const int64_t step = (int64_t)gridDim.x * groups * R;
-  const int64_t first = ((int64_t)blockIdx.x * groups + group) * R;
-  auto piece = [&](int at, int k, int n, int t) {
-    return dyn + ((((at * R + k) * NB + n) * tensors + t) * V::Q) * nthr + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + group, ahead = row;
+  uint8_t *const mine = reinterpret_cast<uint8_t *>(dyn) + threadIdx.x * 16;
+  uint8_t *const ring_end = mine + stages * STAGE;
+  auto bytes = [](int64_t elements) { return elements * (int64_t)sizeof(T); };
+  auto start = [&](const T *p, int64_t ld) {
+    return reinterpret_cast<const char *>(p + row * ld + tid * 8);
   };
-  int64_t ahead = first;
-  auto fill = [&](int at) {
+  const char *dr_ahead = start(a.dr, c.lddr), *dy_ahead = start(a.dy, c.lddy);
+  const char *r_ahead = start(a.r, c.ldr), *b_ahead = start(a.b, c.ldb);
+  char *dx_out = const_cast<char *>(start(a.dx, c.lddx));
+  char *db_out = const_cast<char *>(start(a.db, c.lddb));
+  auto fill = [&](uint8_t *to) {
+    if (ahead < c.rows) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int64_t row = ahead + k;
-      if (row >= c.rows) break;
-      auto copy = [&](int t, const T *from) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          if (!on[n]) continue;
-#pragma unroll
-          for (int q = 0; q < V::Q; ++q)
-            copy16_async(piece(at, k, n, t) + q * nthr, from + col[n] + q * 8 / V::Q);
+      for (int n = 0; n < NB; ++n) {
+        if (!on[n]) continue;
+        if (has_dy) {
+          V::template copy<PIECE>(to, n * 4 + DY, dy_ahead + n * apart);
+          V::template copy<PIECE>(to, n * 4 + RR, r_ahead + n * apart);
         }
-      };
-      if (has_dy) {
-        copy(at_dy, a.dy + row * c.lddy);
-        copy(at_r, a.r + row * c.ldr);
+        if (has_dr) V::template copy<PIECE>(to, n * 4 + DR, dr_ahead + n * apart);
+        if (has_b) V::template copy<PIECE>(to, n * 4 + BB, b_ahead + n * apart);
       }
-      if (has_dr) copy(0, a.dr + row * c.lddr);
-      if (has_b) copy(at_b, a.b + row * c.ldb);
     }
     copy_commit();
     ahead += step;
+    dr_ahead += bytes(step * c.lddr);
+    dy_ahead += bytes(step * c.lddy);
+    r_ahead += bytes(step * c.ldr);
+    b_ahead += bytes(step * c.ldb);
   };
-  for (int i = 0; i < stages - 1; ++i) fill(i);
-  float4 next[R];
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    next[k] = make_float4(0.f, 1.f, 0.f, 1.f);
-    if (first + k < c.rows) next[k] = stats_of(a, first + k);
-  }
-  for (int64_t r0 = (int64_t)blockIdx.x * groups * R; r0 < c.rows; r0 += step) {
-    const int64_t row = r0 + group * R;
+  for (int i = 0; i < stages - 1; ++i) fill(mine + i * STAGE);
+  uint8_t *now = mine, *next = mine + (stages - 1) * STAGE;
+  float4 next_stat = make_float4(0.f, 1.f, 0.f, 1.f);
+  if (row < c.rows) next_stat = stats_of<T, CENTRED>(a, row);
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < c.rows; r0 += step) {
+    const bool live = row < c.rows;
     // (the stage being filled was read by this thread in the iteration before)
-    fill(stage == 0 ? stages - 1 : stage - 1);
-    float4 stat[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      stat[k] = next[k];
-      if (row + step + k < c.rows) next[k] = stats_of(a, row + step + k);
-    }
+    fill(next);
+    const float4 stat = next_stat;
+    if (row + step < c.rows) next_stat = stats_of<T, CENTRED>(a, row + step);
     copies_wait(stages - 1);
-    auto there = [&](int k, int n) { return on[n] && row + k < c.rows; };
-    auto get = [&](int k, int n, int t) { return V::load(piece(stage, k, n, t), nthr); };
-    // the normed row: rh of r, or bh of b
-    auto normed = [&](Block8 &b, float mean, float rstd) {
+    auto get = [&](int n, int t) { return V::template ring<PIECE>(now, n * 4 + t); };
+    auto centred = [&](int n, int t, float mean) {
+      Block8 b = get(n, t);
+      if (CENTRED) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
-        b.v[h] = mul2(CENTRED ? add2(b.v[h], both(-mean)) : b.v[h], both(rstd));
+        for (int h = 0; h < 4; ++h) b.v[h] = add2(b.v[h], both(-mean));
+      }
+      return b;
     };
-    float2 m[R];   // minus the means of w and of w rh
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      m[k] = both(0.f);
-      if (!has_dy) continue;
+    float c2 = 0.f, e2 = 0.f;
+    if (has_dy) {
       float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        if (!there(k, n)) continue;
-        const Block8 dy = get(k, n, at_dy);
-        Block8 rh = get(k, n, at_r);
-        normed(rh, stat[k].z, stat[k].w);
+        if (!live || !on[n]) continue;
+        const Block8 dy = get(n, DY), rc = centred(n, RR, stat.z);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          sum_c[n].v[h] = fma2(dy.v[h], rh.v[h], sum_c[n].v[h]);
-          if (CENTRED) sum_e[n].v[h] = add2(sum_e[n].v[h], dy.v[h]);
           const float2 w = mul2(dy.v[h], p2[n].v[h]);
           if (CENTRED) s1 = add2(s1, w);
-          s2 = fma2(w, rh.v[h], s2);
+          s2 = fma2(w, rc.v[h], s2);
         }
       }
-      m[k] = make_float2(s1.x + s1.y, s2.x + s2.y);
+      if (CENTRED) {
+        const float2 t = group_sum2<WARP>(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
+        e2 = layer2 ? -stat.w * t.x * inv_d : 0.f;
+        c2 = -stat.w * stat.w * stat.w * t.y * inv_d;
+      } else {
+        const float t = group_sum<WARP>(s2.x + s2.y, reinterpret_cast<float (*)[32]>(buf), turn, warps);
+        c2 = -stat.w * stat.w * stat.w * t * inv_d;
+      }
     }
-    auto join_sums = [&](float2 (&s)[R], int kind) {
-      if (!CENTRED && R == 2) {
-        // (an RMS norm takes one sum of each row)
-        const float2 t = group_sum2<WARP>(s[0].y, s[R - 1].y, buf, turn, first_warp, warps);
-        s[0].y = t.x;
-        s[R - 1].y = t.y;
+    Block8 w[NB];
+    float2 s1 = both(0.f), s2 = both(0.f);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      w[n] = fill8(0.f);
+      if (!live || !on[n]) continue;
+      Block8 g = has_dr ? get(n, DR) : fill8(0.f);
+      if (has_dy) {
+        const Block8 rc = centred(n, RR, stat.z);
+        Block8 dy = get(n, DY);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if (CENTRED) {
+            sum_e[n].v[h] = add2(sum_e[n].v[h], dy.v[h]);
+            g.v[h] = add2(g.v[h], both(e2));
+          }
+          dy.v[h] = mul2(dy.v[h], both(stat.w));
+          sum_c[n].v[h] = fma2(dy.v[h], rc.v[h], sum_c[n].v[h]);
+          g.v[h] = fma2(dy.v[h], p2[n].v[h], fma2(rc.v[h], both(c2), g.v[h]));
+        }
+      }
+      if (a.dx) {
+        Block8 t;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) t.v[h] = mul2(both(c.scale), g.v[h]);
+        V::store(dx_out + n * apart, t);
+      }
+      if (DROP) drop8(g, dropout_bits(st, tid + n * tpr, (uint32_t)row), cut);
+      if (CENTRED) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) sum_b[n].v[h] = add2(sum_b[n].v[h], g.v[h]);
+      }
+      if (norm1) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) g.v[h] = mul2(g.v[h], both(stat.y));
+      }
+      if (has_b) {
+        const Block8 bc = centred(n, BB, stat.x);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          sum_a[n].v[h] = fma2(g.v[h], bc.v[h], sum_a[n].v[h]);
+          w[n].v[h] = mul2(g.v[h], p1[n].v[h]);
+          if (CENTRED) s1 = add2(s1, w[n].v[h]);
+          s2 = fma2(w[n].v[h], bc.v[h], s2);
+        }
       } else {
 #pragma unroll
-        for (int k = 0; k < R; ++k)
-          s[k] = group_sum2<WARP>(s[k].x, s[k].y, buf, turn, first_warp, warps);
+        for (int h = 0; h < 4; ++h) w[n].v[h] = mul2(g.v[h], p1[n].v[h]);
       }
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-        s[k] = make_float2(kind == MOE_NORM_LAYER ? -s[k].x * inv_d : 0.f, -s[k].y * inv_d);
-    };
-    if (has_dy) join_sums(m, c.pre);
-    Block8 w[R][NB];
-    float2 q[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      float2 s1 = both(0.f), s2 = both(0.f);
+    }
+    if (a.db) {
+      // (w is rstd1 times the gradient of the normed row)
+      float c1 = 0.f, e1 = 0.f;
+      if (norm1 && CENTRED) {
+        const float2 t = group_sum2<WARP>(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
+        e1 = layer1 ? -t.x * inv_d : 0.f;
+        c1 = -stat.y * stat.y * t.y * inv_d;
+      } else if (norm1) {
+        const float t = group_sum<WARP>(s2.x + s2.y, reinterpret_cast<float (*)[32]>(buf), turn, warps);
+        c1 = -stat.y * stat.y * t * inv_d;
+      }
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        if (!there(k, n)) {
-          w[k][n] = fill8(0.f);
-          continue;
-        }
-        Block8 g = has_dr ? get(k, n, 0) : fill8(0.f);
-        if (has_dy) {
-          const Block8 dy = get(k, n, at_dy);
-          Block8 rh = get(k, n, at_r);
-          normed(rh, stat[k].z, stat[k].w);
+        if (!live || !on[n]) continue;
+        if (norm1) {
+          const Block8 bc = centred(n, BB, stat.x);
 #pragma unroll
           for (int h = 0; h < 4; ++h)
-            g.v[h] = fma2(both(stat[k].w),
-                          fma2(rh.v[h], both(m[k].y),
-                               CENTRED ? fma2(dy.v[h], p2[n].v[h], both(m[k].x))
-                                       : mul2(dy.v[h], p2[n].v[h])),
-                          g.v[h]);
+            w[n].v[h] = fma2(bc.v[h], both(c1), CENTRED ? add2(w[n].v[h], both(e1)) : w[n].v[h]);
         }
-        if (a.dx) {
-          Block8 t;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) t.v[h] = mul2(both(c.scale), g.v[h]);
-          V::store(a.dx + (row + k) * c.lddx + col[n], t);
-        }
-        if (DROP) drop8(g, dropout_bits(st, col[n] >> 3, (uint32_t)(row + k)), cut);
-        if (CENTRED) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) sum_b[n].v[h] = add2(sum_b[n].v[h], g.v[h]);
-        }
-        Block8 bh;
-        if (has_b) {
-          bh = get(k, n, at_b);
-          if (c.post != MOE_NORM_NONE) normed(bh, stat[k].x, stat[k].y);
-#pragma unroll
-          for (int h = 0; h < 4; ++h) sum_a[n].v[h] = fma2(g.v[h], bh.v[h], sum_a[n].v[h]);
-        }
-#pragma unroll
-        for (int h = 0; h < 4; ++h) g.v[h] = mul2(g.v[h], p1[n].v[h]);
-        if (c.post != MOE_NORM_NONE) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            if (CENTRED) s1 = add2(s1, g.v[h]);
-            s2 = fma2(g.v[h], bh.v[h], s2);
-          }
-        } else if (a.db) {
-          V::store(a.db + (row + k) * c.lddb + col[n], g);
-        }
-        w[k][n] = g;
-      }
-      q[k] = make_float2(s1.x + s1.y, s2.x + s2.y);
-    }
-    if (c.post != MOE_NORM_NONE && a.db) {
-      join_sums(q, c.post);
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          if (!there(k, n)) continue;
-          Block8 bh = get(k, n, at_b);
-          normed(bh, stat[k].x, stat[k].y);
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            bh.v[h] = mul2(both(stat[k].y),
-                           fma2(bh.v[h], both(q[k].y),
-                                CENTRED ? add2(w[k][n].v[h], both(q[k].x)) : w[k][n].v[h]));
-          V::store(a.db + (row + k) * c.lddb + col[n], bh);
-        }
+        V::store(db_out + n * apart, w[n]);
       }
     }
-    stage = stage + 1 == stages ? 0 : stage + 1;
+    next = now;
+    now = now + STAGE == ring_end ? mine : now + STAGE;
+    row += step;
+    dx_out += bytes(step * c.lddx);
+    db_out += bytes(step * c.lddb);
   }
   copy_wait<0>();   // (none is in flight: the ones past the last row were empty)
 #pragma unroll
@@ -290,7 +276,7 @@ join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, 
         const Block8 &s = which == 0 ? sum_a[n] : which == 1 ? sum_b[e] : which == 2 ? sum_c[n] : sum_e[e];
 #pragma unroll
         for (int h = 0; h < 4; h += 2)
-          *reinterpret_cast<float4 *>(to + col[n] + 2 * h) =
+          *reinterpret_cast<float4 *>(to + (tid + n * tpr) * 8 + 2 * h) =
               make_float4(s.v[h].x * factor, s.v[h].y * factor, s.v[h + 1].x * factor,
                           s.v[h + 1].y * factor);
       }
@@ -651,24 +637,23 @@ __global__ void __launch_bounds__(1024) join_finish_kernel(const __grid_constant
 
 // Groups of tpr threads in a CTA of up to 512 threads, fewer where there are SMs to
 // spare (one CTA per SM leaves a partial row of each column sum), and the stages
-// of a ring of `stage` bytes per group.
+// of a ring whose stage takes `fixed` bytes and `each` per group.  The column sums
+// (`columns` bytes of a group) take the ring's place at the end.
 struct BwdPlan {
-  int groups, stages, parts, tensors;
+  int groups, stages, parts;
   size_t smem;
 };
 template <typename T>
-BwdPlan plan(const Bwd<T> &a, int tpr, int rows_each, size_t tensor_bytes, size_t masks,
-             size_t columns) {
+BwdPlan plan(const Bwd<T> &a, int tpr, size_t fixed, size_t each, size_t masks, size_t columns) {
   BwdPlan p;
-  p.tensors = (a.dr ? 1 : 0) + (a.has_b ? 1 : 0) + (a.dy ? 2 : 0);
   p.groups = J_THREADS / tpr;
-  while (p.groups > 1 && a.c.rows <= (int64_t)(p.groups / 2) * rows_each * J_PARTS) p.groups /= 2;
-  const size_t stage = p.groups * p.tensors * tensor_bytes;
+  while (p.groups > 1 && a.c.rows <= (int64_t)(p.groups / 2) * J_PARTS) p.groups /= 2;
+  const size_t stage = fixed + p.groups * each;
   p.stages = 3;
   while (p.stages > 1 && p.stages * stage + p.groups * masks > J_SMEM) --p.stages;
   p.smem = p.stages * stage + p.groups * masks;
   if (p.groups > 1 && p.smem < p.groups * columns) p.smem = p.groups * columns;
-  p.parts = (int)grid_of(a.c.rows, p.groups * rows_each, J_PARTS);
+  p.parts = (int)grid_of(a.c.rows, p.groups, J_PARTS);
   return p;
 }
 
@@ -684,41 +669,42 @@ cudaError_t allow_smem(K kernel, bool &set) {
 template <typename T, bool WARP>
 cudaError_t run_odd(const Bwd<T> &a, int tpr, int &parts, cudaStream_t s) {
   auto kernel = join_backward_odd_kernel<T, WARP>;
-  const BwdPlan p = plan(a, tpr, 1, slot_bytes(a.c.d, sizeof(T)), 2 * mask_bytes(a.c.d),
-                         (size_t)tpr * 16 * 4);
+  const int tensors = (a.dr ? 1 : 0) + (a.has_b ? 1 : 0) + (a.dy ? 2 : 0);
+  const BwdPlan p = plan(a, tpr, 0, (size_t)tensors * slot_bytes(a.c.d, sizeof(T)),
+                         2 * mask_bytes(a.c.d), (size_t)tpr * 16 * 4);
   static bool set = false;
   const cudaError_t e = allow_smem(kernel, set);
   if (e != cudaSuccess) return e;
   parts = p.parts;
-  kernel<<<parts, tpr * p.groups, p.smem, s>>>(a, tpr, p.groups, p.stages, p.tensors);
+  kernel<<<parts, tpr * p.groups, p.smem, s>>>(a, tpr, p.groups, p.stages, tensors);
   return cudaGetLastError();
 }
 
-template <typename T, int NB, int R, bool WARP, bool DROP, bool CENTRED>
+template <typename T, int NB, bool WARP, bool DROP, bool CENTRED>
 cudaError_t run_vec(const Bwd<T> &a, int tpr, int &parts, cudaStream_t s) {
-  auto kernel = join_backward_vec_kernel<T, NB, R, WARP, DROP, CENTRED>;
-  const BwdPlan p = plan(a, tpr, R, (size_t)tpr * R * NB * Vec8<T>::Q * 16, 0, (size_t)tpr * NB * 32);
+  auto kernel = join_backward_vec_kernel<T, NB, WARP, DROP, CENTRED>;
+  const BwdPlan p = plan(a, tpr, (size_t)NB * 4 * Vec8<T>::Q * V8_PIECE, 0, 0, (size_t)tpr * NB * 32);
   static bool set = false;
   const cudaError_t e = allow_smem(kernel, set);
   if (e != cudaSuccess) return e;
   parts = p.parts;
-  kernel<<<parts, tpr * p.groups, p.smem, s>>>(a, tpr, p.groups, p.stages, p.tensors);
+  kernel<<<parts, tpr * p.groups, p.smem, s>>>(a, tpr, p.groups, p.stages);
   return cudaGetLastError();
 }
-template <typename T, int NB, int R, bool WARP>
+template <typename T, int NB, bool WARP>
 cudaError_t vec_kinds(const Bwd<T> &a, int tpr, int &parts, cudaStream_t s) {
   const bool centred = a.c.post == MOE_NORM_LAYER || a.c.pre == MOE_NORM_LAYER;
   if (a.threshold)
-    return centred ? run_vec<T, NB, R, WARP, true, true>(a, tpr, parts, s)
-                   : run_vec<T, NB, R, WARP, true, false>(a, tpr, parts, s);
-  return centred ? run_vec<T, NB, R, WARP, false, true>(a, tpr, parts, s)
-                 : run_vec<T, NB, R, WARP, false, false>(a, tpr, parts, s);
+    return centred ? run_vec<T, NB, WARP, true, true>(a, tpr, parts, s)
+                   : run_vec<T, NB, WARP, true, false>(a, tpr, parts, s);
+  return centred ? run_vec<T, NB, WARP, false, true>(a, tpr, parts, s)
+                 : run_vec<T, NB, WARP, false, false>(a, tpr, parts, s);
 }
-template <typename T, int NB, int R>
+template <typename T, int NB>
 cudaError_t vec_rows(const Bwd<T> &a, int &parts, cudaStream_t s) {
   const int tpr = ((a.c.d + 8 * NB - 1) / (8 * NB) + 31) / 32 * 32;
-  return tpr == 32 ? vec_kinds<T, NB, R, true>(a, tpr, parts, s)
-                   : vec_kinds<T, NB, R, false>(a, tpr, parts, s);
+  return tpr == 32 ? vec_kinds<T, NB, true>(a, tpr, parts, s)
+                   : vec_kinds<T, NB, false>(a, tpr, parts, s);
 }
 
 template <typename T>
@@ -751,7 +737,8 @@ cudaError_t backward(const moe_join_config &c, int threshold, const JoinBackward
   int parts = 0;
   cudaError_t e;
   if (tpr && vectors) {
-    e = vec_rows<T, BNB, BR>(a, parts, s);
+    // (fp32: one block per thread where that is enough, so that three rows fit the ring)
+    e = sizeof(T) == 4 && c.d <= 4096 ? vec_rows<T, 1>(a, parts, s) : vec_rows<T, 2>(a, parts, s);
   } else if (tpr) {
     e = tpr == 32 ? run_odd<T, true>(a, tpr, parts, s) : run_odd<T, false>(a, tpr, parts, s);
   } else {

@@ -37,23 +37,47 @@ struct Block8 {
 };
 __device__ __forceinline__ Block8 fill8(float a) { return Block8{both(a), both(a), both(a), both(a)}; }
 
+// A thread's vectors lie a fixed distance apart in the ring, whatever the CTA's size (this
+// one holds up to 512 threads): the offsets of a stage's vectors are constants then (with distances that go by
+// the number of threads the gradient's kernel spent a fifth of its instructions
+// on them).
+constexpr int V8_PIECE = J_THREADS * 16;
 template <typename T>
 struct Vec8 {
   static constexpr int Q = 8 * sizeof(T) / 16;   // 16-byte vectors of a block
-  static __device__ __forceinline__ Block8 load(const uint4 *p, int stride) {
+  static __device__ __forceinline__ Block8 unpack(const uint4 (&raw)[Q]) {
     Block8 b;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) unpack16<T>(p[q * stride], reinterpret_cast<float *>(b.v) + q * 8 / Q);
+    for (int q = 0; q < Q; ++q) unpack16<T>(raw[q], reinterpret_cast<float *>(b.v) + q * 8 / Q);
     return b;
   }
-  static __device__ __forceinline__ void store(T *p, const Block8 &b) {
+  // block number `block` of a stage of the ring, whose first vector of this thread is `at`
+  template <int PIECE>
+  static __device__ __forceinline__ Block8 ring(const uint8_t *at, int block) {
+    uint4 raw[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
-      reinterpret_cast<uint4 *>(p)[q] = pack16<T>(reinterpret_cast<const float *>(b.v) + q * 8 / Q);
+      raw[q] = *reinterpret_cast<const uint4 *>(at + (block * Q + q) * PIECE);
+    return unpack(raw);
+  }
+  template <int PIECE>
+  static __device__ __forceinline__ void copy(uint8_t *at, int block, const char *from) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      copy16_async(reinterpret_cast<uint4 *>(at + (block * Q + q) * PIECE), from + q * 16);
+  }
+  static __device__ __forceinline__ void store(char *to, const Block8 &b) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      reinterpret_cast<uint4 *>(to)[q] = pack16<T>(reinterpret_cast<const float *>(b.v) + q * 8 / Q);
   }
   // a vector of parameters, or `other` where there is none
   static __device__ __forceinline__ Block8 param(const T *v, int col, float other) {
-    return v ? load(reinterpret_cast<const uint4 *>(v + col), 1) : fill8(other);
+    if (v == nullptr) return fill8(other);
+    uint4 raw[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) raw[q] = reinterpret_cast<const uint4 *>(v + col)[q];
+    return unpack(raw);
   }
 };
 

@@ -8,6 +8,12 @@
 
 namespace moe {
 
+// A value that is the same in all lanes (every lane calls), so that the compiler
+// knows it and computes what follows from it once per warp.
+__device__ __forceinline__ uint32_t same_in_warp(uint32_t v) {
+  return __reduce_or_sync(0xffffffffu, v);
+}
+
 struct RngState {
   uint64_t seed, offset;
 };
@@ -16,9 +22,7 @@ struct RngState {
 // it alone, the rounds' keys, then takes the uniform datapath and its registers.
 // (16384 x 7168 bf16 dropout 88 us without, 82 so.)
 __device__ __forceinline__ uint64_t same_in_warp(uint64_t v) {
-  const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)v);
-  const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(v >> 32));
-  return (uint64_t)hi << 32 | lo;
+  return (uint64_t)same_in_warp((uint32_t)(v >> 32)) << 32 | same_in_warp((uint32_t)v);
 }
 // (nullptr: nothing is dropped)
 __device__ __forceinline__ RngState load_state(const RngState *p) {
