@@ -26,59 +26,58 @@ struct Bwd {
 };
 
 
+// A load that stays where it is written, among the copies that it follows: a row ahead
+// of its use (moved down to the use by the compiler, its latency was exposed in
+// every row: 378 us for 301 at 16384 x 7168 bf16).
+__device__ __forceinline__ float load_early(const float *p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // The statistics of a row as the forward left them: the post norm's mean and 1 /
 // deviation, then the pre norm's (MEANS: the means are read).
 template <typename T, bool MEANS = true>
 __device__ __forceinline__ float4 stats_of(const Bwd<T> &a, int64_t row) {
   float4 v = make_float4(0.f, 1.f, 0.f, 1.f);
   if (a.c.post != MOE_NORM_NONE) {
-    if (MEANS) v.x = a.stats[row];
-    v.y = a.stats[a.c.rows + row];
+    if (MEANS) v.x = load_early(a.stats + row);
+    v.y = load_early(a.stats + a.c.rows + row);
   }
   if (a.dy) {
-    if (MEANS) v.z = a.stats[2 * a.c.rows + row];
-    v.w = a.stats[3 * a.c.rows + row];
+    if (MEANS) v.z = load_early(a.stats + 2 * a.c.rows + row);
+    v.w = load_early(a.stats + 3 * a.c.rows + row);
   }
   return v;
 }
 
-// A column sum's partial row of this CTA: put(to) writes a group's sums to to[column];
-// the groups meet in shared memory (the ring's, which is read by then).
-template <typename T, typename Put>
-__device__ __forceinline__ void store_columns(const Bwd<T> &a, float *cols, int width, int group,
-                                              int groups, int which, Put &&put) {
-  float *part = a.parts + ((int64_t)blockIdx.x * J_SUMS + which) * a.c.d;
-  if (groups == 1) {
-    put(part);
-    return;
-  }
-  __syncthreads();
-  put(cols + group * width);
-  __syncthreads();
-  for (int col = threadIdx.x; col < a.c.d; col += blockDim.x) {
-    float t = 0.f;
-    for (int g = 0; g < groups; ++g) t += cols[g * width + col];
-    part[col] = t;
-  }
-}
+// What an iteration moves on by: rows, and bytes of each tensor.
+struct BwdSteps {
+  int64_t rows, dr, dy, r, b, dx, db;
+};
 
-// Rows of whole vectors, as the forward's kernel takes them.  With rc = r - mean2, bc = b
-// - mean1 (the rows themselves without a layer norm, which CENTRED says there is):
+// As the forward's kernel.  With rc = r - mean2, bc = b - mean1 (the rows themselves
+// without a layer norm, which CENTRED says there is):
 //   g = dr + rstd2 dy gamma2 + c2 rc + e2,   c2 = -rstd2^2 mean(w rh),  e2 = -rstd2 mean(w),
 //   h = D(g) rstd1 gate gamma1,   db = h + c1 bc + e1  likewise,
 // so that neither rh nor bh is formed for itself.
-template <typename T, int NB, bool WARP, bool DROP, bool CENTRED>
-__global__ void __launch_bounds__(512, 1)
-join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, int stages) {
-  extern __shared__ __align__(16) uint4 dyn[];   // [stage][block][dr, dy, r, b][vector][thread]
+// One row at a time: the column sums take the registers that two would need.  gate
+// gamma1 lies in shared memory, with a layer norm the sums of u and dy too: with a few
+// values spilled instead, a row waits for the slowest warp's (378 us for 301 at 16384 x
+// 7168 bf16).
+template <typename T, int NB, bool DROP, bool CENTRED, bool ODD>
+__global__ void __launch_bounds__(J_THREADS, 1)
+join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ BwdSteps by, int tpr,
+                     int groups, int stages) {
+  extern __shared__ __align__(16) uint8_t dyn[];   // [stage][block][dr, dy, r, b], own values
   __shared__ float2 buf[2][32];
-  using V = Vec8<T>;
-  constexpr int PIECE = V8_PIECE, STAGE = NB * 4 * V::Q * PIECE;
+  using B = Blocks<T, J_THREADS, ODD>;
+  using Own = Own8<J_THREADS>;
   enum { DR, DY, RR, BB };
+  constexpr int STAGE = NB * 4 * B::BYTES, SIZE = (int)sizeof(T);
   const moe_join_config &c = a.c;
   const int d = c.d, warps = tpr >> 5, warp = threadIdx.x >> 5;
-  const int group = WARP ? warp : warp / warps, tid = threadIdx.x - group * tpr;
-  const int first_warp = group * warps;
+  const int group = warp / warps, tid = threadIdx.x - group * tpr, first_warp = group * warps;
   const bool has_dr = a.dr != nullptr, has_dy = a.dy != nullptr, has_b = a.has_b;
   const bool norm1 = c.post != MOE_NORM_NONE;
   const bool layer1 = CENTRED && c.post == MOE_NORM_LAYER, layer2 = CENTRED && c.pre == MOE_NORM_LAYER;
@@ -87,32 +86,46 @@ join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, 
   const uint32_t cut = (uint32_t)a.threshold << 16;
   int turn = 0;
   pdl_launch_dependents();   // (the column sums wait for this grid to end)
-  const int apart = tpr * 8 * (int)sizeof(T);
-  bool on[NB];
-  // what D's kept elements and dy are multiplied by; the column sums of u bh, dy rh, u
-  // and dy, those of u without dropout's factor
-  Block8 p1[NB], p2[NB], sum_a[NB], sum_c[NB], sum_b[CENTRED ? NB : 1], sum_e[CENTRED ? NB : 1];
+  const int apart = tpr * 8 * SIZE;
+  bool active[NB];
+  int valid[NB], left[NB];
+  // what dy is multiplied by; the column sums of u bh and dy rh, the former without
+  // dropout's factor.  In shared memory: what D's kept elements are multiplied by,
+  // and the sums of u (without the factor) and dy
+  Block8 p2[NB], sum_a[NB], sum_c[NB];
+  uint8_t *const own = dyn + stages * STAGE;
+  auto p1 = [&](int n) { return Own(own + n * Own::BYTES); };
+  auto sum_b = [&](int n) { return Own(own + (NB + n) * Own::BYTES); };
+  auto sum_e = [&](int n) { return Own(own + (2 * NB + n) * Own::BYTES); };
+  auto grow = [](const Own &sum, const Block8 &by) {
+    Block8 s = sum.get();
+#pragma unroll
+    for (int h = 0; h < 4; ++h) s.v[h] = add2(s.v[h], by.v[h]);
+    sum.set(s);
+  };
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     const int col = (tid + n * tpr) * 8;
-    on[n] = col < d;
-    p1[n] = p2[n] = sum_a[n] = sum_c[n] = fill8(0.f);
-    if (CENTRED) sum_b[n] = sum_e[n] = fill8(0.f);
-    if (!on[n]) continue;
-    p1[n] = V::param(a.gate, col, 1.f);
-    p2[n] = V::param(a.pre_gamma, col, 1.f);
-    const Block8 g = V::param(a.post_gamma, col, 1.f);
+    left[n] = (d - col) * SIZE;
+    valid[n] = min(max(d - col, 0), 8);
+    active[n] = ODD ? col - (int)(threadIdx.x & 31) * 8 < d : col < d;
+    sum_a[n] = sum_c[n] = fill8(0.f);
+    p2[n] = param8(a.pre_gamma, col, valid[n], 1.f);
+    Block8 p = param8(a.gate, col, valid[n], 1.f);
+    const Block8 g = param8(a.post_gamma, col, valid[n], 1.f);
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-      p1[n].v[h] = mul2(p1[n].v[h], g.v[h]);
-      if (DROP) p1[n].v[h] = mul2(p1[n].v[h], both(a.factor));
+      p.v[h] = mul2(p.v[h], g.v[h]);
+      if (DROP) p.v[h] = mul2(p.v[h], both(a.factor));
+    }
+    p1(n).set(p);
+    if (CENTRED) {
+      sum_b(n).set(fill8(0.f));
+      sum_e(n).set(fill8(0.f));
     }
   }
-  const int64_t step = (int64_t)gridDim.x * groups;
   int64_t row = (int64_t)blockIdx.x * groups + group, ahead = row;
-  uint8_t *const mine = reinterpret_cast<uint8_t *>(dyn) + threadIdx.x * 16;
-  uint8_t *const ring_end = mine + stages * STAGE;
-  auto bytes = [](int64_t elements) { return elements * (int64_t)sizeof(T); };
+  uint8_t *const mine = dyn + B::place(), *const ring_end = mine + stages * STAGE;
   auto start = [&](const T *p, int64_t ld) {
     return reinterpret_cast<const char *>(p + row * ld + tid * 8);
   };
@@ -120,38 +133,56 @@ join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, 
   const char *r_ahead = start(a.r, c.ldr), *b_ahead = start(a.b, c.ldb);
   char *dx_out = const_cast<char *>(start(a.dx, c.lddx));
   char *db_out = const_cast<char *>(start(a.db, c.lddb));
+  auto at = [&](uint8_t *stage, int n, int t) { return stage + (n * 4 + t) * B::BYTES; };
   auto fill = [&](uint8_t *to) {
     if (ahead < c.rows) {
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        if (!on[n]) continue;
+        if (!active[n]) continue;
         if (has_dy) {
-          V::template copy<PIECE>(to, n * 4 + DY, dy_ahead + n * apart);
-          V::template copy<PIECE>(to, n * 4 + RR, r_ahead + n * apart);
+          B::copy(at(to, n, DY), dy_ahead + n * apart, left[n]);
+          B::copy(at(to, n, RR), r_ahead + n * apart, left[n]);
         }
-        if (has_dr) V::template copy<PIECE>(to, n * 4 + DR, dr_ahead + n * apart);
-        if (has_b) V::template copy<PIECE>(to, n * 4 + BB, b_ahead + n * apart);
+        if (has_dr) B::copy(at(to, n, DR), dr_ahead + n * apart, left[n]);
+        if (has_b) B::copy(at(to, n, BB), b_ahead + n * apart, left[n]);
       }
     }
     copy_commit();
-    ahead += step;
-    dr_ahead += bytes(step * c.lddr);
-    dy_ahead += bytes(step * c.lddy);
-    r_ahead += bytes(step * c.ldr);
-    b_ahead += bytes(step * c.ldb);
+    ahead += by.rows;
+    dr_ahead += by.dr;
+    dy_ahead += by.dy;
+    r_ahead += by.r;
+    b_ahead += by.b;
   };
   for (int i = 0; i < stages - 1; ++i) fill(mine + i * STAGE);
   uint8_t *now = mine, *next = mine + (stages - 1) * STAGE;
   float4 next_stat = make_float4(0.f, 1.f, 0.f, 1.f);
   if (row < c.rows) next_stat = stats_of<T, CENTRED>(a, row);
-  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < c.rows; r0 += step) {
+  for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < c.rows; r0 += by.rows) {
     const bool live = row < c.rows;
-    // (the stage being filled was read by this thread in the iteration before)
+    // (the stage being filled was read in the iteration before, by this thread or its warp)
+    if (ODD) __syncwarp();
     fill(next);
     const float4 stat = next_stat;
-    if (row + step < c.rows) next_stat = stats_of<T, CENTRED>(a, row + step);
+    if (row + by.rows < c.rows) next_stat = stats_of<T, CENTRED>(a, row + by.rows);
     copies_wait(stages - 1);
-    auto get = [&](int n, int t) { return V::template ring<PIECE>(now, n * 4 + t); };
+    if (ODD) {
+      __syncwarp();
+      auto head = [&](const T *p, int64_t ld) {
+        return (int)((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)row * (uint32_t)ld * SIZE) & 15;
+      };
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        if (!live || !active[n]) continue;
+        if (has_dy) {
+          B::realign(at(now, n, DY), head(a.dy, c.lddy));
+          B::realign(at(now, n, RR), head(a.r, c.ldr));
+        }
+        if (has_dr) B::realign(at(now, n, DR), head(a.dr, c.lddr));
+        if (has_b) B::realign(at(now, n, BB), head(a.b, c.ldb));
+      }
+    }
+    auto get = [&](int n, int t) { return B::load(at(now, n, t)); };
     auto centred = [&](int n, int t, float mean) {
       Block8 b = get(n, t);
       if (CENTRED) {
@@ -162,10 +193,11 @@ join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, 
     };
     float c2 = 0.f, e2 = 0.f;
     if (has_dy) {
+      // (a column that is not there has gamma 0)
       float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        if (!live || !on[n]) continue;
+        if (!live || !active[n]) continue;
         const Block8 dy = get(n, DY), rc = centred(n, RR, stat.z);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -175,12 +207,11 @@ join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, 
         }
       }
       if (CENTRED) {
-        const float2 t = group_sum2<WARP>(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
+        const float2 t = row_sum2(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
         e2 = layer2 ? -stat.w * t.x * inv_d : 0.f;
         c2 = -stat.w * stat.w * stat.w * t.y * inv_d;
       } else {
-        const float t = group_sum<WARP>(s2.x + s2.y, reinterpret_cast<float (*)[32]>(buf), turn, warps);
-        c2 = -stat.w * stat.w * stat.w * t * inv_d;
+        c2 = -stat.w * stat.w * stat.w * row_sum(s2.x + s2.y, buf, turn, warps) * inv_d;
       }
     }
     Block8 w[NB];
@@ -188,17 +219,15 @@ join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, 
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       w[n] = fill8(0.f);
-      if (!live || !on[n]) continue;
+      if (!live || !active[n]) continue;
       Block8 g = has_dr ? get(n, DR) : fill8(0.f);
       if (has_dy) {
         const Block8 rc = centred(n, RR, stat.z);
         Block8 dy = get(n, DY);
+        if (CENTRED) grow(sum_e(n), dy);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          if (CENTRED) {
-            sum_e[n].v[h] = add2(sum_e[n].v[h], dy.v[h]);
-            g.v[h] = add2(g.v[h], both(e2));
-          }
+          if (CENTRED) g.v[h] = add2(g.v[h], both(e2));
           dy.v[h] = mul2(dy.v[h], both(stat.w));
           sum_c[n].v[h] = fma2(dy.v[h], rc.v[h], sum_c[n].v[h]);
           g.v[h] = fma2(dy.v[h], p2[n].v[h], fma2(rc.v[h], both(c2), g.v[h]));
@@ -208,280 +237,88 @@ join_backward_vec_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, 
         Block8 t;
 #pragma unroll
         for (int h = 0; h < 4; ++h) t.v[h] = mul2(both(c.scale), g.v[h]);
-        V::store(dx_out + n * apart, t);
+        B::store(at(now, n, DR), dx_out + n * apart, left[n], t);
       }
       if (DROP) drop8(g, dropout_bits(st, tid + n * tpr, (uint32_t)row), cut);
-      if (CENTRED) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) sum_b[n].v[h] = add2(sum_b[n].v[h], g.v[h]);
-      }
+      if (CENTRED) grow(sum_b(n), g);
       if (norm1) {
 #pragma unroll
         for (int h = 0; h < 4; ++h) g.v[h] = mul2(g.v[h], both(stat.y));
       }
+      const Block8 p = p1(n).get();
+#pragma unroll
+      for (int h = 0; h < 4; ++h) w[n].v[h] = mul2(g.v[h], p.v[h]);
       if (has_b) {
         const Block8 bc = centred(n, BB, stat.x);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           sum_a[n].v[h] = fma2(g.v[h], bc.v[h], sum_a[n].v[h]);
-          w[n].v[h] = mul2(g.v[h], p1[n].v[h]);
           if (CENTRED) s1 = add2(s1, w[n].v[h]);
           s2 = fma2(w[n].v[h], bc.v[h], s2);
         }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) w[n].v[h] = mul2(g.v[h], p1[n].v[h]);
       }
     }
     if (a.db) {
       // (w is rstd1 times the gradient of the normed row)
       float c1 = 0.f, e1 = 0.f;
       if (norm1 && CENTRED) {
-        const float2 t = group_sum2<WARP>(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
+        const float2 t = row_sum2(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
         e1 = layer1 ? -t.x * inv_d : 0.f;
         c1 = -stat.y * stat.y * t.y * inv_d;
       } else if (norm1) {
-        const float t = group_sum<WARP>(s2.x + s2.y, reinterpret_cast<float (*)[32]>(buf), turn, warps);
-        c1 = -stat.y * stat.y * t * inv_d;
+        c1 = -stat.y * stat.y * row_sum(s2.x + s2.y, buf, turn, warps) * inv_d;
       }
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        if (!live || !on[n]) continue;
+        if (!live || !active[n]) continue;
         if (norm1) {
           const Block8 bc = centred(n, BB, stat.x);
 #pragma unroll
           for (int h = 0; h < 4; ++h)
             w[n].v[h] = fma2(bc.v[h], both(c1), CENTRED ? add2(w[n].v[h], both(e1)) : w[n].v[h]);
         }
-        V::store(db_out + n * apart, w[n]);
+        B::store(at(now, n, DY), db_out + n * apart, left[n], w[n]);
       }
     }
     next = now;
     now = now + STAGE == ring_end ? mine : now + STAGE;
-    row += step;
-    dx_out += bytes(step * c.lddx);
-    db_out += bytes(step * c.lddb);
+    row += by.rows;
+    dx_out += by.dx;
+    db_out += by.db;
   }
-  copy_wait<0>();   // (none is in flight: the ones past the last row were empty)
+  // each group's sums, and where there are several their sum through shared memory
+  // (the ring's, now read; no copy is in flight: the ones past the last row were
+  // empty)
+  copy_wait<0>();
+  float *const cols = reinterpret_cast<float *>(dyn);
+  const int width = tpr * 8 * NB;
 #pragma unroll
   for (int which = 0; which < J_SUMS; ++which) {
     if (!(a.sums >> which & 1) || (!CENTRED && (which & 1))) continue;
     const float factor = DROP && which < 2 ? a.factor : 1.f;
-    store_columns(a, reinterpret_cast<float *>(dyn), tpr * 8 * NB, group, groups, which,
-                  [&](float *to) {
+    float *part = a.parts + ((int64_t)blockIdx.x * J_SUMS + which) * d;
+    float *to = groups == 1 ? part : cols + group * width;
+    if (groups > 1) __syncthreads();
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        if (!on[n]) continue;
-        const int e = CENTRED ? n : 0;
-        const Block8 &s = which == 0 ? sum_a[n] : which == 1 ? sum_b[e] : which == 2 ? sum_c[n] : sum_e[e];
+    for (int n = 0; n < NB; ++n) {
+      const Block8 s = which == 0 ? sum_a[n] : which == 1 ? sum_b(n).get()
+                       : which == 2 ? sum_c[n] : sum_e(n).get();
+      const float *f = reinterpret_cast<const float *>(s.v);
 #pragma unroll
-        for (int h = 0; h < 4; h += 2)
-          *reinterpret_cast<float4 *>(to + (tid + n * tpr) * 8 + 2 * h) =
-              make_float4(s.v[h].x * factor, s.v[h].y * factor, s.v[h + 1].x * factor,
-                          s.v[h + 1].y * factor);
-      }
-    });
+      for (int i = 0; i < 8; ++i)
+        if (i < valid[n]) to[(tid + n * tpr) * 8 + i] = f[i] * factor;
+    }
+    if (groups == 1) continue;
+    __syncthreads();
+    for (int col = threadIdx.x; col < d; col += blockDim.x) {
+      float t = 0.f;
+      for (int g = 0; g < groups; ++g) t += cols[g * width + col];
+      part[col] = t;
+    }
   }
 }
 
-// Rows that are not whole vectors.
-template <typename T, bool WARP>
-__global__ void __launch_bounds__(J_THREADS, 1)
-join_backward_odd_kernel(const __grid_constant__ Bwd<T> a, int tpr, int groups, int stages, int tensors) {
-  extern __shared__ __align__(16) uint4 dyn[];
-  __shared__ float2 buf[2][32];
-  using C = Chunk<T, 1>;
-  using R = Ring<T>;
-  constexpr int NC = R::NC, H = C::H;
-  const moe_join_config &c = a.c;
-  const int d = c.d, warps = tpr >> 5;
-  const int group = WARP ? threadIdx.x >> 5 : threadIdx.x / tpr;
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x - group * tpr;
-  const int first_warp = group * warps;
-  const R ring{reinterpret_cast<uint8_t *>(dyn), tid, tpr, group, groups, tensors, d,
-               slot_bytes(d, sizeof(T))};
-  uint8_t *space = reinterpret_cast<uint8_t *>(dyn) +
-                   (int64_t)stages * groups * tensors * ring.slot + (int64_t)group * 2 * mask_bytes(d);
-  // where the tensors lie in a stage of the ring
-  const bool has_dr = a.dr != nullptr, has_dy = a.dy != nullptr, has_b = a.has_b;
-  const int at_dr = 0, at_b = has_dr, at_dy = at_b + has_b, at_r = at_dy + 1;
-  const float inv_d = 1.f / (float)d;
-  const bool dropping = a.threshold != 0;
-  const RngState st = load_state(dropping ? a.rng : nullptr);
-  int turn = 0, stage = 0, parity = 0;
-  pdl_launch_dependents();   // (the column sums wait for this grid to end)
-  const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups;
-  const int64_t last = c.rows - 1;
-  auto fill = [&](int64_t row, int to) {
-    if (row < c.rows) {
-      if (has_dy) {
-        ring.copy(to, at_dy, a.dy + row * c.lddy, a.dy + last * c.lddy + d);
-        ring.copy(to, at_r, a.r + row * c.ldr, a.r + last * c.ldr + d);
-      }
-      if (has_dr) ring.copy(to, at_dr, a.dr + row * c.lddr, a.dr + last * c.lddr + d);
-      if (has_b) ring.copy(to, at_b, a.b + row * c.ldb, a.b + last * c.ldb + d);
-    }
-    copy_commit();
-  };
-  // sums of u bh and dy rh, and of u and dy
-  float2 sum_a[NC][H], sum_c[NC][H], sum_b[NC][H], sum_e[NC][H];
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      sum_a[i][h] = sum_b[i][h] = sum_c[i][h] = sum_e[i][h] = both(0.f);
-    }
-  }
-  for (int i = 0; i < stages - 1; ++i) fill(first + group + i * step, i);
-  for (int64_t r0 = first; r0 < c.rows; r0 += step) {
-    const int64_t row = r0 + group;
-    const bool live = row < c.rows;
-    const int64_t ahead = row + (stages - 1) * step;
-    const int next = stage == 0 ? stages - 1 : stage - 1;
-    float4 stat = make_float4(0.f, 1.f, 0.f, 1.f);
-    if (live) stat = stats_of(a, row);
-    uint8_t *masks = space + parity * mask_bytes(d);
-    if (dropping) make_masks(ring, st, (uint32_t)row, a.threshold, masks);
-    parity ^= 1;
-    if (stages == 1) {
-      group_barrier<WARP>();
-      fill(ahead, next);
-      copy_wait<0>();
-      group_barrier<WARP>();
-    } else {
-      copies_wait(stages - 2);
-      group_barrier<WARP>();
-      fill(ahead, next);
-    }
-    const T *b_row = a.b + row * c.ldb, *dr_row = a.dr + row * c.lddr;
-    const T *dy_row = a.dy + row * c.lddy, *r_row = a.r + row * c.ldr;
-    auto there = [&](int i) { return live && ring.col(i) < d; };
-    // dy and rh of chunk i
-    auto pre = [&](int i, float2 (&dy)[H], float2 (&rh)[H]) {
-      ring.get(stage, i, at_dy, dy_row, dy);
-      ring.get(stage, i, at_r, r_row, rh);
-#pragma unroll
-      for (int h = 0; h < H; ++h) rh[h] = mul2(add2(rh[h], both(-stat.z)), both(stat.w));
-    };
-    auto post = [&](int i, float2 (&bh)[H]) {
-      ring.get(stage, i, at_b, b_row, bh);
-      if (c.post != MOE_NORM_NONE) {
-#pragma unroll
-        for (int h = 0; h < H; ++h) bh[h] = mul2(add2(bh[h], both(-stat.x)), both(stat.y));
-      }
-    };
-    float2 m = both(0.f);
-    if (has_dy) {
-      float2 s1 = both(0.f), s2 = both(0.f);
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        if (!there(i)) continue;
-        float2 dy[H], rh[H], q[H];
-        pre(i, dy, rh);
-        params(ring, a.pre_gamma, i, 1.f, q);
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          // (an element that is not there has dy = 0)
-          sum_c[i][h] = fma2(dy[h], rh[h], sum_c[i][h]);
-          sum_e[i][h] = add2(sum_e[i][h], dy[h]);
-          const float2 w = mul2(dy[h], q[h]);
-          s1 = add2(s1, w);
-          s2 = fma2(w, rh[h], s2);
-        }
-      }
-      m = group_sum2<WARP>(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
-      m = make_float2(c.pre == MOE_NORM_LAYER ? -m.x * inv_d : 0.f, -m.y * inv_d);
-    }
-    float2 w[NC][H], s1 = both(0.f), s2 = both(0.f);
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      if (!there(i)) {
-#pragma unroll
-        for (int h = 0; h < H; ++h) w[i][h] = both(0.f);
-        continue;
-      }
-      float2 g[H], q[H], t[H];
-#pragma unroll
-      for (int h = 0; h < H; ++h) g[h] = both(0.f);
-      if (has_dr) ring.get(stage, i, at_dr, dr_row, g);
-      if (has_dy) {
-        float2 dy[H], rh[H];
-        pre(i, dy, rh);
-        params(ring, a.pre_gamma, i, 1.f, q);
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-          g[h] = fma2(both(stat.w),
-                      fma2(rh[h], both(m.y), fma2(dy[h], q[h], both(m.x))),
-                      g[h]);
-        C::mask(ring.col(i), tpr, d, g);
-      }
-      if (a.dx) {
-#pragma unroll
-        for (int h = 0; h < H; ++h) t[h] = mul2(both(c.scale), g[h]);
-        C::store(a.dx + row * c.lddx, ring.col(i), tpr, d, t);
-      }
-      if (dropping) g[0] = drop_pair(ring, masks, i, g[0], a.factor);
-      if (has_b) post(i, t);
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        if (has_b) sum_a[i][h] = fma2(g[h], t[h], sum_a[i][h]);
-        sum_b[i][h] = add2(sum_b[i][h], g[h]);
-      }
-      if (a.gate) {
-        params(ring, a.gate, i, 1.f, q);
-#pragma unroll
-        for (int h = 0; h < H; ++h) g[h] = mul2(g[h], q[h]);
-      }
-      if (c.post != MOE_NORM_NONE) {
-        params(ring, a.post_gamma, i, 1.f, q);
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          g[h] = mul2(g[h], q[h]);
-          s1 = add2(s1, g[h]);
-          s2 = fma2(g[h], t[h], s2);
-        }
-      } else if (a.db) {
-        C::store(a.db + row * c.lddb, ring.col(i), tpr, d, g);
-      }
-#pragma unroll
-      for (int h = 0; h < H; ++h) w[i][h] = g[h];
-    }
-    if (c.post != MOE_NORM_NONE && a.db) {
-      float2 q = group_sum2<WARP>(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
-      q = make_float2(c.post == MOE_NORM_LAYER ? -q.x * inv_d : 0.f, -q.y * inv_d);
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        if (!there(i)) continue;
-        float2 t[H];
-        post(i, t);
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-          t[h] = mul2(both(stat.y),
-                      fma2(t[h], both(q.y), add2(w[i][h], both(q.x))));
-        C::store(a.db + row * c.lddb, ring.col(i), tpr, d, t);
-      }
-    }
-    stage = stage + 1 == stages ? 0 : stage + 1;
-  }
-  copy_wait<0>();   // (none is in flight: the ones past the last row were empty)
-  float *cols = reinterpret_cast<float *>(dyn);
-  const int width = tpr * 16;
-#pragma unroll
-  for (int which = 0; which < J_SUMS; ++which) {
-    if (!(a.sums >> which & 1)) continue;
-    store_columns(a, cols, width, group, groups, which, [&](float *to) {
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        if (ring.col(i) >= d) continue;
-        const float2 v = which == 0 ? sum_a[i][0] : which == 1 ? sum_b[i][0]
-                         : which == 2 ? sum_c[i][0] : sum_e[i][0];
-        to[ring.col(i)] = v.x;
-        if (ring.col(i) + tpr < d) to[ring.col(i) + tpr] = v.y;
-      }
-    });
-  }
-}
-
+// ------------------------------------------------- rows of any width, in passes
 // The stream's gradient R at element i, from the pre norm's means m.
 template <typename T>
 __device__ __forceinline__ float stream_grad(const Bwd<T> &a, int64_t row, int i, float4 st,
@@ -635,76 +472,44 @@ __global__ void __launch_bounds__(1024) join_finish_kernel(const __grid_constant
   if (a.g.pre_beta) a.g.pre_beta[out] = total[3];
 }
 
-// Groups of tpr threads in a CTA of up to 512 threads, fewer where there are SMs to
-// spare (one CTA per SM leaves a partial row of each column sum), and the stages
-// of a ring whose stage takes `fixed` bytes and `each` per group.  The column sums
-// (`columns` bytes of a group) take the ring's place at the end.
-struct BwdPlan {
-  int groups, stages, parts;
-  size_t smem;
-};
-template <typename T>
-BwdPlan plan(const Bwd<T> &a, int tpr, size_t fixed, size_t each, size_t masks, size_t columns) {
-  BwdPlan p;
-  p.groups = J_THREADS / tpr;
-  while (p.groups > 1 && a.c.rows <= (int64_t)(p.groups / 2) * J_PARTS) p.groups /= 2;
-  const size_t stage = fixed + p.groups * each;
-  p.stages = 3;
-  while (p.stages > 1 && p.stages * stage + p.groups * masks > J_SMEM) --p.stages;
-  p.smem = p.stages * stage + p.groups * masks;
-  if (p.groups > 1 && p.smem < p.groups * columns) p.smem = p.groups * columns;
-  p.parts = (int)grid_of(a.c.rows, p.groups, J_PARTS);
-  return p;
-}
-
-template <typename K>
-cudaError_t allow_smem(K kernel, bool &set) {
-  if (set) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, J_SMEM);
-  set = e == cudaSuccess;
-  return e;
-}
-
-template <typename T, bool WARP>
-cudaError_t run_odd(const Bwd<T> &a, int tpr, int &parts, cudaStream_t s) {
-  auto kernel = join_backward_odd_kernel<T, WARP>;
-  const int tensors = (a.dr ? 1 : 0) + (a.has_b ? 1 : 0) + (a.dy ? 2 : 0);
-  const BwdPlan p = plan(a, tpr, 0, (size_t)tensors * slot_bytes(a.c.d, sizeof(T)),
-                         2 * mask_bytes(a.c.d), (size_t)tpr * 16 * 4);
+// (one CTA per SM at most: each leaves a partial row of the column sums, which meet in
+// the ring's place)
+template <typename T, int NB, bool DROP, bool CENTRED, bool ODD>
+cudaError_t run(const Bwd<T> &a, int &parts, cudaStream_t s) {
+  auto kernel = join_backward_kernel<T, NB, DROP, CENTRED, ODD>;
+  const moe_join_config &c = a.c;
+  const int tpr = threads_of(c.d, NB), groups = groups_of(c.rows, 1, tpr, J_THREADS, J_PARTS);
+  const size_t stage = (size_t)NB * 4 * Blocks<T, J_THREADS, ODD>::BYTES;
+  const size_t own = (size_t)NB * (CENTRED ? 3 : 1) * Own8<J_THREADS>::BYTES;
+  const int stages = stages_of(stage, own);
+  static_assert(NB * 4 * Blocks<T, J_THREADS, ODD>::BYTES >= J_THREADS * NB * 32,
+                "the groups' column sums fit a stage");
   static bool set = false;
-  const cudaError_t e = allow_smem(kernel, set);
-  if (e != cudaSuccess) return e;
-  parts = p.parts;
-  kernel<<<parts, tpr * p.groups, p.smem, s>>>(a, tpr, p.groups, p.stages, tensors);
+  if (!set) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, J_SMEM);
+    if (e != cudaSuccess) return e;
+    set = true;
+  }
+  parts = (int)grid_of(c.rows, groups, J_PARTS);
+  const int64_t rows = (int64_t)parts * groups, bytes = rows * sizeof(T);
+  const BwdSteps by{rows,          bytes * c.lddr, bytes * c.lddy, bytes * c.ldr,
+                    bytes * c.ldb, bytes * c.lddx, bytes * c.lddb};
+  kernel<<<parts, tpr * groups, stages * stage + own, s>>>(a, by, tpr, groups, stages);
   return cudaGetLastError();
 }
-
-template <typename T, int NB, bool WARP, bool DROP, bool CENTRED>
-cudaError_t run_vec(const Bwd<T> &a, int tpr, int &parts, cudaStream_t s) {
-  auto kernel = join_backward_vec_kernel<T, NB, WARP, DROP, CENTRED>;
-  const BwdPlan p = plan(a, tpr, (size_t)NB * 4 * Vec8<T>::Q * V8_PIECE, 0, 0, (size_t)tpr * NB * 32);
-  static bool set = false;
-  const cudaError_t e = allow_smem(kernel, set);
-  if (e != cudaSuccess) return e;
-  parts = p.parts;
-  kernel<<<parts, tpr * p.groups, p.smem, s>>>(a, tpr, p.groups, p.stages);
-  return cudaGetLastError();
-}
-template <typename T, int NB, bool WARP>
-cudaError_t vec_kinds(const Bwd<T> &a, int tpr, int &parts, cudaStream_t s) {
+template <typename T, int NB, bool ODD>
+cudaError_t kinds(const Bwd<T> &a, int &parts, cudaStream_t s) {
   const bool centred = a.c.post == MOE_NORM_LAYER || a.c.pre == MOE_NORM_LAYER;
   if (a.threshold)
-    return centred ? run_vec<T, NB, WARP, true, true>(a, tpr, parts, s)
-                   : run_vec<T, NB, WARP, true, false>(a, tpr, parts, s);
-  return centred ? run_vec<T, NB, WARP, false, true>(a, tpr, parts, s)
-                 : run_vec<T, NB, WARP, false, false>(a, tpr, parts, s);
+    return centred ? run<T, NB, true, true, ODD>(a, parts, s) : run<T, NB, true, false, ODD>(a, parts, s);
+  return centred ? run<T, NB, false, true, ODD>(a, parts, s) : run<T, NB, false, false, ODD>(a, parts, s);
 }
-template <typename T, int NB>
-cudaError_t vec_rows(const Bwd<T> &a, int &parts, cudaStream_t s) {
-  const int tpr = ((a.c.d + 8 * NB - 1) / (8 * NB) + 31) / 32 * 32;
-  return tpr == 32 ? vec_kinds<T, NB, true>(a, tpr, parts, s)
-                   : vec_kinds<T, NB, false>(a, tpr, parts, s);
+// fp32: one block per thread where that is enough, so that several rows fit the ring.
+template <typename T, bool ODD>
+cudaError_t backward_ring(const Bwd<T> &a, int &parts, cudaStream_t s) {
+  return sizeof(T) == 4 && a.c.d <= J_MAX_D / 2 ? kinds<T, sizeof(T) == 4 ? 1 : 2, ODD>(a, parts, s)
+                                                : kinds<T, 2, ODD>(a, parts, s);
 }
 
 template <typename T>
@@ -733,14 +538,10 @@ cudaError_t backward(const moe_join_config &c, int threshold, const JoinBackward
            (g.pre_gamma ? 4 : 0) | (g.pre_beta ? 8 : 0);
   a.parts = (float *)scratch;
   const bool vectors = whole_vectors<T>(c, {c.ldb, c.ldr, c.lddr, c.lddy, c.lddx, c.lddb});
-  const int tpr = threads_of(c.d, 16);
   int parts = 0;
   cudaError_t e;
-  if (tpr && vectors) {
-    // (fp32: one block per thread where that is enough, so that three rows fit the ring)
-    e = sizeof(T) == 4 && c.d <= 4096 ? vec_rows<T, 1>(a, parts, s) : vec_rows<T, 2>(a, parts, s);
-  } else if (tpr) {
-    e = tpr == 32 ? run_odd<T, true>(a, tpr, parts, s) : run_odd<T, false>(a, tpr, parts, s);
+  if (c.d <= J_MAX_D) {
+    e = vectors ? backward_ring<T, sizeof(T) == 4>(a, parts, s) : backward_ring<T, true>(a, parts, s);
   } else {
     parts = (int)grid_of(c.rows, 8, 64);
     a.means = (float2 *)((char *)scratch + (size_t)J_PARTS * J_SUMS * c.d * 4);
