@@ -1,20 +1,25 @@
 // Softmax cross entropy of a linear layer over a vocabulary, and its gradient
 // (moe.h has the formulas), in pieces of the vocabulary.
 //
-// Only the tokens that count take part: a first launch packs their rows of x,
-// their targets and (for the gradient) lse and dloss, so that the products run
-// over them alone and nothing a left out row holds, a NaN say, meets a sum.
+// Only the tokens that count take part in the gradient: a first launch packs their
+// rows of x, their targets, lse and dloss, so that the products run over them
+// alone and nothing a left out row holds, a NaN say, meets a sum.  The forward,
+// where a token's sums are its own, packs where that saves tiles of the product
+// (more than 256 tokens on the tensor cores).
 //
-// On the CUDA cores (fp32, and small bf16 problems) a piece's logits lie in the
-// workspace in fp32 with the token contiguous, lT [piece][pitch]: then dx = dl W
-// is a sum over lT's rows (GradProduct: cut into runs where the tiles are few)
-// and dW = dl^T x a product of its rows (RowsProduct).
+// Forward: the product reduces its logits as it forms them, to a maximum and a
+// sum of exponentials per token and tile, which a second launch joins.  No logits
+// are stored.
 //
-// On the tensor cores (other bf16 problems, loss_pair.cu) the forward reduces the
-// logits as it forms them.  The gradient forms a piece's logits again and
-// stores their gradient in bf16, dl [n][pitch], which two products then read: dW
-// (launch_gemm_grad, rounded once from the whole sum over the tokens) and dx,
+// Gradient, on the tensor cores (loss_pair.cu): a piece's logits are formed again
+// and their gradient stored in bf16, dl [n][pitch], which two products then read:
+// dW (launch_gemm_grad, rounded once from the whole sum over the tokens) and dx,
 // which adds up over the pieces in fp32 and is rounded once at the end.
+//
+// Gradient, on the CUDA cores (fp32, and small bf16 problems): dl of a piece in
+// fp32 with the token contiguous, lT [piece][pitch]: then dx = dl W is a sum over
+// lT's rows (GradProduct: cut into runs where the tiles are few) and dW = dl^T x a
+// product of its rows (RowsProduct).
 #include <math.h>
 
 #include "api.h"
@@ -28,19 +33,22 @@
 namespace moe {
 namespace {
 
-constexpr int L_CHUNK = 256;                           // vocabulary entries of a partial sum
-constexpr int64_t L_PIECE_BYTES = (int64_t)256 << 20;  // of a piece's logits, about
+constexpr int L_UNIT = 256;                            // a piece's entries are a multiple of this
+constexpr int64_t L_PIECE_BYTES = (int64_t)256 << 20;  // of a piece's dl, about
 constexpr int64_t L_PIECE_MAX = 1 << 22;               // entries of a piece
 constexpr int L_MAX_SPLITS = 76;
+constexpr int L_PAIRS = 76, L_WRITING = 46;            // SM pairs that the plan counts on
 
 struct LossLayout {
-  size_t status, range, list, target, lse, dloss, at, x, sums, logits, dx, parts, total;
+  size_t status, range, list, target, lse, dloss, at, x, sums, logits, dx, acc, parts, total;
   bool pair;    // on the tensor cores
+  bool packed;  // the forward packs the tokens that count
   int pitch;    // CUDA cores: tokens, rounded up to whole vectors of fp32
-  int piece;    // vocabulary entries of a piece at most (a multiple of L_CHUNK where there are several)
+  int piece;    // vocabulary entries of a piece of the gradient at most
   int pieces;
-  int width, chunks;   // entries per tile of the forward; partial sums per token
-  int planes;          // dx: its partial sums
+  int width, chunks;   // entries per tile of the forward; partial sums per token at most
+  int planes;          // dx: partial sums of a piece
+  bool beside;         // dW and dx run side by side
 };
 
 int elem_size(const moe_loss_config &c) { return c.dtype == MOE_F32 ? 4 : 2; }
@@ -79,14 +87,31 @@ LossLayout loss_layout(const moe_loss_config &c) {
   LossLayout L{};
   const size_t n = c.n, z = elem_size(c);
   L.pair = c.dtype == MOE_BF16 && !small_loss(c);
+  L.packed = L.pair && c.n > 256;
+  // With one block of tokens the gradient's products are bound by reading W and
+  // writing dW: side by side HBM moves both ways.
+  L.beside = L.pair && c.n <= 256;
   L.pitch = (c.n + 3) / 4 * 4;
-  int64_t fit = L_PIECE_BYTES / ((int64_t)L.pitch * (L.pair ? 2 : 4) + 1) / L_CHUNK * L_CHUNK;
-  if (fit > L_PIECE_MAX) fit = L_PIECE_MAX;
-  L.piece = (int)(fit < L_CHUNK ? L_CHUNK : fit < c.vocab ? fit : c.vocab);
-  L.pieces = (int)(((int64_t)c.vocab + L.piece - 1) / L.piece);
+  // pieces of nearly equal size
+  int64_t fit = L_PIECE_BYTES / ((int64_t)(L.pitch > 0 ? L.pitch : 4) * (L.pair ? 2 : 4));
+  fit = (fit < L_UNIT ? L_UNIT : fit > L_PIECE_MAX ? L_PIECE_MAX : fit) / L_UNIT * L_UNIT;
+  L.pieces = (int)((c.vocab + fit - 1) / fit);
+  L.piece = (c.vocab + L.pieces - 1) / L.pieces;
+  if (L.pieces > 1) L.piece = (L.piece + L_UNIT - 1) / L_UNIT * L_UNIT;
+  L.pieces = (c.vocab + L.piece - 1) / L.piece;
+  const int last = c.vocab - (L.pieces - 1) * L.piece;
   L.width = L.pair ? loss_width(c.n, c.vocab) : 0;
-  L.chunks = L.pair ? loss_chunks(c.vocab, L.width) : (c.vocab + L_CHUNK - 1) / L_CHUNK;
-  L.planes = L.pair ? loss_dx_splits(c.n, c.d, L.piece, L_MAX_SPLITS) : L.pieces;
+  L.chunks = L.pair ? loss_chunks(c.vocab, L.width) : (c.vocab + 31) / 32;
+  if (L.pair) {
+    L.planes = loss_dx_splits(c.n, c.d, L.piece, L_MAX_SPLITS, L.beside ? L_PAIRS - L_WRITING : L_PAIRS);
+  } else {
+    L.planes = 1;
+    for (int entries : {L.piece, last}) {
+      const GradProduct p = dx_product(c, L, entries);
+      const int splits = c.n > 0 ? grad_splits_simt(&p, 1) : 1;
+      if (splits > L.planes) L.planes = splits;
+    }
+  }
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t a = off;
@@ -101,27 +126,20 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.dloss = take((size_t)L.pitch * 4);
   L.at = take(n * 4);
   L.x = take(n * c.d * z);
-  const size_t both = off;
   // what the forward alone and the gradient alone use shares its place
+  const size_t both = off;
   L.sums = take(n * L.chunks * sizeof(float2));
-  if (!L.pair) L.logits = take((size_t)L.piece * L.pitch * 4);
   const size_t forward = off;
-  if (L.pair) {
-    off = both;
-    L.logits = take(n * dl_pitch(L.piece) * 2);
-  }
-  L.dx = take((size_t)L.planes * n * c.d * (L.pair ? 4 : z));
+  off = both;
+  L.logits = take(L.pair ? n * dl_pitch(L.piece) * 2 : (size_t)L.piece * L.pitch * 4);
+  L.dx = take((size_t)L.planes * n * c.d * 4);
+  L.acc = take(!L.pair && L.pieces > 1 ? n * c.d * 4 : 0);
   size_t parts = 0;
-  if (L.pair) {
-    for (int entries : {L.piece, c.vocab - (L.pieces - 1) * L.piece}) {
-      const GradProduct p = dw_product(c, entries);
-      const size_t bytes = grad_scratch(&p, 1);
-      if (bytes > parts) parts = bytes;
-    }
-  } else if (c.n > 0) {
-    const GradProduct p = dx_product(c, L, L.piece);
-    const int splits = grad_splits_simt(&p, 1);
-    if (splits > 1) parts = (size_t)splits * n * c.d * 4;
+  for (int entries : {L.piece, last}) {
+    if (!L.pair) break;
+    const GradProduct p = dw_product(c, entries);
+    const size_t bytes = grad_scratch(&p, 1);
+    if (bytes > parts) parts = bytes;
   }
   L.parts = take(parts);
   L.total = off > forward ? off : forward;
@@ -246,129 +264,99 @@ cudaError_t launch_pack(const moe_loss_config &c, const LossLayout &L, const voi
 }
 
 // ------------------------------------------------------------- softmax sums
-// e^(v - m) where m is a maximum of v: 0 terms of an empty maximum stay 0.
 __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f : m; }
 
-// (maximum, sum of e^(l - maximum)) of one chunk of the vocabulary for 32
-// tokens: eight warps of 32 entries each, then joined.
-__global__ void __launch_bounds__(256)
-loss_chunk_kernel(const float *__restrict__ lt, int pitch, int entries, int v0, int chunks,
-                  const int32_t *__restrict__ range, const int32_t *__restrict__ target,
-                  float *__restrict__ at, float2 *__restrict__ sums, const int *status) {
-  __shared__ float2 s[8][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int j = blockIdx.x * 32 + lane, e0 = blockIdx.y * L_CHUNK + warp * 32;
-  pdl_launch_dependents();
-  pdl_wait();
-  if (status_failed(status)) return;
-  const bool there = j < range[1];
-  float v[32], m = -INFINITY, sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[i] = there && e0 + i < entries ? lt[(int64_t)(e0 + i) * pitch + j] : -INFINITY;
-    m = fmaxf(m, v[i]);
-  }
-  const float shift = shift_of(m);
-#pragma unroll
-  for (int i = 0; i < 32; ++i) sum += expf(v[i] - shift);
-  s[warp][lane] = make_float2(m, sum);
-  if (there) {
-    const int t = target[j] - v0 - e0;
-    if (t >= 0 && t < 32 && e0 + t < entries) at[j] = lt[(int64_t)(e0 + t) * pitch + j];
-  }
-  __syncthreads();
-  if (warp != 0 || !there) return;
-  m = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) m = fmaxf(m, s[w][lane].x);
-  sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) sum += s[w][lane].y * expf(s[w][lane].x - shift_of(m));
-  sums[(int64_t)j * chunks + v0 / L_CHUNK + blockIdx.y] = make_float2(m, sum);
-}
-
-// A warp per counted token joins its chunks.
-__global__ void __launch_bounds__(256)
-loss_finish_kernel(const float2 *__restrict__ sums, int chunks, float z_loss,
-                   const int32_t *__restrict__ range, const int32_t *__restrict__ list,
-                   const float *__restrict__ at, float *__restrict__ loss, float *__restrict__ lse_out,
-                   const int *status) {
-  const int lane = threadIdx.x & 31;
-  const int j = blockIdx.x * 8 + (threadIdx.x >> 5);
-  pdl_wait();
-  if (status_failed(status) || j >= range[1]) return;
-  const float2 *mine = sums + (int64_t)j * chunks;
-  float m = -INFINITY, sum = 0.f;
-  for (int i = lane; i < chunks; i += 32) {
-    const float2 v = mine[i];
-    const float up = fmaxf(m, v.x), shift = shift_of(up);
-    sum = sum * expf(m - shift) + v.y * expf(v.x - shift);
-    m = up;
-  }
-  float top = m;
+// Joins (maximum, sum) pairs over a warp.
+__device__ __forceinline__ float2 join_pairs(float2 v) {
+  float top = v.x;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  sum = warp_sum_xor(sum * expf(m - shift_of(top)));
-  if (lane != 0) return;
-  const float lse = top + logf(sum);
-  const int t = list[j];
-  lse_out[t] = lse;
-  loss[t] = lse - at[j] + z_loss * lse * lse;
+  return make_float2(top, warp_sum_xor(v.y * expf(v.x - shift_of(top))));
 }
 
-// lT <- dl, four tokens per thread; columns of tokens that do not count are zero.
-__global__ void __launch_bounds__(256)
-loss_grad_kernel(float4 *__restrict__ lt, int pitch4, int entries, int v0, float z_loss,
-                 const int32_t *__restrict__ range, const int4 *__restrict__ target,
-                 const float4 *__restrict__ lse, const float4 *__restrict__ dloss,
-                 const int *status) {
-  pdl_launch_dependents();
+struct FinishArgs {
+  const float2 *sums;          // [token][pitch], `chunks` of them
+  int chunks, pitch, n, vocab;
+  float z_loss;
+  const int32_t *range, *list; // packed tokens, else nullptr
+  const int32_t *targets;
+  const float *at;
+  float *loss, *lse;
+  int *status;
+};
+// A token's chunks are joined by a warp, or (WIDE: few tokens) by a CTA.
+template <bool WIDE>
+__global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant__ FinishArgs a) {
+  __shared__ float2 s[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = WIDE ? blockIdx.x : blockIdx.x * 8 + warp;
+  constexpr int STEP = WIDE ? 256 : 32;
   pdl_wait();
-  if (status_failed(status)) return;
-  const int m = range[1];
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)entries * pitch4;
-       i += (int64_t)gridDim.x * 256) {
-    const int e = (int)(i / pitch4), q = (int)(i - (int64_t)e * pitch4);
-    const float4 l = lt[i], ls = lse[q], dl = dloss[q];
-    const int4 t = target[q];
-    auto one = [&](int k, float l1, float lse1, float dloss1, int t1) {
-      if (4 * q + k >= m) return 0.f;
-      const float p = expf(l1 - lse1) * fmaf(2.f * z_loss, lse1, 1.f);
-      return dloss1 * (t1 == v0 + e ? p - 1.f : p);
-    };
-    lt[i] = make_float4(one(0, l.x, ls.x, dl.x, t.x), one(1, l.y, ls.y, dl.y, t.y),
-                        one(2, l.z, ls.z, dl.z, t.z), one(3, l.w, ls.w, dl.w, t.w));
+  // (a packed call's bad targets are reported by the launch before, others here, by
+  // CTAs that exchange nothing with others)
+  if (a.range && status_failed(a.status)) return;
+  const int count = a.range ? a.range[1] : a.n;
+  if (j >= count) return;
+  const float2 *mine = a.sums + (int64_t)j * a.pitch;
+  float2 v = make_float2(-INFINITY, 0.f);
+#pragma unroll 4
+  for (int i = WIDE ? threadIdx.x : lane; i < a.chunks; i += STEP) {
+    const float2 u = mine[i];
+    const float up = fmaxf(v.x, u.x), shift = shift_of(up);
+    v.y = v.y * expf(v.x - shift) + u.y * expf(u.x - shift);
+    v.x = up;
   }
+  v = join_pairs(v);
+  if (WIDE) {
+    if (lane == 0) s[warp] = v;
+    __syncthreads();
+    v = join_pairs(lane < 8 ? s[lane] : make_float2(-INFINITY, 0.f));
+  }
+  if (WIDE ? threadIdx.x != 0 : lane != 0) return;
+  const int t = a.list ? a.list[j] : j, target = a.targets[t];
+  float lse = v.x + logf(v.y), loss = lse - a.at[j] + a.z_loss * lse * lse;
+  if (target < 0 || target >= a.vocab) {
+    if (target >= a.vocab) set_status(a.status, MOE_ERR_BAD_INDEX, t);
+    lse = loss = 0.f;
+  }
+  a.lse[t] = lse;
+  a.loss[t] = loss;
 }
 
-// dx of the counted tokens: the partial sums [planes][n][d] of type TI, added in
-// order.
-template <typename T, typename TI>
+// dx of the counted tokens from the partial sums [planes][n][d], added in order; or
+// (acc_out) what a piece adds to the sum of those before, `acc`.
+template <typename T>
 __global__ void __launch_bounds__(256)
-loss_dx_kernel(const TI *__restrict__ parts, int planes, int n, int vecs,
-               const int32_t *__restrict__ range, const int32_t *__restrict__ list,
+loss_dx_kernel(const float *__restrict__ parts, int planes, const float *acc, float *acc_out, int n,
+               int vecs, const int32_t *__restrict__ range, const int32_t *__restrict__ list,
                T *__restrict__ dx, const int *status) {
-  constexpr int N = Vec16<T>::N, NI = Vec16<TI>::N;
+  constexpr int N = Vec16<T>::N, V = N / 4;
   pdl_wait();
   if (status_failed(status)) return;
-  const int64_t total = (int64_t)range[1] * vecs, plane = (int64_t)n * vecs * (N / NI);
+  const int64_t total = (int64_t)range[1] * vecs, plane = (int64_t)n * vecs * V;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
     const int64_t j = i / vecs;
-    const uint4 *from = reinterpret_cast<const uint4 *>(parts) + i * (N / NI);
-    float v[N], w[NI];
+    const float4 *from = reinterpret_cast<const float4 *>(parts) + i * V;
+    float4 v[V];
 #pragma unroll
-    for (int h = 0; h < N / NI; ++h) unpack16<TI>(from[h], v + h * NI);
+    for (int h = 0; h < V; ++h)
+      v[h] = acc ? reinterpret_cast<const float4 *>(acc)[i * V + h] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int p = 1; p < planes; ++p) {
+    for (int p = 0; p < planes; ++p) {
 #pragma unroll
-      for (int h = 0; h < N / NI; ++h) {
-        unpack16<TI>(from[p * plane + h], w);
-#pragma unroll
-        for (int k = 0; k < NI; ++k) v[h * NI + k] += w[k];
+      for (int h = 0; h < V; ++h) {
+        const float4 w = from[p * plane + h];
+        v[h] = make_float4(v[h].x + w.x, v[h].y + w.y, v[h].z + w.z, v[h].w + w.w);
       }
     }
-    reinterpret_cast<uint4 *>(dx)[(int64_t)list[j] * vecs + (i - j * vecs)] = pack16<T>(v);
+    if (acc_out) {
+#pragma unroll
+      for (int h = 0; h < V; ++h) reinterpret_cast<float4 *>(acc_out)[i * V + h] = v[h];
+    } else {
+      reinterpret_cast<uint4 *>(dx)[(int64_t)list[j] * vecs + (i - j * vecs)] =
+          pack16<T>(reinterpret_cast<const float *>(v));
+    }
   }
 }
 
@@ -377,73 +365,55 @@ unsigned blocks_of(int64_t threads) {
   return (unsigned)(b < 1 ? 1 : b < most ? b : most);
 }
 
-// A piece's logits, in the workspace.
-cudaError_t piece_logits(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
-                         int entries, void *ws, cudaStream_t s) {
-  RowsProduct p{};
-  p.dtype = c.dtype;
-  p.epi = kRowsPlain;
-  p.num_experts = 1;
-  p.rows = entries;
-  p.K = c.d;
-  p.N = c.n;
-  p.A = (const char *)W + (size_t)v0 * c.d * elem_size(c);
-  p.B = at<void>(ws, L.x);
-  p.out = at<void>(ws, L.logits);
-  p.ldo = L.pitch;
-  p.out_f32 = c.dtype == MOE_BF16;
-  return launch_rows_simt(p, at<int>(ws, L.status), s);
-}
-
-template <typename T, typename TI>
-cudaError_t finish_dx(const moe_loss_config &c, const LossLayout &L, void *dx, void *ws,
-                      cudaStream_t s) {
-  const int vecs = c.d / Vec16<T>::N;
-  return launch_pdl(loss_dx_kernel<T, TI>, dim3(blocks_of((int64_t)c.n * vecs)), dim3(256), 0, s,
-                    at<TI>(ws, L.dx), L.planes, c.n, vecs, at<int32_t>(ws, L.range),
-                    at<int32_t>(ws, L.list), (T *)dx, at<int>(ws, L.status));
-}
-
-// The operands that a piece's products on the tensor cores share.
-LossProduct pair_product(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
-                         int entries, void *ws) {
-  LossProduct p{};
-  p.n = c.n;
-  p.d = c.d;
-  p.entries = entries;
-  p.v0 = v0;
-  p.range = at<int32_t>(ws, L.range);
-  p.target = at<int32_t>(ws, L.target);
-  p.x = at<void>(ws, L.x);
-  p.W = (const char *)W + (size_t)v0 * c.d * 2;
-  p.width = L.width;
-  p.chunks = L.chunks;
-  p.sums = at<float2>(ws, L.sums);
-  p.at = at<float>(ws, L.at);
-  p.lse = at<float>(ws, L.lse);
-  p.dloss = at<float>(ws, L.dloss);
-  p.z_loss = c.z_loss;
-  p.dl = at<void>(ws, L.logits);
-  p.pitch = dl_pitch(entries);
-  p.planes = at<float>(ws, L.dx);
-  return p;
-}
-
 #define LOSS_TRY(expr)                       \
   do {                                       \
     const cudaError_t _e = (expr);           \
     if (_e != cudaSuccess) return _e;        \
   } while (0)
 
+template <typename T>
+cudaError_t finish_dx(const moe_loss_config &c, const LossLayout &L, int planes, const float *acc,
+                      float *acc_out, void *dx, void *ws, cudaStream_t s) {
+  const int vecs = c.d / Vec16<T>::N;
+  return launch_pdl(loss_dx_kernel<T>, dim3(blocks_of((int64_t)c.n * vecs)), dim3(256), 0, s,
+                    at<float>(ws, L.dx), planes, acc, acc_out, c.n, vecs, at<int32_t>(ws, L.range),
+                    at<int32_t>(ws, L.list), (T *)dx, at<int>(ws, L.status));
+}
+cudaError_t finish_dx(const moe_loss_config &c, const LossLayout &L, int planes, const float *acc,
+                      float *acc_out, void *dx, void *ws, cudaStream_t s) {
+  return c.dtype == MOE_F32 ? finish_dx<float>(c, L, planes, acc, acc_out, dx, ws, s)
+                            : finish_dx<__nv_bfloat16>(c, L, planes, acc, acc_out, dx, ws, s);
+}
+
+// The logits' product on the CUDA cores, over entries v0 .. of the vocabulary.
+RowsProduct simt_product(const moe_loss_config &c, int epi, const void *x, const void *W, int v0,
+                         int entries) {
+  RowsProduct p{};
+  p.dtype = c.dtype;
+  p.epi = epi;
+  p.num_experts = 1;
+  p.rows = entries;
+  p.K = c.d;
+  p.N = c.n;
+  p.A = (const char *)W + (size_t)v0 * c.d * elem_size(c);
+  p.B = x;
+  p.loss.v0 = v0;
+  return p;
+}
+
 cudaError_t piece_gradient_simt(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
-                                int entries, int i, bool dx, void *dW, void *ws, cudaStream_t s) {
+                                int entries, int i, void *dx, void *dW, void *ws, cudaStream_t s) {
   const size_t row = (size_t)c.d * elem_size(c);
   int *status = at<int>(ws, L.status);
-  LOSS_TRY(piece_logits(c, L, W, v0, entries, ws, s));
-  LOSS_TRY(launch_pdl(loss_grad_kernel, dim3(blocks_of((int64_t)entries * L.pitch / 4)), dim3(256),
-                      0, s, at<float4>(ws, L.logits), L.pitch / 4, entries, v0, c.z_loss,
-                      at<int32_t>(ws, L.range), at<int4>(ws, L.target), at<float4>(ws, L.lse),
-                      at<float4>(ws, L.dloss), status));
+  RowsProduct l = simt_product(c, kRowsLossGrad, at<void>(ws, L.x), W, v0, entries);
+  l.out = at<void>(ws, L.logits);
+  l.ldo = L.pitch;
+  l.loss.target = at<int32_t>(ws, L.target);
+  l.loss.range = at<int32_t>(ws, L.range);
+  l.loss.lse = at<float>(ws, L.lse);
+  l.loss.dloss = at<float>(ws, L.dloss);
+  l.loss.z_loss = c.z_loss;
+  LOSS_TRY(launch_rows_simt(l, status, s));
   if (dW) {
     RowsProduct p{};
     p.dtype = c.dtype;
@@ -464,12 +434,36 @@ cudaError_t piece_gradient_simt(const moe_loss_config &c, const LossLayout &L, c
   GradProduct p = dx_product(c, L, entries);
   p.A = at<void>(ws, L.logits);
   p.B = (const char *)W + v0 * row;
-  p.out = at<char>(ws, L.dx) + (size_t)i * c.n * row;
-  return launch_grad_simt(&p, 1, grad_splits_simt(&p, 1), at<float>(ws, L.parts), status, s);
+  const int splits = grad_splits_simt(&p, 1);
+  LOSS_TRY(launch_grad_simt(&p, 1, splits, at<float>(ws, L.dx), status, s, false));
+  float *acc = at<float>(ws, L.acc);
+  return finish_dx(c, L, splits, i > 0 ? acc : nullptr, i + 1 < L.pieces ? acc : nullptr, dx, ws, s);
+}
+
+// The operands that the products on the tensor cores share, over entries v0 .. of
+// the vocabulary.
+LossProduct pair_product(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
+                         int entries, void *ws) {
+  LossProduct p{};
+  p.n = c.n;
+  p.d = c.d;
+  p.entries = entries;
+  p.v0 = v0;
+  p.range = at<int32_t>(ws, L.range);
+  p.target = at<int32_t>(ws, L.target);
+  p.x = at<void>(ws, L.x);
+  p.W = (const char *)W + (size_t)v0 * c.d * 2;
+  p.lse = at<float>(ws, L.lse);
+  p.dloss = at<float>(ws, L.dloss);
+  p.z_loss = c.z_loss;
+  p.dl = at<void>(ws, L.logits);
+  p.pitch = dl_pitch(entries);
+  p.planes = at<float>(ws, L.dx);
+  return p;
 }
 
 cudaError_t piece_gradient_pair(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
-                                int entries, int i, bool dx, void *dW, void *ws, cudaStream_t s) {
+                                int entries, int i, void *dx, void *dW, void *ws, cudaStream_t s) {
   int *status = at<int>(ws, L.status);
   LossProduct p = pair_product(c, L, W, v0, entries, ws);
   LOSS_TRY(launch_loss_logit_grad(p, status, s));
@@ -485,14 +479,22 @@ cudaError_t piece_gradient_pair(const moe_loss_config &c, const LossLayout &L, c
       LOSS_TRY(launch_grad_simt(&g, 1, splits, parts, status, s));
     } else {
       if (!gemm_grad_supported(g)) return cudaErrorNotSupported;
-      LOSS_TRY(launch_gemm_grad(&g, 1, splits, parts, 0, status, s));
+      // (149 tokens, half of them counted, 32003 entries, d 7168: XXX us one after the
+      // other, XXX side by side)
+      const int all = num_sms() / 2, writing = (3 * all + 4) / 5;
+      const bool beside = dx && L.beside && splits == 1;
+      if (beside) p.beside = all - writing;
+      LOSS_TRY(launch_gemm_grad(&g, 1, splits, parts, beside ? writing : 0, status, s));
     }
   }
   if (!dx) return cudaSuccess;
   // (the last piece may be cut into fewer ranges, and adds to the first planes)
-  p.splits = entries == L.piece ? L.planes : loss_dx_splits(c.n, c.d, entries, L.planes);
+  p.splits = entries == L.piece ? L.planes
+                                : loss_dx_splits(c.n, c.d, entries, L.planes,
+                                                 L.beside ? L_PAIRS - L_WRITING : L_PAIRS);
   p.add = i > 0;
-  return launch_loss_dx(p, status, s);
+  LOSS_TRY(launch_loss_dx(p, status, s));
+  return i + 1 < L.pieces ? cudaSuccess : finish_dx(c, L, L.planes, nullptr, nullptr, dx, ws, s);
 }
 
 }  // namespace
@@ -503,24 +505,47 @@ cudaError_t launch_loss(const moe_loss_config &c, const void *x, const void *W,
                         const int32_t *targets, float *loss, float *lse, void *ws, cudaStream_t s) {
   const LossLayout L = loss_layout(c);
   if (L.pair && !loss_pair_supported(c)) return cudaErrorNotSupported;
-  int *status = at<int>(ws, L.status);
-  LOSS_TRY(launch_pack(c, L, x, targets, nullptr, nullptr, loss, lse, nullptr, ws, s));
-  if (L.pair) {
-    LOSS_TRY(launch_loss_sums(pair_product(c, L, W, 0, c.vocab, ws), status, s));
-  } else {
-    for (int v0 = 0; v0 < c.vocab; v0 += L.piece) {
-      const int entries = c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece;
-      LOSS_TRY(piece_logits(c, L, W, v0, entries, ws, s));
-      LOSS_TRY(launch_pdl(loss_chunk_kernel,
-                          dim3((c.n + 31) / 32, (entries + L_CHUNK - 1) / L_CHUNK), dim3(256), 0, s,
-                          at<float>(ws, L.logits), L.pitch, entries, v0, L.chunks,
-                          at<int32_t>(ws, L.range), at<int32_t>(ws, L.target), at<float>(ws, L.at),
-                          at<float2>(ws, L.sums), status));
-    }
+  FinishArgs f{};
+  f.sums = at<float2>(ws, L.sums);
+  f.chunks = f.pitch = L.chunks;
+  f.n = c.n;
+  f.vocab = c.vocab;
+  f.z_loss = c.z_loss;
+  f.targets = targets;
+  f.at = at<float>(ws, L.at);
+  f.loss = loss;
+  f.lse = lse;
+  f.status = at<int>(ws, L.status);
+  if (L.packed) {
+    LOSS_TRY(launch_pack(c, L, x, targets, nullptr, nullptr, loss, lse, nullptr, ws, s));
+    f.range = at<int32_t>(ws, L.range);
+    f.list = at<int32_t>(ws, L.list);
   }
-  return launch_pdl(loss_finish_kernel, dim3((c.n + 7) / 8), dim3(256), 0, s,
-                    at<float2>(ws, L.sums), L.chunks, c.z_loss, at<int32_t>(ws, L.range),
-                    at<int32_t>(ws, L.list), at<float>(ws, L.at), loss, lse, status);
+  if (L.pair) {
+    LossProduct p = pair_product(c, L, W, 0, c.vocab, ws);
+    p.sums = at<float2>(ws, L.sums);
+    p.width = L.width;
+    p.chunks = L.chunks;
+    p.at = at<float>(ws, L.at);
+    if (!L.packed) {
+      p.range = nullptr;
+      p.target = targets;
+      p.x = x;
+    }
+    LOSS_TRY(launch_loss_sums(p, f.status, s));
+  } else {
+    RowsProduct p = simt_product(c, kRowsLossSums, x, W, 0, c.vocab);
+    const int tile = rows_simt_tile(p);
+    f.chunks = (c.vocab + tile - 1) / tile;
+    p.loss.target = targets;
+    p.loss.sums = at<float2>(ws, L.sums);
+    p.loss.chunks = L.chunks;
+    p.loss.at = at<float>(ws, L.at);
+    LOSS_TRY(launch_rows_simt(p, f.status, s));
+  }
+  if (c.n <= 8 * num_sms())
+    return launch_pdl(loss_finish_kernel<true>, dim3(c.n), dim3(256), 0, s, f);
+  return launch_pdl(loss_finish_kernel<false>, dim3((c.n + 7) / 8), dim3(256), 0, s, f);
 }
 
 cudaError_t launch_loss_backward(const moe_loss_config &c, const void *x, const void *W,
@@ -530,14 +555,9 @@ cudaError_t launch_loss_backward(const moe_loss_config &c, const void *x, const 
   if (L.pair && !loss_pair_supported(c)) return cudaErrorNotSupported;
   LOSS_TRY(launch_pack(c, L, x, targets, lse, dloss, nullptr, nullptr, dx, ws, s));
   auto piece = L.pair ? piece_gradient_pair : piece_gradient_simt;
-  for (int v0 = 0, i = 0; v0 < c.vocab; v0 += L.piece, ++i) {
-    const int entries = c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece;
-    LOSS_TRY(piece(c, L, W, v0, entries, i, dx != nullptr, dW, ws, s));
-  }
-  if (!dx) return cudaSuccess;
-  if (c.dtype == MOE_F32) return finish_dx<float, float>(c, L, dx, ws, s);
-  return L.pair ? finish_dx<__nv_bfloat16, float>(c, L, dx, ws, s)
-                : finish_dx<__nv_bfloat16, __nv_bfloat16>(c, L, dx, ws, s);
+  for (int v0 = 0, i = 0; v0 < c.vocab; v0 += L.piece, ++i)
+    LOSS_TRY(piece(c, L, W, v0, c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece, i, dx, dW, ws, s));
+  return cudaSuccess;
 }
 
 }  // namespace moe

@@ -8,7 +8,8 @@
 
 namespace moe {
 
-// Tokens are packed rows [n][d] of which range[1] count (read on the device);
+// Tokens are rows [n][d] of which the first range[1] count (read on the device; all
+// without a range);
 // `entries` of the vocabulary from v0 on, W their rows [entries][d].
 struct LossProduct {
   int n, d, entries, v0;
@@ -28,14 +29,17 @@ struct LossProduct {
   // what they hold, or stored
   float *planes;
   int splits, add;
+  // 0, or the SM pairs that dx takes beside the launch before, whose results it does
+  // not read
+  int beside;
 };
 
 bool loss_pair_supported(const moe_loss_config &c);   // (makes CUDA calls)
 // Entries per tile of the forward, and how many partial sums that makes.
 int loss_width(int n, int vocab);
 inline int loss_chunks(int vocab, int width) { return 2 * ((vocab + width - 1) / width); }
-// Ranges of the entries for dx, `most` at most.
-int loss_dx_splits(int n, int d, int entries, int most);
+// Ranges of the entries for dx on so many SM pairs, `most` at most.
+int loss_dx_splits(int n, int d, int entries, int most, int pairs);
 
 cudaError_t launch_loss_sums(const LossProduct &p, int *status, cudaStream_t s);
 cudaError_t launch_loss_logit_grad(const LossProduct &p, int *status, cudaStream_t s);

@@ -132,12 +132,13 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
     tc::fence_mbar_init();
   }
   // (all above ran beside the end of the kernel before; from here on its
-  // results are read)
-  pdl_wait();
+  // results are read, or with `beside` those of the ones before it, which lets this
+  // one start once they are complete)
+  if (MODE != kDx || !p.beside) pdl_wait();
   if (threadIdx.x == 0) {
     sh.failed_on_entry = status_failed(args.status) ? 1 : 0;
     sh.abort = sh.failed_on_entry;
-    sh.counted = min(max(p.range[1], 0), p.n);
+    sh.counted = p.range ? min(max(p.range[1], 0), p.n) : p.n;
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -389,6 +390,7 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
   }
   if (threadIdx.x == 0 && sh.abort && !sh.failed_on_entry)
     set_status(args.status, MOE_ERR_TIMEOUT, blockIdx.x);
+  if (MODE == kDx && p.beside) pdl_wait();   // (ends after the launch before)
 }
 
 constexpr int kPairs = 76;   // SM pairs that the plans count on
@@ -425,7 +427,7 @@ cudaError_t launch(const LMaps &maps, const LArgs &a, cudaStream_t s) {
       pairs = num_sms() / 2;
     }
   }
-  cfg.gridDim = dim3(2 * pairs);
+  cfg.gridDim = dim3(2 * (a.p.beside ? a.p.beside : pairs));
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
@@ -463,7 +465,7 @@ int loss_width(int n, int vocab) {
   return best;
 }
 
-int loss_dx_splits(int n, int d, int entries, int most) {
+int loss_dx_splits(int n, int d, int entries, int most, int pairs) {
   const int64_t tiles = (((int64_t)n + 2 * LM - 1) / (2 * LM)) * ((d + LN - 1) / LN);
   const int KB = (entries + LK - 1) / LK;
   int best = 1;
@@ -474,8 +476,8 @@ int loss_dx_splits(int n, int d, int entries, int most) {
     const int each = (KB + s - 1) / s;
     if ((KB + each - 1) / each != s) continue;   // (a range would be empty)
     if (s > 1 && each < 8) break;
-    const double cost = (double)((tiles * s + kPairs - 1) / kPairs) * (each + 12) +
-                        (double)s * n * d * 8e-6;
+    const double cost = (double)((tiles * s + pairs - 1) / pairs) * (each + 12) +
+                        (double)s * n * d * 4e-6;
     if (cost < 0.97 * least) {
       least = cost;
       best = s;

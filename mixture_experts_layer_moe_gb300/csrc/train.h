@@ -53,6 +53,25 @@ enum {
   kRowsSwiglu = 2,      // out = silu(A B) * (A B2), out_g = A B, out_u = A B2
   kRowsReluGrad = 3,    // out = A B where h > 0
   kRowsSwigluGrad = 4,  // v = A B: out = v u s (1 + g (1 - s)), out_u = v g s
+  // on the CUDA cores, A the vocabulary's rows and B the tokens' (LossTerms below)
+  kRowsLossSums = 5,    // v = A B: a maximum and a sum of exponentials per token
+  kRowsLossGrad = 6,    // out = dloss (e^(v - lse) (1 + 2 z lse) - [target]), fp32
+};
+
+// What the cross entropy's epilogues take: per token, and the vocabulary entry of
+// row 0.
+struct LossTerms {
+  const int32_t *target;
+  int v0;
+  // kRowsLossSums: sums [tokens][chunks], of one tile of entries each from chunk0 on;
+  // the target's logit
+  float2 *sums;
+  int chunks, chunk0;
+  float *at;
+  // kRowsLossGrad: tokens from range[1] on do not count
+  const int32_t *range;
+  const float *lse, *dloss;
+  float z_loss;
 };
 
 // Products that write rows of the segments: for q in segment e,
@@ -73,13 +92,15 @@ struct RowsProduct {
   int add_k;
   int beside;                  // see launch_gemm_grad
   // For a bf16 layer: A and A2 are fp32 (on the CUDA cores), or out and out_u of a
-  // gradient (on the CUDA cores also out of a plain product) are
+  // gradient are
   int a_f32, out_f32;
-  // kRowsPlain on the CUDA cores: elements from one row of out to the next, a
-  // multiple of 4 (0: N).  With it N may be any number; columns up to the next
-  // multiple of 4 are written as zeros.
+  // kRowsLossGrad: elements from one row of out to the next, a multiple of 4; columns
+  // from N on are written as zeros
   int ldo;
+  LossTerms loss;
 };
+// Entries of a tile of rows (p as launch_rows_simt takes it).
+int rows_simt_tile(const RowsProduct &p);
 // fp32, and small bf16 products: at most so many multiplications each.
 constexpr int64_t kSmallProducts = 1 << 24;
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s);
@@ -112,8 +133,10 @@ int grad_splits_simt(const GradProduct *p, int count);
 // adds the runs where the rows are cut into several; splits, parts: as
 // grad_splits and grad_scratch (below) say.
 bool grads_small(const GradProduct *p, int count);
+// add = false: the runs' partial sums stay in parts [problem][expert][run][M][N], also of
+// one run.
 cudaError_t launch_grad_simt(const GradProduct *p, int count, int splits, float *parts, int *status,
-                             cudaStream_t s);
+                             cudaStream_t s, bool add = true);
 // The same on tensor cores (bf16; SM pairs).
 bool gemm_grad_supported(const GradProduct &p);
 // Runs that the segments' rows are cut into where the problems are too few to

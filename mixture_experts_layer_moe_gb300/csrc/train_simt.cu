@@ -210,6 +210,45 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int row
   return false;
 }
 
+// The tile's sums for the cross entropy: thread by thread over its rows, then over the
+// threads of a column through `scratch` (the operands' shared memory).
+template <int TILE>
+__device__ __forceinline__ void loss_sums(const RowsProduct &p, const float2 (&acc)[4][2],
+                                          float *scratch, const Place<TILE> &me, int row0, int end,
+                                          int c) {
+  constexpr int ROWS = Place<TILE>::ROWS, PARTS = TILE / ROWS, LD = PARTS + 1;
+  static_assert(sizeof(float) * 2 * TILE * LD <= 2 * sizeof(typename Geo<TILE>::Buf), "scratch");
+  float *tops = scratch, *sums = scratch + TILE * LD;
+  const LossTerms &t = p.loss;
+  __syncthreads();   // (the operands have been read)
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int target = c + j < p.N ? t.target[c + j] - t.v0 - row0 - me.row : -1;
+    float l[ROWS], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const bool there = row0 + me.row + i < end;
+      l[i] = there ? (j & 1 ? acc[i][j / 2].y : acc[i][j / 2].x) : -INFINITY;
+      if (there && i == target) t.at[c + j] = l[i];
+      top = fmaxf(top, l[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) sum += expf(l[i] - (top == -INFINITY ? 0.f : top));
+    tops[(me.col + j) * LD + me.row / ROWS] = top;
+    sums[(me.col + j) * LD + me.row / ROWS] = sum;
+  }
+  __syncthreads();
+  const int col = threadIdx.x, token = c - me.col + col;
+  if (col >= TILE || token >= p.N) return;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) top = fmaxf(top, tops[col * LD + i]);
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i)
+    sum += sums[col * LD + i] * expf(tops[col * LD + i] - (top == -INFINITY ? 0.f : top));
+  t.sums[(int64_t)token * t.chunks + t.chunk0 + blockIdx.x] = make_float2(top, sum);
+}
+
 // Steps of a product, with the next step's loads in flight: load(step) fills the
 // registers, store(buffer) writes them to shared memory, multiply(buffer) takes
 // the step.
@@ -282,12 +321,16 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
   join_groups<TILE>(acc, &pool[0][0][0], me.tx, me.ty, me.g);
   if constexpr (DUAL) join_groups<TILE>(acc2, &pool[0][0][0], me.tx, me.ty, me.g);
   const int c = n0 + me.col;   // (N, or out's pitch, is a multiple of 4)
+  if constexpr (EPI == kRowsLossSums) {
+    loss_sums<TILE>(p, acc, &pool[0][0][0], me, row0, end, c);
+    return;
+  }
   if (c >= N) return;
 #pragma unroll
   for (int i = 0; i < Place<TILE>::ROWS; ++i) {
     const int r = row0 + me.row + i;
     if (r >= end) continue;
-    const int64_t at = (int64_t)r * (EPI == kRowsPlain && p.ldo ? p.ldo : N) + c;
+    const int64_t at = (int64_t)r * (EPI == kRowsLossGrad ? p.ldo : N) + c;
     float v[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
     if constexpr (EPI == kRowsRelu) {
 #pragma unroll
@@ -315,6 +358,19 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
       }
       put4<TO>(p.out_u, at, du);
     }
+    if constexpr (EPI == kRowsLossGrad) {
+      const LossTerms &t = p.loss;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (c + j >= t.range[1]) {
+          v[j] = 0.f;
+          continue;
+        }
+        const float lse = t.lse[c + j];
+        const float prob = expf(v[j] - lse) * fmaf(2.f * t.z_loss, lse, 1.f);
+        v[j] = t.dloss[c + j] * (t.target[c + j] == t.v0 + r ? prob - 1.f : prob);
+      }
+    }
     if (EPI == kRowsPlain && p.add) {
       // the sum of this row's add_k other rows
       for (int j = 0; j < p.add_k; ++j) {
@@ -340,6 +396,7 @@ __global__ void __launch_bounds__(T_THREADS) rows_simt_kernel(RowsProduct p, int
 struct GradSet {
   GradProduct p[kMaxGradProblems];
   int first[kMaxGradProblems + 1];   // an expert's tiles before problem i
+  bool partial;                      // the outputs are partial sums, in fp32
 };
 template <typename T, int TILE>
 __global__ void __launch_bounds__(T_THREADS)
@@ -402,7 +459,7 @@ grad_simt_kernel(const __grid_constant__ GradSet set, int *status) {
     const float v[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
     if (m >= M) continue;
     const int64_t at = (((int64_t)e * gridDim.z + blockIdx.z) * M + m) * N + c;
-    if (gridDim.z > 1) put4<float>(p.out, at, v);   // partial sums
+    if (set.partial) put4<float>(p.out, at, v);
     else put4<T>(p.out, at, v);
   }
 }
@@ -445,12 +502,13 @@ cudaError_t launch_rows(const RowsProduct &p, int *status, cudaStream_t s) {
   if constexpr (sizeof(T) == 2) {
     // (fp32 dg, du and dl)
     auto wide = p.a_f32 ? rows_simt_kernel<T, kRowsPlain, true, TILE, float>
-                : p.epi == kRowsPlain   ? rows_simt_kernel<T, kRowsPlain, false, TILE, T, float>
                 : p.epi == kRowsReluGrad ? rows_simt_kernel<T, kRowsReluGrad, true, TILE, T, float>
                                          : rows_simt_kernel<T, kRowsSwigluGrad, true, TILE, T, float>;
     if (p.a_f32 || p.out_f32) return launch_pdl(wide, grid, dim3(T_THREADS), 0, s, p, status);
   }
-  auto with = p.epi == kRowsPlain && p.b_rows ? rows_simt_kernel<T, kRowsPlain, true, TILE>
+  auto with = p.epi == kRowsLossSums   ? rows_simt_kernel<T, kRowsLossSums, false, TILE>
+              : p.epi == kRowsLossGrad ? rows_simt_kernel<T, kRowsLossGrad, false, TILE, T, float>
+              : p.epi == kRowsPlain && p.b_rows ? rows_simt_kernel<T, kRowsPlain, true, TILE>
               : p.epi == kRowsPlain           ? rows_simt_kernel<T, kRowsPlain, false, TILE>
               : p.epi == kRowsRelu            ? rows_simt_kernel<T, kRowsRelu, false, TILE>
               : p.epi == kRowsSwiglu          ? rows_simt_kernel<T, kRowsSwiglu, false, TILE>
@@ -464,11 +522,14 @@ bool large_tiles(int64_t tiles) { return tiles >= num_sms(); }
 
 }  // namespace
 
+int rows_simt_tile(const RowsProduct &p) {
+  return p.dtype == MOE_F32 && large_tiles((int64_t)((p.rows + 63) / 64) * ((p.N + 63) / 64)) ? 64 : 32;
+}
+
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s) {
   if (p.dtype == MOE_BF16) return launch_rows<__nv_bfloat16, 32>(p, status, s);
-  return large_tiles((int64_t)((p.rows + 63) / 64) * ((p.N + 63) / 64))
-             ? launch_rows<float, 64>(p, status, s)
-             : launch_rows<float, 32>(p, status, s);
+  return rows_simt_tile(p) == 64 ? launch_rows<float, 64>(p, status, s)
+                                 : launch_rows<float, 32>(p, status, s);
 }
 
 // bf16 gradients take the pair kernel where it is the faster.  CUDA cores / pair
@@ -505,7 +566,7 @@ int grad_splits_simt(const GradProduct *p, int count) {
 }
 
 cudaError_t launch_grad_simt(const GradProduct *p, int count, int splits, float *parts, int *status,
-                             cudaStream_t s) {
+                             cudaStream_t s, bool add) {
   const int E = p[0].offsets ? p[0].num_experts : 1;
   GradSet set{};
   auto lay = [&](int tile) {
@@ -520,7 +581,8 @@ cudaError_t launch_grad_simt(const GradProduct *p, int count, int splits, float 
   const dim3 grid(lay(large ? 64 : 32), E, splits);
   GradSum sum{};
   int64_t most = 0;
-  if (splits > 1) {
+  set.partial = splits > 1 || !add;
+  if (set.partial) {
     for (int i = 0; i < count; ++i) {
       const int64_t per = (int64_t)p[i].M * p[i].N;
       sum.part[i] = parts;
@@ -538,7 +600,7 @@ cudaError_t launch_grad_simt(const GradProduct *p, int count, int splits, float 
               : large ? grad_simt_kernel<float, 64>
                       : grad_simt_kernel<float, 32>;
   const cudaError_t e = launch_pdl(with, grid, dim3(T_THREADS), 0, s, set, status);
-  if (e != cudaSuccess || splits == 1) return e;
+  if (e != cudaSuccess || splits == 1 || !add) return e;
   const int64_t blocks = (most / 4 + 255) / 256;
   return launch_pdl(bf16 ? simt_sum_kernel<__nv_bfloat16> : simt_sum_kernel<float>,
                     dim3((unsigned)(blocks < 608 ? blocks : 608), count), dim3(256), 0, s, sum);
