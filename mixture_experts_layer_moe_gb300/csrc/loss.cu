@@ -37,7 +37,6 @@ constexpr int L_UNIT = 256;                            // a piece's entries are 
 constexpr int64_t L_PIECE_BYTES = (int64_t)256 << 20;  // of a piece's dl, about
 constexpr int64_t L_PIECE_MAX = 1 << 22;               // entries of a piece
 constexpr int L_MAX_SPLITS = 76;
-constexpr int L_PAIRS = 76, L_WRITING = 46;            // SM pairs that the plan counts on
 
 struct LossLayout {
   size_t status, range, list, target, lse, dloss, at, x, sums, logits, dx, acc, parts, total;
@@ -48,7 +47,7 @@ struct LossLayout {
   int pieces;
   int width, chunks;   // entries per tile of the forward; partial sums per token at most
   int planes;          // dx: partial sums of a piece
-  bool beside;         // dW and dx run side by side
+  bool few;            // dx and dW in one pass (loss_few.cu)
 };
 
 int elem_size(const moe_loss_config &c) { return c.dtype == MOE_F32 ? 4 : 2; }
@@ -83,14 +82,16 @@ GradProduct dw_product(const moe_loss_config &c, int entries) {
   return p;
 }
 
+int dx_splits(const moe_loss_config &c, const LossLayout &L, int entries, int most) {
+  return L.few ? loss_few_splits(c.d, entries, most) : loss_dx_splits(c.n, c.d, entries, most);
+}
+
 LossLayout loss_layout(const moe_loss_config &c) {
   LossLayout L{};
   const size_t n = c.n, z = elem_size(c);
   L.pair = c.dtype == MOE_BF16 && !small_loss(c);
   L.packed = L.pair && c.n > 256;
-  // With one block of tokens the gradient's products are bound by reading W and
-  // writing dW: side by side HBM moves both ways.
-  L.beside = L.pair && c.n <= 256;
+  L.few = L.pair && c.n <= kLossFewTokens;
   L.pitch = (c.n + 3) / 4 * 4;
   // pieces of nearly equal size
   int64_t fit = L_PIECE_BYTES / ((int64_t)(L.pitch > 0 ? L.pitch : 4) * (L.pair ? 2 : 4));
@@ -103,7 +104,7 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.width = L.pair ? loss_width(c.n, c.vocab) : 0;
   L.chunks = L.pair ? loss_chunks(c.vocab, L.width) : (c.vocab + 31) / 32;
   if (L.pair) {
-    L.planes = loss_dx_splits(c.n, c.d, L.piece, L_MAX_SPLITS, L.beside ? L_PAIRS - L_WRITING : L_PAIRS);
+    L.planes = dx_splits(c, L, L.piece, L_MAX_SPLITS);
   } else {
     L.planes = 1;
     for (int entries : {L.piece, last}) {
@@ -136,7 +137,7 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.acc = take(!L.pair && L.pieces > 1 ? n * c.d * 4 : 0);
   size_t parts = 0;
   for (int entries : {L.piece, last}) {
-    if (!L.pair) break;
+    if (!L.pair || L.few) break;
     const GradProduct p = dw_product(c, entries);
     const size_t bytes = grad_scratch(&p, 1);
     if (bytes > parts) parts = bytes;
@@ -466,34 +467,30 @@ cudaError_t piece_gradient_pair(const moe_loss_config &c, const LossLayout &L, c
                                 int entries, int i, void *dx, void *dW, void *ws, cudaStream_t s) {
   int *status = at<int>(ws, L.status);
   LossProduct p = pair_product(c, L, W, v0, entries, ws);
+  void *out = dW ? (char *)dW + (size_t)v0 * c.d * 2 : nullptr;
+  // (the last piece may be cut into fewer ranges, and adds to the first planes)
+  p.splits = entries == L.piece ? L.planes : dx_splits(c, L, entries, L.planes);
+  p.add = i > 0;
   LOSS_TRY(launch_loss_logit_grad(p, status, s));
-  if (dW) {
+  if (L.few) {
+    LOSS_TRY(launch_loss_few(p, out, dx != nullptr, status, s));
+  } else if (dW) {
     GradProduct g = dw_product(c, entries);
     g.offsets = p.range;
     g.A = p.dl;
     g.B = p.x;
-    g.out = (char *)dW + (size_t)v0 * c.d * 2;
+    g.out = out;
     const int splits = grad_splits(&g, 1);
     float *parts = at<float>(ws, L.parts);
     if (grads_small(&g, 1)) {
       LOSS_TRY(launch_grad_simt(&g, 1, splits, parts, status, s));
     } else {
       if (!gemm_grad_supported(g)) return cudaErrorNotSupported;
-      // (149 tokens, half of them counted, 32003 entries, d 7168: XXX us one after the
-      // other, XXX side by side)
-      const int all = num_sms() / 2, writing = (3 * all + 4) / 5;
-      const bool beside = dx && L.beside && splits == 1;
-      if (beside) p.beside = all - writing;
-      LOSS_TRY(launch_gemm_grad(&g, 1, splits, parts, beside ? writing : 0, status, s));
+      LOSS_TRY(launch_gemm_grad(&g, 1, splits, parts, 0, status, s));
     }
   }
   if (!dx) return cudaSuccess;
-  // (the last piece may be cut into fewer ranges, and adds to the first planes)
-  p.splits = entries == L.piece ? L.planes
-                                : loss_dx_splits(c.n, c.d, entries, L.planes,
-                                                 L.beside ? L_PAIRS - L_WRITING : L_PAIRS);
-  p.add = i > 0;
-  LOSS_TRY(launch_loss_dx(p, status, s));
+  if (!L.few) LOSS_TRY(launch_loss_dx(p, status, s));
   return i + 1 < L.pieces ? cudaSuccess : finish_dx(c, L, L.planes, nullptr, nullptr, dx, ws, s);
 }
 

@@ -29,20 +29,24 @@ struct LossProduct {
   // what they hold, or stored
   float *planes;
   int splits, add;
-  // 0, or the SM pairs that dx takes beside the launch before, whose results it does
-  // not read
-  int beside;
 };
 
 bool loss_pair_supported(const moe_loss_config &c);   // (makes CUDA calls)
 // Entries per tile of the forward, and how many partial sums that makes.
 int loss_width(int n, int vocab);
 inline int loss_chunks(int vocab, int width) { return 2 * ((vocab + width - 1) / width); }
-// Ranges of the entries for dx on so many SM pairs, `most` at most.
-int loss_dx_splits(int n, int d, int entries, int most, int pairs);
+// Ranges of the entries for dx, `most` at most.
+int loss_dx_splits(int n, int d, int entries, int most);
 
 cudaError_t launch_loss_sums(const LossProduct &p, int *status, cudaStream_t s);
 cudaError_t launch_loss_logit_grad(const LossProduct &p, int *status, cudaStream_t s);
 cudaError_t launch_loss_dx(const LossProduct &p, int *status, cudaStream_t s);
+
+// dx (as launch_loss_dx leaves it) and dW [entries][d] (or nullptr) in one pass over W, for
+// kLossFewTokens at most; and into how many ranges of the entries dx is cut.
+constexpr int kLossFewTokens = 192;
+int loss_few_splits(int d, int entries, int most);
+cudaError_t launch_loss_few(const LossProduct &p, void *dW, bool want_dx, int *status,
+                            cudaStream_t s);
 
 }  // namespace moe

@@ -4,7 +4,8 @@
 //   kSums   l[t][v] = sum_k x[t][k] W[v][k], which the epilogue reduces to a
 //           maximum and a sum of exponentials per token as it drains the tile;
 //   kGrad   the same product, turned into dl = dloss (e^(l - lse) (1 + 2 z lse) -
-//           [v = target]) in the epilogue and stored in bf16;
+//           [v = target]) in the epilogue and stored in bf16 (zeros in the rows of the
+//           last 32 tokens that do not count);
 //   kDx     dx[t][c] = sum_v dl[t][v] W[v][c], W read as it is stored (an N-major
 //           operand), in fp32.
 // With a token per lane the softmax runs over a thread's own accumulator columns:
@@ -132,9 +133,8 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
     tc::fence_mbar_init();
   }
   // (all above ran beside the end of the kernel before; from here on its
-  // results are read, or with `beside` those of the ones before it, which lets this
-  // one start once they are complete)
-  if (MODE != kDx || !p.beside) pdl_wait();
+  // results are read)
+  pdl_wait();
   if (threadIdx.x == 0) {
     sh.failed_on_entry = status_failed(args.status) ? 1 : 0;
     sh.abort = sh.failed_on_entry;
@@ -322,7 +322,7 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
               float g[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                g[i] = scale * exp2_fast((__uint_as_float(a[i]) - lse) * kLog2e);
+                g[i] = there ? scale * exp2_fast((__uint_as_float(a[i]) - lse) * kLog2e) : 0.f;
               const int here = target - c - 32 * half;
               if (__any_sync(0xffffffffu, here >= 0 && here < 32)) {
 #pragma unroll
@@ -390,7 +390,6 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
   }
   if (threadIdx.x == 0 && sh.abort && !sh.failed_on_entry)
     set_status(args.status, MOE_ERR_TIMEOUT, blockIdx.x);
-  if (MODE == kDx && p.beside) pdl_wait();   // (ends after the launch before)
 }
 
 constexpr int kPairs = 76;   // SM pairs that the plans count on
@@ -427,7 +426,7 @@ cudaError_t launch(const LMaps &maps, const LArgs &a, cudaStream_t s) {
       pairs = num_sms() / 2;
     }
   }
-  cfg.gridDim = dim3(2 * (a.p.beside ? a.p.beside : pairs));
+  cfg.gridDim = dim3(2 * pairs);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
@@ -465,7 +464,7 @@ int loss_width(int n, int vocab) {
   return best;
 }
 
-int loss_dx_splits(int n, int d, int entries, int most, int pairs) {
+int loss_dx_splits(int n, int d, int entries, int most) {
   const int64_t tiles = (((int64_t)n + 2 * LM - 1) / (2 * LM)) * ((d + LN - 1) / LN);
   const int KB = (entries + LK - 1) / LK;
   int best = 1;
@@ -476,7 +475,7 @@ int loss_dx_splits(int n, int d, int entries, int most, int pairs) {
     const int each = (KB + s - 1) / s;
     if ((KB + each - 1) / each != s) continue;   // (a range would be empty)
     if (s > 1 && each < 8) break;
-    const double cost = (double)((tiles * s + pairs - 1) / pairs) * (each + 12) +
+    const double cost = (double)((tiles * s + kPairs - 1) / kPairs) * (each + 12) +
                         (double)s * n * d * 4e-6;
     if (cost < 0.97 * least) {
       least = cost;
