@@ -106,6 +106,7 @@ struct GArgs {
   const uint4 *add;
   const int32_t *add_inv;
   int add_k;
+  const float *scale;   // whole sums are multiplied by *scale (nullptr: 1)
 };
 struct GMaps {
   CUtensorMap a[kMaxGradProblems], b[kMaxGradProblems], out[kMaxGradProblems];
@@ -452,6 +453,7 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
     const uint32_t tempty_first = map_to_rank(tc::smem_u32(&sh.tempty[0]), 0);
     uint8_t *stage_out = smem + STAGES * G_STAGE + (warp - 2) * G_OUT;
     int local = 0;
+    const float scale = args.scale ? *args.scale : 1.f;
     GatherRing gather{sh, args, smem + STAGES * G_STAGE + (G_EPI + (warp - 2) * G_RING) * G_OUT,
                       pair, n_pairs, num_tiles, (int)rank, quarter, part, lane};
     if (ADD) gather.start();
@@ -480,6 +482,13 @@ gemm_grad_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ GAr
           for (int i = 0; i < 32; ++i) a[0][i] = a[1][i] = 0;
         }
         if (!rows_ok) continue;
+        if (!SPLIT && args.scale) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            a[0][i] = __float_as_uint(__uint_as_float(a[0][i]) * scale);
+            a[1][i] = __float_as_uint(__uint_as_float(a[1][i]) * scale);
+          }
+        }
         if (ADD)
           for (int j = 0; j < args.add_k; ++j) gather.add(a);
 #pragma unroll
@@ -540,11 +549,13 @@ struct SumArgs {
   __nv_bfloat16 *out[kMaxGradProblems];
   int64_t per_expert[kMaxGradProblems];   // M * N (a multiple of 8)
   int experts, splits;
+  const float *scale;
   int *status;
 };
 __global__ void __launch_bounds__(256) grad_sum_kernel(SumArgs a) {
   pdl_wait();
   if (status_failed(a.status)) return;
+  const float k = a.scale ? *a.scale : 1.f;
   const int p = blockIdx.y;
   const int64_t per = a.per_expert[p], total = per * a.experts;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < total;
@@ -558,7 +569,9 @@ __global__ void __launch_bounds__(256) grad_sum_kernel(SumArgs a) {
       x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
       y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
     }
-    auto pack = [](float l, float h) { return bf16x2_bits(__float_as_uint(l), __float_as_uint(h)); };
+    auto pack = [k](float l, float h) {
+      return bf16x2_bits(__float_as_uint(l * k), __float_as_uint(h * k));
+    };
     *reinterpret_cast<uint4 *>(a.out[p] + i) =
         make_uint4(pack(x.x, x.y), pack(x.z, x.w), pack(y.x, y.y), pack(y.z, y.w));
   }
@@ -633,7 +646,9 @@ bool gemm_grad_supported(const GradProduct &p) {
 // columns and their sum.)
 int grad_splits(const GradProduct *p, int count) {
   if (count == 0) return 1;
-  if (grads_small(p, count)) return grad_splits_simt(p, count);
+  return grads_small(p, count) ? grad_splits_simt(p, count) : gemm_grad_splits(p, count);
+}
+int gemm_grad_splits(const GradProduct *p, int count) {
   const int64_t tiles = tiles_of(p, count, GN);
   const int E = p[0].offsets ? p[0].num_experts : 1;
   if (tiles >= kPairs) return 1;
@@ -661,12 +676,14 @@ cudaError_t launch_gemm_grad(const GradProduct *p, int count, int splits, float 
   a.status = status;
   a.splits = splits;
   a.beside = beside;
+  a.scale = p[0].scale;
   a.width = width_of(p, count, splits);
   const int E = p[0].offsets ? p[0].num_experts : 1;
   const uint32_t box[2] = {64, GK}, box_out[3] = {splits > 1 ? 32u : 64u, 32, 1};
   SumArgs sum{};
   sum.experts = E;
   sum.splits = splits;
+  sum.scale = p[0].scale;
   sum.status = status;
   int64_t most = 0;
   for (int i = 0; i < count; ++i) {

@@ -39,7 +39,7 @@ constexpr int64_t L_PIECE_MAX = 1 << 22;               // entries of a piece
 constexpr int L_MAX_SPLITS = 76;
 
 struct LossLayout {
-  size_t status, range, list, target, lse, dloss, at, x, sums, logits, dx, acc, parts, total;
+  size_t status, range, scale, list, target, lse, dloss, at, x, sums, logits, dx, acc, parts, total;
   bool pair;    // on the tensor cores
   bool packed;  // the forward packs the tokens that count
   int pitch;    // CUDA cores: tokens, rounded up to whole vectors of fp32
@@ -121,6 +121,7 @@ LossLayout loss_layout(const moe_loss_config &c) {
   };
   L.status = take(256);
   L.range = take(8);
+  L.scale = take(4);
   L.list = take(n * 4);
   L.target = take((size_t)L.pitch * 4);
   L.lse = take((size_t)L.pitch * 4);
@@ -139,7 +140,8 @@ LossLayout loss_layout(const moe_loss_config &c) {
   for (int entries : {L.piece, last}) {
     if (!L.pair || L.few) break;
     const GradProduct p = dw_product(c, entries);
-    const size_t bytes = grad_scratch(&p, 1);
+    const int splits = gemm_grad_splits(&p, 1);
+    const size_t bytes = splits > 1 ? (size_t)splits * entries * c.d * 4 : 0;
     if (bytes > parts) parts = bytes;
   }
   L.parts = take(parts);
@@ -159,6 +161,7 @@ struct PackArgs {
   int32_t *range;              // {0, tokens that count}
   int32_t *list, *target;
   float *lse_c, *dloss_c;
+  float *scale;                // the largest finite |dloss| of those tokens
   uint4 *x_c;                  // rows past the last counted one are zero
   // outputs of the tokens left out
   float *loss_out, *lse_out;
@@ -170,6 +173,7 @@ constexpr int PACK_THREADS = 256;
 // A CTA takes `per` tokens; how many count before them it finds for itself.
 __global__ void __launch_bounds__(PACK_THREADS) loss_pack_kernel(const __grid_constant__ PackArgs a) {
   __shared__ int failed, before, part[PACK_THREADS / 32];
+  __shared__ float largest[PACK_THREADS / 32];
   __shared__ int place[32];   // counted: its position; left out: -1 - the row that it leaves zero
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -223,6 +227,22 @@ __global__ void __launch_bounds__(PACK_THREADS) loss_pack_kernel(const __grid_co
     }
   }
   __syncthreads();
+  if (a.dloss && blockIdx.x == gridDim.x - 1) {
+    // (in the last CTA, which has seen all targets before its own)
+    float most = 0.f;
+    for (int t = threadIdx.x; t < a.n; t += PACK_THREADS) {
+      const float v = fabsf(a.dloss[t]);
+      if (counts(a.targets[t]) && isfinite(v)) most = fmaxf(most, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) largest[warp] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < PACK_THREADS / 32; ++w) most = fmaxf(most, largest[w]);
+      *a.scale = most;
+    }
+  }
   // a warp per row, or the whole CTA for its one row
   const int step = a.per == 1 ? PACK_THREADS : 32, who = a.per == 1 ? 0 : warp;
   for (int i = who; i < count; i += PACK_THREADS / 32) {
@@ -256,6 +276,7 @@ cudaError_t launch_pack(const moe_loss_config &c, const LossLayout &L, const voi
   a.target = at<int32_t>(ws, L.target);
   a.lse_c = at<float>(ws, L.lse);
   a.dloss_c = at<float>(ws, L.dloss);
+  a.scale = at<float>(ws, L.scale);
   a.x_c = at<uint4>(ws, L.x);
   a.loss_out = loss_out;
   a.lse_out = lse_out;
@@ -324,17 +345,18 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant_
   a.loss[t] = loss;
 }
 
-// dx of the counted tokens from the partial sums [planes][n][d], added in order; or
-// (acc_out) what a piece adds to the sum of those before, `acc`.
+// dx of the counted tokens from the partial sums [planes][n][d], added in order (times
+// *scale, if given); or (acc_out) what a piece adds to the sum of those before, `acc`.
 template <typename T>
 __global__ void __launch_bounds__(256)
 loss_dx_kernel(const float *__restrict__ parts, int planes, const float *acc, float *acc_out, int n,
-               int vecs, const int32_t *__restrict__ range, const int32_t *__restrict__ list,
-               T *__restrict__ dx, const int *status) {
+               int vecs, const float *scale, const int32_t *__restrict__ range,
+               const int32_t *__restrict__ list, T *__restrict__ dx, const int *status) {
   constexpr int N = Vec16<T>::N, V = N / 4;
   pdl_wait();
   if (status_failed(status)) return;
   const int64_t total = (int64_t)range[1] * vecs, plane = (int64_t)n * vecs * V;
+  const float k = scale ? *scale : 1.f;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
     const int64_t j = i / vecs;
@@ -355,6 +377,9 @@ loss_dx_kernel(const float *__restrict__ parts, int planes, const float *acc, fl
 #pragma unroll
       for (int h = 0; h < V; ++h) reinterpret_cast<float4 *>(acc_out)[i * V + h] = v[h];
     } else {
+#pragma unroll
+      for (int h = 0; h < V; ++h)
+        v[h] = make_float4(v[h].x * k, v[h].y * k, v[h].z * k, v[h].w * k);
       reinterpret_cast<uint4 *>(dx)[(int64_t)list[j] * vecs + (i - j * vecs)] =
           pack16<T>(reinterpret_cast<const float *>(v));
     }
@@ -377,7 +402,8 @@ cudaError_t finish_dx(const moe_loss_config &c, const LossLayout &L, int planes,
                       float *acc_out, void *dx, void *ws, cudaStream_t s) {
   const int vecs = c.d / Vec16<T>::N;
   return launch_pdl(loss_dx_kernel<T>, dim3(blocks_of((int64_t)c.n * vecs)), dim3(256), 0, s,
-                    at<float>(ws, L.dx), planes, acc, acc_out, c.n, vecs, at<int32_t>(ws, L.range),
+                    at<float>(ws, L.dx), planes, acc, acc_out, c.n, vecs,
+                    L.pair ? at<float>(ws, L.scale) : nullptr, at<int32_t>(ws, L.range),
                     at<int32_t>(ws, L.list), (T *)dx, at<int>(ws, L.status));
 }
 cudaError_t finish_dx(const moe_loss_config &c, const LossLayout &L, int planes, const float *acc,
@@ -456,6 +482,7 @@ LossProduct pair_product(const moe_loss_config &c, const LossLayout &L, const vo
   p.W = (const char *)W + (size_t)v0 * c.d * 2;
   p.lse = at<float>(ws, L.lse);
   p.dloss = at<float>(ws, L.dloss);
+  p.scale = at<float>(ws, L.scale);
   p.z_loss = c.z_loss;
   p.dl = at<void>(ws, L.logits);
   p.pitch = dl_pitch(entries);
@@ -480,14 +507,9 @@ cudaError_t piece_gradient_pair(const moe_loss_config &c, const LossLayout &L, c
     g.A = p.dl;
     g.B = p.x;
     g.out = out;
-    const int splits = grad_splits(&g, 1);
-    float *parts = at<float>(ws, L.parts);
-    if (grads_small(&g, 1)) {
-      LOSS_TRY(launch_grad_simt(&g, 1, splits, parts, status, s));
-    } else {
-      if (!gemm_grad_supported(g)) return cudaErrorNotSupported;
-      LOSS_TRY(launch_gemm_grad(&g, 1, splits, parts, 0, status, s));
-    }
+    g.scale = p.scale;
+    if (!gemm_grad_supported(g)) return cudaErrorNotSupported;
+    LOSS_TRY(launch_gemm_grad(&g, 1, gemm_grad_splits(&g, 1), at<float>(ws, L.parts), 0, status, s));
   }
   if (!dx) return cudaSuccess;
   if (!L.few) LOSS_TRY(launch_loss_dx(p, status, s));

@@ -20,8 +20,9 @@ struct LossProduct {
   float2 *sums;
   int width, chunks;      // entries per tile
   float *at;
-  // the logits' gradient, bf16 [n][pitch], columns from `entries` on zero
-  const float *lse, *dloss;
+  // the logits' gradient divided by *scale, bf16 [n][pitch], columns from `entries` on
+  // zero; dx is left divided by it too, dW is not
+  const float *lse, *dloss, *scale;
   float z_loss;
   void *dl;
   int pitch;

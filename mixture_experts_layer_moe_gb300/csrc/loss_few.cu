@@ -55,6 +55,7 @@ struct FArgs {
   int n, d, entries, splits;
   int want_dx, want_dw, add;
   const int32_t *range;
+  const float *scale;   // dW's sums are multiplied by it
   int *status;
 };
 struct FMaps {
@@ -227,6 +228,7 @@ loss_few_kernel(const __grid_constant__ FMaps maps, const __grid_constant__ FArg
       }
     };
     bool ok = !sh.failed_on_entry;
+    const float scale = *args.scale;
     if (args.want_dw) {
       int local = 0;
       for (int vb = vb0; vb < vb1 && ok; ++vb, ++local) {
@@ -260,8 +262,8 @@ loss_few_kernel(const __grid_constant__ FMaps maps, const __grid_constant__ FArg
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 h =
-                  __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * i]) * scale,
+                                                             __uint_as_float(v[2 * i + 1]) * scale);
               w[i] = *reinterpret_cast<const uint32_t *>(&h);
             }
             *reinterpret_cast<uint4 *>(mine + ((q ^ (lane & 7)) << 4)) =
@@ -329,7 +331,7 @@ int loss_few_splits(int d, int entries, int most) {
 
 cudaError_t launch_loss_few(const LossProduct &p, void *dW, bool want_dx, int *status,
                             cudaStream_t s) {
-  FArgs a{p.n, p.d, p.entries, p.splits, want_dx, dW != nullptr, p.add, p.range, status};
+  FArgs a{p.n, p.d, p.entries, p.splits, want_dx, dW != nullptr, p.add, p.range, p.scale, status};
   FMaps m{};
   auto bf16_map = [](CUtensorMap *t, const void *ptr, int rank, const uint64_t *dims,
                      const uint32_t *box) {

@@ -4,10 +4,15 @@
 //   kSums   l[t][v] = sum_k x[t][k] W[v][k], which the epilogue reduces to a
 //           maximum and a sum of exponentials per token as it drains the tile;
 //   kGrad   the same product, turned into dl = dloss (e^(l - lse) (1 + 2 z lse) -
-//           [v = target]) in the epilogue and stored in bf16 (zeros in the rows of the
+//           [v = target]) / unit in the epilogue and stored in bf16 (zeros in the rows of the
 //           last 32 tokens that do not count);
 //   kDx     dx[t][c] = sum_v dl[t][v] W[v][c], W read as it is stored (an N-major
 //           operand), in fp32.
+// unit is the largest |dloss|: divided by it, the target's entry of a token whose
+// probability is small is near -1 and so nearly exact.  (With dloss = 1 / count in
+// it, rounding it is off the same way for every token, and so is the whole gradient:
+// 4096 tokens, 65536 entries, dx and dW 2.6e-3 of their norms off, 1.9e-3 so, 1.7e-3
+// being the result's own rounding.)
 // With a token per lane the softmax runs over a thread's own accumulator columns:
 // no exchange between lanes, and neither logits nor exponentials leave the SM.
 // (With tokens on the N side, as the experts' products have them, every column of
@@ -53,6 +58,12 @@ constexpr size_t L_SMEM = 1024 + (size_t)LS * L_STAGE + (size_t)L_EPI * L_OUT;
 constexpr int L_BAND = 16;
 constexpr uint32_t L_TMEM_COLS = 512;
 constexpr float kLog2e = 1.4426950408889634f;
+// kSums: k-blocks that the tensor core adds up by itself.  Its sums are cut off, not
+// rounded, at each step, so that their error grows with the number of steps;
+// longer reductions are added up in registers, rounded.  (4096 tokens over 131072 entries,
+// d 4096: the losses 2.0e-6 of their norm off, 4.8e-7 so; 2494 us without and 2560
+// with, 8 k-blocks 2.3e-7 and 2780.)
+constexpr int L_UNIT_KB = 16, L_UNIT_FEW_KB = 8;   // (one block of tokens: HBM bounds it)
 
 struct LShared {
   uint64_t full[LS];    // first CTA: both CTAs' boxes landed
@@ -149,6 +160,7 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
   const int m = sh.counted, mt = (m + 2 * LM - 1) / (2 * LM), nt = (args.cols + width - 1) / width;
   const int KB = (args.K + LK - 1) / LK, splits = MODE == kDx ? p.splits : 1;
   const int num_tiles = mt * nt * splits;
+  const int sum_unit = mt > 1 ? L_UNIT_KB : L_UNIT_FEW_KB;
   volatile int *abort = &sh.abort;
 
   if (warp == 0) {
@@ -212,27 +224,32 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
       const uint32_t b_lo = (uint32_t)b_desc, b_hi = (uint32_t)(b_desc >> 32);
       const uint32_t idesc =
           tc::idesc_bf16_f32(2 * LM, width) | (MODE == kDx ? tc::kIdescBMajorMN : 0u);
-      for (int t = pair; t < num_tiles && ok && !*abort; t += n_pairs, ++local) {
+      for (int t = pair; t < num_tiles && ok && !*abort; t += n_pairs) {
         const LTile tl = l_decode(t, mt, nt, KB, splits, width);
-        const int acc = local & 1;
-        if (!mbar_wait_cluster(&sh.tempty[acc], ((local >> 1) & 1) ^ 1u, abort)) break;
-        tc::tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * LN);
-        for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
-          if (!tc::mbar_wait(&sh.full[stage], phase, abort)) { ok = false; break; }
+        // (one loop with a test for a unit's start in it: 5 % slower)
+        const int unit = MODE == kSums ? sum_unit : tl.kb1 - tl.kb0;
+        for (int ku = tl.kb0; ku < tl.kb1; ku += unit, ++local) {
+          const int ke = min(tl.kb1, ku + unit);
+          if (!mbar_wait_cluster(&sh.tempty[local & 1], ((local >> 1) & 1) ^ 1u, abort)) ok = false;
+          if (!ok) break;
           tc::tc_fence_after();
-          // (low descriptor words: 16-byte units; 16 elements of a contiguous
-          // reduction are 32 bytes, 16 rows 2048)
-          const uint32_t at = (uint32_t)(stage * (L_STAGE / 16));
+          const uint32_t d_tmem = tmem_base + (uint32_t)((local & 1) * LN);
+          for (int kb = ku; kb < ke; ++kb) {
+            if (!tc::mbar_wait(&sh.full[stage], phase, abort)) { ok = false; break; }
+            tc::tc_fence_after();
+            // (low descriptor words: 16-byte units; 16 elements of a contiguous
+            // reduction are 32 bytes, 16 rows 2048)
+            const uint32_t at = (uint32_t)(stage * (L_STAGE / 16));
 #pragma unroll
-          for (int k = 0; k < LK / 16; ++k)
-            mma2_bf16_lo(d_tmem, a_lo + at + k * 2, a_hi, b_lo + at + k * (MODE == kDx ? 128 : 2),
-                         b_hi, idesc, (kb != tl.kb0 || k != 0) ? 1u : 0u);
-          mma2_commit_both(&sh.empty[stage]);
-          if (++stage == LS) { stage = 0; phase ^= 1u; }
+            for (int k = 0; k < LK / 16; ++k)
+              mma2_bf16_lo(d_tmem, a_lo + at + k * 2, a_hi, b_lo + at + k * (MODE == kDx ? 128 : 2),
+                           b_hi, idesc, (kb != ku || k != 0) ? 1u : 0u);
+            mma2_commit_both(&sh.empty[stage]);
+            if (++stage == LS) { stage = 0; phase ^= 1u; }
+          }
+          if (!ok) break;
+          mma2_commit_both(&sh.tfull[local & 1]);
         }
-        if (!ok) break;
-        mma2_commit_both(&sh.tfull[acc]);
       }
       if (*abort) {
         mma2_commit_self(&sh.drain);
@@ -246,12 +263,12 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
     const uint32_t tempty_first = map_to_rank(tc::smem_u32(&sh.tempty[0]), 0);
     uint8_t *stage_out = smem + LS * L_STAGE + (warp - 2) * L_OUT;
     int local = 0;
+    bool ok = true;
     for (int t = pair; t < num_tiles; t += n_pairs, ++local) {
       const LTile tl = l_decode(t, mt, nt, KB, splits, width);
       const int row = tl.row0 + (int)rank * LM + quarter * 32;   // this warp's first token
       const int j = row + lane;
       const bool there = j < m;
-      const int acc = local & 1;
       // this token's target, from the tile's first column on
       int target = -1;
       float lse = 0.f, scale = 0.f, dloss = 0.f;
@@ -259,28 +276,64 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
         target = p.target[j] - p.v0 - tl.col0;
         if (MODE == kGrad) {
           lse = p.lse[j];
-          dloss = p.dloss[j];
+          const float unit = *p.scale;
+          dloss = unit > 0.f ? p.dloss[j] / unit : 0.f;
           scale = dloss * fmaf(2.f * p.z_loss, lse, 1.f);
         }
       }
-      const bool ok = tc::mbar_wait(&sh.tfull[acc], (local >> 1) & 1, abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc::tc_fence_after();
+      // kSums: the logits of this warp's turns of 32 columns, unit by unit
+      constexpr int TURNS = MODE == kSums ? LN / 64 : 1;
+      float sum_of[TURNS][32];
+      if constexpr (MODE == kSums) {
+        for (int kb = tl.kb0; kb < tl.kb1; kb += sum_unit) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&sh.tfull[local & 1], (local >> 1) & 1, abort));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (row < m) {
+            const uint32_t tb = lane_base + (uint32_t)((local & 1) * LN);
+#pragma unroll
+            for (int q = 0; q < 2 * TURNS; ++q) {
+              const int c = part * 32 + (q >> 1) * 64;
+              if (c >= width) continue;
+              uint32_t a[16];
+              tc::tmem_ld16(tb + (uint32_t)(c + (q & 1) * 16), a);
+              tc::tmem_ld_wait();
+              float *to = sum_of[q >> 1] + (q & 1) * 16;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                to[i] = __uint_as_float(a[i]) + (kb == tl.kb0 ? 0.f : to[i]);
+            }
+          }
+          if (kb + sum_unit < tl.kb1) {   // (the last unit is released below)
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+              mbar_arrive_cluster(tempty_first + (uint32_t)((local & 1) * sizeof(uint64_t)));
+            ++local;
+          }
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sh.tfull[local & 1], (local >> 1) & 1, abort));
+        tc::tc_fence_after();
+      }
+      if (!ok) break;
+      const int acc = local & 1;
       const uint32_t tb = lane_base + (uint32_t)(acc * LN);
+      if constexpr (MODE == kSums) {
+        // the accumulator is drained: the MMAs go on while the sums are formed
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty_first + (uint32_t)(acc * sizeof(uint64_t)));
+      }
       if (row < m) {
         if constexpr (MODE == kSums) {
-          // running maximum and sum over this warp's turns of 32 columns
           float top = -INFINITY, sum = 0.f;
-#pragma unroll 1
-          for (int c = part * 32; c < width; c += 64) {
-            const int left = args.cols - tl.col0 - c;   // columns that there are
-            if (left <= 0) break;
-            uint32_t a[32];
-            tc::tmem_ld32(tb + (uint32_t)c, a);
-            tc::tmem_ld_wait();
-            float l[32], up = top;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) l[i] = __uint_as_float(a[i]);
+          for (int q = 0; q < TURNS; ++q) {
+            const int c = part * 32 + q * 64;
+            const int left = args.cols - tl.col0 - c;   // columns that there are
+            if (c >= width || left <= 0) continue;
+            float (&l)[32] = sum_of[q], up = top;
             if (left < 32) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -370,9 +423,11 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
           }
         }
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty_first + (uint32_t)(acc * sizeof(uint64_t)));
+      if constexpr (MODE != kSums) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty_first + (uint32_t)(acc * sizeof(uint64_t)));
+      }
     }
     if (MODE != kSums && lane == 0) tc::bulk_wait_all();
   }

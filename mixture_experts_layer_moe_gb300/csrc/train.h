@@ -125,6 +125,8 @@ struct GradProduct {
   const void *A, *B;
   void *out;                // [E][M][N]
   int a_f32;                // on the CUDA cores, for a bf16 layer: A is fp32
+  const float *scale;       // on the tensor cores: the sums are multiplied by *scale (nullptr: 1);
+                            // the first problem's holds for all of a launch
 };
 constexpr int kMaxGradProblems = 3;
 int grad_splits_simt(const GradProduct *p, int count);
@@ -143,6 +145,7 @@ bool gemm_grad_supported(const GradProduct &p);
 // fill the SMs (1: not cut), and the scratch that the partial sums take.  Both
 // go by the shapes alone.
 int grad_splits(const GradProduct *p, int count);
+int gemm_grad_splits(const GradProduct *p, int count);   // (whatever their size)
 size_t grad_scratch(const GradProduct *p, int count);
 // beside: 0, or the SM pairs that it takes so that the next launch, a b_rows
 // RowsProduct with `beside` pairs of its own that does not read its results,

@@ -478,7 +478,7 @@ class _Vectors:
         if unknown:
             raise ValueError(f"no vectors of a block joint: {sorted(unknown)}")
         self.tensors = {k: t for k, t in tensors.items() if t is not None}
-        kinds = {(t.numel(), t.dtype, t.device) for t in self.tensors.values()}
+        kinds = {(t.numel(), t.dtype, t.get_device()) for t in self.tensors.values()}
         if len(kinds) > 1:
             raise ValueError("the vectors of a block joint are of one length, type and device")
         self.d, self.dtype, self.device = kinds.pop() if kinds else (None, dtype, None)
@@ -486,11 +486,10 @@ class _Vectors:
             raise ValueError(f"these vectors of a block joint hold {dtype}")
         self.ref = ctypes.byref(struct(**{k: _ptr(t) for k, t in self.tensors.items()}))
 
-    def check(self, rows: torch.Tensor, dtype):
-        if self.tensors and (self.d != rows.shape[1] or self.dtype is not dtype
-                             or self.device != rows.device):
-            raise ValueError(f"the vectors of a block joint must hold {rows.shape[1]} values of "
-                             f"{dtype} on {rows.device}")
+    def check(self, d: int, dtype, device: int):
+        if self.tensors and (self.d != d or self.dtype is not dtype or self.device != device):
+            raise ValueError(f"the vectors of a block joint must hold {d} values of {dtype} on the "
+                             "rows' device")
 
 
 def make_join_params(vectors: dict) -> _Vectors:
@@ -505,17 +504,20 @@ def make_join_grads(vectors: dict) -> _Vectors:
     return _Vectors(moe_join_grads, vectors, torch.float32)
 
 
-def _step_rows(t: Optional[torch.Tensor], like: torch.Tensor) -> tuple[Optional[int], int]:
-    """(pointer, elements between rows) of rows shaped as `like`; None: (None, 0)."""
+def _step_rows(t: Optional[torch.Tensor], shape, dtype, device) -> tuple[Optional[int], int]:
+    """(pointer, elements between rows) of [rows, d] rows; None: (None, 0).  (The checks are a
+    good part of a small call's time.)"""
     if t is None:
         return None, 0
-    if t.shape != like.shape or t.dtype is not like.dtype or t.device != like.device:
-        raise ValueError(f"rows must be {list(like.shape)} of {like.dtype} on {like.device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"rows must be {list(shape)} of {dtype} on one device")
+    d = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), d
     ld, one = t.stride()
-    d = t.shape[1]
     if one != 1 and d > 1:
         raise ValueError("rows must be dense")
-    if t.shape[0] <= 1:
+    if shape[0] <= 1:
         return t.data_ptr(), d
     if ld < d:
         raise ValueError("rows must not overlap (an expanded tensor: .contiguous())")
@@ -529,26 +531,28 @@ def _step_dtype(x: torch.Tensor) -> int:
     return code
 
 
-def _fp32(t: Optional[torch.Tensor], shape, like: torch.Tensor) -> Optional[int]:
+def _fp32(t: Optional[torch.Tensor], shape, device) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.shape != shape or t.device != like.device:
-        raise ValueError(f"expected a float32 tensor of {list(shape)} on {like.device}")
+    if t.dtype is not torch.float32 or t.shape != shape or t.get_device() != device:
+        raise ValueError(f"expected a float32 tensor of {list(shape)} on the rows' device")
     return _ptr(t)
 
 
-def _rng(rng: Optional[torch.Tensor], like: torch.Tensor) -> Optional[int]:
+def _rng(rng: Optional[torch.Tensor], device) -> Optional[int]:
     """The generator's state: a device tensor of two 64-bit integers, seed and offset."""
     if rng is None:
         return None
-    if rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2 or rng.device != like.device:
-        raise ValueError(f"the generator's state is a tensor of two 64-bit integers on {like.device}")
+    if (rng.dtype is not torch.int64 and rng.dtype is not torch.uint64) or rng.numel() != 2 or \
+            rng.get_device() != device:
+        raise ValueError("the generator's state is a tensor of two 64-bit integers on the rows' "
+                         "device")
     return _ptr(rng)
 
 
-def _bytes(ws: torch.Tensor, like: torch.Tensor) -> tuple[int, int]:
-    if ws.dtype is not torch.uint8 or ws.device != like.device:
-        raise ValueError(f"a workspace is a uint8 tensor on {like.device}")
+def _bytes(ws: torch.Tensor, device) -> tuple[int, int]:
+    if ws.dtype is not torch.uint8 or ws.get_device() != device:
+        raise ValueError("a workspace is a uint8 tensor on the rows' device")
     return _ptr(ws), ws.numel()
 
 
@@ -561,12 +565,11 @@ def moe_dropout(x, y, p: float, rng=None, stream=None):
     """y = dropout of x [rows, d] (rows may lie apart; y may be x).  rng: device tensor of two
     64-bit integers (seed, offset), read when the kernel runs; the same state gives the same
     elements, so the gradient is this call on dy."""
-    code = _step_dtype(x)
-    n, d = x.shape
-    xp, ldx = _step_rows(x, x)
-    yp, ldy = _step_rows(y, x)
-    _check(_lib.moe_dropout(_dropout_config(n, ldx, ldy, d, code, p), xp, _rng(rng, x), yp,
-                            _stream(stream)), "moe_dropout")
+    code, shape, dtype, dev = _step_dtype(x), x.shape, x.dtype, x.get_device()
+    xp, ldx = _step_rows(x, shape, dtype, dev)
+    yp, ldy = _step_rows(y, shape, dtype, dev)
+    _check(_lib.moe_dropout(_dropout_config(shape[0], ldx, ldy, shape[1], code, p), xp,
+                            _rng(rng, dev), yp, _stream(stream)), "moe_dropout")
 
 
 @functools.lru_cache(maxsize=256)
@@ -580,16 +583,16 @@ def moe_block_join(x, b, params: _Vectors, r, y, stats, *, post="rms", pre="rms"
                    rng=None, eps=1e-5, stream=None):
     """r = scale x + gate . dropout(post(b)), y = pre(r); rows [rows, d] may lie apart.  params:
     make_join_params; y None when pre is "none"; stats fp32 [4, rows] or None."""
-    code = _step_dtype(x)
-    n, d = x.shape
-    xp, ldx = _step_rows(x, x)
-    bp, ldb = _step_rows(b, x)
-    rp, ldr = _step_rows(r, x)
-    yp, ldy = _step_rows(y, x)
-    params.check(x, x.dtype)
+    code, shape, dtype, dev = _step_dtype(x), x.shape, x.dtype, x.get_device()
+    n, d = shape
+    xp, ldx = _step_rows(x, shape, dtype, dev)
+    bp, ldb = _step_rows(b, shape, dtype, dev)
+    rp, ldr = _step_rows(r, shape, dtype, dev)
+    yp, ldy = _step_rows(y, shape, dtype, dev)
+    params.check(d, dtype, dev)
     _check(_lib.moe_block_join(
         _join_config(n, ldx, ldb, ldr, ldy, 0, 0, 0, 0, d, code, post, pre, eps, scale, p), xp, bp,
-        params.ref, _rng(rng, x), rp, yp, _fp32(stats, (4, n), x), _stream(stream)),
+        params.ref, _rng(rng, dev), rp, yp, _fp32(stats, (4, n), dev), _stream(stream)),
         "moe_block_join")
 
 
@@ -610,20 +613,20 @@ def moe_block_join_backward(b, r, stats, params: _Vectors, dr, dy, dx, db, grads
     like = next((t for t in (dr, dy, b) if t is not None), None)
     if like is None:
         raise ValueError("a block joint's gradient needs dr, dy or b")
-    code = _step_dtype(like)
-    n, d = like.shape
-    bp, ldb = _step_rows(b, like)
-    rp, ldr = _step_rows(r, like)
-    drp, lddr = _step_rows(dr, like)
-    dyp, lddy = _step_rows(dy, like)
-    dxp, lddx = _step_rows(dx, like)
-    dbp, lddb = _step_rows(db, like)
-    params.check(like, like.dtype)
-    grads.check(like, torch.float32)
+    code, shape, dtype, dev = _step_dtype(like), like.shape, like.dtype, like.get_device()
+    n, d = shape
+    bp, ldb = _step_rows(b, shape, dtype, dev)
+    rp, ldr = _step_rows(r, shape, dtype, dev)
+    drp, lddr = _step_rows(dr, shape, dtype, dev)
+    dyp, lddy = _step_rows(dy, shape, dtype, dev)
+    dxp, lddx = _step_rows(dx, shape, dtype, dev)
+    dbp, lddb = _step_rows(db, shape, dtype, dev)
+    params.check(d, dtype, dev)
+    grads.check(d, torch.float32, dev)
     _check(_lib.moe_block_join_backward(
         _join_config(n, 0, ldb, ldr, 0, lddx, lddb, lddr, lddy, d, code, post, pre, 0.0, scale, p),
-        bp, rp, _fp32(stats, (4, n), like), params.ref, _rng(rng, like), drp, dyp, dxp, dbp,
-        grads.ref, *_bytes(ws, like), _stream(stream)), "moe_block_join_backward")
+        bp, rp, _fp32(stats, (4, n), dev), params.ref, _rng(rng, dev), drp, dyp, dxp, dbp,
+        grads.ref, *_bytes(ws, dev), _stream(stream)), "moe_block_join_backward")
 
 
 @functools.lru_cache(maxsize=256)
@@ -632,13 +635,13 @@ def _loss_config(n, d, vocab, dtype, z_loss):
 
 
 def _loss_operands(x, W, targets, z_loss):
-    code = _step_dtype(x)
+    code, dev = _step_dtype(x), x.get_device()
     n, d = x.shape
-    if W.dim() != 2 or W.shape[1] != d or W.dtype is not x.dtype or W.device != x.device:
-        raise ValueError(f"W must be [vocab, {d}] of {x.dtype} on {x.device}")
-    if targets.shape != (n,) or targets.dtype is not torch.int32 or targets.device != x.device:
-        raise ValueError(f"targets must be [{n}] of int32 on {x.device}")
-    return (_loss_config(n, d, W.shape[0], code, z_loss), _ptr(x), _ptr(W), _ptr(targets)), n
+    if W.dim() != 2 or W.shape[1] != d or W.dtype is not x.dtype or W.get_device() != dev:
+        raise ValueError(f"W must be [vocab, {d}] of {x.dtype} on the rows' device")
+    if targets.shape != (n,) or targets.dtype is not torch.int32 or targets.get_device() != dev:
+        raise ValueError(f"targets must be [{n}] of int32 on the rows' device")
+    return (_loss_config(n, d, W.shape[0], code, z_loss), _ptr(x), _ptr(W), _ptr(targets)), n, dev
 
 
 def moe_cross_entropy_workspace_size(n: int, d: int, vocab: int, dtype: str) -> int:
@@ -663,20 +666,20 @@ def alloc_cross_entropy_workspace(n: int, d: int, vocab: int, dtype: str,
 def moe_cross_entropy(x, W, targets, loss, lse, ws, z_loss=0.0, stream=None):
     """loss, lse fp32 [n] of x [n, d] W [vocab, d]^T against targets int32 [n] (negative: left
     out); ws: moe_cross_entropy_workspace_size bytes (alloc_cross_entropy_workspace)."""
-    args, n = _loss_operands(x, W, targets, z_loss)
-    _check(_lib.moe_cross_entropy(*args, _fp32(loss, (n,), x), _fp32(lse, (n,), x),
-                                  *_bytes(ws, x), _stream(stream)), "moe_cross_entropy")
+    args, n, dev = _loss_operands(x, W, targets, z_loss)
+    _check(_lib.moe_cross_entropy(*args, _fp32(loss, (n,), dev), _fp32(lse, (n,), dev),
+                                  *_bytes(ws, dev), _stream(stream)), "moe_cross_entropy")
 
 
 def moe_cross_entropy_backward(x, W, targets, lse, dloss, dx, dW, ws, z_loss=0.0, stream=None):
     """dx, dW (either may be None) from dloss fp32 [n] and lse as moe_cross_entropy wrote it."""
-    args, n = _loss_operands(x, W, targets, z_loss)
+    args, n, dev = _loss_operands(x, W, targets, z_loss)
     for t, like in ((dx, x), (dW, W)):
         if t is not None and (t.shape != like.shape or t.dtype is not like.dtype
-                              or t.device != like.device):
+                              or t.get_device() != dev):
             raise ValueError("dx and dW are shaped and typed as x and W")
-    _check(_lib.moe_cross_entropy_backward(*args, _fp32(lse, (n,), x), _fp32(dloss, (n,), x),
-                                           _ptr(dx), _ptr(dW), *_bytes(ws, x), _stream(stream)),
+    _check(_lib.moe_cross_entropy_backward(*args, _fp32(lse, (n,), dev), _fp32(dloss, (n,), dev),
+                                           _ptr(dx), _ptr(dW), *_bytes(ws, dev), _stream(stream)),
            "moe_cross_entropy_backward")
 
 
