@@ -641,3 +641,281 @@ def test_the_layer_between_joints(lib):
         slope, want = (ends[0] - ends[1]) / (2 * h), (grad * step.double()).sum().item()
         # fp32 losses of about 4, off by some 2^-22, over 2 h; the third derivative times h^2 / 6
         assert abs(slope - want) <= 4 * 2 ** -20 / (2 * h) + 50 * h * h, (slope, want)
+
+
+# ------------------------------------------- large problems, against 64 bits on the GPU
+def _loss_reference(x, W, t, lse, dloss, z_loss, dtype, step=4096):
+    """loss, lse, dx, dW in float64 and their error bounds as in the tests above, over pieces of the
+    vocabulary."""
+    n, d = x.shape
+    V_, k, u = W.shape[0], 2 if dtype == "bf16" else 1, _u(dtype)
+    x64, ax = x.double(), x.double().abs()
+    t, counted = t.long(), (t >= 0)[:, None]
+    ls, dl_scale = lse.double()[:, None], torch.where(counted, dloss.double()[:, None], 0.0)
+    f64 = dict(dtype=torch.float64, device="cuda")
+    dx, ex, dW, eW = (torch.zeros(s, **f64) for s in ((n, d), (n, d), (V_, d), (V_, d)))
+    for v in range(0, V_, step):
+        Wp = W[v:v + step].double()
+        l = x64 @ Wp.T
+        el = k * d * V * (ax @ Wp.abs().T)
+        p = torch.exp(l - ls) * (1 + 2 * z_loss * ls).abs()
+        hot = torch.zeros_like(p)
+        here = torch.nonzero((t >= v) & (t < v + step))[:, 0]
+        hot[here, t[here] - v] = 1.0
+        dl = dl_scale * (p - hot)
+        e = dl_scale.abs() * (p * (el + el * el + 2 ** -20 + 2 ** -22 * (l - ls).abs() + 4 * V)
+                              + 5 * V * (p + hot))
+        e = e + u * (dl.abs() + e)
+        a = dl.abs() + e
+        dx += dl @ Wp
+        ex += (e + k * (V_ + 16) * V * a) @ Wp.abs()
+        dW[v:v + step] = dl.T @ x64
+        eW[v:v + step] = (e + k * (n + 16) * V * a).T @ ax
+    return dx, ex + u * (dx.abs() + ex), dW, eW + u * (dW.abs() + eW)
+
+
+def _close(got, want, bound, what):
+    _within(got, want.cpu(), bound.cpu(), what)
+
+
+# several pieces of the vocabulary: on the tensor cores, for few tokens, on the CUDA cores
+@pytest.mark.parametrize("n,d,vocab,dtype", [(2500, 64, 60001, "bf16"), (190, 8, 720001, "bf16"),
+                                             (3001, 8, 30001, "f32"), (5000, 16, 27777, "bf16")])
+def test_cross_entropy_in_pieces(lib, n, d, vocab, dtype):
+    x, W, t, left = _loss_case(n, d, vocab, dtype, 0.1, 7)
+    clean = torch.where(left[:, None], 0, x)
+    lse64 = torch.zeros(n, dtype=torch.float64, device="cuda")
+    top = torch.zeros_like(lse64)
+    for a in range(0, n, 256):
+        l = clean[a:a + 256].double() @ W.double().T
+        lse64[a:a + 256], top[a:a + 256] = torch.logsumexp(l, 1), l.amax(1)
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, dtype)
+    ws[256:] = 0xFF
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    lib.moe_cross_entropy(x, W, t, loss, lse, ws, 1e-3)
+    counted = t >= 0
+    # |l| <= sum |x| |W| <= |x| |W| (norms), the largest of the rows of W
+    el = 2 * d * V * clean.double().norm(dim=1) * W.double().norm(dim=1).max()
+    e = el + 2 ** -20 + 2 ** -22 * 20 + (64 + vocab / 8192) * V + 2 * V * (lse64.abs() + top.abs())
+    _close(lse, torch.where(counted, lse64, 0.0), torch.where(counted, e, 0.0), "lse")
+    dloss = _randn(_gen(3), n)
+    dx, dW = torch.full_like(x, float("nan")), torch.full_like(W, float("nan"))
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, dx, dW, ws, 1e-3)
+    _ok(lib, ws)
+    wdx, ex, wdW, eW = _loss_reference(clean, W, t, lse, dloss, 1e-3, dtype)
+    _close(dx, wdx, ex, "dx")
+    _close(dW, wdW, eW, "dW")
+    again = torch.empty_like(dx), torch.empty_like(dW)
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, again[0], None, ws, 1e-3)
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, None, again[1], ws, 1e-3)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dW)
+
+
+# counted tokens round the boxes that few tokens are cut into, with rows of NaN between
+@pytest.mark.parametrize("counted", [1, 15, 16, 17, 31, 32, 33, 64, 65, 96, 97, 127, 128, 129, 144, 160,
+                                     161, 191, 192])
+@pytest.mark.parametrize("d,vocab", [(328, 1300), (1032, 259)])
+def test_cross_entropy_backward_of_few_tokens(lib, counted, d, vocab):
+    x, W, t, _ = _loss_case(192, d, vocab, "bf16", 0.0, counted)
+    out = torch.randperm(192, generator=torch.Generator().manual_seed(counted))[counted:].cuda()
+    t[out], x[out] = -5, float("nan")
+    clean = x.clone()
+    clean[out] = 0
+    lse = torch.where(t >= 0, torch.logsumexp(clean.double() @ W.double().T, 1), 0.0).float()
+    dloss = _randn(_gen(counted), 192)
+    ws = lib.alloc_cross_entropy_workspace(192, d, vocab, "bf16")
+    ws[256:] = 0xFF
+    dx, dW = torch.full_like(x, float("nan")), torch.full_like(W, float("nan"))
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, dx, dW, ws)
+    _ok(lib, ws)
+    wdx, ex, wdW, eW = _loss_reference(clean, W, t, lse, dloss, 0.0, "bf16")
+    _close(dx, wdx, ex, "dx")
+    _close(dW, wdW, eW, "dW")
+    assert (dx[out] == 0).all()
+
+
+@pytest.mark.parametrize("n,d,vocab,dtype", [(50, 320, 1100, "bf16"), (400, 320, 1100, "bf16"),
+                                             (50, 64, 300, "f32")])
+def test_cross_entropy_backward_of_uneven_weights(lib, n, d, vocab, dtype):
+    """dloss of any size, zero and not finite: the result of a token goes by its own."""
+    x, W, t, _ = _loss_case(n, d, vocab, dtype, 0.0, 1)
+    lse = torch.logsumexp(x.double() @ W.double().T, 1).float()
+    dloss = _randn(_gen(9), n) * 10.0 ** torch.linspace(-18, 3, n, device="cuda")
+    dloss[5] = 0.0
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, dtype)
+    dx, dW = torch.empty_like(x), torch.empty_like(W)
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, dx, dW, ws)
+    wdx, ex, wdW, eW = _loss_reference(x, W, t, lse, dloss, 0.0, dtype)
+    _close(dx, wdx, ex, "dx")
+    _close(dW, wdW, eW, "dW")
+    assert (dx[5] == 0).all()
+    for bad in (float("nan"), float("inf")):
+        spoilt = dloss.clone()
+        spoilt[7] = bad
+        dx2 = torch.empty_like(x)
+        lib.moe_cross_entropy_backward(x, W, t, lse, spoilt, dx2, dW, ws)
+        others = torch.arange(n, device="cuda") != 7
+        assert torch.equal(dx2[others], dx[others]) and not torch.isfinite(dx2[7]).any()
+    lib.moe_cross_entropy_backward(x, W, t, lse, torch.zeros_like(dloss), dx, dW, ws)
+    assert (dx == 0).all() and (dW == 0).all()
+
+
+def test_calls_on_two_streams(lib):
+    """Two problems at once, each on a stream and in a workspace of its own; one workspace for
+    problems of several shapes in turn."""
+    cases = [_loss_case(300, 512, 5000, "bf16", 0.1, 1), _loss_case(120, 256, 9000, "bf16", 0.3, 2)]
+    size = max(lib.moe_cross_entropy_workspace_size(c[0].shape[0], c[0].shape[1], c[1].shape[0], "bf16")
+               for c in cases)
+
+    def call(c, ws):
+        x, W, t, _ = c
+        n = x.shape[0]
+        loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        dx, dW = torch.empty_like(x), torch.empty_like(W)
+        lib.moe_cross_entropy(x, W, t, loss, lse, ws)
+        lib.moe_cross_entropy_backward(x, W, t, lse, torch.ones_like(loss), dx, dW, ws)
+        return loss, lse, dx, dW
+
+    shared = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = [call(c, shared) for c in cases]
+    spaces = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for c, ws, s in zip(cases, spaces, streams):
+            with torch.cuda.stream(s):
+                got.append(call(c, ws))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            for p, q in zip(a, b):
+                assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [17, 40, 264, 1003, 5000])
+def test_join_rows_anywhere(lib, d, dtype):
+    """Rows at every distance from a vector's boundary, in tensors of different distances, give the
+    bits of dense rows."""
+    params, x, b, dr, dy, kw = _join_case(37, d, 0, dtype, "rms", "layer", True, 0.2, 0.5)
+    w = lib.make_join_params(params)
+    ws = torch.empty(lib.moe_block_join_workspace_size(37, d, dtype), dtype=torch.uint8, device="cuda")
+
+    def run(pads):
+        pad = iter(pads)
+        place = lambda t: _rows(t, next(pad))
+        out = lambda: _out(37, d, next(pad), dtype)
+        r, y, stats = out(), out(), torch.empty(4, 37, device="cuda")
+        lib.moe_block_join(place(x), place(b), w, r, y, stats, **kw)
+        grads = {k: torch.empty(d, device="cuda") for k in params}
+        dx, db = out(), out()
+        lib.moe_block_join_backward(place(b), r, stats, w, place(dr), place(dy), dx, db,
+                                    lib.make_join_grads(grads), ws, **kw)
+        return [r, y, stats, dx, db, *grads.values()]
+
+    want = run([1] * 9)
+    for shift in range(1, 16, 3):
+        got = run([(shift * (i + 1)) % 17 + 1 for i in range(9)])
+        for a, c in zip(want, got):
+            assert torch.equal(a, c)
+
+
+# ------------------------------------------------------- offsets past 32 bits
+def test_dropout_past_32_bits(lib):
+    rows = 2 ** 31 + 77
+    x = torch.ones(rows, 1, dtype=torch.bfloat16, device="cuda")
+    rng = _rng(21, 22)
+    lib.moe_dropout(x, x, 0.5, rng)
+    words = S.philox4x32_10((np.zeros(100, np.uint64), np.arange(rows - 100, rows).astype(np.uint64),
+                             22, 0), (21, 0))
+    keep = torch.from_numpy((words[0] & np.uint64(0xFFFF)) >= S.threshold(0.5))
+    assert torch.equal(x[-100:, 0].cpu().float(), torch.where(keep, 2.0, 0.0))
+
+
+def test_join_past_32_bits(lib):
+    """The last of rows that hold more than 2^32 elements (without dropout a row's result is its
+    own), and column sums over all of them."""
+    rows, d = 1_100_001, 4096
+    g = _gen(2)
+    v = _randn(g, d, dtype="bf16", std=0.2, mean=1.0)
+    w = lib.make_join_params(dict(post_gamma=v, pre_gamma=v))
+    kw = dict(post="rms", pre="rms")
+    tail = [_randn(g, 8, d, dtype="bf16") for _ in range(4)]
+    big = [torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for t, s in zip(big, tail):
+        t[-8:] = s
+    r, y = torch.empty_like(big[0]), torch.empty_like(big[0])
+    stats = torch.empty(4, rows, device="cuda")
+    lib.moe_block_join(*big, w, r, y, stats, **kw)
+    few = [torch.empty(8, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    few_stats = torch.empty(4, 8, device="cuda")
+    lib.moe_block_join(*tail[:2], w, *few, few_stats, **kw)
+    # few rows are summed by more threads, in another order: each order is off by at most
+    # (adds + 8) v relative for sums of squares, so the two by e; then r = x + z with |z| <= |r| + |x|,
+    # y = r gamma rstd, and each is rounded once on either side
+    e = 2 * (_adds(d) + 8) * V
+    near = lambda got, want, bound: ((got.double() - want.double()).abs() <= bound + TINY).all()
+    assert near(stats[:, -8:], few_stats, 2 * e * few_stats.abs())
+    u, ax = _u("bf16"), tail[0].double().abs()
+    assert near(r[-8:], few[0], 2 * u * few[0].double().abs() + 2 * e * (few[0].double().abs() + ax))
+    scale = v.double().abs() * few_stats[3].double()[:, None]
+    assert near(y[-8:], few[1], 2 * u * few[1].double().abs() + 8 * e * (few[1].double().abs() + scale * ax))
+    # (b is needed again; x and y make room for dy, dx and db)
+    dy = y.zero_()
+    dy[-8:] = tail[2]
+    dx, db = big[0], torch.empty_like(r)
+    grads = dict(pre_gamma=torch.empty(d, device="cuda"))
+    ws = torch.empty(lib.moe_block_join_workspace_size(rows, d, "bf16"), dtype=torch.uint8, device="cuda")
+    lib.moe_block_join_backward(big[1], r, stats, w, None, dy, dx, db, lib.make_join_grads(grads), ws, **kw)
+    few_dx, few_db = torch.empty_like(few[0]), torch.empty_like(few[0])
+    few_grads = dict(pre_gamma=torch.empty(d, device="cuda"))
+    few, few_stats = [r[-8:]], stats[:, -8:].contiguous()
+    lib.moe_block_join_backward(tail[1], few[0], few_stats, w, None, tail[2], few_dx, few_db,
+                                lib.make_join_grads(few_grads), ws, **kw)
+    assert torch.equal(dx[-8:], few_dx) and torch.equal(db[-8:], few_db)
+    # (the other rows add zeros; sums of 8 terms in another order)
+    a, b = grads["pre_gamma"], few_grads["pre_gamma"]
+    rh = (few[0].double() * few_stats[3].double()[:, None])
+    assert ((a - b).abs() <= 16 * V * (tail[2].double() * rh).abs().sum(0) + TINY).all()
+
+
+@pytest.mark.parametrize("n,d,vocab", [(5, 4096, 600_000), (600_000, 4096, 40)])
+def test_cross_entropy_past_32_bits(lib, n, d, vocab):
+    """More than 2^31 elements in W, or in x."""
+    g = _gen(4)
+    W = torch.randn(vocab, d, dtype=torch.bfloat16, generator=g, device="cuda") * 0.02
+    x = torch.randn(n, d, dtype=torch.bfloat16, generator=g, device="cuda")
+    t = torch.randint(vocab, (n,), generator=g, device="cuda").to(torch.int32)
+    t[-1], t[0] = vocab - 1, -1
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, "bf16")
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    lib.moe_cross_entropy(x, W, t, loss, lse, ws)
+    dloss = torch.full((n,), 1.0 / n, device="cuda")
+    dx, dW = torch.empty_like(x), torch.empty_like(W)
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, dx, dW, ws)
+    _ok(lib, ws)
+    # the last tokens, and the last entries of the vocabulary
+    k, m = min(n, 5), min(vocab, 40)
+    l = x[-k:].double() @ W.double().T if vocab * d < 2 ** 31 else torch.cat(
+        [x[-k:].double() @ W[v:v + 65536].double().T for v in range(0, vocab, 65536)], 1)
+    counted = t[-k:] >= 0
+    wlse = torch.where(counted, torch.logsumexp(l, 1), 0.0)
+    bound = 2 * d * V * x[-k:].double().norm(dim=1) * W[:1000].double().norm(dim=1).max() * 1.2 + 1e-4
+    assert ((lse[-k:].double() - wlse).abs() <= bound).all()
+    p = torch.exp(l - wlse[:, None])
+    p[torch.arange(k, device="cuda"), t[-k:].long().clamp(min=0)] -= 1
+    p = torch.where(counted[:, None], p / n, 0.0)
+    wdx = sum(p[:, v:v + 65536] @ W[v:v + 65536].double() for v in range(0, vocab, 65536))
+    # norms: dl and the result rounded to bf16 (2^-8 at most each), fp32 sums far below
+    for got, want in ((dx[-k:], wdx),):
+        assert ((got.double() - want).norm(dim=1) <= 2.2 * 2 ** -8 * want.norm(dim=1) + 1e-30).all()
+    pm = torch.zeros(n, m, dtype=torch.float64, device="cuda")
+    for a in range(0, n, 65536):
+        ls = lse[a:a + 65536].double()[:, None]
+        q = torch.exp(x[a:a + 65536].double() @ W[-m:].double().T - ls)
+        tt = t[a:a + 65536].long() - (vocab - m)
+        hot = torch.nonzero(tt >= 0)[:, 0]
+        q[hot, tt[hot]] -= 1
+        pm[a:a + 65536] = torch.where((t[a:a + 65536] >= 0)[:, None], q / n, 0.0)
+    wdW = sum(pm[a:a + 65536].T @ x[a:a + 65536].double() for a in range(0, n, 65536))
+    assert (dW[-m:].double() - wdW).norm() <= 2.2 * 2 ** -8 * wdW.norm()
