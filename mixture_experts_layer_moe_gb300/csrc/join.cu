@@ -142,8 +142,8 @@ join_kernel(const __grid_constant__ Fwd<T> a, const __grid_constant__ FwdSteps b
   for (int64_t r0 = (int64_t)blockIdx.x * groups * R; r0 < c.rows; r0 += by.rows) {
     // (the stage being filled was read in the iteration before, by this thread or its warp)
     if (ODD) __syncwarp();
-    fill(next);
-    copies_wait(stages - 1);
+    if (stages == 1) fill(next);
+    copies_wait(stages - 2);
     auto there = [&](int k, int n) { return active[n] && row + k < c.rows; };
     if (ODD) {
       __syncwarp();
@@ -178,6 +178,8 @@ join_kernel(const __grid_constant__ Fwd<T> a, const __grid_constant__ FwdSteps b
         }
       }
     }
+    // (here, and not before the loads above: the copies' instructions would delay them)
+    if (stages > 1) fill(next);
     if (layer1) {
       sums(s);
 #pragma unroll

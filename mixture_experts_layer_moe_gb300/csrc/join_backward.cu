@@ -162,10 +162,10 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
     const bool live = row < c.rows;
     // (the stage being filled was read in the iteration before, by this thread or its warp)
     if (ODD) __syncwarp();
-    fill(next);
+    if (stages == 1) fill(next);
     const float4 stat = next_stat;
     if (row + by.rows < c.rows) next_stat = stats_of<T, CENTRED>(a, row + by.rows);
-    copies_wait(stages - 1);
+    copies_wait(stages - 2);
     if (ODD) {
       __syncwarp();
       auto head = [&](const T *p, int64_t ld) {
@@ -206,6 +206,7 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
           s2 = fma2(w, rc.v[h], s2);
         }
       }
+      if (stages > 1) fill(next);
       if (CENTRED) {
         const float2 t = row_sum2(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
         e2 = layer2 ? -stat.w * t.x * inv_d : 0.f;
@@ -214,6 +215,7 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
         c2 = -stat.w * stat.w * stat.w * row_sum(s2.x + s2.y, buf, turn, warps) * inv_d;
       }
     }
+    if (stages > 1 && !has_dy) fill(next);
     Block8 w[NB];
     float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
