@@ -16,6 +16,8 @@ namespace moe {
 namespace {
 
 constexpr int D_THREADS = 256;
+// Rows this wide at least go by pieces (16384 x 1001: 27 us so, 25 by elements).
+constexpr int D_PIECES = 2048;
 
 // A block of eight elements as 16-byte vectors.
 template <typename T>
@@ -99,6 +101,64 @@ __global__ void __launch_bounds__(D_THREADS) dropout_kernel(const __grid_constan
   }
 }
 
+// bf16 rows anywhere whose elements lie alike in x and y (a row starts h elements into
+// an aligned piece of eight in both): by pieces.  Lanes 1-31 of a warp take 31
+// neighbouring pieces; a piece's elements are the last h of one block and the first 8
+// - h of the next, whose masks the lane and the one before it make.  (16383 x 7167 141 us
+// by single elements, 107 so.)
+__global__ void __launch_bounds__(D_THREADS)
+dropout_pieces_kernel(const __grid_constant__ DropArgs a, const __nv_bfloat16 *x, __nv_bfloat16 *y) {
+  using T = __nv_bfloat16;
+  const moe_dropout_config &c = a.c;
+  const RngState st = load_state(a.threshold ? a.rng : nullptr);
+  const int lane = threadIdx.x & 31;
+  const int64_t start = (int64_t)blockIdx.x * (D_THREADS / 32) + (threadIdx.x >> 5);
+  int64_t r = start / a.blocks;   // (here blocks of 31 pieces, one per warp)
+  int k = (int)(start - r * a.blocks);
+  constexpr int U = 2;
+  while (r < c.rows) {
+    uint4 v[U];
+    int64_t at[U];
+    int piece[U], e0[U], h[U];
+    bool whole[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      at[u] = r;
+      const T *row = x + r * c.ldx;
+      h[u] = (int)(reinterpret_cast<uintptr_t>(row) & 15) / 2;
+      piece[u] = 31 * k + lane - 1;
+      e0[u] = piece[u] * 8 - h[u];
+      whole[u] = r < c.rows && lane > 0 && e0[u] >= 0 && e0[u] + 8 <= c.d;
+      if (whole[u]) v[u] = *reinterpret_cast<const uint4 *>(row + e0[u]);
+      r += a.step_rows;
+      k += a.step_blocks;
+      if (k >= a.blocks) {
+        k -= a.blocks;
+        ++r;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (at[u] >= c.rows) break;
+      const uint32_t own = dropout_keep(st, max(piece[u], 0), (uint32_t)at[u], a.threshold);
+      const uint32_t before = __shfl_up_sync(0xffffffffu, own, 1);
+      const uint32_t keep = (before | own << 8) >> (8 - h[u]);
+      T *to = y + at[u] * c.ldy + e0[u];
+      if (whole[u]) {
+        float f[8];
+        unpack16<T>(v[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = keep >> i & 1 ? f[i] * a.factor : 0.f;
+        *reinterpret_cast<uint4 *>(to) = pack16<T>(f);
+      } else if (lane > 0) {
+        const T *from = x + at[u] * c.ldx + e0[u];
+        for (int i = max(0, -e0[u]); i < min(8, c.d - e0[u]); ++i)
+          to[i] = Elem<T>::from_f(keep >> i & 1 ? Elem<T>::load(from + i) * a.factor : 0.f);
+      }
+    }
+  }
+}
+
 // Rows anywhere: a warp takes 256 columns of a row, a lane makes the mask of a
 // block, and the elements go by lanes.
 template <typename T>
@@ -143,13 +203,18 @@ cudaError_t launch(const moe_dropout_config &c, int threshold, const T *x, const
   constexpr int E = Vec16<T>::N;
   DropArgs a{c, rng, threshold, 0, dropout_factor(threshold), 0, 0};
   const bool vectors = c.rows == 1 || (c.ldx % E == 0 && c.ldy % E == 0);
-  a.blocks = vectors ? (c.d + 7) / 8 : (c.d + 255) / 256;
+  const bool pieces =
+      !vectors && sizeof(T) == 2 && (c.ldx - c.ldy) % 8 == 0 && c.d >= D_PIECES;
+  a.blocks = vectors ? (c.d + 7) / 8 : pieces ? ((c.d + 14) / 8 + 30) / 31 : (c.d + 255) / 256;
   const int per = vectors ? D_THREADS : D_THREADS / 32;
   const int64_t want = (c.rows * a.blocks + per - 1) / per, most = (int64_t)num_sms() * 8;
   const int64_t grid = want < most ? want : most;
   a.step_rows = grid * per / a.blocks;
   a.step_blocks = (int)(grid * per - a.step_rows * a.blocks);
   if (vectors) dropout_kernel<T, U><<<(unsigned)grid, D_THREADS, 0, s>>>(a, x, y);
+  else if (pieces)
+    dropout_pieces_kernel<<<(unsigned)grid, D_THREADS, 0, s>>>(a, (const __nv_bfloat16 *)x,
+                                                               (__nv_bfloat16 *)y);
   else dropout_odd_kernel<T><<<(unsigned)grid, D_THREADS, 0, s>>>(a, x, y);
   return cudaGetLastError();
 }

@@ -919,3 +919,20 @@ def test_cross_entropy_past_32_bits(lib, n, d, vocab):
         pm[a:a + 65536] = torch.where((t[a:a + 65536] >= 0)[:, None], q / n, 0.0)
     wdW = sum(pm[a:a + 65536].T @ x[a:a + 65536].double() for a in range(0, n, 65536))
     assert (dW[-m:].double() - wdW).norm() <= 2.2 * 2 ** -8 * wdW.norm()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d", [(29, 2051), (7, 4099), (33, 2048), (5, 250)])
+def test_dropout_rows_anywhere(lib, rows, d, dtype):
+    """Rows at every distance from a vector's boundary, alike in x and y and not, give the bits of
+    dense rows."""
+    g = _gen(d)
+    x, rng = _randn(g, rows, d, dtype=dtype), _rng(77, 78)
+    want = torch.empty_like(x)
+    lib.moe_dropout(x, want, 0.4, rng)
+    assert torch.equal(want.cpu() == 0, S.dropout(x, rng, 0.4) == 0)
+    for pad in range(1, 9):
+        for other in (pad, pad + 8, pad + 3):
+            y = _out(rows, d, other, dtype)
+            lib.moe_dropout(_rows(x, pad), y, 0.4, rng)
+            assert torch.equal(y, want) and _gaps_stay(y, other)
