@@ -1,6 +1,6 @@
 /*
  * moe.h - C ABI of the GB300 (sm_103a) Mixture-of-Experts layer: the forward
- * pass, and the gradients that train it.
+ * pass, the gradients that train it, and what stands round it in a training step.
  *
  * The layer, as "How Mixture of Experts Scales Model Parameters" states it:
  *   X (n x d) -> router: one d x E linear layer, softmax per row
@@ -602,9 +602,9 @@ moe_status moe_cross_entropy(const moe_loss_config *cfg, const void *x, const vo
  *   dl_j = dloss * (e^{l_j - lse} (1 + 2 z_loss lse) - [j = v]),
  *   dx = dl W,   dW = dl^T x.
  * dx [n][d], dW [vocab][d], each may be NULL.  Rows of dx of left out tokens are
- * zero, and these tokens add nothing to dW.  bf16: dl is rounded once to bf16
- * where it is a tensor-core operand (small problems, on the CUDA cores, keep it
- * in fp32). */
+ * zero, and these tokens add nothing to dW.  bf16: dl, divided by the largest
+ * finite |dloss|, is rounded once to bf16 where it is a tensor-core operand (small
+ * problems, on the CUDA cores, keep it in fp32). */
 moe_status moe_cross_entropy_backward(const moe_loss_config *cfg, const void *x, const void *W,
                                       const int32_t *targets, const float *lse,
                                       const float *dloss, void *dx, void *dW, void *ws,
