@@ -524,11 +524,15 @@ def _step_rows(t: Optional[torch.Tensor], shape, dtype, device) -> tuple[Optiona
     return t.data_ptr(), ld
 
 
-def _step_dtype(x: torch.Tensor) -> int:
+def _step_dtype(x: torch.Tensor) -> tuple[int, int]:
+    """(moe_dtype of the rows, their device)."""
     code = _NORM_DTYPE.get(x.dtype)
     if code is None or x.dim() != 2:
         raise ValueError("rows must be a [rows, d] tensor of float32 or bfloat16")
-    return code
+    dev = x.get_device()
+    if dev >= 0 and dev != torch.cuda.current_device():
+        raise ValueError("the tensors must lie on the current device")
+    return code, dev
 
 
 def _fp32(t: Optional[torch.Tensor], shape, device) -> Optional[int]:
@@ -565,7 +569,8 @@ def moe_dropout(x, y, p: float, rng=None, stream=None):
     """y = dropout of x [rows, d] (rows may lie apart; y may be x).  rng: device tensor of two
     64-bit integers (seed, offset), read when the kernel runs; the same state gives the same
     elements, so the gradient is this call on dy."""
-    code, shape, dtype, dev = _step_dtype(x), x.shape, x.dtype, x.get_device()
+    code, dev = _step_dtype(x)
+    shape, dtype = x.shape, x.dtype
     xp, ldx = _step_rows(x, shape, dtype, dev)
     yp, ldy = _step_rows(y, shape, dtype, dev)
     _check(_lib.moe_dropout(_dropout_config(shape[0], ldx, ldy, shape[1], code, p), xp,
@@ -583,7 +588,8 @@ def moe_block_join(x, b, params: _Vectors, r, y, stats, *, post="rms", pre="rms"
                    rng=None, eps=1e-5, stream=None):
     """r = scale x + gate . dropout(post(b)), y = pre(r); rows [rows, d] may lie apart.  params:
     make_join_params; y None when pre is "none"; stats fp32 [4, rows] or None."""
-    code, shape, dtype, dev = _step_dtype(x), x.shape, x.dtype, x.get_device()
+    code, dev = _step_dtype(x)
+    shape, dtype = x.shape, x.dtype
     n, d = shape
     xp, ldx = _step_rows(x, shape, dtype, dev)
     bp, ldb = _step_rows(b, shape, dtype, dev)
@@ -613,7 +619,8 @@ def moe_block_join_backward(b, r, stats, params: _Vectors, dr, dy, dx, db, grads
     like = next((t for t in (dr, dy, b) if t is not None), None)
     if like is None:
         raise ValueError("a block joint's gradient needs dr, dy or b")
-    code, shape, dtype, dev = _step_dtype(like), like.shape, like.dtype, like.get_device()
+    code, dev = _step_dtype(like)
+    shape, dtype = like.shape, like.dtype
     n, d = shape
     bp, ldb = _step_rows(b, shape, dtype, dev)
     rp, ldr = _step_rows(r, shape, dtype, dev)
@@ -635,7 +642,7 @@ def _loss_config(n, d, vocab, dtype, z_loss):
 
 
 def _loss_operands(x, W, targets, z_loss):
-    code, dev = _step_dtype(x), x.get_device()
+    code, dev = _step_dtype(x)
     n, d = x.shape
     if W.dim() != 2 or W.shape[1] != d or W.dtype is not x.dtype or W.get_device() != dev:
         raise ValueError(f"W must be [vocab, {d}] of {x.dtype} on the rows' device")

@@ -936,3 +936,18 @@ def test_dropout_rows_anywhere(lib, rows, d, dtype):
             y = _out(rows, d, other, dtype)
             lib.moe_dropout(_rows(x, pad), y, 0.4, rng)
             assert torch.equal(y, want) and _gaps_stay(y, other)
+
+
+def test_tensors_of_another_device_are_refused(lib, monkeypatch):
+    x, t = torch.zeros(4, 64, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    f, ws = torch.zeros(4, device="cuda"), torch.zeros(1024, dtype=torch.uint8, device="cuda")
+    v, none = lib.make_join_params({}), lib.make_join_grads({})
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: lib.moe_dropout(x, x, 0.0),
+                 lambda: lib.moe_block_join(x, x, v, x, None, None, post="none", pre="none"),
+                 lambda: lib.moe_block_join_backward(x, None, None, v, x, None, x, x, none, ws,
+                                                     post="none", pre="none"),
+                 lambda: lib.moe_cross_entropy(x, x, t, f, f, ws),
+                 lambda: lib.moe_cross_entropy_backward(x, x, t, f, f, x, x, ws)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
