@@ -572,8 +572,8 @@ moe_status moe_block_join_backward(const moe_join_config *cfg, const void *b, co
 /* Softmax cross entropy of a linear layer over a vocabulary. */
 typedef struct {
   int32_t n;           /* tokens, 0 .. 1048576 (else MOE_ERR_UNSUPPORTED) */
-  int32_t d;           /* a multiple of 4 (f32) or 8 (bf16), else MOE_ERR_UNSUPPORTED */
-  int32_t vocab;       /* 1 .. 16777216, of any size in between */
+  int32_t d;           /* 4 .. 65536, a multiple of 4 (f32) or 8 (bf16), likewise */
+  int32_t vocab;       /* 1 .. 16777216, any number in between, likewise */
   int32_t dtype;       /* MOE_F32 or MOE_BF16: x, W and their gradients */
   float z_loss;        /* finite, >= 0 */
   int32_t reserved;    /* 0 */
@@ -589,8 +589,8 @@ moe_status moe_cross_entropy_workspace_size(const moe_loss_config *cfg, size_t *
 /* Per token t with target v = targets[t]:
  *   l = x[t] W^T,   lse = log sum_j e^{l_j},   loss = lse - l_v + z_loss * lse^2.
  * x [n][d], W [vocab][d]; targets int32 [n]; loss, lse fp32 [n].  A negative
- * target leaves its token out: loss and lse are 0, and whatever its row of x
- * holds is not read.  A target >= vocab sets MOE_ERR_BAD_INDEX (detail: the
+ * target leaves its token out: loss and lse are 0, whatever its row of x
+ * holds.  A target >= vocab sets MOE_ERR_BAD_INDEX (detail: the
  * token); the outputs are then not valid.  The logits are never stored as a
  * whole. */
 moe_status moe_cross_entropy(const moe_loss_config *cfg, const void *x, const void *W,

@@ -172,7 +172,7 @@ struct PackArgs {
 constexpr int PACK_THREADS = 256;
 // A CTA takes `per` tokens; how many count before them it finds for itself.
 __global__ void __launch_bounds__(PACK_THREADS) loss_pack_kernel(const __grid_constant__ PackArgs a) {
-  __shared__ int failed, before, part[PACK_THREADS / 32];
+  __shared__ int failed, part[PACK_THREADS / 32];
   __shared__ float largest[PACK_THREADS / 32];
   __shared__ int place[32];   // counted: its position; left out: -1 - the row that it leaves zero
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

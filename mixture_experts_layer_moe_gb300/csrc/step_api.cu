@@ -12,7 +12,7 @@ namespace moe {
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 32;   // (a row's index is 32 bits of the counter)
-constexpr int kMaxTokens = 1 << 20, kMaxVocab = 1 << 24;
+constexpr int kMaxTokens = 1 << 20, kMaxVocab = 1 << 24, kMaxWidth = 1 << 16;   // of the loss
 
 bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
 
@@ -70,7 +70,7 @@ moe_status check_loss(const moe_loss_config *c) {
     return MOE_ERR_INVALID_ARG;
   if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if (!(c->z_loss >= 0.f) || !isfinite(c->z_loss)) return MOE_ERR_INVALID_ARG;
-  if (c->n > kMaxTokens || c->vocab > kMaxVocab) return MOE_ERR_UNSUPPORTED;
+  if (c->n > kMaxTokens || c->vocab > kMaxVocab || c->d > kMaxWidth) return MOE_ERR_UNSUPPORTED;
   return c->d % (c->dtype == MOE_F32 ? 4 : 8) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 

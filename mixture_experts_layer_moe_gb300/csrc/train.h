@@ -63,10 +63,9 @@ enum {
 struct LossTerms {
   const int32_t *target;
   int v0;
-  // kRowsLossSums: sums [tokens][chunks], of one tile of entries each from chunk0 on;
-  // the target's logit
+  // kRowsLossSums: sums [tokens][chunks], of one tile of entries each; the target's logit
   float2 *sums;
-  int chunks, chunk0;
+  int chunks;
   float *at;
   // kRowsLossGrad: tokens from range[1] on do not count
   const int32_t *range;

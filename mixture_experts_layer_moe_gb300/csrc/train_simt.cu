@@ -246,7 +246,7 @@ __device__ __forceinline__ void loss_sums(const RowsProduct &p, const float2 (&a
 #pragma unroll
   for (int i = 0; i < PARTS; ++i)
     sum += sums[col * LD + i] * expf(tops[col * LD + i] - (top == -INFINITY ? 0.f : top));
-  t.sums[(int64_t)token * t.chunks + t.chunk0 + blockIdx.x] = make_float2(top, sum);
+  t.sums[(int64_t)token * t.chunks + blockIdx.x] = make_float2(top, sum);
 }
 
 // Steps of a product, with the next step's loads in flight: load(step) fills the

@@ -129,6 +129,7 @@ def _loss_back(moe, x=FAKE, W=FAKE, t=FAKE, lse=FAKE, loss=FAKE, dx=FAKE, dW=FAK
 LOSS = [
     (dict(n=-1), INVALID), (dict(n=2 ** 20 + 1), UNSUPPORTED), (dict(d=0), INVALID),
     (dict(d=60), UNSUPPORTED), (dict(d=66, dtype=0), UNSUPPORTED), (dict(vocab=0), INVALID),
+    (dict(d=65544), UNSUPPORTED),
     (dict(vocab=2 ** 24 + 1), UNSUPPORTED), (dict(dtype=2), INVALID), (dict(reserved=1), INVALID),
     (dict(z_loss=-1.0), INVALID), (dict(z_loss=float("nan")), INVALID),
     (dict(z_loss=float("inf")), INVALID), (dict(x=None), INVALID), (dict(x=FAKE + 8), INVALID),
