@@ -494,9 +494,9 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
  *   the kernel runs (a captured graph follows its contents); may be NULL when
  *   T = 0.  y may be x itself (with ldy = ldx). */
 typedef struct {
-  int64_t rows;        /* 0 .. 2^32 */
+  int64_t rows;        /* 0 .. 2^32 (else MOE_ERR_UNSUPPORTED) */
   int64_t ldx, ldy;    /* as moe_norm_config's: elements between rows, 0 for d */
-  int32_t d;           /* >= 1 */
+  int32_t d;           /* 1 .. 2^30, likewise */
   int32_t dtype;       /* MOE_F32 or MOE_BF16 */
   float p;             /* 0 <= p, and T < 65536 */
   int32_t reserved;    /* 0 */
@@ -509,10 +509,10 @@ moe_status moe_dropout(const moe_dropout_config *cfg, const void *x, const uint6
 typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
 
 typedef struct {
-  int64_t rows;              /* 0 .. 2^32 */
+  int64_t rows;              /* 0 .. 2^32 (else MOE_ERR_UNSUPPORTED) */
   int64_t ldx, ldb, ldr, ldy;          /* as moe_norm_config's, of x, b, r, y */
   int64_t lddx, lddb, lddr, lddy;      /* of their gradients */
-  int32_t d;                 /* >= 1 */
+  int32_t d;                 /* 1 .. 2^30, likewise */
   int32_t dtype;             /* MOE_F32 or MOE_BF16: rows, gate, gammas, betas */
   int32_t post, pre;         /* moe_norm_kind */
   float eps;                 /* >= 0, of both norms */

@@ -12,6 +12,7 @@ namespace moe {
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 32;   // (a row's index is 32 bits of the counter)
+constexpr int kMaxD = 1 << 30;                   // (columns are counted in int, rounded up)
 constexpr int kMaxTokens = 1 << 20, kMaxVocab = 1 << 24, kMaxWidth = 1 << 16;   // of the loss
 
 bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
@@ -19,7 +20,7 @@ bool ok_or_null(const void *p) { return p == nullptr || aligned(p, 16); }
 moe_status check_rows(int64_t rows, int32_t d, int32_t dtype, int32_t reserved) {
   if (rows < 0 || d < 1 || reserved != 0) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-  return rows > kMaxRows ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return rows > kMaxRows || d > kMaxD ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 // A leading dimension: 0 stands for d.

@@ -25,6 +25,7 @@ def _dropout(moe, x=FAKE, rng=FAKE, y=FAKE, **kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), INVALID), (dict(rows=2 ** 32 + 1), UNSUPPORTED), (dict(d=0), INVALID),
+    (dict(d=2 ** 30 + 1), UNSUPPORTED), (dict(d=2 ** 31 - 1), UNSUPPORTED),
     (dict(dtype=2), INVALID), (dict(reserved=1), INVALID), (dict(p=-0.1), INVALID),
     (dict(p=1.0), INVALID), (dict(p=0.999999), INVALID), (dict(p=float("nan")), INVALID),
     (dict(ldx=63), INVALID), (dict(ldy=1), INVALID), (dict(ldx=2 ** 62), INVALID),
@@ -55,6 +56,7 @@ def _join(moe, x=FAKE, b=FAKE, rng=None, r=2 * FAKE, y=FAKE, stats=None, vectors
 
 JOIN_CONFIGS = [
     (dict(rows=-1), INVALID), (dict(rows=2 ** 32 + 1), UNSUPPORTED), (dict(d=0), INVALID),
+    (dict(d=2 ** 30 + 1), UNSUPPORTED), (dict(d=2 ** 31 - 1), UNSUPPORTED),
     (dict(dtype=2), INVALID), (dict(reserved=1), INVALID), (dict(post=3), INVALID),
     (dict(pre=-1), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
     (dict(eps=float("inf")), INVALID), (dict(scale=float("nan")), INVALID),
