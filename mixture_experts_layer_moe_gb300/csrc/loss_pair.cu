@@ -277,7 +277,8 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
         if (MODE == kGrad) {
           lse = p.lse[j];
           const float unit = *p.scale;
-          dloss = unit > 0.f ? p.dloss[j] / unit : 0.f;
+          // (unit 0: what there is is zero or not finite, and stays so times it)
+          dloss = unit > 0.f ? p.dloss[j] / unit : p.dloss[j];
           scale = dloss * fmaf(2.f * p.z_loss, lse, 1.f);
         }
       }

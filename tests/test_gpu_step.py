@@ -951,3 +951,25 @@ def test_tensors_of_another_device_are_refused(lib, monkeypatch):
                  lambda: lib.moe_cross_entropy_backward(x, x, t, f, f, x, x, ws)):
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+@pytest.mark.parametrize("n,d,vocab,dtype", [(1, 512, 5000, "bf16"), (50, 320, 1100, "bf16"),
+                                             (400, 320, 1100, "bf16"), (50, 64, 300, "bf16"),
+                                             (50, 64, 300, "f32")])
+def test_cross_entropy_backward_of_no_finite_weight(lib, n, d, vocab, dtype):
+    """A step gone wrong shows in the gradient: no finite dloss leaves no finite gradient."""
+    x, W, t, _ = _loss_case(n, d, vocab, dtype, 0.0, 3)
+    lse = torch.logsumexp(x.double() @ W.double().T, 1).float()
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, dtype)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        dx, dW = torch.zeros_like(x), torch.zeros_like(W)
+        lib.moe_cross_entropy_backward(x, W, t, lse, torch.full_like(lse, bad), dx, dW, ws)
+        _ok(lib, ws)
+        assert not torch.isfinite(dx).any() and not torch.isfinite(dW).any()
+    # beside tokens of weight zero, whose rows stay zero
+    weights = torch.zeros_like(lse)
+    weights[n // 2] = float("nan")
+    dx = torch.zeros_like(x)
+    lib.moe_cross_entropy_backward(x, W, t, lse, weights, dx, None, ws)
+    others = torch.arange(n, device="cuda") != n // 2
+    assert (dx[others] == 0).all() and not torch.isfinite(dx[n // 2]).any()
