@@ -366,10 +366,13 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
           for (int c = part * 64; c < width; c += 128) {
             const int left = args.cols - tl.col0 - c;
             if (left <= 0) break;
+            // (the last turn of an odd number of 32 columns)
+            const bool narrow = width - c < 64;
             if (lane == 0) tc::bulk_wait_read<0>();   // the store before has read the buffer
             __syncwarp();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+              if (half == 1 && narrow) break;
               uint32_t a[32];
               tc::tmem_ld32(tb + (uint32_t)(c + 32 * half), a);
               tc::tmem_ld_wait();
@@ -391,12 +394,18 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const float *v = g + q * 8;
-                *reinterpret_cast<uint4 *>(stage_out + lane * 128 +
-                                           (((half * 4 + q) ^ (lane & 7)) << 4)) =
-                    make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                               pack_bf16(v[6], v[7]));
+                const uint4 w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                           pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+                const int col = tl.col0 + c + q * 8;
+                if (!narrow)
+                  *reinterpret_cast<uint4 *>(stage_out + lane * 128 +
+                                             (((half * 4 + q) ^ (lane & 7)) << 4)) = w;
+                else if (j < p.n && col < p.pitch)   // (pitch: whole vectors)
+                  *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.dl) +
+                                             (int64_t)j * p.pitch + col) = w;
               }
             }
+            if (narrow) break;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) tc::tma_store_3d(&maps.out, stage_out, tl.col0 + c, row, 0);
@@ -549,13 +558,8 @@ cudaError_t launch_loss_sums(const LossProduct &p, int *status, cudaStream_t s) 
 }
 
 cudaError_t launch_loss_logit_grad(const LossProduct &p, int *status, cudaStream_t s) {
-  // (whole stores of 64 columns)
-  int width = LN;
-  const int64_t blocks = ((int64_t)p.n + 2 * LM - 1) / (2 * LM);
-  for (int w = LN - 64; w >= 64; w -= 64)
-    if (rounds_cost(blocks * ((p.entries + w - 1) / w), w) <
-        rounds_cost(blocks * ((p.entries + width - 1) / width), width))
-      width = w;
+  // (in steps of 64 columns, whole stores: 300 tokens, d 7168, 32003 entries 457 us for 432)
+  const int width = loss_width(p.n, p.entries);
   LArgs a{p, p.entries, p.d, width, status};
   LMaps m{};
   const uint64_t dout[3] = {(uint64_t)p.pitch, (uint64_t)p.n, 1};

@@ -973,3 +973,24 @@ def test_cross_entropy_backward_of_no_finite_weight(lib, n, d, vocab, dtype):
     lib.moe_cross_entropy_backward(x, W, t, lse, weights, dx, None, ws)
     others = torch.arange(n, device="cuda") != n // 2
     assert (dx[others] == 0).all() and not torch.isfinite(dx[n // 2]).any()
+
+
+# vocabularies whose tiles of 96, 160 and 224 entries end in their last 32, of odd length
+@pytest.mark.parametrize("n,d,vocab", [(40, 264, 4871), (600, 72, 1601), (257, 136, 4931), (600, 72, 4899),
+                                       (257, 64, 7361), (40, 72, 14755)])
+def test_cross_entropy_backward_of_tiles_of_any_width(lib, n, d, vocab):
+    x, W, t, left = _loss_case(n, d, vocab, "bf16", 0.2, 11)
+    t[::3] = torch.where(t[::3] >= 0, vocab - 1 - torch.arange(len(t[::3]), device="cuda") % 40,
+                         t[::3].long()).to(torch.int32)      # (targets at the last tile's end)
+    clean = torch.where(left[:, None], 0, x)
+    lse = torch.where(t >= 0, torch.logsumexp(clean.double() @ W.double().T, 1), 0.0).float()
+    dloss = _randn(_gen(n), n)
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, "bf16")
+    ws[256:] = 0xFF
+    dx, dW = torch.full_like(x, float("nan")), torch.full_like(W, float("nan"))
+    lib.moe_cross_entropy_backward(x, W, t, lse, dloss, dx, dW, ws)
+    _ok(lib, ws)
+    wdx, ex, wdW, eW = _loss_reference(clean, W, t, lse, dloss, 0.0, "bf16")
+    _close(dx, wdx, ex, "dx")
+    _close(dW, wdW, eW, "dW")
+    assert (dx[left] == 0).all()
