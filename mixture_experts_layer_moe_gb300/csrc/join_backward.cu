@@ -56,6 +56,18 @@ struct BwdSteps {
   int64_t rows, dr, dy, r, b, dx, db;
 };
 
+template <typename T, int NB, bool CENTRED, bool ODD>
+struct BwdRing {
+  static constexpr int STAGE = NB * 4 * Blocks<T, J_THREADS, ODD>::BYTES;
+  static constexpr int OWN = NB * (CENTRED ? 3 : 1) * Own8<J_THREADS>::BYTES;
+  static constexpr int STAGES = stages_of(STAGE, OWN);
+  // The pre norm's sums over a row are formed with the post norm's over the row before, so
+  // that one barrier serves both: 287 us for 243 (16384 x 7168 bf16).  A row must have
+  // landed sooner for it, which loses with two stages (layer norms 368 / 402).
+  static constexpr bool AHEAD = STAGES > 2;
+  static_assert(!(AHEAD && CENTRED), "two sums at once");
+};
+
 // As the forward's kernel.  With rc = r - mean2, bc = b - mean1 (the rows themselves
 // without a layer norm, which CENTRED says there is):
 //   g = dr + rstd2 dy gamma2 + c2 rc + e2,   c2 = -rstd2^2 mean(w rh),  e2 = -rstd2 mean(w),
@@ -68,13 +80,15 @@ struct BwdSteps {
 template <typename T, int NB, bool DROP, bool CENTRED, bool ODD>
 __global__ void __launch_bounds__(J_THREADS, 1)
 join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ BwdSteps by, int tpr,
-                     int groups, int stages) {
+                     int groups) {
   extern __shared__ __align__(16) uint8_t dyn[];   // [stage][block][dr, dy, r, b], own values
   __shared__ float2 buf[2][32];
   using B = Blocks<T, J_THREADS, ODD>;
   using Own = Own8<J_THREADS>;
+  using R = BwdRing<T, NB, CENTRED, ODD>;
   enum { DR, DY, RR, BB };
-  constexpr int STAGE = NB * 4 * B::BYTES, SIZE = (int)sizeof(T);
+  constexpr int STAGE = R::STAGE, STAGES = R::STAGES, SIZE = (int)sizeof(T);
+  constexpr bool AHEAD = R::AHEAD;
   const moe_join_config &c = a.c;
   const int d = c.d, warps = tpr >> 5, warp = threadIdx.x >> 5;
   const int group = warp / warps, tid = threadIdx.x - group * tpr, first_warp = group * warps;
@@ -93,7 +107,7 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
   // dropout's factor.  In shared memory: what D's kept elements are multiplied by,
   // and the sums of u (without the factor) and dy
   Block8 p2[NB], sum_a[NB], sum_c[NB];
-  uint8_t *const own = dyn + stages * STAGE;
+  uint8_t *const own = dyn + STAGES * STAGE;
   auto p1 = [&](int n) { return Own(own + n * Own::BYTES); };
   auto sum_b = [&](int n) { return Own(own + (NB + n) * Own::BYTES); };
   auto sum_e = [&](int n) { return Own(own + (2 * NB + n) * Own::BYTES); };
@@ -125,7 +139,7 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
     }
   }
   int64_t row = (int64_t)blockIdx.x * groups + group, ahead = row;
-  uint8_t *const mine = dyn + B::place(), *const ring_end = mine + stages * STAGE;
+  uint8_t *const mine = dyn + B::place(), *const ring_end = mine + STAGES * STAGE;
   auto start = [&](const T *p, int64_t ld) {
     return reinterpret_cast<const char *>(p + row * ld + tid * 8);
   };
@@ -154,68 +168,82 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
     r_ahead += by.r;
     b_ahead += by.b;
   };
-  for (int i = 0; i < stages - 1; ++i) fill(mine + i * STAGE);
-  uint8_t *now = mine, *next = mine + (stages - 1) * STAGE;
+  // the elements of a row that landed, where its threads read them
+  auto align = [&](uint8_t *stage, int64_t row) {
+    if (!ODD) return;
+    __syncwarp();
+    if (row >= c.rows) return;
+    auto head = [&](const T *p, int64_t ld) {
+      return (int)((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)row * (uint32_t)ld * SIZE) & 15;
+    };
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      if (!active[n]) continue;
+      if (has_dy) {
+        B::realign(at(stage, n, DY), head(a.dy, c.lddy));
+        B::realign(at(stage, n, RR), head(a.r, c.ldr));
+      }
+      if (has_dr) B::realign(at(stage, n, DR), head(a.dr, c.lddr));
+      if (has_b) B::realign(at(stage, n, BB), head(a.b, c.ldb));
+    }
+  };
+  auto centred = [&](uint8_t *at, float mean) {
+    Block8 b = B::load(at);
+    if (CENTRED) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) b.v[h] = add2(b.v[h], both(-mean));
+    }
+    return b;
+  };
+  // this thread's share of the sums of w and w rc (a column that is not there has gamma 0)
+  auto pre_sums = [&](uint8_t *stage, int64_t row, float mean) {
+    float2 s1 = both(0.f), s2 = both(0.f);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      if (row >= c.rows || !active[n]) continue;
+      const Block8 dy = B::load(at(stage, n, DY)), rc = centred(at(stage, n, RR), mean);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const float2 w = mul2(dy.v[h], p2[n].v[h]);
+        if (CENTRED) s1 = add2(s1, w);
+        s2 = fma2(w, rc.v[h], s2);
+      }
+    }
+    return make_float2(s1.x + s1.y, s2.x + s2.y);
+  };
+  for (int i = 0; i < STAGES - 1; ++i) fill(mine + i * STAGE);
+  uint8_t *now = mine, *next = mine + (STAGES - 1) * STAGE;
   float4 next_stat = make_float4(0.f, 1.f, 0.f, 1.f);
   if (row < c.rows) next_stat = stats_of<T, CENTRED>(a, row);
+  // a norm's sums over the group
+  auto join = [&](float2 v) {
+    if (CENTRED) return row_sum2(v.x, v.y, buf, turn, first_warp, warps);
+    return make_float2(0.f, row_sum(v.y, buf, turn, warps));
+  };
+  float2 pre = both(0.f);   // AHEAD: those of the pre norm over the coming row
+  if (AHEAD) {
+    copies_wait(STAGES - 2);
+    align(now, row);
+    if (has_dy) pre = join(pre_sums(now, row, next_stat.z));
+  }
+  const bool norm_b = norm1 && a.db != nullptr;
   for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < c.rows; r0 += by.rows) {
     const bool live = row < c.rows;
     // (the stage being filled was read in the iteration before, by this thread or its warp)
     if (ODD) __syncwarp();
-    if (stages == 1) fill(next);
+    if (STAGES == 1) fill(next);
     const float4 stat = next_stat;
     if (row + by.rows < c.rows) next_stat = stats_of<T, CENTRED>(a, row + by.rows);
-    copies_wait(stages - 2);
-    if (ODD) {
-      __syncwarp();
-      auto head = [&](const T *p, int64_t ld) {
-        return (int)((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)row * (uint32_t)ld * SIZE) & 15;
-      };
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        if (!live || !active[n]) continue;
-        if (has_dy) {
-          B::realign(at(now, n, DY), head(a.dy, c.lddy));
-          B::realign(at(now, n, RR), head(a.r, c.ldr));
-        }
-        if (has_dr) B::realign(at(now, n, DR), head(a.dr, c.lddr));
-        if (has_b) B::realign(at(now, n, BB), head(a.b, c.ldb));
-      }
+    if (!AHEAD) {
+      copies_wait(STAGES - 2);
+      align(now, row);
+      if (has_dy) pre = pre_sums(now, row, stat.z);
+      if (STAGES > 1) fill(next);
+      if (has_dy) pre = join(pre);
     }
+    const float c2 = -stat.w * stat.w * stat.w * pre.y * inv_d;
+    const float e2 = layer2 ? -stat.w * pre.x * inv_d : 0.f;
     auto get = [&](int n, int t) { return B::load(at(now, n, t)); };
-    auto centred = [&](int n, int t, float mean) {
-      Block8 b = get(n, t);
-      if (CENTRED) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) b.v[h] = add2(b.v[h], both(-mean));
-      }
-      return b;
-    };
-    float c2 = 0.f, e2 = 0.f;
-    if (has_dy) {
-      // (a column that is not there has gamma 0)
-      float2 s1 = both(0.f), s2 = both(0.f);
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        if (!live || !active[n]) continue;
-        const Block8 dy = get(n, DY), rc = centred(n, RR, stat.z);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const float2 w = mul2(dy.v[h], p2[n].v[h]);
-          if (CENTRED) s1 = add2(s1, w);
-          s2 = fma2(w, rc.v[h], s2);
-        }
-      }
-      if (stages > 1) fill(next);
-      if (CENTRED) {
-        const float2 t = row_sum2(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
-        e2 = layer2 ? -stat.w * t.x * inv_d : 0.f;
-        c2 = -stat.w * stat.w * stat.w * t.y * inv_d;
-      } else {
-        c2 = -stat.w * stat.w * stat.w * row_sum(s2.x + s2.y, buf, turn, warps) * inv_d;
-      }
-    }
-    if (stages > 1 && !has_dy) fill(next);
     Block8 w[NB];
     float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
@@ -224,7 +252,7 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
       if (!live || !active[n]) continue;
       Block8 g = has_dr ? get(n, DR) : fill8(0.f);
       if (has_dy) {
-        const Block8 rc = centred(n, RR, stat.z);
+        const Block8 rc = centred(at(now, n, RR), stat.z);
         Block8 dy = get(n, DY);
         if (CENTRED) grow(sum_e(n), dy);
 #pragma unroll
@@ -251,7 +279,7 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
 #pragma unroll
       for (int h = 0; h < 4; ++h) w[n].v[h] = mul2(g.v[h], p.v[h]);
       if (has_b) {
-        const Block8 bc = centred(n, BB, stat.x);
+        const Block8 bc = centred(at(now, n, BB), stat.x);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           sum_a[n].v[h] = fma2(g.v[h], bc.v[h], sum_a[n].v[h]);
@@ -260,21 +288,29 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
         }
       }
     }
+    uint8_t *const then = now + STAGE == ring_end ? mine : now + STAGE;
+    float2 post = make_float2(s1.x + s1.y, s2.x + s2.y);
+    if (AHEAD) {
+      fill(next);   // (here: before the row's work 233 us for 219 without a post norm)
+      copies_wait(STAGES - 2);
+      align(then, row + by.rows);
+      if (has_dy) pre = pre_sums(then, row + by.rows, next_stat.z);
+      if (norm_b || has_dy) {
+        const float2 t = row_sum2(post.y, pre.y, buf, turn, first_warp, warps);
+        post.y = t.x;
+        pre.y = t.y;
+      }
+    } else if (norm_b) {
+      post = join(post);
+    }
     if (a.db) {
       // (w is rstd1 times the gradient of the normed row)
-      float c1 = 0.f, e1 = 0.f;
-      if (norm1 && CENTRED) {
-        const float2 t = row_sum2(s1.x + s1.y, s2.x + s2.y, buf, turn, first_warp, warps);
-        e1 = layer1 ? -t.x * inv_d : 0.f;
-        c1 = -stat.y * stat.y * t.y * inv_d;
-      } else if (norm1) {
-        c1 = -stat.y * stat.y * row_sum(s2.x + s2.y, buf, turn, warps) * inv_d;
-      }
+      const float c1 = -stat.y * stat.y * post.y * inv_d, e1 = layer1 ? -post.x * inv_d : 0.f;
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         if (!live || !active[n]) continue;
         if (norm1) {
-          const Block8 bc = centred(n, BB, stat.x);
+          const Block8 bc = centred(at(now, n, BB), stat.x);
 #pragma unroll
           for (int h = 0; h < 4; ++h)
             w[n].v[h] = fma2(bc.v[h], both(c1), CENTRED ? add2(w[n].v[h], both(e1)) : w[n].v[h]);
@@ -283,7 +319,7 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
       }
     }
     next = now;
-    now = now + STAGE == ring_end ? mine : now + STAGE;
+    now = then;
     row += by.rows;
     dx_out += by.dx;
     db_out += by.db;
@@ -487,11 +523,8 @@ cudaError_t run(const Bwd<T> &a, int &parts, cudaStream_t s) {
   auto kernel = join_backward_kernel<T, NB, DROP, CENTRED, ODD>;
   const moe_join_config &c = a.c;
   const int tpr = threads_of(c.d, NB), groups = groups_of(c.rows, 1, tpr, J_THREADS, J_PARTS);
-  const size_t stage = (size_t)NB * 4 * Blocks<T, J_THREADS, ODD>::BYTES;
-  const size_t own = (size_t)NB * (CENTRED ? 3 : 1) * Own8<J_THREADS>::BYTES;
-  const int stages = stages_of(stage, own);
-  static_assert(NB * 4 * Blocks<T, J_THREADS, ODD>::BYTES >= J_THREADS * NB * 32,
-                "the groups' column sums fit a stage");
+  using R = BwdRing<T, NB, CENTRED, ODD>;
+  static_assert(R::STAGE >= J_THREADS * NB * 32, "the groups' column sums fit a stage");
   static bool set = false;
   if (!set) {
     const cudaError_t e =
@@ -503,7 +536,7 @@ cudaError_t run(const Bwd<T> &a, int &parts, cudaStream_t s) {
   const int64_t rows = (int64_t)parts * groups, bytes = rows * sizeof(T);
   const BwdSteps by{rows,          bytes * c.lddr, bytes * c.lddy, bytes * c.ldr,
                     bytes * c.ldb, bytes * c.lddx, bytes * c.lddb};
-  kernel<<<parts, tpr * groups, stages * stage + own, s>>>(a, by, tpr, groups, stages);
+  kernel<<<parts, tpr * groups, R::STAGES * R::STAGE + R::OWN, s>>>(a, by, tpr, groups);
   return cudaGetLastError();
 }
 template <typename T, int NB, bool ODD>

@@ -256,7 +256,7 @@ inline int groups_of(int64_t rows, int rows_each, int tpr, int threads, int sms)
 }
 
 // Stages of a ring that fits beside `other` bytes.
-inline int stages_of(size_t stage, size_t other) {
+__host__ __device__ constexpr int stages_of(size_t stage, size_t other) {
   int stages = 3;
   while (stages > 1 && stages * stage + other > (size_t)J_SMEM) --stages;
   return stages;
