@@ -582,7 +582,7 @@ typedef struct {
 /* Bytes of workspace for the two entry points below, a status word at its start
  * (moe_status_check); nothing else in it lives from one call to the next, and it
  * may be any workspace that is large enough.  Holds the logits of a piece of the
- * vocabulary (about 256 MB), 8 bytes per token and 256 entries of the
+ * vocabulary (about 256 MB, or 8192 entries), 8 bytes per token and 256 entries of the
  * vocabulary, and a few copies of x.  Host-only. */
 moe_status moe_cross_entropy_workspace_size(const moe_loss_config *cfg, size_t *bytes);
 

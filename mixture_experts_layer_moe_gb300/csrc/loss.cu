@@ -36,6 +36,11 @@ namespace {
 constexpr int L_UNIT = 256;                            // a piece's entries are a multiple of this
 constexpr int64_t L_PIECE_BYTES = (int64_t)256 << 20;  // of a piece's dl, about
 constexpr int64_t L_PIECE_MAX = 1 << 22;               // entries of a piece
+// Entries of a piece at least: with fewer, dx is read and written again for few products.
+// (32000 entries, us without a least / 2048 / 4096 / 8192: 131072 tokens, d 2048 37210 / 33718 /
+// 32153 / 31937; 262144, d 1024 50749 / 34778 / 33664 / 33234; f32, 131072 tokens, d 64, 4099
+// entries 21264 / 11524 / 8891 / 7112.)
+constexpr int64_t L_PIECE_MIN = 8192;
 constexpr int L_MAX_SPLITS = 76;
 
 struct LossLayout {
@@ -95,7 +100,7 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.pitch = (c.n + 3) / 4 * 4;
   // pieces of nearly equal size
   int64_t fit = L_PIECE_BYTES / ((int64_t)(L.pitch > 0 ? L.pitch : 4) * (L.pair ? 2 : 4));
-  fit = (fit < L_UNIT ? L_UNIT : fit > L_PIECE_MAX ? L_PIECE_MAX : fit) / L_UNIT * L_UNIT;
+  fit = (fit < L_PIECE_MIN ? L_PIECE_MIN : fit > L_PIECE_MAX ? L_PIECE_MAX : fit) / L_UNIT * L_UNIT;
   L.pieces = (int)((c.vocab + fit - 1) / fit);
   L.piece = (c.vocab + L.pieces - 1) / L.pieces;
   if (L.pieces > 1) L.piece = (L.piece + L_UNIT - 1) / L_UNIT * L_UNIT;
