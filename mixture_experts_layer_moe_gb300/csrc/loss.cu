@@ -87,6 +87,20 @@ GradProduct dw_product(const moe_loss_config &c, int entries) {
   return p;
 }
 
+// dW of a piece on the CUDA cores (operands unset).
+RowsProduct dw_product_simt(const moe_loss_config &c, int entries) {
+  RowsProduct p{};
+  p.dtype = c.dtype;
+  p.epi = kRowsPlain;
+  p.b_rows = 1;
+  p.num_experts = 1;
+  p.rows = entries;
+  p.K = c.n;
+  p.N = c.d;
+  p.a_f32 = c.dtype == MOE_BF16;
+  return p;
+}
+
 int dx_splits(const moe_loss_config &c, const LossLayout &L, int entries, int most) {
   return L.few ? loss_few_splits(c.d, entries, most) : loss_dx_splits(c.n, c.d, entries, most);
 }
@@ -143,9 +157,14 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.acc = take(!L.pair && L.pieces > 1 ? n * c.d * 4 : 0);
   size_t parts = 0;
   for (int entries : {L.piece, last}) {
-    if (!L.pair || L.few) break;
-    const GradProduct p = dw_product(c, entries);
-    const int splits = gemm_grad_splits(&p, 1);
+    if (L.few) break;
+    int splits;
+    if (L.pair) {
+      const GradProduct p = dw_product(c, entries);
+      splits = gemm_grad_splits(&p, 1);
+    } else {
+      splits = rows_runs_simt(dw_product_simt(c, entries));
+    }
     const size_t bytes = splits > 1 ? (size_t)splits * entries * c.d * 4 : 0;
     if (bytes > parts) parts = bytes;
   }
@@ -447,20 +466,17 @@ cudaError_t piece_gradient_simt(const moe_loss_config &c, const LossLayout &L, c
   l.loss.z_loss = c.z_loss;
   LOSS_TRY(launch_rows_simt(l, status, s));
   if (dW) {
-    RowsProduct p{};
-    p.dtype = c.dtype;
-    p.epi = kRowsPlain;
-    p.b_rows = 1;
-    p.num_experts = 1;
-    p.rows = entries;
-    p.K = c.n;
-    p.N = c.d;
+    RowsProduct p = dw_product_simt(c, entries);
+    void *out = (char *)dW + v0 * row;
+    float *parts = at<float>(ws, L.parts);
     p.lda = L.pitch;
     p.A = at<void>(ws, L.logits);
     p.B = at<void>(ws, L.x);
-    p.out = (char *)dW + v0 * row;
-    p.a_f32 = c.dtype == MOE_BF16;
+    p.k_runs = rows_runs_simt(p);
+    p.out = p.k_runs > 1 ? parts : out;
     LOSS_TRY(launch_rows_simt(p, status, s));
+    if (p.k_runs > 1)
+      LOSS_TRY(add_runs_simt(c.dtype, parts, p.k_runs, (int64_t)entries * c.d, out, status, s));
   }
   if (!dx) return cudaSuccess;
   GradProduct p = dx_product(c, L, entries);

@@ -93,6 +93,9 @@ struct RowsProduct {
   // For a bf16 layer: A and A2 are fp32 (on the CUDA cores), or out and out_u of a
   // gradient are
   int a_f32, out_f32;
+  // kRowsPlain, b_rows, one segment, on the CUDA cores: runs that the reduction is cut into
+  // (0: one); out is then fp32 [run][rows][N], for add_runs_simt
+  int k_runs;
   // kRowsLossGrad: elements from one row of out to the next, a multiple of 4; columns
   // from N on are written as zeros
   int ldo;
@@ -103,6 +106,11 @@ int rows_simt_tile(const RowsProduct &p);
 // fp32, and small bf16 products: at most so many multiplications each.
 constexpr int64_t kSmallProducts = 1 << 24;
 cudaError_t launch_rows_simt(const RowsProduct &p, int *status, cudaStream_t s);
+// Runs for such a product whose tiles leave most SMs without work.
+int rows_runs_simt(const RowsProduct &p);
+// out[i] = sum of parts [run][count], in order (count: a multiple of 4).
+cudaError_t add_runs_simt(int dtype, const float *parts, int runs, int64_t count, void *out,
+                          int *status, cudaStream_t s);
 
 // The same with the reduction cut into ranges where its tiles are few (bf16), or
 // whole with fp32 outputs: how many ranges (1: not cut; by the shape alone), the

@@ -678,10 +678,12 @@ def _close(got, want, bound, what):
     _within(got, want.cpu(), bound.cpu(), what)
 
 
-# several pieces of the vocabulary: on the tensor cores, for few tokens, on the CUDA cores
+# several pieces of the vocabulary: on the tensor cores, for few tokens, on the CUDA cores; runs of
+# the tokens there
 @pytest.mark.parametrize("n,d,vocab,dtype", [(2500, 64, 60001, "bf16"), (190, 8, 720001, "bf16"),
                                              (3001, 8, 30001, "f32"), (5000, 16, 27777, "bf16"),
-                                             (20000, 64, 9001, "bf16"), (12000, 8, 9001, "f32")])
+                                             (20000, 64, 9001, "bf16"), (12000, 8, 9001, "f32"),
+                                             (5001, 16, 203, "bf16"), (9001, 36, 77, "f32")])
 def test_cross_entropy_in_pieces(lib, n, d, vocab, dtype):
     x, W, t, left = _loss_case(n, d, vocab, dtype, 0.1, 7)
     clean = torch.where(left[:, None], 0, x)
