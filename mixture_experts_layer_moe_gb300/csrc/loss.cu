@@ -19,7 +19,8 @@
 // Gradient, on the CUDA cores (fp32, and small bf16 problems): dl of a piece in
 // fp32 with the token contiguous, lT [piece][pitch]: then dx = dl W is a sum over
 // lT's rows (GradProduct: cut into runs where the tiles are few) and dW = dl^T x a
-// product of its rows (RowsProduct).
+// product of its rows (RowsProduct).  For a few fp32 tokens both, and the forward, are
+// streams over W (loss_stream.cu).
 #include <math.h>
 
 #include "api.h"
@@ -53,6 +54,7 @@ struct LossLayout {
   int width, chunks;   // entries per tile of the forward; partial sums per token at most
   int planes;          // dx: partial sums of a piece
   bool few;            // dx and dW in one pass (loss_few.cu)
+  bool stream;         // fp32, by streams over W (loss_stream.cu)
 };
 
 int elem_size(const moe_loss_config &c) { return c.dtype == MOE_F32 ? 4 : 2; }
@@ -111,6 +113,7 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.pair = c.dtype == MOE_BF16 && !small_loss(c);
   L.packed = L.pair && c.n > 256;
   L.few = L.pair && c.n <= kLossFewTokens;
+  L.stream = loss_stream_supported(c);
   L.pitch = (c.n + 3) / 4 * 4;
   // pieces of nearly equal size
   int64_t fit = L_PIECE_BYTES / ((int64_t)(L.pitch > 0 ? L.pitch : 4) * (L.pair ? 2 : 4));
@@ -122,7 +125,9 @@ LossLayout loss_layout(const moe_loss_config &c) {
   const int last = c.vocab - (L.pieces - 1) * L.piece;
   L.width = L.pair ? loss_width(c.n, c.vocab) : 0;
   L.chunks = L.pair ? loss_chunks(c.vocab, L.width) : (c.vocab + 31) / 32;
-  if (L.pair) {
+  if (L.stream) {
+    L.planes = loss_stream_splits(c.d, L.piece, 2 * L_MAX_SPLITS);
+  } else if (L.pair) {
     L.planes = dx_splits(c, L, L.piece, L_MAX_SPLITS);
   } else {
     L.planes = 1;
@@ -157,7 +162,7 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.acc = take(!L.pair && L.pieces > 1 ? n * c.d * 4 : 0);
   size_t parts = 0;
   for (int entries : {L.piece, last}) {
-    if (L.few) break;
+    if (L.few || L.stream) break;
     int splits;
     if (L.pair) {
       const GradProduct p = dw_product(c, entries);
@@ -371,42 +376,93 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant_
 
 // dx of the counted tokens from the partial sums [planes][n][d], added in order (times
 // *scale, if given); or (acc_out) what a piece adds to the sum of those before, `acc`.
+struct DxArgs {
+  const float *parts, *acc;
+  float *acc_out;
+  int planes, n, vecs;
+  const float *scale;
+  const int32_t *range, *list;
+  void *dx;
+  const int *status;
+};
+// Vector i of it, v = the planes' sum.
 template <typename T>
-__global__ void __launch_bounds__(256)
-loss_dx_kernel(const float *__restrict__ parts, int planes, const float *acc, float *acc_out, int n,
-               int vecs, const float *scale, const int32_t *__restrict__ range,
-               const int32_t *__restrict__ list, T *__restrict__ dx, const int *status) {
+__device__ __forceinline__ void put_dx(const DxArgs &a, int64_t i, float4 (&v)[Vec16<T>::N / 4], float k) {
+  constexpr int V = Vec16<T>::N / 4;
+  const int64_t j = i / a.vecs;
+  if (a.acc_out) {
+#pragma unroll
+    for (int h = 0; h < V; ++h) reinterpret_cast<float4 *>(a.acc_out)[i * V + h] = v[h];
+  } else {
+#pragma unroll
+    for (int h = 0; h < V; ++h) v[h] = make_float4(v[h].x * k, v[h].y * k, v[h].z * k, v[h].w * k);
+    reinterpret_cast<uint4 *>(a.dx)[(int64_t)a.list[j] * a.vecs + (i - j * a.vecs)] =
+        pack16<T>(reinterpret_cast<const float *>(v));
+  }
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+template <typename T>
+__global__ void __launch_bounds__(256) loss_dx_kernel(const __grid_constant__ DxArgs a) {
   constexpr int N = Vec16<T>::N, V = N / 4;
   pdl_wait();
-  if (status_failed(status)) return;
-  const int64_t total = (int64_t)range[1] * vecs, plane = (int64_t)n * vecs * V;
-  const float k = scale ? *scale : 1.f;
+  if (status_failed(a.status)) return;
+  const int64_t total = (int64_t)a.range[1] * a.vecs, plane = (int64_t)a.n * a.vecs * V;
+  const float k = a.scale ? *a.scale : 1.f;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
-    const int64_t j = i / vecs;
-    const float4 *from = reinterpret_cast<const float4 *>(parts) + i * V;
+    const float4 *from = reinterpret_cast<const float4 *>(a.parts) + i * V;
     float4 v[V];
 #pragma unroll
     for (int h = 0; h < V; ++h)
-      v[h] = acc ? reinterpret_cast<const float4 *>(acc)[i * V + h] : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[h] = a.acc ? reinterpret_cast<const float4 *>(a.acc)[i * V + h] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int p = 0; p < planes; ++p) {
+    for (int p = 0; p < a.planes; ++p) {
 #pragma unroll
-      for (int h = 0; h < V; ++h) {
-        const float4 w = from[p * plane + h];
-        v[h] = make_float4(v[h].x + w.x, v[h].y + w.y, v[h].z + w.z, v[h].w + w.w);
+      for (int h = 0; h < V; ++h) v[h] = add4(v[h], from[p * plane + h]);
+    }
+    put_dx<T>(a, i, v, k);
+  }
+}
+// Many planes: 32 vectors per CTA, whose warps take the planes in turn; their sums are
+// added in order.
+template <typename T>
+__global__ void __launch_bounds__(256) loss_dx_wide_kernel(const __grid_constant__ DxArgs a) {
+  constexpr int N = Vec16<T>::N, V = N / 4;
+  __shared__ float4 s[8][V][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  if (status_failed(a.status)) return;
+  const int64_t total = (int64_t)a.range[1] * a.vecs, plane = (int64_t)a.n * a.vecs * V;
+  const float k = a.scale ? *a.scale : 1.f;
+  for (int64_t i0 = (int64_t)blockIdx.x * 32; i0 < total; i0 += (int64_t)gridDim.x * 32) {
+    const int64_t i = i0 + lane;
+    float4 v[V];
+#pragma unroll
+    for (int h = 0; h < V; ++h) v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < total) {
+      const float4 *from = reinterpret_cast<const float4 *>(a.parts) + i * V;
+#pragma unroll 8
+      for (int p = warp; p < a.planes; p += 8) {
+#pragma unroll
+        for (int h = 0; h < V; ++h) v[h] = add4(v[h], from[p * plane + h]);
       }
     }
-    if (acc_out) {
 #pragma unroll
-      for (int h = 0; h < V; ++h) reinterpret_cast<float4 *>(acc_out)[i * V + h] = v[h];
-    } else {
+    for (int h = 0; h < V; ++h) s[warp][h][lane] = v[h];
+    __syncthreads();
+    if (warp == 0 && i < total) {
 #pragma unroll
-      for (int h = 0; h < V; ++h)
-        v[h] = make_float4(v[h].x * k, v[h].y * k, v[h].z * k, v[h].w * k);
-      reinterpret_cast<uint4 *>(dx)[(int64_t)list[j] * vecs + (i - j * vecs)] =
-          pack16<T>(reinterpret_cast<const float *>(v));
+      for (int h = 0; h < V; ++h) {
+        v[h] = a.acc ? reinterpret_cast<const float4 *>(a.acc)[i * V + h]
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v[h] = add4(v[h], s[w][h][lane]);
+      }
+      put_dx<T>(a, i, v, k);
     }
+    __syncthreads();
   }
 }
 
@@ -421,19 +477,15 @@ unsigned blocks_of(int64_t threads) {
     if (_e != cudaSuccess) return _e;        \
   } while (0)
 
-template <typename T>
 cudaError_t finish_dx(const moe_loss_config &c, const LossLayout &L, int planes, const float *acc,
                       float *acc_out, void *dx, void *ws, cudaStream_t s) {
-  const int vecs = c.d / Vec16<T>::N;
-  return launch_pdl(loss_dx_kernel<T>, dim3(blocks_of((int64_t)c.n * vecs)), dim3(256), 0, s,
-                    at<float>(ws, L.dx), planes, acc, acc_out, c.n, vecs,
-                    L.pair ? at<float>(ws, L.scale) : nullptr, at<int32_t>(ws, L.range),
-                    at<int32_t>(ws, L.list), (T *)dx, at<int>(ws, L.status));
-}
-cudaError_t finish_dx(const moe_loss_config &c, const LossLayout &L, int planes, const float *acc,
-                      float *acc_out, void *dx, void *ws, cudaStream_t s) {
-  return c.dtype == MOE_F32 ? finish_dx<float>(c, L, planes, acc, acc_out, dx, ws, s)
-                            : finish_dx<__nv_bfloat16>(c, L, planes, acc, acc_out, dx, ws, s);
+  const bool f32 = c.dtype == MOE_F32, wide = planes >= 16;
+  const DxArgs a{at<float>(ws, L.dx), acc, acc_out, planes, c.n, c.d * elem_size(c) / 16,
+                 L.pair ? at<float>(ws, L.scale) : nullptr, at<int32_t>(ws, L.range),
+                 at<int32_t>(ws, L.list), dx, at<int>(ws, L.status)};
+  auto kernel = f32 ? (wide ? loss_dx_wide_kernel<float> : loss_dx_kernel<float>)
+                    : (wide ? loss_dx_wide_kernel<__nv_bfloat16> : loss_dx_kernel<__nv_bfloat16>);
+  return launch_pdl(kernel, dim3(blocks_of((int64_t)c.n * a.vecs * (wide ? 8 : 1))), dim3(256), 0, s, a);
 }
 
 // The logits' product on the CUDA cores, over entries v0 .. of the vocabulary.
@@ -450,6 +502,43 @@ RowsProduct simt_product(const moe_loss_config &c, int epi, const void *x, const
   p.B = x;
   p.loss.v0 = v0;
   return p;
+}
+
+// The operands that the products on the tensor cores and the streams share, over entries
+// v0 .. of the vocabulary, whose rows are W.
+LossProduct loss_product(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
+                         int entries, void *ws) {
+  LossProduct p{};
+  p.n = c.n;
+  p.d = c.d;
+  p.entries = entries;
+  p.v0 = v0;
+  p.range = at<int32_t>(ws, L.range);
+  p.target = at<int32_t>(ws, L.target);
+  p.x = at<void>(ws, L.x);
+  p.W = W;
+  p.lse = at<float>(ws, L.lse);
+  p.dloss = at<float>(ws, L.dloss);
+  p.scale = at<float>(ws, L.scale);
+  p.z_loss = c.z_loss;
+  p.dl = at<void>(ws, L.logits);
+  p.pitch = dl_pitch(entries);
+  p.planes = at<float>(ws, L.dx);
+  return p;
+}
+
+cudaError_t piece_gradient_stream(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
+                                  int entries, int i, void *dx, void *dW, void *ws, cudaStream_t s) {
+  int *status = at<int>(ws, L.status);
+  const size_t first = (size_t)v0 * c.d;
+  LossProduct p = loss_product(c, L, (const float *)W + first, v0, entries, ws);
+  p.pitch = L.pitch;
+  p.splits = loss_stream_splits(c.d, entries, L.planes);
+  float *dl = at<float>(ws, L.logits), *acc = at<float>(ws, L.acc);
+  LOSS_TRY(launch_loss_stream(p, dl, loss_stream_chunks(c), status, s));
+  LOSS_TRY(launch_loss_stream_grads(p, dl, dW ? (float *)dW + first : nullptr, dx != nullptr, status, s));
+  if (!dx) return cudaSuccess;
+  return finish_dx(c, L, p.splits, i > 0 ? acc : nullptr, i + 1 < L.pieces ? acc : nullptr, dx, ws, s);
 }
 
 cudaError_t piece_gradient_simt(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
@@ -488,33 +577,10 @@ cudaError_t piece_gradient_simt(const moe_loss_config &c, const LossLayout &L, c
   return finish_dx(c, L, splits, i > 0 ? acc : nullptr, i + 1 < L.pieces ? acc : nullptr, dx, ws, s);
 }
 
-// The operands that the products on the tensor cores share, over entries v0 .. of
-// the vocabulary.
-LossProduct pair_product(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
-                         int entries, void *ws) {
-  LossProduct p{};
-  p.n = c.n;
-  p.d = c.d;
-  p.entries = entries;
-  p.v0 = v0;
-  p.range = at<int32_t>(ws, L.range);
-  p.target = at<int32_t>(ws, L.target);
-  p.x = at<void>(ws, L.x);
-  p.W = (const char *)W + (size_t)v0 * c.d * 2;
-  p.lse = at<float>(ws, L.lse);
-  p.dloss = at<float>(ws, L.dloss);
-  p.scale = at<float>(ws, L.scale);
-  p.z_loss = c.z_loss;
-  p.dl = at<void>(ws, L.logits);
-  p.pitch = dl_pitch(entries);
-  p.planes = at<float>(ws, L.dx);
-  return p;
-}
-
 cudaError_t piece_gradient_pair(const moe_loss_config &c, const LossLayout &L, const void *W, int v0,
                                 int entries, int i, void *dx, void *dW, void *ws, cudaStream_t s) {
   int *status = at<int>(ws, L.status);
-  LossProduct p = pair_product(c, L, W, v0, entries, ws);
+  LossProduct p = loss_product(c, L, (const char *)W + (size_t)v0 * c.d * 2, v0, entries, ws);
   void *out = dW ? (char *)dW + (size_t)v0 * c.d * 2 : nullptr;
   // (the last piece may be cut into fewer ranges, and adds to the first planes)
   p.splits = entries == L.piece ? L.planes : dx_splits(c, L, entries, L.planes);
@@ -562,7 +628,7 @@ cudaError_t launch_loss(const moe_loss_config &c, const void *x, const void *W,
     f.list = at<int32_t>(ws, L.list);
   }
   if (L.pair) {
-    LossProduct p = pair_product(c, L, W, 0, c.vocab, ws);
+    LossProduct p = loss_product(c, L, W, 0, c.vocab, ws);
     p.sums = at<float2>(ws, L.sums);
     p.width = L.width;
     p.chunks = L.chunks;
@@ -573,6 +639,15 @@ cudaError_t launch_loss(const moe_loss_config &c, const void *x, const void *W,
       p.x = x;
     }
     LOSS_TRY(launch_loss_sums(p, f.status, s));
+  } else if (L.stream) {
+    LossProduct p = loss_product(c, L, W, 0, c.vocab, ws);
+    p.target = targets;
+    p.x = x;
+    p.sums = at<float2>(ws, L.sums);
+    p.chunks = L.chunks;
+    p.at = at<float>(ws, L.at);
+    f.chunks = loss_stream_chunks(c);
+    LOSS_TRY(launch_loss_stream(p, nullptr, f.chunks, f.status, s));
   } else {
     RowsProduct p = simt_product(c, kRowsLossSums, x, W, 0, c.vocab);
     const int tile = rows_simt_tile(p);
@@ -594,7 +669,7 @@ cudaError_t launch_loss_backward(const moe_loss_config &c, const void *x, const 
   const LossLayout L = loss_layout(c);
   if (L.pair && !loss_pair_supported(c)) return cudaErrorNotSupported;
   LOSS_TRY(launch_pack(c, L, x, targets, lse, dloss, nullptr, nullptr, dx, ws, s));
-  auto piece = L.pair ? piece_gradient_pair : piece_gradient_simt;
+  auto piece = L.pair ? piece_gradient_pair : L.stream ? piece_gradient_stream : piece_gradient_simt;
   for (int v0 = 0, i = 0; v0 < c.vocab; v0 += L.piece, ++i)
     LOSS_TRY(piece(c, L, W, v0, c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece, i, dx, dW, ws, s));
   return cudaSuccess;

@@ -362,6 +362,12 @@ LOSS_CASES = [
     (1, 4, 1, "f32", 0.0), (1, 4, 3, "f32", 0.0), (3, 12, 5, "f32", 0.0), (2, 64, 257, "f32", 0.5),
     (33, 36, 300, "f32", 0.3), (256, 128, 4099, "f32", 0.1), (70, 260, 515, "f32", 0.0),
     (1000, 64, 1027, "f32", 0.2), (2500, 16, 130, "f32", 0.1), (17000, 8, 40, "f32", 0.5),
+    # few fp32 tokens, up to and past what is held of them
+    (1, 64, 1, "f32", 0.0), (1, 512, 8192, "f32", 0.0), (1, 2884, 20011, "f32", 0.0),
+    (2, 132, 65, "f32", 0.0), (3, 100, 999, "f32", 0.3), (4, 68, 33, "f32", 0.0),
+    (5, 260, 5155, "f32", 0.4), (6, 64, 30, "f32", 0.0), (7, 1028, 70, "f32", 0.3),
+    (8, 64, 9001, "f32", 0.2), (8, 6144, 333, "f32", 0.0), (8, 6148, 333, "f32", 0.0),
+    (9, 256, 700, "f32", 0.0),
 ]
 
 
@@ -683,7 +689,8 @@ def _close(got, want, bound, what):
 @pytest.mark.parametrize("n,d,vocab,dtype", [(2500, 64, 60001, "bf16"), (190, 8, 720001, "bf16"),
                                              (3001, 8, 30001, "f32"), (5000, 16, 27777, "bf16"),
                                              (20000, 64, 9001, "bf16"), (12000, 8, 9001, "f32"),
-                                             (5001, 16, 203, "bf16"), (9001, 36, 77, "f32")])
+                                             (5001, 16, 203, "bf16"), (9001, 36, 77, "f32"),
+                                             (2, 64, 4194561, "f32")])
 def test_cross_entropy_in_pieces(lib, n, d, vocab, dtype):
     x, W, t, left = _loss_case(n, d, vocab, dtype, 0.1, 7)
     clean = torch.where(left[:, None], 0, x)
