@@ -425,8 +425,9 @@ __global__ void __launch_bounds__(256) loss_dx_kernel(const __grid_constant__ Dx
     put_dx<T>(a, i, v, k);
   }
 }
-// Many planes: 32 vectors per CTA, whose warps take the planes in turn; their sums are
-// added in order.
+// 16 planes and more: 32 vectors per CTA, whose warps take the planes in turn; their sums
+// are added in order.  (One fp32 token, d 512, 8192 entries, 152 planes: 33.3 us for 20.6; from 4
+// planes on 300 bf16 tokens, d 7168 took 459 for 441.)
 template <typename T>
 __global__ void __launch_bounds__(256) loss_dx_wide_kernel(const __grid_constant__ DxArgs a) {
   constexpr int N = Vec16<T>::N, V = N / 4;

@@ -462,7 +462,7 @@ def test_cross_entropy_backward(lib, n, d, vocab, dtype, out, z_loss):
 
 
 @pytest.mark.parametrize("n,d,vocab,dtype", [(40, 64, 500, "bf16"), (300, 512, 3000, "bf16"),
-                                             (40, 64, 500, "f32")])
+                                             (40, 64, 500, "f32"), (4, 64, 500, "f32")])
 def test_cross_entropy_of_no_counted_token(lib, n, d, vocab, dtype):
     x, W, t, _ = _loss_case(n, d, vocab, dtype, 1.1)
     ws = lib.alloc_cross_entropy_workspace(n, d, vocab, dtype)
@@ -965,7 +965,7 @@ def test_tensors_of_another_device_are_refused(lib, monkeypatch):
 
 @pytest.mark.parametrize("n,d,vocab,dtype", [(1, 512, 5000, "bf16"), (50, 320, 1100, "bf16"),
                                              (400, 320, 1100, "bf16"), (50, 64, 300, "bf16"),
-                                             (50, 64, 300, "f32")])
+                                             (50, 64, 300, "f32"), (4, 64, 300, "f32")])
 def test_cross_entropy_backward_of_no_finite_weight(lib, n, d, vocab, dtype):
     """A step gone wrong shows in the gradient: no finite dloss leaves no finite gradient."""
     x, W, t, _ = _loss_case(n, d, vocab, dtype, 0.0, 3)
