@@ -19,8 +19,9 @@
 // Gradient, on the CUDA cores (fp32, and small bf16 problems): dl of a piece in
 // fp32 with the token contiguous, lT [piece][pitch]: then dx = dl W is a sum over
 // lT's rows (GradProduct: cut into runs where the tiles are few) and dW = dl^T x a
-// product of its rows (RowsProduct).  For a few fp32 tokens both, and the forward, are
-// streams over W (loss_stream.cu).
+// product of its rows (RowsProduct).
+//
+// A few tokens' forward, and in fp32 their gradient, are streams over W (loss_stream.cu).
 #include <math.h>
 
 #include "api.h"
@@ -54,7 +55,7 @@ struct LossLayout {
   int width, chunks;   // entries per tile of the forward; partial sums per token at most
   int planes;          // dx: partial sums of a piece
   bool few;            // dx and dW in one pass (loss_few.cu)
-  bool stream;         // fp32, by streams over W (loss_stream.cu)
+  bool stream, stream_grad;   // the forward, the gradient by streams over W (loss_stream.cu)
 };
 
 int elem_size(const moe_loss_config &c) { return c.dtype == MOE_F32 ? 4 : 2; }
@@ -114,6 +115,7 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.packed = L.pair && c.n > 256;
   L.few = L.pair && c.n <= kLossFewTokens;
   L.stream = loss_stream_supported(c);
+  L.stream_grad = L.stream && c.dtype == MOE_F32;
   L.pitch = (c.n + 3) / 4 * 4;
   // pieces of nearly equal size
   int64_t fit = L_PIECE_BYTES / ((int64_t)(L.pitch > 0 ? L.pitch : 4) * (L.pair ? 2 : 4));
@@ -124,8 +126,8 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.pieces = (c.vocab + L.piece - 1) / L.piece;
   const int last = c.vocab - (L.pieces - 1) * L.piece;
   L.width = L.pair ? loss_width(c.n, c.vocab) : 0;
-  L.chunks = L.pair ? loss_chunks(c.vocab, L.width) : (c.vocab + 31) / 32;
-  if (L.stream) {
+  L.chunks = L.stream ? loss_stream_chunks(c) : L.pair ? loss_chunks(c.vocab, L.width) : (c.vocab + 31) / 32;
+  if (L.stream_grad) {
     L.planes = loss_stream_splits(c.d, L.piece, 2 * L_MAX_SPLITS);
   } else if (L.pair) {
     L.planes = dx_splits(c, L, L.piece, L_MAX_SPLITS);
@@ -162,7 +164,7 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.acc = take(!L.pair && L.pieces > 1 ? n * c.d * 4 : 0);
   size_t parts = 0;
   for (int entries : {L.piece, last}) {
-    if (L.few || L.stream) break;
+    if (L.few || L.stream_grad) break;
     int splits;
     if (L.pair) {
       const GradProduct p = dw_product(c, entries);
@@ -536,7 +538,7 @@ cudaError_t piece_gradient_stream(const moe_loss_config &c, const LossLayout &L,
   p.pitch = L.pitch;
   p.splits = loss_stream_splits(c.d, entries, L.planes);
   float *dl = at<float>(ws, L.logits), *acc = at<float>(ws, L.acc);
-  LOSS_TRY(launch_loss_stream(p, dl, loss_stream_chunks(c), status, s));
+  LOSS_TRY(launch_loss_stream_logit_grad(p, dl, loss_stream_chunks(c), status, s));
   LOSS_TRY(launch_loss_stream_grads(p, dl, dW ? (float *)dW + first : nullptr, dx != nullptr, status, s));
   if (!dx) return cudaSuccess;
   return finish_dx(c, L, p.splits, i > 0 ? acc : nullptr, i + 1 < L.pieces ? acc : nullptr, dx, ws, s);
@@ -628,7 +630,16 @@ cudaError_t launch_loss(const moe_loss_config &c, const void *x, const void *W,
     f.range = at<int32_t>(ws, L.range);
     f.list = at<int32_t>(ws, L.list);
   }
-  if (L.pair) {
+  if (L.stream) {
+    LossProduct p = loss_product(c, L, W, 0, c.vocab, ws);
+    p.target = targets;
+    p.x = x;
+    p.sums = at<float2>(ws, L.sums);
+    p.chunks = L.chunks;
+    p.at = at<float>(ws, L.at);
+    f.chunks = loss_stream_chunks(c);
+    LOSS_TRY(launch_loss_stream_sums(c.dtype, p, f.chunks, f.status, s));
+  } else if (L.pair) {
     LossProduct p = loss_product(c, L, W, 0, c.vocab, ws);
     p.sums = at<float2>(ws, L.sums);
     p.width = L.width;
@@ -640,15 +651,6 @@ cudaError_t launch_loss(const moe_loss_config &c, const void *x, const void *W,
       p.x = x;
     }
     LOSS_TRY(launch_loss_sums(p, f.status, s));
-  } else if (L.stream) {
-    LossProduct p = loss_product(c, L, W, 0, c.vocab, ws);
-    p.target = targets;
-    p.x = x;
-    p.sums = at<float2>(ws, L.sums);
-    p.chunks = L.chunks;
-    p.at = at<float>(ws, L.at);
-    f.chunks = loss_stream_chunks(c);
-    LOSS_TRY(launch_loss_stream(p, nullptr, f.chunks, f.status, s));
   } else {
     RowsProduct p = simt_product(c, kRowsLossSums, x, W, 0, c.vocab);
     const int tile = rows_simt_tile(p);
@@ -670,7 +672,7 @@ cudaError_t launch_loss_backward(const moe_loss_config &c, const void *x, const 
   const LossLayout L = loss_layout(c);
   if (L.pair && !loss_pair_supported(c)) return cudaErrorNotSupported;
   LOSS_TRY(launch_pack(c, L, x, targets, lse, dloss, nullptr, nullptr, dx, ws, s));
-  auto piece = L.pair ? piece_gradient_pair : L.stream ? piece_gradient_stream : piece_gradient_simt;
+  auto piece = L.pair ? piece_gradient_pair : L.stream_grad ? piece_gradient_stream : piece_gradient_simt;
   for (int v0 = 0, i = 0; v0 < c.vocab; v0 += L.piece, ++i)
     LOSS_TRY(piece(c, L, W, v0, c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece, i, dx, dW, ws, s));
   return cudaSuccess;

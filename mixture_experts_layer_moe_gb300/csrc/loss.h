@@ -50,13 +50,16 @@ int loss_few_splits(int d, int entries, int most);
 cudaError_t launch_loss_few(const LossProduct &p, void *dW, bool want_dx, int *status,
                             cudaStream_t s);
 
-// A few tokens in fp32, by streams over W (loss_stream.cu).  The forward's partial sums per
-// token, or with dl [entries][pitch] the gradient of the logits; then dx (planes, of `splits`
-// ranges of the entries) and dW.
+// A few tokens, by streams over W (loss_stream.cu).  The forward's partial sums per token; in
+// fp32 the gradient of the logits, dl [entries][pitch], then dx (planes, of `splits` ranges of
+// the entries) and dW.
 bool loss_stream_supported(const moe_loss_config &c);
 int loss_stream_chunks(const moe_loss_config &c);   // CTAs, and partial sums per token
 int loss_stream_splits(int d, int entries, int most);
-cudaError_t launch_loss_stream(const LossProduct &p, float *dl, int grid, int *status, cudaStream_t s);
+cudaError_t launch_loss_stream_sums(int dtype, const LossProduct &p, int grid, int *status,
+                                    cudaStream_t s);
+cudaError_t launch_loss_stream_logit_grad(const LossProduct &p, float *dl, int grid, int *status,
+                                          cudaStream_t s);
 cudaError_t launch_loss_stream_grads(const LossProduct &p, const float *dl, float *dW, bool want_dx,
                                      int *status, cudaStream_t s);
 

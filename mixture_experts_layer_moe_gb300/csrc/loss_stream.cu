@@ -1,12 +1,15 @@
-// The cross entropy of a few tokens in fp32: as many streams over the vocabulary's rows W
-// [entries][d] as there are warps.
+// The cross entropy of a few tokens, and in fp32 its gradient: as many streams over the
+// vocabulary's rows W [entries][d] as there are warps.
 //
 //   loss_stream_kernel   l[t][v] = sum_k x[t][k] W[v][k], reduced to a maximum and a sum of
 //                        exponentials per token, or (GRAD) turned into its gradient dl [v][pitch];
 //   loss_stream_grads_kernel   dx[t] = sum_v dl[v][t] W[v] and dW[v] = sum_t dl[v][t] x[t] in one
 //                        pass, W read once and dW written once.
-// Bytes bound both: a value of W serves at most 8 tokens.  (A tile of 32 x 32 outputs
-// reads and multiplies for 32 tokens whatever their number.)  Tiles / streams, us: one token,
+// Bytes bound both: a value of W serves at most 8 tokens.  In bf16 the tensor cores' kernel
+// is as fast from 4 tokens on.  It / the streams, us, d 2880, 131072 entries: one token 130 / 117
+// (6.5 TB/s), 2 130 / 120, 3 130 / 131, 5 130 / 229; d 4096, 32000 entries, 3 tokens 53 / 50; d 8192,
+// 8192 entries 45 / 28.  In fp32 a tile of 32 x 32 outputs reads and multiplies for 32 tokens
+// whatever their number.  Tiles / streams, us: one token,
 // d 4096, 50000 entries 812 / 127 (6.5 TB/s) and its gradient 1648 / 399; 8 tokens 816 / 153 and
 // 1669 / 479; d 512, 8192 entries, 8 tokens 20.8 / 11.0 and 42.7 / 28.5; d 64 12.2 / 10.0 and
 // 22.9 / 17.8; d 8 10.6 / 10.8 and 21.2 / 28.7.
@@ -16,6 +19,7 @@
 #include "fp32x2.cuh"
 #include "launch.h"
 #include "loss.h"
+#include "vec16.cuh"
 
 namespace moe {
 namespace {
@@ -24,7 +28,7 @@ constexpr int S_THREADS = 512, S_WARPS = S_THREADS / 32;
 constexpr int S_X = 48 * 1024;      // floats of the tokens' rows in shared memory at most
 constexpr int S_GRADS = 256;        // threads of the second kernel
 constexpr int S_DL = 256;           // entries whose dl it holds
-constexpr int S_TOKENS = 8;         // at most
+constexpr int S_TOKENS = 8, S_TOKENS_BF16 = 4;   // at most
 constexpr int S_MIN_D = 64;
 
 struct StreamArgs {
@@ -56,12 +60,20 @@ __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f
 // d 4096, 50000 entries.)
 __host__ __device__ constexpr int entries_of(int tokens) { return tokens > 4 ? 2 : 4; }
 
+// Columns of a token's row in shared memory.
+template <typename T>
+__host__ __device__ constexpr int whole_steps(int d) {
+  constexpr int STEP = 32 * Vec16<T>::N;
+  return (d + STEP - 1) / STEP * STEP;
+}
+
 // A warp takes R neighbouring entries at a time, whose sums for NT tokens it spreads
 // over its lanes; a lane goes on with one of them.
-template <int NT, bool GRAD>
+template <typename T, int NT, bool GRAD>
 __global__ void __launch_bounds__(S_THREADS, 1) loss_stream_kernel(const __grid_constant__ StreamArgs a) {
   constexpr int R = entries_of(NT), V = R * NT, EACH = 32 / V;
-  extern __shared__ __align__(16) float xs[];   // [NT][d]
+  constexpr int N = Vec16<T>::N, STEP = 32 * N;   // columns of a lane, and of a warp
+  extern __shared__ __align__(16) float xs[];     // [NT][d rounded up to whole steps]
   __shared__ float2 pairs[S_WARPS][32];
   const LossProduct &p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -69,9 +81,18 @@ __global__ void __launch_bounds__(S_THREADS, 1) loss_stream_kernel(const __grid_
   pdl_wait();
   if (status_failed(a.status)) return;
   const int count = GRAD ? min(max(p.range[1], 0), p.n) : p.n;
-  const float4 *x = static_cast<const float4 *>(p.x);
-  for (int i = threadIdx.x; i < NT * (d / 4); i += S_THREADS)
-    reinterpret_cast<float4 *>(xs)[i] = i < p.n * (d / 4) ? x[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+  // (a step's first four columns of every lane, then in bf16 the other four)
+  const int pitch = whole_steps<T>(d);
+  for (int i = threadIdx.x; i < NT * (d / N); i += S_THREADS) {
+    const int k = i / (d / N), c = i - k * (d / N);
+    float f[N] = {};
+    if (k < p.n) unpack16<T>(static_cast<const uint4 *>(p.x)[i], f);
+    float *to = xs + k * pitch + c / 32 * STEP + c % 32 * 4;
+#pragma unroll
+    for (int h = 0; h < N / 4; ++h)
+      *reinterpret_cast<float4 *>(to + h * 128) =
+          make_float4(f[h * 4], f[h * 4 + 1], f[h * 4 + 2], f[h * 4 + 3]);
+  }
   // this lane's token and entry of the R
   const int q = lane / EACH, t = q % NT, r = q / NT;
   const bool lead = lane % EACH == 0, there = t < count;
@@ -86,25 +107,29 @@ __global__ void __launch_bounds__(S_THREADS, 1) loss_stream_kernel(const __grid_
   float top = -INFINITY, sum = 0.f;
   for (int e0 = ((int)blockIdx.x * S_WARPS + warp) * R; e0 < entries;
        e0 += (int)gridDim.x * S_WARPS * R) {
-    const float *row[R];
+    const T *row[R];
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      row[i] = static_cast<const float *>(p.W) + (int64_t)min(e0 + i, entries - 1) * d;
+      row[i] = static_cast<const T *>(p.W) + (int64_t)min(e0 + i, entries - 1) * d;
     float2 acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = both(0.f);
 #pragma unroll 2
-    for (int c = lane * 4; c < d; c += 128) {
-      float4 w[R];
+    for (int c = lane * N, at = lane * 4; c < d; c += STEP, at += STEP) {
+      float w[R][N];
 #pragma unroll
-      for (int i = 0; i < R; ++i) w[i] = __ldcs(reinterpret_cast<const float4 *>(row[i] + c));
+      for (int i = 0; i < R; ++i) unpack16<T>(__ldcs(reinterpret_cast<const uint4 *>(row[i] + c)), w[i]);
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
-        const float4 v = *reinterpret_cast<const float4 *>(xs + k * d + c);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          acc[i * NT + k] = fma2(make_float2(w[i].x, w[i].y), make_float2(v.x, v.y), acc[i * NT + k]);
-          acc[i * NT + k] = fma2(make_float2(w[i].z, w[i].w), make_float2(v.z, v.w), acc[i * NT + k]);
+        for (int h = 0; h < N / 4; ++h) {
+          const float4 v = *reinterpret_cast<const float4 *>(xs + k * pitch + at + h * 128);
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            float2 &s = acc[i * NT + k];
+            s = fma2(make_float2(w[i][h * 4], w[i][h * 4 + 1]), make_float2(v.x, v.y), s);
+            s = fma2(make_float2(w[i][h * 4 + 2], w[i][h * 4 + 3]), make_float2(v.z, v.w), s);
+          }
         }
       }
     }
@@ -244,17 +269,17 @@ int across(int d) {
   return tx;
 }
 
-template <int NT, bool GRAD>
+template <typename T, int NT, bool GRAD>
 cudaError_t launch(const StreamArgs &a, int grid, cudaStream_t s) {
   static bool set = false;
   if (!set) {
     const cudaError_t e = cudaFuncSetAttribute(
-        loss_stream_kernel<NT, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_X * 4);
+        loss_stream_kernel<T, NT, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_X * 4);
     if (e != cudaSuccess) return e;
     set = true;
   }
-  return launch_pdl(loss_stream_kernel<NT, GRAD>, dim3(grid), dim3(S_THREADS),
-                    (size_t)NT * a.p.d * 4, s, a);
+  return launch_pdl(loss_stream_kernel<T, NT, GRAD>, dim3(grid), dim3(S_THREADS),
+                    (size_t)NT * whole_steps<T>(a.p.d) * 4, s, a);
 }
 
 int tokens_of(int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : S_TOKENS; }
@@ -262,8 +287,8 @@ int tokens_of(int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : S_TOKENS; }
 }  // namespace
 
 bool loss_stream_supported(const moe_loss_config &c) {
-  return c.dtype == MOE_F32 && c.n >= 1 && c.n <= S_TOKENS && c.d >= S_MIN_D &&
-         (int64_t)tokens_of(c.n) * c.d <= S_X;
+  const int64_t row = c.dtype == MOE_F32 ? whole_steps<float>(c.d) : whole_steps<__nv_bfloat16>(c.d);
+  return c.n >= 1 && c.n <= (c.dtype == MOE_F32 ? S_TOKENS : S_TOKENS_BF16) && c.d >= S_MIN_D && tokens_of(c.n) * row <= S_X;
 }
 
 int loss_stream_chunks(const moe_loss_config &c) {
@@ -280,14 +305,24 @@ int loss_stream_splits(int d, int entries, int most) {
   return s < 1 ? 1 : s;
 }
 
-cudaError_t launch_loss_stream(const LossProduct &p, float *dl, int grid, int *status, cudaStream_t s) {
-  const StreamArgs a{p, dl, status};
-  switch (tokens_of(p.n)) {
-    case 1: return dl ? launch<1, true>(a, grid, s) : launch<1, false>(a, grid, s);
-    case 2: return dl ? launch<2, true>(a, grid, s) : launch<2, false>(a, grid, s);
-    case 4: return dl ? launch<4, true>(a, grid, s) : launch<4, false>(a, grid, s);
-    default: return dl ? launch<S_TOKENS, true>(a, grid, s) : launch<S_TOKENS, false>(a, grid, s);
+template <typename T, bool GRAD>
+static cudaError_t launch_tokens(const StreamArgs &a, int grid, cudaStream_t s) {
+  switch (tokens_of(a.p.n)) {
+    case 1: return launch<T, 1, GRAD>(a, grid, s);
+    case 2: return launch<T, 2, GRAD>(a, grid, s);
+    case 4: return launch<T, 4, GRAD>(a, grid, s);
+    default: return launch<T, sizeof(T) == 4 ? S_TOKENS : S_TOKENS_BF16, GRAD>(a, grid, s);
   }
+}
+cudaError_t launch_loss_stream_sums(int dtype, const LossProduct &p, int grid, int *status,
+                                    cudaStream_t s) {
+  const StreamArgs a{p, nullptr, status};
+  return dtype == MOE_F32 ? launch_tokens<float, false>(a, grid, s)
+                          : launch_tokens<__nv_bfloat16, false>(a, grid, s);
+}
+cudaError_t launch_loss_stream_logit_grad(const LossProduct &p, float *dl, int grid, int *status,
+                                          cudaStream_t s) {
+  return launch_tokens<float, true>(StreamArgs{p, dl, status}, grid, s);
 }
 
 cudaError_t launch_loss_stream_grads(const LossProduct &p, const float *dl, float *dW, bool want_dx,
