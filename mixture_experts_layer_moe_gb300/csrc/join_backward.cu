@@ -241,7 +241,9 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
       if (STAGES > 1) fill(next);
       if (has_dy) pre = join(pre);
     }
-    const float c2 = -stat.w * stat.w * stat.w * pre.y * inv_d;
+    // (1 / deviation meets the sum before itself: its cube alone leaves fp32's range for rows of
+    // a root mean square above 4e12 or below 1e-13)
+    const float c2 = -stat.w * (stat.w * (stat.w * pre.y * inv_d));
     const float e2 = layer2 ? -stat.w * pre.x * inv_d : 0.f;
     auto get = [&](int n, int t) { return B::load(at(now, n, t)); };
     Block8 w[NB];
@@ -305,7 +307,7 @@ join_backward_kernel(const __grid_constant__ Bwd<T> a, const __grid_constant__ B
     }
     if (a.db) {
       // (w is rstd1 times the gradient of the normed row)
-      const float c1 = -stat.y * stat.y * post.y * inv_d, e1 = layer1 ? -post.x * inv_d : 0.f;
+      const float c1 = -stat.y * (stat.y * post.y * inv_d), e1 = layer1 ? -post.x * inv_d : 0.f;
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         if (!live || !active[n]) continue;
