@@ -592,13 +592,16 @@ moe_status moe_cross_entropy_workspace_size(const moe_loss_config *cfg, size_t *
  * target leaves its token out: loss and lse are 0, whatever its row of x
  * holds.  A target >= vocab sets MOE_ERR_BAD_INDEX (detail: the
  * token); the outputs are then not valid.  The logits are never stored as a
- * whole. */
+ * whole.  loss is formed from the largest logit, not from lse: the loss of a sure
+ * token keeps its digits however far from zero its logits lie, and no loss is
+ * negative. */
 moe_status moe_cross_entropy(const moe_loss_config *cfg, const void *x, const void *W,
                              const int32_t *targets, float *loss, float *lse, void *ws,
                              size_t ws_bytes, void *stream);
 
 /* Its gradient, from dloss fp32 [n] (of each token's loss) and lse as
- * moe_cross_entropy wrote it.  The logits are formed again:
+ * moe_cross_entropy wrote it.  The logits are formed again (dl is as exact as lse,
+ * which fp32 rounds at the logits' size):
  *   dl_j = dloss * (e^{l_j - lse} (1 + 2 z_loss lse) - [j = v]),
  *   dx = dl W,   dW = dl^T x.
  * dx [n][d], dW [vocab][d], each may be NULL.  Rows of dx of left out tokens are

@@ -367,7 +367,11 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const __grid_constant_
   }
   if (WIDE ? threadIdx.x != 0 : lane != 0) return;
   const int t = a.list ? a.list[j] : j, target = a.targets[t];
-  float lse = v.x + logf(v.y), loss = lse - a.at[j] + a.z_loss * lse * lse;
+  // (the target's logit meets the maximum first: from lse, rounded at the logits' size, it would
+  // leave a sure token's loss nothing but that rounding.  The sum holds the maximum's 1, so no loss
+  // is negative.)
+  const float log_sum = logf(v.y);
+  float lse = v.x + log_sum, loss = (v.x - a.at[j]) + log_sum + a.z_loss * lse * lse;
   if (target < 0 || target >= a.vocab) {
     if (target >= a.vocab) set_status(a.status, MOE_ERR_BAD_INDEX, t);
     lse = loss = 0.f;

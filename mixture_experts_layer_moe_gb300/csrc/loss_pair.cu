@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "fp32x2.cuh"
 #include "launch.h"
 #include "loss.h"
 #include "pair_common.cuh"
@@ -350,14 +351,17 @@ loss_pair_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LAr
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) up = fmaxf(up, l[i]);
-            const float shift = up == -INFINITY ? 0.f : up * kLog2e;
+            // (the maximum is taken away before the factor: taken away after it, rounded, it would be off
+            // by up to half an ulp of itself, and every exponential by that as a factor)
+            const float2 shift = both(up == -INFINITY ? 0.f : -up);
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              s0 += exp2_fast(fmaf(l[i], kLog2e, -shift));
-              s1 += exp2_fast(fmaf(l[i + 1], kLog2e, -shift));
+              const float2 e = mul2(add2(make_float2(l[i], l[i + 1]), shift), both(kLog2e));
+              s0 += exp2_fast(e.x);
+              s1 += exp2_fast(e.y);
             }
-            sum = fmaf(sum, exp2_fast(fmaf(top, kLog2e, -shift)), s0 + s1);
+            sum = fmaf(sum, exp2_fast((top + shift.x) * kLog2e), s0 + s1);
             top = up;
           }
           if (there) p.sums[(size_t)j * p.chunks + 2 * tl.col + part] = make_float2(top, sum);

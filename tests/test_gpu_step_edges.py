@@ -1,9 +1,11 @@
 """GPU: the ends of the operators' ranges round the layer, against the float64 oracle: rows of any
-magnitude.  Bounds as in test_gpu_step.py, from the arithmetic."""
+magnitude, logits far from zero.  Bounds as in test_gpu_step.py, from the arithmetic."""
 import pytest
 import torch
 
-from test_gpu_step import _check_join, _check_join_backward, _join_case, _rows
+from oracle import step_oracle as S
+from test_gpu_step import (DT, V, _check_join, _check_join_backward, _gen, _join_case, _ok, _randn,
+                           _rows, _within)
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +55,42 @@ def test_join_of_rows_of_zeros_and_a_tiny_eps(lib, post, pre, d, dtype):
     params, x, b, dr, dy, kw = _join_case(11, d, 0, dtype, post, pre, True, 0.2, 1.0, beta=False)
     x[4], b[4] = 0, 0
     _check_both(lib, (params, x, b, dr, dy, kw), 1e-30, 0, dtype)
+
+
+# ------------------------------------------------- cross entropy, logits far from zero
+# n, d, vocab, dtype: each kernel that forms a token's sums: streams; the CUDA cores' tiles of 32
+# and 64; SM pairs, with one block of tokens and several, in one unit and more
+FORWARDS = [(3, 64, 4000, "bf16"), (8, 64, 4000, "f32"), (40, 64, 999, "bf16"), (40, 64, 999, "f32"),
+            (1000, 64, 4000, "f32"), (40, 512, 4000, "bf16"), (40, 2048, 999, "bf16"),
+            (300, 512, 4000, "bf16"), (300, 2048, 999, "bf16")]
+
+
+@pytest.mark.parametrize("n,d,vocab,dtype", FORWARDS)
+def test_cross_entropy_of_a_sure_token_far_from_zero(lib, n, d, vocab, dtype):
+    """Logits c - gap, exact in fp32, with one entry at the top and the others 13 and more below: the
+    loss is about the others' sum of exponentials, whatever c, and never negative."""
+    g = _gen(n + vocab)
+    top = 7 * n % vocab
+    gap = (104 + torch.randint(148, (vocab,), generator=g, device="cuda")) / 8
+    gap[top] = 0
+    W, x = torch.zeros(vocab, d, device="cuda"), torch.zeros(n, d, device="cuda")
+    W[:, 0], W[:, d - 1] = 23.25, -gap
+    x[:, 0] = torch.tensor([128.0, 0.0, -128.0, 1024.0, 16.0], device="cuda").repeat(n)[:n]
+    x[:, d - 1] = 1
+    W, x = W.to(DT[dtype]), x.to(DT[dtype])
+    t = torch.full((n,), top, dtype=torch.int32, device="cuda")
+    t[2::3] = torch.arange(len(t[2::3]), device="cuda").to(torch.int32) % vocab
+    ws = lib.alloc_cross_entropy_workspace(n, d, vocab, dtype)
+    ws[256:] = 0xFF
+    loss, lse = (torch.full((n,), float("nan"), device="cuda") for _ in range(2))
+    lib.moe_cross_entropy(x, W, t, loss, lse, ws)
+    _ok(lib, ws)
+    wloss, wlse, logits = S.cross_entropy(x, W, t)
+    below = logits.amax(1, keepdim=True) - logits
+    # the exponentials but for the top's, which is 1; the fp32 sum; the logarithm and the last sums
+    e = ((torch.softmax(logits, 1) * (2 ** -20 + 2 ** -22 * below) * (below > 0)).sum(1)
+         + (64 + vocab / 8192) * V)
+    at = below.gather(1, t.cpu().long()[:, None])[:, 0]
+    _within(loss, wloss, e + 4 * V * (at + wloss), "loss")
+    _within(lse, wlse, e + 2 * V * wlse.abs(), "lse")
+    assert (loss >= 0).all()
