@@ -581,9 +581,15 @@ typedef struct {
 
 /* Bytes of workspace for the two entry points below, a status word at its start
  * (moe_status_check); nothing else in it lives from one call to the next, and it
- * may be any workspace that is large enough.  Holds the logits of a piece of the
- * vocabulary (about 256 MB, or 8192 entries), 8 bytes per token and 256 entries of the
- * vocabulary, and a few copies of x.  Host-only. */
+ * may be any workspace that is large enough.  Holds a copy of x and 20 bytes per token,
+ * and, in the same place, whichever is more of
+ *   - the forward's partial sums, 8 bytes each: per token two for each 256 entries of the
+ *     vocabulary in bf16, four in f32 (few tiles: up to eight);
+ *   - the gradient's logits of a piece of the vocabulary (about 256 MB, or 8192 entries
+ *     where that is more; 2 bytes each, 4 in f32 and small problems), the partial sums of
+ *     dx, fp32 copies of x (152 at most, 4 where n d is 2^24 or more), and those of dW
+ *     where its tiles are few (40 MB at most).
+ * Host-only. */
 moe_status moe_cross_entropy_workspace_size(const moe_loss_config *cfg, size_t *bytes);
 
 /* Per token t with target v = targets[t]:

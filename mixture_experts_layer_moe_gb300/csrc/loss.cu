@@ -52,7 +52,7 @@ struct LossLayout {
   int pitch;    // CUDA cores: tokens, rounded up to whole vectors of fp32
   int piece;    // vocabulary entries of a piece of the gradient at most
   int pieces;
-  int width, chunks;   // entries per tile of the forward; partial sums per token at most
+  int width, chunks;   // entries per tile of the forward; partial sums per token
   int planes;          // dx: partial sums of a piece
   bool few;            // dx and dW in one pass (loss_few.cu)
   bool stream, stream_grad;   // the forward, the gradient by streams over W (loss_stream.cu)
@@ -104,6 +104,15 @@ RowsProduct dw_product_simt(const moe_loss_config &c, int entries) {
   return p;
 }
 
+// Entries of a tile of the forward on the CUDA cores.
+int sums_tile(const moe_loss_config &c) {
+  RowsProduct p{};
+  p.dtype = c.dtype;
+  p.rows = c.vocab;
+  p.N = c.n;
+  return rows_simt_tile(p);
+}
+
 int dx_splits(const moe_loss_config &c, const LossLayout &L, int entries, int most) {
   return L.few ? loss_few_splits(c.d, entries, most) : loss_dx_splits(c.n, c.d, entries, most);
 }
@@ -126,7 +135,9 @@ LossLayout loss_layout(const moe_loss_config &c) {
   L.pieces = (c.vocab + L.piece - 1) / L.piece;
   const int last = c.vocab - (L.pieces - 1) * L.piece;
   L.width = L.pair ? loss_width(c.n, c.vocab) : 0;
-  L.chunks = L.stream ? loss_stream_chunks(c) : L.pair ? loss_chunks(c.vocab, L.width) : (c.vocab + 31) / 32;
+  if (L.stream) L.chunks = loss_stream_chunks(c);
+  else if (L.pair) L.chunks = loss_chunks(c.vocab, L.width);
+  else L.chunks = (c.vocab + sums_tile(c) - 1) / sums_tile(c);
   if (L.stream_grad) {
     L.planes = loss_stream_splits(c.d, L.piece, 2 * L_MAX_SPLITS);
   } else if (L.pair) {
@@ -657,8 +668,6 @@ cudaError_t launch_loss(const moe_loss_config &c, const void *x, const void *W,
     LOSS_TRY(launch_loss_sums(p, f.status, s));
   } else {
     RowsProduct p = simt_product(c, kRowsLossSums, x, W, 0, c.vocab);
-    const int tile = rows_simt_tile(p);
-    f.chunks = (c.vocab + tile - 1) / tile;
     p.loss.target = targets;
     p.loss.sums = at<float2>(ws, L.sums);
     p.loss.chunks = L.chunks;

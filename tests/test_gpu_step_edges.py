@@ -94,3 +94,33 @@ def test_cross_entropy_of_a_sure_token_far_from_zero(lib, n, d, vocab, dtype):
     _within(loss, wloss, e + 4 * V * (at + wloss), "loss")
     _within(lse, wlse, e + 2 * V * wlse.abs(), "lse")
     assert (loss >= 0).all()
+
+
+# ------------------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("n,d,vocab,dtype", [(4096, 4, 2 ** 22 + 5, "f32"), (1000, 64, 4001, "f32"),
+                                             (70, 64, 3001, "f32"), (1000, 64, 4001, "bf16"),
+                                             (40, 64, 999, "bf16"), (3, 64, 4001, "f32")])
+def test_cross_entropy_stays_in_its_workspace(lib, n, d, vocab, dtype):
+    """What lies behind a workspace of the stated size stays, and the sums in it are whole."""
+    g = _gen(n + d)
+    x, W = _randn(g, n, d, dtype=dtype), _randn(g, vocab, d, dtype=dtype, std=d ** -0.5)
+    t = torch.randint(vocab, (n,), generator=g, device="cuda").to(torch.int32)
+    size = lib.moe_cross_entropy_workspace_size(n, d, vocab, dtype)
+    space = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = space[:size]
+    ws[:256] = 0
+    loss, lse = (torch.full((n,), float("nan"), device="cuda") for _ in range(2))
+    lib.moe_cross_entropy(x, W, t, loss, lse, ws)
+    dx, dW = torch.full_like(x, float("nan")), torch.full_like(W, float("nan"))
+    lib.moe_cross_entropy_backward(x, W, t, lse, torch.ones_like(lse), dx, dW, ws)
+    _ok(lib, ws)
+    assert (space[size:] == 0xA5).all()
+    assert all(torch.isfinite(v).all() for v in (loss, dx, dW))
+    some = torch.arange(0, n, max(1, n // 8), device="cuda")
+    logits = x[some].double() @ W.double().T
+    want, top = torch.logsumexp(logits, 1), logits.amax(1)
+    # |l| <= |x| |W| (norms); exponents of at most the logits' range; the sum; the last roundings
+    k = 2 if dtype == "bf16" else 1
+    e = (k * d * V * x[some].double().norm(dim=1) * W.double().norm(dim=1).max() + 2 ** -20
+         + 2 ** -22 * (top - logits.amin(1)) + (64 + vocab / 8192) * V + 2 * V * (want.abs() + top.abs()))
+    assert ((lse[some].double() - want).abs() <= e).all()
