@@ -355,10 +355,17 @@ def alloc_train_workspace(cfg, device="cuda") -> torch.Tensor:
 _NORM_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
+def _int32(size: int) -> int:
+    """A size that its struct holds in 32 bits (ctypes would cut it off without a word)."""
+    if size >= 2 ** 31:
+        raise ValueError(f"a size of {size} is not supported: it takes more than 32 bits")
+    return size
+
+
 @functools.lru_cache(maxsize=256)
 def _norm_config(rows, ldx, ldy, lddx, lddy, d, dtype, eps):
     """A moe_norm_config by reference (the library only reads it)."""
-    return ctypes.byref(moe_norm_config(rows, ldx, ldy, lddx, lddy, d, dtype, eps, 0))
+    return ctypes.byref(moe_norm_config(rows, ldx, ldy, lddx, lddy, _int32(d), dtype, eps, 0))
 
 
 def _norm_rows(t: torch.Tensor, shape, dtype) -> tuple[int, int]:
@@ -410,7 +417,7 @@ def moe_layernorm_workspace_size(rows: int, d: int, dtype: str) -> int:
     """dtype "f32" or "bf16".  Enough for rows of any leading dimension."""
     out, need = ctypes.c_size_t(0), 0
     for ld in (d, d + 1):
-        c = moe_norm_config(rows, ld, ld, ld, ld, d, _DTYPE[dtype], 0.0, 0)
+        c = moe_norm_config(rows, ld, ld, ld, ld, _int32(d), _DTYPE[dtype], 0.0, 0)
         _check(_lib.moe_layernorm_workspace_size(ctypes.byref(c), ctypes.byref(out)),
                "moe_layernorm_workspace_size")
         need = max(need, out.value)
@@ -562,7 +569,7 @@ def _bytes(ws: torch.Tensor, device) -> tuple[int, int]:
 
 @functools.lru_cache(maxsize=256)
 def _dropout_config(rows, ldx, ldy, d, dtype, p):
-    return ctypes.byref(moe_dropout_config(rows, ldx, ldy, d, dtype, p, 0))
+    return ctypes.byref(moe_dropout_config(rows, ldx, ldy, _int32(d), dtype, p, 0))
 
 
 def moe_dropout(x, y, p: float, rng=None, stream=None):
@@ -580,8 +587,8 @@ def moe_dropout(x, y, p: float, rng=None, stream=None):
 @functools.lru_cache(maxsize=256)
 def _join_config(rows, ldx, ldb, ldr, ldy, lddx, lddb, lddr, lddy, d, dtype, post, pre, eps, scale,
                  p):
-    return ctypes.byref(moe_join_config(rows, ldx, ldb, ldr, ldy, lddx, lddb, lddr, lddy, d, dtype,
-                                        _JOIN_NORM[post], _JOIN_NORM[pre], eps, scale, p, 0))
+    return ctypes.byref(moe_join_config(rows, ldx, ldb, ldr, ldy, lddx, lddb, lddr, lddy, _int32(d),
+                                        dtype, _JOIN_NORM[post], _JOIN_NORM[pre], eps, scale, p, 0))
 
 
 def moe_block_join(x, b, params: _Vectors, r, y, stats, *, post="rms", pre="rms", scale=1.0, p=0.0,
@@ -605,7 +612,7 @@ def moe_block_join(x, b, params: _Vectors, r, y, stats, *, post="rms", pre="rms"
 def moe_block_join_workspace_size(rows: int, d: int, dtype: str) -> int:
     """dtype "f32" or "bf16".  Enough for any norms and leading dimensions."""
     out = ctypes.c_size_t(0)
-    c = moe_join_config(rows=rows, d=d, dtype=_DTYPE[dtype])
+    c = moe_join_config(rows=rows, d=_int32(d), dtype=_DTYPE[dtype])
     _check(_lib.moe_block_join_workspace_size(ctypes.byref(c), ctypes.byref(out)),
            "moe_block_join_workspace_size")
     return out.value
@@ -638,7 +645,7 @@ def moe_block_join_backward(b, r, stats, params: _Vectors, dr, dy, dx, db, grads
 
 @functools.lru_cache(maxsize=256)
 def _loss_config(n, d, vocab, dtype, z_loss):
-    return ctypes.byref(moe_loss_config(n, d, vocab, dtype, z_loss, 0))
+    return ctypes.byref(moe_loss_config(_int32(n), _int32(d), _int32(vocab), dtype, z_loss, 0))
 
 
 def _loss_operands(x, W, targets, z_loss):
@@ -654,7 +661,7 @@ def _loss_operands(x, W, targets, z_loss):
 def moe_cross_entropy_workspace_size(n: int, d: int, vocab: int, dtype: str) -> int:
     """dtype "f32" or "bf16"."""
     out = ctypes.c_size_t(0)
-    c = moe_loss_config(n, d, vocab, _DTYPE[dtype], 0.0, 0)
+    c = moe_loss_config(_int32(n), _int32(d), _int32(vocab), _DTYPE[dtype], 0.0, 0)
     _check(_lib.moe_cross_entropy_workspace_size(ctypes.byref(c), ctypes.byref(out)),
            "moe_cross_entropy_workspace_size")
     return out.value

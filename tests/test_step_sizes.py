@@ -2,6 +2,7 @@
 import math
 
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -39,3 +40,35 @@ def test_cross_entropy_workspace_holds_what_is_stated(moe, n, d, vocab, dtype):
     assert got % 256 == 0
     # (every part starts on 256 bytes)
     assert copy + 256 <= got <= copy + max(sums, gradient) + 20 * 256
+
+
+@pytest.mark.parametrize("size", [2 ** 31, 2 ** 32 + 8])
+def test_binding_refuses_sizes_past_32_bits(moe, monkeypatch, size):
+    """Cut off to 32 bits, 2^32 + 8 would pass for 8 and most of the result stay unwritten."""
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail(f"{name} was reached")
+
+    monkeypatch.setattr(moe, "_lib", Lib())
+    meta = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device="meta")
+    wide, one, ws = meta(1, size), meta(1), meta(16, dtype=torch.uint8)
+    rng, none = meta(2, dtype=torch.int64), moe.make_join_grads({})
+    v = moe.make_join_params(dict(pre_gamma=meta(size)))
+    long, t = meta(size, 8), meta(size, dtype=torch.int32)
+    for call in (
+            lambda: moe.moe_dropout(wide, wide, 0.1, rng, stream=0),
+            lambda: moe.moe_block_join(wide, wide, v, wide, wide, None, post="none", stream=0),
+            lambda: moe.moe_block_join_backward(wide, wide, meta(4, 1), v, wide, wide, wide, wide, none,
+                                                ws, post="none", stream=0),
+            lambda: moe.moe_block_join_workspace_size(1, size, "bf16"),
+            lambda: moe.moe_cross_entropy(long, meta(5, 8), t, meta(size), meta(size), ws, stream=0),
+            lambda: moe.moe_cross_entropy(meta(1, 8), long, t[:1], one, one, ws, stream=0),
+            lambda: moe.moe_cross_entropy_backward(long, meta(5, 8), t, meta(size), meta(size), long,
+                                                   None, ws, stream=0),
+            lambda: moe.moe_cross_entropy_workspace_size(size, 8, 5, "f32"),
+            lambda: moe.moe_cross_entropy_workspace_size(5, 8, size, "f32"),
+            lambda: moe.alloc_cross_entropy_workspace(5, size, 5, "f32"),
+            lambda: moe.moe_layernorm(wide, meta(size), None, wide, one, one, stream=0),
+            lambda: moe.moe_layernorm_workspace_size(1, size, "f32")):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
