@@ -12,7 +12,7 @@ constexpr int J_SUMS = 4;      // sum u bh, sum u, sum dy rh, sum dy
 template <typename T>
 struct Bwd {
   moe_join_config c;
-  const T *b, *r, *gate, *post_gamma, *post_beta, *pre_gamma, *pre_beta;
+  const T *b, *r, *gate, *post_gamma, *post_beta, *pre_gamma;
   const float *stats;
   const RngState *rng;
   const T *dr, *dy;
@@ -567,7 +567,6 @@ cudaError_t backward(const moe_join_config &c, int threshold, const JoinBackward
   a.post_gamma = (const T *)f.w.post_gamma;
   a.post_beta = (const T *)f.w.post_beta;
   a.pre_gamma = (const T *)f.w.pre_gamma;
-  a.pre_beta = (const T *)f.w.pre_beta;
   a.stats = f.stats;
   a.rng = reinterpret_cast<const RngState *>(f.rng);
   a.dr = (const T *)f.dr;
