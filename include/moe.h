@@ -492,7 +492,9 @@ moe_status moe_route_backward(const moe_config *cfg, const void *x, const moe_we
  * they are below T.
  *   rng: DEVICE pointer to {uint64 seed, uint64 offset}, 8-byte aligned, read when
  *   the kernel runs (a captured graph follows its contents); may be NULL when
- *   T = 0.  y may be x itself (with ldy = ldx). */
+ *   T = 0.  Calls with the same state drop the same elements: each dropout of a step needs
+ *   an offset of its own, and none that another step has (step * dropouts + which, not
+ *   step + which).  y may be x itself (with ldy = ldx). */
 typedef struct {
   int64_t rows;        /* 0 .. 2^32 (else MOE_ERR_UNSUPPORTED) */
   int64_t ldx, ldy;    /* as moe_norm_config's: elements between rows, 0 for d */
@@ -539,7 +541,9 @@ typedef struct {
 
 /* The joint of a block with the residual stream, in one pass over the rows:
  *   z = post(b),   r = scale * x + gate . D(z),   y = pre(r)
- * with D the dropout of moe_dropout (element (r, c) of the call's rows).  x: the
+ * with D the dropout of moe_dropout (element (r, c) of the call's rows; its state's offset
+ * is this joint's own, as there).  Rows wider than 8192 are read in several passes, and take
+ * several times as long for their size.  x: the
  * residual stream, b: the block's output, r: the new stream, y: what the next
  * block reads (NULL when pre is NONE, needed otherwise).  Both norms and the sum
  * are formed in fp32 from the fp32 values (y from r before it is rounded).
@@ -569,7 +573,9 @@ moe_status moe_block_join_backward(const moe_join_config *cfg, const void *b, co
                                    void *db, const moe_join_grads *grads, void *ws,
                                    size_t ws_bytes, void *stream);
 
-/* Softmax cross entropy of a linear layer over a vocabulary. */
+/* Softmax cross entropy of a linear layer over a vocabulary.  bf16 products run on the
+ * tensor cores, f32 ones on the CUDA cores (36 TFLOP/s): f32 is for small models and
+ * checks, and a library's products are faster for large ones. */
 typedef struct {
   int32_t n;           /* tokens, 0 .. 1048576 (else MOE_ERR_UNSUPPORTED) */
   int32_t d;           /* 4 .. 65536, a multiple of 4 (f32) or 8 (bf16), likewise */

@@ -551,7 +551,8 @@ def _fp32(t: Optional[torch.Tensor], shape, device) -> Optional[int]:
 
 
 def _rng(rng: Optional[torch.Tensor], device) -> Optional[int]:
-    """The generator's state: a device tensor of two 64-bit integers, seed and offset."""
+    """The generator's state: a device tensor of two 64-bit integers, seed and offset (one of its
+    own for each dropout and joint of each step: the same state drops the same elements)."""
     if rng is None:
         return None
     if (rng.dtype is not torch.int64 and rng.dtype is not torch.uint64) or rng.numel() != 2 or \
